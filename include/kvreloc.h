@@ -16,6 +16,10 @@
  *   - kv_patch     adds Kamera's rank-m conditioning patch U_m V_mᵀ to stored
  *                  rows; the same patch can be fused into kv_relocate.
  *                  [Kamera §2: KV^(B|A) = R(δ)·KV(B|∅) + U_m V_mᵀ]
+ *   - kv_quantize / kv_dequantize write rows into an 8-bit pool and read them
+ *                  back.
+ *   - kv_attention computes new tokens' attention over the paged cache, bf16
+ *                  or 8-bit, optionally through a sliding window with sinks.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -376,6 +380,128 @@ kv_status kv_fingerprint(int64_t num_ranges, const int64_t *d_start, const int64
                          int64_t total_tokens, const int32_t *d_tokens, uint64_t fp_seed,
                          uint64_t *d_fingerprint, void *d_workspace, size_t workspace_bytes,
                          kv_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Quantised cache rows
+ *
+ * A quantised pool holds the rows of a kv_pool_desc in 8-bit floating point
+ * (e4m3: 4 significant bits, largest value 448) with one fp32 scale for every
+ * 128 consecutive values of a row: a head of K or V, or a quarter of an MLA
+ * latent.  The scale of a group is a power of two,
+ *     s = 2^e,  e the smallest integer with max|x| <= 448 * 2^e, e >= -120
+ * (the maximum over the group's finite values; s = 1 when it is 0), the stored
+ * value is x / s rounded to nearest even, and a value that is not finite is
+ * stored as NaN.  value * s has 4 significant bits, so reading a row back is
+ * exact in bf16.  MLA rows keep k_pe in bf16 (rot_scale = NULL): it carries the
+ * position that kv_relocate turns; head rows keep K and V in e4m3.
+ * ------------------------------------------------------------------- */
+typedef struct {
+    int32_t num_layers;        /* L */
+    int32_t block_size;        /* tokens per paged block */
+    int64_t num_slots;         /* slots per layer; a multiple of block_size */
+    void *copy_base;           /* e4m3: MLA c_KV, or V */
+    int64_t copy_layer_stride; /* elements (bytes), multiples of 16 */
+    int64_t copy_slot_stride;
+    int32_t copy_dim;
+    float *copy_scale;         /* [layer][slot][copy_dim / 128], strides in floats */
+    int64_t copy_scale_layer_stride;
+    int64_t copy_scale_slot_stride;
+    void *rot_base;            /* e4m3 K with rot_scale, or bf16 k_pe without */
+    int64_t rot_layer_stride;  /* elements of its type, multiples of 16 bytes */
+    int64_t rot_slot_stride;
+    int32_t rot_heads;
+    int32_t rot_head_dim;
+    float *rot_scale;          /* [layer][slot][rot_heads]; NULL: rot is bf16 (MLA) */
+    int64_t rot_scale_layer_stride;
+    int64_t rot_scale_slot_stride;
+} kv_quant_pool_desc;
+
+/* Bytes of device workspace kv_quantize and kv_dequantize need (256-byte
+ * aligned); 0 for an invalid pool. */
+size_t kv_quantize_workspace_size(const kv_quant_pool_desc *pool);
+
+/* Write rows into a quantised pool: row i of `src` (slot d_src_slots[i], or
+ * slot i when d_src_slots is NULL) goes to slot d_dst_slots[i] of `dst`, in
+ * layers dst_layer .. dst_layer + src->num_layers - 1 (layer l of src in layer
+ * dst_layer + l).  `src` describes new rows ([layers][rows], block_size 1) or a
+ * paged pool.  Slots of dst that occur twice hold either row.  An index outside
+ * its pool is skipped and sets KV_ERR_OUT_OF_RANGE.  One kernel. */
+kv_status kv_quantize(const kv_pool_desc *src, const int32_t *d_src_slots,
+                      const kv_quant_pool_desc *dst, int32_t dst_layer, int64_t num_rows,
+                      const int32_t *d_dst_slots, void *d_workspace, size_t workspace_bytes,
+                      kv_stream_t stream);
+
+/* Read rows of a quantised pool back: slot d_src_slots[i] of layers src_layer
+ * .. src_layer + dst->num_layers - 1 goes to slot d_dst_slots[i] of `dst` (slot
+ * i when d_dst_slots is NULL), each value exactly.  Errors as kv_quantize.
+ * One kernel. */
+kv_status kv_dequantize(const kv_quant_pool_desc *src, int32_t src_layer,
+                        const int32_t *d_src_slots, const kv_pool_desc *dst, int64_t num_rows,
+                        const int32_t *d_dst_slots, void *d_workspace, size_t workspace_bytes,
+                        kv_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Attention of new tokens over the paged cache
+ *
+ * Sequence s has n = d_q_off[s+1] - d_q_off[s] new tokens (queries) and
+ * d_kv_len[s] cached tokens, the new ones among them: query i stands at
+ * position p = d_kv_len[s] - n + i.  It sees key k (0 <= k < d_kv_len[s]) when
+ *     causal: k <= p,   and   window > 0: k > p - window  or  k < sinks.
+ * Over the keys it sees, per query head h,
+ *     S_k = scale * q . key_k,  lse = log Σ_k exp(S_k),
+ *     out = Σ_k exp(S_k - lse) value_k.
+ * A query that sees no key (p < 0, or an empty cache) gets out = 0 and
+ * lse = -infinity.  Keys that a query does not see have no part in its result,
+ * whatever they hold.
+ * Head rows: query head h reads head h / (num_heads / rot_heads); key = the
+ * rotary part, value = the copy part, 128 wide each.  MLA rows (absorbed form):
+ * every query head reads the one row, key = c_KV ‖ k_pe (576 wide), value =
+ * c_KV (512 wide).
+ * Products of bf16 values are summed in fp32; scores, maxima and sums are
+ * fp32; the weights exp(S_k - max) are rounded to bf16 for the second product
+ * (the sum in lse uses the unrounded ones), and out once to bf16.
+ * ------------------------------------------------------------------- */
+typedef struct {
+    int32_t num_seqs;
+    int32_t max_q_len;             /* at least every sequence's new tokens */
+    int32_t max_kv_len;            /* at least every d_kv_len */
+    int32_t max_blocks;            /* entries of a block-table row */
+    const int32_t *d_q_off;        /* [num_seqs + 1], first 0, last total_q */
+    const int32_t *d_kv_len;       /* [num_seqs] */
+    const int32_t *d_block_tables; /* [num_seqs][max_blocks] */
+    int32_t causal;                /* 0 or 1 */
+    int32_t window;                /* 0: no window; needs causal = 1 otherwise */
+    int32_t sinks;                 /* with a window: first tokens that stay visible */
+    float scale;                   /* finite, > 0 */
+} kv_attn_desc;
+
+/* Bytes of workspace a kv_attention / kv_attention_quant call needs (256-byte
+ * aligned), 0 for invalid arguments. */
+size_t kv_attention_workspace_size(const kv_pool_desc *pool, const kv_attn_desc *attn,
+                                   int64_t total_q, int32_t num_heads);
+size_t kv_attention_quant_workspace_size(const kv_quant_pool_desc *pool, const kv_attn_desc *attn,
+                                         int64_t total_q, int32_t num_heads);
+
+/* Attention over one layer of a bf16 pool (kv_attention) or of a quantised
+ * one (kv_attention_quant).  Element (t, h, i) of the queries is the bf16 at
+ * d_q + t*q_tok_stride + h*q_head_stride + i, of the result likewise at d_out
+ * (strides multiples of 8 elements, bases 16-byte aligned); d_lse (NULL = not
+ * wanted) is fp32 [total_q][num_heads].  num_heads is a multiple of rot_heads,
+ * at most 128 query heads to a key head (else KV_ERR_UNSUPPORTED).  A sequence
+ * whose lengths on the device pass max_q_len, max_kv_len or its block-table row
+ * is skipped, and a block id outside the pool reads as rows of zeros; both set
+ * KV_ERR_OUT_OF_RANGE. */
+kv_status kv_attention(const kv_pool_desc *pool, int32_t layer, const kv_attn_desc *attn,
+                       int64_t total_q, int32_t num_heads, const void *d_q, int64_t q_tok_stride,
+                       int64_t q_head_stride, void *d_out, int64_t out_tok_stride,
+                       int64_t out_head_stride, float *d_lse, void *d_workspace,
+                       size_t workspace_bytes, kv_stream_t stream);
+kv_status kv_attention_quant(const kv_quant_pool_desc *pool, int32_t layer,
+                             const kv_attn_desc *attn, int64_t total_q, int32_t num_heads,
+                             const void *d_q, int64_t q_tok_stride, int64_t q_head_stride,
+                             void *d_out, int64_t out_tok_stride, int64_t out_head_stride,
+                             float *d_lse, void *d_workspace, size_t workspace_bytes,
+                             kv_stream_t stream);
 
 /* Debug checks of the caller contracts that the in-place kernels rely on
  * (process-wide; off by default).  When on:

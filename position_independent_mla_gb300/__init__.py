@@ -9,6 +9,8 @@ missing, importing the binding's entry points raises.
     kv_splice(pool, ...)         in-place Leyline AMORTIZE / FORGET directive
     kv_splice_composed(pool, ...) several directives per sequence as one edit
     kv_patch(pool, ...)          in-place rank-m patch U_m V_mᵀ
+    kv_quantize / kv_dequantize  rows into an 8-bit pool and back
+    kv_attention(pool, ...)      new tokens' attention over a bf16 or 8-bit pool
 """
 from __future__ import annotations
 
@@ -71,6 +73,45 @@ class kv_patch_desc(C.Structure):
     ]
 
 
+class kv_quant_pool_desc(C.Structure):
+    _fields_ = [
+        ("num_layers", C.c_int32),
+        ("block_size", C.c_int32),
+        ("num_slots", C.c_int64),
+        ("copy_base", C.c_void_p),
+        ("copy_layer_stride", C.c_int64),
+        ("copy_slot_stride", C.c_int64),
+        ("copy_dim", C.c_int32),
+        ("copy_scale", C.c_void_p),
+        ("copy_scale_layer_stride", C.c_int64),
+        ("copy_scale_slot_stride", C.c_int64),
+        ("rot_base", C.c_void_p),
+        ("rot_layer_stride", C.c_int64),
+        ("rot_slot_stride", C.c_int64),
+        ("rot_heads", C.c_int32),
+        ("rot_head_dim", C.c_int32),
+        ("rot_scale", C.c_void_p),
+        ("rot_scale_layer_stride", C.c_int64),
+        ("rot_scale_slot_stride", C.c_int64),
+    ]
+
+
+class kv_attn_desc(C.Structure):
+    _fields_ = [
+        ("num_seqs", C.c_int32),
+        ("max_q_len", C.c_int32),
+        ("max_kv_len", C.c_int32),
+        ("max_blocks", C.c_int32),
+        ("d_q_off", C.c_void_p),
+        ("d_kv_len", C.c_void_p),
+        ("d_block_tables", C.c_void_p),
+        ("causal", C.c_int32),
+        ("window", C.c_int32),
+        ("sinks", C.c_int32),
+        ("scale", C.c_float),
+    ]
+
+
 class kv_splice_tile(C.Structure):
     _fields_ = [
         ("src_lo", C.c_int64),
@@ -99,6 +140,8 @@ def load(build_if_missing: bool = False) -> C.CDLL:
     lib = C.CDLL(LIB_PATH)
     vp, i32, i64, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
     P, PP = C.POINTER(kv_pool_desc), C.POINTER(kv_patch_desc)
+    Q, A = C.POINTER(kv_quant_pool_desc), C.POINTER(kv_attn_desc)
+    attn = [i32, A, i64, i32, vp, i64, i64, vp, i64, i64, vp, vp, sz, vp]
     sig = {
         "kv_workspace_size": (sz, [P, i64, i32]),
         "kv_relocate": (i32, [P, P, i32, i64, vp, vp, vp, vp, vp, vp, i32, i32, PP, vp, sz, vp]),
@@ -121,6 +164,13 @@ def load(build_if_missing: bool = False) -> C.CDLL:
         "kv_cdc": (i32, [i32, vp, i64, vp, C.c_uint64, C.c_uint64, C.c_uint64, i64, vp, vp, vp,
                          vp, sz, vp]),
         "kv_fingerprint": (i32, [i64, vp, vp, i64, vp, C.c_uint64, vp, vp, sz, vp]),
+        "kv_quantize_workspace_size": (sz, [Q]),
+        "kv_quantize": (i32, [P, vp, Q, i32, i64, vp, vp, sz, vp]),
+        "kv_dequantize": (i32, [Q, i32, vp, P, i64, vp, vp, sz, vp]),
+        "kv_attention_workspace_size": (sz, [P, A, i64, i32]),
+        "kv_attention_quant_workspace_size": (sz, [Q, A, i64, i32]),
+        "kv_attention": (i32, [P, *attn]),
+        "kv_attention_quant": (i32, [Q, *attn]),
         "kv_status_string": (C.c_char_p, [i32]),
         "kv_version": (i32, []),
     }
@@ -217,6 +267,50 @@ def patch_desc(rank: int, u: Sequence[Optional[torch.Tensor]],
         if check_extents:
             d.u_rows[ch] = uu.shape[1]
             d.v_slots[ch] = vv.shape[1]
+    return d
+
+
+def quant_pool_desc(copy: torch.Tensor, copy_scale: torch.Tensor, rot: torch.Tensor,
+                    rot_scale: Optional[torch.Tensor], block_size: int,
+                    rot_heads: int) -> kv_quant_pool_desc:
+    """Describe a quantised pool: ``copy`` e4m3 [L][slots][copy_dim] with
+    ``copy_scale`` fp32 [L][slots][copy_dim/128]; ``rot`` e4m3
+    [L][slots][heads*128] with ``rot_scale`` fp32 [L][slots][heads] (head rows),
+    or bf16 [L][slots][64] with None (MLA).  Any strides with a unit last one."""
+    e4m3 = torch.float8_e4m3fn
+    assert copy.dtype == e4m3 and copy_scale.dtype == torch.float32
+    assert rot.dtype == (torch.bfloat16 if rot_scale is None else e4m3)
+    L, S, cd = copy.shape
+    assert rot.shape[:2] == copy.shape[:2] and copy_scale.shape == (L, S, cd // 128)
+    assert copy.stride(2) == 1 and rot.stride(2) == 1 and copy_scale.stride(2) == 1
+    if rot_scale is not None:
+        assert rot_scale.dtype == torch.float32 and rot_scale.stride(2) == 1
+        assert rot_scale.shape == (L, S, rot.shape[2] // 128)
+    rs = (0, 0) if rot_scale is None else rot_scale.stride()[:2]
+    d = kv_quant_pool_desc(
+        L, block_size, S, copy.data_ptr(), copy.stride(0), copy.stride(1), cd,
+        copy_scale.data_ptr(), copy_scale.stride(0), copy_scale.stride(1), rot.data_ptr(),
+        rot.stride(0), rot.stride(1), rot_heads, rot.shape[2] // rot_heads, _ptr(rot_scale), *rs)
+    d._tensors = (copy, copy_scale, rot, rot_scale)
+    return d
+
+
+def attn_desc(q_off: torch.Tensor, kv_len: torch.Tensor, block_tables: torch.Tensor,
+              max_q_len: int, max_kv_len: int, scale: float, causal: bool = True,
+              window: int = 0, sinks: int = 0) -> kv_attn_desc:
+    """Describe a batch for kv_attention; one description serves every layer of
+    a step.  Device int32: ``q_off`` (seqs + 1,) offsets of the new tokens,
+    ``kv_len`` (seqs,) cached tokens with the new ones, ``block_tables``
+    (seqs, max_blocks).  ``window`` > 0 keeps the last ``window`` keys of each
+    query and the first ``sinks`` tokens."""
+    for t in (q_off, kv_len, block_tables):
+        assert t.dtype == torch.int32 and t.is_contiguous()
+    assert block_tables.dim() == 2 and q_off.numel() == kv_len.numel() + 1
+    assert block_tables.shape[0] == kv_len.numel()
+    d = kv_attn_desc(kv_len.numel(), int(max_q_len), int(max_kv_len), block_tables.shape[1],
+                     q_off.data_ptr(), kv_len.data_ptr(), block_tables.data_ptr(), int(causal),
+                     int(window), int(sinks), float(scale))
+    d._tensors = (q_off, kv_len, block_tables)
     return d
 
 
@@ -333,6 +427,84 @@ def kv_patch(pool: kv_pool_desc, num_chunks: int, total_tokens: int, tok_off, ch
         C.byref(patch), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
     if check:
         _check(st, "kv_patch")
+    return st
+
+
+def quant_workspace(pool: kv_quant_pool_desc, device="cuda") -> torch.Tensor:
+    """A device workspace for kv_quantize / kv_dequantize on ``pool``."""
+    n = int(load().kv_quantize_workspace_size(C.byref(pool)))
+    if n == 0:
+        raise KVError(KV_ERR_INVALID_ARG, "kv_quantize_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def kv_quantize(src: kv_pool_desc, src_slots, dst: kv_quant_pool_desc, dst_layer: int,
+                num_rows: int, dst_slots, ws: torch.Tensor, stream=None,
+                check: bool = True) -> int:
+    """Rows of ``src`` (slots ``src_slots``, device int32; None: row i) into the
+    quantised pool's slots ``dst_slots``, layers ``dst_layer`` onwards."""
+    st = load().kv_quantize(C.byref(src), _ptr(src_slots), C.byref(dst), int(dst_layer),
+                            int(num_rows), _ptr(dst_slots), ws.data_ptr(), ws.nbytes,
+                            _stream(stream))
+    if check:
+        _check(st, "kv_quantize")
+    return st
+
+
+def kv_dequantize(src: kv_quant_pool_desc, src_layer: int, src_slots, dst: kv_pool_desc,
+                  num_rows: int, dst_slots, ws: torch.Tensor, stream=None,
+                  check: bool = True) -> int:
+    """Slots ``src_slots`` of the quantised pool back into bf16 rows of ``dst``
+    (slots ``dst_slots``; None: row i)."""
+    st = load().kv_dequantize(C.byref(src), int(src_layer), _ptr(src_slots), C.byref(dst),
+                              int(num_rows), _ptr(dst_slots), ws.data_ptr(), ws.nbytes,
+                              _stream(stream))
+    if check:
+        _check(st, "kv_dequantize")
+    return st
+
+
+def kv_attention_workspace_size(pool, attn: kv_attn_desc, total_q: int, num_heads: int) -> int:
+    """Bytes of workspace for kv_attention on a pool of either kind."""
+    lib = load()
+    f = (lib.kv_attention_quant_workspace_size if isinstance(pool, kv_quant_pool_desc)
+         else lib.kv_attention_workspace_size)
+    return int(f(C.byref(pool), C.byref(attn), int(total_q), int(num_heads)))
+
+
+def attn_workspace(pool, attn: kv_attn_desc, q: torch.Tensor) -> torch.Tensor:
+    """A device workspace for kv_attention of queries like ``q``."""
+    n = kv_attention_workspace_size(pool, attn, q.shape[0], q.shape[1])
+    if n == 0:
+        raise KVError(KV_ERR_INVALID_ARG, "kv_attention_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def kv_attention(pool, layer: int, attn: kv_attn_desc, q: torch.Tensor, out: torch.Tensor,
+                 lse: Optional[torch.Tensor], ws: torch.Tensor, stream=None,
+                 check: bool = True) -> int:
+    """Attention of the new tokens ``q`` bf16 (tokens, heads, key width) over
+    layer ``layer`` of ``pool`` (a kv_pool_desc or a kv_quant_pool_desc) into
+    ``out`` bf16 (tokens, heads, value width) and ``lse`` fp32 (tokens, heads)
+    or None.  Key / value width: 128 / 128, MLA 576 / 512."""
+    n, heads, dk = q.shape
+    mla = pool.rot_heads == 1
+    if (q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16
+            or dk != (pool.copy_dim + pool.rot_head_dim if mla else pool.rot_head_dim)
+            or out.shape != (n, heads, pool.copy_dim if mla else dk)
+            or q.stride(2) != 1 or out.stride(2) != 1):
+        raise ValueError("kv_attention: q (tokens, heads, key width) and out (tokens, heads, "
+                         "value width) must be bf16 with a unit last stride")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, heads)
+                            or not lse.is_contiguous()):
+        raise ValueError("kv_attention: lse must be contiguous fp32 (tokens, heads)")
+    lib = load()
+    f = lib.kv_attention_quant if isinstance(pool, kv_quant_pool_desc) else lib.kv_attention
+    st = f(C.byref(pool), layer, C.byref(attn), n, heads, q.data_ptr(), q.stride(0), q.stride(1),
+           out.data_ptr(), out.stride(0), out.stride(1), None if lse is None else lse.data_ptr(),
+           ws.data_ptr(), ws.nbytes, _stream(stream))
+    if check:
+        _check(st, "kv_attention")
     return st
 
 

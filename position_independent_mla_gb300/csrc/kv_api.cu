@@ -5,6 +5,7 @@
 // the launches.  Every step of the data path runs in the kernels.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <map>
@@ -13,6 +14,7 @@
 
 #include "kvreloc.h"
 #include "kv_launch.h"
+#include "kv_serve.h"
 
 using namespace kvr;
 
@@ -1106,9 +1108,18 @@ kv_status kv_get_device_status(const void *d_workspace, kv_stream_t stream)
         return KV_ERR_WORKSPACE;
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return KV_ERR_CUDA;
-    uint32_t st = 0;
-    if (cudaMemcpy(&st, d_workspace, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess)
+    uint32_t head[kHeaderCountWord + 1];
+    if (cudaMemcpy(head, d_workspace, sizeof head, cudaMemcpyDeviceToHost) != cudaSuccess)
         return KV_ERR_CUDA;
+    uint32_t st = head[0];
+    if (head[kHeaderCountWord] > 0) { // one word per block of the call (kv_serve.h)
+        std::vector<uint32_t> words(head[kHeaderCountWord]);
+        if (cudaMemcpy(words.data(), static_cast<const char *>(d_workspace) + kHeaderBytes,
+                       words.size() * sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
+            return KV_ERR_CUDA;
+        for (size_t i = 0; i < words.size() && st == kStatusOk; ++i)
+            st = words[i];
+    }
     return static_cast<kv_status>(st);
 }
 
@@ -1172,6 +1183,286 @@ const char *kv_status_string(kv_status s)
 }
 
 int32_t kv_version(void) { return 200; }
+
+} // extern "C"
+
+// ---------------------------------------------------------------------------
+// Quantised rows and attention over the paged cache
+// ---------------------------------------------------------------------------
+
+namespace {
+
+bool quant_pool_ok(const kv_quant_pool_desc *p)
+{
+    if (!p)
+        return false;
+    if (p->num_layers <= 0 || p->block_size <= 0 || p->num_slots <= 0 ||
+        p->num_slots % p->block_size != 0 || p->copy_dim <= 0 || p->copy_dim % kGroup != 0 ||
+        p->rot_heads <= 0 || p->rot_head_dim <= 0 || p->rot_head_dim % 16 != 0)
+        return false;
+    if (!p->copy_base || !p->rot_base || !p->copy_scale || !aligned16(p->copy_base) ||
+        !aligned16(p->rot_base) || !aligned_to(p->copy_scale, 4) || !aligned_to(p->rot_scale, 4))
+        return false;
+    const int64_t rot_unit = p->rot_scale ? 16 : 8;
+    const int64_t s[4] = {p->copy_layer_stride, p->copy_slot_stride, p->rot_layer_stride,
+                          p->rot_slot_stride};
+    for (int i = 0; i < 4; ++i)
+        if (s[i] < 0 || s[i] % (i < 2 ? 16 : rot_unit) != 0)
+            return false;
+    return p->copy_scale_layer_stride >= 0 && p->copy_scale_slot_stride >= 0 &&
+           p->rot_scale_layer_stride >= 0 && p->rot_scale_slot_stride >= 0;
+}
+
+// The bf16 shape of a quantised pool's rows; e4m3 K needs 128-wide heads, and
+// MLA rows keep k_pe in bf16.
+bool quant_row_kind(const kv_quant_pool_desc *p, RowKind *kind)
+{
+    kv_pool_desc d{};
+    d.copy_dim = p->copy_dim;
+    d.rot_heads = p->rot_heads;
+    d.rot_head_dim = p->rot_head_dim;
+    return row_kind(&d, kind) && (*kind == RowKind::Mla) == (p->rot_scale == nullptr);
+}
+
+QuantView quant_view(const kv_quant_pool_desc *p, int64_t layer)
+{
+    const int64_t rb = p->rot_scale ? 1 : 2;
+    QuantView v;
+    v.copy_ls = p->copy_layer_stride;
+    v.copy_ss = p->copy_slot_stride;
+    v.copy = static_cast<char *>(p->copy_base) + layer * v.copy_ls;
+    v.cs_ls = p->copy_scale_layer_stride;
+    v.cs_ss = p->copy_scale_slot_stride;
+    v.cs = p->copy_scale + layer * v.cs_ls;
+    v.rot_ls = p->rot_layer_stride * rb;
+    v.rot_ss = p->rot_slot_stride * rb;
+    v.rot = static_cast<char *>(p->rot_base) + layer * v.rot_ls;
+    v.rs_ls = p->rot_scale_layer_stride;
+    v.rs_ss = p->rot_scale_slot_stride;
+    v.rs = p->rot_scale ? p->rot_scale + layer * v.rs_ls : nullptr;
+    v.num_slots = p->num_slots;
+    return v;
+}
+
+constexpr size_t kQuantWorkspace = kHeaderBytes + ((kQuantMaxBlocks * 4 + 255) / 256) * 256;
+
+// Shared body of kv_quantize (read = false) and kv_dequantize.
+kv_status quant_impl(const kv_quant_pool_desc *pool, int32_t layer, const int32_t *pool_slots,
+                     const kv_pool_desc *rows, const int32_t *row_slots, int64_t num_rows,
+                     void *ws, size_t ws_bytes, cudaStream_t stream, bool read)
+{
+    t_launches = 0;
+    if (!quant_pool_ok(pool) || !pool_ok(rows))
+        return KV_ERR_INVALID_ARG;
+    if (rows->copy_dim != pool->copy_dim || rows->rot_heads != pool->rot_heads ||
+        rows->rot_head_dim != pool->rot_head_dim)
+        return KV_ERR_INVALID_ARG;
+    RowKind kind;
+    if (!quant_row_kind(pool, &kind))
+        return KV_ERR_UNSUPPORTED;
+    if (layer < 0 || layer > pool->num_layers - rows->num_layers || num_rows < 0 ||
+        num_rows > 0x7FFFFFFFll)
+        return KV_ERR_INVALID_ARG;
+    if ((num_rows > 0 && !pool_slots) || !aligned_to(pool_slots, 4) || !aligned_to(row_slots, 4))
+        return KV_ERR_INVALID_ARG;
+    if (!row_slots && num_rows > rows->num_slots)
+        return KV_ERR_INVALID_ARG;
+    kv_status st = ws_ok(ws, ws_bytes, kQuantWorkspace);
+    if (st != KV_OK)
+        return st;
+    if (num_rows == 0) {
+        KV_CUDA(cudaMemsetAsync(ws, 0, kHeaderBytes, stream));
+        return KV_OK;
+    }
+    QuantParams qp{};
+    qp.rows = view_of(rows);
+    qp.pool = quant_view(pool, layer);
+    qp.row_slot = row_slots;
+    qp.pool_slot = pool_slots;
+    qp.num_rows = num_rows;
+    qp.layers = rows->num_layers;
+    qp.header = static_cast<uint32_t *>(ws);
+    KV_CUDA(mark(t_ev_start, stream));
+    KV_CUDA(read ? launch_dequantize(qp, kind, stream) : launch_quantize(qp, kind, stream));
+    ++t_launches;
+    KV_CUDA(mark(t_ev_stop, stream));
+    return KV_OK;
+}
+
+// Argument checks shared by the attention calls and their workspace sizes.
+kv_status attn_ok(const kv_attn_desc *a, int64_t total_q, int32_t heads, int32_t kv_heads)
+{
+    if (!a || a->num_seqs < 0 || a->max_q_len < 0 || a->max_kv_len < 0 || a->max_blocks < 0 ||
+        total_q < 0 || total_q > 0x7FFFFFFFll || heads <= 0 || heads % kv_heads != 0)
+        return KV_ERR_INVALID_ARG;
+    if ((a->causal != 0 && a->causal != 1) || a->window < 0 || a->sinks < 0 ||
+        (a->window > 0 && !a->causal) || !(a->scale > 0.0f) || !(a->scale < INFINITY))
+        return KV_ERR_INVALID_ARG;
+    if (total_q > (int64_t)a->num_seqs * a->max_q_len)
+        return KV_ERR_INVALID_ARG;
+    return heads / kv_heads > 128 ? KV_ERR_UNSUPPORTED : KV_OK;
+}
+
+size_t attn_workspace(const kv_attn_desc *, int64_t, int32_t) { return kHeaderBytes; }
+
+kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind kind,
+                         int64_t num_slots, int32_t block, int32_t kv_heads,
+                         const kv_attn_desc *a, int64_t total_q, int32_t heads, const void *q,
+                         int64_t q_ts, int64_t q_hs, void *out, int64_t o_ts, int64_t o_hs,
+                         float *lse, void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    kv_status st = attn_ok(a, total_q, heads, kv_heads);
+    if (st != KV_OK)
+        return st;
+    const int64_t strides[4] = {q_ts, q_hs, o_ts, o_hs};
+    for (int64_t s : strides)
+        if (s < 0 || s % 8 != 0)
+            return KV_ERR_INVALID_ARG;
+    if (total_q > 0 && (!q || !out || !a->d_q_off || !a->d_kv_len ||
+                        (a->max_kv_len > 0 && (!a->d_block_tables || a->max_blocks == 0))))
+        return KV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned_to(lse, 4) || !aligned_to(a->d_q_off, 4) ||
+        !aligned_to(a->d_kv_len, 4) || !aligned_to(a->d_block_tables, 4))
+        return KV_ERR_INVALID_ARG;
+    if ((st = ws_ok(ws, ws_bytes, attn_workspace(a, total_q, heads))) != KV_OK)
+        return st;
+    KV_CUDA(cudaMemsetAsync(ws, 0, kHeaderBytes, stream));
+    if (total_q == 0)
+        return KV_OK;
+    AttnParams p{};
+    if (quant) {
+        p.copy = quant->copy;
+        p.rot = quant->rot;
+        p.copy_ss = quant->copy_ss;
+        p.rot_ss = quant->rot_ss;
+        p.cs = quant->cs;
+        p.cs_ss = quant->cs_ss;
+        p.rs = quant->rs;
+        p.rs_ss = quant->rs_ss;
+    } else {
+        p.copy = bf16->copy;
+        p.rot = bf16->rot;
+        p.copy_ss = bf16->copy_ss;
+        p.rot_ss = bf16->rot_ss;
+    }
+    p.num_blocks = num_slots / block;
+    p.block = block;
+    p.q = static_cast<const char *>(q);
+    p.q_ts = q_ts * 2;
+    p.q_hs = q_hs * 2;
+    p.out = static_cast<char *>(out);
+    p.o_ts = o_ts * 2;
+    p.o_hs = o_hs * 2;
+    p.lse = lse;
+    p.total_q = total_q;
+    p.heads = heads;
+    p.group = heads / kv_heads;
+    p.num_seqs = a->num_seqs;
+    p.max_q_len = a->max_q_len;
+    p.max_kv_len = a->max_kv_len;
+    p.max_blocks = a->max_blocks;
+    p.q_off = a->d_q_off;
+    p.kv_len = a->d_kv_len;
+    p.block_tables = a->d_block_tables;
+    p.causal = a->causal;
+    p.window = a->window;
+    p.sinks = a->sinks;
+    p.scale = a->scale;
+    p.header = static_cast<uint32_t *>(ws);
+    KV_CUDA(mark(t_ev_start, stream));
+    KV_CUDA(launch_attention(p, kind, stream));
+    ++t_launches;
+    KV_CUDA(mark(t_ev_stop, stream));
+    return KV_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+size_t kv_quantize_workspace_size(const kv_quant_pool_desc *pool)
+{
+    return quant_pool_ok(pool) ? kQuantWorkspace : 0;
+}
+
+kv_status kv_quantize(const kv_pool_desc *src, const int32_t *d_src_slots,
+                      const kv_quant_pool_desc *dst, int32_t dst_layer, int64_t num_rows,
+                      const int32_t *d_dst_slots, void *d_workspace, size_t workspace_bytes,
+                      kv_stream_t stream)
+{
+    return quant_impl(dst, dst_layer, d_dst_slots, src, d_src_slots, num_rows, d_workspace,
+                      workspace_bytes, reinterpret_cast<cudaStream_t>(stream), false);
+}
+
+kv_status kv_dequantize(const kv_quant_pool_desc *src, int32_t src_layer,
+                        const int32_t *d_src_slots, const kv_pool_desc *dst, int64_t num_rows,
+                        const int32_t *d_dst_slots, void *d_workspace, size_t workspace_bytes,
+                        kv_stream_t stream)
+{
+    return quant_impl(src, src_layer, d_src_slots, dst, d_dst_slots, num_rows, d_workspace,
+                      workspace_bytes, reinterpret_cast<cudaStream_t>(stream), true);
+}
+
+size_t kv_attention_workspace_size(const kv_pool_desc *pool, const kv_attn_desc *attn,
+                                   int64_t total_q, int32_t num_heads)
+{
+    RowKind kind;
+    if (!pool_ok(pool) || !row_kind(pool, &kind) ||
+        attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK)
+        return 0;
+    return attn_workspace(attn, total_q, num_heads);
+}
+
+size_t kv_attention_quant_workspace_size(const kv_quant_pool_desc *pool, const kv_attn_desc *attn,
+                                         int64_t total_q, int32_t num_heads)
+{
+    RowKind kind;
+    if (!quant_pool_ok(pool) || !quant_row_kind(pool, &kind) ||
+        attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK)
+        return 0;
+    return attn_workspace(attn, total_q, num_heads);
+}
+
+kv_status kv_attention(const kv_pool_desc *pool, int32_t layer, const kv_attn_desc *attn,
+                       int64_t total_q, int32_t num_heads, const void *d_q, int64_t q_tok_stride,
+                       int64_t q_head_stride, void *d_out, int64_t out_tok_stride,
+                       int64_t out_head_stride, float *d_lse, void *d_workspace,
+                       size_t workspace_bytes, kv_stream_t stream)
+{
+    t_launches = 0;
+    if (!pool_ok(pool) || layer < 0 || layer >= pool->num_layers)
+        return KV_ERR_INVALID_ARG;
+    RowKind kind;
+    if (!row_kind(pool, &kind))
+        return KV_ERR_UNSUPPORTED;
+    PoolView v = view_of(pool);
+    v.copy += layer * v.copy_ls;
+    v.rot += layer * v.rot_ls;
+    return attention_impl(&v, nullptr, kind, pool->num_slots, pool->block_size, pool->rot_heads,
+                          attn, total_q, num_heads, d_q, q_tok_stride, q_head_stride, d_out,
+                          out_tok_stride, out_head_stride, d_lse, d_workspace, workspace_bytes,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+kv_status kv_attention_quant(const kv_quant_pool_desc *pool, int32_t layer,
+                             const kv_attn_desc *attn, int64_t total_q, int32_t num_heads,
+                             const void *d_q, int64_t q_tok_stride, int64_t q_head_stride,
+                             void *d_out, int64_t out_tok_stride, int64_t out_head_stride,
+                             float *d_lse, void *d_workspace, size_t workspace_bytes,
+                             kv_stream_t stream)
+{
+    t_launches = 0;
+    if (!quant_pool_ok(pool) || layer < 0 || layer >= pool->num_layers)
+        return KV_ERR_INVALID_ARG;
+    RowKind kind;
+    if (!quant_row_kind(pool, &kind))
+        return KV_ERR_UNSUPPORTED;
+    const QuantView v = quant_view(pool, layer);
+    return attention_impl(nullptr, &v, kind, pool->num_slots, pool->block_size, pool->rot_heads,
+                          attn, total_q, num_heads, d_q, q_tok_stride, q_head_stride, d_out,
+                          out_tok_stride, out_head_stride, d_lse, d_workspace, workspace_bytes,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
 
 } // extern "C"
 

@@ -1,0 +1,80 @@
+// kv_serve.h -- parameters and launchers of the serving operators: quantised
+// cache rows (kv_quant.cu) and attention over the paged cache (kv_attention.cu).
+#pragma once
+
+#include "kv_launch.h"
+
+namespace kvr {
+
+constexpr int kGroup = 128; // values that share one scale of a quantised row
+
+// Status of a call without a clearing launch: every block of the call's main
+// kernel writes its own word after the workspace header (0 or an error code)
+// and block 0 writes the header, so nothing needs to be zero beforehand;
+// kv_get_device_status scans the words.
+constexpr int kHeaderCountWord = 8; // header word: number of block words (0: word 0 holds all)
+
+__device__ __forceinline__ void write_block_status(uint32_t *header, uint32_t code,
+                                                   uint32_t block, uint32_t blocks)
+{
+    header[kHeaderBytes / 4 + block] = code;
+    if (block == 0) {
+        header[0] = kStatusOk;
+        header[kHeaderCountWord] = blocks;
+    }
+}
+
+// A quantised pool as the kernels see it: byte addresses and byte strides,
+// scales in floats.
+struct QuantView {
+    char *copy;
+    int64_t copy_ls, copy_ss;
+    float *cs;
+    int64_t cs_ls, cs_ss;
+    char *rot;
+    int64_t rot_ls, rot_ss;
+    float *rs; // nullptr: rot is bf16
+    int64_t rs_ls, rs_ss;
+    int64_t num_slots;
+};
+
+struct QuantParams {
+    PoolView rows;           // the bf16 side
+    QuantView pool;          // at its first layer of the call
+    const int32_t *row_slot; // bf16 side: slot of row i (nullptr: i)
+    const int32_t *pool_slot;
+    int64_t num_rows;
+    int32_t layers;
+    uint32_t *header;
+};
+
+cudaError_t launch_quantize(const QuantParams &p, RowKind kind, cudaStream_t stream);
+cudaError_t launch_dequantize(const QuantParams &p, RowKind kind, cudaStream_t stream);
+constexpr int kQuantMaxBlocks = 152 * 8; // persistent grid of both
+
+struct AttnParams {
+    // one layer of the pool: bf16 rows, or e4m3 rows with scales (cs != nullptr)
+    const char *copy, *rot;
+    int64_t copy_ss, rot_ss; // bytes
+    const float *cs, *rs;    // scales (floats per slot: cs_ss, rs_ss)
+    int64_t cs_ss, rs_ss;
+    int64_t num_blocks;
+    int32_t block;
+    // queries and results, byte strides
+    const char *q;
+    int64_t q_ts, q_hs;
+    char *out;
+    int64_t o_ts, o_hs;
+    float *lse;
+    int64_t total_q;
+    int32_t heads, group; // query heads; query heads per key head
+    int32_t num_seqs, max_q_len, max_kv_len, max_blocks;
+    const int32_t *q_off, *kv_len, *block_tables;
+    int32_t causal, window, sinks;
+    float scale;
+    uint32_t *header;
+};
+
+cudaError_t launch_attention(const AttnParams &p, RowKind kind, cudaStream_t stream);
+
+} // namespace kvr
