@@ -1303,7 +1303,36 @@ kv_status attn_ok(const kv_attn_desc *a, int64_t total_q, int32_t heads, int32_t
     return heads / kv_heads > 128 ? KV_ERR_UNSUPPORTED : KV_OK;
 }
 
-size_t attn_workspace(const kv_attn_desc *, int64_t, int32_t) { return kHeaderBytes; }
+AttnPlan attn_plan(RowKind kind, const kv_attn_desc *a, int64_t total_q, int32_t heads,
+                   int32_t kv_heads)
+{
+    AttnShape s{};
+    s.total_q = total_q;
+    s.num_seqs = a->num_seqs;
+    s.max_q_len = a->max_q_len;
+    s.max_kv_len = a->max_kv_len;
+    s.window = a->window;
+    s.sinks = a->sinks;
+    s.group = heads / kv_heads;
+    s.kv_heads = kv_heads;
+    return plan_attention(kind, s);
+}
+
+// Workspace: header, a status word per block, then (keys split) the parts' lse
+// and the parts.
+struct AttnLayout {
+    size_t lse, part, bytes;
+};
+
+AttnLayout attn_layout(RowKind kind, const AttnPlan &pl, int64_t total_q, int32_t heads)
+{
+    const size_t rows = pl.max_splits > 1 ? (size_t)pl.max_splits * total_q * heads : 0;
+    AttnLayout l;
+    l.lse = align256(kHeaderBytes + (size_t)pl.blocks * 4);
+    l.part = align256(l.lse + rows * 4);
+    l.bytes = align256(l.part + rows * (kind == RowKind::Mla ? 512 : 128) * 4);
+    return l;
+}
 
 kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind kind,
                          int64_t num_slots, int32_t block, int32_t kv_heads,
@@ -1314,7 +1343,8 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
     kv_status st = attn_ok(a, total_q, heads, kv_heads);
     if (st != KV_OK)
         return st;
-    const int64_t strides[4] = {q_ts, q_hs, o_ts, o_hs};
+    const int64_t strides[4] = {total_q > 1 ? q_ts : 0, heads > 1 ? q_hs : 0,
+                                total_q > 1 ? o_ts : 0, heads > 1 ? o_hs : 0};
     for (int64_t s : strides)
         if (s < 0 || s % 8 != 0)
             return KV_ERR_INVALID_ARG;
@@ -1324,11 +1354,16 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
     if (!aligned16(q) || !aligned16(out) || !aligned_to(lse, 4) || !aligned_to(a->d_q_off, 4) ||
         !aligned_to(a->d_kv_len, 4) || !aligned_to(a->d_block_tables, 4))
         return KV_ERR_INVALID_ARG;
-    if ((st = ws_ok(ws, ws_bytes, attn_workspace(a, total_q, heads))) != KV_OK)
+    const AttnPlan pl = attn_plan(kind, a, total_q, heads, kv_heads);
+    const AttnLayout lay = attn_layout(kind, pl, total_q, heads);
+    if (pl.blocks > 0x7FFFFFFFll)
+        return KV_ERR_INVALID_ARG;
+    if ((st = ws_ok(ws, ws_bytes, lay.bytes)) != KV_OK)
         return st;
-    KV_CUDA(cudaMemsetAsync(ws, 0, kHeaderBytes, stream));
-    if (total_q == 0)
+    if (total_q == 0) {
+        KV_CUDA(cudaMemsetAsync(ws, 0, kHeaderBytes, stream));
         return KV_OK;
+    }
     AttnParams p{};
     if (quant) {
         p.copy = quant->copy;
@@ -1368,10 +1403,15 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
     p.window = a->window;
     p.sinks = a->sinks;
     p.scale = a->scale;
+    p.split_tiles = pl.split_tiles;
+    p.max_splits = pl.max_splits;
+    p.part_lse = reinterpret_cast<float *>(static_cast<char *>(ws) + lay.lse);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + lay.part);
+    p.wait_limit_ns = g_wait_limit_ns.load();
     p.header = static_cast<uint32_t *>(ws);
     KV_CUDA(mark(t_ev_start, stream));
-    KV_CUDA(launch_attention(p, kind, stream));
-    ++t_launches;
+    KV_CUDA(launch_attention(p, kind, pl, stream));
+    t_launches += pl.max_splits > 1 ? 2 : 1;
     KV_CUDA(mark(t_ev_stop, stream));
     return KV_OK;
 }
@@ -1410,7 +1450,9 @@ size_t kv_attention_workspace_size(const kv_pool_desc *pool, const kv_attn_desc 
     if (!pool_ok(pool) || !row_kind(pool, &kind) ||
         attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK)
         return 0;
-    return attn_workspace(attn, total_q, num_heads);
+    return attn_layout(kind, attn_plan(kind, attn, total_q, num_heads, pool->rot_heads), total_q,
+                       num_heads)
+        .bytes;
 }
 
 size_t kv_attention_quant_workspace_size(const kv_quant_pool_desc *pool, const kv_attn_desc *attn,
@@ -1420,7 +1462,9 @@ size_t kv_attention_quant_workspace_size(const kv_quant_pool_desc *pool, const k
     if (!quant_pool_ok(pool) || !quant_row_kind(pool, &kind) ||
         attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK)
         return 0;
-    return attn_workspace(attn, total_q, num_heads);
+    return attn_layout(kind, attn_plan(kind, attn, total_q, num_heads, pool->rot_heads), total_q,
+                       num_heads)
+        .bytes;
 }
 
 kv_status kv_attention(const kv_pool_desc *pool, int32_t layer, const kv_attn_desc *attn,

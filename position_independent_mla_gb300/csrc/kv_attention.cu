@@ -1,10 +1,36 @@
-// kv_attention.cu -- attention of new tokens over the paged cache.
+// kv_attention.cu -- attention of new tokens over the paged cache on the
+// 5th-generation tensor cores (tcgen05).
 //
-// The plainest form: a block per (query token, head), a warp per key, the
-// running maximum and sum of the softmax in registers, the four warps' parts
-// joined at the end.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+//     S = scale * Q Kᵀ,  O = softmax(S) V,  lse = log Σ exp(S)
+//
+// for one layer of a paged pool, with one pass over the keys: for a tile of
+// keys the running maximum m and sum l of every query row are updated, the
+// weights 2^((s - m) * scale * log2 e) are rounded to bf16 and multiplied with
+// V onto the accumulator O, which is rescaled when m moves.
+//
+// Rows.  The query heads that share a key head are packed with the tokens:
+// row r of a (sequence, key head) is token r / group, head r % group, and a
+// block owns NT tiles of 128 rows (the M of one MMA).  So 32 query heads of one
+// new token over 8 key heads read each key once, and a chunk of many tokens
+// fills whole tiles.
+//
+// Roles of a block's four warpgroups (512 threads):
+//   softmax  a thread per row: reads its row of S from tensor memory, masks,
+//            keeps m and l in registers, writes the bf16 weights back over S
+//            (they are the A operand of the second MMA) and at the end O / l;
+//   load     bring rows of the pool through the block table into shared memory
+//            in the 128-byte swizzled layout that the MMAs read;
+//   mma      one thread issues every MMA.
+// O stays in tensor memory.  It is rescaled only when some row's maximum grew by
+// more than 2^8 since it was last fixed: until then the weights stay below 2^8,
+// which fp32 sums and bf16 weights hold without loss.
+//
+// Long axes are split: blocks take runs of `split_tiles` key tiles of a row
+// tile, write normalised fp32 parts with their lse, and a second kernel joins
+// them.  The split depends only on sizes, so results repeat bit for bit.
+//
+// Every wait is bounded; a block whose wait runs out reports KV_ERR_TIMEOUT.
+#include <algorithm>
 
 #include "kv_device.cuh"
 #include "kv_serve.h"
@@ -13,135 +39,1364 @@ namespace kvr {
 
 namespace {
 
-constexpr int kSimpleThreads = 128;
+constexpr int kRows = 128;         // rows per tile: the M of an MMA
+constexpr int kAttnThreads = 512;  // four warpgroups
+constexpr int kRegMma = 56;        // registers of a thread of the MMA warpgroup
+constexpr float kLazy = 8.0f;      // log2 of the growth of a maximum that O tolerates
 
-// N values at element `at` of a row: bf16, or e4m3 times the group's scale.
-template <int N>
-__device__ __forceinline__ void load_row(const char *row, const float *scale, int at, float *v)
+// ---------------------------------------------------------------------------
+// PTX pieces
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p)
 {
-    if (scale) {
-        const float s = scale[at / kGroup];
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void bar_signal(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Signals `bar` when this thread's earlier cp.async copies have landed.
+__device__ __forceinline__ void bar_signal_copies(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Signals `bar` when every MMA this thread issued before has finished.
+__device__ __forceinline__ void bar_signal_mma(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                 "selp.b32 %0, 1, 0, p;\n}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
+// Bounded wait for a phase; false when it ran out here or elsewhere in the
+// block (*abort).
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity,
+                                                  volatile int *abort, int64_t limit_ns)
+{
+    const uint64_t t0 = global_ns();
+    for (uint32_t it = 0; it < (1u << 26); ++it) {
+        if (bar_try(bar, parity))
+            return true;
+        if ((it & 15u) == 15u && (*abort || (int64_t)(global_ns() - t0) > limit_ns))
+            break;
+    }
+    *abort = 1;
+    return false;
+}
+
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *abort,
+                                         int64_t limit_ns)
+{
+    return bar_try(bar, parity) || bar_wait_slow(bar, parity, abort, limit_ns);
+}
+
+__device__ __forceinline__ void mma_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void mma_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <int R>
+__device__ __forceinline__ void reg_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+template <int R>
+__device__ __forceinline__ void reg_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// 16-byte copy to shared memory; bytes = 0 writes zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void sts16(uint32_t dst, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t src)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(src)
+                 : "memory");
+    return v;
+}
+
+#define KV_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), \
+                    "=r"(a[i + 5]), "=r"(a[i + 6]), "=r"(a[i + 7])
+#define KV_P8(a, i) "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3]), "+r"(a[i + 4]), \
+                    "+r"(a[i + 5]), "+r"(a[i + 6]), "+r"(a[i + 7])
+#define KV_W8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), \
+                    "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
+
+// 32 columns of this thread's tensor-memory lane (no wait).
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : KV_R8(r, 0), KV_R8(r, 8), KV_R8(r, 16), KV_R8(r, 24)
+                 : "r"(addr));
+}
+
+// Uses of r stay behind the wait that comes before this.
+__device__ __forceinline__ void tmem_pin32(uint32_t *r)
+{
+    asm volatile("" : KV_P8(r, 0), KV_P8(r, 8), KV_P8(r, 16), KV_P8(r, 24));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::KV_W8(r, 0),
+                 KV_W8(r, 8), KV_W8(r, 16), KV_W8(r, 24), "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::KV_W8(r, 0),
+                 KV_W8(r, 8), "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand in panels of 64 bf16 columns: rows of 128 bytes, the
+// 16-byte piece c of row r at c ^ (r & 7) (128-byte swizzle), 1024 bytes per
+// eight rows.  Along a K-major operand the next 16 columns are 32 bytes on;
+// of an MN-major one (V: the MMA's N runs along the row) the next 16 keys are
+// 2048 bytes on and the next 64 columns `lead` bytes.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
+           ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// kind::f16: D fp32, A and B bf16; B along K (0) or along N (1).
+template <int N, int BMAJOR>
+__device__ __forceinline__ constexpr uint32_t mma_desc()
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)BMAJOR << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+
+template <int N>
+__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t acc)
+{
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(mma_desc<N, 0>()), "r"(acc)
+                 : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t acc)
+{
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(mma_desc<N, 1>()), "r"(acc)
+                 : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Four e4m3 values to bf16 pairs, times 2^120 and `mul` (a bf16 pair).  Moved
+// into a bf16's exponent and top mantissa bits a value reads 2^-120 of itself,
+// subnormal ones included, so one exact product puts it right.
+__device__ __forceinline__ uint2 e4m3_bf16(uint32_t w, uint32_t mul, uint32_t mul2, bool two)
+{
+    uint2 r;
+    uint32_t *o = &r.x;
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            uint32_t h2;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(*reinterpret_cast<const uint16_t *>(row + at + i)));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-            v[i] = f.x * s;
-            v[i + 1] = f.y * s;
-        }
-    } else {
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t y = __byte_perm(w, 0, i == 0 ? 0x1404 : 0x3424); // bytes at 15..8, 31..24
+        uint32_t b = (y & 0x80008000u) | ((y & 0x7F007F00u) >> 4);
+        // 0x7F is NaN in e4m3: 480 as plain bits
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(mul));
+        if (two)
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(mul2));
+        o[i] = b;
+    }
+    return r;
+}
+
+// A value of 0x7F or 0xFF among four e4m3 values.
+__device__ __forceinline__ bool e4m3_has_nan(uint32_t w)
+{
+    const uint32_t m = w & 0x7F7F7F7Fu;
+    return ((m + 0x01010101u) & 0x80808080u) != 0u;
+}
+
+// Sixteen e4m3 values (one 16-byte piece) to two pieces of bf16, scale 2^e.
+__device__ __forceinline__ void convert16(uint4 v, float scale, uint4 &lo, uint4 &hi)
+{
+    // scale = 2^e: bf16 bits of 2^(120 + min(e, 7)), and of what is left of e
+    const int e = (int)(__float_as_uint(scale) >> 23) - 127;
+    const int e1 = min(e, 7);
+    const uint32_t m1 = (uint32_t)(120 + e1 + 127) << 7, m2 = (uint32_t)(e - e1 + 127) << 7;
+    const uint32_t a = m1 * 0x10001u, b = m2 * 0x10001u;
+    const bool two = e > 7;
+    const uint2 r0 = e4m3_bf16(v.x, a, b, two), r1 = e4m3_bf16(v.y, a, b, two);
+    const uint2 r2 = e4m3_bf16(v.z, a, b, two), r3 = e4m3_bf16(v.w, a, b, two);
+    lo = make_uint4(r0.x, r0.y, r1.x, r1.y);
+    hi = make_uint4(r2.x, r2.y, r3.x, r3.y);
+    if (e4m3_has_nan(v.x) || e4m3_has_nan(v.y) || e4m3_has_nan(v.z) || e4m3_has_nan(v.w)) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t *o[2] = {&lo.x, &hi.x};
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(row + (at + i) * 2);
-            v[i] = __uint_as_float(w << 16);
-            v[i + 1] = __uint_as_float(w & 0xFFFF0000u);
-        }
+        for (int i = 0; i < 16; ++i)
+            if (((w[i >> 2] >> ((i & 3) * 8)) & 0x7Fu) == 0x7Fu)
+                o[i >> 3][(i & 7) >> 1] |= (i & 1) ? 0x7FC00000u : 0x7FC0u;
     }
 }
 
-template <bool MLA>
-__global__ void __launch_bounds__(kSimpleThreads) attention_simple_kernel(
+// Zeroes the values of a bf16 pair that are not finite; true if any was.
+__device__ __forceinline__ bool drop_nonfinite(uint32_t &w)
+{
+    const bool lo = (w & 0x7F80u) == 0x7F80u, hi = (w & 0x7F800000u) == 0x7F800000u;
+    w &= (lo ? 0xFFFF0000u : ~0u) & (hi ? 0x0000FFFFu : ~0u);
+    return lo || hi;
+}
+
+// ---------------------------------------------------------------------------
+// Geometry
+// ---------------------------------------------------------------------------
+
+// Head rows: K and V tiles of 128 keys x 128, a ring of stages.
+template <bool QUANT_, int NT_>
+struct HeadGeo {
+    static constexpr bool MLA = false, QUANT = QUANT_;
+    static constexpr int NT = NT_, KT = 128;
+    static constexpr int QPANELS = 2, OC = 128;    // panels of a query row; columns of O
+    static constexpr int DV = 128;
+    static constexpr int LOAD_WG = NT == 2 ? 1 : 2; // load warpgroups
+    static constexpr int STAGE = 2 * 128 * 128;    // bytes of a K or V tile
+    static constexpr int STAGES = NT == 2 ? 5 : 6;
+    static constexpr int BARS = 2 * STAGES;
+    static constexpr int RING = STAGES * STAGE;
+    static constexpr int REG_SOFTMAX = NT == 2 ? 168 : 200;
+    static constexpr int REG_LOAD = 120;
+    // columns of tensor memory: S (and P over it) per tile or per buffer, O
+    static constexpr int S_COL(int i) { return i * 128; }
+    static constexpr int O_COL(int t) { return 256 + t * 128; }
+};
+
+// MLA rows: a tile of 64 latent rows is both K (9 panels: 512 + 64 columns) and
+// V; a block makes one half of the 512 value columns (O of 128 x 512 fp32 would
+// fill tensor memory).  Q takes 144 KB of shared memory, so there is one tile of
+// rows, in two parts: the value panels of this half, and the other five; the
+// next tile waits in the load threads' registers.
+template <bool QUANT_>
+struct MlaGeo {
+    static constexpr bool MLA = true, QUANT = QUANT_;
+    static constexpr int NT = 1, KT = 64;
+    static constexpr int QPANELS = 9, OC = 256;
+    static constexpr int DV = 512;
+    static constexpr int LOAD_WG = 2;
+    static constexpr int PANEL = 64 * 128;
+    static constexpr int BARS = 4; // full, empty of the two parts
+    static constexpr int RING = 9 * PANEL;
+    static constexpr int REG_SOFTMAX = 200;
+    static constexpr int REG_LOAD = 128;
+    static constexpr int S_COL(int i) { return 256 + i * 64; }
+    static constexpr int O_COL(int) { return 0; }
+};
+
+template <class G>
+struct Smem {
+    static constexpr int Q = 0;                                  // [NT][QPANELS][128 rows][128 B]
+    static constexpr int RING = G::NT * G::QPANELS * 128 * 128;  // K and V
+    static constexpr int BAR = RING + G::RING;                   // barriers
+    // q, out; then per tile or buffer: S ready, P ready; O steps; then the ring's
+    static constexpr int NBARS = 8 + G::BARS;
+    static constexpr int BYTES = BAR + NBARS * 8 + 1024;         // + alignment of the base
+};
+
+enum { kBarQ = 0, kBarDone = 1, kBarS = 2, kBarP = 4, kBarO = 6, kBarRing = 8 };
+
+// What a block works on, the same for every thread.
+struct Work {
+    int seq, head;       // sequence, key head (MLA: half of the value columns)
+    int n, len;          // new tokens, cached tokens
+    int64_t q0;          // first query token of the sequence
+    int row0;            // first row of the block within (sequence, key head)
+    int beg, end;        // virtual key tiles of this block
+    int sink_tiles;      // virtual tile v < sink_tiles is tile v, else first + v - sink_tiles
+    int first;
+    int lo, hi, sk;      // keys that some row sees: [lo, hi) and [0, sk)
+    int split, splits;
+};
+
+// Mask of the rows of one 128-row tile.
+struct TileMask {
+    int pos0, pos1;      // positions of the first and last token
+    int hi0, hi1;        // first key not seen by the first / last token
+    int lo0, lo1;        // first key in the window of the first / last token
+    int sk;              // sinks outside the last token's window
+    int rows;            // rows that exist
+};
+
+__device__ __forceinline__ TileMask tile_mask(const AttnParams &p, int n, int len, int row0)
+{
+    TileMask m;
+    const int total = n * p.group;
+    m.rows = max(0, min(kRows, total - row0));
+    const int i0 = row0 / p.group, i1 = (row0 + max(m.rows, 1) - 1) / p.group;
+    m.pos0 = len - n + i0;
+    m.pos1 = len - n + i1;
+    m.hi0 = p.causal ? max(0, min(len, m.pos0 + 1)) : len;
+    m.hi1 = p.causal ? max(0, min(len, m.pos1 + 1)) : len;
+    m.lo0 = p.window ? max(0, m.pos0 - p.window + 1) : 0;
+    m.lo1 = p.window ? max(0, m.pos1 - p.window + 1) : 0;
+    m.sk = p.window ? min(p.sinks, m.lo1) : 0;
+    return m;
+}
+
+// Key tile kt has a key that some row of the tile sees.
+template <int KT>
+__device__ __forceinline__ bool tile_active(const TileMask &m, int kt)
+{
+    const int k0 = kt * KT;
+    return m.rows > 0 && k0 < m.hi1 && (k0 + KT > m.lo0 || k0 < m.sk);
+}
+
+// Every row of the tile sees every key of tile kt.
+template <int KT>
+__device__ __forceinline__ bool tile_full(const AttnParams &p, const TileMask &m, int kt)
+{
+    const int k0 = kt * KT;
+    return k0 + KT <= m.hi0 && (k0 >= m.lo1 || k0 + KT <= p.sinks);
+}
+
+// The key range of the rows of a block and its virtual tiles: returns their
+// number.
+template <int KT, int NT>
+__device__ __forceinline__ int key_tiles(const AttnParams &p, Work &w)
+{
+    const TileMask a = tile_mask(p, w.n, w.len, w.row0);
+    TileMask b = a;
+    if (NT == 2) {
+        const TileMask c = tile_mask(p, w.n, w.len, w.row0 + kRows);
+        if (c.rows > 0)
+            b = c;
+    }
+    w.lo = a.lo0;
+    w.hi = b.hi1;
+    w.sk = p.window ? min(p.sinks, w.lo) : 0;
+    w.first = w.lo / KT;
+    w.sink_tiles = min((w.sk + KT - 1) / KT, w.first);
+    return w.hi <= 0 ? 0 : w.sink_tiles + max(0, (w.hi + KT - 1) / KT - w.first);
+}
+
+__device__ __forceinline__ int real_tile(const Work &w, int v)
+{
+    return v < w.sink_tiles ? v : w.first + v - w.sink_tiles;
+}
+
+// Lengths of sequence s; false when they do not fit what the call stated.
+__device__ __forceinline__ bool seq_queries(const AttnParams &p, int s, int64_t &q0, int &n)
+{
+    const int a = p.q_off[s], b = p.q_off[s + 1];
+    q0 = a;
+    n = b - a;
+    if (a < 0 || b < a || b > p.total_q || n > p.max_q_len) {
+        n = 0;
+        return false;
+    }
+    return true;
+}
+
+__device__ __forceinline__ bool seq_keys(const AttnParams &p, int s, int &len)
+{
+    len = p.kv_len[s];
+    return len >= 0 && len <= p.max_kv_len && (int64_t)len <= (int64_t)p.max_blocks * p.block;
+}
+
+// Row tile `tile` of the call -> sequence and row tile within it: one warp
+// counts the sequences' tiles 32 at a time.  Returns false past the last tile;
+// `bad`: some sequence's offsets do not fit.
+template <int ROWS>
+__device__ __forceinline__ bool find_tile(const AttnParams &p, int tile, int lane, int &seq, int &at,
+                                          bool &bad)
+{
+    int before = 0;
+    bad = false;
+    bool found = false;
+    for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+        int n = 0, tiles = 0;
+        int64_t q0;
+        if (s0 + lane < p.num_seqs) {
+            if (!seq_queries(p, s0 + lane, q0, n))
+                bad = true;
+            tiles = (n * p.group + ROWS - 1) / ROWS;
+        }
+        int sum = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+            if (lane >= d)
+                sum += o;
+        }
+        const bool mine = !found && tile >= before + sum - tiles && tile < before + sum;
+        const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine);
+        if (who) {
+            const int l = __ffs((int)who) - 1;
+            seq = s0 + l;
+            // the last tiles of a causal chunk see the most keys: first
+            const int t = __shfl_sync(0xFFFFFFFFu, tiles, l), e = __shfl_sync(0xFFFFFFFFu, sum, l);
+            at = t - 1 - (tile - (before + e - t));
+            found = true;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    bad = __any_sync(0xFFFFFFFFu, bad);
+    return found;
+}
+
+// Slot of key k of the block's sequence, or -1: not seen by any row, or (bad)
+// its block lies outside the pool.
+__device__ __forceinline__ int64_t key_slot(const AttnParams &p, const Work &w, int k, bool &bad)
+{
+    if (k >= w.hi || (k < w.lo && k >= w.sk))
+        return -1;
+    const int b = (int)((uint32_t)k / (uint32_t)p.block);
+    const int32_t blk = __ldg(p.block_tables + (int64_t)w.seq * p.max_blocks + b);
+    if (blk < 0 || blk >= p.num_blocks) {
+        bad = true;
+        return -1;
+    }
+    return (int64_t)blk * p.block + (k - b * p.block);
+}
+
+// ---------------------------------------------------------------------------
+// Load roles
+// ---------------------------------------------------------------------------
+
+// Query rows of one tile into their panels; rows past the end are zeros.
+template <class G>
+__device__ __forceinline__ void load_queries(const AttnParams &p, const Work &w, uint32_t q_smem,
+                                             int tid, int threads)
+{
+    constexpr int PIECES = G::QPANELS * 8;
+    for (int i = tid; i < G::NT * kRows * PIECES; i += threads) {
+        const int r = i / PIECES, c = i - r * PIECES;
+        const int row = w.row0 + r, tok = row / p.group, g = row - tok * p.group;
+        const bool ok = tok < w.n;
+        const int h = G::MLA ? g : w.head * p.group + g;
+        const char *src = p.q + (ok ? (w.q0 + tok) * p.q_ts + h * p.q_hs : 0) + c * 16;
+        const int t = r >> 7, rr = r & 127;
+        copy16(q_smem + ((t * G::QPANELS + (c >> 3)) << 14) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
+               src, ok ? 16u : 0u);
+    }
+}
+
+// Head rows in bf16: copied straight into the ring.  A lane owns one key row of
+// its warp; 16 lanes copy the 256 bytes of a row.
+template <class G>
+__device__ __forceinline__ bool load_heads_bf16(const AttnParams &p, const Work &w, uint32_t ring,
+                                                uint32_t bars, int warp, int lane,
+                                                volatile int *abort, bool &bad)
+{
+    constexpr int WARPS = G::LOAD_WG * 4, ROWS = G::KT / WARPS; // rows of a warp: 32 or 16
+    const int base = warp * ROWS;
+    const int c = lane & 15, half = lane >> 4;
+    auto slot_at = [&](int v) {
+        return v < w.end ? key_slot(p, w, real_tile(w, v) * G::KT + base + (lane & (ROWS - 1)), bad)
+                         : (int64_t)-1;
+    };
+    int64_t next = slot_at(w.beg);
+    int stage = 0, phase = 1;
+    for (int v = w.beg; v < w.end; ++v) {
+        const int64_t slot = next;
+        next = slot_at(v + 1); // the next tile's block ids, in flight with this tile
+#pragma unroll
+        for (int part = 0; part < 2; ++part) { // K, then V
+            const char *src = part == 0 ? p.rot : p.copy;
+            const int64_t ss = part == 0 ? p.rot_ss : p.copy_ss;
+            if (!bar_wait(bars + (G::STAGES + stage) * 8, phase, abort, p.wait_limit_ns))
+                return false;
+            const uint32_t dst = ring + stage * G::STAGE + ((c >> 3) << 14);
+            const char *col = src + w.head * 256 + c * 16;
+#pragma unroll
+            for (int i = 0; i < ROWS / 2; ++i) {
+                const int r = i * 2 + half;
+                const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, r);
+                const int row = base + r;
+                copy16(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4), col + (s < 0 ? 0 : s * ss),
+                       s < 0 ? 0u : 16u);
+            }
+            bar_signal_copies(bars + stage * 8);
+            if (++stage == G::STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+    }
+    return true;
+}
+
+// Head rows in e4m3: the next K and V tile wait in registers while the one
+// before is converted into the ring.  8 lanes hold the 128 bytes of a row.
+template <class G>
+__device__ __forceinline__ bool load_heads_e4m3(const AttnParams &p, const Work &w, uint32_t ring,
+                                                uint32_t bars, int warp, int lane,
+                                                volatile int *abort, bool &bad)
+{
+    constexpr int WARPS = G::LOAD_WG * 4, ROWS = G::KT / WARPS, IT = ROWS / 4;
+    const int base = warp * ROWS;
+    const int c = lane & 7, sub = lane >> 3;
+    uint4 raw[2][IT];
+    float scale[2];
+    auto slot_at = [&](int v) {
+        return v < w.end ? key_slot(p, w, real_tile(w, v) * G::KT + base + (lane & (ROWS - 1)), bad)
+                         : (int64_t)-1;
+    };
+    auto fetch = [&](int part, int64_t slot) {
+        const char *src = (part == 0 ? p.rot : p.copy) + w.head * 128 + c * 16;
+        const int64_t ss = part == 0 ? p.rot_ss : p.copy_ss;
+        const float *sc = part == 0 ? p.rs + slot * p.rs_ss : p.cs + slot * p.cs_ss;
+        scale[part] = slot < 0 ? 1.0f : __ldg(sc + w.head);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, i * 4 + sub);
+            raw[part][i] = s < 0 ? make_uint4(0, 0, 0, 0)
+                                 : __ldg(reinterpret_cast<const uint4 *>(src + s * ss));
+        }
+    };
+    int64_t next = slot_at(w.beg);
+    fetch(0, next);
+    fetch(1, next);
+    next = slot_at(w.beg + 1);
+    int stage = 0, phase = 1;
+    for (int v = w.beg; v < w.end; ++v) {
+        const int64_t slot = next;
+        next = slot_at(v + 2);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            if (!bar_wait(bars + (G::STAGES + stage) * 8, phase, abort, p.wait_limit_ns))
+                return false;
+            const uint32_t dst = ring + stage * G::STAGE + ((c >> 2) << 14);
+            const int first = c >> 2; // odd pieces first in the upper panel: no bank conflict
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int r = i * 4 + sub, row = base + r;
+                const float s = __shfl_sync(0xFFFFFFFFu, scale[part], r);
+                uint4 a, b;
+                convert16(raw[part][i], s, a, b);
+                const int c0 = (2 * c + first) & 7, c1 = (2 * c + 1 - first) & 7;
+                sts16(dst + row * 128 + ((c0 ^ (row & 7)) << 4), first ? b : a);
+                sts16(dst + row * 128 + ((c1 ^ (row & 7)) << 4), first ? a : b);
+            }
+            async_fence();
+            bar_signal(bars + stage * 8);
+            if (v + 1 < w.end)
+                fetch(part, slot);
+            if (++stage == G::STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+    }
+    return true;
+}
+
+// MLA rows.  Part 0: the other half's value panels and k_pe, part 1: this half's
+// value panels.  A warp owns 8 rows; 8 lanes hold a 128-byte piece of a row.
+template <class G>
+__device__ __forceinline__ bool load_mla(const AttnParams &p, const Work &w, uint32_t ring,
+                                         uint32_t bars, int warp, int lane, volatile int *abort,
+                                         bool &bad)
+{
+    constexpr int PG = G::QUANT ? 4 : 8;         // 128-byte pieces of the latent row
+    constexpr int HALF = PG / 2;                 // of one half
+    const int base = warp * 8, c = lane & 7, sub = lane >> 3;
+    uint4 lat[2][HALF][2], pe[2];
+    float scale[2][2];
+    auto slot_at = [&](int v) {
+        return v < w.end ? key_slot(p, w, real_tile(w, v) * G::KT + base + c, bad) : (int64_t)-1;
+    };
+    auto fetch = [&](int part, int64_t slot) {
+        const int half = part == 0 ? 1 - w.head : w.head;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, i * 4 + sub);
+            const char *src = p.copy + (s < 0 ? 0 : s * p.copy_ss) + half * HALF * 128 + c * 16;
+#pragma unroll
+            for (int g = 0; g < HALF; ++g)
+                lat[part][g][i] = s < 0 ? make_uint4(0, 0, 0, 0)
+                                        : __ldg(reinterpret_cast<const uint4 *>(src + g * 128));
+            if (part == 0)
+                pe[i] = s < 0 ? make_uint4(0, 0, 0, 0)
+                              : __ldg(reinterpret_cast<const uint4 *>(p.rot + s * p.rot_ss + c * 16));
+        }
+        if (G::QUANT) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) // lane c of each eight: the row's scale
+                scale[part][g] = slot < 0 ? 1.0f : __ldg(p.cs + slot * p.cs_ss + half * 2 + g);
+        }
+    };
+    auto store = [&](int part) {
+        const int half = part == 0 ? 1 - w.head : w.head;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = i * 4 + sub, row = base + r;
+            const uint32_t at = ring + row * 128;
+            if (G::QUANT) {
+                const int first = c >> 2;
+                const int c0 = (2 * c + first) & 7, c1 = (2 * c + 1 - first) & 7;
+#pragma unroll
+                for (int g = 0; g < HALF; ++g) {
+                    const float s = __shfl_sync(0xFFFFFFFFu, scale[part][g & 1], r);
+                    uint4 a, b;
+                    convert16(lat[part][g][i], s, a, b);
+                    const uint32_t dst = at + (half * 4 + g * 2 + (c >> 2)) * G::PANEL;
+                    sts16(dst + ((c0 ^ (row & 7)) << 4), first ? b : a);
+                    sts16(dst + ((c1 ^ (row & 7)) << 4), first ? a : b);
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < HALF; ++g)
+                    sts16(at + (half * 4 + g) * G::PANEL + ((c ^ (row & 7)) << 4), lat[part][g][i]);
+            }
+            if (part == 0)
+                sts16(at + 8 * G::PANEL + ((c ^ (row & 7)) << 4), pe[i]);
+        }
+    };
+    int64_t next = slot_at(w.beg);
+    fetch(0, next);
+    fetch(1, next);
+    next = slot_at(w.beg + 1);
+    int phase = 1;
+    for (int v = w.beg; v < w.end; ++v) {
+        const int64_t slot = next;
+        next = slot_at(v + 2);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            if (!bar_wait(bars + (2 + part) * 8, phase, abort, p.wait_limit_ns))
+                return false;
+            store(part);
+            async_fence();
+            bar_signal(bars + part * 8);
+            if (v + 1 < w.end)
+                fetch(part, slot);
+        }
+        phase ^= 1;
+    }
+    return true;
+}
+
+// ---------------------------------------------------------------------------
+// MMA role (one thread)
+// ---------------------------------------------------------------------------
+
+// S = Q Kᵀ of one row tile over panels [p0, p1) of K.
+template <int N, int PANEL>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q, uint32_t k, int p0, int p1,
+                                             bool first)
+{
+    for (int pn = p0; pn < p1; ++pn) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+            mma_smem<N>(d, operand(q + (pn << 14) + kk * 32, 16),
+                        operand(k + pn * PANEL + kk * 32, 16), !(first && pn == p0 && kk == 0));
+    }
+}
+
+// O += P V: P in tensor memory (two keys to a column), V in panels.
+template <int N, int KT>
+__device__ __forceinline__ void issue_values(uint32_t d, uint32_t pt, uint32_t v, bool first)
+{
+#pragma unroll
+    for (int kk = 0; kk < KT / 16; ++kk)
+        mma_tmem<N>(d, pt + kk * 8, operand(v + kk * 2048, KT * 128), !(first && kk == 0));
+}
+
+template <class G>
+__device__ __forceinline__ bool run_mma_heads2(const AttnParams &p, const Work &w,
+                                               const TileMask (&mask)[2], uint32_t tmem,
+                                               uint32_t q_smem, uint32_t ring, uint32_t bars,
+                                               volatile int *abort)
+{
+    const uint32_t full = bars + kBarRing * 8, empty = full + G::STAGES * 8;
+    bool pend[2] = {false, false}, begun[2] = {false, false};
+    uint32_t pphase[2] = {0, 0};
+    int stage = 0, phase = 0;         // of K of tile v
+    int vstage = 0;                   // of V of the tile before
+    bool v_open = false;              // V of the tile before is still held
+    auto values = [&](int t) {
+        if (!bar_wait(bars + (kBarP + t) * 8, pphase[t], abort, p.wait_limit_ns))
+            return false;
+        pphase[t] ^= 1;
+        mma_fence_after();
+        issue_values<128, 128>(tmem + G::O_COL(t), tmem + G::S_COL(t), ring + vstage * G::STAGE,
+                               !begun[t]);
+        begun[t] = true;
+        pend[t] = false;
+        return true;
+    };
+    for (int v = w.beg; v < w.end; ++v) {
+        const int kt = real_tile(w, v);
+        if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
+            return false;
+        async_fence();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (pend[t] && !values(t))
+                return false;
+            if (t == 1 && v_open)
+                bar_signal_mma(empty + vstage * 8);
+            if (tile_active<G::KT>(mask[t], kt)) {
+                issue_scores<128, 16384>(tmem + G::S_COL(t), q_smem + (t << 15),
+                                         ring + stage * G::STAGE, 0, 2, true);
+                bar_signal_mma(bars + (kBarS + t) * 8);
+                pend[t] = true;
+            }
+        }
+        bar_signal_mma(empty + stage * 8);
+        if (++stage == G::STAGES) {
+            stage = 0;
+            phase ^= 1;
+        }
+        // V of this tile is the next stage; the weights come later
+        vstage = stage;
+        if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
+            return false;
+        async_fence();
+        v_open = true;
+        if (++stage == G::STAGES) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+        if (pend[t] && !values(t))
+            return false;
+    bar_signal_mma(bars + kBarDone * 8);
+    return true;
+}
+
+// One row tile, two buffers of S: the scores of a tile are formed while the
+// softmax of the one before runs.
+template <class G>
+__device__ __forceinline__ bool run_mma_one(const AttnParams &p, const Work &w, uint32_t tmem,
+                                            uint32_t q_smem, uint32_t ring, uint32_t bars,
+                                            volatile int *abort)
+{
+    const uint32_t full = bars + kBarRing * 8;
+    uint32_t pphase[2] = {0, 0};
+    int stage = 0, phase = 0, vstage = 0;
+    const int own = w.head * 4, other = 4 - own; // MLA: value panels of this half, of the other
+    for (int v = w.beg; v <= w.end; ++v) {
+        const int i = (v - w.beg) & 1;
+        const uint32_t s_col = tmem + G::S_COL(i);
+        const bool more = v < w.end;
+        if (more) {
+            if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
+                return false;
+            async_fence();
+            if constexpr (G::MLA) {
+                issue_scores<64, G::PANEL>(s_col, q_smem, ring, other, other + 4, true);
+                issue_scores<64, G::PANEL>(s_col, q_smem, ring, 8, 9, false);
+                bar_signal_mma(full + 2 * 8);
+            } else {
+                issue_scores<128, 16384>(s_col, q_smem, ring + stage * G::STAGE, 0, 2, true);
+                bar_signal_mma(bars + (kBarS + i) * 8);
+                bar_signal_mma(full + (G::STAGES + stage) * 8);
+                if (++stage == G::STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (v > w.beg) { // weights of the tile before
+            if (!bar_wait(bars + (kBarP + (1 - i)) * 8, pphase[1 - i], abort, p.wait_limit_ns))
+                return false;
+            pphase[1 - i] ^= 1;
+            mma_fence_after();
+            if constexpr (G::MLA) {
+                issue_values<256, 64>(tmem + G::O_COL(0), tmem + G::S_COL(1 - i),
+                                      ring + own * G::PANEL, v == w.beg + 1);
+                bar_signal_mma(full + 3 * 8);
+            } else {
+                issue_values<128, 128>(tmem + G::O_COL(0), tmem + G::S_COL(1 - i),
+                                       ring + vstage * G::STAGE, v == w.beg + 1);
+                bar_signal_mma(full + (G::STAGES + vstage) * 8);
+            }
+            bar_signal_mma(bars + kBarO * 8);
+        }
+        if (more) {
+            if constexpr (G::MLA) {
+                if (!bar_wait(full + 8, phase, abort, p.wait_limit_ns))
+                    return false;
+                async_fence();
+                issue_scores<64, G::PANEL>(s_col, q_smem, ring, own, own + 4, false);
+                bar_signal_mma(bars + (kBarS + i) * 8);
+                phase ^= 1;
+            } else {
+                vstage = stage;
+                if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
+                    return false;
+                async_fence();
+                if (++stage == G::STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    }
+    bar_signal_mma(bars + kBarDone * 8);
+    return true;
+}
+
+// ---------------------------------------------------------------------------
+// Softmax role (a thread per row)
+// ---------------------------------------------------------------------------
+
+struct RowState {
+    float top = -INFINITY; // maximum that the weights and O are taken against
+    float sum = 0.0f;
+};
+
+// Value `col` of key slot `s` as an fp32 if it is not finite, else 0.
+template <class G>
+__device__ __forceinline__ float nonfinite_value(const AttnParams &p, int64_t s, int col)
+{
+    const char *row = p.copy + s * p.copy_ss;
+    if (G::QUANT)
+        return (*reinterpret_cast<const uint8_t *>(row + col) & 0x7Fu) == 0x7Fu
+                   ? __uint_as_float(0x7FC00000u)
+                   : 0.0f;
+    const uint32_t b = *reinterpret_cast<const uint16_t *>(row + col * 2);
+    return (b & 0x7F80u) == 0x7F80u ? __uint_as_float(b << 16) : 0.0f;
+}
+
+template <class G>
+__device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, const TileMask &m,
+                                            int t, uint32_t tmem, uint32_t ring, uint32_t bars,
+                                            int warp, int lane, int warps, volatile int *abort,
+                                            volatile int *dirty)
+{
+    constexpr int KT = G::KT;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const int r = warp * 32 + lane;
+    const int row = w.row0 + t * kRows + r;
+    const int tok = row / p.group, g = row - tok * p.group;
+    const bool valid = r < m.rows;
+    const int pos = w.len - w.n + tok;
+    // keys this row sees: [lo, hi) and [0, sk)
+    const int hi = !valid ? 0 : p.causal ? min(w.len, pos + 1) : w.len;
+    const int lo = p.window ? max(0, pos - p.window + 1) : 0;
+    const int sk = p.window ? min(p.sinks, hi) : 0;
+    const bool one_token = G::NT == 1 && m.pos0 == m.pos1;
+    const float c = p.scale * 1.4426950408889634f;
+    RowState st;
+    int done = 0; // tiles of this row tile so far
+    for (int v = w.beg; v < w.end; ++v) {
+        const int kt = real_tile(w, v);
+        if (G::NT == 2 && !tile_active<KT>(m, kt))
+            continue;
+        const int buf = G::NT == 2 ? t : (done & 1);
+        const uint32_t s_col = tmem + G::S_COL(buf) + lanes;
+        const uint32_t parity = G::NT == 2 ? (done & 1) : ((done >> 1) & 1);
+        if (!bar_wait(bars + (kBarS + buf) * 8, parity, abort, p.wait_limit_ns))
+            return false;
+        mma_fence_after();
+        uint32_t s[KT];
+#pragma unroll
+        for (int i = 0; i < KT; i += 32)
+            tmem_ld32(s_col + i, s + i);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < KT; i += 32)
+            tmem_pin32(s + i);
+        const bool full = tile_full<KT>(p, m, kt);
+        if (!full) {
+            const int k0 = kt * KT;
+#pragma unroll
+            for (int i = 0; i < KT; ++i) {
+                const int k = k0 + i;
+                const bool see = k < hi && (k >= lo || k < sk);
+                s[i] = see ? s[i] : 0xFF800000u;
+            }
+        }
+        float top = __uint_as_float(s[0]);
+#pragma unroll
+        for (int i = 1; i < KT; ++i)
+            top = fmaxf(top, __uint_as_float(s[i]));
+        top = fmaxf(top, st.top);
+        const bool grew = (top - st.top) * c > kLazy; // also from -inf
+        if (done == 0) {
+            st.top = top;
+        } else if (__any_sync(0xFFFFFFFFu, grew)) {
+            // O of the tiles before is complete: NT = 2 issues it before these scores
+            if (G::NT == 1 &&
+                !bar_wait(bars + kBarO * 8, (done - 1) & 1, abort, p.wait_limit_ns))
+                return false;
+            if (G::NT == 1)
+                mma_fence_after();
+            const float f = grew ? exp2_fast((st.top - top) * c) : 1.0f;
+            if (grew) {
+                st.top = top;
+                st.sum *= f;
+            }
+#pragma unroll 1
+            for (int i = 0; i < G::OC; i += 32) {
+                uint32_t o[32];
+                tmem_ld32(tmem + G::O_COL(t) + lanes + i, o);
+                tmem_ld_wait();
+                tmem_pin32(o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st32(tmem + G::O_COL(t) + lanes + i, o);
+            }
+        }
+        const float off = st.top == -INFINITY ? 0.0f : -st.top * c;
+        const f2 c2 = f2_of_bits(__float_as_uint(c), __float_as_uint(c));
+        const f2 off2 = f2_of_bits(__float_as_uint(off), __float_as_uint(off));
+        f2 sum2 = f2_of_bits(0u, 0u);
+#pragma unroll
+        for (int i = 0; i < KT; i += 32) {
+            uint32_t w16[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const f2 x = f2_fma(f2_of_bits(s[i + 2 * j], s[i + 2 * j + 1]), c2, off2);
+                float a, b;
+                asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+                a = exp2_fast(a);
+                b = exp2_fast(b);
+                sum2 = f2_add(sum2, f2_of_bits(__float_as_uint(a), __float_as_uint(b)));
+                w16[j] = pack_bf16(a, b);
+            }
+            tmem_st16(s_col + i / 2, w16);
+        }
+        float sa, sb;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(sa), "=f"(sb) : "l"(sum2));
+        st.sum += sa + sb;
+        tmem_st_wait();
+        if (!full && !one_token) {
+            // A weight of 0 does not keep an infinite or NaN value out of the
+            // product: take such values out of V here; rows that do see them get
+            // them back at the end.
+            const int ord = v - w.beg;
+            uint32_t vbase;
+            int pieces;
+            if (G::MLA) {
+                if (!bar_wait(bars + (kBarRing + 1) * 8, ord & 1, abort, p.wait_limit_ns))
+                    return false;
+                vbase = ring + w.head * 4 * 8192;
+                pieces = 4 * 8192 / 16;
+            } else {
+                constexpr int ST = G::BARS / 2;
+                const int item = 2 * ord + 1;
+                if (!bar_wait(bars + (kBarRing + item % ST) * 8, (item / ST) & 1, abort,
+                              p.wait_limit_ns))
+                    return false;
+                vbase = ring + (item % ST) * (G::RING / ST);
+                pieces = G::RING / ST / 16;
+            }
+            bool any = false;
+            for (int i = warp * 32 + lane; i < pieces; i += warps * 32) {
+                uint4 x = lds16(vbase + i * 16);
+                const bool a = drop_nonfinite(x.x), b = drop_nonfinite(x.y);
+                const bool d = drop_nonfinite(x.z), e = drop_nonfinite(x.w);
+                if (a || b || d || e) {
+                    *dirty = 1;
+                    __threadfence_block();
+                    sts16(vbase + i * 16, x);
+                    any = true;
+                }
+            }
+            if (any)
+                async_fence();
+        }
+        mma_fence_before();
+        bar_signal(bars + (kBarP + buf) * 8);
+        ++done;
+    }
+    // O is complete
+    if (!bar_wait(bars + kBarDone * 8, 0, abort, p.wait_limit_ns))
+        return false;
+    mma_fence_after();
+    const float inv = st.sum == 0.0f || done == 0 ? 0.0f : 1.0f / st.sum;
+    const int h = G::MLA ? g : w.head * p.group + g;
+    const int64_t at = (w.q0 + tok) * p.heads + h;
+    const float lse = st.sum == 0.0f ? -INFINITY : st.top * p.scale + logf(st.sum);
+    const int col0 = G::MLA ? w.head * 256 : 0;
+    const bool parts = w.splits > 1;
+    if (valid && (!G::MLA || w.head == 0)) {
+        if (parts)
+            p.part_lse[w.split * p.total_q * p.heads + at] = lse;
+        else if (p.lse)
+            p.lse[at] = lse;
+    }
+    char *out = p.out + (w.q0 + tok) * p.o_ts + h * p.o_hs + col0 * 2;
+    float *part = p.part + (w.split * p.total_q * p.heads + at) * G::DV + col0;
+#pragma unroll 1
+    for (int i = 0; i < G::OC; i += 32) {
+        uint32_t o[32];
+        tmem_ld32(tmem + G::O_COL(t) + lanes + i, o);
+        tmem_ld_wait();
+        tmem_pin32(o);
+        float f[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            f[j] = st.sum == 0.0f ? 0.0f : __uint_as_float(o[j]) * inv;
+        if (*dirty) {
+            for (int v = w.beg; v < w.end; ++v) {
+                const int k0 = real_tile(w, v) * KT;
+                for (int k = k0; k < k0 + KT; ++k) {
+                    if (!valid || !(k < hi && (k >= lo || k < sk)))
+                        continue;
+                    bool bad = false;
+                    const int64_t s = key_slot(p, w, k, bad);
+                    if (s < 0)
+                        continue;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        f[j] += nonfinite_value<G>(p, s, (G::MLA ? col0 : w.head * 128) + i + j);
+                }
+            }
+        }
+        if (!valid)
+            continue;
+        if (parts) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<float4 *>(part + i + j) =
+                    make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+                *reinterpret_cast<uint4 *>(out + (i + j) * 2) =
+                    make_uint4(pack_bf16(f[j], f[j + 1]), pack_bf16(f[j + 2], f[j + 3]),
+                               pack_bf16(f[j + 4], f[j + 5]), pack_bf16(f[j + 6], f[j + 7]));
+        }
+    }
+    return true;
+}
+
+// ---------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------
+
+template <class G>
+__global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
     const __grid_constant__ AttnParams p)
 {
-    constexpr int DK = MLA ? 576 : 128, DV = MLA ? 512 : 128;
-    constexpr int VL = DV / 32, KL = DK / 32; // values per lane
-    __shared__ float s_max[4], s_sum[4], s_acc[4][DV];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = blockIdx.x;
-    const int h = blockIdx.y, hk = h / p.group;
-    int lo = 0, hi = p.num_seqs; // the last sequence that starts at or before t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        (p.q_off[mid] <= t ? lo : hi) = mid;
+    using S = Smem<G>;
+    extern __shared__ unsigned char raw_smem[];
+    __shared__ Work s_work;
+    __shared__ uint32_t s_tmem, s_status;
+    __shared__ int s_go;
+    __shared__ volatile int s_abort, s_dirty;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+    const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const uint32_t q_smem = smem + S::Q, ring = smem + S::RING, bars = smem + S::BAR;
+
+    if (warp == 0) {
+        // block -> (row tile, key head or half, split); heads of one row tile and
+        // its halves are neighbours, so their rows meet in L2
+        const int heads = G::MLA ? 2 : p.heads / p.group;
+        uint32_t x = blockIdx.x;
+        Work w;
+        w.head = (int)(x % heads);
+        x /= heads;
+        w.split = (int)(x % p.max_splits);
+        int seq = 0, at = 0;
+        bool bad = false;
+        bool go = find_tile<kRows * G::NT>(p, (int)(x / p.max_splits), lane, seq, at, bad);
+        w.seq = seq;
+        if (go) {
+            seq_queries(p, seq, w.q0, w.n);
+            if (!seq_keys(p, seq, w.len)) {
+                bad = true;
+                go = false;
+            }
+        }
+        if (go) {
+            w.row0 = at * kRows * G::NT;
+            const int nv = key_tiles<G::KT, G::NT>(p, w);
+            w.splits = max(1, (nv + p.split_tiles - 1) / p.split_tiles);
+            w.beg = w.split * p.split_tiles;
+            w.end = min(nv, w.beg + p.split_tiles);
+            go = w.split < w.splits;
+        }
+        if (lane == 0) {
+            s_work = w;
+            s_go = go;
+            s_status = bad ? kStatusOutOfRange : kStatusOk;
+            s_abort = 0;
+            s_dirty = 0;
+        }
     }
-    const int n = p.q_off[lo + 1] - p.q_off[lo], len = p.kv_len[lo];
-    if (n < 0 || n > p.max_q_len || len < 0 || len > p.max_kv_len ||
-        (int64_t)len > (int64_t)p.max_blocks * p.block || t >= p.q_off[lo + 1]) {
-        if (threadIdx.x == 0)
-            set_status(p.header, kStatusOutOfRange);
+    __syncthreads();
+    if (!s_go) {
+        if (tid == 0)
+            write_block_status(p.header, s_status, blockIdx.x, gridDim.x);
         return;
     }
-    const int pos = len - n + (int)(t - p.q_off[lo]);
-    float q[KL], acc[VL], top = -INFINITY, sum = 0.0f;
-    const char *qr = p.q + t * p.q_ts + h * p.q_hs;
-    load_row<VL>(qr, nullptr, lane * VL, q);
-    if (MLA)
-        load_row<2>(qr, nullptr, 512 + lane * 2, q + VL);
-    for (int i = 0; i < VL; ++i)
-        acc[i] = 0.0f;
-    const int end = p.causal ? min(len, pos + 1) : len;
-    const int first = p.window ? max(0, pos - p.window + 1) : 0;
-    const int nsink = p.window ? max(0, min(min(p.sinks, first), end)) : 0;
-    for (int j = warp; j < nsink + max(0, end - first); j += 4) {
-        const int k = j < nsink ? j : first + (j - nsink);
-        const int32_t blk = p.block_tables[(int64_t)lo * p.max_blocks + k / p.block];
-        if (blk < 0 || blk >= p.num_blocks) {
-            if (lane == 0)
-                set_status(p.header, kStatusOutOfRange);
-            continue;
+    const Work w = s_work;
+    TileMask mask[2];
+    mask[0] = tile_mask(p, w.n, w.len, w.row0);
+    mask[1] = tile_mask(p, w.n, w.len, w.row0 + kRows);
+    if (tid == 0) {
+        bar_init(bars + kBarQ * 8, G::LOAD_WG * 128);
+        bar_init(bars + kBarDone * 8, 1);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(bars + (kBarS + i) * 8, 1);
+            const int rows = mask[G::NT == 2 ? i : 0].rows;
+            bar_init(bars + (kBarP + i) * 8, max(1, (rows + 31) / 32) * 32);
         }
-        const int64_t slot = (int64_t)blk * p.block + k % p.block;
-        const char *cr = p.copy + slot * p.copy_ss, *rr = p.rot + slot * p.rot_ss;
-        const float *cs = p.cs ? p.cs + slot * p.cs_ss : nullptr;
-        const float *rs = p.rs ? p.rs + slot * p.rs_ss : nullptr;
-        float key[KL], val[VL], dot = 0.0f;
-        if (MLA) {
-            load_row<VL>(cr, cs, lane * VL, val);
-            for (int i = 0; i < VL; ++i)
-                key[i] = val[i];
-            load_row<2>(rr, nullptr, lane * 2, key + VL);
-        } else {
-            load_row<VL>(cr, cs, hk * 128 + lane * VL, val);
-            load_row<KL>(rr, rs, hk * 128 + lane * KL, key);
+        bar_init(bars + kBarO * 8, 1);
+        bar_init(bars + (kBarO + 1) * 8, 1); // drain
+        for (int i = 0; i < G::BARS / 2; ++i) {
+            bar_init(bars + (kBarRing + i) * 8, G::LOAD_WG * 128);
+            bar_init(bars + (kBarRing + G::BARS / 2 + i) * 8, 1);
         }
-#pragma unroll
-        for (int i = 0; i < KL; ++i)
-            dot = fmaf(q[i], key[i], dot);
-        for (int x = 16; x > 0; x >>= 1)
-            dot += __shfl_xor_sync(0xFFFFFFFFu, dot, x);
-        dot *= p.scale;
-        const float m = fmaxf(top, dot);
-        const float f = m == -INFINITY ? 1.0f : __expf(top - m);
-        const float e = dot == -INFINITY ? 0.0f : __expf(dot - m);
-        sum = sum * f + e;
-        for (int i = 0; i < VL; ++i)
-            acc[i] = acc[i] * f + e * val[i];
-        top = m;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (lane == 0) {
-        s_max[warp] = top;
-        s_sum[warp] = sum;
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&s_tmem)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    for (int i = 0; i < VL; ++i)
-        s_acc[warp][lane * VL + i] = acc[i];
+    mma_fence_before();
     __syncthreads();
-    const float m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-    float f[4], total = 0.0f;
-    for (int w = 0; w < 4; ++w) {
-        f[w] = s_max[w] == -INFINITY ? 0.0f : __expf(s_max[w] - m);
-        total += f[w] * s_sum[w];
+    mma_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t tmem = s_tmem;
+
+    if (wg < G::NT) {
+        reg_inc<G::REG_SOFTMAX>();
+        const int t = wg, wl = warp & 3, warps = (mask[t].rows + 31) / 32;
+        if (wl < warps)
+            run_softmax<G>(p, w, mask[t], t, tmem, ring, bars, wl, lane, warps, &s_abort, &s_dirty);
+    } else if (wg < G::NT + G::LOAD_WG) {
+        reg_dec<G::REG_LOAD>();
+        const int lt = tid - G::NT * 128, lw = lt >> 5;
+        load_queries<G>(p, w, q_smem, lt, G::LOAD_WG * 128);
+        bar_signal_copies(bars + kBarQ * 8);
+        bool bad = false;
+        if constexpr (G::MLA)
+            load_mla<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
+        else if constexpr (G::QUANT)
+            load_heads_e4m3<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
+        else
+            load_heads_bf16<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
+        if (bad)
+            s_status = kStatusOutOfRange;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        reg_dec<kRegMma>();
+        if (warp == 12 && lane == 0) {
+            bool ok = bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
+            if (ok) {
+                async_fence();
+                if constexpr (G::NT == 2)
+                    ok = run_mma_heads2<G>(p, w, mask, tmem, q_smem, ring, bars, &s_abort);
+                else
+                    ok = run_mma_one<G>(p, w, tmem, q_smem, ring, bars, &s_abort);
+            }
+            if (!ok) { // let what was issued finish before tensor memory goes
+                int none = 0;
+                bar_signal_mma(bars + (kBarO + 1) * 8);
+                bar_wait(bars + (kBarO + 1) * 8, 0, &none, 1000000000ll);
+            }
+        }
     }
-    for (int d = threadIdx.x; d < DV; d += kSimpleThreads) {
-        float o = 0.0f;
-        for (int w = 0; w < 4; ++w)
-            o += f[w] * s_acc[w][d];
-        reinterpret_cast<__nv_bfloat16 *>(p.out + t * p.o_ts + h * p.o_hs)[d] =
-            __float2bfloat16_rn(total == 0.0f ? 0.0f : o / total);
+    mma_fence_before();
+    __syncthreads();
+    mma_fence_after();
+    if (warp == 12)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+    if (tid == 0)
+        write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, gridDim.x);
+}
+
+// Joins the parts of rows whose keys were split: a warp per (token, head).
+//   lse = log Σ exp(lse_s),  out = Σ exp(lse_s - lse) out_s
+template <class G>
+__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnParams p)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = p.total_q * p.heads;
+    const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t tok = at / p.heads;
+    const int h = (int)(at - tok * p.heads);
+    int splits = 0;
+    if (at < rows) {
+        int a = 0, b = p.num_seqs; // the last sequence that starts at or before the token
+        while (b - a > 1) {
+            const int mid = (a + b) / 2;
+            if (p.q_off[mid] <= tok)
+                a = mid;
+            else
+                b = mid;
+        }
+        Work w;
+        if (seq_queries(p, a, w.q0, w.n) && seq_keys(p, a, w.len) && tok >= w.q0 &&
+            tok < w.q0 + w.n) {
+            const int row = (int)(tok - w.q0) * p.group + h % p.group;
+            w.row0 = row / (kRows * G::NT) * (kRows * G::NT);
+            splits = (key_tiles<G::KT, G::NT>(p, w) + p.split_tiles - 1) / p.split_tiles;
+        }
     }
-    if (threadIdx.x == 0 && p.lse)
-        p.lse[t * p.heads + h] = total == 0.0f ? -INFINITY : m + logf(total);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (splits <= 1)
+        return; // the row's block wrote it
+    float top = -INFINITY;
+    for (int s = lane; s < splits; s += 32)
+        top = fmaxf(top, p.part_lse[s * rows + at]);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float acc[G::DV / 32] = {}, sum = 0.0f;
+    for (int s = 0; s < splits; ++s) {
+        const float wgt = expf(p.part_lse[s * rows + at] - ref);
+        sum += wgt;
+        const float4 *o = reinterpret_cast<const float4 *>(p.part + (s * rows + at) * G::DV);
+#pragma unroll
+        for (int i = 0; i < G::DV / 128; ++i) {
+            const float4 x = o[i * 32 + lane];
+            acc[i * 4] = fmaf(wgt, x.x, acc[i * 4]);
+            acc[i * 4 + 1] = fmaf(wgt, x.y, acc[i * 4 + 1]);
+            acc[i * 4 + 2] = fmaf(wgt, x.z, acc[i * 4 + 2]);
+            acc[i * 4 + 3] = fmaf(wgt, x.w, acc[i * 4 + 3]);
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    char *out = p.out + tok * p.o_ts + h * p.o_hs;
+#pragma unroll
+    for (int i = 0; i < G::DV / 128; ++i)
+        *reinterpret_cast<uint2 *>(out + (i * 128 + lane * 4) * 2) =
+            make_uint2(pack_bf16(acc[i * 4] * inv, acc[i * 4 + 1] * inv),
+                       pack_bf16(acc[i * 4 + 2] * inv, acc[i * 4 + 3] * inv));
+    if (lane == 0 && p.lse)
+        p.lse[at] = sum == 0.0f ? -INFINITY : ref + logf(sum);
+}
+
+template <class G>
+cudaError_t launch(const AttnParams &p, int64_t blocks, cudaStream_t stream)
+{
+    constexpr int bytes = Smem<G>::BYTES;
+    static_assert(bytes <= 227 * 1024, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(attention_kernel<G>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess)
+        return e;
+    // the register shares of the warpgroups come out of what a block starts with
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, attention_kernel<G>)) != cudaSuccess)
+        return e;
+    if (G::NT * G::REG_SOFTMAX + G::LOAD_WG * G::REG_LOAD + (4 - G::NT - G::LOAD_WG) * kRegMma >
+        4 * fa.numRegs)
+        return cudaErrorInvalidConfiguration;
+    attention_kernel<G><<<(unsigned)blocks, kAttnThreads, bytes, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess || p.max_splits == 1)
+        return e;
+    // the join starts while the last blocks run and waits for them on the device
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((p.total_q * p.heads + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<G>, p);
 }
 
 } // namespace
 
-cudaError_t launch_attention(const AttnParams &p, RowKind kind, cudaStream_t stream)
+AttnPlan plan_attention(RowKind kind, const AttnShape &a)
 {
-    const dim3 grid((unsigned)p.total_q, (unsigned)p.heads);
+    const bool mla = kind == RowKind::Mla;
+    const int64_t kt = mla ? 64 : 128;
+    AttnPlan pl{};
+    pl.row_tiles = !mla && (int64_t)a.max_q_len * a.group > kRows ? 2 : 1;
+    const int64_t rows = kRows * pl.row_tiles;
+    // row tiles over all sequences: at most one partly filled one each
+    const int64_t tiles = a.total_q * a.group / rows + a.num_seqs;
+    const int64_t units = tiles * (mla ? 2 : a.kv_heads);
+    // most key tiles of one row tile
+    int64_t nv = (a.max_kv_len + kt - 1) / kt;
+    if (a.window > 0) {
+        const int64_t toks = (rows + a.group - 1) / a.group + 1;
+        const int64_t w = (std::min<int64_t>(a.sinks, a.max_kv_len) + kt - 1) / kt +
+                          (a.window + toks + kt - 1) / kt + 1;
+        nv = std::min(nv, w);
+    }
+    nv = std::max<int64_t>(nv, 1);
+    // pieces of the key axis: enough blocks for a few on every SM, none shorter
+    // than four tiles (a block's start and end cost about as much as two)
+    const int64_t want = std::max<int64_t>(4, (units * nv + 4 * 152 - 1) / (4 * 152));
+    pl.split_tiles = (int32_t)std::min(nv, want);
+    pl.max_splits = (int32_t)((nv + pl.split_tiles - 1) / pl.split_tiles);
+    pl.blocks = units * pl.max_splits;
+    return pl;
+}
+
+cudaError_t launch_attention(const AttnParams &p, RowKind kind, const AttnPlan &pl,
+                             cudaStream_t stream)
+{
+    const bool quant = p.cs != nullptr;
     if (kind == RowKind::Mla)
-        attention_simple_kernel<true><<<grid, kSimpleThreads, 0, stream>>>(p);
-    else
-        attention_simple_kernel<false><<<grid, kSimpleThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+        return quant ? launch<MlaGeo<true>>(p, pl.blocks, stream)
+                     : launch<MlaGeo<false>>(p, pl.blocks, stream);
+    if (pl.row_tiles == 2)
+        return quant ? launch<HeadGeo<true, 2>>(p, pl.blocks, stream)
+                     : launch<HeadGeo<false, 2>>(p, pl.blocks, stream);
+    return quant ? launch<HeadGeo<true, 1>>(p, pl.blocks, stream)
+                 : launch<HeadGeo<false, 1>>(p, pl.blocks, stream);
 }
 
 } // namespace kvr

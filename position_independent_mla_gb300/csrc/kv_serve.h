@@ -72,9 +72,29 @@ struct AttnParams {
     const int32_t *q_off, *kv_len, *block_tables;
     int32_t causal, window, sinks;
     float scale;
+    // split of the key axis, and the parts that are joined afterwards
+    int32_t split_tiles, max_splits;
+    float *part, *part_lse; // [max_splits][total_q][heads][value width], [..][heads]
+    int64_t wait_limit_ns;
     uint32_t *header;
 };
 
-cudaError_t launch_attention(const AttnParams &p, RowKind kind, cudaStream_t stream);
+// Sizes of a call that the host knows, and the launch they lead to.
+struct AttnShape {
+    int64_t total_q;
+    int32_t num_seqs, max_q_len, max_kv_len, window, sinks;
+    int32_t group, kv_heads;
+};
+
+struct AttnPlan {
+    int32_t row_tiles;   // 128-row tiles of a block
+    int32_t split_tiles; // key tiles of a block
+    int32_t max_splits;
+    int64_t blocks;
+};
+
+AttnPlan plan_attention(RowKind kind, const AttnShape &a);
+cudaError_t launch_attention(const AttnParams &p, RowKind kind, const AttnPlan &pl,
+                             cudaStream_t stream);
 
 } // namespace kvr
