@@ -20,7 +20,7 @@
 //            (they are the A operand of the second MMA) and at the end O / l;
 //   load     bring rows of the pool through the block table into shared memory
 //            in the 128-byte swizzled layout that the MMAs read;
-//   mma      one thread issues every MMA.
+//   mma      one warp issues every MMA.
 // O stays in tensor memory.  It is rescaled only when some row's maximum grew by
 // more than 2^8 since it was last fixed: until then the weights stay below 2^8,
 // which fp32 sums and bf16 weights hold without loss.
@@ -31,6 +31,8 @@
 //
 // Every wait is bounded; a block whose wait runs out reports KV_ERR_TIMEOUT.
 #include <algorithm>
+
+#include <cudaTypedefs.h>
 
 #include "kv_device.cuh"
 #include "kv_serve.h"
@@ -63,17 +65,46 @@ __device__ __forceinline__ void bar_signal(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// `count` arrivals at once; the phase then also waits for `bytes` of bulk copies.
+__device__ __forceinline__ void bar_signal_bulk(uint32_t bar, uint32_t count, uint32_t bytes)
+{
+    if (bytes)
+        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar),
+                     "r"(bytes)
+                     : "memory");
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+// Box of a tensor map at column x, row y; what lies outside the tensor is zero.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                         uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+                 "l"(map), "r"(bar), "r"(x), "r"(y)
+                 : "memory");
+}
+
 // Signals `bar` when this thread's earlier cp.async copies have landed.
 __device__ __forceinline__ void bar_signal_copies(uint32_t bar)
 {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Signals `bar` when every MMA this thread issued before has finished.
-__device__ __forceinline__ void bar_signal_mma(uint32_t bar)
+// Signals `bar` when every MMA the lead lane issued before has finished.
+__device__ __forceinline__ void bar_signal_mma(uint32_t bar, uint32_t lead)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+    asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+                 "r"(lead)
                  : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect_lane()
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.b32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r;
 }
 
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
@@ -87,26 +118,23 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-// Bounded wait for a phase; false when it ran out here or elsewhere in the
-// block (*abort).
-__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity,
-                                                  volatile int *abort, int64_t limit_ns)
+// Bounded wait of a whole warp for a phase; false, for every lane, when it ran
+// out here or elsewhere in the block (*abort).
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *abort,
+                                         int64_t limit_ns)
 {
+    if (__all_sync(0xFFFFFFFFu, bar_try(bar, parity)))
+        return true;
     const uint64_t t0 = global_ns();
-    for (uint32_t it = 0; it < (1u << 26); ++it) {
-        if (bar_try(bar, parity))
+    for (uint32_t it = 1; it < (1u << 26); ++it) {
+        if (__all_sync(0xFFFFFFFFu, bar_try(bar, parity)))
             return true;
-        if ((it & 15u) == 15u && (*abort || (int64_t)(global_ns() - t0) > limit_ns))
+        if ((it & 15u) == 0u &&
+            __any_sync(0xFFFFFFFFu, *abort != 0 || (int64_t)(global_ns() - t0) > limit_ns))
             break;
     }
     *abort = 1;
     return false;
-}
-
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *abort,
-                                         int64_t limit_ns)
-{
-    return bar_try(bar, parity) || bar_wait_slow(bar, parity, abort, limit_ns);
 }
 
 __device__ __forceinline__ void mma_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -196,12 +224,14 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // 16-byte piece c of row r at c ^ (r & 7) (128-byte swizzle), 1024 bytes per
 // eight rows.  Along a K-major operand the next 16 columns are 32 bytes on;
 // of an MN-major one (V: the MMA's N runs along the row) the next 16 keys are
-// 2048 bytes on and the next 64 columns `lead` bytes.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead)
+// 2048 bytes on and the next 64 columns `lead` bytes.  The low word holds the
+// address, in units of 16 bytes, and the lead; the high word is the same for all.
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t lead)
 {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
-           ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+    return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
 }
+
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 // kind::f16: D fp32, A and B bf16; B along K (0) or along N (1).
 template <int N, int BMAJOR>
@@ -211,21 +241,27 @@ __device__ __forceinline__ constexpr uint32_t mma_desc()
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 }
 
+// The MMA warp runs as one: every lane holds the same operands (they stay in
+// uniform registers) and the lane with `lead` set issues.
 template <int N>
-__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t acc)
+__device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t acc,
+                                         uint32_t lead)
 {
-    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(mma_desc<N, 0>()), "r"(acc)
+    asm volatile("{\n.reg .pred p, q;\n.reg .b64 x, y;\nsetp.ne.b32 p, %4, 0;\n"
+                 "setp.ne.b32 q, %6, 0;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %5};\n"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(mma_desc<N, 0>()), "r"(acc), "r"(kOperandHigh), "r"(lead)
                  : "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t acc)
+template <int N, int BMAJOR>
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t acc,
+                                         uint32_t lead)
 {
-    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(mma_desc<N, 1>()), "r"(acc)
+    asm volatile("{\n.reg .pred p, q;\n.reg .b64 y;\nsetp.ne.b32 p, %4, 0;\n"
+                 "setp.ne.b32 q, %6, 0;\nmov.b64 y, {%2, %5};\n"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(mma_desc<N, BMAJOR>()), "r"(acc), "r"(kOperandHigh), "r"(lead)
                  : "memory");
 }
 
@@ -243,54 +279,54 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
-// Four e4m3 values to bf16 pairs, times 2^120 and `mul` (a bf16 pair).  Moved
-// into a bf16's exponent and top mantissa bits a value reads 2^-120 of itself,
-// subnormal ones included, so one exact product puts it right.
-__device__ __forceinline__ uint2 e4m3_bf16(uint32_t w, uint32_t mul, uint32_t mul2, bool two)
+// Two e4m3 values (bytes 1 and 3 of y) to a bf16 pair, times `mul`.  Moved into
+// a bf16's exponent and top mantissa bits a value reads 2^-120 of itself,
+// subnormal ones included, so one exact product with 2^120 * scale puts it right.
+__device__ __forceinline__ uint32_t e4m3_bf16(uint32_t y, uint32_t mul)
 {
-    uint2 r;
-    uint32_t *o = &r.x;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t y = __byte_perm(w, 0, i == 0 ? 0x1404 : 0x3424); // bytes at 15..8, 31..24
-        uint32_t b = (y & 0x80008000u) | ((y & 0x7F007F00u) >> 4);
-        // 0x7F is NaN in e4m3: 480 as plain bits
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(mul));
-        if (two)
-            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(mul2));
-        o[i] = b;
-    }
-    return r;
+    uint32_t b = (y & 0x80008000u) | ((y >> 4) & 0x07F007F0u);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(mul));
+    return b;
 }
 
-// A value of 0x7F or 0xFF among four e4m3 values.
-__device__ __forceinline__ bool e4m3_has_nan(uint32_t w)
+// A value of 0x7F or 0xFF (NaN) among four e4m3 values sets a bit.
+__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w)
 {
-    const uint32_t m = w & 0x7F7F7F7Fu;
-    return ((m + 0x01010101u) & 0x80808080u) != 0u;
+    return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
-// Sixteen e4m3 values (one 16-byte piece) to two pieces of bf16, scale 2^e.
-__device__ __forceinline__ void convert16(uint4 v, float scale, uint4 &lo, uint4 &hi)
+// Scale 2^e of a row as the multiplier pairs of convert16: 2^(120 + min(e, 7)),
+// the largest that bf16 holds, and what is left of e (1 but for huge rows).
+__device__ __forceinline__ uint32_t scale_mul(float scale)
 {
-    // scale = 2^e: bf16 bits of 2^(120 + min(e, 7)), and of what is left of e
     const int e = (int)(__float_as_uint(scale) >> 23) - 127;
-    const int e1 = min(e, 7);
-    const uint32_t m1 = (uint32_t)(120 + e1 + 127) << 7, m2 = (uint32_t)(e - e1 + 127) << 7;
-    const uint32_t a = m1 * 0x10001u, b = m2 * 0x10001u;
-    const bool two = e > 7;
-    const uint2 r0 = e4m3_bf16(v.x, a, b, two), r1 = e4m3_bf16(v.y, a, b, two);
-    const uint2 r2 = e4m3_bf16(v.z, a, b, two), r3 = e4m3_bf16(v.w, a, b, two);
-    lo = make_uint4(r0.x, r0.y, r1.x, r1.y);
-    hi = make_uint4(r2.x, r2.y, r3.x, r3.y);
-    if (e4m3_has_nan(v.x) || e4m3_has_nan(v.y) || e4m3_has_nan(v.z) || e4m3_has_nan(v.w)) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t *o[2] = {&lo.x, &hi.x};
+    return (uint32_t)(247 + min(e, 7)) << 7 | (uint32_t)(127 + max(e - 7, 0)) << 23;
+}
+
+// Sixteen e4m3 values (one 16-byte piece) to two pieces of bf16.
+__device__ __forceinline__ void convert16(uint4 v, uint32_t mul, uint4 &lo, uint4 &hi)
+{
+    const uint32_t m = __byte_perm(mul, 0, 0x1010);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r[2 * i] = e4m3_bf16(__byte_perm(w[i], 0, 0x1404), m);
+        r[2 * i + 1] = e4m3_bf16(__byte_perm(w[i], 0, 0x3424), m);
+    }
+    const uint32_t nan = e4m3_nan(v.x) | e4m3_nan(v.y) | e4m3_nan(v.z) | e4m3_nan(v.w);
+    if (nan | ((mul >> 16) ^ 0x3F80u)) { // rare: NaN, or a scale above 2^7
+        const uint32_t m2 = __byte_perm(mul, 0, 0x3232);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(r[i]), "r"(m2));
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             if (((w[i >> 2] >> ((i & 3) * 8)) & 0x7Fu) == 0x7Fu)
-                o[i >> 3][(i & 7) >> 1] |= (i & 1) ? 0x7FC00000u : 0x7FC0u;
+                r[i >> 1] |= (i & 1) ? 0x7FC00000u : 0x7FC0u;
     }
+    lo = make_uint4(r[0], r[1], r[2], r[3]);
+    hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
 // Zeroes the values of a bf16 pair that are not finite; true if any was.
@@ -310,7 +346,7 @@ template <bool QUANT_, int NT_>
 struct HeadGeo {
     static constexpr bool MLA = false, QUANT = QUANT_;
     static constexpr int NT = NT_, KT = 128;
-    static constexpr int QPANELS = 2, OC = 128;    // panels of a query row; columns of O
+    static constexpr int QPANELS = 2, OC = 128;    // query panels in shared memory; columns of O
     static constexpr int DV = 128;
     static constexpr int LOAD_WG = NT == 2 ? 1 : 2; // load warpgroups
     static constexpr int STAGE = 2 * 128 * 128;    // bytes of a K or V tile
@@ -326,23 +362,31 @@ struct HeadGeo {
 
 // MLA rows: a tile of 64 latent rows is both K (9 panels: 512 + 64 columns) and
 // V; a block makes one half of the 512 value columns (O of 128 x 512 fp32 would
-// fill tensor memory).  Q takes 144 KB of shared memory, so there is one tile of
-// rows, in two parts: the value panels of this half, and the other five; the
-// next tile waits in the load threads' registers.
+// fill tensor memory).  The value panels of this half (4) serve both products
+// and live longer than the other 5 panels, so the two kinds have rings of their
+// own, two tiles each.  Query panels: those of this half stay in tensor memory
+// (they fit beside O and two S), the other five in shared memory.
 template <bool QUANT_>
 struct MlaGeo {
     static constexpr bool MLA = true, QUANT = QUANT_;
     static constexpr int NT = 1, KT = 64;
-    static constexpr int QPANELS = 9, OC = 256;
+    static constexpr int QPANELS = 5, OC = 256;
     static constexpr int DV = 512;
     static constexpr int LOAD_WG = 2;
     static constexpr int PANEL = 64 * 128;
-    static constexpr int BARS = 4; // full, empty of the two parts
-    static constexpr int RING = 9 * PANEL;
+    static constexpr int OTHER = 5 * PANEL, OWN = 4 * PANEL; // bytes of a tile's parts
+    static constexpr int BARS = 8; // full, empty of two stages of two parts
+    static constexpr int RING = 2 * (OTHER + OWN);
     static constexpr int REG_SOFTMAX = 200;
-    static constexpr int REG_LOAD = 128;
+    static constexpr int REG_LOAD = 120;
     static constexpr int S_COL(int i) { return 256 + i * 64; }
     static constexpr int O_COL(int) { return 0; }
+    static constexpr int Q_COL = 384;
+    // addresses of part 0 (other half, k_pe) and 1 (this half) of stage i
+    __device__ static uint32_t part(uint32_t ring, int which, int i)
+    {
+        return ring + (which == 0 ? i * OTHER : 2 * OTHER + i * OWN);
+    }
 };
 
 template <class G>
@@ -526,135 +570,282 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, const Work &w,
         const int row = w.row0 + r, tok = row / p.group, g = row - tok * p.group;
         const bool ok = tok < w.n;
         const int h = G::MLA ? g : w.head * p.group + g;
-        const char *src = p.q + (ok ? (w.q0 + tok) * p.q_ts + h * p.q_hs : 0) + c * 16;
+        // MLA: the other half's panels, then k_pe's
+        const int col = !G::MLA ? c : c < 32 ? (1 - w.head) * 32 + c : c + 32;
+        const char *src = p.q + (ok ? (w.q0 + tok) * p.q_ts + h * p.q_hs : 0) + col * 16;
         const int t = r >> 7, rr = r & 127;
         copy16(q_smem + ((t * G::QPANELS + (c >> 3)) << 14) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
                src, ok ? 16u : 0u);
     }
 }
 
-// Head rows in bf16: copied straight into the ring.  A lane owns one key row of
-// its warp; 16 lanes copy the 256 bytes of a row.
+// Every key of tile kt is seen by some row: its rows can be copied as they are.
+template <int KT>
+__device__ __forceinline__ bool tile_whole(const Work &w, int kt)
+{
+    const int k0 = kt * KT;
+    return (k0 >= w.lo && k0 + KT <= w.hi) || k0 + KT <= w.sk;
+}
+
+// Row of the pool where box `lane` of tile kt starts; past the pool (zeros) for a
+// bad block id.
+template <int KT>
+__device__ __forceinline__ int box_row(const AttnParams &p, const Work &w, int kt, int lane, bool &bad)
+{
+    const int64_t s = lane * p.box_rows < KT ? key_slot(p, w, kt * KT + lane * p.box_rows, bad) : 0;
+    return (int)(s < 0 ? p.num_blocks * p.block : s);
+}
+
+// Box copies that may be in flight, a bit per barrier.  A block waits for them
+// before its shared memory goes, also when it gives up early.
+struct Flights {
+    uint32_t boxes = 0, parity = 0;
+
+    __device__ void filled(int bar, bool by_boxes, int full_parity)
+    {
+        const uint32_t bit = 1u << bar;
+        boxes = by_boxes ? boxes | bit : boxes & ~bit;
+        parity = full_parity ? parity | bit : parity & ~bit;
+    }
+
+    __device__ void land(uint32_t bars)
+    {
+        int none = 0;
+        for (int i = 0; i < 32; ++i)
+            if ((boxes >> i) & 1u)
+                bar_wait(bars + i * 8, (parity >> i) & 1u, &none, 1000000000ll);
+    }
+};
+
+// Head rows in bf16, straight into the ring.  Whole tiles are boxes of the
+// tensor maps that one warp asks for (a box is at most a block of the pool); tiles
+// that hold keys nobody sees, and pools whose blocks do not divide a tile, are
+// copied row by row with zeros in the place of those keys: a lane owns one key
+// row of its warp, 16 lanes copy the 256 bytes of a row.  Every warp waits for
+// every stage and signals it, also where one warp copies for all: none may run
+// ahead or fall behind by more than a phase, the parity would not show it.
 template <class G>
-__device__ __forceinline__ bool load_heads_bf16(const AttnParams &p, const Work &w, uint32_t ring,
+__device__ __forceinline__ void load_heads_bf16(const AttnParams &p, const Work &w, uint32_t ring,
                                                 uint32_t bars, int warp, int lane,
                                                 volatile int *abort, bool &bad)
 {
     constexpr int WARPS = G::LOAD_WG * 4, ROWS = G::KT / WARPS; // rows of a warp: 32 or 16
     const int base = warp * ROWS;
     const int c = lane & 15, half = lane >> 4;
-    auto slot_at = [&](int v) {
-        return v < w.end ? key_slot(p, w, real_tile(w, v) * G::KT + base + (lane & (ROWS - 1)), bad)
-                         : (int64_t)-1;
+    auto whole = [&](int v) { return p.box_rows > 0 && tile_whole<G::KT>(w, real_tile(w, v)); };
+    auto rows_at = [&](int v) -> int64_t {
+        if (v >= w.end)
+            return -1;
+        const int kt = real_tile(w, v);
+        if (whole(v))
+            return warp == 0 ? box_row<G::KT>(p, w, kt, lane, bad) : 0;
+        return key_slot(p, w, kt * G::KT + base + (lane & (ROWS - 1)), bad);
     };
-    int64_t next = slot_at(w.beg);
+    int64_t next = rows_at(w.beg);
+    Flights fly;
     int stage = 0, phase = 1;
-    for (int v = w.beg; v < w.end; ++v) {
+    bool ok = true;
+    for (int v = w.beg; ok && v < w.end; ++v) {
         const int64_t slot = next;
-        next = slot_at(v + 1); // the next tile's block ids, in flight with this tile
+        next = rows_at(v + 1); // the next tile's block ids, in flight with this tile
+        const bool boxes = whole(v);
 #pragma unroll
         for (int part = 0; part < 2; ++part) { // K, then V
-            const char *src = part == 0 ? p.rot : p.copy;
-            const int64_t ss = part == 0 ? p.rot_ss : p.copy_ss;
-            if (!bar_wait(bars + (G::STAGES + stage) * 8, phase, abort, p.wait_limit_ns))
-                return false;
-            const uint32_t dst = ring + stage * G::STAGE + ((c >> 3) << 14);
-            const char *col = src + w.head * 256 + c * 16;
+            const uint32_t full = bars + stage * 8, dst = ring + stage * G::STAGE;
+            ok = bar_wait(full + G::STAGES * 8, phase, abort, p.wait_limit_ns);
+            if (!ok)
+                break;
+            fly.filled(stage, boxes, phase ^ 1);
+            if (boxes) {
+                __syncwarp();
+                if (lane == 0)
+                    bar_signal_bulk(full, 32, warp == 0 ? G::STAGE : 0);
+                if (warp == 0) {
+                    if (lane * p.box_rows < G::KT) {
+                        const CUtensorMap *map = part == 0 ? &p.rot_map : &p.copy_map;
+                        const uint32_t at = dst + lane * p.box_rows * 128;
+                        copy_box(at, map, w.head * 128, (int)slot, full);
+                        copy_box(at + 16384, map, w.head * 128 + 64, (int)slot, full);
+                    }
+                }
+            } else {
+                const char *src = part == 0 ? p.rot : p.copy;
+                const int64_t ss = part == 0 ? p.rot_ss : p.copy_ss;
+                const char *col = src + w.head * 256 + c * 16;
 #pragma unroll
-            for (int i = 0; i < ROWS / 2; ++i) {
-                const int r = i * 2 + half;
-                const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, r);
-                const int row = base + r;
-                copy16(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4), col + (s < 0 ? 0 : s * ss),
-                       s < 0 ? 0u : 16u);
+                for (int i = 0; i < ROWS / 2; ++i) {
+                    const int r = i * 2 + half;
+                    const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, r);
+                    const int row = base + r;
+                    copy16(dst + ((c >> 3) << 14) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                           col + (s < 0 ? 0 : s * ss), s < 0 ? 0u : 16u);
+                }
+                bar_signal_copies(full);
             }
-            bar_signal_copies(bars + stage * 8);
             if (++stage == G::STAGES) {
                 stage = 0;
                 phase ^= 1;
             }
         }
     }
-    return true;
+    if (warp == 0)
+        fly.land(bars);
 }
 
-// Head rows in e4m3: the next K and V tile wait in registers while the one
-// before is converted into the ring.  8 lanes hold the 128 bytes of a row.
+// Head rows in e4m3: the next tiles (one, or two where a thread holds less of
+// each) wait in registers while the one before is converted into the ring.  8
+// lanes hold the 128 bytes of a row.
 template <class G>
-__device__ __forceinline__ bool load_heads_e4m3(const AttnParams &p, const Work &w, uint32_t ring,
+__device__ __forceinline__ void load_heads_e4m3(const AttnParams &p, const Work &w, uint32_t ring,
                                                 uint32_t bars, int warp, int lane,
                                                 volatile int *abort, bool &bad)
 {
-    constexpr int WARPS = G::LOAD_WG * 4, ROWS = G::KT / WARPS, IT = ROWS / 4;
+    constexpr int WARPS = G::LOAD_WG * 4, ROWS = G::KT / WARPS, IT = ROWS / 4, AHEAD = 8 / IT;
     const int base = warp * ROWS;
     const int c = lane & 7, sub = lane >> 3;
-    uint4 raw[2][IT];
-    float scale[2];
+    uint4 raw[AHEAD][2][IT];
+    uint32_t mul[AHEAD][2];
     auto slot_at = [&](int v) {
         return v < w.end ? key_slot(p, w, real_tile(w, v) * G::KT + base + (lane & (ROWS - 1)), bad)
                          : (int64_t)-1;
     };
-    auto fetch = [&](int part, int64_t slot) {
+    auto fetch = [&](uint4 (&to)[IT], uint32_t &m, int part, int64_t slot) {
         const char *src = (part == 0 ? p.rot : p.copy) + w.head * 128 + c * 16;
         const int64_t ss = part == 0 ? p.rot_ss : p.copy_ss;
         const float *sc = part == 0 ? p.rs + slot * p.rs_ss : p.cs + slot * p.cs_ss;
-        scale[part] = slot < 0 ? 1.0f : __ldg(sc + w.head);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, i * 4 + sub);
-            raw[part][i] = s < 0 ? make_uint4(0, 0, 0, 0)
-                                 : __ldg(reinterpret_cast<const uint4 *>(src + s * ss));
+            to[i] = s < 0 ? make_uint4(0, 0, 0, 0)
+                          : ld_stream(src + s * ss);
         }
+        m = scale_mul(slot < 0 ? 1.0f : __ldg(sc + w.head));
     };
-    int64_t next = slot_at(w.beg);
-    fetch(0, next);
-    fetch(1, next);
-    next = slot_at(w.beg + 1);
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+        const int64_t slot = slot_at(w.beg + a);
+        fetch(raw[a][0], mul[a][0], 0, slot);
+        fetch(raw[a][1], mul[a][1], 1, slot);
+    }
+    int64_t next = slot_at(w.beg + AHEAD);
+    // a lane's two pieces of a row: the odd one first in the upper panel, so that
+    // the eight lanes of a row meet eight different 16-byte columns
+    const int first = c >> 2;
+    const int c0 = (2 * c + first) & 7, c1 = (2 * c + 1 - first) & 7;
     int stage = 0, phase = 1;
-    for (int v = w.beg; v < w.end; ++v) {
-        const int64_t slot = next;
-        next = slot_at(v + 2);
+    for (int v0 = w.beg; v0 < w.end; v0 += AHEAD) {
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-            if (!bar_wait(bars + (G::STAGES + stage) * 8, phase, abort, p.wait_limit_ns))
-                return false;
-            const uint32_t dst = ring + stage * G::STAGE + ((c >> 2) << 14);
-            const int first = c >> 2; // odd pieces first in the upper panel: no bank conflict
+        for (int a = 0; a < AHEAD; ++a) {
+            const int v = v0 + a;
+            if (v >= w.end)
+                break;
+            const int64_t slot = next;
+            next = slot_at(v + AHEAD + 1);
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int r = i * 4 + sub, row = base + r;
-                const float s = __shfl_sync(0xFFFFFFFFu, scale[part], r);
-                uint4 a, b;
-                convert16(raw[part][i], s, a, b);
-                const int c0 = (2 * c + first) & 7, c1 = (2 * c + 1 - first) & 7;
-                sts16(dst + row * 128 + ((c0 ^ (row & 7)) << 4), first ? b : a);
-                sts16(dst + row * 128 + ((c1 ^ (row & 7)) << 4), first ? a : b);
-            }
-            async_fence();
-            bar_signal(bars + stage * 8);
-            if (v + 1 < w.end)
-                fetch(part, slot);
-            if (++stage == G::STAGES) {
-                stage = 0;
-                phase ^= 1;
+            for (int part = 0; part < 2; ++part) {
+                if (!bar_wait(bars + (G::STAGES + stage) * 8, phase, abort, p.wait_limit_ns))
+                    return;
+                const uint32_t dst = ring + stage * G::STAGE + (first << 14) + base * 128;
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    const int r = i * 4 + sub;
+                    const uint32_t m = __shfl_sync(0xFFFFFFFFu, mul[a][part], r);
+                    uint4 x, y;
+                    convert16(raw[a][part][i], m, x, y);
+                    sts16(dst + r * 128 + ((c0 ^ (r & 7)) << 4), first ? y : x);
+                    sts16(dst + r * 128 + ((c1 ^ (r & 7)) << 4), first ? x : y);
+                }
+                async_fence();
+                bar_signal(bars + stage * 8);
+                fetch(raw[a][part], mul[a][part], part, slot);
+                if (++stage == G::STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
         }
     }
-    return true;
 }
 
-// MLA rows.  Part 0: the other half's value panels and k_pe, part 1: this half's
-// value panels.  A warp owns 8 rows; 8 lanes hold a 128-byte piece of a row.
+// MLA rows in bf16: boxes for whole tiles, else row by row with zeros in the
+// place of keys that nobody sees.  Part 0: the other half's panels and k_pe,
+// part 1: this half's.  A warp owns 8 rows; 8 lanes copy 128 bytes of a row.
 template <class G>
-__device__ __forceinline__ bool load_mla(const AttnParams &p, const Work &w, uint32_t ring,
-                                         uint32_t bars, int warp, int lane, volatile int *abort,
-                                         bool &bad)
+__device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w, uint32_t ring,
+                                              uint32_t bars, int warp, int lane,
+                                              volatile int *abort, bool &bad)
 {
-    constexpr int PG = G::QUANT ? 4 : 8;         // 128-byte pieces of the latent row
-    constexpr int HALF = PG / 2;                 // of one half
     const int base = warp * 8, c = lane & 7, sub = lane >> 3;
-    uint4 lat[2][HALF][2], pe[2];
-    float scale[2][2];
+    auto whole = [&](int v) { return p.box_rows > 0 && tile_whole<G::KT>(w, real_tile(w, v)); };
+    auto rows_at = [&](int v) -> int64_t {
+        if (v >= w.end)
+            return -1;
+        const int kt = real_tile(w, v);
+        if (whole(v))
+            return warp == 0 ? box_row<G::KT>(p, w, kt, lane, bad) : 0;
+        return key_slot(p, w, kt * G::KT + base + c, bad);
+    };
+    int64_t next = rows_at(w.beg);
+    Flights fly;
+    bool ok = true;
+    for (int v = w.beg; ok && v < w.end; ++v) {
+        const int64_t slot = next;
+        next = rows_at(v + 1);
+        const bool boxes = whole(v);
+        const int ord = v - w.beg, stage = ord & 1, phase = ((ord >> 1) & 1) ^ 1;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            const uint32_t full = bars + (part * 2 + stage) * 8, dst = G::part(ring, part, stage);
+            const int half = part == 0 ? 1 - w.head : w.head;
+            ok = bar_wait(full + 4 * 8, phase, abort, p.wait_limit_ns);
+            if (!ok)
+                break;
+            fly.filled(part * 2 + stage, boxes, phase ^ 1);
+            if (boxes) {
+                __syncwarp();
+                if (lane == 0)
+                    bar_signal_bulk(full, 32, warp != 0 ? 0 : part == 0 ? G::OTHER : G::OWN);
+                if (warp == 0) {
+                    if (lane * p.box_rows < G::KT) {
+                        const uint32_t at = dst + lane * p.box_rows * 128;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            copy_box(at + i * G::PANEL, &p.copy_map, half * 256 + i * 64, (int)slot,
+                                     full);
+                        if (part == 0)
+                            copy_box(at + 4 * G::PANEL, &p.rot_map, 0, (int)slot, full);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, i * 4 + sub);
+                    const int row = base + i * 4 + sub;
+                    const uint32_t at = dst + row * 128 + ((c ^ (row & 7)) << 4), n = s < 0 ? 0 : 16;
+                    const char *src = p.copy + (s < 0 ? 0 : s * p.copy_ss) + half * 512 + c * 16;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        copy16(at + g * G::PANEL, src + g * 128, n);
+                    if (part == 0)
+                        copy16(at + 4 * G::PANEL, p.rot + (s < 0 ? 0 : s * p.rot_ss) + c * 16, n);
+                }
+                bar_signal_copies(full);
+            }
+        }
+    }
+    if (warp == 0)
+        fly.land(bars);
+}
+
+// MLA rows with an e4m3 latent: the next tile waits in registers.
+template <class G>
+__device__ __forceinline__ void load_mla_e4m3(const AttnParams &p, const Work &w, uint32_t ring,
+                                              uint32_t bars, int warp, int lane,
+                                              volatile int *abort, bool &bad)
+{
+    const int base = warp * 8, c = lane & 7, sub = lane >> 3;
+    uint4 lat[2][2][2], pe[2]; // [part][group of 128][row]
+    uint32_t mul[2][2];
     auto slot_at = [&](int v) {
         return v < w.end ? key_slot(p, w, real_tile(w, v) * G::KT + base + c, bad) : (int64_t)-1;
     };
@@ -663,102 +854,91 @@ __device__ __forceinline__ bool load_mla(const AttnParams &p, const Work &w, uin
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, i * 4 + sub);
-            const char *src = p.copy + (s < 0 ? 0 : s * p.copy_ss) + half * HALF * 128 + c * 16;
+            const char *src = p.copy + (s < 0 ? 0 : s * p.copy_ss) + half * 256 + c * 16;
 #pragma unroll
-            for (int g = 0; g < HALF; ++g)
+            for (int g = 0; g < 2; ++g)
                 lat[part][g][i] = s < 0 ? make_uint4(0, 0, 0, 0)
                                         : __ldg(reinterpret_cast<const uint4 *>(src + g * 128));
             if (part == 0)
                 pe[i] = s < 0 ? make_uint4(0, 0, 0, 0)
                               : __ldg(reinterpret_cast<const uint4 *>(p.rot + s * p.rot_ss + c * 16));
         }
-        if (G::QUANT) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) // lane c of each eight: the row's scale
-                scale[part][g] = slot < 0 ? 1.0f : __ldg(p.cs + slot * p.cs_ss + half * 2 + g);
-        }
+        for (int g = 0; g < 2; ++g) // lane c of each eight: the row's scale
+            mul[part][g] =
+                scale_mul(slot < 0 ? 1.0f : __ldg(p.cs + slot * p.cs_ss + half * 2 + g));
     };
-    auto store = [&](int part) {
-        const int half = part == 0 ? 1 - w.head : w.head;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = i * 4 + sub, row = base + r;
-            const uint32_t at = ring + row * 128;
-            if (G::QUANT) {
-                const int first = c >> 2;
-                const int c0 = (2 * c + first) & 7, c1 = (2 * c + 1 - first) & 7;
-#pragma unroll
-                for (int g = 0; g < HALF; ++g) {
-                    const float s = __shfl_sync(0xFFFFFFFFu, scale[part][g & 1], r);
-                    uint4 a, b;
-                    convert16(lat[part][g][i], s, a, b);
-                    const uint32_t dst = at + (half * 4 + g * 2 + (c >> 2)) * G::PANEL;
-                    sts16(dst + ((c0 ^ (row & 7)) << 4), first ? b : a);
-                    sts16(dst + ((c1 ^ (row & 7)) << 4), first ? a : b);
-                }
-            } else {
-#pragma unroll
-                for (int g = 0; g < HALF; ++g)
-                    sts16(at + (half * 4 + g) * G::PANEL + ((c ^ (row & 7)) << 4), lat[part][g][i]);
-            }
-            if (part == 0)
-                sts16(at + 8 * G::PANEL + ((c ^ (row & 7)) << 4), pe[i]);
-        }
-    };
+    const int first = c >> 2;
+    const int c0 = (2 * c + first) & 7, c1 = (2 * c + 1 - first) & 7;
     int64_t next = slot_at(w.beg);
     fetch(0, next);
     fetch(1, next);
     next = slot_at(w.beg + 1);
-    int phase = 1;
     for (int v = w.beg; v < w.end; ++v) {
         const int64_t slot = next;
         next = slot_at(v + 2);
+        const int ord = v - w.beg, stage = ord & 1, phase = ((ord >> 1) & 1) ^ 1;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
-            if (!bar_wait(bars + (2 + part) * 8, phase, abort, p.wait_limit_ns))
-                return false;
-            store(part);
+            const uint32_t full = bars + (part * 2 + stage) * 8, dst = G::part(ring, part, stage);
+            if (!bar_wait(full + 4 * 8, phase, abort, p.wait_limit_ns))
+                return;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = i * 4 + sub;
+                const uint32_t at = dst + (base + r) * 128;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint4 x, y;
+                    convert16(lat[part][g][i], __shfl_sync(0xFFFFFFFFu, mul[part][g], r), x, y);
+                    const uint32_t to = at + (g * 2 + first) * G::PANEL;
+                    sts16(to + ((c0 ^ (r & 7)) << 4), first ? y : x);
+                    sts16(to + ((c1 ^ (r & 7)) << 4), first ? x : y);
+                }
+                if (part == 0)
+                    sts16(at + 4 * G::PANEL + ((c ^ (r & 7)) << 4), pe[i]);
+            }
             async_fence();
-            bar_signal(bars + part * 8);
-            if (v + 1 < w.end)
-                fetch(part, slot);
+            bar_signal(full);
+            fetch(part, slot);
         }
-        phase ^= 1;
     }
-    return true;
 }
 
 // ---------------------------------------------------------------------------
-// MMA role (one thread)
+// MMA role (one warp)
 // ---------------------------------------------------------------------------
 
-// S = Q Kᵀ of one row tile over panels [p0, p1) of K.
-template <int N, int PANEL>
-__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q, uint32_t k, int p0, int p1,
-                                             bool first)
+// S = Q Kᵀ of one row tile over PN panels of Q and K.
+template <int N, int PANEL, int PN>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q, uint32_t k, bool first,
+                                             uint32_t lead)
 {
-    for (int pn = p0; pn < p1; ++pn) {
+    const uint32_t a = operand(q, 16), b = operand(k, 16);
+#pragma unroll
+    for (int pn = 0; pn < PN; ++pn)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-            mma_smem<N>(d, operand(q + (pn << 14) + kk * 32, 16),
-                        operand(k + pn * PANEL + kk * 32, 16), !(first && pn == p0 && kk == 0));
-    }
+            mma_smem<N>(d, a + pn * (16384 >> 4) + kk * 2, b + pn * (PANEL >> 4) + kk * 2,
+                        !(first && pn == 0 && kk == 0), lead);
 }
 
 // O += P V: P in tensor memory (two keys to a column), V in panels.
 template <int N, int KT>
-__device__ __forceinline__ void issue_values(uint32_t d, uint32_t pt, uint32_t v, bool first)
+__device__ __forceinline__ void issue_values(uint32_t d, uint32_t pt, uint32_t v, bool first,
+                                             uint32_t lead)
 {
+    const uint32_t b = operand(v, KT * 128);
 #pragma unroll
     for (int kk = 0; kk < KT / 16; ++kk)
-        mma_tmem<N>(d, pt + kk * 8, operand(v + kk * 2048, KT * 128), !(first && kk == 0));
+        mma_tmem<N, 1>(d, pt + kk * 8, b + kk * (2048 >> 4), !(first && kk == 0), lead);
 }
 
 template <class G>
 __device__ __forceinline__ bool run_mma_heads2(const AttnParams &p, const Work &w,
                                                const TileMask (&mask)[2], uint32_t tmem,
                                                uint32_t q_smem, uint32_t ring, uint32_t bars,
-                                               volatile int *abort)
+                                               uint32_t lead, volatile int *abort)
 {
     const uint32_t full = bars + kBarRing * 8, empty = full + G::STAGES * 8;
     bool pend[2] = {false, false}, begun[2] = {false, false};
@@ -772,7 +952,7 @@ __device__ __forceinline__ bool run_mma_heads2(const AttnParams &p, const Work &
         pphase[t] ^= 1;
         mma_fence_after();
         issue_values<128, 128>(tmem + G::O_COL(t), tmem + G::S_COL(t), ring + vstage * G::STAGE,
-                               !begun[t]);
+                               !begun[t], lead);
         begun[t] = true;
         pend[t] = false;
         return true;
@@ -787,15 +967,15 @@ __device__ __forceinline__ bool run_mma_heads2(const AttnParams &p, const Work &
             if (pend[t] && !values(t))
                 return false;
             if (t == 1 && v_open)
-                bar_signal_mma(empty + vstage * 8);
+                bar_signal_mma(empty + vstage * 8, lead);
             if (tile_active<G::KT>(mask[t], kt)) {
-                issue_scores<128, 16384>(tmem + G::S_COL(t), q_smem + (t << 15),
-                                         ring + stage * G::STAGE, 0, 2, true);
-                bar_signal_mma(bars + (kBarS + t) * 8);
+                issue_scores<128, 16384, 2>(tmem + G::S_COL(t), q_smem + (t << 15),
+                                            ring + stage * G::STAGE, true, lead);
+                bar_signal_mma(bars + (kBarS + t) * 8, lead);
                 pend[t] = true;
             }
         }
-        bar_signal_mma(empty + stage * 8);
+        bar_signal_mma(empty + stage * 8, lead);
         if (++stage == G::STAGES) {
             stage = 0;
             phase ^= 1;
@@ -815,7 +995,7 @@ __device__ __forceinline__ bool run_mma_heads2(const AttnParams &p, const Work &
     for (int t = 0; t < 2; ++t)
         if (pend[t] && !values(t))
             return false;
-    bar_signal_mma(bars + kBarDone * 8);
+    bar_signal_mma(bars + kBarDone * 8, lead);
     return true;
 }
 
@@ -824,59 +1004,61 @@ __device__ __forceinline__ bool run_mma_heads2(const AttnParams &p, const Work &
 template <class G>
 __device__ __forceinline__ bool run_mma_one(const AttnParams &p, const Work &w, uint32_t tmem,
                                             uint32_t q_smem, uint32_t ring, uint32_t bars,
-                                            volatile int *abort)
+                                            uint32_t lead, volatile int *abort)
 {
     const uint32_t full = bars + kBarRing * 8;
-    uint32_t pphase[2] = {0, 0};
     int stage = 0, phase = 0, vstage = 0;
-    const int own = w.head * 4, other = 4 - own; // MLA: value panels of this half, of the other
     for (int v = w.beg; v <= w.end; ++v) {
-        const int i = (v - w.beg) & 1;
+        const int ord = v - w.beg, i = ord & 1, turn = (ord >> 1) & 1;
         const uint32_t s_col = tmem + G::S_COL(i);
         const bool more = v < w.end;
         if (more) {
-            if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
-                return false;
-            async_fence();
             if constexpr (G::MLA) {
-                issue_scores<64, G::PANEL>(s_col, q_smem, ring, other, other + 4, true);
-                issue_scores<64, G::PANEL>(s_col, q_smem, ring, 8, 9, false);
-                bar_signal_mma(full + 2 * 8);
+                if (!bar_wait(full + i * 8, turn, abort, p.wait_limit_ns))
+                    return false;
+                async_fence();
+                issue_scores<64, G::PANEL, 5>(s_col, q_smem, G::part(ring, 0, i), true, lead);
+                bar_signal_mma(full + (4 + i) * 8, lead);
+                if (!bar_wait(full + (2 + i) * 8, turn, abort, p.wait_limit_ns))
+                    return false;
+                async_fence();
+                const uint32_t k = operand(G::part(ring, 1, i), 16);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    mma_tmem<64, 0>(s_col, tmem + G::Q_COL + j * 8,
+                                    k + (j >> 2) * (G::PANEL >> 4) + (j & 3) * 2, 1u, lead);
+                bar_signal_mma(bars + (kBarS + i) * 8, lead);
             } else {
-                issue_scores<128, 16384>(s_col, q_smem, ring + stage * G::STAGE, 0, 2, true);
-                bar_signal_mma(bars + (kBarS + i) * 8);
-                bar_signal_mma(full + (G::STAGES + stage) * 8);
+                if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
+                    return false;
+                async_fence();
+                issue_scores<128, 16384, 2>(s_col, q_smem, ring + stage * G::STAGE, true, lead);
+                bar_signal_mma(bars + (kBarS + i) * 8, lead);
+                bar_signal_mma(full + (G::STAGES + stage) * 8, lead);
                 if (++stage == G::STAGES) {
                     stage = 0;
                     phase ^= 1;
                 }
             }
         }
-        if (v > w.beg) { // weights of the tile before
-            if (!bar_wait(bars + (kBarP + (1 - i)) * 8, pphase[1 - i], abort, p.wait_limit_ns))
+        if (ord > 0) { // weights of the tile before
+            const int j = 1 - i;
+            if (!bar_wait(bars + (kBarP + j) * 8, ((ord - 1) >> 1) & 1, abort, p.wait_limit_ns))
                 return false;
-            pphase[1 - i] ^= 1;
             mma_fence_after();
             if constexpr (G::MLA) {
-                issue_values<256, 64>(tmem + G::O_COL(0), tmem + G::S_COL(1 - i),
-                                      ring + own * G::PANEL, v == w.beg + 1);
-                bar_signal_mma(full + 3 * 8);
+                issue_values<256, 64>(tmem + G::O_COL(0), tmem + G::S_COL(j), G::part(ring, 1, j),
+                                      ord == 1, lead);
+                bar_signal_mma(full + (6 + j) * 8, lead);
             } else {
-                issue_values<128, 128>(tmem + G::O_COL(0), tmem + G::S_COL(1 - i),
-                                       ring + vstage * G::STAGE, v == w.beg + 1);
-                bar_signal_mma(full + (G::STAGES + vstage) * 8);
+                issue_values<128, 128>(tmem + G::O_COL(0), tmem + G::S_COL(j),
+                                       ring + vstage * G::STAGE, ord == 1, lead);
+                bar_signal_mma(full + (G::STAGES + vstage) * 8, lead);
             }
-            bar_signal_mma(bars + kBarO * 8);
+            bar_signal_mma(bars + kBarO * 8, lead);
         }
-        if (more) {
-            if constexpr (G::MLA) {
-                if (!bar_wait(full + 8, phase, abort, p.wait_limit_ns))
-                    return false;
-                async_fence();
-                issue_scores<64, G::PANEL>(s_col, q_smem, ring, own, own + 4, false);
-                bar_signal_mma(bars + (kBarS + i) * 8);
-                phase ^= 1;
-            } else {
+        if constexpr (!G::MLA) {
+            if (more) {
                 vstage = stage;
                 if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
                     return false;
@@ -888,7 +1070,7 @@ __device__ __forceinline__ bool run_mma_one(const AttnParams &p, const Work &w, 
             }
         }
     }
-    bar_signal_mma(bars + kBarDone * 8);
+    bar_signal_mma(bars + kBarDone * 8, lead);
     return true;
 }
 
@@ -933,6 +1115,26 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
     const int sk = p.window ? min(p.sinks, hi) : 0;
     const bool one_token = G::NT == 1 && m.pos0 == m.pos1;
     const float c = p.scale * 1.4426950408889634f;
+    if constexpr (G::MLA) { // the query panels of this half, a row to a lane
+        const char *src = p.q + (valid ? (w.q0 + tok) * p.q_ts + g * p.q_hs : 0) + w.head * 512;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            uint32_t x[32];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint4 y = valid ? __ldg(reinterpret_cast<const uint4 *>(src + i * 128) + j)
+                                      : make_uint4(0, 0, 0, 0);
+                x[4 * j] = y.x;
+                x[4 * j + 1] = y.y;
+                x[4 * j + 2] = y.z;
+                x[4 * j + 3] = y.w;
+            }
+            tmem_st32(tmem + G::Q_COL + i * 32 + lanes, x);
+        }
+        tmem_st_wait();
+        mma_fence_before();
+        bar_signal(bars + kBarQ * 8);
+    }
     RowState st;
     int done = 0; // tiles of this row tile so far
     for (int v = w.beg; v < w.end; ++v) {
@@ -963,11 +1165,16 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
                 s[i] = see ? s[i] : 0xFF800000u;
             }
         }
-        float top = __uint_as_float(s[0]);
+        float t4[4]; // four chains: the maximum's latency, not its count, is what costs
 #pragma unroll
-        for (int i = 1; i < KT; ++i)
-            top = fmaxf(top, __uint_as_float(s[i]));
-        top = fmaxf(top, st.top);
+        for (int i = 0; i < 4; ++i)
+            t4[i] = fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 4]));
+#pragma unroll
+        for (int i = 8; i < KT; i += 8)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                t4[j] = fmaxf(t4[j], fmaxf(__uint_as_float(s[i + j]), __uint_as_float(s[i + j + 4])));
+        const float top = fmaxf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), st.top);
         const bool grew = (top - st.top) * c > kLazy; // also from -inf
         if (done == 0) {
             st.top = top;
@@ -998,7 +1205,7 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
         const float off = st.top == -INFINITY ? 0.0f : -st.top * c;
         const f2 c2 = f2_of_bits(__float_as_uint(c), __float_as_uint(c));
         const f2 off2 = f2_of_bits(__float_as_uint(off), __float_as_uint(off));
-        f2 sum2 = f2_of_bits(0u, 0u);
+        f2 sum2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int i = 0; i < KT; i += 32) {
             uint32_t w16[16];
@@ -1009,13 +1216,15 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
                 asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
                 a = exp2_fast(a);
                 b = exp2_fast(b);
-                sum2 = f2_add(sum2, f2_of_bits(__float_as_uint(a), __float_as_uint(b)));
+                sum2[j & 3] = f2_add(sum2[j & 3], f2_of_bits(__float_as_uint(a), __float_as_uint(b)));
                 w16[j] = pack_bf16(a, b);
             }
             tmem_st16(s_col + i / 2, w16);
         }
         float sa, sb;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(sa), "=f"(sb) : "l"(sum2));
+        asm("mov.b64 {%0, %1}, %2;"
+            : "=f"(sa), "=f"(sb)
+            : "l"(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]))));
         st.sum += sa + sb;
         tmem_st_wait();
         if (!full && !one_token) {
@@ -1026,10 +1235,11 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
             uint32_t vbase;
             int pieces;
             if (G::MLA) {
-                if (!bar_wait(bars + (kBarRing + 1) * 8, ord & 1, abort, p.wait_limit_ns))
+                if (!bar_wait(bars + (kBarRing + 2 + (ord & 1)) * 8, (ord >> 1) & 1, abort,
+                              p.wait_limit_ns))
                     return false;
-                vbase = ring + w.head * 4 * 8192;
-                pieces = 4 * 8192 / 16;
+                vbase = MlaGeo<G::QUANT>::part(ring, 1, ord & 1);
+                pieces = MlaGeo<G::QUANT>::OWN / 16;
             } else {
                 constexpr int ST = G::BARS / 2;
                 const int item = 2 * ord + 1;
@@ -1185,7 +1395,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
     mask[0] = tile_mask(p, w.n, w.len, w.row0);
     mask[1] = tile_mask(p, w.n, w.len, w.row0 + kRows);
     if (tid == 0) {
-        bar_init(bars + kBarQ * 8, G::LOAD_WG * 128);
+        bar_init(bars + kBarQ * 8,
+                 G::LOAD_WG * 128 + (G::MLA ? (mask[0].rows + 31) / 32 * 32 : 0));
         bar_init(bars + kBarDone * 8, 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(bars + (kBarS + i) * 8, 1);
@@ -1224,8 +1435,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
         load_queries<G>(p, w, q_smem, lt, G::LOAD_WG * 128);
         bar_signal_copies(bars + kBarQ * 8);
         bool bad = false;
-        if constexpr (G::MLA)
-            load_mla<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
+        if constexpr (G::MLA && G::QUANT)
+            load_mla_e4m3<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
+        else if constexpr (G::MLA)
+            load_mla_bf16<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
         else if constexpr (G::QUANT)
             load_heads_e4m3<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
         else
@@ -1235,18 +1448,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         reg_dec<kRegMma>();
-        if (warp == 12 && lane == 0) {
+        if (warp == 12) {
+            const uint32_t lead = elect_lane();
             bool ok = bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
             if (ok) {
                 async_fence();
+                mma_fence_after();
                 if constexpr (G::NT == 2)
-                    ok = run_mma_heads2<G>(p, w, mask, tmem, q_smem, ring, bars, &s_abort);
+                    ok = run_mma_heads2<G>(p, w, mask, tmem, q_smem, ring, bars, lead, &s_abort);
                 else
-                    ok = run_mma_one<G>(p, w, tmem, q_smem, ring, bars, &s_abort);
+                    ok = run_mma_one<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
             }
             if (!ok) { // let what was issued finish before tensor memory goes
                 int none = 0;
-                bar_signal_mma(bars + (kBarO + 1) * 8);
+                bar_signal_mma(bars + (kBarO + 1) * 8, lead);
                 bar_wait(bars + (kBarO + 1) * 8, 0, &none, 1000000000ll);
             }
         }
@@ -1323,8 +1538,33 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
         p.lse[at] = sum == 0.0f ? -INFINITY : ref + logf(sum);
 }
 
+// Tensor map of one part of the pool's rows (`width` bf16 columns): boxes of 64
+// columns and p.box_rows rows, swizzled as the MMAs read them.
+bool encode_map(CUtensorMap *map, const char *base, int64_t row_bytes, int64_t rows, int width,
+                int box_rows)
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                             cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    if (!encode)
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<char *>(base), dims, strides,
+                  box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class G>
-cudaError_t launch(const AttnParams &p, int64_t blocks, cudaStream_t stream)
+cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
 {
     constexpr int bytes = Smem<G>::BYTES;
     static_assert(bytes <= 227 * 1024, "shared memory");
@@ -1332,6 +1572,20 @@ cudaError_t launch(const AttnParams &p, int64_t blocks, cudaStream_t stream)
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess)
         return e;
+    // bf16 rows are copied as boxes where a block of the pool is a multiple of 8
+    // rows (the swizzle's period) and divides a key tile, or the other way round
+    p.box_rows = 0;
+    if constexpr (!G::QUANT) {
+        const int b = p.block;
+        const int64_t rows = p.num_blocks * b;
+        const int heads = G::MLA ? 1 : p.heads / p.group;
+        if (b % 8 == 0 && (G::KT % b == 0 || b % G::KT == 0) && rows < 0x7FFFFFFFll) {
+            const int box = std::min(b, G::KT);
+            if (encode_map(&p.copy_map, p.copy, p.copy_ss, rows, G::MLA ? 512 : heads * 128, box) &&
+                encode_map(&p.rot_map, p.rot, p.rot_ss, rows, G::MLA ? 64 : heads * 128, box))
+                p.box_rows = box;
+        }
+    }
     // the register shares of the warpgroups come out of what a block starts with
     cudaFuncAttributes fa;
     if ((e = cudaFuncGetAttributes(&fa, attention_kernel<G>)) != cudaSuccess)
@@ -1385,8 +1639,7 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
     return pl;
 }
 
-cudaError_t launch_attention(const AttnParams &p, RowKind kind, const AttnPlan &pl,
-                             cudaStream_t stream)
+cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cudaStream_t stream)
 {
     const bool quant = p.cs != nullptr;
     if (kind == RowKind::Mla)

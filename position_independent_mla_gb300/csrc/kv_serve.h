@@ -2,6 +2,8 @@
 // cache rows (kv_quant.cu) and attention over the paged cache (kv_attention.cu).
 #pragma once
 
+#include <cuda.h>
+
 #include "kv_launch.h"
 
 namespace kvr {
@@ -77,6 +79,9 @@ struct AttnParams {
     float *part, *part_lse; // [max_splits][total_q][heads][value width], [..][heads]
     int64_t wait_limit_ns;
     uint32_t *header;
+    // bf16 pools, filled in by launch_attention: rows of a box (0: no boxes)
+    int32_t box_rows;
+    CUtensorMap copy_map, rot_map;
 };
 
 // Sizes of a call that the host knows, and the launch they lead to.
@@ -94,7 +99,6 @@ struct AttnPlan {
 };
 
 AttnPlan plan_attention(RowKind kind, const AttnShape &a);
-cudaError_t launch_attention(const AttnParams &p, RowKind kind, const AttnPlan &pl,
-                             cudaStream_t stream);
+cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cudaStream_t stream);
 
 } // namespace kvr

@@ -88,6 +88,15 @@ def test_long_context(kind):
     Batch(kind, [(1, 20011), (2, 9000)], HEADS[kind], seed=12).check()
 
 
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("kind,heads,lens", [("gqa", 32, [(1500, 5003)]), ("mla", 128, [(64, 5003)]),
+                                             ("gqa", 32, [(1, 9001)] * 40),
+                                             ("mla", 128, [(1, 6001)] * 40)])
+def test_long_runs_of_whole_tiles_before_a_partial_one(kind, heads, lens, quant):
+    """Every stage of the rings is reused many times within a block."""
+    Batch(kind, lens, heads, quant=quant, seed=19).check()
+
+
 @pytest.mark.parametrize("kind,quant", [("mla", False), ("gqa", False), ("gqa4", True)])
 def test_places_that_are_not_seen_may_hold_anything(kind, quant):
     """NaN beyond the cached tokens, in unused blocks, before the window."""
