@@ -31,6 +31,7 @@
 //
 // Every wait is bounded; a block whose wait runs out reports KV_ERR_TIMEOUT.
 #include <algorithm>
+#include <type_traits>
 
 #include <cudaTypedefs.h>
 
@@ -153,6 +154,27 @@ __device__ __forceinline__ void reg_dec()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// All but this thread's newest N groups of copies have landed.
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float lds4(uint32_t src)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(src) : "memory");
+    return v;
+}
+
 // 16-byte copy to shared memory; bytes = 0 writes zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes)
 {
@@ -209,6 +231,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r)
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : KV_R8(r, 0), KV_R8(r, 8)
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_pin16(uint32_t *r)
+{
+    asm volatile("" : KV_P8(r, 0), KV_P8(r, 8));
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -233,24 +268,25 @@ __device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t lead)
 
 constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 
-// kind::f16: D fp32, A and B bf16; B along K (0) or along N (1).
-template <int N, int BMAJOR>
+// kind::f16: D fp32, A and B bf16; each along K (0) or along M / N (1).
+template <int N, int BMAJOR, int AMAJOR = 0>
 __device__ __forceinline__ constexpr uint32_t mma_desc()
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)BMAJOR << 16) |
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)AMAJOR << 15) | ((uint32_t)BMAJOR << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 }
 
 // The MMA warp runs as one: every lane holds the same operands (they stay in
 // uniform registers) and the lane with `lead` set issues.
-template <int N>
+template <int N, int MAJOR = 0>
 __device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t acc,
-                                         uint32_t lead)
+                                         uint32_t lead, uint32_t b_high = kOperandHigh)
 {
     asm volatile("{\n.reg .pred p, q;\n.reg .b64 x, y;\nsetp.ne.b32 p, %4, 0;\n"
-                 "setp.ne.b32 q, %6, 0;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %5};\n"
+                 "setp.ne.b32 q, %6, 0;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %7};\n"
                  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d),
-                 "r"(a), "r"(b), "r"(mma_desc<N, 0>()), "r"(acc), "r"(kOperandHigh), "r"(lead)
+                 "r"(a), "r"(b), "r"(mma_desc<N, MAJOR, MAJOR>()), "r"(acc), "r"(kOperandHigh),
+                 "r"(lead), "r"(b_high)
                  : "memory");
 }
 
@@ -303,7 +339,17 @@ __device__ __forceinline__ uint32_t scale_mul(float scale)
     return (uint32_t)(247 + min(e, 7)) << 7 | (uint32_t)(127 + max(e - 7, 0)) << 23;
 }
 
-// Sixteen e4m3 values (one 16-byte piece) to two pieces of bf16.
+// A 16-byte piece needs convert_rare: it holds a NaN, or its scale is above 2^7.
+__device__ __forceinline__ uint32_t rare16(uint4 v, uint32_t mul)
+{
+    return e4m3_nan(v.x) | e4m3_nan(v.y) | e4m3_nan(v.z) | e4m3_nan(v.w) |
+           ((mul >> 16) ^ 0x3F80u);
+}
+
+// Sixteen e4m3 values (one 16-byte piece) to two pieces of bf16.  RARE: with the
+// second factor of the scale, and NaN.  The callers test a whole batch of pieces
+// first, so that the usual form is free of branches and its chains interleave.
+template <bool RARE>
 __device__ __forceinline__ void convert16(uint4 v, uint32_t mul, uint4 &lo, uint4 &hi)
 {
     const uint32_t m = __byte_perm(mul, 0, 0x1010);
@@ -314,8 +360,7 @@ __device__ __forceinline__ void convert16(uint4 v, uint32_t mul, uint4 &lo, uint
         r[2 * i] = e4m3_bf16(__byte_perm(w[i], 0, 0x1404), m);
         r[2 * i + 1] = e4m3_bf16(__byte_perm(w[i], 0, 0x3424), m);
     }
-    const uint32_t nan = e4m3_nan(v.x) | e4m3_nan(v.y) | e4m3_nan(v.z) | e4m3_nan(v.w);
-    if (nan | ((mul >> 16) ^ 0x3F80u)) { // rare: NaN, or a scale above 2^7
+    if constexpr (RARE) {
         const uint32_t m2 = __byte_perm(mul, 0, 0x3232);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -329,12 +374,17 @@ __device__ __forceinline__ void convert16(uint4 v, uint32_t mul, uint4 &lo, uint
     hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// Zeroes the values of a bf16 pair that are not finite; true if any was.
-__device__ __forceinline__ bool drop_nonfinite(uint32_t &w)
+// Sets bit 15 or 31 when the low or the high bf16 of a pair is not finite.
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w)
 {
-    const bool lo = (w & 0x7F80u) == 0x7F80u, hi = (w & 0x7F800000u) == 0x7F800000u;
-    w &= (lo ? 0xFFFF0000u : ~0u) & (hi ? 0x0000FFFFu : ~0u);
-    return lo || hi;
+    return (w & 0x7F807F80u) + 0x00800080u;
+}
+
+// The pair with values that are not finite zeroed.
+__device__ __forceinline__ uint32_t finite2(uint32_t w)
+{
+    const uint32_t n = nonfinite2(w);
+    return w & ((n & 0x8000u) ? 0xFFFF0000u : ~0u) & ((n & 0x80000000u) ? 0xFFFFu : ~0u);
 }
 
 // ---------------------------------------------------------------------------
@@ -350,9 +400,13 @@ struct HeadGeo {
     static constexpr int DV = 128;
     static constexpr int LOAD_WG = NT == 2 ? 1 : 2; // load warpgroups
     static constexpr int STAGE = 2 * 128 * 128;    // bytes of a K or V tile
-    static constexpr int STAGES = NT == 2 ? 5 : 6;
+    // e4m3: RAW tiles of K or V as they are stored, and their scales, wait in
+    // shared memory to be converted
+    static constexpr int RAW = !QUANT ? 0 : NT == 2 ? 3 : 5;
+    static constexpr int STAGES = QUANT ? (NT == 2 ? 3 : 3) : NT == 2 ? 5 : 6;
     static constexpr int BARS = 2 * STAGES;
-    static constexpr int RING = STAGES * STAGE;
+    static constexpr int RAW_AT = STAGES * STAGE, RAW_STAGE = STAGE / 2 + 512;
+    static constexpr int RING = RAW_AT + RAW * RAW_STAGE;
     static constexpr int REG_SOFTMAX = NT == 2 ? 168 : 200;
     static constexpr int REG_LOAD = 120;
     // columns of tensor memory: S (and P over it) per tile or per buffer, O
@@ -540,19 +594,31 @@ __device__ __forceinline__ bool find_tile(const AttnParams &p, int tile, int lan
     return found;
 }
 
-// Slot of key k of the block's sequence, or -1: not seen by any row, or (bad)
-// its block lies outside the pool.
-__device__ __forceinline__ int64_t key_slot(const AttnParams &p, const Work &w, int k, bool &bad)
+__device__ __forceinline__ bool key_seen(const Work &w, int k)
 {
-    if (k >= w.hi || (k < w.lo && k >= w.sk))
-        return -1;
+    return k < w.hi && (k >= w.lo || k < w.sk);
+}
+
+// Block id of key k of the block's sequence (anything for keys that no row sees).
+// The load roles ask for it well before they use it: the first use waits.
+__device__ __forceinline__ int32_t key_block(const AttnParams &p, const Work &w, int k)
+{
     const int b = (int)((uint32_t)k / (uint32_t)p.block);
-    const int32_t blk = __ldg(p.block_tables + (int64_t)w.seq * p.max_blocks + b);
+    return key_seen(w, k) ? __ldg(p.block_tables + (int64_t)w.seq * p.max_blocks + b) : 0;
+}
+
+// Slot of key k in block `blk`, or -1: not seen by any row, or (bad) the block
+// lies outside the pool.
+__device__ __forceinline__ int64_t key_slot(const AttnParams &p, const Work &w, int k, int32_t blk,
+                                            bool &bad)
+{
+    if (!key_seen(w, k))
+        return -1;
     if (blk < 0 || blk >= p.num_blocks) {
         bad = true;
         return -1;
     }
-    return (int64_t)blk * p.block + (k - b * p.block);
+    return (int64_t)blk * p.block + (int)((uint32_t)k % (uint32_t)p.block);
 }
 
 // ---------------------------------------------------------------------------
@@ -585,15 +651,6 @@ __device__ __forceinline__ bool tile_whole(const Work &w, int kt)
 {
     const int k0 = kt * KT;
     return (k0 >= w.lo && k0 + KT <= w.hi) || k0 + KT <= w.sk;
-}
-
-// Row of the pool where box `lane` of tile kt starts; past the pool (zeros) for a
-// bad block id.
-template <int KT>
-__device__ __forceinline__ int box_row(const AttnParams &p, const Work &w, int kt, int lane, bool &bad)
-{
-    const int64_t s = lane * p.box_rows < KT ? key_slot(p, w, kt * KT + lane * p.box_rows, bad) : 0;
-    return (int)(s < 0 ? p.num_blocks * p.block : s);
 }
 
 // Box copies that may be in flight, a bit per barrier.  A block waits for them
@@ -633,22 +690,22 @@ __device__ __forceinline__ void load_heads_bf16(const AttnParams &p, const Work 
     const int base = warp * ROWS;
     const int c = lane & 15, half = lane >> 4;
     auto whole = [&](int v) { return p.box_rows > 0 && tile_whole<G::KT>(w, real_tile(w, v)); };
-    auto rows_at = [&](int v) -> int64_t {
-        if (v >= w.end)
-            return -1;
-        const int kt = real_tile(w, v);
-        if (whole(v))
-            return warp == 0 ? box_row<G::KT>(p, w, kt, lane, bad) : 0;
-        return key_slot(p, w, kt * G::KT + base + (lane & (ROWS - 1)), bad);
+    // the key whose slot this lane looks up: the first of its box, or its row's
+    auto key_at = [&](int v) {
+        const int k0 = real_tile(w, v) * G::KT;
+        return whole(v) ? k0 + min(lane * p.box_rows, G::KT - 1) : k0 + base + (lane & (ROWS - 1));
     };
-    int64_t next = rows_at(w.beg);
+    int32_t next = w.beg < w.end ? key_block(p, w, key_at(w.beg)) : 0;
     Flights fly;
     int stage = 0, phase = 1;
     bool ok = true;
     for (int v = w.beg; ok && v < w.end; ++v) {
-        const int64_t slot = next;
-        next = rows_at(v + 1); // the next tile's block ids, in flight with this tile
+        const int64_t slot = key_slot(p, w, key_at(v), next, bad);
+        if (v + 1 < w.end)
+            next = key_block(p, w, key_at(v + 1));
         const bool boxes = whole(v);
+        // a bad block reads past the pool: zeros
+        const int row0 = (int)(slot < 0 ? p.num_blocks * p.block : slot);
 #pragma unroll
         for (int part = 0; part < 2; ++part) { // K, then V
             const uint32_t full = bars + stage * 8, dst = ring + stage * G::STAGE;
@@ -664,8 +721,8 @@ __device__ __forceinline__ void load_heads_bf16(const AttnParams &p, const Work 
                     if (lane * p.box_rows < G::KT) {
                         const CUtensorMap *map = part == 0 ? &p.rot_map : &p.copy_map;
                         const uint32_t at = dst + lane * p.box_rows * 128;
-                        copy_box(at, map, w.head * 128, (int)slot, full);
-                        copy_box(at + 16384, map, w.head * 128 + 64, (int)slot, full);
+                        copy_box(at, map, w.head * 128, row0, full);
+                        copy_box(at + 16384, map, w.head * 128 + 64, row0, full);
                     }
                 }
             } else {
@@ -692,77 +749,112 @@ __device__ __forceinline__ void load_heads_bf16(const AttnParams &p, const Work 
         fly.land(bars);
 }
 
-// Head rows in e4m3: the next tiles (one, or two where a thread holds less of
-// each) wait in registers while the one before is converted into the ring.  8
-// lanes hold the 128 bytes of a row.
+// Head rows in e4m3: copied as they are stored, RAW tiles ahead, then converted
+// into the ring.  A thread converts the pieces that it copied itself, so a
+// warp waits for nobody else's copies.  8 lanes hold the 128 bytes of a row.
 template <class G>
 __device__ __forceinline__ void load_heads_e4m3(const AttnParams &p, const Work &w, uint32_t ring,
                                                 uint32_t bars, int warp, int lane,
                                                 volatile int *abort, bool &bad)
 {
-    constexpr int WARPS = G::LOAD_WG * 4, ROWS = G::KT / WARPS, IT = ROWS / 4, AHEAD = 8 / IT;
-    const int base = warp * ROWS;
+    constexpr int WARPS = G::LOAD_WG * 4, ROWS = G::KT / WARPS, IT = ROWS / 4;
+    const int base = warp * ROWS, own = lane & (ROWS - 1);
     const int c = lane & 7, sub = lane >> 3;
-    uint4 raw[AHEAD][2][IT];
-    uint32_t mul[AHEAD][2];
-    auto slot_at = [&](int v) {
-        return v < w.end ? key_slot(p, w, real_tile(w, v) * G::KT + base + (lane & (ROWS - 1)), bad)
-                         : (int64_t)-1;
-    };
-    auto fetch = [&](uint4 (&to)[IT], uint32_t &m, int part, int64_t slot) {
-        const char *src = (part == 0 ? p.rot : p.copy) + w.head * 128 + c * 16;
-        const int64_t ss = part == 0 ? p.rot_ss : p.copy_ss;
-        const float *sc = part == 0 ? p.rs + slot * p.rs_ss : p.cs + slot * p.cs_ss;
+    const uint32_t raw = ring + G::RAW_AT;
+    const int items = 2 * (w.end - w.beg); // K, V of each tile
+    auto key_at = [&](int v) { return real_tile(w, v) * G::KT + base + own; };
+    auto block_at = [&](int v) { return v < w.end ? key_block(p, w, key_at(v)) : 0; };
+    const char *const src[2] = {p.rot + w.head * 128 + c * 16, p.copy + w.head * 128 + c * 16};
+    const float *const sc[2] = {p.rs + w.head, p.cs + w.head};
+    int slot = -1; // of this lane's row in the tile last asked for
+    int ask_v = w.beg, ask_stage = 0;
+    int32_t blk = block_at(w.beg);
+    // asks for item n (K of a tile before its V)
+    auto ask = [&](int n) {
+        if (n < items) {
+            if (!(n & 1)) {
+                slot = (int)key_slot(p, w, key_at(ask_v), blk, bad);
+                blk = block_at(++ask_v);
+            }
+            const bool v = n & 1;
+            const char *const from = v ? src[1] : src[0];
+            const int64_t ss = v ? p.copy_ss : p.rot_ss;
+            const uint32_t to = raw + ask_stage * G::RAW_STAGE;
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, i * 4 + sub);
-            to[i] = s < 0 ? make_uint4(0, 0, 0, 0)
-                          : ld_stream(src + s * ss);
+            for (int i = 0; i < IT; ++i) {
+                const int s = __shfl_sync(0xFFFFFFFFu, slot, i * 4 + sub);
+                copy16(to + ((warp * IT + i) * 32 + lane) * 16, from + (s < 0 ? 0 : s * ss),
+                       s < 0 ? 0u : 16u);
+            }
+            if (lane < ROWS)
+                copy4(to + G::STAGE / 2 + (base + own) * 4,
+                      (v ? sc[1] : sc[0]) + (slot < 0 ? 0 : slot * (v ? p.cs_ss : p.rs_ss)));
+            if (++ask_stage == G::RAW)
+                ask_stage = 0;
         }
-        m = scale_mul(slot < 0 ? 1.0f : __ldg(sc + w.head));
+        copy_commit();
     };
-#pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
-        const int64_t slot = slot_at(w.beg + a);
-        fetch(raw[a][0], mul[a][0], 0, slot);
-        fetch(raw[a][1], mul[a][1], 1, slot);
-    }
-    int64_t next = slot_at(w.beg + AHEAD);
+    for (int n = 0; n < G::RAW; ++n)
+        ask(n);
     // a lane's two pieces of a row: the odd one first in the upper panel, so that
     // the eight lanes of a row meet eight different 16-byte columns
     const int first = c >> 2;
     const int c0 = (2 * c + first) & 7, c1 = (2 * c + 1 - first) & 7;
-    int stage = 0, phase = 1;
-    for (int v0 = w.beg; v0 < w.end; v0 += AHEAD) {
+    int stage = 0, phase = 1, from_stage = 0;
+#pragma unroll 1
+    for (int n = 0; n < items; ++n) {
+        copy_wait<G::RAW - 1>();
+        __syncwarp(); // the scales of the warp's rows came through other lanes
+        if (!bar_wait(bars + (G::STAGES + stage) * 8, phase, abort, p.wait_limit_ns))
+            return;
+        const uint32_t from = raw + from_stage * G::RAW_STAGE;
+        const uint32_t dst = ring + stage * G::STAGE + (first << 14) + base * 128;
+        constexpr int B = 4; // pieces at a time
+#pragma unroll 1
+        for (int i0 = 0; i0 < IT; i0 += B) {
+            uint4 x[B];
+            uint32_t mul[B], rare = 0;
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            const int v = v0 + a;
-            if (v >= w.end)
-                break;
-            const int64_t slot = next;
-            next = slot_at(v + AHEAD + 1);
+            for (int i = 0; i < B; ++i) {
+                x[i] = lds16(from + ((warp * IT + i0 + i) * 32 + lane) * 16);
+                mul[i] = scale_mul(lds4(from + G::STAGE / 2 + (base + (i0 + i) * 4 + sub) * 4));
+            }
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                if (!bar_wait(bars + (G::STAGES + stage) * 8, phase, abort, p.wait_limit_ns))
-                    return;
-                const uint32_t dst = ring + stage * G::STAGE + (first << 14) + base * 128;
+            for (int i = 0; i < B; ++i)
+                rare |= rare16(x[i], mul[i]);
+            auto store = [&](int r, const uint4 &lo, const uint4 &hi) {
+                sts16(dst + r * 128 + ((c0 ^ (r & 7)) << 4), first ? hi : lo);
+                sts16(dst + r * 128 + ((c1 ^ (r & 7)) << 4), first ? lo : hi);
+            };
+            if (!rare) {
 #pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    const int r = i * 4 + sub;
-                    const uint32_t m = __shfl_sync(0xFFFFFFFFu, mul[a][part], r);
-                    uint4 x, y;
-                    convert16(raw[a][part][i], m, x, y);
-                    sts16(dst + r * 128 + ((c0 ^ (r & 7)) << 4), first ? y : x);
-                    sts16(dst + r * 128 + ((c1 ^ (r & 7)) << 4), first ? x : y);
+                for (int i = 0; i < B; ++i) {
+                    uint4 lo, hi;
+                    convert16<false>(x[i], mul[i], lo, hi);
+                    store((i0 + i) * 4 + sub, lo, hi);
                 }
-                async_fence();
-                bar_signal(bars + stage * 8);
-                fetch(raw[a][part], mul[a][part], part, slot);
-                if (++stage == G::STAGES) {
-                    stage = 0;
-                    phase ^= 1;
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < B; ++i) {
+                    uint4 lo, hi;
+                    const uint32_t at = from + ((warp * IT + i0 + i) * 32 + lane) * 16;
+                    convert16<true>(
+                        lds16(at),
+                        scale_mul(lds4(from + G::STAGE / 2 + (base + (i0 + i) * 4 + sub) * 4)), lo,
+                        hi);
+                    store((i0 + i) * 4 + sub, lo, hi);
                 }
             }
+        }
+        async_fence();
+        bar_signal(bars + stage * 8);
+        __syncwarp(); // every lane has read the scales before they are replaced
+        ask(n + G::RAW);
+        if (++from_stage == G::RAW)
+            from_stage = 0;
+        if (++stage == G::STAGES) {
+            stage = 0;
+            phase ^= 1;
         }
     }
 }
@@ -777,21 +869,19 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
 {
     const int base = warp * 8, c = lane & 7, sub = lane >> 3;
     auto whole = [&](int v) { return p.box_rows > 0 && tile_whole<G::KT>(w, real_tile(w, v)); };
-    auto rows_at = [&](int v) -> int64_t {
-        if (v >= w.end)
-            return -1;
-        const int kt = real_tile(w, v);
-        if (whole(v))
-            return warp == 0 ? box_row<G::KT>(p, w, kt, lane, bad) : 0;
-        return key_slot(p, w, kt * G::KT + base + c, bad);
+    auto key_at = [&](int v) {
+        const int k0 = real_tile(w, v) * G::KT;
+        return whole(v) ? k0 + min(lane * p.box_rows, G::KT - 1) : k0 + base + c;
     };
-    int64_t next = rows_at(w.beg);
+    int32_t next = w.beg < w.end ? key_block(p, w, key_at(w.beg)) : 0;
     Flights fly;
     bool ok = true;
     for (int v = w.beg; ok && v < w.end; ++v) {
-        const int64_t slot = next;
-        next = rows_at(v + 1);
+        const int64_t slot = key_slot(p, w, key_at(v), next, bad);
+        if (v + 1 < w.end)
+            next = key_block(p, w, key_at(v + 1));
         const bool boxes = whole(v);
+        const int row0 = (int)(slot < 0 ? p.num_blocks * p.block : slot);
         const int ord = v - w.beg, stage = ord & 1, phase = ((ord >> 1) & 1) ^ 1;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
@@ -810,10 +900,9 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
                         const uint32_t at = dst + lane * p.box_rows * 128;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            copy_box(at + i * G::PANEL, &p.copy_map, half * 256 + i * 64, (int)slot,
-                                     full);
+                            copy_box(at + i * G::PANEL, &p.copy_map, half * 256 + i * 64, row0, full);
                         if (part == 0)
-                            copy_box(at + 4 * G::PANEL, &p.rot_map, 0, (int)slot, full);
+                            copy_box(at + 4 * G::PANEL, &p.rot_map, 0, row0, full);
                     }
                 }
             } else {
@@ -845,9 +934,11 @@ __device__ __forceinline__ void load_mla_e4m3(const AttnParams &p, const Work &w
 {
     const int base = warp * 8, c = lane & 7, sub = lane >> 3;
     uint4 lat[2][2][2], pe[2]; // [part][group of 128][row]
-    uint32_t mul[2][2];
-    auto slot_at = [&](int v) {
-        return v < w.end ? key_slot(p, w, real_tile(w, v) * G::KT + base + c, bad) : (int64_t)-1;
+    float scale[2][2];
+    auto key_at = [&](int v) { return real_tile(w, v) * G::KT + base + c; };
+    auto block_at = [&](int v) { return v < w.end ? key_block(p, w, key_at(v)) : 0; };
+    auto slot_at = [&](int v, int32_t blk) {
+        return v < w.end ? key_slot(p, w, key_at(v), blk, bad) : (int64_t)-1;
     };
     auto fetch = [&](int part, int64_t slot) {
         const int half = part == 0 ? 1 - w.head : w.head;
@@ -865,39 +956,53 @@ __device__ __forceinline__ void load_mla_e4m3(const AttnParams &p, const Work &w
         }
 #pragma unroll
         for (int g = 0; g < 2; ++g) // lane c of each eight: the row's scale
-            mul[part][g] =
-                scale_mul(slot < 0 ? 1.0f : __ldg(p.cs + slot * p.cs_ss + half * 2 + g));
+            scale[part][g] = slot < 0 ? 1.0f : __ldg(p.cs + slot * p.cs_ss + half * 2 + g);
     };
     const int first = c >> 2;
     const int c0 = (2 * c + first) & 7, c1 = (2 * c + 1 - first) & 7;
-    int64_t next = slot_at(w.beg);
-    fetch(0, next);
-    fetch(1, next);
-    next = slot_at(w.beg + 1);
+    const int64_t slot0 = slot_at(w.beg, block_at(w.beg));
+    fetch(0, slot0);
+    fetch(1, slot0);
+    int32_t next = block_at(w.beg + 1);
     for (int v = w.beg; v < w.end; ++v) {
-        const int64_t slot = next;
-        next = slot_at(v + 2);
+        const int64_t slot = slot_at(v + 1, next);
+        next = block_at(v + 2);
         const int ord = v - w.beg, stage = ord & 1, phase = ((ord >> 1) & 1) ^ 1;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
             const uint32_t full = bars + (part * 2 + stage) * 8, dst = G::part(ring, part, stage);
             if (!bar_wait(full + 4 * 8, phase, abort, p.wait_limit_ns))
                 return;
+            const uint32_t mul[2] = {scale_mul(scale[part][0]), scale_mul(scale[part][1])};
+            uint32_t m[2][2], rare = 0;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = i * 4 + sub;
-                const uint32_t at = dst + (base + r) * 128;
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    uint4 x, y;
-                    convert16(lat[part][g][i], __shfl_sync(0xFFFFFFFFu, mul[part][g], r), x, y);
-                    const uint32_t to = at + (g * 2 + first) * G::PANEL;
-                    sts16(to + ((c0 ^ (r & 7)) << 4), first ? y : x);
-                    sts16(to + ((c1 ^ (r & 7)) << 4), first ? x : y);
+                    m[i][g] = __shfl_sync(0xFFFFFFFFu, mul[g], i * 4 + sub);
+                    rare |= rare16(lat[part][g][i], m[i][g]);
                 }
-                if (part == 0)
-                    sts16(at + 4 * G::PANEL + ((c ^ (r & 7)) << 4), pe[i]);
-            }
+            auto store = [&](auto kind) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = i * 4 + sub;
+                    const uint32_t at = dst + (base + r) * 128;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        uint4 x, y;
+                        convert16<decltype(kind)::value>(lat[part][g][i], m[i][g], x, y);
+                        const uint32_t to = at + (g * 2 + first) * G::PANEL;
+                        sts16(to + ((c0 ^ (r & 7)) << 4), first ? y : x);
+                        sts16(to + ((c1 ^ (r & 7)) << 4), first ? x : y);
+                    }
+                    if (part == 0)
+                        sts16(at + 4 * G::PANEL + ((c ^ (r & 7)) << 4), pe[i]);
+                }
+            };
+            if (rare)
+                store(std::true_type{});
+            else
+                store(std::false_type{});
             async_fence();
             bar_signal(full);
             fetch(part, slot);
@@ -1078,6 +1183,12 @@ __device__ __forceinline__ bool run_mma_one(const AttnParams &p, const Work &w, 
 // Softmax role (a thread per row)
 // ---------------------------------------------------------------------------
 
+// The lowest n of 32 bits (none below 0, all above 31).
+__device__ __forceinline__ uint32_t below(int n)
+{
+    return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
 struct RowState {
     float top = -INFINITY; // maximum that the weights and O are taken against
     float sum = 0.0f;
@@ -1157,12 +1268,13 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
             tmem_pin32(s + i);
         const bool full = tile_full<KT>(p, m, kt);
         if (!full) {
-            const int k0 = kt * KT;
 #pragma unroll
-            for (int i = 0; i < KT; ++i) {
-                const int k = k0 + i;
-                const bool see = k < hi && (k >= lo || k < sk);
-                s[i] = see ? s[i] : 0xFF800000u;
+            for (int i = 0; i < KT; i += 32) { // a bit per key that is seen
+                const int k0 = kt * KT + i;
+                const uint32_t see = below(hi - k0) & (~below(lo - k0) | below(sk - k0));
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    s[i + j] = (see >> j) & 1u ? s[i + j] : 0xFF800000u;
             }
         }
         float t4[4]; // four chains: the maximum's latency, not its count, is what costs
@@ -1241,28 +1353,35 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
                 vbase = MlaGeo<G::QUANT>::part(ring, 1, ord & 1);
                 pieces = MlaGeo<G::QUANT>::OWN / 16;
             } else {
-                constexpr int ST = G::BARS / 2;
+                constexpr int ST = G::BARS / 2, BYTES = 2 * KT * 128;
                 const int item = 2 * ord + 1;
                 if (!bar_wait(bars + (kBarRing + item % ST) * 8, (item / ST) & 1, abort,
                               p.wait_limit_ns))
                     return false;
-                vbase = ring + (item % ST) * (G::RING / ST);
-                pieces = G::RING / ST / 16;
+                vbase = ring + (item % ST) * BYTES;
+                pieces = BYTES / 16;
             }
-            bool any = false;
-            for (int i = warp * 32 + lane; i < pieces; i += warps * 32) {
-                uint4 x = lds16(vbase + i * 16);
-                const bool a = drop_nonfinite(x.x), b = drop_nonfinite(x.y);
-                const bool d = drop_nonfinite(x.z), e = drop_nonfinite(x.w);
-                if (a || b || d || e) {
-                    *dirty = 1;
-                    __threadfence_block();
-                    sts16(vbase + i * 16, x);
-                    any = true;
+            uint32_t bad = 0;
+            for (int i = warp * 32 + lane; i < pieces; i += warps * 32 * 4) {
+                uint4 x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[j] = lds16(vbase + min(i + j * warps * 32, pieces - 1) * 16);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    bad |= nonfinite2(x[j].x) | nonfinite2(x[j].y) | nonfinite2(x[j].z) |
+                           nonfinite2(x[j].w);
+            }
+            if (bad & 0x80008000u) {
+                *dirty = 1;
+                __threadfence_block();
+                for (int i = warp * 32 + lane; i < pieces; i += warps * 32) {
+                    const uint4 x = lds16(vbase + i * 16);
+                    sts16(vbase + i * 16, make_uint4(finite2(x.x), finite2(x.y), finite2(x.z),
+                                                     finite2(x.w)));
                 }
-            }
-            if (any)
                 async_fence();
+            }
         }
         mma_fence_before();
         bar_signal(bars + (kBarP + buf) * 8);
@@ -1303,7 +1422,7 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
                     if (!valid || !(k < hi && (k >= lo || k < sk)))
                         continue;
                     bool bad = false;
-                    const int64_t s = key_slot(p, w, k, bad);
+                    const int64_t s = key_slot(p, w, k, key_block(p, w, k), bad);
                     if (s < 0)
                         continue;
 #pragma unroll
@@ -1475,6 +1594,352 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
         write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, gridDim.x);
 }
 
+// ---------------------------------------------------------------------------
+// One new token per sequence, up to 16 query heads to a key head
+// ---------------------------------------------------------------------------
+//
+// With so few rows the products are turned round: keys are the M of the MMA,
+//     Sᵀ (128 keys x 16 rows) = K Qᵀ,   Oᵀ (128 x 16) += Vᵀ Pᵀ,
+// so a thread has one key and all rows: R exponentials a tile instead of 128, and
+// its key's mask is one comparison.  The rows' maxima are references that all
+// threads hold; a vote finds a score that passes its reference by more than
+// 2^8, and only then are the true maxima formed across the block and O rescaled.
+// Sums stay per key until the end.  An MMA with N = 16 takes 40 clocks (the
+// operand A is read at 128 bytes a clock), 640 a tile, where the tile's rows take
+// 2700 (bf16) or 1400 (e4m3) from HBM: the kernel is bound by memory.  Two
+// blocks share an SM, so that one's start and end lie under the other's loads.
+template <bool QUANT_>
+struct FewGeo {
+    static constexpr bool MLA = false, QUANT = QUANT_;
+    static constexpr int NT = 1, KT = 128;
+    static constexpr int DV = 128;
+    static constexpr int LOAD_WG = 1;
+    static constexpr int STAGE = 2 * 128 * 128, STAGES = QUANT ? 2 : 3;
+    static constexpr int RAW = QUANT ? 2 : 0;
+    static constexpr int RAW_AT = STAGES * STAGE, RAW_STAGE = STAGE / 2 + 512;
+    static constexpr int RING = RAW_AT + RAW * RAW_STAGE;
+    static constexpr int Q_BYTES = 2 * 16 * 128, P_BYTES = 128 * 32;
+    static constexpr int P_AT = RING, Q_AT = P_AT + 2 * P_BYTES, BAR_AT = Q_AT + Q_BYTES;
+    static constexpr int BYTES = BAR_AT + (kBarRing + 2 * STAGES) * 8 + 1024;
+    static constexpr int COLS = 64; // tensor memory: S at 0 and 16, O at 32
+};
+
+constexpr int kFewThreads = 288; // 4 softmax warps, 4 load warps, 1 MMA warp
+constexpr int kFewRows = 16;
+
+// Byte of (key, first of 8 rows) of Pᵀ: core matrices of 8 keys x 8 rows (16 bytes
+// a key), the second 8 rows 128 bytes on, the next 8 keys 256 bytes on.
+__device__ __forceinline__ uint32_t few_weight(int key) { return (key >> 3) * 256 + (key & 7) * 16; }
+
+// A vote over the four softmax warps.  Each of them comes to every vote, also
+// when its own wait ran out: they go on or give up together.
+__device__ __forceinline__ bool softmax_any(bool x)
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 q, %1, 0;\n"
+                 "barrier.cta.red.or.pred p, 1, 128, q;\nselp.b32 %0, 1, 0, p;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)x)
+                 : "memory");
+    return r != 0;
+}
+
+template <class G, int R>
+__device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, uint32_t tmem,
+                                            uint32_t smem, uint32_t bars, int tid,
+                                            volatile int *abort, float (*red)[kFewRows])
+{
+    const int warp = tid >> 5, lane = tid & 31;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const float c = p.scale * 1.4426950408889634f;
+    float ref[R], sum[R]; // references in units of log2
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        ref[r] = -INFINITY;
+        sum[r] = 0.0f;
+    }
+    for (int v = w.beg; v < w.end; ++v) {
+        const int ord = v - w.beg, i = ord & 1;
+        const int k = real_tile(w, v) * G::KT + tid;
+        const bool see = k < w.hi && (k >= w.lo || k < w.sk);
+        bool ok = bar_wait(bars + (kBarS + i) * 8, (ord >> 1) & 1, abort, p.wait_limit_ns);
+        mma_fence_after();
+        uint32_t raw[16];
+        tmem_ld16(tmem + i * 16 + lanes, raw);
+        tmem_ld_wait();
+        tmem_pin16(raw);
+        float x[R];
+        bool grew = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            x[r] = see ? __uint_as_float(raw[r]) * c : -INFINITY;
+            grew |= x[r] - ref[r] > kLazy;
+        }
+        if (softmax_any(grew || !ok)) {
+            if (softmax_any(!ok))
+                return false;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float m = x[r];
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1)
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+                if (lane == 0)
+                    red[warp][r] = m;
+            }
+            bar_wait_all(1, 128);
+            float f[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float m = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
+                const bool up = m - ref[r] > kLazy;
+                f[r] = up ? exp2_fast(ref[r] - m) : 1.0f;
+                ref[r] = up ? m : ref[r];
+                sum[r] *= f[r];
+            }
+            if (ord > 0) { // a lane of Oᵀ is a value column, its columns are the rows
+                ok = bar_wait(bars + kBarO * 8, (ord - 1) & 1, abort, p.wait_limit_ns);
+                if (softmax_any(!ok))
+                    return false;
+                mma_fence_after();
+                uint32_t o[16];
+                tmem_ld16(tmem + 32 + lanes, o);
+                tmem_ld_wait();
+                tmem_pin16(o);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
+                tmem_st16(tmem + 32 + lanes, o);
+                tmem_st_wait();
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            x[r] = exp2_fast(x[r] - (ref[r] == -INFINITY ? 0.0f : ref[r]));
+            sum[r] += x[r];
+        }
+        const uint32_t at = smem + G::P_AT + i * G::P_BYTES + few_weight(tid);
+#pragma unroll
+        for (int r = 0; r < R; r += 8)
+            sts16(at + r * 16, make_uint4(pack_bf16(x[r], x[r + 1]), pack_bf16(x[r + 2], x[r + 3]),
+                                          pack_bf16(x[r + 4], x[r + 5]),
+                                          pack_bf16(x[r + 6], x[r + 7])));
+        async_fence();
+        mma_fence_before();
+        bar_signal(bars + (kBarP + i) * 8);
+    }
+    if (softmax_any(!bar_wait(bars + kBarDone * 8, 0, abort, p.wait_limit_ns)))
+        return false;
+    mma_fence_after();
+    // the sums of the block's keys
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float m = sum[r];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            m += __shfl_xor_sync(0xFFFFFFFFu, m, d);
+        if (lane == 0)
+            red[warp][r] = m;
+    }
+    bar_wait_all(1, 128);
+    uint32_t o[16];
+    tmem_ld16(tmem + 32 + lanes, o);
+    tmem_ld_wait();
+    tmem_pin16(o);
+    const bool parts = w.splits > 1;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (r >= p.group)
+            break;
+        const float l = (red[0][r] + red[1][r]) + (red[2][r] + red[3][r]);
+        const float y = l == 0.0f ? 0.0f : __uint_as_float(o[r]) / l;
+        const int h = w.head * p.group + r;
+        const int64_t at = w.q0 * p.heads + h;
+        if (parts)
+            p.part[(w.split * p.total_q * p.heads + at) * G::DV + tid] = y;
+        else
+            *reinterpret_cast<uint16_t *>(p.out + w.q0 * p.o_ts + h * p.o_hs + tid * 2) =
+                (uint16_t)pack_bf16(y, y);
+        if (tid == 0) {
+            const float lse = l == 0.0f ? -INFINITY : ref[r] * 0.6931471805599453f + logf(l);
+            if (parts)
+                p.part_lse[w.split * p.total_q * p.heads + at] = lse;
+            else if (p.lse)
+                p.lse[at] = lse;
+        }
+    }
+    return true;
+}
+
+template <class G>
+__device__ __forceinline__ bool few_mma(const AttnParams &p, const Work &w, uint32_t tmem,
+                                        uint32_t smem, uint32_t bars, uint32_t lead,
+                                        volatile int *abort)
+{
+    const uint32_t full = bars + kBarRing * 8, empty = full + G::STAGES * 8;
+    const uint32_t q = operand(smem + G::Q_AT, 16);
+    // Pᵀ: no swizzle; 256 bytes to the next 8 keys, 128 to the next 8 rows
+    constexpr uint32_t kWeightHigh = (128u >> 4) | (1u << 14);
+    int stage = 0, phase = 0, vstage = 0;
+    auto next = [&] {
+        if (++stage == G::STAGES) {
+            stage = 0;
+            phase ^= 1;
+        }
+    };
+    for (int v = w.beg; v <= w.end; ++v) {
+        const int ord = v - w.beg, i = ord & 1;
+        const bool more = v < w.end;
+        if (more) {
+            if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
+                return false;
+            async_fence();
+            const uint32_t k = operand(smem + stage * G::STAGE, 16);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                mma_smem<kFewRows>(tmem + i * 16, k + (j >> 2) * (16384 >> 4) + (j & 3) * 2,
+                                   q + (j >> 2) * (2048 >> 4) + (j & 3) * 2, j > 0, lead);
+            bar_signal_mma(bars + (kBarS + i) * 8, lead);
+            bar_signal_mma(empty + stage * 8, lead);
+            next();
+        }
+        if (ord > 0) {
+            const int b = 1 - i;
+            if (!bar_wait(bars + (kBarP + b) * 8, ((ord - 1) >> 1) & 1, abort, p.wait_limit_ns))
+                return false;
+            mma_fence_after();
+            const uint32_t a = operand(smem + vstage * G::STAGE, 16384);
+            const uint32_t pt = operand(smem + G::P_AT + b * G::P_BYTES, 256);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                mma_smem<kFewRows, 1>(tmem + 32, a + j * (2048 >> 4), pt + j * (512 >> 4),
+                                      ord > 1 || j > 0, lead, kWeightHigh);
+            bar_signal_mma(empty + vstage * 8, lead);
+            bar_signal_mma(bars + kBarO * 8, lead);
+        }
+        if (more) {
+            vstage = stage;
+            if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
+                return false;
+            async_fence();
+            next();
+        }
+    }
+    bar_signal_mma(bars + kBarDone * 8, lead);
+    return true;
+}
+
+template <class G, int R>
+__global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
+    const __grid_constant__ AttnParams p)
+{
+    extern __shared__ unsigned char raw_smem[];
+    __shared__ uint32_t s_tmem, s_status;
+    __shared__ volatile int s_abort;
+    __shared__ float s_red[4][kFewRows];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const uint32_t bars = smem + G::BAR_AT;
+
+    const int heads = p.heads / p.group;
+    Work w;
+    w.head = (int)(blockIdx.x % heads);
+    w.split = (int)(blockIdx.x / heads % p.max_splits);
+    w.seq = (int)(blockIdx.x / heads / p.max_splits);
+    w.row0 = 0;
+    bool bad = !seq_queries(p, w.seq, w.q0, w.n);
+    bool go = w.n > 0;
+    if (go && !seq_keys(p, w.seq, w.len)) {
+        bad = true;
+        go = false;
+    }
+    if (go) {
+        const int nv = key_tiles<G::KT, 1>(p, w);
+        w.splits = max(1, (nv + p.split_tiles - 1) / p.split_tiles);
+        w.beg = w.split * p.split_tiles;
+        w.end = min(nv, w.beg + p.split_tiles);
+        go = w.split < w.splits;
+    }
+    if (!go) {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if (tid == 0)
+            write_block_status(p.header, bad ? kStatusOutOfRange : kStatusOk, blockIdx.x,
+                               gridDim.x);
+        return;
+    }
+    if (tid == 0) {
+        s_status = kStatusOk;
+        s_abort = 0;
+        bar_init(bars + kBarQ * 8, 128);
+        bar_init(bars + kBarDone * 8, 1);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(bars + (kBarS + i) * 8, 1);
+            bar_init(bars + (kBarP + i) * 8, 128);
+            bar_init(bars + (kBarO + i) * 8, 1); // the second: drain
+        }
+        for (int i = 0; i < G::STAGES; ++i) {
+            bar_init(bars + (kBarRing + i) * 8, 128);
+            bar_init(bars + (kBarRing + G::STAGES + i) * 8, 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&s_tmem)),
+                     "r"((uint32_t)G::COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    mma_fence_before();
+    __syncthreads();
+    mma_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t tmem = s_tmem;
+
+    if (warp < 4) {
+        few_softmax<G, R>(p, w, tmem, smem, bars, tid, &s_abort, s_red);
+    } else if (warp < 8) {
+        const int lt = tid - 128;
+        for (int i = lt; i < kFewRows * 16; i += 128) { // the queries; rows past the group are 0
+            const int r = i >> 4, c = i & 15;
+            const bool ok = r < p.group;
+            const char *src =
+                p.q + w.q0 * p.q_ts + (int64_t)(w.head * p.group + (ok ? r : 0)) * p.q_hs + c * 16;
+            copy16(smem + G::Q_AT + (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4), src,
+                   ok ? 16u : 0u);
+        }
+        bar_signal_copies(bars + kBarQ * 8);
+        bool out = false;
+        if constexpr (G::QUANT)
+            load_heads_e4m3<G>(p, w, smem, bars + kBarRing * 8, warp - 4, lane, &s_abort, out);
+        else
+            load_heads_bf16<G>(p, w, smem, bars + kBarRing * 8, warp - 4, lane, &s_abort, out);
+        if (out)
+            s_status = kStatusOutOfRange;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        const uint32_t lead = elect_lane();
+        bool ok = bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
+        if (ok) {
+            async_fence();
+            ok = few_mma<G>(p, w, tmem, smem, bars, lead, &s_abort);
+        }
+        if (!ok) { // let what was issued finish before tensor memory goes
+            int none = 0;
+            bar_signal_mma(bars + (kBarO + 1) * 8, lead);
+            bar_wait(bars + (kBarO + 1) * 8, 0, &none, 1000000000ll);
+        }
+    }
+    mma_fence_before();
+    __syncthreads();
+    mma_fence_after();
+    if (warp == 8)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"((uint32_t)G::COLS));
+    if (tid == 0)
+        write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, gridDim.x);
+}
+
 // Joins the parts of rows whose keys were split: a warp per (token, head).
 //   lse = log Σ exp(lse_s),  out = Σ exp(lse_s - lse) out_s
 template <class G>
@@ -1563,40 +2028,30 @@ bool encode_map(CUtensorMap *map, const char *base, int64_t row_bytes, int64_t r
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 rows are copied as boxes where a block of the pool is a multiple of 8
+// rows (the swizzle's period) and divides a key tile, or the other way round.
 template <class G>
-cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
+void set_boxes(AttnParams &p)
 {
-    constexpr int bytes = Smem<G>::BYTES;
-    static_assert(bytes <= 227 * 1024, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(attention_kernel<G>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess)
-        return e;
-    // bf16 rows are copied as boxes where a block of the pool is a multiple of 8
-    // rows (the swizzle's period) and divides a key tile, or the other way round
     p.box_rows = 0;
-    if constexpr (!G::QUANT) {
-        const int b = p.block;
-        const int64_t rows = p.num_blocks * b;
-        const int heads = G::MLA ? 1 : p.heads / p.group;
-        if (b % 8 == 0 && (G::KT % b == 0 || b % G::KT == 0) && rows < 0x7FFFFFFFll) {
-            const int box = std::min(b, G::KT);
-            if (encode_map(&p.copy_map, p.copy, p.copy_ss, rows, G::MLA ? 512 : heads * 128, box) &&
-                encode_map(&p.rot_map, p.rot, p.rot_ss, rows, G::MLA ? 64 : heads * 128, box))
-                p.box_rows = box;
-        }
-    }
-    // the register shares of the warpgroups come out of what a block starts with
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, attention_kernel<G>)) != cudaSuccess)
-        return e;
-    if (G::NT * G::REG_SOFTMAX + G::LOAD_WG * G::REG_LOAD + (4 - G::NT - G::LOAD_WG) * kRegMma >
-        4 * fa.numRegs)
-        return cudaErrorInvalidConfiguration;
-    attention_kernel<G><<<(unsigned)blocks, kAttnThreads, bytes, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess || p.max_splits == 1)
-        return e;
-    // the join starts while the last blocks run and waits for them on the device
+    const int b = p.block;
+    const int64_t rows = p.num_blocks * b;
+    const int heads = p.heads / p.group;
+    if (G::QUANT || b % 8 != 0 || (G::KT % b != 0 && b % G::KT != 0) || rows >= 0x7FFFFFFFll)
+        return;
+    const int box = std::min(b, G::KT);
+    if (encode_map(&p.copy_map, p.copy, p.copy_ss, rows, G::MLA ? 512 : heads * 128, box) &&
+        encode_map(&p.rot_map, p.rot, p.rot_ss, rows, G::MLA ? 64 : heads * 128, box))
+        p.box_rows = box;
+}
+
+// Joins split rows; starts while the last blocks run and waits for them on the
+// device.
+template <class G>
+cudaError_t launch_join(const AttnParams &p, cudaStream_t stream)
+{
+    if (p.max_splits == 1)
+        return cudaSuccess;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -1609,6 +2064,44 @@ cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, attention_join_kernel<G>, p);
 }
 
+template <class G>
+cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
+{
+    constexpr int bytes = Smem<G>::BYTES;
+    static_assert(bytes <= 227 * 1024, "shared memory");
+    set_boxes<G>(p);
+    cudaError_t e = cudaFuncSetAttribute(attention_kernel<G>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess)
+        return e;
+    // the register shares of the warpgroups come out of what a block starts with
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, attention_kernel<G>)) != cudaSuccess)
+        return e;
+    if (G::NT * G::REG_SOFTMAX + G::LOAD_WG * G::REG_LOAD + (4 - G::NT - G::LOAD_WG) * kRegMma >
+        4 * fa.numRegs)
+        return cudaErrorInvalidConfiguration;
+    attention_kernel<G><<<(unsigned)blocks, kAttnThreads, bytes, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess)
+        return e;
+    return launch_join<G>(p, stream);
+}
+
+template <class G, int R>
+cudaError_t launch_few(AttnParams &p, int64_t blocks, cudaStream_t stream)
+{
+    static_assert(G::BYTES <= 113 * 1024, "two blocks to an SM");
+    set_boxes<G>(p);
+    cudaError_t e = cudaFuncSetAttribute(attention_few_kernel<G, R>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, G::BYTES);
+    if (e != cudaSuccess)
+        return e;
+    attention_few_kernel<G, R><<<(unsigned)blocks, kFewThreads, G::BYTES, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess)
+        return e;
+    return launch_join<G>(p, stream);
+}
+
 } // namespace
 
 AttnPlan plan_attention(RowKind kind, const AttnShape &a)
@@ -1616,10 +2109,11 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
     const bool mla = kind == RowKind::Mla;
     const int64_t kt = mla ? 64 : 128;
     AttnPlan pl{};
-    pl.row_tiles = !mla && (int64_t)a.max_q_len * a.group > kRows ? 2 : 1;
-    const int64_t rows = kRows * pl.row_tiles;
+    const bool few = !mla && a.max_q_len <= 1 && a.group <= kFewRows;
+    pl.row_tiles = few ? 0 : !mla && (int64_t)a.max_q_len * a.group > kRows ? 2 : 1;
+    const int64_t rows = kRows * std::max(1, pl.row_tiles);
     // row tiles over all sequences: at most one partly filled one each
-    const int64_t tiles = a.total_q * a.group / rows + a.num_seqs;
+    const int64_t tiles = few ? a.num_seqs : a.total_q * a.group / rows + a.num_seqs;
     const int64_t units = tiles * (mla ? 2 : a.kv_heads);
     // most key tiles of one row tile
     int64_t nv = (a.max_kv_len + kt - 1) / kt;
@@ -1632,7 +2126,8 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
     nv = std::max<int64_t>(nv, 1);
     // pieces of the key axis: enough blocks for a few on every SM, none shorter
     // than four tiles (a block's start and end cost about as much as two)
-    const int64_t want = std::max<int64_t>(4, (units * nv + 4 * 152 - 1) / (4 * 152));
+    const int64_t slots = (few ? 2 * 152 : 152) * 4;
+    const int64_t want = std::max<int64_t>(4, (units * nv + slots - 1) / slots);
     pl.split_tiles = (int32_t)std::min(nv, want);
     pl.max_splits = (int32_t)((nv + pl.split_tiles - 1) / pl.split_tiles);
     pl.blocks = units * pl.max_splits;
@@ -1645,6 +2140,12 @@ cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cu
     if (kind == RowKind::Mla)
         return quant ? launch<MlaGeo<true>>(p, pl.blocks, stream)
                      : launch<MlaGeo<false>>(p, pl.blocks, stream);
+    if (pl.row_tiles == 0 && p.group <= 8)
+        return quant ? launch_few<FewGeo<true>, 8>(p, pl.blocks, stream)
+                     : launch_few<FewGeo<false>, 8>(p, pl.blocks, stream);
+    if (pl.row_tiles == 0)
+        return quant ? launch_few<FewGeo<true>, 16>(p, pl.blocks, stream)
+                     : launch_few<FewGeo<false>, 16>(p, pl.blocks, stream);
     if (pl.row_tiles == 2)
         return quant ? launch<HeadGeo<true, 2>>(p, pl.blocks, stream)
                      : launch<HeadGeo<false, 2>>(p, pl.blocks, stream);

@@ -92,7 +92,7 @@ struct AttnShape {
 };
 
 struct AttnPlan {
-    int32_t row_tiles;   // 128-row tiles of a block
+    int32_t row_tiles;   // 128-row tiles of a block; 0: the kernel for few rows
     int32_t split_tiles; // key tiles of a block
     int32_t max_splits;
     int64_t blocks;
