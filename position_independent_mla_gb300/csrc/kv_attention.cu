@@ -34,6 +34,7 @@
 #include <type_traits>
 
 #include <cudaTypedefs.h>
+#include <cuda_fp16.h>
 
 #include "kv_device.cuh"
 #include "kv_serve.h"
@@ -287,6 +288,20 @@ __device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uin
                  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d),
                  "r"(a), "r"(b), "r"(mma_desc<N, MAJOR, MAJOR>()), "r"(acc), "r"(kOperandHigh),
                  "r"(lead), "r"(b_high)
+                 : "memory");
+}
+
+// kind::f8f6f4: D fp32, A and B e4m3.
+template <int N, int MAJOR>
+__device__ __forceinline__ void mma_smem_e4m3(uint32_t d, uint32_t a, uint32_t b, uint32_t acc,
+                                              uint32_t lead, uint32_t b_high)
+{
+    constexpr uint32_t desc = (1u << 4) | ((uint32_t)MAJOR << 15) | ((uint32_t)MAJOR << 16) |
+                              ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+    asm volatile("{\n.reg .pred p, q;\n.reg .b64 x, y;\nsetp.ne.b32 p, %4, 0;\n"
+                 "setp.ne.b32 q, %6, 0;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %7};\n"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(desc), "r"(acc), "r"(kOperandHigh), "r"(lead), "r"(b_high)
                  : "memory");
 }
 
@@ -674,21 +689,22 @@ struct Flights {
     }
 };
 
-// Head rows in bf16, straight into the ring.  Whole tiles are boxes of the
+// Head rows into the ring as they are stored.  Whole tiles are boxes of the
 // tensor maps that one warp asks for (a box is at most a block of the pool); tiles
 // that hold keys nobody sees, and pools whose blocks do not divide a tile, are
 // copied row by row with zeros in the place of those keys: a lane owns one key
-// row of its warp, 16 lanes copy the 256 bytes of a row.  Every warp waits for
+// row of its warp, 16 lanes copy 256 bytes (8 lanes 128).  Every warp waits for
 // every stage and signals it, also where one warp copies for all: none may run
 // ahead or fall behind by more than a phase, the parity would not show it.
 template <class G>
-__device__ __forceinline__ void load_heads_bf16(const AttnParams &p, const Work &w, uint32_t ring,
+__device__ __forceinline__ void load_heads(const AttnParams &p, const Work &w, uint32_t ring,
                                                 uint32_t bars, int warp, int lane,
                                                 volatile int *abort, bool &bad)
 {
     constexpr int WARPS = G::LOAD_WG * 4, ROWS = G::KT / WARPS; // rows of a warp: 32 or 16
     const int base = warp * ROWS;
-    const int c = lane & 15, half = lane >> 4;
+    constexpr int PIECES = G::STAGE / G::KT / 16, PER = 32 / PIECES; // of a row; rows at a time
+    const int c = lane & (PIECES - 1), sub = lane / PIECES;
     auto whole = [&](int v) { return p.box_rows > 0 && tile_whole<G::KT>(w, real_tile(w, v)); };
     // the key whose slot this lane looks up: the first of its box, or its row's
     auto key_at = [&](int v) {
@@ -722,16 +738,17 @@ __device__ __forceinline__ void load_heads_bf16(const AttnParams &p, const Work 
                         const CUtensorMap *map = part == 0 ? &p.rot_map : &p.copy_map;
                         const uint32_t at = dst + lane * p.box_rows * 128;
                         copy_box(at, map, w.head * 128, row0, full);
-                        copy_box(at + 16384, map, w.head * 128 + 64, row0, full);
+                        if (PIECES == 16) // 64 columns of bf16 to a box
+                            copy_box(at + 16384, map, w.head * 128 + 64, row0, full);
                     }
                 }
             } else {
                 const char *src = part == 0 ? p.rot : p.copy;
                 const int64_t ss = part == 0 ? p.rot_ss : p.copy_ss;
-                const char *col = src + w.head * 256 + c * 16;
+                const char *col = src + w.head * PIECES * 16 + c * 16;
 #pragma unroll
-                for (int i = 0; i < ROWS / 2; ++i) {
-                    const int r = i * 2 + half;
+                for (int i = 0; i < ROWS / PER; ++i) {
+                    const int r = i * PER + sub;
                     const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, r);
                     const int row = base + r;
                     copy16(dst + ((c >> 3) << 14) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
@@ -1561,7 +1578,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
         else if constexpr (G::QUANT)
             load_heads_e4m3<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
         else
-            load_heads_bf16<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
+            load_heads<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
         if (bad)
             s_status = kStatusOutOfRange;
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -1606,30 +1623,68 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
 // 2^8, and only then are the true maxima formed across the block and O rescaled.
 // Sums stay per key until the end.  An MMA with N = 16 takes 40 clocks (the
 // operand A is read at 128 bytes a clock), 640 a tile, where the tile's rows take
-// 2700 (bf16) or 1400 (e4m3) from HBM: the kernel is bound by memory.  Two
-// blocks share an SM, so that one's start and end lie under the other's loads.
-template <bool QUANT_>
+// 2700 from HBM: the kernel is bound by memory.  Two blocks share an SM, so that
+// one's start and end lie under the other's loads.
+//
+// e4m3 rows go into 8-bit MMAs as they are stored; 1400 clocks of HBM a tile
+// leave no time to widen them.  Queries and weights are split instead, x = hi +
+// lo / 16 with both parts e4m3: with 4 bits each that is every bit of a bf16
+// query, and a weight to 2^-8, as good as bf16 (below 2^-10 of the row's
+// reference to 2^-18 of it).  The parts are rows of their own (16 for up to 8
+// heads, 32 for up to 16).  A key's scale multiplies its scores, its value's scale
+// 2^e its weights: they are 2^(s + e - reference), the references being those of
+// s + e, and the sums take 2^-e of them.
+template <bool QUANT_, int R_>
 struct FewGeo {
     static constexpr bool MLA = false, QUANT = QUANT_;
+    static constexpr int R = R_;                    // rows: 8 or 16
+    static constexpr int N = QUANT ? 2 * R : 16;    // rows of the MMAs
     static constexpr int NT = 1, KT = 128;
     static constexpr int DV = 128;
     static constexpr int LOAD_WG = 1;
-    static constexpr int STAGE = 2 * 128 * 128, STAGES = QUANT ? 2 : 3;
-    static constexpr int RAW = QUANT ? 2 : 0;
-    static constexpr int RAW_AT = STAGES * STAGE, RAW_STAGE = STAGE / 2 + 512;
-    static constexpr int RING = RAW_AT + RAW * RAW_STAGE;
-    static constexpr int Q_BYTES = 2 * 16 * 128, P_BYTES = 128 * 32;
+    static constexpr int STAGE = (QUANT ? 1 : 2) * 128 * 128, STAGES = QUANT ? 6 : 3;
+    static constexpr int RING = STAGES * STAGE;
+    // a key's weights: N values of 1 or 2 bytes
+    static constexpr int Q_BYTES = N * (QUANT ? 128 : 256), P_BYTES = 128 * N * (QUANT ? 1 : 2);
     static constexpr int P_AT = RING, Q_AT = P_AT + 2 * P_BYTES, BAR_AT = Q_AT + Q_BYTES;
     static constexpr int BYTES = BAR_AT + (kBarRing + 2 * STAGES) * 8 + 1024;
-    static constexpr int COLS = 64; // tensor memory: S at 0 and 16, O at 32
+    // tensor memory: two S, O
+    static constexpr int O_COL = 2 * N, COLS = 4 * N;
 };
 
 constexpr int kFewThreads = 288; // 4 softmax warps, 4 load warps, 1 MMA warp
 constexpr int kFewRows = 16;
+constexpr float kLazyFew = 4.0f;   // growth of a reference: e4m3 weights start at 2^4, end at 448
 
 // Byte of (key, first of 8 rows) of Pᵀ: core matrices of 8 keys x 8 rows (16 bytes
 // a key), the second 8 rows 128 bytes on, the next 8 keys 256 bytes on.
 __device__ __forceinline__ uint32_t few_weight(int key) { return (key >> 3) * 256 + (key & 7) * 16; }
+
+// Two values to e4m3 parts x = hi + lo / 16.
+__device__ __forceinline__ void split_e4m3(float a, float b, uint32_t &hi, uint32_t &lo)
+{
+    uint16_t h, l;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
+    uint32_t w;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(w) : "h"(h));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(l)
+        : "f"((b - f.y) * 16.0f), "f"((a - f.x) * 16.0f));
+    hi = h;
+    lo = l;
+}
+
+// Eight values to eight bytes of each part.
+__device__ __forceinline__ void split8(const float *x, uint2 &hi, uint2 &lo)
+{
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        split_e4m3(x[2 * i], x[2 * i + 1], h[i], l[i]);
+    hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+}
 
 // A vote over the four softmax warps.  Each of them comes to every vote, also
 // when its own wait ran out: they go on or give up together.
@@ -1644,11 +1699,13 @@ __device__ __forceinline__ bool softmax_any(bool x)
     return r != 0;
 }
 
-template <class G, int R>
+template <class G>
 __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, uint32_t tmem,
                                             uint32_t smem, uint32_t bars, int tid,
-                                            volatile int *abort, float (*red)[kFewRows])
+                                            volatile int *abort, float (*red)[kFewRows],
+                                            const float *q_scale)
 {
+    constexpr int R = G::R;
     const int warp = tid >> 5, lane = tid & 31;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     const float c = p.scale * 1.4426950408889634f;
@@ -1658,22 +1715,60 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
         ref[r] = -INFINITY;
         sum[r] = 0.0f;
     }
+    // e4m3: this thread's key's scales, asked for a tile ahead
+    float ks = 1.0f, vs = 1.0f;
+    int32_t blk = 0;
+    bool none = false;
+    auto key_at = [&](int v) { return real_tile(w, v) * G::KT + tid; };
+    auto ask = [&](int v, int32_t b) {
+        const int64_t slot = v < w.end ? key_slot(p, w, key_at(v), b, none) : -1;
+        ks = slot < 0 ? 1.0f : __ldg(p.rs + slot * p.rs_ss + w.head);
+        vs = slot < 0 ? 1.0f : __ldg(p.cs + slot * p.cs_ss + w.head);
+    };
+    if constexpr (G::QUANT) {
+        if (w.beg < w.end)
+            ask(w.beg, key_block(p, w, key_at(w.beg)));
+        if (w.beg + 1 < w.end)
+            blk = key_block(p, w, key_at(w.beg + 1));
+    }
     for (int v = w.beg; v < w.end; ++v) {
         const int ord = v - w.beg, i = ord & 1;
-        const int k = real_tile(w, v) * G::KT + tid;
-        const bool see = k < w.hi && (k >= w.lo || k < w.sk);
+        const bool see = key_seen(w, key_at(v));
+        const float my_ks = ks, my_vs = vs;
+        if constexpr (G::QUANT) {
+            ask(v + 1, blk);
+            if (v + 2 < w.end)
+                blk = key_block(p, w, key_at(v + 2));
+        }
         bool ok = bar_wait(bars + (kBarS + i) * 8, (ord >> 1) & 1, abort, p.wait_limit_ns);
         mma_fence_after();
-        uint32_t raw[16];
-        tmem_ld16(tmem + i * 16 + lanes, raw);
+        uint32_t raw[G::N];
+#pragma unroll
+        for (int n = 0; n < G::N; n += 16)
+            tmem_ld16(tmem + i * G::N + n + lanes, raw + n);
         tmem_ld_wait();
-        tmem_pin16(raw);
-        float x[R];
+#pragma unroll
+        for (int n = 0; n < G::N; n += 16)
+            tmem_pin16(raw + n);
+        float x[R], inv = 1.0f;
+        if constexpr (G::QUANT) {
+            const float e = (float)((int)(__float_as_uint(my_vs) >> 23) - 127);
+            inv = __uint_as_float((254u << 23) - __float_as_uint(my_vs)); // 1 / 2^e
+            const float cks = c * my_ks;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                x[r] = fmaf(fmaf(__uint_as_float(raw[R + r]), 0.0625f, __uint_as_float(raw[r])),
+                            cks * q_scale[r], e);
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                x[r] = __uint_as_float(raw[r]) * c;
+        }
         bool grew = false;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            x[r] = see ? __uint_as_float(raw[r]) * c : -INFINITY;
-            grew |= x[r] - ref[r] > kLazy;
+            x[r] = see ? x[r] : -INFINITY;
+            grew |= x[r] - ref[r] > kLazyFew;
         }
         if (softmax_any(grew || !ok)) {
             if (softmax_any(!ok))
@@ -1692,7 +1787,7 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const float m = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
-                const bool up = m - ref[r] > kLazy;
+                const bool up = m - ref[r] > kLazyFew;
                 f[r] = up ? exp2_fast(ref[r] - m) : 1.0f;
                 ref[r] = up ? m : ref[r];
                 sum[r] *= f[r];
@@ -1702,28 +1797,52 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
                 if (softmax_any(!ok))
                     return false;
                 mma_fence_after();
-                uint32_t o[16];
-                tmem_ld16(tmem + 32 + lanes, o);
-                tmem_ld_wait();
-                tmem_pin16(o);
+                uint32_t o[G::N];
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-                    o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
-                tmem_st16(tmem + 32 + lanes, o);
+                for (int n = 0; n < G::N; n += 16)
+                    tmem_ld16(tmem + G::O_COL + n + lanes, o + n);
+                tmem_ld_wait();
+#pragma unroll
+                for (int n = 0; n < G::N; n += 16)
+                    tmem_pin16(o + n);
+#pragma unroll
+                for (int n = 0; n < G::N; ++n)
+                    if (G::QUANT || n < R)
+                        o[n] = __float_as_uint(__uint_as_float(o[n]) * f[n % R]);
+#pragma unroll
+                for (int n = 0; n < G::N; n += 16)
+                    tmem_st16(tmem + G::O_COL + n + lanes, o + n);
                 tmem_st_wait();
             }
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             x[r] = exp2_fast(x[r] - (ref[r] == -INFINITY ? 0.0f : ref[r]));
-            sum[r] += x[r];
+            sum[r] = G::QUANT ? fmaf(x[r], inv, sum[r]) : sum[r] + x[r];
         }
-        const uint32_t at = smem + G::P_AT + i * G::P_BYTES + few_weight(tid);
+        const uint32_t buf = smem + G::P_AT + i * G::P_BYTES;
+        if constexpr (G::QUANT) {
+            // 16 bytes a key and 16 rows: the high parts, then the low ones
 #pragma unroll
-        for (int r = 0; r < R; r += 8)
-            sts16(at + r * 16, make_uint4(pack_bf16(x[r], x[r + 1]), pack_bf16(x[r + 2], x[r + 3]),
-                                          pack_bf16(x[r + 4], x[r + 5]),
-                                          pack_bf16(x[r + 6], x[r + 7])));
+            for (int r = 0; r < R; ++r)
+                x[r] *= 16.0f;
+            uint2 hi[R / 8], lo[R / 8];
+#pragma unroll
+            for (int r = 0; r < R; r += 8)
+                split8(x + r, hi[r / 8], lo[r / 8]);
+            if constexpr (R == 8) {
+                sts16(buf + tid * 16, make_uint4(hi[0].x, hi[0].y, lo[0].x, lo[0].y));
+            } else {
+                sts16(buf + few_weight(tid), make_uint4(hi[0].x, hi[0].y, hi[1].x, hi[1].y));
+                sts16(buf + few_weight(tid) + 128, make_uint4(lo[0].x, lo[0].y, lo[1].x, lo[1].y));
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; r += 8)
+                sts16(buf + few_weight(tid) + r * 16,
+                      make_uint4(pack_bf16(x[r], x[r + 1]), pack_bf16(x[r + 2], x[r + 3]),
+                                 pack_bf16(x[r + 4], x[r + 5]), pack_bf16(x[r + 6], x[r + 7])));
+        }
         async_fence();
         mma_fence_before();
         bar_signal(bars + (kBarP + i) * 8);
@@ -1742,17 +1861,24 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
             red[warp][r] = m;
     }
     bar_wait_all(1, 128);
-    uint32_t o[16];
-    tmem_ld16(tmem + 32 + lanes, o);
+    uint32_t o[G::N];
+#pragma unroll
+    for (int n = 0; n < G::N; n += 16)
+        tmem_ld16(tmem + G::O_COL + n + lanes, o + n);
     tmem_ld_wait();
-    tmem_pin16(o);
+#pragma unroll
+    for (int n = 0; n < G::N; n += 16)
+        tmem_pin16(o + n);
     const bool parts = w.splits > 1;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         if (r >= p.group)
             break;
         const float l = (red[0][r] + red[1][r]) + (red[2][r] + red[3][r]);
-        const float y = l == 0.0f ? 0.0f : __uint_as_float(o[r]) / l;
+        float y = __uint_as_float(o[r]);
+        if constexpr (G::QUANT)
+            y = fmaf(__uint_as_float(o[R + r]), 0.0625f, y) * 0.0625f;
+        y = l == 0.0f ? 0.0f : y / l;
         const int h = w.head * p.group + r;
         const int64_t at = w.q0 * p.heads + h;
         if (parts)
@@ -1778,8 +1904,10 @@ __device__ __forceinline__ bool few_mma(const AttnParams &p, const Work &w, uint
 {
     const uint32_t full = bars + kBarRing * 8, empty = full + G::STAGES * 8;
     const uint32_t q = operand(smem + G::Q_AT, 16);
-    // Pᵀ: no swizzle; 256 bytes to the next 8 keys, 128 to the next 8 rows
+    // Pᵀ: no swizzle; core matrices of 8 keys x 16 bytes, 128 bytes to the rows of the
+    // next 16 bytes, P_BYTES / 16 to the next 8 keys
     constexpr uint32_t kWeightHigh = (128u >> 4) | (1u << 14);
+    constexpr uint32_t kKeys8 = G::P_BYTES / 16;
     int stage = 0, phase = 0, vstage = 0;
     auto next = [&] {
         if (++stage == G::STAGES) {
@@ -1795,10 +1923,17 @@ __device__ __forceinline__ bool few_mma(const AttnParams &p, const Work &w, uint
                 return false;
             async_fence();
             const uint32_t k = operand(smem + stage * G::STAGE, 16);
+            if constexpr (G::QUANT) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                mma_smem<kFewRows>(tmem + i * 16, k + (j >> 2) * (16384 >> 4) + (j & 3) * 2,
+                for (int j = 0; j < 4; ++j) // 32 columns of 8 bits
+                    mma_smem_e4m3<G::N, 0>(tmem + i * G::N, k + j * 2, q + j * 2, j > 0, lead,
+                                           kOperandHigh);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    mma_smem<G::N>(tmem + i * G::N, k + (j >> 2) * (16384 >> 4) + (j & 3) * 2,
                                    q + (j >> 2) * (2048 >> 4) + (j & 3) * 2, j > 0, lead);
+            }
             bar_signal_mma(bars + (kBarS + i) * 8, lead);
             bar_signal_mma(empty + stage * 8, lead);
             next();
@@ -1809,11 +1944,20 @@ __device__ __forceinline__ bool few_mma(const AttnParams &p, const Work &w, uint
                 return false;
             mma_fence_after();
             const uint32_t a = operand(smem + vstage * G::STAGE, 16384);
-            const uint32_t pt = operand(smem + G::P_AT + b * G::P_BYTES, 256);
+            const uint32_t pt = operand(smem + G::P_AT + b * G::P_BYTES, kKeys8);
+            if constexpr (G::QUANT) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                mma_smem<kFewRows, 1>(tmem + 32, a + j * (2048 >> 4), pt + j * (512 >> 4),
-                                      ord > 1 || j > 0, lead, kWeightHigh);
+                for (int j = 0; j < 4; ++j) // 32 keys
+                    mma_smem_e4m3<G::N, 1>(tmem + G::O_COL, a + j * (4096 >> 4),
+                                           pt + j * (4 * kKeys8 >> 4), ord > 1 || j > 0, lead,
+                                           kWeightHigh);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) // 16 keys
+                    mma_smem<G::N, 1>(tmem + G::O_COL, a + j * (2048 >> 4),
+                                      pt + j * (2 * kKeys8 >> 4), ord > 1 || j > 0, lead,
+                                      kWeightHigh);
+            }
             bar_signal_mma(empty + vstage * 8, lead);
             bar_signal_mma(bars + kBarO * 8, lead);
         }
@@ -1829,14 +1973,59 @@ __device__ __forceinline__ bool few_mma(const AttnParams &p, const Work &w, uint
     return true;
 }
 
-template <class G, int R>
+// The queries of a block as e4m3 parts, a row's largest value in [128, 256) after a
+// power-of-two scale; rows past the group are 0.  16 threads to a row.
+template <class G>
+__device__ __forceinline__ void few_queries_e4m3(const AttnParams &p, const Work &w, uint32_t q_smem,
+                                                 int lt, float *q_scale)
+{
+    for (int r = lt >> 4; r < G::R; r += 8) {
+        const int c = lt & 15;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < p.group)
+            v = __ldg(reinterpret_cast<const uint4 *>(
+                    p.q + w.q0 * p.q_ts + (int64_t)(w.head * p.group + r) * p.q_hs) + c);
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t a = u[i] & 0x7FFFu, b = (u[i] >> 16) & 0x7FFFu;
+            m = max(m, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1)
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        // 2^e of the row's scale: the exponent of its largest value, less 7
+        const int e = min(max((int)(m >> 7) - 134, -120), 120);
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16) * inv;
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u) * inv;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) // what was infinite is NaN
+            x[i] = fabsf(x[i]) < 256.0f ? x[i] : __uint_as_float(0x7FC00000u);
+        uint2 hi, lo;
+        split8(x, hi, lo);
+        const uint32_t at = q_smem + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi.x), "r"(hi.y) : "memory");
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + G::R * 128), "r"(lo.x), "r"(lo.y)
+                     : "memory");
+        if (c == 0)
+            q_scale[r] = __uint_as_float((uint32_t)(127 + e) << 23);
+    }
+}
+
+template <class G>
 __global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
     const __grid_constant__ AttnParams p)
 {
     extern __shared__ unsigned char raw_smem[];
     __shared__ uint32_t s_tmem, s_status;
     __shared__ volatile int s_abort;
-    __shared__ float s_red[4][kFewRows];
+    __shared__ float s_red[4][kFewRows], s_qscale[kFewRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
     const uint32_t bars = smem + G::BAR_AT;
@@ -1897,23 +2086,29 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
     const uint32_t tmem = s_tmem;
 
     if (warp < 4) {
-        few_softmax<G, R>(p, w, tmem, smem, bars, tid, &s_abort, s_red);
+        if constexpr (G::QUANT) // the scales of the queries
+            bar_wait_all(2, 256);
+        few_softmax<G>(p, w, tmem, smem, bars, tid, &s_abort, s_red, s_qscale);
     } else if (warp < 8) {
         const int lt = tid - 128;
-        for (int i = lt; i < kFewRows * 16; i += 128) { // the queries; rows past the group are 0
-            const int r = i >> 4, c = i & 15;
-            const bool ok = r < p.group;
-            const char *src =
-                p.q + w.q0 * p.q_ts + (int64_t)(w.head * p.group + (ok ? r : 0)) * p.q_hs + c * 16;
-            copy16(smem + G::Q_AT + (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4), src,
-                   ok ? 16u : 0u);
+        if constexpr (G::QUANT) {
+            few_queries_e4m3<G>(p, w, smem + G::Q_AT, lt, s_qscale);
+            bar_arrive(2, 256);
+            async_fence();
+            bar_signal(bars + kBarQ * 8);
+        } else {
+            for (int i = lt; i < kFewRows * 16; i += 128) { // rows past the group are 0
+                const int r = i >> 4, c = i & 15;
+                const bool ok = r < p.group;
+                const char *src = p.q + w.q0 * p.q_ts +
+                                  (int64_t)(w.head * p.group + (ok ? r : 0)) * p.q_hs + c * 16;
+                copy16(smem + G::Q_AT + (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                       src, ok ? 16u : 0u);
+            }
+            bar_signal_copies(bars + kBarQ * 8);
         }
-        bar_signal_copies(bars + kBarQ * 8);
         bool out = false;
-        if constexpr (G::QUANT)
-            load_heads_e4m3<G>(p, w, smem, bars + kBarRing * 8, warp - 4, lane, &s_abort, out);
-        else
-            load_heads_bf16<G>(p, w, smem, bars + kBarRing * 8, warp - 4, lane, &s_abort, out);
+        load_heads<G>(p, w, smem, bars + kBarRing * 8, warp - 4, lane, &s_abort, out);
         if (out)
             s_status = kStatusOutOfRange;
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -2003,10 +2198,10 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
         p.lse[at] = sum == 0.0f ? -INFINITY : ref + logf(sum);
 }
 
-// Tensor map of one part of the pool's rows (`width` bf16 columns): boxes of 64
-// columns and p.box_rows rows, swizzled as the MMAs read them.
+// Tensor map of one part of the pool's rows (`width` columns of bf16 or bytes): boxes
+// of 128 bytes and p.box_rows rows, swizzled as the MMAs read them.
 bool encode_map(CUtensorMap *map, const char *base, int64_t row_bytes, int64_t rows, int width,
-                int box_rows)
+                int box_rows, bool bytes)
 {
     static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         void *f = nullptr;
@@ -2021,15 +2216,16 @@ bool encode_map(CUtensorMap *map, const char *base, int64_t row_bytes, int64_t r
         return false;
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<char *>(base), dims, strides,
+    const cuuint32_t box[2] = {bytes ? 128u : 64u, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    return encode(map,
+                  bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<char *>(base), dims, strides,
                   box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// bf16 rows are copied as boxes where a block of the pool is a multiple of 8
-// rows (the swizzle's period) and divides a key tile, or the other way round.
+// Rows are copied as boxes where a block of the pool is a multiple of 8 rows (the
+// swizzle's period) and divides a key tile, or the other way round.
 template <class G>
 void set_boxes(AttnParams &p)
 {
@@ -2037,11 +2233,12 @@ void set_boxes(AttnParams &p)
     const int b = p.block;
     const int64_t rows = p.num_blocks * b;
     const int heads = p.heads / p.group;
-    if (G::QUANT || b % 8 != 0 || (G::KT % b != 0 && b % G::KT != 0) || rows >= 0x7FFFFFFFll)
+    if (b % 8 != 0 || (G::KT % b != 0 && b % G::KT != 0) || rows >= 0x7FFFFFFFll)
         return;
     const int box = std::min(b, G::KT);
-    if (encode_map(&p.copy_map, p.copy, p.copy_ss, rows, G::MLA ? 512 : heads * 128, box) &&
-        encode_map(&p.rot_map, p.rot, p.rot_ss, rows, G::MLA ? 64 : heads * 128, box))
+    const int copy = G::MLA ? 512 : heads * 128, rot = G::MLA ? 64 : heads * 128;
+    if (encode_map(&p.copy_map, p.copy, p.copy_ss, rows, copy, box, G::QUANT) &&
+        encode_map(&p.rot_map, p.rot, p.rot_ss, rows, rot, box, G::QUANT))
         p.box_rows = box;
 }
 
@@ -2069,7 +2266,8 @@ cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
 {
     constexpr int bytes = Smem<G>::BYTES;
     static_assert(bytes <= 227 * 1024, "shared memory");
-    set_boxes<G>(p);
+    if (!G::QUANT) // e4m3 rows are converted on their way
+        set_boxes<G>(p);
     cudaError_t e = cudaFuncSetAttribute(attention_kernel<G>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess)
@@ -2087,16 +2285,16 @@ cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
     return launch_join<G>(p, stream);
 }
 
-template <class G, int R>
+template <class G>
 cudaError_t launch_few(AttnParams &p, int64_t blocks, cudaStream_t stream)
 {
     static_assert(G::BYTES <= 113 * 1024, "two blocks to an SM");
     set_boxes<G>(p);
-    cudaError_t e = cudaFuncSetAttribute(attention_few_kernel<G, R>,
+    cudaError_t e = cudaFuncSetAttribute(attention_few_kernel<G>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, G::BYTES);
     if (e != cudaSuccess)
         return e;
-    attention_few_kernel<G, R><<<(unsigned)blocks, kFewThreads, G::BYTES, stream>>>(p);
+    attention_few_kernel<G><<<(unsigned)blocks, kFewThreads, G::BYTES, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     return launch_join<G>(p, stream);
@@ -2141,11 +2339,11 @@ cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cu
         return quant ? launch<MlaGeo<true>>(p, pl.blocks, stream)
                      : launch<MlaGeo<false>>(p, pl.blocks, stream);
     if (pl.row_tiles == 0 && p.group <= 8)
-        return quant ? launch_few<FewGeo<true>, 8>(p, pl.blocks, stream)
-                     : launch_few<FewGeo<false>, 8>(p, pl.blocks, stream);
+        return quant ? launch_few<FewGeo<true, 8>>(p, pl.blocks, stream)
+                     : launch_few<FewGeo<false, 8>>(p, pl.blocks, stream);
     if (pl.row_tiles == 0)
-        return quant ? launch_few<FewGeo<true>, 16>(p, pl.blocks, stream)
-                     : launch_few<FewGeo<false>, 16>(p, pl.blocks, stream);
+        return quant ? launch_few<FewGeo<true, 16>>(p, pl.blocks, stream)
+                     : launch_few<FewGeo<false, 16>>(p, pl.blocks, stream);
     if (pl.row_tiles == 2)
         return quant ? launch<HeadGeo<true, 2>>(p, pl.blocks, stream)
                      : launch<HeadGeo<false, 2>>(p, pl.blocks, stream);
