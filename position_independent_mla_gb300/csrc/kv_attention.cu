@@ -14,10 +14,10 @@
 // new token over 8 key heads read each key once, and a chunk of many tokens
 // fills whole tiles.
 //
-// Roles of a block's four warpgroups (512 threads):
-//   softmax  a thread per row: reads its row of S from tensor memory, masks,
-//            keeps m and l in registers, writes the bf16 weights back over S
-//            (they are the A operand of the second MMA) and at the end O / l;
+// Roles of a block's 13 warps:
+//   softmax  4 a row tile, a thread per row: reads its row of S from tensor memory,
+//            masks, keeps m and l in registers, writes the bf16 weights back over
+//            S (they are the A operand of the second MMA) and at the end O / l;
 //   load     bring rows of the pool through the block table into shared memory
 //            in the 128-byte swizzled layout that the MMAs read;
 //   mma      one warp issues every MMA.
@@ -44,8 +44,8 @@ namespace kvr {
 namespace {
 
 constexpr int kRows = 128;         // rows per tile: the M of an MMA
-constexpr int kAttnThreads = 512;  // four warpgroups
-constexpr int kRegMma = 56;        // registers of a thread of the MMA warpgroup
+constexpr int kAttnThreads = 416;  // 13 warps, the last of them issues the MMAs
+constexpr int kMmaWarp = 12;
 constexpr float kLazy = 8.0f;      // log2 of the growth of a maximum that O tolerates
 
 // ---------------------------------------------------------------------------
@@ -60,6 +60,11 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p)
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void bar_init_fence()
+{
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
 __device__ __forceinline__ void bar_signal(uint32_t bar)
@@ -84,6 +89,14 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, i
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
                  "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
                  "l"(map), "r"(bar), "r"(x), "r"(y)
+                 : "memory");
+}
+
+// A box of a tensor map on its way to L2.
+__device__ __forceinline__ void prefetch_box(const CUtensorMap *map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x),
+                 "r"(y)
                  : "memory");
 }
 
@@ -143,18 +156,6 @@ __device__ __forceinline__ void mma_fence_before() { asm volatile("tcgen05.fence
 __device__ __forceinline__ void mma_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-template <int R>
-__device__ __forceinline__ void reg_inc()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-
-template <int R>
-__device__ __forceinline__ void reg_dec()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
-
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -198,6 +199,20 @@ __device__ __forceinline__ uint4 lds16(uint32_t src)
                  : "r"(src)
                  : "memory");
     return v;
+}
+
+// Columns of tensor memory for the block, by one warp; the address is left at `to`.
+__device__ __forceinline__ void tmem_alloc(uint32_t to, uint32_t columns)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t columns)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
 }
 
 #define KV_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), \
@@ -323,6 +338,20 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// 32 bytes, aligned so: a whole sector of a row.
+__device__ __forceinline__ void st32(void *to, const uint32_t *r)
+{
+    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::KV_W8(r, 0), "l"(to)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     uint32_t r;
@@ -413,7 +442,7 @@ struct HeadGeo {
     static constexpr int NT = NT_, KT = 128;
     static constexpr int QPANELS = 2, OC = 128;    // query panels in shared memory; columns of O
     static constexpr int DV = 128;
-    static constexpr int LOAD_WG = NT == 2 ? 1 : 2; // load warpgroups
+    static constexpr int LOAD_WARPS = 12 - 4 * NT;
     static constexpr int STAGE = 2 * 128 * 128;    // bytes of a K or V tile
     // e4m3: RAW tiles of K or V as they are stored, and their scales, wait in
     // shared memory to be converted
@@ -422,8 +451,6 @@ struct HeadGeo {
     static constexpr int BARS = 2 * STAGES;
     static constexpr int RAW_AT = STAGES * STAGE, RAW_STAGE = STAGE / 2 + 512;
     static constexpr int RING = RAW_AT + RAW * RAW_STAGE;
-    static constexpr int REG_SOFTMAX = NT == 2 ? 168 : 200;
-    static constexpr int REG_LOAD = 120;
     // columns of tensor memory: S (and P over it) per tile or per buffer, O
     static constexpr int S_COL(int i) { return i * 128; }
     static constexpr int O_COL(int t) { return 256 + t * 128; }
@@ -441,13 +468,11 @@ struct MlaGeo {
     static constexpr int NT = 1, KT = 64;
     static constexpr int QPANELS = 5, OC = 256;
     static constexpr int DV = 512;
-    static constexpr int LOAD_WG = 2;
+    static constexpr int LOAD_WARPS = 8;
     static constexpr int PANEL = 64 * 128;
     static constexpr int OTHER = 5 * PANEL, OWN = 4 * PANEL; // bytes of a tile's parts
     static constexpr int BARS = 8; // full, empty of two stages of two parts
     static constexpr int RING = 2 * (OTHER + OWN);
-    static constexpr int REG_SOFTMAX = 200;
-    static constexpr int REG_LOAD = 120;
     static constexpr int S_COL(int i) { return 256 + i * 64; }
     static constexpr int O_COL(int) { return 0; }
     static constexpr int Q_COL = 384;
@@ -568,22 +593,24 @@ __device__ __forceinline__ bool seq_keys(const AttnParams &p, int s, int &len)
     return len >= 0 && len <= p.max_kv_len && (int64_t)len <= (int64_t)p.max_blocks * p.block;
 }
 
-// Row tile `tile` of the call -> sequence and row tile within it: one warp
-// counts the sequences' tiles 32 at a time.  Returns false past the last tile;
-// `bad`: some sequence's offsets do not fit.
+// Row tile `tile` of the call -> sequence, its queries and keys, and the row tile
+// within it: one warp counts the sequences' tiles 32 at a time.  Returns false past
+// the last tile or for a sequence whose keys do not fit; `bad`: some sequence's
+// offsets, or this one's keys, do not fit what the call stated.
 template <int ROWS>
-__device__ __forceinline__ bool find_tile(const AttnParams &p, int tile, int lane, int &seq, int &at,
+__device__ __forceinline__ bool find_tile(const AttnParams &p, int tile, int lane, Work &w, int &at,
                                           bool &bad)
 {
     int before = 0;
-    bad = false;
-    bool found = false;
+    bool found = false, wrong = false, keys = false;
     for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-        int n = 0, tiles = 0;
-        int64_t q0;
+        int n = 0, tiles = 0, len = 0;
+        int64_t q0 = 0;
+        bool fits = false;
         if (s0 + lane < p.num_seqs) {
+            fits = seq_keys(p, s0 + lane, len);
             if (!seq_queries(p, s0 + lane, q0, n))
-                bad = true;
+                wrong = true;
             tiles = (n * p.group + ROWS - 1) / ROWS;
         }
         int sum = tiles;
@@ -597,7 +624,11 @@ __device__ __forceinline__ bool find_tile(const AttnParams &p, int tile, int lan
         const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine);
         if (who) {
             const int l = __ffs((int)who) - 1;
-            seq = s0 + l;
+            w.seq = s0 + l;
+            w.n = __shfl_sync(0xFFFFFFFFu, n, l);
+            w.len = __shfl_sync(0xFFFFFFFFu, len, l);
+            w.q0 = __shfl_sync(0xFFFFFFFFu, q0, l);
+            keys = __shfl_sync(0xFFFFFFFFu, (int)fits, l) != 0;
             // the last tiles of a causal chunk see the most keys: first
             const int t = __shfl_sync(0xFFFFFFFFu, tiles, l), e = __shfl_sync(0xFFFFFFFFu, sum, l);
             at = t - 1 - (tile - (before + e - t));
@@ -605,8 +636,8 @@ __device__ __forceinline__ bool find_tile(const AttnParams &p, int tile, int lan
         }
         before += __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
-    bad = __any_sync(0xFFFFFFFFu, bad);
-    return found;
+    bad = __any_sync(0xFFFFFFFFu, wrong) || (found && !keys);
+    return found && keys;
 }
 
 __device__ __forceinline__ bool key_seen(const Work &w, int k)
@@ -640,23 +671,38 @@ __device__ __forceinline__ int64_t key_slot(const AttnParams &p, const Work &w, 
 // Load roles
 // ---------------------------------------------------------------------------
 
-// Query rows of one tile into their panels; rows past the end are zeros.
+// Query rows of row tile t into their panels, by the tile's 128 softmax threads; rows
+// past the end are zeros.  A group of threads takes whole panels of a row, then the
+// row `step` further on, so one division finds token and head of the first.
 template <class G>
 __device__ __forceinline__ void load_queries(const AttnParams &p, const Work &w, uint32_t q_smem,
-                                             int tid, int threads)
+                                             int t, int tid)
 {
-    constexpr int PIECES = G::QPANELS * 8;
-    for (int i = tid; i < G::NT * kRows * PIECES; i += threads) {
-        const int r = i / PIECES, c = i - r * PIECES;
-        const int row = w.row0 + r, tok = row / p.group, g = row - tok * p.group;
-        const bool ok = tok < w.n;
+    constexpr int LANES = G::MLA ? 8 : 16, step = 128 / LANES;
+    const int c = tid & (LANES - 1);
+    const int row = w.row0 + t * kRows + tid / LANES;
+    int tok = row / p.group, g = row - tok * p.group;
+    const int dt = step / p.group, dg = step - dt * p.group;
+    const uint32_t dst = q_smem + ((t * G::QPANELS + (c >> 3)) << 14);
+    for (int rr = tid / LANES; rr < kRows; rr += step) {
+        const uint32_t n = tok < w.n ? 16u : 0u;
         const int h = G::MLA ? g : w.head * p.group + g;
-        // MLA: the other half's panels, then k_pe's
-        const int col = !G::MLA ? c : c < 32 ? (1 - w.head) * 32 + c : c + 32;
-        const char *src = p.q + (ok ? (w.q0 + tok) * p.q_ts + h * p.q_hs : 0) + col * 16;
-        const int t = r >> 7, rr = r & 127;
-        copy16(q_smem + ((t * G::QPANELS + (c >> 3)) << 14) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
-               src, ok ? 16u : 0u);
+        const char *src = p.q + (n ? (w.q0 + tok) * p.q_ts + h * p.q_hs : 0) + c * 16;
+        const uint32_t to = dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
+        if constexpr (G::MLA) { // the other half's panels, then k_pe's
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                copy16(to + (i << 14), src + (1 - w.head) * 512 + i * 128, n);
+            copy16(to + (4 << 14), src + 1024, n);
+        } else {
+            copy16(to, src, n);
+        }
+        tok += dt;
+        g += dg;
+        if (g >= p.group) {
+            g -= p.group;
+            ++tok;
+        }
     }
 }
 
@@ -689,6 +735,40 @@ struct Flights {
     }
 };
 
+// Stages filled by cp.async: their threads wait for the copies, make them visible to
+// the MMAs and signal, one stage behind the one that they are filling.
+struct Copies {
+    uint32_t full = 0; // barrier of the stage that is not signalled yet
+
+    __device__ void flush()
+    {
+        if (full) {
+            copy_wait<0>();
+            async_fence();
+            bar_signal(full);
+            full = 0;
+        }
+    }
+
+    __device__ void filled(uint32_t bar)
+    {
+        copy_commit();
+        if (full) {
+            copy_wait<1>();
+            async_fence();
+            bar_signal(full);
+        }
+        full = bar;
+    }
+
+    // before a wait for a stage: nobody waits for this one meanwhile
+    __device__ void before_wait(uint32_t empty, uint32_t parity)
+    {
+        if (full && !__all_sync(0xFFFFFFFFu, bar_try(empty, parity)))
+            flush();
+    }
+};
+
 // Head rows into the ring as they are stored.  Whole tiles are boxes of the
 // tensor maps that one warp asks for (a box is at most a block of the pool); tiles
 // that hold keys nobody sees, and pools whose blocks do not divide a tile, are
@@ -701,7 +781,7 @@ __device__ __forceinline__ void load_heads(const AttnParams &p, const Work &w, u
                                                 uint32_t bars, int warp, int lane,
                                                 volatile int *abort, bool &bad)
 {
-    constexpr int WARPS = G::LOAD_WG * 4, ROWS = G::KT / WARPS; // rows of a warp: 32 or 16
+    constexpr int WARPS = G::LOAD_WARPS, ROWS = G::KT / WARPS; // rows of a warp: 32 or 16
     const int base = warp * ROWS;
     constexpr int PIECES = G::STAGE / G::KT / 16, PER = 32 / PIECES; // of a row; rows at a time
     const int c = lane & (PIECES - 1), sub = lane / PIECES;
@@ -713,6 +793,7 @@ __device__ __forceinline__ void load_heads(const AttnParams &p, const Work &w, u
     };
     int32_t next = w.beg < w.end ? key_block(p, w, key_at(w.beg)) : 0;
     Flights fly;
+    Copies copies;
     int stage = 0, phase = 1;
     bool ok = true;
     for (int v = w.beg; ok && v < w.end; ++v) {
@@ -725,11 +806,13 @@ __device__ __forceinline__ void load_heads(const AttnParams &p, const Work &w, u
 #pragma unroll
         for (int part = 0; part < 2; ++part) { // K, then V
             const uint32_t full = bars + stage * 8, dst = ring + stage * G::STAGE;
+            copies.before_wait(full + G::STAGES * 8, phase);
             ok = bar_wait(full + G::STAGES * 8, phase, abort, p.wait_limit_ns);
             if (!ok)
                 break;
             fly.filled(stage, boxes, phase ^ 1);
             if (boxes) {
+                copies.flush();
                 __syncwarp();
                 if (lane == 0)
                     bar_signal_bulk(full, 32, warp == 0 ? G::STAGE : 0);
@@ -754,7 +837,7 @@ __device__ __forceinline__ void load_heads(const AttnParams &p, const Work &w, u
                     copy16(dst + ((c >> 3) << 14) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
                            col + (s < 0 ? 0 : s * ss), s < 0 ? 0u : 16u);
                 }
-                bar_signal_copies(full);
+                copies.filled(full);
             }
             if (++stage == G::STAGES) {
                 stage = 0;
@@ -762,6 +845,7 @@ __device__ __forceinline__ void load_heads(const AttnParams &p, const Work &w, u
             }
         }
     }
+    copies.flush();
     if (warp == 0)
         fly.land(bars);
 }
@@ -774,7 +858,7 @@ __device__ __forceinline__ void load_heads_e4m3(const AttnParams &p, const Work 
                                                 uint32_t bars, int warp, int lane,
                                                 volatile int *abort, bool &bad)
 {
-    constexpr int WARPS = G::LOAD_WG * 4, ROWS = G::KT / WARPS, IT = ROWS / 4;
+    constexpr int WARPS = G::LOAD_WARPS, ROWS = G::KT / WARPS, IT = ROWS / 4;
     const int base = warp * ROWS, own = lane & (ROWS - 1);
     const int c = lane & 7, sub = lane >> 3;
     const uint32_t raw = ring + G::RAW_AT;
@@ -884,6 +968,7 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
                                               uint32_t bars, int warp, int lane,
                                               volatile int *abort, bool &bad)
 {
+    constexpr int AHEAD = 3;
     const int base = warp * 8, c = lane & 7, sub = lane >> 3;
     auto whole = [&](int v) { return p.box_rows > 0 && tile_whole<G::KT>(w, real_tile(w, v)); };
     auto key_at = [&](int v) {
@@ -892,6 +977,7 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
     };
     int32_t next = w.beg < w.end ? key_block(p, w, key_at(w.beg)) : 0;
     Flights fly;
+    Copies copies;
     bool ok = true;
     for (int v = w.beg; ok && v < w.end; ++v) {
         const int64_t slot = key_slot(p, w, key_at(v), next, bad);
@@ -900,15 +986,30 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
         const bool boxes = whole(v);
         const int row0 = (int)(slot < 0 ? p.num_blocks * p.block : slot);
         const int ord = v - w.beg, stage = ord & 1, phase = ((ord >> 1) & 1) ^ 1;
+        // a tile's copies are asked for little more than a tile ahead, less than HBM
+        // takes: another warp brings this half's columns to L2 before
+        if (warp == 1 && v + AHEAD < w.end && whole(v + AHEAD) && lane * p.box_rows < G::KT) {
+            const int k = key_at(v + AHEAD);
+            const int64_t at = key_slot(p, w, k, key_block(p, w, k), bad);
+            if (at >= 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    prefetch_box(&p.copy_map, w.head * 256 + i * 64, (int)at);
+                if (w.head == 0)
+                    prefetch_box(&p.rot_map, 0, (int)at);
+            }
+        }
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
             const uint32_t full = bars + (part * 2 + stage) * 8, dst = G::part(ring, part, stage);
             const int half = part == 0 ? 1 - w.head : w.head;
+            copies.before_wait(full + 4 * 8, phase);
             ok = bar_wait(full + 4 * 8, phase, abort, p.wait_limit_ns);
             if (!ok)
                 break;
             fly.filled(part * 2 + stage, boxes, phase ^ 1);
             if (boxes) {
+                copies.flush();
                 __syncwarp();
                 if (lane == 0)
                     bar_signal_bulk(full, 32, warp != 0 ? 0 : part == 0 ? G::OTHER : G::OWN);
@@ -935,10 +1036,11 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
                     if (part == 0)
                         copy16(at + 4 * G::PANEL, p.rot + (s < 0 ? 0 : s * p.rot_ss) + c * 16, n);
                 }
-                bar_signal_copies(full);
+                copies.filled(full);
             }
         }
     }
+    copies.flush();
     if (warp == 0)
         fly.land(bars);
 }
@@ -1057,11 +1159,12 @@ __device__ __forceinline__ void issue_values(uint32_t d, uint32_t pt, uint32_t v
 }
 
 template <class G>
-__device__ __forceinline__ bool run_mma_heads2(const AttnParams &p, const Work &w,
-                                               const TileMask (&mask)[2], uint32_t tmem,
-                                               uint32_t q_smem, uint32_t ring, uint32_t bars,
-                                               uint32_t lead, volatile int *abort)
+__device__ __forceinline__ bool run_mma_two(const AttnParams &p, const Work &w, uint32_t tmem,
+                                            uint32_t q_smem, uint32_t ring, uint32_t bars,
+                                            uint32_t lead, volatile int *abort)
 {
+    const TileMask mask[2] = {tile_mask(p, w.n, w.len, w.row0),
+                              tile_mask(p, w.n, w.len, w.row0 + kRows)};
     const uint32_t full = bars + kBarRing * 8, empty = full + G::STAGES * 8;
     bool pend[2] = {false, false}, begun[2] = {false, false};
     uint32_t pphase[2] = {0, 0};
@@ -1083,7 +1186,6 @@ __device__ __forceinline__ bool run_mma_heads2(const AttnParams &p, const Work &
         const int kt = real_tile(w, v);
         if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
             return false;
-        async_fence();
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             if (pend[t] && !values(t))
@@ -1106,7 +1208,6 @@ __device__ __forceinline__ bool run_mma_heads2(const AttnParams &p, const Work &
         vstage = stage;
         if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
             return false;
-        async_fence();
         v_open = true;
         if (++stage == G::STAGES) {
             stage = 0;
@@ -1138,12 +1239,10 @@ __device__ __forceinline__ bool run_mma_one(const AttnParams &p, const Work &w, 
             if constexpr (G::MLA) {
                 if (!bar_wait(full + i * 8, turn, abort, p.wait_limit_ns))
                     return false;
-                async_fence();
                 issue_scores<64, G::PANEL, 5>(s_col, q_smem, G::part(ring, 0, i), true, lead);
                 bar_signal_mma(full + (4 + i) * 8, lead);
                 if (!bar_wait(full + (2 + i) * 8, turn, abort, p.wait_limit_ns))
                     return false;
-                async_fence();
                 const uint32_t k = operand(G::part(ring, 1, i), 16);
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
@@ -1153,7 +1252,6 @@ __device__ __forceinline__ bool run_mma_one(const AttnParams &p, const Work &w, 
             } else {
                 if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
                     return false;
-                async_fence();
                 issue_scores<128, 16384, 2>(s_col, q_smem, ring + stage * G::STAGE, true, lead);
                 bar_signal_mma(bars + (kBarS + i) * 8, lead);
                 bar_signal_mma(full + (G::STAGES + stage) * 8, lead);
@@ -1184,7 +1282,6 @@ __device__ __forceinline__ bool run_mma_one(const AttnParams &p, const Work &w, 
                 vstage = stage;
                 if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
                     return false;
-                async_fence();
                 if (++stage == G::STAGES) {
                     stage = 0;
                     phase ^= 1;
@@ -1224,6 +1321,32 @@ __device__ __forceinline__ float nonfinite_value(const AttnParams &p, int64_t s,
     return (b & 0x7F80u) == 0x7F80u ? __uint_as_float(b << 16) : 0.0f;
 }
 
+// MLA: the query panels of this half into tensor memory, a row to a lane.
+template <class G>
+__device__ __forceinline__ void queries_to_tmem(const AttnParams &p, const Work &w, uint32_t tmem,
+                                                int warp, int lane, int rows)
+{
+    const int r = warp * 32 + lane, row = w.row0 + r, tok = row / p.group;
+    const bool valid = r < rows;
+    const char *src =
+        p.q + (valid ? (w.q0 + tok) * p.q_ts + (row - tok * p.group) * p.q_hs : 0) + w.head * 512;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        uint32_t x[32];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint4 y = valid ? __ldg(reinterpret_cast<const uint4 *>(src + i * 128) + j)
+                                  : make_uint4(0, 0, 0, 0);
+            x[4 * j] = y.x;
+            x[4 * j + 1] = y.y;
+            x[4 * j + 2] = y.z;
+            x[4 * j + 3] = y.w;
+        }
+        tmem_st32(tmem + G::Q_COL + i * 32 + ((uint32_t)(warp * 32) << 16), x);
+    }
+    tmem_st_wait();
+}
+
 template <class G>
 __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, const TileMask &m,
                                             int t, uint32_t tmem, uint32_t ring, uint32_t bars,
@@ -1243,26 +1366,6 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
     const int sk = p.window ? min(p.sinks, hi) : 0;
     const bool one_token = G::NT == 1 && m.pos0 == m.pos1;
     const float c = p.scale * 1.4426950408889634f;
-    if constexpr (G::MLA) { // the query panels of this half, a row to a lane
-        const char *src = p.q + (valid ? (w.q0 + tok) * p.q_ts + g * p.q_hs : 0) + w.head * 512;
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            uint32_t x[32];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint4 y = valid ? __ldg(reinterpret_cast<const uint4 *>(src + i * 128) + j)
-                                      : make_uint4(0, 0, 0, 0);
-                x[4 * j] = y.x;
-                x[4 * j + 1] = y.y;
-                x[4 * j + 2] = y.z;
-                x[4 * j + 3] = y.w;
-            }
-            tmem_st32(tmem + G::Q_COL + i * 32 + lanes, x);
-        }
-        tmem_st_wait();
-        mma_fence_before();
-        bar_signal(bars + kBarQ * 8);
-    }
     RowState st;
     int done = 0; // tiles of this row tile so far
     for (int v = w.beg; v < w.end; ++v) {
@@ -1275,35 +1378,40 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
         if (!bar_wait(bars + (kBarS + buf) * 8, parity, abort, p.wait_limit_ns))
             return false;
         mma_fence_after();
-        uint32_t s[KT];
-#pragma unroll
-        for (int i = 0; i < KT; i += 32)
-            tmem_ld32(s_col + i, s + i);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < KT; i += 32)
-            tmem_pin32(s + i);
         const bool full = tile_full<KT>(p, m, kt);
-        if (!full) {
+        // Two passes over the row in pieces of 32 scores, the next piece on its way
+        // while one is worked on: short loops stay in the instruction cache, which
+        // a row held in registers and unrolled did not.
+        uint32_t sa[32], sb[32];
+        auto mask = [&](uint32_t(&s)[32], int i) {
+            const int k0 = kt * KT + i; // a bit per key that is seen
+            const uint32_t see = below(hi - k0) & (~below(lo - k0) | below(sk - k0));
 #pragma unroll
-            for (int i = 0; i < KT; i += 32) { // a bit per key that is seen
-                const int k0 = kt * KT + i;
-                const uint32_t see = below(hi - k0) & (~below(lo - k0) | below(sk - k0));
+            for (int j = 0; j < 32; ++j)
+                s[j] = (see >> j) & 1u ? s[j] : 0xFF800000u;
+        };
+        float t4[4] = {st.top, -INFINITY, -INFINITY, -INFINITY}; // chains of maxima
+        auto take_max = [&](uint32_t(&s)[32], int i) {
+            if (!full)
+                mask(s, i);
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    s[i + j] = (see >> j) & 1u ? s[i + j] : 0xFF800000u;
-            }
+            for (int j = 0; j < 16; ++j)
+                t4[j & 3] = max3(t4[j & 3], __uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+        };
+        tmem_ld32(s_col, sa);
+#pragma unroll 1
+        for (int i = 0; i < KT; i += 64) {
+            tmem_ld_wait();
+            tmem_pin32(sa);
+            tmem_ld32(s_col + i + 32, sb);
+            take_max(sa, i);
+            tmem_ld_wait();
+            tmem_pin32(sb);
+            if (i + 64 < KT)
+                tmem_ld32(s_col + i + 64, sa);
+            take_max(sb, i + 32);
         }
-        float t4[4]; // four chains: the maximum's latency, not its count, is what costs
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            t4[i] = fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 4]));
-#pragma unroll
-        for (int i = 8; i < KT; i += 8)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                t4[j] = fmaxf(t4[j], fmaxf(__uint_as_float(s[i + j]), __uint_as_float(s[i + j + 4])));
-        const float top = fmaxf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), st.top);
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         const bool grew = (top - st.top) * c > kLazy; // also from -inf
         if (done == 0) {
             st.top = top;
@@ -1331,16 +1439,18 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
                 tmem_st32(tmem + G::O_COL(t) + lanes + i, o);
             }
         }
+        tmem_ld32(s_col, sa); // the second pass begins
         const float off = st.top == -INFINITY ? 0.0f : -st.top * c;
         const f2 c2 = f2_of_bits(__float_as_uint(c), __float_as_uint(c));
         const f2 off2 = f2_of_bits(__float_as_uint(off), __float_as_uint(off));
         f2 sum2[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int i = 0; i < KT; i += 32) {
+        auto take_weights = [&](uint32_t(&s)[32], int i) {
+            if (!full)
+                mask(s, i);
             uint32_t w16[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const f2 x = f2_fma(f2_of_bits(s[i + 2 * j], s[i + 2 * j + 1]), c2, off2);
+                const f2 x = f2_fma(f2_of_bits(s[2 * j], s[2 * j + 1]), c2, off2);
                 float a, b;
                 asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
                 a = exp2_fast(a);
@@ -1348,13 +1458,25 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
                 sum2[j & 3] = f2_add(sum2[j & 3], f2_of_bits(__float_as_uint(a), __float_as_uint(b)));
                 w16[j] = pack_bf16(a, b);
             }
-            tmem_st16(s_col + i / 2, w16);
+            tmem_st16(s_col + i / 2, w16); // over scores that have been read
+        };
+#pragma unroll 1
+        for (int i = 0; i < KT; i += 64) {
+            tmem_ld_wait();
+            tmem_pin32(sa);
+            tmem_ld32(s_col + i + 32, sb);
+            take_weights(sa, i);
+            tmem_ld_wait();
+            tmem_pin32(sb);
+            if (i + 64 < KT)
+                tmem_ld32(s_col + i + 64, sa);
+            take_weights(sb, i + 32);
         }
-        float sa, sb;
+        float s0, s1;
         asm("mov.b64 {%0, %1}, %2;"
-            : "=f"(sa), "=f"(sb)
+            : "=f"(s0), "=f"(s1)
             : "l"(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]))));
-        st.sum += sa + sb;
+        st.sum += s0 + s1;
         tmem_st_wait();
         if (!full && !one_token) {
             // A weight of 0 does not keep an infinite or NaN value out of the
@@ -1421,6 +1543,7 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
             p.lse[at] = lse;
     }
     char *out = p.out + (w.q0 + tok) * p.o_ts + h * p.o_hs + col0 * 2;
+    const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0; // a row's sectors are whole
     float *part = p.part + (w.split * p.total_q * p.heads + at) * G::DV + col0;
 #pragma unroll 1
     for (int i = 0; i < G::OC; i += 32) {
@@ -1452,15 +1575,24 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
             continue;
         if (parts) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<float4 *>(part + i + j) =
-                    make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
-        } else {
+            for (int j = 0; j < 32; ++j)
+                o[j] = __float_as_uint(f[j]);
 #pragma unroll
             for (int j = 0; j < 32; j += 8)
-                *reinterpret_cast<uint4 *>(out + (i + j) * 2) =
-                    make_uint4(pack_bf16(f[j], f[j + 1]), pack_bf16(f[j + 2], f[j + 3]),
-                               pack_bf16(f[j + 4], f[j + 5]), pack_bf16(f[j + 6], f[j + 7]));
+                st32(part + i + j, o + j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                o[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+            if (wide) {
+                st32(out + i * 2, o);
+                st32(out + i * 2 + 32, o + 8);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; j += 4)
+                    *reinterpret_cast<uint4 *>(out + i * 2 + j * 4) =
+                        make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            }
         }
     }
     return true;
@@ -1480,7 +1612,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
     __shared__ uint32_t s_tmem, s_status;
     __shared__ int s_go;
     __shared__ volatile int s_abort, s_dirty;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
     const uint32_t q_smem = smem + S::Q, ring = smem + S::RING, bars = smem + S::BAR;
 
@@ -1489,21 +1621,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
         // its halves are neighbours, so their rows meet in L2
         const int heads = G::MLA ? 2 : p.heads / p.group;
         uint32_t x = blockIdx.x;
-        Work w;
+        Work w{};
         w.head = (int)(x % heads);
         x /= heads;
         w.split = (int)(x % p.max_splits);
-        int seq = 0, at = 0;
+        int at = 0;
         bool bad = false;
-        bool go = find_tile<kRows * G::NT>(p, (int)(x / p.max_splits), lane, seq, at, bad);
-        w.seq = seq;
-        if (go) {
-            seq_queries(p, seq, w.q0, w.n);
-            if (!seq_keys(p, seq, w.len)) {
-                bad = true;
-                go = false;
-            }
-        }
+        bool go = find_tile<kRows * G::NT>(p, (int)(x / p.max_splits), lane, w, at, bad);
         if (go) {
             w.row0 = at * kRows * G::NT;
             const int nv = key_tiles<G::KT, G::NT>(p, w);
@@ -1518,41 +1642,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
             s_status = bad ? kStatusOutOfRange : kStatusOk;
             s_abort = 0;
             s_dirty = 0;
+            for (int i = 0; i < 2; ++i) { // the warps that have rows signal the weights
+                const int rows = tile_mask(p, w.n, w.len, w.row0 + (G::NT == 2 ? i : 0) * kRows).rows;
+                bar_init(bars + (kBarP + i) * 8, max(1, (rows + 31) / 32) * 32);
+            }
+            bar_init_fence();
         }
-    }
-    __syncthreads();
-    if (!s_go) {
-        if (tid == 0)
-            write_block_status(p.header, s_status, blockIdx.x, gridDim.x);
-        return;
-    }
-    const Work w = s_work;
-    TileMask mask[2];
-    mask[0] = tile_mask(p, w.n, w.len, w.row0);
-    mask[1] = tile_mask(p, w.n, w.len, w.row0 + kRows);
-    if (tid == 0) {
-        bar_init(bars + kBarQ * 8,
-                 G::LOAD_WG * 128 + (G::MLA ? (mask[0].rows + 31) / 32 * 32 : 0));
+    } else if (warp == 1 && lane == 0) {
+        bar_init(bars + kBarQ * 8, G::NT * 128);
         bar_init(bars + kBarDone * 8, 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(bars + (kBarS + i) * 8, 1);
-            const int rows = mask[G::NT == 2 ? i : 0].rows;
-            bar_init(bars + (kBarP + i) * 8, max(1, (rows + 31) / 32) * 32);
+            bar_init(bars + (kBarO + i) * 8, 1); // the second: drain
         }
-        bar_init(bars + kBarO * 8, 1);
-        bar_init(bars + (kBarO + 1) * 8, 1); // drain
         for (int i = 0; i < G::BARS / 2; ++i) {
-            bar_init(bars + (kBarRing + i) * 8, G::LOAD_WG * 128);
+            bar_init(bars + (kBarRing + i) * 8, G::LOAD_WARPS * 32);
             bar_init(bars + (kBarRing + G::BARS / 2 + i) * 8, 1);
         }
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == 12) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(&s_tmem)),
-                     "r"(512u)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        bar_init_fence();
+    } else if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(&s_tmem), 512);
     }
     mma_fence_before();
     __syncthreads();
@@ -1560,16 +1669,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = s_tmem;
 
-    if (wg < G::NT) {
-        reg_inc<G::REG_SOFTMAX>();
-        const int t = wg, wl = warp & 3, warps = (mask[t].rows + 31) / 32;
+    if (!s_go) {
+        // nothing for this block
+    } else if (warp < G::NT * 4) {
+        const Work w = s_work;
+        const int t = warp >> 2;
+        const TileMask mask = tile_mask(p, w.n, w.len, w.row0 + t * kRows);
+        const int wl = warp & 3, warps = (mask.rows + 31) / 32;
+        load_queries<G>(p, w, q_smem, t, tid & 127);
+        if constexpr (G::MLA)
+            queries_to_tmem<G>(p, w, tmem, wl, lane, mask.rows);
+        copy_commit();
+        copy_wait<0>();
+        async_fence();
+        mma_fence_before();
+        bar_signal(bars + kBarQ * 8);
         if (wl < warps)
-            run_softmax<G>(p, w, mask[t], t, tmem, ring, bars, wl, lane, warps, &s_abort, &s_dirty);
-    } else if (wg < G::NT + G::LOAD_WG) {
-        reg_dec<G::REG_LOAD>();
-        const int lt = tid - G::NT * 128, lw = lt >> 5;
-        load_queries<G>(p, w, q_smem, lt, G::LOAD_WG * 128);
-        bar_signal_copies(bars + kBarQ * 8);
+            run_softmax<G>(p, w, mask, t, tmem, ring, bars, wl, lane, warps, &s_abort, &s_dirty);
+    } else if (warp < kMmaWarp) {
+        const Work w = s_work;
+        const int lw = warp - G::NT * 4;
         bool bad = false;
         if constexpr (G::MLA && G::QUANT)
             load_mla_e4m3<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
@@ -1583,30 +1702,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
             s_status = kStatusOutOfRange;
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
-        reg_dec<kRegMma>();
-        if (warp == 12) {
-            const uint32_t lead = elect_lane();
-            bool ok = bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
-            if (ok) {
-                async_fence();
-                mma_fence_after();
-                if constexpr (G::NT == 2)
-                    ok = run_mma_heads2<G>(p, w, mask, tmem, q_smem, ring, bars, lead, &s_abort);
-                else
-                    ok = run_mma_one<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
-            }
-            if (!ok) { // let what was issued finish before tensor memory goes
-                int none = 0;
-                bar_signal_mma(bars + (kBarO + 1) * 8, lead);
-                bar_wait(bars + (kBarO + 1) * 8, 0, &none, 1000000000ll);
-            }
+        const Work w = s_work;
+        const uint32_t lead = elect_lane();
+        bool ok = bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
+        if (ok) {
+            mma_fence_after();
+            if constexpr (G::NT == 2)
+                ok = run_mma_two<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
+            else
+                ok = run_mma_one<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
+        }
+        if (!ok) { // let what was issued finish before tensor memory goes
+            int none = 0;
+            bar_signal_mma(bars + (kBarO + 1) * 8, lead);
+            bar_wait(bars + (kBarO + 1) * 8, 0, &none, 1000000000ll);
         }
     }
     mma_fence_before();
     __syncthreads();
     mma_fence_after();
-    if (warp == 12)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+    if (warp == kMmaWarp)
+        tmem_free(tmem, 512);
     if (tid == 0)
         write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, gridDim.x);
 }
@@ -1641,7 +1757,7 @@ struct FewGeo {
     static constexpr int N = QUANT ? 2 * R : 16;    // rows of the MMAs
     static constexpr int NT = 1, KT = 128;
     static constexpr int DV = 128;
-    static constexpr int LOAD_WG = 1;
+    static constexpr int LOAD_WARPS = 4;
     static constexpr int STAGE = (QUANT ? 1 : 2) * 128 * 128, STAGES = QUANT ? 6 : 3;
     static constexpr int RING = STAGES * STAGE;
     // a key's weights: N values of 1 or 2 bytes
@@ -1921,7 +2037,6 @@ __device__ __forceinline__ bool few_mma(const AttnParams &p, const Work &w, uint
         if (more) {
             if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
                 return false;
-            async_fence();
             const uint32_t k = operand(smem + stage * G::STAGE, 16);
             if constexpr (G::QUANT) {
 #pragma unroll
@@ -1965,7 +2080,6 @@ __device__ __forceinline__ bool few_mma(const AttnParams &p, const Work &w, uint
             vstage = stage;
             if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
                 return false;
-            async_fence();
             next();
         }
     }
@@ -2070,15 +2184,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
             bar_init(bars + (kBarRing + i) * 8, 128);
             bar_init(bars + (kBarRing + G::STAGES + i) * 8, 1);
         }
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        bar_init_fence();
     }
-    if (warp == 8) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(&s_tmem)),
-                     "r"((uint32_t)G::COLS)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    if (warp == 8)
+        tmem_alloc(smem_u32(&s_tmem), G::COLS);
     mma_fence_before();
     __syncthreads();
     mma_fence_after();
@@ -2129,8 +2238,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
     __syncthreads();
     mma_fence_after();
     if (warp == 8)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"((uint32_t)G::COLS));
+        tmem_free(tmem, G::COLS);
     if (tid == 0)
         write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, gridDim.x);
 }
@@ -2272,13 +2380,6 @@ cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess)
         return e;
-    // the register shares of the warpgroups come out of what a block starts with
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, attention_kernel<G>)) != cudaSuccess)
-        return e;
-    if (G::NT * G::REG_SOFTMAX + G::LOAD_WG * G::REG_LOAD + (4 - G::NT - G::LOAD_WG) * kRegMma >
-        4 * fa.numRegs)
-        return cudaErrorInvalidConfiguration;
     attention_kernel<G><<<(unsigned)blocks, kAttnThreads, bytes, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
