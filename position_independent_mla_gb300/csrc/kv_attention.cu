@@ -14,10 +14,13 @@
 // new token over 8 key heads read each key once, and a chunk of many tokens
 // fills whole tiles.
 //
-// Roles of a block's 13 warps:
-//   softmax  4 a row tile, a thread per row: reads its row of S from tensor memory,
-//            masks, keeps m and l in registers, writes the bf16 weights back over
-//            S (they are the A operand of the second MMA) and at the end O / l;
+// Roles of a block's warps:
+//   softmax  8 a row tile, two threads to a row, one for each half of its keys: read
+//            the row of S from tensor memory, mask, keep m and l in registers,
+//            write the bf16 weights back over S (they are the A operand of the
+//            second MMA) and at the end O / l.  The two exchange their maxima for
+//            every tile through shared memory: a row's chain of 128 exponentials
+//            in one thread was what the MMAs waited for;
 //   load     bring rows of the pool through the block table into shared memory
 //            in the 128-byte swizzled layout that the MMAs read;
 //   mma      one warp issues every MMA.
@@ -31,6 +34,7 @@
 //
 // Every wait is bounded; a block whose wait runs out reports KV_ERR_TIMEOUT.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include <cudaTypedefs.h>
@@ -44,8 +48,6 @@ namespace kvr {
 namespace {
 
 constexpr int kRows = 128;         // rows per tile: the M of an MMA
-constexpr int kAttnThreads = 416;  // 13 warps, the last of them issues the MMAs
-constexpr int kMmaWarp = 12;
 constexpr float kLazy = 8.0f;      // log2 of the growth of a maximum that O tolerates
 
 // ---------------------------------------------------------------------------
@@ -442,12 +444,12 @@ struct HeadGeo {
     static constexpr int NT = NT_, KT = 128;
     static constexpr int QPANELS = 2, OC = 128;    // query panels in shared memory; columns of O
     static constexpr int DV = 128;
-    static constexpr int LOAD_WARPS = 12 - 4 * NT;
+    static constexpr int SOFT_WARPS = 8 * NT, LOAD_WARPS = NT == 2 ? 4 : 8;
     static constexpr int STAGE = 2 * 128 * 128;    // bytes of a K or V tile
     // e4m3: RAW tiles of K or V as they are stored, and their scales, wait in
     // shared memory to be converted
     static constexpr int RAW = !QUANT ? 0 : NT == 2 ? 3 : 5;
-    static constexpr int STAGES = QUANT ? (NT == 2 ? 3 : 3) : NT == 2 ? 5 : 6;
+    static constexpr int STAGES = QUANT ? 3 : NT == 2 ? 4 : 5;
     static constexpr int BARS = 2 * STAGES;
     static constexpr int RAW_AT = STAGES * STAGE, RAW_STAGE = STAGE / 2 + 512;
     static constexpr int RING = RAW_AT + RAW * RAW_STAGE;
@@ -468,7 +470,7 @@ struct MlaGeo {
     static constexpr int NT = 1, KT = 64;
     static constexpr int QPANELS = 5, OC = 256;
     static constexpr int DV = 512;
-    static constexpr int LOAD_WARPS = 8;
+    static constexpr int SOFT_WARPS = 8, LOAD_WARPS = 8;
     static constexpr int PANEL = 64 * 128;
     static constexpr int OTHER = 5 * PANEL, OWN = 4 * PANEL; // bytes of a tile's parts
     static constexpr int BARS = 8; // full, empty of two stages of two parts
@@ -482,6 +484,12 @@ struct MlaGeo {
         return ring + (which == 0 ? i * OTHER : 2 * OTHER + i * OWN);
     }
 };
+
+template <class G>
+constexpr int kMmaWarp = G::SOFT_WARPS + G::LOAD_WARPS;
+
+template <class G>
+constexpr int kAttnThreads = (kMmaWarp<G> + 1) * 32;
 
 template <class G>
 struct Smem {
@@ -671,14 +679,14 @@ __device__ __forceinline__ int64_t key_slot(const AttnParams &p, const Work &w, 
 // Load roles
 // ---------------------------------------------------------------------------
 
-// Query rows of row tile t into their panels, by the tile's 128 softmax threads; rows
+// Query rows of row tile t into their panels, by the tile's 256 softmax threads; rows
 // past the end are zeros.  A group of threads takes whole panels of a row, then the
 // row `step` further on, so one division finds token and head of the first.
 template <class G>
 __device__ __forceinline__ void load_queries(const AttnParams &p, const Work &w, uint32_t q_smem,
                                              int t, int tid)
 {
-    constexpr int LANES = G::MLA ? 8 : 16, step = 128 / LANES;
+    constexpr int LANES = G::MLA ? 8 : 16, step = 256 / LANES;
     const int c = tid & (LANES - 1);
     const int row = w.row0 + t * kRows + tid / LANES;
     int tok = row / p.group, g = row - tok * p.group;
@@ -1147,7 +1155,8 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q, uint32_t k,
                         !(first && pn == 0 && kk == 0), lead);
 }
 
-// O += P V: P in tensor memory (two keys to a column), V in panels.
+// O += P V: P in tensor memory, two keys to a column, each half of the keys over its
+// half of S; V in panels.
 template <int N, int KT>
 __device__ __forceinline__ void issue_values(uint32_t d, uint32_t pt, uint32_t v, bool first,
                                              uint32_t lead)
@@ -1155,7 +1164,8 @@ __device__ __forceinline__ void issue_values(uint32_t d, uint32_t pt, uint32_t v
     const uint32_t b = operand(v, KT * 128);
 #pragma unroll
     for (int kk = 0; kk < KT / 16; ++kk)
-        mma_tmem<N, 1>(d, pt + kk * 8, b + kk * (2048 >> 4), !(first && kk == 0), lead);
+        mma_tmem<N, 1>(d, pt + (kk < KT / 32 ? kk * 8 : KT / 2 + (kk - KT / 32) * 8),
+                       b + kk * (2048 >> 4), !(first && kk == 0), lead);
 }
 
 template <class G>
@@ -1305,8 +1315,21 @@ __device__ __forceinline__ uint32_t below(int n)
 
 struct RowState {
     float top = -INFINITY; // maximum that the weights and O are taken against
-    float sum = 0.0f;
+    float sum = 0.0f;      // of this thread's half of the keys
 };
+
+// What the two threads of a row exchange, and a flag by which their warps give up
+// together: a warp whose wait ran out still comes to the next exchange.
+// The maxima alternate between two places from tile to tile; MLA, whose shared memory
+// is full, has one place and a second meeting after it was read.
+template <class G>
+struct RowPairs {
+    static constexpr int PLACES = G::MLA ? 1 : 2;
+    float max[PLACES][2][G::NT * kRows]; // [place][half][row]
+    volatile int failed[8];         // [pair of warps]
+};
+
+__device__ __forceinline__ void pair_sync(int pair) { bar_wait_all(1 + pair, 64); }
 
 // Value `col` of key slot `s` as an fp32 if it is not finite, else 0.
 template <class G>
@@ -1321,17 +1344,17 @@ __device__ __forceinline__ float nonfinite_value(const AttnParams &p, int64_t s,
     return (b & 0x7F80u) == 0x7F80u ? __uint_as_float(b << 16) : 0.0f;
 }
 
-// MLA: the query panels of this half into tensor memory, a row to a lane.
+// MLA: two of the query panels of this half into tensor memory, a row to a lane.
 template <class G>
 __device__ __forceinline__ void queries_to_tmem(const AttnParams &p, const Work &w, uint32_t tmem,
-                                                int warp, int lane, int rows)
+                                                int warp, int lane, int rows, int panel)
 {
     const int r = warp * 32 + lane, row = w.row0 + r, tok = row / p.group;
     const bool valid = r < rows;
     const char *src =
         p.q + (valid ? (w.q0 + tok) * p.q_ts + (row - tok * p.group) * p.q_hs : 0) + w.head * 512;
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
+    for (int i = panel; i < panel + 2; ++i) {
         uint32_t x[32];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -1347,14 +1370,18 @@ __device__ __forceinline__ void queries_to_tmem(const AttnParams &p, const Work 
     tmem_st_wait();
 }
 
+// `warp` (0..3) owns rows 32 * warp ..., `half` says which keys of a tile are this
+// thread's; `warps` of the four have rows.
 template <class G>
-__device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, const TileMask &m,
+__device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, const TileMask &m,
                                             int t, uint32_t tmem, uint32_t ring, uint32_t bars,
-                                            int warp, int lane, int warps, volatile int *abort,
-                                            volatile int *dirty)
+                                            int warp, int half, int lane, int warps,
+                                            volatile int *abort, volatile int *dirty,
+                                            RowPairs<G> &pairs)
 {
-    constexpr int KT = G::KT;
+    constexpr int KT = G::KT, HK = KT / 2, HO = G::OC / 2; // keys, columns of O of a thread
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const int pair = t * 4 + warp;
     const int r = warp * 32 + lane;
     const int row = w.row0 + t * kRows + r;
     const int tok = row / p.group, g = row - tok * p.group;
@@ -1366,88 +1393,91 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
     const int sk = p.window ? min(p.sinks, hi) : 0;
     const bool one_token = G::NT == 1 && m.pos0 == m.pos1;
     const float c = p.scale * 1.4426950408889634f;
+    const uint32_t o_col = tmem + G::O_COL(t) + half * HO + lanes;
     RowState st;
     int done = 0; // tiles of this row tile so far
+    bool ok = true;
     for (int v = w.beg; v < w.end; ++v) {
         const int kt = real_tile(w, v);
         if (G::NT == 2 && !tile_active<KT>(m, kt))
             continue;
         const int buf = G::NT == 2 ? t : (done & 1);
-        const uint32_t s_col = tmem + G::S_COL(buf) + lanes;
+        const uint32_t s_col = tmem + G::S_COL(buf) + half * HK + lanes;
         const uint32_t parity = G::NT == 2 ? (done & 1) : ((done >> 1) & 1);
-        if (!bar_wait(bars + (kBarS + buf) * 8, parity, abort, p.wait_limit_ns))
-            return false;
+        ok = ok && bar_wait(bars + (kBarS + buf) * 8, parity, abort, p.wait_limit_ns);
         mma_fence_after();
         const bool full = tile_full<KT>(p, m, kt);
-        // Two passes over the row in pieces of 32 scores, the next piece on its way
-        // while one is worked on: short loops stay in the instruction cache, which
-        // a row held in registers and unrolled did not.
-        uint32_t sa[32], sb[32];
+        // Two passes over the half row in pieces of 32 scores: short loops stay in the
+        // instruction cache, which a row held in registers and unrolled did not.
         auto mask = [&](uint32_t(&s)[32], int i) {
-            const int k0 = kt * KT + i; // a bit per key that is seen
+            const int k0 = kt * KT + half * HK + i; // a bit per key that is seen
             const uint32_t see = below(hi - k0) & (~below(lo - k0) | below(sk - k0));
 #pragma unroll
             for (int j = 0; j < 32; ++j)
                 s[j] = (see >> j) & 1u ? s[j] : 0xFF800000u;
         };
-        float t4[4] = {st.top, -INFINITY, -INFINITY, -INFINITY}; // chains of maxima
-        auto take_max = [&](uint32_t(&s)[32], int i) {
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}; // chains of maxima
+#pragma unroll 1
+        for (int i = 0; i < HK; i += 32) {
+            uint32_t s[32];
+            tmem_ld32(s_col + i, s);
+            tmem_ld_wait();
+            tmem_pin32(s);
             if (!full)
                 mask(s, i);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 t4[j & 3] = max3(t4[j & 3], __uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
-        };
-        tmem_ld32(s_col, sa);
-#pragma unroll 1
-        for (int i = 0; i < KT; i += 64) {
-            tmem_ld_wait();
-            tmem_pin32(sa);
-            tmem_ld32(s_col + i + 32, sb);
-            take_max(sa, i);
-            tmem_ld_wait();
-            tmem_pin32(sb);
-            if (i + 64 < KT)
-                tmem_ld32(s_col + i + 64, sa);
-            take_max(sb, i + 32);
         }
-        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        const int place = done % RowPairs<G>::PLACES;
+        pairs.max[place][half][t * kRows + r] = top;
+        if (!ok)
+            pairs.failed[pair] = 1;
+        pair_sync(pair);
+        if (pairs.failed[pair])
+            return;
+        top = max3(top, pairs.max[place][half ^ 1][t * kRows + r], st.top);
+        if (RowPairs<G>::PLACES == 1)
+            pair_sync(pair);
         const bool grew = (top - st.top) * c > kLazy; // also from -inf
         if (done == 0) {
             st.top = top;
         } else if (__any_sync(0xFFFFFFFFu, grew)) {
             // O of the tiles before is complete: NT = 2 issues it before these scores
-            if (G::NT == 1 &&
-                !bar_wait(bars + kBarO * 8, (done - 1) & 1, abort, p.wait_limit_ns))
-                return false;
-            if (G::NT == 1)
+            if (G::NT == 1) {
+                ok = bar_wait(bars + kBarO * 8, (done - 1) & 1, abort, p.wait_limit_ns);
                 mma_fence_after();
+            }
             const float f = grew ? exp2_fast((st.top - top) * c) : 1.0f;
             if (grew) {
                 st.top = top;
                 st.sum *= f;
             }
 #pragma unroll 1
-            for (int i = 0; i < G::OC; i += 32) {
+            for (int i = 0; i < HO; i += 32) {
                 uint32_t o[32];
-                tmem_ld32(tmem + G::O_COL(t) + lanes + i, o);
+                tmem_ld32(o_col + i, o);
                 tmem_ld_wait();
                 tmem_pin32(o);
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st32(tmem + G::O_COL(t) + lanes + i, o);
+                tmem_st32(o_col + i, o);
             }
         }
-        tmem_ld32(s_col, sa); // the second pass begins
         const float off = st.top == -INFINITY ? 0.0f : -st.top * c;
         const f2 c2 = f2_of_bits(__float_as_uint(c), __float_as_uint(c));
         const f2 off2 = f2_of_bits(__float_as_uint(off), __float_as_uint(off));
-        f2 sum2[4] = {0ull, 0ull, 0ull, 0ull};
-        auto take_weights = [&](uint32_t(&s)[32], int i) {
+        f2 sum2[2] = {0ull, 0ull};
+#pragma unroll 1
+        for (int i = 0; i < HK; i += 32) {
+            uint32_t s[32];
+            tmem_ld32(s_col + i, s);
+            tmem_ld_wait();
+            tmem_pin32(s);
             if (!full)
                 mask(s, i);
-            uint32_t w16[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const f2 x = f2_fma(f2_of_bits(s[2 * j], s[2 * j + 1]), c2, off2);
@@ -1455,27 +1485,13 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
                 asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
                 a = exp2_fast(a);
                 b = exp2_fast(b);
-                sum2[j & 3] = f2_add(sum2[j & 3], f2_of_bits(__float_as_uint(a), __float_as_uint(b)));
-                w16[j] = pack_bf16(a, b);
+                sum2[j & 1] = f2_add(sum2[j & 1], f2_of_bits(__float_as_uint(a), __float_as_uint(b)));
+                s[j] = pack_bf16(a, b);
             }
-            tmem_st16(s_col + i / 2, w16); // over scores that have been read
-        };
-#pragma unroll 1
-        for (int i = 0; i < KT; i += 64) {
-            tmem_ld_wait();
-            tmem_pin32(sa);
-            tmem_ld32(s_col + i + 32, sb);
-            take_weights(sa, i);
-            tmem_ld_wait();
-            tmem_pin32(sb);
-            if (i + 64 < KT)
-                tmem_ld32(s_col + i + 64, sa);
-            take_weights(sb, i + 32);
+            tmem_st16(s_col + i / 2, s); // over scores that have been read
         }
         float s0, s1;
-        asm("mov.b64 {%0, %1}, %2;"
-            : "=f"(s0), "=f"(s1)
-            : "l"(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]))));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(f2_add(sum2[0], sum2[1])));
         st.sum += s0 + s1;
         tmem_st_wait();
         if (!full && !one_token) {
@@ -1485,27 +1501,25 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
             const int ord = v - w.beg;
             uint32_t vbase;
             int pieces;
-            if (G::MLA) {
-                if (!bar_wait(bars + (kBarRing + 2 + (ord & 1)) * 8, (ord >> 1) & 1, abort,
-                              p.wait_limit_ns))
-                    return false;
-                vbase = MlaGeo<G::QUANT>::part(ring, 1, ord & 1);
-                pieces = MlaGeo<G::QUANT>::OWN / 16;
+            if constexpr (G::MLA) {
+                ok = ok && bar_wait(bars + (kBarRing + 2 + (ord & 1)) * 8, (ord >> 1) & 1, abort,
+                                    p.wait_limit_ns);
+                vbase = G::part(ring, 1, ord & 1);
+                pieces = G::OWN / 16;
             } else {
-                constexpr int ST = G::BARS / 2, BYTES = 2 * KT * 128;
-                const int item = 2 * ord + 1;
-                if (!bar_wait(bars + (kBarRing + item % ST) * 8, (item / ST) & 1, abort,
-                              p.wait_limit_ns))
-                    return false;
-                vbase = ring + (item % ST) * BYTES;
-                pieces = BYTES / 16;
+                const int item = 2 * ord + 1, at = item % G::STAGES;
+                ok = ok && bar_wait(bars + (kBarRing + at) * 8, (item / G::STAGES) & 1, abort,
+                                    p.wait_limit_ns);
+                vbase = ring + at * G::STAGE;
+                pieces = G::STAGE / 16;
             }
+            const int me = (half * warps + warp) * 32 + lane, all = warps * 64;
             uint32_t bad = 0;
-            for (int i = warp * 32 + lane; i < pieces; i += warps * 32 * 4) {
+            for (int i = me; i < pieces; i += all * 4) {
                 uint4 x[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    x[j] = lds16(vbase + min(i + j * warps * 32, pieces - 1) * 16);
+                    x[j] = lds16(vbase + min(i + j * all, pieces - 1) * 16);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     bad |= nonfinite2(x[j].x) | nonfinite2(x[j].y) | nonfinite2(x[j].z) |
@@ -1514,7 +1528,7 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
             if (bad & 0x80008000u) {
                 *dirty = 1;
                 __threadfence_block();
-                for (int i = warp * 32 + lane; i < pieces; i += warps * 32) {
+                for (int i = me; i < pieces; i += all) {
                     const uint4 x = lds16(vbase + i * 16);
                     sts16(vbase + i * 16, make_uint4(finite2(x.x), finite2(x.y), finite2(x.z),
                                                      finite2(x.w)));
@@ -1527,16 +1541,24 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
         ++done;
     }
     // O is complete
-    if (!bar_wait(bars + kBarDone * 8, 0, abort, p.wait_limit_ns))
-        return false;
+    ok = ok && bar_wait(bars + kBarDone * 8, 0, abort, p.wait_limit_ns);
     mma_fence_after();
-    const float inv = st.sum == 0.0f || done == 0 ? 0.0f : 1.0f / st.sum;
+    const int place = done % RowPairs<G>::PLACES;
+    pairs.max[place][half][t * kRows + r] = st.sum;
+    if (!ok)
+        pairs.failed[pair] = 1;
+    pair_sync(pair);
+    if (pairs.failed[pair])
+        return;
+    const float sum = half == 0 ? st.sum + pairs.max[place][1][t * kRows + r]
+                                : pairs.max[place][0][t * kRows + r] + st.sum;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int h = G::MLA ? g : w.head * p.group + g;
     const int64_t at = (w.q0 + tok) * p.heads + h;
-    const float lse = st.sum == 0.0f ? -INFINITY : st.top * p.scale + logf(st.sum);
-    const int col0 = G::MLA ? w.head * 256 : 0;
+    const int col0 = (G::MLA ? w.head * 256 : 0) + half * HO;
     const bool parts = w.splits > 1;
-    if (valid && (!G::MLA || w.head == 0)) {
+    if (valid && half == 0 && (!G::MLA || w.head == 0)) {
+        const float lse = sum == 0.0f ? -INFINITY : st.top * p.scale + logf(sum);
         if (parts)
             p.part_lse[w.split * p.total_q * p.heads + at] = lse;
         else if (p.lse)
@@ -1546,15 +1568,14 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0; // a row's sectors are whole
     float *part = p.part + (w.split * p.total_q * p.heads + at) * G::DV + col0;
 #pragma unroll 1
-    for (int i = 0; i < G::OC; i += 32) {
+    for (int i = 0; i < HO; i += 32) {
         uint32_t o[32];
-        tmem_ld32(tmem + G::O_COL(t) + lanes + i, o);
+        tmem_ld32(o_col + i, o);
         tmem_ld_wait();
         tmem_pin32(o);
-        float f[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-            f[j] = st.sum == 0.0f ? 0.0f : __uint_as_float(o[j]) * inv;
+            o[j] = sum == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[j]) * inv);
         if (*dirty) {
             for (int v = w.beg; v < w.end; ++v) {
                 const int k0 = real_tile(w, v) * KT;
@@ -1567,7 +1588,9 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
                         continue;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        f[j] += nonfinite_value<G>(p, s, (G::MLA ? col0 : w.head * 128) + i + j);
+                        o[j] = __float_as_uint(
+                            __uint_as_float(o[j]) +
+                            nonfinite_value<G>(p, s, (G::MLA ? 0 : w.head * 128) + col0 + i + j));
                 }
             }
         }
@@ -1575,15 +1598,12 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
             continue;
         if (parts) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                o[j] = __float_as_uint(f[j]);
-#pragma unroll
             for (int j = 0; j < 32; j += 8)
                 st32(part + i + j, o + j);
         } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                o[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+                o[j] = pack_bf16(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
             if (wide) {
                 st32(out + i * 2, o);
                 st32(out + i * 2 + 32, o + 8);
@@ -1595,7 +1615,6 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
             }
         }
     }
-    return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -1603,7 +1622,7 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
 // ---------------------------------------------------------------------------
 
 template <class G>
-__global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
+__global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
     const __grid_constant__ AttnParams p)
 {
     using S = Smem<G>;
@@ -1612,6 +1631,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
     __shared__ uint32_t s_tmem, s_status;
     __shared__ int s_go;
     __shared__ volatile int s_abort, s_dirty;
+    __shared__ RowPairs<G> s_pairs;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
     const uint32_t q_smem = smem + S::Q, ring = smem + S::RING, bars = smem + S::BAR;
@@ -1642,14 +1662,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
             s_status = bad ? kStatusOutOfRange : kStatusOk;
             s_abort = 0;
             s_dirty = 0;
+            for (int i = 0; i < 8; ++i)
+                s_pairs.failed[i] = 0;
             for (int i = 0; i < 2; ++i) { // the warps that have rows signal the weights
                 const int rows = tile_mask(p, w.n, w.len, w.row0 + (G::NT == 2 ? i : 0) * kRows).rows;
-                bar_init(bars + (kBarP + i) * 8, max(1, (rows + 31) / 32) * 32);
+                bar_init(bars + (kBarP + i) * 8, max(1, (rows + 31) / 32) * 64);
             }
             bar_init_fence();
         }
     } else if (warp == 1 && lane == 0) {
-        bar_init(bars + kBarQ * 8, G::NT * 128);
+        bar_init(bars + kBarQ * 8, G::SOFT_WARPS * 32);
         bar_init(bars + kBarDone * 8, 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(bars + (kBarS + i) * 8, 1);
@@ -1660,7 +1682,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
             bar_init(bars + (kBarRing + G::BARS / 2 + i) * 8, 1);
         }
         bar_init_fence();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp<G>) {
         tmem_alloc(smem_u32(&s_tmem), 512);
     }
     mma_fence_before();
@@ -1671,24 +1693,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
 
     if (!s_go) {
         // nothing for this block
-    } else if (warp < G::NT * 4) {
+    } else if (warp < G::SOFT_WARPS) {
         const Work w = s_work;
-        const int t = warp >> 2;
+        const int t = warp >> 3, half = (warp >> 2) & 1;
         const TileMask mask = tile_mask(p, w.n, w.len, w.row0 + t * kRows);
         const int wl = warp & 3, warps = (mask.rows + 31) / 32;
-        load_queries<G>(p, w, q_smem, t, tid & 127);
+        load_queries<G>(p, w, q_smem, t, tid & 255);
         if constexpr (G::MLA)
-            queries_to_tmem<G>(p, w, tmem, wl, lane, mask.rows);
+            queries_to_tmem<G>(p, w, tmem, wl, lane, mask.rows, half * 2);
         copy_commit();
         copy_wait<0>();
         async_fence();
         mma_fence_before();
         bar_signal(bars + kBarQ * 8);
         if (wl < warps)
-            run_softmax<G>(p, w, mask, t, tmem, ring, bars, wl, lane, warps, &s_abort, &s_dirty);
-    } else if (warp < kMmaWarp) {
+            run_softmax<G>(p, w, mask, t, tmem, ring, bars, wl, half, lane, warps, &s_abort,
+                           &s_dirty, s_pairs);
+    } else if (warp < kMmaWarp<G>) {
         const Work w = s_work;
-        const int lw = warp - G::NT * 4;
+        const int lw = warp - G::SOFT_WARPS;
         bool bad = false;
         if constexpr (G::MLA && G::QUANT)
             load_mla_e4m3<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
@@ -1721,7 +1744,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attention_kernel(
     mma_fence_before();
     __syncthreads();
     mma_fence_after();
-    if (warp == kMmaWarp)
+    if (warp == kMmaWarp<G>)
         tmem_free(tmem, 512);
     if (tid == 0)
         write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, gridDim.x);
@@ -2369,18 +2392,32 @@ cudaError_t launch_join(const AttnParams &p, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, attention_join_kernel<G>, p);
 }
 
+// The kernel's limit of dynamic shared memory, raised once on each device.
+template <auto KERNEL>
+cudaError_t allow_smem(int bytes)
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load() >> dev) & 1u))
+        return e;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64)
+        done.fetch_or(uint64_t(1) << dev);
+    return e;
+}
+
 template <class G>
 cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
 {
     constexpr int bytes = Smem<G>::BYTES;
-    static_assert(bytes <= 227 * 1024, "shared memory");
+    static_assert(bytes + sizeof(RowPairs<G>) + 256 <= 227 * 1024, "shared memory");
     if (!G::QUANT) // e4m3 rows are converted on their way
         set_boxes<G>(p);
-    cudaError_t e = cudaFuncSetAttribute(attention_kernel<G>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = allow_smem<attention_kernel<G>>(bytes);
     if (e != cudaSuccess)
         return e;
-    attention_kernel<G><<<(unsigned)blocks, kAttnThreads, bytes, stream>>>(p);
+    attention_kernel<G><<<(unsigned)blocks, kAttnThreads<G>, bytes, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     return launch_join<G>(p, stream);
@@ -2391,8 +2428,7 @@ cudaError_t launch_few(AttnParams &p, int64_t blocks, cudaStream_t stream)
 {
     static_assert(G::BYTES <= 113 * 1024, "two blocks to an SM");
     set_boxes<G>(p);
-    cudaError_t e = cudaFuncSetAttribute(attention_few_kernel<G>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, G::BYTES);
+    cudaError_t e = allow_smem<attention_few_kernel<G>>(G::BYTES);
     if (e != cudaSuccess)
         return e;
     attention_few_kernel<G><<<(unsigned)blocks, kFewThreads, G::BYTES, stream>>>(p);

@@ -9,10 +9,10 @@
 // rounding is the one to e4m3.
 //
 // Both directions are bound by HBM: a value is read once and written once
-// (2 + 1 bytes, the scales 4 bytes per 128).  A warp takes one row of one
-// layer at a time, 16 lanes to a group: 16-byte accesses on the bf16 side,
-// 8-byte ones on the e4m3 side, up to eight in flight per lane; the group's
-// maximum is four shuffles.
+// (2 + 1 bytes, the scales 4 bytes per 128).  A warp takes a few rows of one layer
+// at a time (MLA rows of 576 values two at a time: 1152 rows x 61 layers read back in
+// 25 us, one by one in 29, four by four in 27): segments of whole groups, 16 lanes to a group, 16-byte accesses on the bf16 side and 8-byte
+// ones on the e4m3 side; a group's maximum is four shuffles.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -24,13 +24,17 @@ namespace kvr {
 namespace {
 
 constexpr int kQuantThreads = 256;
+constexpr int64_t kFewRows = 152 * 32; // rows that leave warps without work
 
-// Row shapes: 16-byte bf16 pieces of the copy and rotary part; ROTQ: the
-// rotary part is quantised too.
-template <int COPY, int ROT, bool ROTQ_>
+// Row shapes: 16-byte bf16 pieces of the copy part (and of the rotary part, where that
+// is quantised too: it is as wide); ROWS: rows of a warp's unit.
+template <int COPY, int ROT, bool ROTQ_, int ROWS_>
 struct QRow {
-    static constexpr int CP = COPY / 8, RP = ROT / 8;
+    static constexpr int CP = COPY / 8;
     static constexpr bool ROTQ = ROTQ_;
+    static constexpr int ROWS = ROWS_, SEGS = ROWS * (ROTQ ? 2 : 1);
+    static_assert(!ROTQ || COPY == ROT, "segments of one width");
+    static_assert(ROTQ || (ROT == 64 && ROWS <= 4), "8 lanes to a k_pe row");
 };
 
 // Exponent e of a group's scale from the bits of its largest finite magnitude
@@ -48,40 +52,66 @@ __device__ __forceinline__ float exp2_int(int e) // -126 <= e <= 127
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// Largest finite magnitude of a 16-byte piece, as bf16 bits.
-__device__ __forceinline__ uint32_t piece_max(uint4 v)
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t a = w[i] & 0x7FFFu, b = (w[i] >> 16) & 0x7FFFu;
-        m = max(m, a < 0x7F80u ? a : 0u);
-        m = max(m, b < 0x7F80u ? b : 0u);
-    }
-    return m;
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
-// Two values to e4m3; finite values are at most 448 here, so anything above
-// was infinite and becomes NaN.
+// Largest magnitudes of a 16-byte piece's even and odd values: the bits of a
+// positive bf16 order like the value, those that are not finite above all others.
+__device__ __forceinline__ uint32_t piece_max(uint4 v)
+{
+    const uint32_t m = 0x7FFF7FFFu;
+    return max_u16x2(max_u16x2(v.x & m, v.y & m), max_u16x2(v.z & m, v.w & m));
+}
+
+// A piece with the values that are not finite set to 0.
+__device__ __forceinline__ uint4 finite_piece(uint4 v)
+{
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] &= (w[i] & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : ~0u;
+        w[i] &= (w[i] & 0x7F800000u) == 0x7F800000u ? 0x0000FFFFu : ~0u;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Largest value over the 16 lanes of a group.
+__device__ __forceinline__ uint32_t group_max(uint32_t m)
+{
+#pragma unroll
+    for (int x = 8; x > 0; x >>= 1)
+        m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+    return max(m & 0xFFFFu, m >> 16);
+}
+
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
 {
-    const float nan = __uint_as_float(0x7FC00000u);
-    lo = fabsf(lo) <= 448.0f ? lo : nan;
-    hi = fabsf(hi) <= 448.0f ? hi : nan;
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
+// Eight values times inv to e4m3: at most 448 where they are finite.  RARE: others
+// among them, which become NaN.
+template <bool RARE>
 __device__ __forceinline__ uint2 quant_piece(uint4 v, float inv)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t h[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        h[i] = e4m3x2(__uint_as_float(w[i] << 16) * inv,
-                      __uint_as_float(w[i] & 0xFFFF0000u) * inv);
+    for (int i = 0; i < 4; ++i) {
+        float lo = __uint_as_float(w[i] << 16) * inv, hi = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
+        if (RARE) {
+            const float nan = __uint_as_float(0x7FC00000u);
+            lo = fabsf(lo) <= 448.0f ? lo : nan;
+            hi = fabsf(hi) <= 448.0f ? hi : nan;
+        }
+        h[i] = e4m3x2(lo, hi);
+    }
     return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
@@ -99,86 +129,130 @@ __device__ __forceinline__ uint4 value_piece(uint2 v, float s)
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Quantise NP 16-byte pieces (16 to a group) of one row.
-template <int NP>
-__device__ __forceinline__ void quant_part(const char *src, char *dst, float *scale, int lane)
+// A run of values of one row: bf16 at `rows`, e4m3 at `pool` with its scales.  NULL:
+// skipped.
+struct Segment {
+    char *rows, *pool;
+    float *scale;
+};
+
+// Quantise N segments of NP 16-byte pieces (16 to a group).
+template <int NP, int N>
+__device__ __forceinline__ void quantise(const Segment (&seg)[N], int lane)
 {
-    constexpr int IT = NP / 32, B = IT < 8 ? IT : 8;
+    constexpr int IT = NP / 32, B = IT * N > 8 ? 8 / N : IT;
     static_assert(NP % 32 == 0 && IT % B == 0, "whole groups");
 #pragma unroll 1
     for (int b = 0; b < IT; b += B) {
-        uint4 v[B];
+        uint4 v[N][B] = {}; // a skipped segment counts as zeros
 #pragma unroll
-        for (int i = 0; i < B; ++i)
-            v[i] = ld_stream(src + ((b + i) * 32 + lane) * 16);
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
-            uint32_t m = piece_max(v[i]);
+            for (int i = 0; i < B; ++i)
+                if (seg[n].rows)
+                    v[n][i] = ld_stream(seg[n].rows + ((b + i) * 32 + lane) * 16);
 #pragma unroll
-            for (int x = 8; x > 0; x >>= 1)
-                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-            const int e = scale_exp(m), at = (b + i) * 32 + lane;
-            *reinterpret_cast<uint2 *>(dst + at * 8) = quant_piece(v[i], exp2_int(-e));
-            if ((lane & 15) == 0)
-                scale[at >> 4] = exp2_int(e);
-        }
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                uint32_t m = group_max(piece_max(v[n][i]));
+                const bool rare = __any_sync(0xFFFFFFFFu, m >= 0x7F80u);
+                if (rare)
+                    m = group_max(piece_max(finite_piece(v[n][i])));
+                const int e = scale_exp(m), at = (b + i) * 32 + lane;
+                if (seg[n].rows) {
+                    *reinterpret_cast<uint2 *>(seg[n].pool + at * 8) =
+                        rare ? quant_piece<true>(v[n][i], exp2_int(-e))
+                             : quant_piece<false>(v[n][i], exp2_int(-e));
+                    if ((lane & 15) == 0)
+                        seg[n].scale[at >> 4] = exp2_int(e);
+                }
+            }
     }
 }
 
-template <int NP>
-__device__ __forceinline__ void value_part(const char *src, char *dst, const float *scale, int lane)
+// Read N segments back.
+template <int NP, int N>
+__device__ __forceinline__ void dequantise(const Segment (&seg)[N], int lane)
 {
-    constexpr int IT = NP / 32, B = IT < 8 ? IT : 8;
+    constexpr int IT = NP / 32, B = IT * N > 8 ? 8 / N : IT;
 #pragma unroll 1
     for (int b = 0; b < IT; b += B) {
-        uint2 v[B];
-        float s[B];
+        uint2 v[N][B];
+        float s[N][B];
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int at = (b + i) * 32 + lane;
-            v[i] = __ldcs(reinterpret_cast<const uint2 *>(src + at * 8));
-            s[i] = __ldg(scale + (at >> 4));
-        }
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int i = 0; i < B; ++i)
-            st_stream(dst + ((b + i) * 32 + lane) * 16, value_piece(v[i], s[i]));
+            for (int i = 0; i < B; ++i) {
+                const int at = (b + i) * 32 + lane;
+                if (seg[n].rows) {
+                    v[n][i] = __ldcs(reinterpret_cast<const uint2 *>(seg[n].pool + at * 8));
+                    s[n][i] = __ldg(seg[n].scale + (at >> 4));
+                }
+            }
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+                if (seg[n].rows)
+                    st_stream(seg[n].rows + ((b + i) * 32 + lane) * 16,
+                              value_piece(v[n][i], s[n][i]));
     }
 }
 
-// One warp per (layer, row); READ: pool -> rows, else rows -> pool.
+// A warp takes units of R::ROWS rows of a layer; READ: pool -> rows, else rows ->
+// pool.
 template <class R, bool READ>
 __global__ void __launch_bounds__(kQuantThreads) quant_kernel(const __grid_constant__ QuantParams p)
 {
+    constexpr int ROWS = R::ROWS;
     const int lane = threadIdx.x & 31;
-    const int64_t total = p.num_rows * p.layers;
+    const int64_t per_layer = (p.num_rows + ROWS - 1) / ROWS, total = per_layer * p.layers;
     const int64_t step = (int64_t)gridDim.x * (kQuantThreads / 32);
     int bad = 0;
-    for (int64_t w = (int64_t)blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5); w < total;
-         w += step) {
-        const int64_t l = w / p.num_rows, i = w - l * p.num_rows;
-        const int64_t rs = p.row_slot ? p.row_slot[i] : i, ps = p.pool_slot[i];
-        if (rs < 0 || rs >= p.rows.num_slots || ps < 0 || ps >= p.pool.num_slots) {
-            bad = 1;
-            continue;
+    for (int64_t u = (int64_t)blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5); u < total;
+         u += step) {
+        const int64_t l = u / per_layer, i = (u - l * per_layer) * ROWS + (lane & (ROWS - 1));
+        int64_t rs = -1, ps = -1; // slots of row lane % ROWS of the unit
+        if (i < p.num_rows) {
+            rs = p.row_slot ? p.row_slot[i] : i;
+            ps = p.pool_slot[i];
+            if (rs < 0 || rs >= p.rows.num_slots || ps < 0 || ps >= p.pool.num_slots) {
+                bad = 1;
+                rs = -1;
+            }
         }
-        char *rc = p.rows.copy + l * p.rows.copy_ls + rs * p.rows.copy_ss;
-        char *rr = p.rows.rot + l * p.rows.rot_ls + rs * p.rows.rot_ss;
-        char *pc = p.pool.copy + l * p.pool.copy_ls + ps * p.pool.copy_ss;
-        char *pr = p.pool.rot + l * p.pool.rot_ls + ps * p.pool.rot_ss;
-        float *cs = p.pool.cs + l * p.pool.cs_ls + ps * p.pool.cs_ss;
-        float *xs = R::ROTQ ? p.pool.rs + l * p.pool.rs_ls + ps * p.pool.rs_ss : nullptr;
-        if constexpr (READ) {
-            value_part<R::CP>(pc, rc, cs, lane);
+        char *const rc = p.rows.copy + l * p.rows.copy_ls, *const rr = p.rows.rot + l * p.rows.rot_ls;
+        char *const pc = p.pool.copy + l * p.pool.copy_ls, *const pr = p.pool.rot + l * p.pool.rot_ls;
+        Segment seg[R::SEGS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const int64_t a = __shfl_sync(0xFFFFFFFFu, rs, r), b = __shfl_sync(0xFFFFFFFFu, ps, r);
+            const bool ok = a >= 0;
+            seg[r] = {ok ? rc + a * p.rows.copy_ss : nullptr, pc + b * p.pool.copy_ss,
+                      p.pool.cs + l * p.pool.cs_ls + b * p.pool.cs_ss};
             if constexpr (R::ROTQ)
-                value_part<R::RP>(pr, rr, xs, lane);
-            else if (lane < R::RP)
-                st_stream(rr + lane * 16, ld_stream(pr + lane * 16));
-        } else {
-            quant_part<R::CP>(rc, pc, cs, lane);
-            if constexpr (R::ROTQ)
-                quant_part<R::RP>(rr, pr, xs, lane);
-            else if (lane < R::RP)
-                *reinterpret_cast<uint4 *>(pr + lane * 16) = ld_stream(rr + lane * 16);
+                seg[ROWS + r] = {ok ? rr + a * p.rows.rot_ss : nullptr, pr + b * p.pool.rot_ss,
+                                 p.pool.rs + l * p.pool.rs_ls + b * p.pool.rs_ss};
+        }
+        // MLA: 8 lanes to the k_pe of a row
+        const int64_t ka = __shfl_sync(0xFFFFFFFFu, rs, lane >> 3);
+        const int64_t kb = __shfl_sync(0xFFFFFFFFu, ps, lane >> 3);
+        const bool has_pe = !R::ROTQ && lane < ROWS * 8 && ka >= 0;
+        char *const kr = rr + ka * p.rows.rot_ss + (lane & 7) * 16;
+        char *const kp = pr + kb * p.pool.rot_ss + (lane & 7) * 16;
+        uint4 pe = make_uint4(0, 0, 0, 0);
+        if (has_pe)
+            pe = ld_stream(READ ? kp : kr);
+        if constexpr (READ)
+            dequantise<R::CP>(seg, lane);
+        else
+            quantise<R::CP>(seg, lane);
+        if (has_pe) {
+            if (READ)
+                st_stream(kr, pe);
+            else
+                *reinterpret_cast<uint4 *>(kp) = pe;
         }
     }
     bad = __syncthreads_or(bad);
@@ -186,27 +260,36 @@ __global__ void __launch_bounds__(kQuantThreads) quant_kernel(const __grid_const
         write_block_status(p.header, bad ? kStatusOutOfRange : kStatusOk, blockIdx.x, gridDim.x);
 }
 
+template <class R, bool READ>
+cudaError_t launch_row(const QuantParams &p, cudaStream_t stream)
+{
+    constexpr int WARPS = kQuantThreads / 32;
+    const int64_t units = (p.num_rows + R::ROWS - 1) / R::ROWS * p.layers;
+    const int64_t want = (units + WARPS - 1) / WARPS;
+    const int blocks = (int)(want < kQuantMaxBlocks ? want : kQuantMaxBlocks);
+    quant_kernel<R, READ><<<blocks, kQuantThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
 template <bool READ>
 cudaError_t launch(const QuantParams &p, RowKind kind, cudaStream_t stream)
 {
-    const int64_t warps = p.num_rows * p.layers;
-    const int64_t want = (warps + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
-    const int blocks = (int)(want < kQuantMaxBlocks ? want : kQuantMaxBlocks);
+    // few rows (a decode step): one to a warp, more of them at work at once
+    const bool few = p.num_rows * p.layers <= kFewRows;
     switch (kind) {
     case RowKind::Mla:
-        quant_kernel<QRow<512, 64, false>, READ><<<blocks, kQuantThreads, 0, stream>>>(p);
-        break;
+        return few ? launch_row<QRow<512, 64, false, 1>, READ>(p, stream)
+                   : launch_row<QRow<512, 64, false, 2>, READ>(p, stream);
     case RowKind::Gqa:
-        quant_kernel<QRow<1024, 1024, true>, READ><<<blocks, kQuantThreads, 0, stream>>>(p);
-        break;
+        return launch_row<QRow<1024, 1024, true, 1>, READ>(p, stream);
     case RowKind::Gqa4:
-        quant_kernel<QRow<512, 512, true>, READ><<<blocks, kQuantThreads, 0, stream>>>(p);
-        break;
+        if (few)
+            return launch_row<QRow<512, 512, true, 1>, READ>(p, stream);
+        return launch_row<QRow<512, 512, true, 2>, READ>(p, stream);
     case RowKind::Mha:
-        quant_kernel<QRow<4096, 4096, true>, READ><<<blocks, kQuantThreads, 0, stream>>>(p);
-        break;
+        return launch_row<QRow<4096, 4096, true, 1>, READ>(p, stream);
     }
-    return cudaGetLastError();
+    return cudaErrorInvalidValue;
 }
 
 } // namespace
