@@ -158,6 +158,18 @@ __device__ __forceinline__ void mma_fence_before() { asm volatile("tcgen05.fence
 __device__ __forceinline__ void mma_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+template <int R>
+__device__ __forceinline__ void reg_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+template <int R>
+__device__ __forceinline__ void reg_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -470,7 +482,8 @@ struct MlaGeo {
     static constexpr int NT = 1, KT = 64;
     static constexpr int QPANELS = 5, OC = 256;
     static constexpr int DV = 512;
-    static constexpr int SOFT_WARPS = 8, LOAD_WARPS = 8;
+    // e4m3 rows are converted by the load warps: twice as many
+    static constexpr int SOFT_WARPS = 8, LOAD_WARPS = QUANT ? 16 : 8;
     static constexpr int PANEL = 64 * 128;
     static constexpr int OTHER = 5 * PANEL, OWN = 4 * PANEL; // bytes of a tile's parts
     static constexpr int BARS = 8; // full, empty of two stages of two parts
@@ -488,8 +501,15 @@ struct MlaGeo {
 template <class G>
 constexpr int kMmaWarp = G::SOFT_WARPS + G::LOAD_WARPS;
 
+// Two row tiles: 16 softmax warps that hold 64 scores a thread need more registers than
+// the other roles, which give some back; whole warpgroups, then.
 template <class G>
-constexpr int kAttnThreads = (kMmaWarp<G> + 1) * 32;
+constexpr bool kShares = G::NT == 2;
+
+constexpr int kSoftRegs = 96, kLoadRegs = 56, kMmaRegs = 40;
+
+template <class G>
+constexpr int kAttnThreads = (kMmaWarp<G> + (kShares<G> ? 4 : 1)) * 32;
 
 template <class G>
 struct Smem {
@@ -1059,31 +1079,26 @@ __device__ __forceinline__ void load_mla_e4m3(const AttnParams &p, const Work &w
                                               uint32_t bars, int warp, int lane,
                                               volatile int *abort, bool &bad)
 {
-    const int base = warp * 8, c = lane & 7, sub = lane >> 3;
-    uint4 lat[2][2][2], pe[2]; // [part][group of 128][row]
+    const int base = warp * 4, c = lane & 7, sub = lane >> 3;
+    uint4 lat[2][2], pe; // [part][group of 128]
     float scale[2][2];
-    auto key_at = [&](int v) { return real_tile(w, v) * G::KT + base + c; };
+    auto key_at = [&](int v) { return real_tile(w, v) * G::KT + base + sub; };
     auto block_at = [&](int v) { return v < w.end ? key_block(p, w, key_at(v)) : 0; };
     auto slot_at = [&](int v, int32_t blk) {
         return v < w.end ? key_slot(p, w, key_at(v), blk, bad) : (int64_t)-1;
     };
     auto fetch = [&](int part, int64_t slot) {
         const int half = part == 0 ? 1 - w.head : w.head;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const char *src = p.copy + slot * p.copy_ss + half * 256 + c * 16;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, i * 4 + sub);
-            const char *src = p.copy + (s < 0 ? 0 : s * p.copy_ss) + half * 256 + c * 16;
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-                lat[part][g][i] = s < 0 ? make_uint4(0, 0, 0, 0)
-                                        : __ldg(reinterpret_cast<const uint4 *>(src + g * 128));
-            if (part == 0)
-                pe[i] = s < 0 ? make_uint4(0, 0, 0, 0)
-                              : __ldg(reinterpret_cast<const uint4 *>(p.rot + s * p.rot_ss + c * 16));
-        }
-#pragma unroll
-        for (int g = 0; g < 2; ++g) // lane c of each eight: the row's scale
+        for (int g = 0; g < 2; ++g) {
+            lat[part][g] = slot < 0 ? zero : __ldg(reinterpret_cast<const uint4 *>(src + g * 128));
             scale[part][g] = slot < 0 ? 1.0f : __ldg(p.cs + slot * p.cs_ss + half * 2 + g);
+        }
+        if (part == 0)
+            pe = slot < 0 ? zero
+                          : __ldg(reinterpret_cast<const uint4 *>(p.rot + slot * p.rot_ss + c * 16));
     };
     const int first = c >> 2;
     const int c0 = (2 * c + first) & 7, c1 = (2 * c + 1 - first) & 7;
@@ -1101,30 +1116,20 @@ __device__ __forceinline__ void load_mla_e4m3(const AttnParams &p, const Work &w
             if (!bar_wait(full + 4 * 8, phase, abort, p.wait_limit_ns))
                 return;
             const uint32_t mul[2] = {scale_mul(scale[part][0]), scale_mul(scale[part][1])};
-            uint32_t m[2][2], rare = 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    m[i][g] = __shfl_sync(0xFFFFFFFFu, mul[g], i * 4 + sub);
-                    rare |= rare16(lat[part][g][i], m[i][g]);
-                }
+            const uint32_t rare = rare16(lat[part][0], mul[0]) | rare16(lat[part][1], mul[1]);
+            const int row = base + sub;
+            const uint32_t at = dst + row * 128;
             auto store = [&](auto kind) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = i * 4 + sub;
-                    const uint32_t at = dst + (base + r) * 128;
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        uint4 x, y;
-                        convert16<decltype(kind)::value>(lat[part][g][i], m[i][g], x, y);
-                        const uint32_t to = at + (g * 2 + first) * G::PANEL;
-                        sts16(to + ((c0 ^ (r & 7)) << 4), first ? y : x);
-                        sts16(to + ((c1 ^ (r & 7)) << 4), first ? x : y);
-                    }
-                    if (part == 0)
-                        sts16(at + 4 * G::PANEL + ((c ^ (r & 7)) << 4), pe[i]);
+                for (int g = 0; g < 2; ++g) {
+                    uint4 x, y;
+                    convert16<decltype(kind)::value>(lat[part][g], mul[g], x, y);
+                    const uint32_t to = at + (g * 2 + first) * G::PANEL;
+                    sts16(to + ((c0 ^ (row & 7)) << 4), first ? y : x);
+                    sts16(to + ((c1 ^ (row & 7)) << 4), first ? x : y);
                 }
+                if (part == 0)
+                    sts16(at + 4 * G::PANEL + ((c ^ (row & 7)) << 4), pe);
             };
             if (rare)
                 store(std::true_type{});
@@ -1407,28 +1412,29 @@ __device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, 
         ok = ok && bar_wait(bars + (kBarS + buf) * 8, parity, abort, p.wait_limit_ns);
         mma_fence_after();
         const bool full = tile_full<KT>(p, m, kt);
-        // Two passes over the half row in pieces of 32 scores: short loops stay in the
-        // instruction cache, which a row held in registers and unrolled did not.
-        auto mask = [&](uint32_t(&s)[32], int i) {
-            const int k0 = kt * KT + half * HK + i; // a bit per key that is seen
-            const uint32_t see = below(hi - k0) & (~below(lo - k0) | below(sk - k0));
+        // the half row in registers: tensor memory takes some 300 clocks to answer, once
+        uint32_t s[HK];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                s[j] = (see >> j) & 1u ? s[j] : 0xFF800000u;
-        };
-        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}; // chains of maxima
-#pragma unroll 1
-        for (int i = 0; i < HK; i += 32) {
-            uint32_t s[32];
-            tmem_ld32(s_col + i, s);
-            tmem_ld_wait();
-            tmem_pin32(s);
-            if (!full)
-                mask(s, i);
+        for (int i = 0; i < HK; i += 32)
+            tmem_ld32(s_col + i, s + i);
+        tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                t4[j & 3] = max3(t4[j & 3], __uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+        for (int i = 0; i < HK; i += 32)
+            tmem_pin32(s + i);
+        if (!full) {
+#pragma unroll
+            for (int i = 0; i < HK; i += 32) { // a bit per key that is seen
+                const int k0 = kt * KT + half * HK + i;
+                const uint32_t see = below(hi - k0) & (~below(lo - k0) | below(sk - k0));
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    s[i + j] = (see >> j) & 1u ? s[i + j] : 0xFF800000u;
+            }
         }
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}; // chains of maxima
+#pragma unroll
+        for (int j = 0; j < HK / 2; ++j)
+            t4[j & 3] = max3(t4[j & 3], __uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
         float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         const int place = done % RowPairs<G>::PLACES;
         pairs.max[place][half][t * kRows + r] = top;
@@ -1455,40 +1461,34 @@ __device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, 
                 st.sum *= f;
             }
 #pragma unroll 1
-            for (int i = 0; i < HO; i += 32) {
-                uint32_t o[32];
-                tmem_ld32(o_col + i, o);
+            for (int i = 0; i < HO; i += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_col + i, o);
                 tmem_ld_wait();
-                tmem_pin32(o);
+                tmem_pin16(o);
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < 16; ++j)
                     o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st32(o_col + i, o);
+                tmem_st16(o_col + i, o);
             }
         }
         const float off = st.top == -INFINITY ? 0.0f : -st.top * c;
         const f2 c2 = f2_of_bits(__float_as_uint(c), __float_as_uint(c));
         const f2 off2 = f2_of_bits(__float_as_uint(off), __float_as_uint(off));
         f2 sum2[2] = {0ull, 0ull};
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < HK; i += 32) {
-            uint32_t s[32];
-            tmem_ld32(s_col + i, s);
-            tmem_ld_wait();
-            tmem_pin32(s);
-            if (!full)
-                mask(s, i);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const f2 x = f2_fma(f2_of_bits(s[2 * j], s[2 * j + 1]), c2, off2);
+                const f2 x = f2_fma(f2_of_bits(s[i + 2 * j], s[i + 2 * j + 1]), c2, off2);
                 float a, b;
                 asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
                 a = exp2_fast(a);
                 b = exp2_fast(b);
                 sum2[j & 1] = f2_add(sum2[j & 1], f2_of_bits(__float_as_uint(a), __float_as_uint(b)));
-                s[j] = pack_bf16(a, b);
+                s[i / 2 + j] = pack_bf16(a, b);
             }
-            tmem_st16(s_col + i / 2, s); // over scores that have been read
+            tmem_st16(s_col + i / 2, s + i / 2); // over scores that have been read
         }
         float s0, s1;
         asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(f2_add(sum2[0], sum2[1])));
@@ -1694,6 +1694,8 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
     if (!s_go) {
         // nothing for this block
     } else if (warp < G::SOFT_WARPS) {
+        if constexpr (kShares<G>)
+            reg_inc<kSoftRegs>();
         const Work w = s_work;
         const int t = warp >> 3, half = (warp >> 2) & 1;
         const TileMask mask = tile_mask(p, w.n, w.len, w.row0 + t * kRows);
@@ -1710,6 +1712,8 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
             run_softmax<G>(p, w, mask, t, tmem, ring, bars, wl, half, lane, warps, &s_abort,
                            &s_dirty, s_pairs);
     } else if (warp < kMmaWarp<G>) {
+        if constexpr (kShares<G>)
+            reg_dec<kLoadRegs>();
         const Work w = s_work;
         const int lw = warp - G::SOFT_WARPS;
         bool bad = false;
@@ -1725,6 +1729,10 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
             s_status = kStatusOutOfRange;
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
+        if constexpr (kShares<G>)
+            reg_dec<kMmaRegs>();
+    }
+    if (s_go && warp == kMmaWarp<G>) {
         const Work w = s_work;
         const uint32_t lead = elect_lane();
         bool ok = bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
@@ -2417,6 +2425,14 @@ cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
     cudaError_t e = allow_smem<attention_kernel<G>>(bytes);
     if (e != cudaSuccess)
         return e;
+    if (kShares<G>) { // the shares come out of what a block starts with, or it would wait
+        cudaFuncAttributes fa;
+        if ((e = cudaFuncGetAttributes(&fa, attention_kernel<G>)) != cudaSuccess)
+            return e;
+        if (G::SOFT_WARPS * kSoftRegs + G::LOAD_WARPS * kLoadRegs + 4 * kMmaRegs >
+            kAttnThreads<G> / 32 * fa.numRegs)
+            return cudaErrorInvalidConfiguration;
+    }
     attention_kernel<G><<<(unsigned)blocks, kAttnThreads<G>, bytes, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
