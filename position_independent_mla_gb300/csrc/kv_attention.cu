@@ -742,26 +742,16 @@ __device__ __forceinline__ bool tile_whole(const Work &w, int kt)
     return (k0 >= w.lo && k0 + KT <= w.hi) || k0 + KT <= w.sk;
 }
 
-// Box copies that may be in flight, a bit per barrier.  A block waits for them
-// before its shared memory goes, also when it gives up early.
-struct Flights {
-    uint32_t boxes = 0, parity = 0;
-
-    __device__ void filled(int bar, bool by_boxes, int full_parity)
-    {
-        const uint32_t bit = 1u << bar;
-        boxes = by_boxes ? boxes | bit : boxes & ~bit;
-        parity = full_parity ? parity | bit : parity & ~bit;
-    }
-
-    __device__ void land(uint32_t bars)
-    {
-        int none = 0;
-        for (int i = 0; i < 32; ++i)
-            if ((boxes >> i) & 1u)
-                bar_wait(bars + i * 8, (parity >> i) & 1u, &none, 1000000000ll);
-    }
-};
+// Waits for the boxes that may be in flight when `filled` tiles went into a ring, also
+// when the block gives up early: its shared memory goes after that.
+template <int STAGES>
+__device__ __forceinline__ void copies_land(uint32_t full, int filled)
+{
+    int none = 0;
+    for (int i = 0; i < STAGES; ++i)
+        if (filled > i)
+            bar_wait(full + i * 8, ((filled - 1 - i) / STAGES) & 1, &none, 10000000ll);
+}
 
 // Stages filled by cp.async: their threads wait for the copies, make them visible to
 // the MMAs and signal, one stage behind the one that they are filling.
@@ -797,63 +787,107 @@ struct Copies {
     }
 };
 
+// A vote over the load warps, also their meeting point.
+template <class G>
+__device__ __forceinline__ bool load_any(bool x)
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 q, %1, 0;\n"
+                 "barrier.cta.red.or.pred p, 15, %2, q;\nselp.b32 %0, 1, 0, p;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)x), "n"(G::LOAD_WARPS * 32)
+                 : "memory");
+    return r != 0;
+}
+
 // Head rows into the ring as they are stored.  Whole tiles are boxes of the
-// tensor maps that one warp asks for (a box is at most a block of the pool); tiles
-// that hold keys nobody sees, and pools whose blocks do not divide a tile, are
-// copied row by row with zeros in the place of those keys: a lane owns one key
-// row of its warp, 16 lanes copy 256 bytes (8 lanes 128).  Every warp waits for
-// every stage and signals it, also where one warp copies for all: none may run
-// ahead or fall behind by more than a phase, the parity would not show it.
+// tensor maps that one warp asks for (a box is at most a block of the pool), a run
+// of tiles in a loop of few instructions: a tile's boxes have to go out within the
+// time of its MMAs.  Tiles that hold keys nobody sees, and pools whose blocks do
+// not divide a tile, are copied row by row by all warps with zeros in the place of
+// those keys: a lane owns one key row of its warp, 16 lanes copy 256 bytes (8 lanes
+// 128).  The warps meet after every run, so none waits for a stage that is more than
+// one phase away, which a parity would not show; a warp whose wait ran out goes on to
+// the next meeting, where they all give up.
 template <class G>
 __device__ __forceinline__ void load_heads(const AttnParams &p, const Work &w, uint32_t ring,
-                                                uint32_t bars, int warp, int lane,
-                                                volatile int *abort, bool &bad)
+                                           uint32_t bars, int warp, int lane,
+                                           volatile int *abort, bool &bad)
 {
     constexpr int WARPS = G::LOAD_WARPS, ROWS = G::KT / WARPS; // rows of a warp: 32 or 16
-    const int base = warp * ROWS;
     constexpr int PIECES = G::STAGE / G::KT / 16, PER = 32 / PIECES; // of a row; rows at a time
+    const int base = warp * ROWS;
     const int c = lane & (PIECES - 1), sub = lane / PIECES;
+    const int32_t *const table = p.block_tables + (int64_t)w.seq * p.max_blocks;
     auto whole = [&](int v) { return p.box_rows > 0 && tile_whole<G::KT>(w, real_tile(w, v)); };
-    // the key whose slot this lane looks up: the first of its box, or its row's
-    auto key_at = [&](int v) {
-        const int k0 = real_tile(w, v) * G::KT;
-        return whole(v) ? k0 + min(lane * p.box_rows, G::KT - 1) : k0 + base + (lane & (ROWS - 1));
-    };
-    int32_t next = w.beg < w.end ? key_block(p, w, key_at(w.beg)) : 0;
-    Flights fly;
     Copies copies;
-    int stage = 0, phase = 1;
+    int stage = 0, phase = 1, filled = 0;
     bool ok = true;
-    for (int v = w.beg; ok && v < w.end; ++v) {
-        const int64_t slot = key_slot(p, w, key_at(v), next, bad);
-        if (v + 1 < w.end)
-            next = key_block(p, w, key_at(v + 1));
-        const bool boxes = whole(v);
-        // a bad block reads past the pool: zeros
-        const int row0 = (int)(slot < 0 ? p.num_blocks * p.block : slot);
+    auto next = [&] {
+        ++filled;
+        if (++stage == G::STAGES) {
+            stage = 0;
+            phase ^= 1;
+        }
+    };
+    for (int v = w.beg; v < w.end;) {
+        if (whole(v)) {
+            int last = v + 1;
+            while (last < w.end && whole(last))
+                ++last;
+            copies.flush();
+            if (warp == 0) {
+                // a tile is `per` blocks, or a part of one
+                const int per = G::KT / p.box_rows, in = p.block / p.box_rows;
+                const bool mine = lane < per;
+                auto block_of = [&](int kt) { return in == 1 ? kt * per + lane : kt / in; };
+                int kt = real_tile(w, v);
+                int32_t blk = mine ? __ldg(table + block_of(kt)) : 0;
+                for (int u = v; ok && u < last; ++u) {
+                    const int row = (in == 1 ? 0 : (kt % in) * G::KT) + blk * p.block;
+                    const bool fits = (uint32_t)blk < (uint32_t)p.num_blocks;
+                    bad |= !fits;
+                    const int y = fits ? row : (int)(p.num_blocks * p.block); // else zeros
+                    kt = real_tile(w, u + 1);
+                    if (mine && u + 1 < last)
+                        blk = __ldg(table + block_of(kt));
 #pragma unroll
-        for (int part = 0; part < 2; ++part) { // K, then V
-            const uint32_t full = bars + stage * 8, dst = ring + stage * G::STAGE;
-            copies.before_wait(full + G::STAGES * 8, phase);
-            ok = bar_wait(full + G::STAGES * 8, phase, abort, p.wait_limit_ns);
-            if (!ok)
-                break;
-            fly.filled(stage, boxes, phase ^ 1);
-            if (boxes) {
-                copies.flush();
-                __syncwarp();
-                if (lane == 0)
-                    bar_signal_bulk(full, 32, warp == 0 ? G::STAGE : 0);
-                if (warp == 0) {
-                    if (lane * p.box_rows < G::KT) {
-                        const CUtensorMap *map = part == 0 ? &p.rot_map : &p.copy_map;
-                        const uint32_t at = dst + lane * p.box_rows * 128;
-                        copy_box(at, map, w.head * 128, row0, full);
-                        if (PIECES == 16) // 64 columns of bf16 to a box
-                            copy_box(at + 16384, map, w.head * 128 + 64, row0, full);
+                    for (int part = 0; part < 2; ++part) { // K, then V
+                        const uint32_t full = bars + stage * 8;
+                        ok = ok && bar_wait(full + G::STAGES * 8, phase, abort, p.wait_limit_ns);
+                        if (!ok)
+                            break;
+                        if (lane == 0)
+                            bar_signal_bulk(full, WARPS * 32, G::STAGE);
+                        if (mine) {
+                            const CUtensorMap *map = part == 0 ? &p.rot_map : &p.copy_map;
+                            const uint32_t at = ring + stage * G::STAGE + lane * p.box_rows * 128;
+                            copy_box(at, map, w.head * 128, y, full);
+                            if (PIECES == 16) // 64 columns of bf16 to a box
+                                copy_box(at + 16384, map, w.head * 128 + 64, y, full);
+                        }
+                        next();
                     }
                 }
-            } else {
+            } else { // where warp 0 will be
+                filled += 2 * (last - v);
+                stage += 2 * (last - v);
+                phase ^= (stage / G::STAGES) & 1;
+                stage %= G::STAGES;
+            }
+            v = last;
+            if (load_any<G>(!ok))
+                break;
+            continue;
+        }
+        const int k = real_tile(w, v) * G::KT + base + (lane & (ROWS - 1));
+        const int64_t slot = key_slot(p, w, k, key_block(p, w, k), bad);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            const uint32_t full = bars + stage * 8, dst = ring + stage * G::STAGE;
+            copies.before_wait(full + G::STAGES * 8, phase);
+            ok = ok && bar_wait(full + G::STAGES * 8, phase, abort, p.wait_limit_ns);
+            if (ok) {
                 const char *src = part == 0 ? p.rot : p.copy;
                 const int64_t ss = part == 0 ? p.rot_ss : p.copy_ss;
                 const char *col = src + w.head * PIECES * 16 + c * 16;
@@ -866,16 +900,14 @@ __device__ __forceinline__ void load_heads(const AttnParams &p, const Work &w, u
                            col + (s < 0 ? 0 : s * ss), s < 0 ? 0u : 16u);
                 }
                 copies.filled(full);
-            }
-            if (++stage == G::STAGES) {
-                stage = 0;
-                phase ^= 1;
+                next();
             }
         }
+        ++v;
     }
     copies.flush();
     if (warp == 0)
-        fly.land(bars);
+        copies_land<G::STAGES>(bars, filled);
 }
 
 // Head rows in e4m3: copied as they are stored, RAW tiles ahead, then converted
@@ -1004,7 +1036,7 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
         return whole(v) ? k0 + min(lane * p.box_rows, G::KT - 1) : k0 + base + c;
     };
     int32_t next = w.beg < w.end ? key_block(p, w, key_at(w.beg)) : 0;
-    Flights fly;
+    int filled[2] = {0, 0}; // tiles of each part
     Copies copies;
     bool ok = true;
     for (int v = w.beg; ok && v < w.end; ++v) {
@@ -1035,7 +1067,7 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
             ok = bar_wait(full + 4 * 8, phase, abort, p.wait_limit_ns);
             if (!ok)
                 break;
-            fly.filled(part * 2 + stage, boxes, phase ^ 1);
+            ++filled[part];
             if (boxes) {
                 copies.flush();
                 __syncwarp();
@@ -1070,7 +1102,8 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
     }
     copies.flush();
     if (warp == 0)
-        fly.land(bars);
+        for (int part = 0; part < 2; ++part)
+            copies_land<2>(bars + part * 16, filled[part]);
 }
 
 // MLA rows with an e4m3 latent: the next tile waits in registers.
