@@ -18,9 +18,8 @@
 //   softmax  8 a row tile, two threads to a row, one for each half of its keys: read
 //            the row of S from tensor memory, mask, keep m and l in registers,
 //            write the bf16 weights back over S (they are the A operand of the
-//            second MMA) and at the end O / l.  The two exchange their maxima for
-//            every tile through shared memory: a row's chain of 128 exponentials
-//            in one thread was what the MMAs waited for;
+//            second MMA) and at the end O / l.  They vote for every tile whether a
+//            maximum has outgrown its reference, and exchange maxima only then;
 //   load     bring rows of the pool through the block table into shared memory
 //            in the 128-byte swizzled layout that the MMAs read;
 //   mma      one warp issues every MMA.
@@ -1356,18 +1355,35 @@ struct RowState {
     float sum = 0.0f;      // of this thread's half of the keys
 };
 
-// What the two threads of a row exchange, and a flag by which their warps give up
-// together: a warp whose wait ran out still comes to the next exchange.
-// The maxima alternate between two places from tile to tile; MLA, whose shared memory
-// is full, has one place and a second meeting after it was read.
+// What the two threads of a row exchange.
 template <class G>
 struct RowPairs {
-    static constexpr int PLACES = G::MLA ? 1 : 2;
-    float max[PLACES][2][G::NT * kRows]; // [place][half][row]
-    volatile int failed[8];         // [pair of warps]
+    float value[2][G::NT * kRows]; // [half][row]
 };
 
-__device__ __forceinline__ void pair_sync(int pair) { bar_wait_all(1 + pair, 64); }
+// A vote over the two warps that share 32 rows.  Both come to every vote, also when a
+// wait of one ran out: they go on or give up together.
+__device__ __forceinline__ bool pair_any(int pair, bool x)
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 q, %1, 0;\n"
+                 "barrier.cta.red.or.pred p, %2, 64, q;\nselp.b32 %0, 1, 0, p;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)x), "r"(1 + pair)
+                 : "memory");
+    return r != 0;
+}
+
+// The other thread's value; the place is free again when both have read.
+template <class G>
+__device__ __forceinline__ float pair_swap(RowPairs<G> &pairs, int pair, int half, int row, float x)
+{
+    pairs.value[half][row] = x;
+    bar_wait_all(1 + pair, 64);
+    const float y = pairs.value[half ^ 1][row];
+    bar_wait_all(1 + pair, 64);
+    return y;
+}
 
 // Value `col` of key slot `s` as an fp32 if it is not finite, else 0.
 template <class G>
@@ -1469,40 +1485,34 @@ __device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, 
         for (int j = 0; j < HK / 2; ++j)
             t4[j & 3] = max3(t4[j & 3], __uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
         float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-        const int place = done % RowPairs<G>::PLACES;
-        pairs.max[place][half][t * kRows + r] = top;
-        if (!ok)
-            pairs.failed[pair] = 1;
-        pair_sync(pair);
-        if (pairs.failed[pair])
-            return;
-        top = max3(top, pairs.max[place][half ^ 1][t * kRows + r], st.top);
-        if (RowPairs<G>::PLACES == 1)
-            pair_sync(pair);
-        const bool grew = (top - st.top) * c > kLazy; // also from -inf
-        if (done == 0) {
-            st.top = top;
-        } else if (__any_sync(0xFFFFFFFFu, grew)) {
-            // O of the tiles before is complete: NT = 2 issues it before these scores
-            if (G::NT == 1) {
-                ok = bar_wait(bars + kBarO * 8, (done - 1) & 1, abort, p.wait_limit_ns);
-                mma_fence_after();
-            }
+        bool grew = (top - st.top) * c > kLazy; // also from -inf
+        if (pair_any(pair, grew || !ok)) {
+            if (pair_any(pair, !ok))
+                return;
+            top = fmaxf(top, pair_swap<G>(pairs, pair, half, t * kRows + r, top));
+            grew = (top - st.top) * c > kLazy;
             const float f = grew ? exp2_fast((st.top - top) * c) : 1.0f;
             if (grew) {
                 st.top = top;
                 st.sum *= f;
             }
+            if (done > 0) {
+                // O of the tiles before is complete: NT = 2 issues it before these scores
+                if (G::NT == 1) {
+                    ok = bar_wait(bars + kBarO * 8, (done - 1) & 1, abort, p.wait_limit_ns);
+                    mma_fence_after();
+                }
 #pragma unroll 1
-            for (int i = 0; i < HO; i += 16) {
-                uint32_t o[16];
-                tmem_ld16(o_col + i, o);
-                tmem_ld_wait();
-                tmem_pin16(o);
+                for (int i = 0; i < HO; i += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(o_col + i, o);
+                    tmem_ld_wait();
+                    tmem_pin16(o);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st16(o_col + i, o);
+                    for (int j = 0; j < 16; ++j)
+                        o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                    tmem_st16(o_col + i, o);
+                }
             }
         }
         const float off = st.top == -INFINITY ? 0.0f : -st.top * c;
@@ -1576,15 +1586,10 @@ __device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, 
     // O is complete
     ok = ok && bar_wait(bars + kBarDone * 8, 0, abort, p.wait_limit_ns);
     mma_fence_after();
-    const int place = done % RowPairs<G>::PLACES;
-    pairs.max[place][half][t * kRows + r] = st.sum;
-    if (!ok)
-        pairs.failed[pair] = 1;
-    pair_sync(pair);
-    if (pairs.failed[pair])
+    if (pair_any(pair, !ok))
         return;
-    const float sum = half == 0 ? st.sum + pairs.max[place][1][t * kRows + r]
-                                : pairs.max[place][0][t * kRows + r] + st.sum;
+    const float other = pair_swap<G>(pairs, pair, half, t * kRows + r, st.sum);
+    const float sum = half == 0 ? st.sum + other : other + st.sum; // the same in both
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int h = G::MLA ? g : w.head * p.group + g;
     const int64_t at = (w.q0 + tok) * p.heads + h;
@@ -1695,8 +1700,6 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
             s_status = bad ? kStatusOutOfRange : kStatusOk;
             s_abort = 0;
             s_dirty = 0;
-            for (int i = 0; i < 8; ++i)
-                s_pairs.failed[i] = 0;
             for (int i = 0; i < 2; ++i) { // the warps that have rows signal the weights
                 const int rows = tile_mask(p, w.n, w.len, w.row0 + (G::NT == 2 ? i : 0) * kRows).rows;
                 bar_init(bars + (kBarP + i) * 8, max(1, (rows + 31) / 32) * 64);
