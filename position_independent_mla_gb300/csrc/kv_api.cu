@@ -1303,10 +1303,11 @@ kv_status attn_ok(const kv_attn_desc *a, int64_t total_q, int32_t heads, int32_t
     return heads / kv_heads > 128 ? KV_ERR_UNSUPPORTED : KV_OK;
 }
 
-AttnPlan attn_plan(RowKind kind, const kv_attn_desc *a, int64_t total_q, int32_t heads,
-                   int32_t kv_heads)
+AttnPlan attn_plan(RowKind kind, bool quant, const kv_attn_desc *a, int64_t total_q,
+                   int32_t heads, int32_t kv_heads)
 {
     AttnShape s{};
+    s.quant = quant;
     s.total_q = total_q;
     s.num_seqs = a->num_seqs;
     s.max_q_len = a->max_q_len;
@@ -1318,19 +1319,30 @@ AttnPlan attn_plan(RowKind kind, const kv_attn_desc *a, int64_t total_q, int32_t
     return plan_attention(kind, s);
 }
 
-// Workspace: header, a status word per block, then (keys split) the parts' lse
-// and the parts.
+// Workspace: header, a status word per block, then (keys split) the parts' lse and the
+// parts, then (rows widened) their block table and the rows.
 struct AttnLayout {
-    size_t lse, part, bytes;
+    size_t lse, part, table, rows, bytes;
+    int64_t pad;      // widened rows of a sequence
+    int64_t row_size; // bytes of one
+    int32_t expand_blocks;
 };
 
-AttnLayout attn_layout(RowKind kind, const AttnPlan &pl, int64_t total_q, int32_t heads)
+AttnLayout attn_layout(RowKind kind, const AttnPlan &pl, const kv_attn_desc *a, int64_t total_q,
+                       int32_t heads, int32_t kv_heads)
 {
+    const bool mla = kind == RowKind::Mla;
     const size_t rows = pl.max_splits > 1 ? (size_t)pl.max_splits * total_q * heads : 0;
     AttnLayout l;
-    l.lse = align256(kHeaderBytes + (size_t)pl.blocks * 4);
+    l.pad = (a->max_kv_len + kExpandBlock - 1) / kExpandBlock * kExpandBlock;
+    const int64_t wide = pl.expand ? l.pad * a->num_seqs : 0;
+    l.row_size = mla ? 1152 : kv_heads * 512;
+    l.expand_blocks = wide > 0 ? expand_blocks(wide) : 0;
+    l.lse = align256(kHeaderBytes + (size_t)(pl.blocks + l.expand_blocks) * 4);
     l.part = align256(l.lse + rows * 4);
-    l.bytes = align256(l.part + rows * (kind == RowKind::Mla ? 512 : 128) * 4);
+    l.table = align256(l.part + rows * (mla ? 512 : 128) * 4);
+    l.rows = align256(l.table + (size_t)(wide / kExpandBlock) * 4);
+    l.bytes = align256(l.rows + (size_t)wide * l.row_size);
     return l;
 }
 
@@ -1354,9 +1366,9 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
     if (!aligned16(q) || !aligned16(out) || !aligned_to(lse, 4) || !aligned_to(a->d_q_off, 4) ||
         !aligned_to(a->d_kv_len, 4) || !aligned_to(a->d_block_tables, 4))
         return KV_ERR_INVALID_ARG;
-    const AttnPlan pl = attn_plan(kind, a, total_q, heads, kv_heads);
-    const AttnLayout lay = attn_layout(kind, pl, total_q, heads);
-    if (pl.blocks > 0x7FFFFFFFll)
+    const AttnPlan pl = attn_plan(kind, quant != nullptr, a, total_q, heads, kv_heads);
+    const AttnLayout lay = attn_layout(kind, pl, a, total_q, heads, kv_heads);
+    if (pl.blocks > 0x7FFFFFFFll || num_slots > 0x7FFFFFFFll)
         return KV_ERR_INVALID_ARG;
     if ((st = ws_ok(ws, ws_bytes, lay.bytes)) != KV_OK)
         return st;
@@ -1396,6 +1408,7 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
     p.max_q_len = a->max_q_len;
     p.max_kv_len = a->max_kv_len;
     p.max_blocks = a->max_blocks;
+    p.max_keys = (int64_t)a->max_blocks * block;
     p.q_off = a->d_q_off;
     p.kv_len = a->d_kv_len;
     p.block_tables = a->d_block_tables;
@@ -1409,7 +1422,44 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
     p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + lay.part);
     p.wait_limit_ns = g_wait_limit_ns.load();
     p.header = static_cast<uint32_t *>(ws);
+    p.status_words = (uint32_t)(pl.blocks + lay.expand_blocks);
     KV_CUDA(mark(t_ev_start, stream));
+    if (lay.expand_blocks > 0) {
+        const bool mla = kind == RowKind::Mla;
+        char *const base = static_cast<char *>(ws) + lay.rows;
+        ExpandParams e{};
+        e.rows.copy = base;
+        e.rows.rot = base + (mla ? 1024 : lay.row_size / 2);
+        e.rows.copy_ss = e.rows.rot_ss = lay.row_size;
+        e.pool = *quant;
+        e.pad = lay.pad;
+        e.num_blocks = p.num_blocks;
+        e.block = block;
+        e.num_seqs = a->num_seqs;
+        e.max_kv_len = a->max_kv_len;
+        e.max_blocks = a->max_blocks;
+        e.window = a->window;
+        e.sinks = a->sinks;
+        e.q_off = a->d_q_off;
+        e.kv_len = a->d_kv_len;
+        e.block_tables = a->d_block_tables;
+        e.table = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + lay.table);
+        e.status = p.header + kHeaderBytes / 4 + pl.blocks;
+        e.blocks = lay.expand_blocks;
+        KV_CUDA(launch_expand(e, kind, stream));
+        ++t_launches;
+        // the attention reads the widened rows through a table of their own; what it
+        // says of lengths is said of the caller's table above
+        p.copy = e.rows.copy;
+        p.rot = e.rows.rot;
+        p.copy_ss = p.rot_ss = lay.row_size;
+        p.cs = p.rs = nullptr;
+        p.block = kExpandBlock;
+        p.block_tables = e.table;
+        p.num_blocks = lay.pad / kExpandBlock * a->num_seqs;
+        p.max_keys = std::min<int64_t>((int64_t)p.max_blocks * block, lay.pad);
+        p.max_blocks = (int32_t)(lay.pad / kExpandBlock);
+    }
     KV_CUDA(launch_attention(p, kind, pl, stream));
     t_launches += pl.max_splits > 1 ? 2 : 1;
     KV_CUDA(mark(t_ev_stop, stream));
@@ -1450,8 +1500,8 @@ size_t kv_attention_workspace_size(const kv_pool_desc *pool, const kv_attn_desc 
     if (!pool_ok(pool) || !row_kind(pool, &kind) ||
         attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK)
         return 0;
-    return attn_layout(kind, attn_plan(kind, attn, total_q, num_heads, pool->rot_heads), total_q,
-                       num_heads)
+    return attn_layout(kind, attn_plan(kind, false, attn, total_q, num_heads, pool->rot_heads), attn,
+                       total_q, num_heads, pool->rot_heads)
         .bytes;
 }
 
@@ -1462,8 +1512,8 @@ size_t kv_attention_quant_workspace_size(const kv_quant_pool_desc *pool, const k
     if (!quant_pool_ok(pool) || !quant_row_kind(pool, &kind) ||
         attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK)
         return 0;
-    return attn_layout(kind, attn_plan(kind, attn, total_q, num_heads, pool->rot_heads), total_q,
-                       num_heads)
+    return attn_layout(kind, attn_plan(kind, true, attn, total_q, num_heads, pool->rot_heads), attn,
+                       total_q, num_heads, pool->rot_heads)
         .bytes;
 }
 

@@ -47,6 +47,7 @@ namespace kvr {
 namespace {
 
 constexpr int kRows = 128;         // rows per tile: the M of an MMA
+constexpr int64_t kExpandBytes = int64_t(2) << 30; // largest workspace for widened rows
 constexpr float kLazy = 8.0f;      // log2 of the growth of a maximum that O tolerates
 
 // ---------------------------------------------------------------------------
@@ -455,11 +456,12 @@ struct HeadGeo {
     static constexpr int NT = NT_, KT = 128;
     static constexpr int QPANELS = 2, OC = 128;    // query panels in shared memory; columns of O
     static constexpr int DV = 128;
+    static_assert(NT == 1 || !QUANT, "e4m3 rows are widened before two row tiles read them");
     static constexpr int SOFT_WARPS = 8 * NT, LOAD_WARPS = NT == 2 ? 4 : 8;
     static constexpr int STAGE = 2 * 128 * 128;    // bytes of a K or V tile
     // e4m3: RAW tiles of K or V as they are stored, and their scales, wait in
     // shared memory to be converted
-    static constexpr int RAW = !QUANT ? 0 : NT == 2 ? 3 : 5;
+    static constexpr int RAW = QUANT ? 5 : 0;
     static constexpr int STAGES = QUANT ? 3 : NT == 2 ? 4 : 5;
     static constexpr int BARS = 2 * STAGES;
     static constexpr int RAW_AT = STAGES * STAGE, RAW_STAGE = STAGE / 2 + 512;
@@ -601,6 +603,17 @@ __device__ __forceinline__ int real_tile(const Work &w, int v)
     return v < w.sink_tiles ? v : w.first + v - w.sink_tiles;
 }
 
+// The block's share of nv key tiles: as many equal runs as runs of split_tiles would be.
+// False where there is none.
+__device__ __forceinline__ bool take_split(const AttnParams &p, int nv, Work &w)
+{
+    w.splits = max(1, (nv + p.split_tiles - 1) / p.split_tiles);
+    const int run = (nv + w.splits - 1) / w.splits;
+    w.beg = min(nv, w.split * run);
+    w.end = min(nv, w.beg + run);
+    return w.split < w.splits;
+}
+
 // Lengths of sequence s; false when they do not fit what the call stated.
 __device__ __forceinline__ bool seq_queries(const AttnParams &p, int s, int64_t &q0, int &n)
 {
@@ -617,7 +630,7 @@ __device__ __forceinline__ bool seq_queries(const AttnParams &p, int s, int64_t 
 __device__ __forceinline__ bool seq_keys(const AttnParams &p, int s, int &len)
 {
     len = p.kv_len[s];
-    return len >= 0 && len <= p.max_kv_len && (int64_t)len <= (int64_t)p.max_blocks * p.block;
+    return len >= 0 && len <= p.max_kv_len && (int64_t)len <= p.max_keys;
 }
 
 // Row tile `tile` of the call -> sequence, its queries and keys, and the row tile
@@ -1689,10 +1702,7 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
         if (go) {
             w.row0 = at * kRows * G::NT;
             const int nv = key_tiles<G::KT, G::NT>(p, w);
-            w.splits = max(1, (nv + p.split_tiles - 1) / p.split_tiles);
-            w.beg = w.split * p.split_tiles;
-            w.end = min(nv, w.beg + p.split_tiles);
-            go = w.split < w.splits;
+            go = take_split(p, nv, w);
         }
         if (lane == 0) {
             s_work = w;
@@ -1791,7 +1801,7 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
     if (warp == kMmaWarp<G>)
         tmem_free(tmem, 512);
     if (tid == 0)
-        write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, gridDim.x);
+        write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, p.status_words);
 }
 
 // ---------------------------------------------------------------------------
@@ -2225,16 +2235,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
     }
     if (go) {
         const int nv = key_tiles<G::KT, 1>(p, w);
-        w.splits = max(1, (nv + p.split_tiles - 1) / p.split_tiles);
-        w.beg = w.split * p.split_tiles;
-        w.end = min(nv, w.beg + p.split_tiles);
-        go = w.split < w.splits;
+        go = take_split(p, nv, w);
     }
     if (!go) {
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (tid == 0)
             write_block_status(p.header, bad ? kStatusOutOfRange : kStatusOk, blockIdx.x,
-                               gridDim.x);
+                               p.status_words);
         return;
     }
     if (tid == 0) {
@@ -2307,7 +2314,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
     if (warp == 8)
         tmem_free(tmem, G::COLS);
     if (tid == 0)
-        write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, gridDim.x);
+        write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, p.status_words);
 }
 
 // Joins the parts of rows whose keys were split: a warp per (token, head).
@@ -2497,7 +2504,13 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
     const int64_t kt = mla ? 64 : 128;
     AttnPlan pl{};
     const bool few = !mla && a.max_q_len <= 1 && a.group <= kFewRows;
-    pl.row_tiles = few ? 0 : !mla && (int64_t)a.max_q_len * a.group > kRows ? 2 : 1;
+    // More than one row tile to a sequence: e4m3 rows are widened once, in a pass of
+    // their own, where the workspace for that stays moderate.  8 chunks of up to 513
+    // tokens x 28 heads: 265 us when every tile widened them; an MLA batch 372 us.
+    const bool tiles_share = (int64_t)a.max_q_len * a.group > kRows;
+    const int64_t rows_bytes = (int64_t)a.num_seqs * a.max_kv_len * (mla ? 1152 : a.kv_heads * 512);
+    pl.expand = a.quant && tiles_share && rows_bytes <= kExpandBytes;
+    pl.row_tiles = few ? 0 : !mla && tiles_share && (!a.quant || pl.expand) ? 2 : 1;
     const int64_t rows = kRows * std::max(1, pl.row_tiles);
     // row tiles over all sequences: at most one partly filled one each
     const int64_t tiles = few ? a.num_seqs : a.total_q * a.group / rows + a.num_seqs;
@@ -2513,8 +2526,11 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
     nv = std::max<int64_t>(nv, 1);
     // pieces of the key axis: enough blocks for a few on every SM, none shorter
     // than four tiles (a block's start and end cost about as much as two)
-    const int64_t slots = (few ? 2 * 152 : 152) * 4;
-    const int64_t want = std::max<int64_t>(4, (units * nv + slots - 1) / slots);
+    // (whole rows when there are units for two rounds, and their parts need no joining)
+    const int64_t slots = few ? 2 * 152 : 152;
+    const int64_t want = units >= 2 * slots && !few
+                             ? nv
+                             : std::max<int64_t>(4, (units * nv + 4 * slots - 1) / (4 * slots));
     pl.split_tiles = (int32_t)std::min(nv, want);
     pl.max_splits = (int32_t)((nv + pl.split_tiles - 1) / pl.split_tiles);
     pl.blocks = units * pl.max_splits;
@@ -2534,8 +2550,7 @@ cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cu
         return quant ? launch_few<FewGeo<true, 16>>(p, pl.blocks, stream)
                      : launch_few<FewGeo<false, 16>>(p, pl.blocks, stream);
     if (pl.row_tiles == 2)
-        return quant ? launch<HeadGeo<true, 2>>(p, pl.blocks, stream)
-                     : launch<HeadGeo<false, 2>>(p, pl.blocks, stream);
+        return launch<HeadGeo<false, 2>>(p, pl.blocks, stream);
     return quant ? launch<HeadGeo<true, 1>>(p, pl.blocks, stream)
                  : launch<HeadGeo<false, 1>>(p, pl.blocks, stream);
 }

@@ -129,8 +129,8 @@ __device__ __forceinline__ uint4 value_piece(uint2 v, float s)
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// A run of values of one row: bf16 at `rows`, e4m3 at `pool` with its scales.  NULL:
-// skipped.
+// A run of values of one row: bf16 at `rows` (NULL: skipped), e4m3 at `pool` (NULL, read
+// back only: zeros) with its scales.
 struct Segment {
     char *rows, *pool;
     float *scale;
@@ -171,21 +171,21 @@ __device__ __forceinline__ void quantise(const Segment (&seg)[N], int lane)
     }
 }
 
-// Read N segments back.
-template <int NP, int N>
+// Read N segments back; KEEP: into rows that are read again soon.
+template <int NP, int N, bool KEEP>
 __device__ __forceinline__ void dequantise(const Segment (&seg)[N], int lane)
 {
     constexpr int IT = NP / 32, B = IT * N > 8 ? 8 / N : IT;
 #pragma unroll 1
     for (int b = 0; b < IT; b += B) {
-        uint2 v[N][B];
-        float s[N][B];
+        uint2 v[N][B] = {};
+        float s[N][B] = {};
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int i = 0; i < B; ++i) {
                 const int at = (b + i) * 32 + lane;
-                if (seg[n].rows) {
+                if (seg[n].rows && seg[n].pool) {
                     v[n][i] = __ldcs(reinterpret_cast<const uint2 *>(seg[n].pool + at * 8));
                     s[n][i] = __ldg(seg[n].scale + (at >> 4));
                 }
@@ -194,9 +194,59 @@ __device__ __forceinline__ void dequantise(const Segment (&seg)[N], int lane)
         for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int i = 0; i < B; ++i)
-                if (seg[n].rows)
-                    st_stream(seg[n].rows + ((b + i) * 32 + lane) * 16,
-                              value_piece(v[n][i], s[n][i]));
+                if (seg[n].rows) {
+                    char *const to = seg[n].rows + ((b + i) * 32 + lane) * 16;
+                    if (KEEP)
+                        *reinterpret_cast<uint4 *>(to) = value_piece(v[n][i], s[n][i]);
+                    else
+                        st_stream(to, value_piece(v[n][i], s[n][i]));
+                }
+    }
+}
+
+// What to do with a unit of rows: write them into the pool, read them back, or read
+// them back for kernels that follow.
+enum class Move { Write, Read, Keep };
+
+// One unit of R::ROWS rows of layer l: row lane % ROWS has slot rs of `rows` (-1:
+// skipped) and ps of `pool` (-1, reading: zeros).
+template <class R, Move M>
+__device__ __forceinline__ void move_unit(const PoolView &rows, const QuantView &pool, int64_t l,
+                                          int64_t rs, int64_t ps, int lane)
+{
+    constexpr int ROWS = R::ROWS;
+    char *const rc = rows.copy + l * rows.copy_ls, *const rr = rows.rot + l * rows.rot_ls;
+    char *const pc = pool.copy + l * pool.copy_ls, *const pr = pool.rot + l * pool.rot_ls;
+    Segment seg[R::SEGS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int64_t a = __shfl_sync(0xFFFFFFFFu, rs, r), b = __shfl_sync(0xFFFFFFFFu, ps, r);
+        const bool row = a >= 0, old = b >= 0;
+        seg[r] = {row ? rc + a * rows.copy_ss : nullptr, old ? pc + b * pool.copy_ss : nullptr,
+                  pool.cs + l * pool.cs_ls + b * pool.cs_ss};
+        if constexpr (R::ROTQ)
+            seg[ROWS + r] = {row ? rr + a * rows.rot_ss : nullptr,
+                             old ? pr + b * pool.rot_ss : nullptr,
+                             pool.rs + l * pool.rs_ls + b * pool.rs_ss};
+    }
+    // MLA: 8 lanes to the k_pe of a row
+    const int64_t ka = __shfl_sync(0xFFFFFFFFu, rs, lane >> 3);
+    const int64_t kb = __shfl_sync(0xFFFFFFFFu, ps, lane >> 3);
+    const bool has_pe = !R::ROTQ && lane < ROWS * 8 && ka >= 0;
+    char *const kr = rr + ka * rows.rot_ss + (lane & 7) * 16;
+    char *const kp = pr + kb * pool.rot_ss + (lane & 7) * 16;
+    uint4 pe = make_uint4(0, 0, 0, 0);
+    if (has_pe && (M == Move::Write || kb >= 0))
+        pe = ld_stream(M == Move::Write ? kr : kp);
+    if constexpr (M == Move::Write)
+        quantise<R::CP>(seg, lane);
+    else
+        dequantise<R::CP, R::SEGS, M == Move::Keep>(seg, lane);
+    if (has_pe) {
+        if (M == Move::Read)
+            st_stream(kr, pe);
+        else
+            *reinterpret_cast<uint4 *>(M == Move::Write ? kp : kr) = pe;
     }
 }
 
@@ -222,42 +272,60 @@ __global__ void __launch_bounds__(kQuantThreads) quant_kernel(const __grid_const
                 rs = -1;
             }
         }
-        char *const rc = p.rows.copy + l * p.rows.copy_ls, *const rr = p.rows.rot + l * p.rows.rot_ls;
-        char *const pc = p.pool.copy + l * p.pool.copy_ls, *const pr = p.pool.rot + l * p.pool.rot_ls;
-        Segment seg[R::SEGS];
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            const int64_t a = __shfl_sync(0xFFFFFFFFu, rs, r), b = __shfl_sync(0xFFFFFFFFu, ps, r);
-            const bool ok = a >= 0;
-            seg[r] = {ok ? rc + a * p.rows.copy_ss : nullptr, pc + b * p.pool.copy_ss,
-                      p.pool.cs + l * p.pool.cs_ls + b * p.pool.cs_ss};
-            if constexpr (R::ROTQ)
-                seg[ROWS + r] = {ok ? rr + a * p.rows.rot_ss : nullptr, pr + b * p.pool.rot_ss,
-                                 p.pool.rs + l * p.pool.rs_ls + b * p.pool.rs_ss};
-        }
-        // MLA: 8 lanes to the k_pe of a row
-        const int64_t ka = __shfl_sync(0xFFFFFFFFu, rs, lane >> 3);
-        const int64_t kb = __shfl_sync(0xFFFFFFFFu, ps, lane >> 3);
-        const bool has_pe = !R::ROTQ && lane < ROWS * 8 && ka >= 0;
-        char *const kr = rr + ka * p.rows.rot_ss + (lane & 7) * 16;
-        char *const kp = pr + kb * p.pool.rot_ss + (lane & 7) * 16;
-        uint4 pe = make_uint4(0, 0, 0, 0);
-        if (has_pe)
-            pe = ld_stream(READ ? kp : kr);
-        if constexpr (READ)
-            dequantise<R::CP>(seg, lane);
-        else
-            quantise<R::CP>(seg, lane);
-        if (has_pe) {
-            if (READ)
-                st_stream(kr, pe);
-            else
-                *reinterpret_cast<uint4 *>(kp) = pe;
-        }
+        move_unit<R, READ ? Move::Read : Move::Write>(p.rows, p.pool, l, rs, ps, lane);
     }
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0)
         write_block_status(p.header, bad ? kStatusOutOfRange : kStatusOk, blockIdx.x, gridDim.x);
+}
+
+// The cached rows of a batch that its queries see, as bf16 rows: key k of sequence s
+// goes to row s * p.pad + k.  Rows of a bad block become zeros.  Also writes the block
+// table of those rows.
+template <class R>
+__global__ void __launch_bounds__(kQuantThreads) expand_kernel(const __grid_constant__ ExpandParams p)
+{
+    constexpr int ROWS = R::ROWS;
+    const int lane = threadIdx.x & 31;
+    const int64_t total = (int64_t)p.num_seqs * p.pad / ROWS;
+    const int64_t step = (int64_t)gridDim.x * (kQuantThreads / 32);
+    int bad = 0;
+    for (int64_t i = (int64_t)blockIdx.x * kQuantThreads + threadIdx.x;
+         i < (int64_t)p.num_seqs * (p.pad / kExpandBlock); i += (int64_t)gridDim.x * kQuantThreads)
+        p.table[i] = (int32_t)i;
+    for (int64_t u = (int64_t)blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5); u < total;
+         u += step) {
+        const int64_t row = u * ROWS + (lane & (ROWS - 1));
+        const int s = (int)(u * ROWS / p.pad), k = (int)(row - (int64_t)s * p.pad);
+        const int n = p.q_off[s + 1] - p.q_off[s], len = p.kv_len[s];
+        // sequences whose lengths do not fit are left to the attention kernel
+        const bool fits = n > 0 && len >= 0 && len <= p.max_kv_len &&
+                          (int64_t)len <= (int64_t)p.max_blocks * p.block;
+        const int lo = p.window ? len - n - p.window + 1 : 0;
+        const bool seen = fits && k < len && (k >= lo || k < p.sinks);
+        if (!__any_sync(0xFFFFFFFFu, seen))
+            continue;
+        int64_t ps = -1;
+        if (seen) {
+            const int b = (int)((uint32_t)k / (uint32_t)p.block);
+            const int32_t blk = p.block_tables[(int64_t)s * p.max_blocks + b];
+            if (blk < 0 || blk >= p.num_blocks)
+                bad = 1;
+            else
+                ps = (int64_t)blk * p.block + (k - b * p.block);
+        }
+        move_unit<R, Move::Keep>(p.rows, p.pool, 0, seen ? row : -1, ps, lane);
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0)
+        p.status[blockIdx.x] = bad ? kStatusOutOfRange : kStatusOk;
+}
+
+template <class R>
+cudaError_t launch_expand_row(const ExpandParams &p, cudaStream_t stream)
+{
+    expand_kernel<R><<<p.blocks, kQuantThreads, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 template <class R, bool READ>
@@ -302,6 +370,27 @@ cudaError_t launch_quantize(const QuantParams &p, RowKind kind, cudaStream_t str
 cudaError_t launch_dequantize(const QuantParams &p, RowKind kind, cudaStream_t stream)
 {
     return launch<true>(p, kind, stream);
+}
+
+int expand_blocks(int64_t rows)
+{
+    const int64_t want = (rows + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
+    return (int)(want < kQuantMaxBlocks ? want : kQuantMaxBlocks);
+}
+
+cudaError_t launch_expand(const ExpandParams &p, RowKind kind, cudaStream_t stream)
+{
+    switch (kind) {
+    case RowKind::Mla:
+        return launch_expand_row<QRow<512, 64, false, 2>>(p, stream);
+    case RowKind::Gqa:
+        return launch_expand_row<QRow<1024, 1024, true, 1>>(p, stream);
+    case RowKind::Gqa4:
+        return launch_expand_row<QRow<512, 512, true, 2>>(p, stream);
+    case RowKind::Mha:
+        return launch_expand_row<QRow<4096, 4096, true, 1>>(p, stream);
+    }
+    return cudaErrorInvalidValue;
 }
 
 } // namespace kvr

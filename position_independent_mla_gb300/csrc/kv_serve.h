@@ -54,6 +54,25 @@ cudaError_t launch_quantize(const QuantParams &p, RowKind kind, cudaStream_t str
 cudaError_t launch_dequantize(const QuantParams &p, RowKind kind, cudaStream_t stream);
 constexpr int kQuantMaxBlocks = 152 * 8; // persistent grid of both
 
+// Rows of a quantised pool that a batch attends to, widened once into bf16 rows of
+// the workspace for row tiles that would each convert them again.
+constexpr int kExpandBlock = 64; // block size of the rows it writes
+
+struct ExpandParams {
+    PoolView rows;  // written: [num_seqs][pad] rows
+    QuantView pool; // at the layer of the call
+    int64_t pad;    // rows of a sequence: a multiple of kExpandBlock
+    int64_t num_blocks;
+    int32_t block, num_seqs, max_kv_len, max_blocks, window, sinks;
+    const int32_t *q_off, *kv_len, *block_tables;
+    int32_t *table;   // written: [num_seqs][pad / kExpandBlock]
+    uint32_t *status; // a word per block
+    int32_t blocks;
+};
+
+int expand_blocks(int64_t rows); // blocks of a launch over so many rows
+cudaError_t launch_expand(const ExpandParams &p, RowKind kind, cudaStream_t stream);
+
 struct AttnParams {
     // one layer of the pool: bf16 rows, or e4m3 rows with scales (cs != nullptr)
     const char *copy, *rot;
@@ -71,6 +90,7 @@ struct AttnParams {
     int64_t total_q;
     int32_t heads, group; // query heads; query heads per key head
     int32_t num_seqs, max_q_len, max_kv_len, max_blocks;
+    int64_t max_keys; // that a block-table row of the caller holds
     const int32_t *q_off, *kv_len, *block_tables;
     int32_t causal, window, sinks;
     float scale;
@@ -79,6 +99,7 @@ struct AttnParams {
     float *part, *part_lse; // [max_splits][total_q][heads][value width], [..][heads]
     int64_t wait_limit_ns;
     uint32_t *header;
+    uint32_t status_words; // of the call: this kernel's blocks, and those of an expansion
     // bf16 pools, filled in by launch_attention: rows of a box (0: no boxes)
     int32_t box_rows;
     CUtensorMap copy_map, rot_map;
@@ -86,12 +107,14 @@ struct AttnParams {
 
 // Sizes of a call that the host knows, and the launch they lead to.
 struct AttnShape {
+    bool quant;
     int64_t total_q;
     int32_t num_seqs, max_q_len, max_kv_len, window, sinks;
     int32_t group, kv_heads;
 };
 
 struct AttnPlan {
+    bool expand;         // e4m3 rows are widened first
     int32_t row_tiles;   // 128-row tiles of a block; 0: the kernel for few rows
     int32_t split_tiles; // key tiles of a block
     int32_t max_splits;
