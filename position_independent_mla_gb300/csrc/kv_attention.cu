@@ -1032,9 +1032,13 @@ __device__ __forceinline__ void load_heads_e4m3(const AttnParams &p, const Work 
     }
 }
 
-// MLA rows in bf16: boxes for whole tiles, else row by row with zeros in the
-// place of keys that nobody sees.  Part 0: the other half's panels and k_pe,
-// part 1: this half's.  A warp owns 8 rows; 8 lanes copy 128 bytes of a row.
+// MLA rows in bf16.  Part 0: the other half's panels and k_pe, part 1: this half's.  In a
+// run of whole tiles one warp asks for the boxes of each part, so that part 0 of the
+// next tile, whose stage is free after the scores, does not wait for part 1 of this
+// one, and a third brings this half's columns of a later tile to L2: a stage is free
+// little more than a tile ahead, less than HBM takes.  Other tiles are copied row by
+// row, with zeros in the place of keys that nobody sees: a warp owns 8 rows, 8 lanes
+// copy 128 bytes of a row.  The warps meet after every run (see load_heads).
 template <class G>
 __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w, uint32_t ring,
                                               uint32_t bars, int warp, int lane,
@@ -1042,80 +1046,98 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
 {
     constexpr int AHEAD = 3;
     const int base = warp * 8, c = lane & 7, sub = lane >> 3;
+    const int32_t *const table = p.block_tables + (int64_t)w.seq * p.max_blocks;
     auto whole = [&](int v) { return p.box_rows > 0 && tile_whole<G::KT>(w, real_tile(w, v)); };
-    auto key_at = [&](int v) {
-        const int k0 = real_tile(w, v) * G::KT;
-        return whole(v) ? k0 + min(lane * p.box_rows, G::KT - 1) : k0 + base + c;
-    };
-    int32_t next = w.beg < w.end ? key_block(p, w, key_at(w.beg)) : 0;
-    int filled[2] = {0, 0}; // tiles of each part
     Copies copies;
     bool ok = true;
-    for (int v = w.beg; ok && v < w.end; ++v) {
-        const int64_t slot = key_slot(p, w, key_at(v), next, bad);
-        if (v + 1 < w.end)
-            next = key_block(p, w, key_at(v + 1));
-        const bool boxes = whole(v);
-        const int row0 = (int)(slot < 0 ? p.num_blocks * p.block : slot);
-        const int ord = v - w.beg, stage = ord & 1, phase = ((ord >> 1) & 1) ^ 1;
-        // a tile's copies are asked for little more than a tile ahead, less than HBM
-        // takes: another warp brings this half's columns to L2 before
-        if (warp == 1 && v + AHEAD < w.end && whole(v + AHEAD) && lane * p.box_rows < G::KT) {
-            const int k = key_at(v + AHEAD);
-            const int64_t at = key_slot(p, w, k, key_block(p, w, k), bad);
-            if (at >= 0) {
+    int v = w.beg;
+    while (v < w.end) {
+        if (whole(v)) {
+            int last = v + 1;
+            while (last < w.end && whole(last))
+                ++last;
+            copies.flush();
+            if (warp < 3) {
+                // a tile is `per` blocks, or a part of one; warp 2 is AHEAD of the others
+                const int per = G::KT / p.box_rows, in = p.block / p.box_rows;
+                const int skip = warp == 2 ? AHEAD : 0, part = warp == 0 ? 0 : 1;
+                const int half = part == 0 ? 1 - w.head : w.head;
+                const bool mine = lane < per;
+                auto ask = [&](int u) {
+                    const int kt = real_tile(w, u);
+                    return mine && u < last ? __ldg(table + (in == 1 ? kt * per + lane : kt / in)) : 0;
+                };
+                int32_t blk = ask(v + skip);
+                for (int u = v; ok && u < last; ++u) {
+                    const int kt = real_tile(w, u + skip);
+                    const bool fits = (uint32_t)blk < (uint32_t)p.num_blocks;
+                    bad |= !fits;
+                    const int y = fits ? (in == 1 ? 0 : (kt % in) * G::KT) + blk * p.block
+                                       : (int)(p.num_blocks * p.block); // past the pool: zeros
+                    blk = ask(u + 1 + skip);
+                    const int ord = u - w.beg, stage = ord & 1, phase = ((ord >> 1) & 1) ^ 1;
+                    const uint32_t full = bars + (part * 2 + stage) * 8;
+                    ok = bar_wait(full + 4 * 8, phase, abort, p.wait_limit_ns);
+                    if (!ok)
+                        break;
+                    if (warp == 2) {
+                        if (mine && u + skip < last) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    prefetch_box(&p.copy_map, w.head * 256 + i * 64, (int)at);
-                if (w.head == 0)
-                    prefetch_box(&p.rot_map, 0, (int)at);
+                            for (int i = 0; i < 4; ++i)
+                                prefetch_box(&p.copy_map, half * 256 + i * 64, y);
+                            if (w.head == 0)
+                                prefetch_box(&p.rot_map, 0, y);
+                        }
+                        continue;
+                    }
+                    if (lane == 0)
+                        bar_signal_bulk(full, G::LOAD_WARPS * 32, part == 0 ? G::OTHER : G::OWN);
+                    if (mine) {
+                        const uint32_t at = G::part(ring, part, stage) + lane * p.box_rows * 128;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            copy_box(at + i * G::PANEL, &p.copy_map, half * 256 + i * 64, y, full);
+                        if (part == 0)
+                            copy_box(at + 4 * G::PANEL, &p.rot_map, 0, y, full);
+                    }
+                }
             }
+            v = last;
+            if (load_any<G>(!ok))
+                break;
+            continue;
         }
+        const int k = real_tile(w, v) * G::KT + base + c;
+        const int64_t slot = key_slot(p, w, k, key_block(p, w, k), bad);
+        const int ord = v - w.beg, stage = ord & 1, phase = ((ord >> 1) & 1) ^ 1;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
             const uint32_t full = bars + (part * 2 + stage) * 8, dst = G::part(ring, part, stage);
             const int half = part == 0 ? 1 - w.head : w.head;
             copies.before_wait(full + 4 * 8, phase);
-            ok = bar_wait(full + 4 * 8, phase, abort, p.wait_limit_ns);
+            ok = ok && bar_wait(full + 4 * 8, phase, abort, p.wait_limit_ns);
             if (!ok)
-                break;
-            ++filled[part];
-            if (boxes) {
-                copies.flush();
-                __syncwarp();
-                if (lane == 0)
-                    bar_signal_bulk(full, 32, warp != 0 ? 0 : part == 0 ? G::OTHER : G::OWN);
-                if (warp == 0) {
-                    if (lane * p.box_rows < G::KT) {
-                        const uint32_t at = dst + lane * p.box_rows * 128;
+                continue;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            copy_box(at + i * G::PANEL, &p.copy_map, half * 256 + i * 64, row0, full);
-                        if (part == 0)
-                            copy_box(at + 4 * G::PANEL, &p.rot_map, 0, row0, full);
-                    }
-                }
-            } else {
+            for (int i = 0; i < 2; ++i) {
+                const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, i * 4 + sub);
+                const int row = base + i * 4 + sub;
+                const uint32_t at = dst + row * 128 + ((c ^ (row & 7)) << 4), n = s < 0 ? 0 : 16;
+                const char *src = p.copy + (s < 0 ? 0 : s * p.copy_ss) + half * 512 + c * 16;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, i * 4 + sub);
-                    const int row = base + i * 4 + sub;
-                    const uint32_t at = dst + row * 128 + ((c ^ (row & 7)) << 4), n = s < 0 ? 0 : 16;
-                    const char *src = p.copy + (s < 0 ? 0 : s * p.copy_ss) + half * 512 + c * 16;
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        copy16(at + g * G::PANEL, src + g * 128, n);
-                    if (part == 0)
-                        copy16(at + 4 * G::PANEL, p.rot + (s < 0 ? 0 : s * p.rot_ss) + c * 16, n);
-                }
-                copies.filled(full);
+                for (int g = 0; g < 4; ++g)
+                    copy16(at + g * G::PANEL, src + g * 128, n);
+                if (part == 0)
+                    copy16(at + 4 * G::PANEL, p.rot + (s < 0 ? 0 : s * p.rot_ss) + c * 16, n);
             }
+            copies.filled(full);
         }
+        ++v;
     }
     copies.flush();
-    if (warp == 0)
+    if (warp == 0) // the last tiles of both parts; after an early end some never come
         for (int part = 0; part < 2; ++part)
-            copies_land<2>(bars + part * 16, filled[part]);
+            copies_land<2>(bars + part * 16, v - w.beg);
 }
 
 // MLA rows with an e4m3 latent: the next tile waits in registers.
