@@ -474,8 +474,9 @@ struct HeadGeo {
 // MLA rows: a tile of 64 latent rows is both K (9 panels: 512 + 64 columns) and
 // V; a block makes one half of the 512 value columns (O of 128 x 512 fp32 would
 // fill tensor memory).  The value panels of this half (4) serve both products
-// and live longer than the other 5 panels, so the two kinds have rings of their
-// own, two tiles each.  Query panels: those of this half stay in tensor memory
+// and live longer than the other 5 panels, so they have rings of their own, two tiles
+// each, and are halved again: the values' product of one pair of panels frees them while
+// the other pair's runs.  Query panels: those of this half stay in tensor memory
 // (they fit beside O and two S), the other five in shared memory.
 template <bool QUANT_>
 struct MlaGeo {
@@ -487,15 +488,15 @@ struct MlaGeo {
     static constexpr int SOFT_WARPS = 8, LOAD_WARPS = QUANT ? 16 : 8;
     static constexpr int PANEL = 64 * 128;
     static constexpr int OTHER = 5 * PANEL, OWN = 4 * PANEL; // bytes of a tile's parts
-    static constexpr int BARS = 8; // full, empty of two stages of two parts
+    static constexpr int PARTS = 3; // the other half and k_pe; two pairs of this half
+    static constexpr int BARS = 4 * PARTS; // full, empty of two stages of each
     static constexpr int RING = 2 * (OTHER + OWN);
     static constexpr int S_COL(int i) { return 256 + i * 64; }
     static constexpr int O_COL(int) { return 0; }
     static constexpr int Q_COL = 384;
-    // addresses of part 0 (other half, k_pe) and 1 (this half) of stage i
     __device__ static uint32_t part(uint32_t ring, int which, int i)
     {
-        return ring + (which == 0 ? i * OTHER : 2 * OTHER + i * OWN);
+        return ring + (which == 0 ? i * OTHER : 2 * OTHER + i * OWN + (which - 1) * 2 * PANEL);
     }
 };
 
@@ -1032,11 +1033,10 @@ __device__ __forceinline__ void load_heads_e4m3(const AttnParams &p, const Work 
     }
 }
 
-// MLA rows in bf16.  Part 0: the other half's panels and k_pe, part 1: this half's.  In a
-// run of whole tiles one warp asks for the boxes of each part, so that part 0 of the
-// next tile, whose stage is free after the scores, does not wait for part 1 of this
-// one, and a third brings this half's columns of a later tile to L2: a stage is free
-// little more than a tile ahead, less than HBM takes.  Other tiles are copied row by
+// MLA rows in bf16.  In a run of whole tiles a warp for each part asks for its boxes, so
+// that part 0 of the next tile, whose stage is free after the scores, does not wait for
+// the others of this one, and a fourth brings this half's columns of a later tile to L2: a
+// stage is free little more than a tile ahead, less than HBM takes.  Other tiles are copied row by
 // row, with zeros in the place of keys that nobody sees: a warp owns 8 rows, 8 lanes
 // copy 128 bytes of a row.  The warps meet after every run (see load_heads).
 template <class G>
@@ -1057,11 +1057,12 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
             while (last < w.end && whole(last))
                 ++last;
             copies.flush();
-            if (warp < 3) {
-                // a tile is `per` blocks, or a part of one; warp 2 is AHEAD of the others
+            if (warp <= G::PARTS) {
+                // a tile is `per` blocks, or a part of one; the last warp is AHEAD of the others
                 const int per = G::KT / p.box_rows, in = p.block / p.box_rows;
-                const int skip = warp == 2 ? AHEAD : 0, part = warp == 0 ? 0 : 1;
-                const int half = part == 0 ? 1 - w.head : w.head;
+                const bool before = warp == G::PARTS;
+                const int skip = before ? AHEAD : 0, part = before ? G::PARTS - 1 : warp;
+                const int col = part == 0 ? (1 - w.head) * 256 : w.head * 256 + (part - 1) * 128;
                 const bool mine = lane < per;
                 auto ask = [&](int u) {
                     const int kt = real_tile(w, u);
@@ -1077,28 +1078,31 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
                     blk = ask(u + 1 + skip);
                     const int ord = u - w.beg, stage = ord & 1, phase = ((ord >> 1) & 1) ^ 1;
                     const uint32_t full = bars + (part * 2 + stage) * 8;
-                    ok = bar_wait(full + 4 * 8, phase, abort, p.wait_limit_ns);
+                    ok = bar_wait(full + G::BARS / 2 * 8, phase, abort, p.wait_limit_ns);
                     if (!ok)
                         break;
-                    if (warp == 2) {
+                    if (before) {
                         if (mine && u + skip < last) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                prefetch_box(&p.copy_map, half * 256 + i * 64, y);
+                                prefetch_box(&p.copy_map, w.head * 256 + i * 64, y);
                             if (w.head == 0)
                                 prefetch_box(&p.rot_map, 0, y);
                         }
                         continue;
                     }
                     if (lane == 0)
-                        bar_signal_bulk(full, G::LOAD_WARPS * 32, part == 0 ? G::OTHER : G::OWN);
+                        bar_signal_bulk(full, G::LOAD_WARPS * 32,
+                                        part == 0 ? G::OTHER : 2 * G::PANEL);
                     if (mine) {
                         const uint32_t at = G::part(ring, part, stage) + lane * p.box_rows * 128;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            copy_box(at + i * G::PANEL, &p.copy_map, half * 256 + i * 64, y, full);
-                        if (part == 0)
+                        copy_box(at, &p.copy_map, col, y, full);
+                        copy_box(at + G::PANEL, &p.copy_map, col + 64, y, full);
+                        if (part == 0) {
+                            copy_box(at + 2 * G::PANEL, &p.copy_map, col + 128, y, full);
+                            copy_box(at + 3 * G::PANEL, &p.copy_map, col + 192, y, full);
                             copy_box(at + 4 * G::PANEL, &p.rot_map, 0, y, full);
+                        }
                     }
                 }
             }
@@ -1111,11 +1115,11 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
         const int64_t slot = key_slot(p, w, k, key_block(p, w, k), bad);
         const int ord = v - w.beg, stage = ord & 1, phase = ((ord >> 1) & 1) ^ 1;
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
+        for (int part = 0; part < G::PARTS; ++part) {
             const uint32_t full = bars + (part * 2 + stage) * 8, dst = G::part(ring, part, stage);
-            const int half = part == 0 ? 1 - w.head : w.head;
-            copies.before_wait(full + 4 * 8, phase);
-            ok = ok && bar_wait(full + 4 * 8, phase, abort, p.wait_limit_ns);
+            const int col = part == 0 ? (1 - w.head) * 512 : w.head * 512 + (part - 1) * 256;
+            copies.before_wait(full + G::BARS / 2 * 8, phase);
+            ok = ok && bar_wait(full + G::BARS / 2 * 8, phase, abort, p.wait_limit_ns);
             if (!ok)
                 continue;
 #pragma unroll
@@ -1123,9 +1127,9 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
                 const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, i * 4 + sub);
                 const int row = base + i * 4 + sub;
                 const uint32_t at = dst + row * 128 + ((c ^ (row & 7)) << 4), n = s < 0 ? 0 : 16;
-                const char *src = p.copy + (s < 0 ? 0 : s * p.copy_ss) + half * 512 + c * 16;
+                const char *src = p.copy + (s < 0 ? 0 : s * p.copy_ss) + col + c * 16;
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
+                for (int g = 0; g < (part == 0 ? 4 : 2); ++g)
                     copy16(at + g * G::PANEL, src + g * 128, n);
                 if (part == 0)
                     copy16(at + 4 * G::PANEL, p.rot + (s < 0 ? 0 : s * p.rot_ss) + c * 16, n);
@@ -1135,8 +1139,8 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
         ++v;
     }
     copies.flush();
-    if (warp == 0) // the last tiles of both parts; after an early end some never come
-        for (int part = 0; part < 2; ++part)
+    if (warp == 0) // the last tiles of each part; after an early end some never come
+        for (int part = 0; part < G::PARTS; ++part)
             copies_land<2>(bars + part * 16, v - w.beg);
 }
 
@@ -1180,7 +1184,8 @@ __device__ __forceinline__ void load_mla_e4m3(const AttnParams &p, const Work &w
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
             const uint32_t full = bars + (part * 2 + stage) * 8, dst = G::part(ring, part, stage);
-            if (!bar_wait(full + 4 * 8, phase, abort, p.wait_limit_ns))
+            if (!bar_wait(full + G::BARS / 2 * 8, phase, abort, p.wait_limit_ns) ||
+                (part == 1 && !bar_wait(full + (G::BARS / 2 + 2) * 8, phase, abort, p.wait_limit_ns)))
                 return;
             const uint32_t mul[2] = {scale_mul(scale[part][0]), scale_mul(scale[part][1])};
             const uint32_t rare = rare16(lat[part][0], mul[0]) | rare16(lat[part][1], mul[1]);
@@ -1204,6 +1209,8 @@ __device__ __forceinline__ void load_mla_e4m3(const AttnParams &p, const Work &w
                 store(std::false_type{});
             async_fence();
             bar_signal(full);
+            if (part == 1) // both pairs of panels
+                bar_signal(full + 16);
             fetch(part, slot);
         }
     }
@@ -1322,14 +1329,17 @@ __device__ __forceinline__ bool run_mma_one(const AttnParams &p, const Work &w, 
                 if (!bar_wait(full + i * 8, turn, abort, p.wait_limit_ns))
                     return false;
                 issue_scores<64, G::PANEL, 5>(s_col, q_smem, G::part(ring, 0, i), true, lead);
-                bar_signal_mma(full + (4 + i) * 8, lead);
-                if (!bar_wait(full + (2 + i) * 8, turn, abort, p.wait_limit_ns))
-                    return false;
-                const uint32_t k = operand(G::part(ring, 1, i), 16);
+                bar_signal_mma(full + (G::BARS / 2 + i) * 8, lead);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    mma_tmem<64, 0>(s_col, tmem + G::Q_COL + j * 8,
-                                    k + (j >> 2) * (G::PANEL >> 4) + (j & 3) * 2, 1u, lead);
+                for (int pair = 0; pair < 2; ++pair) {
+                    if (!bar_wait(full + (2 + 2 * pair + i) * 8, turn, abort, p.wait_limit_ns))
+                        return false;
+                    const uint32_t k = operand(G::part(ring, 1 + pair, i), 16);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        mma_tmem<64, 0>(s_col, tmem + G::Q_COL + (pair * 8 + j) * 8,
+                                        k + (j >> 2) * (G::PANEL >> 4) + (j & 3) * 2, 1u, lead);
+                }
                 bar_signal_mma(bars + (kBarS + i) * 8, lead);
             } else {
                 if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
@@ -1349,9 +1359,12 @@ __device__ __forceinline__ bool run_mma_one(const AttnParams &p, const Work &w, 
                 return false;
             mma_fence_after();
             if constexpr (G::MLA) {
-                issue_values<256, 64>(tmem + G::O_COL(0), tmem + G::S_COL(j), G::part(ring, 1, j),
-                                      ord == 1, lead);
-                bar_signal_mma(full + (6 + j) * 8, lead);
+#pragma unroll
+                for (int pair = 0; pair < 2; ++pair) {
+                    issue_values<128, 64>(tmem + G::O_COL(0) + pair * 128, tmem + G::S_COL(j),
+                                          G::part(ring, 1 + pair, j), ord == 1, lead);
+                    bar_signal_mma(full + (G::BARS / 2 + 2 + 2 * pair + j) * 8, lead);
+                }
             } else {
                 issue_values<128, 128>(tmem + G::O_COL(0), tmem + G::S_COL(j),
                                        ring + vstage * G::STAGE, ord == 1, lead);
@@ -1580,8 +1593,9 @@ __device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, 
             uint32_t vbase;
             int pieces;
             if constexpr (G::MLA) {
-                ok = ok && bar_wait(bars + (kBarRing + 2 + (ord & 1)) * 8, (ord >> 1) & 1, abort,
-                                    p.wait_limit_ns);
+                for (int part = 1; part < G::PARTS; ++part)
+                    ok = ok && bar_wait(bars + (kBarRing + part * 2 + (ord & 1)) * 8,
+                                        (ord >> 1) & 1, abort, p.wait_limit_ns);
                 vbase = G::part(ring, 1, ord & 1);
                 pieces = G::OWN / 16;
             } else {
