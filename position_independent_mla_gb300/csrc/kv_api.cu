@@ -1404,6 +1404,7 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
     p.total_q = total_q;
     p.heads = heads;
     p.group = heads / kv_heads;
+    p.kv_heads = kv_heads;
     p.num_seqs = a->num_seqs;
     p.max_q_len = a->max_q_len;
     p.max_kv_len = a->max_kv_len;

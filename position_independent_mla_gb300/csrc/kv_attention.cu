@@ -552,7 +552,8 @@ __device__ __forceinline__ TileMask tile_mask(const AttnParams &p, int n, int le
     TileMask m;
     const int total = n * p.group;
     m.rows = max(0, min(kRows, total - row0));
-    const int i0 = row0 / p.group, i1 = (row0 + max(m.rows, 1) - 1) / p.group;
+    const int i0 = p.by_group.quotient(row0);
+    const int i1 = p.by_group.quotient(row0 + max(m.rows, 1) - 1);
     m.pos0 = len - n + i0;
     m.pos1 = len - n + i1;
     m.hi0 = p.causal ? max(0, min(len, m.pos0 + 1)) : len;
@@ -608,8 +609,8 @@ __device__ __forceinline__ int real_tile(const Work &w, int v)
 // False where there is none.
 __device__ __forceinline__ bool take_split(const AttnParams &p, int nv, Work &w)
 {
-    w.splits = max(1, (nv + p.split_tiles - 1) / p.split_tiles);
-    const int run = (nv + w.splits - 1) / w.splits;
+    w.splits = max(1, p.by_run.quotient(nv + p.split_tiles - 1));
+    const int run = w.splits == 1 ? nv : (nv + w.splits - 1) / w.splits;
     w.beg = min(nv, w.split * run);
     w.end = min(nv, w.beg + run);
     return w.split < w.splits;
@@ -690,7 +691,7 @@ __device__ __forceinline__ bool key_seen(const Work &w, int k)
 // The load roles ask for it well before they use it: the first use waits.
 __device__ __forceinline__ int32_t key_block(const AttnParams &p, const Work &w, int k)
 {
-    const int b = (int)((uint32_t)k / (uint32_t)p.block);
+    const int b = p.by_block.quotient(k);
     return key_seen(w, k) ? __ldg(p.block_tables + (int64_t)w.seq * p.max_blocks + b) : 0;
 }
 
@@ -705,7 +706,7 @@ __device__ __forceinline__ int64_t key_slot(const AttnParams &p, const Work &w, 
         bad = true;
         return -1;
     }
-    return (int64_t)blk * p.block + (int)((uint32_t)k % (uint32_t)p.block);
+    return (int64_t)blk * p.block + (k - p.by_block.quotient(k) * p.block);
 }
 
 // ---------------------------------------------------------------------------
@@ -722,8 +723,8 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, const Work &w,
     constexpr int LANES = G::MLA ? 8 : 16, step = 256 / LANES;
     const int c = tid & (LANES - 1);
     const int row = w.row0 + t * kRows + tid / LANES;
-    int tok = row / p.group, g = row - tok * p.group;
-    const int dt = step / p.group, dg = step - dt * p.group;
+    int tok = p.by_group.quotient(row), g = row - tok * p.group;
+    const int dt = p.by_group.quotient(step), dg = step - dt * p.group;
     const uint32_t dst = q_smem + ((t * G::QPANELS + (c >> 3)) << 14);
     for (int rr = tid / LANES; rr < kRows; rr += step) {
         const uint32_t n = tok < w.n ? 16u : 0u;
@@ -1451,24 +1452,23 @@ template <class G>
 __device__ __forceinline__ void queries_to_tmem(const AttnParams &p, const Work &w, uint32_t tmem,
                                                 int warp, int lane, int rows, int panel)
 {
-    const int r = warp * 32 + lane, row = w.row0 + r, tok = row / p.group;
+    const int r = warp * 32 + lane, row = w.row0 + r, tok = p.by_group.quotient(row);
     const bool valid = r < rows;
     const char *src =
         p.q + (valid ? (w.q0 + tok) * p.q_ts + (row - tok * p.group) * p.q_hs : 0) + w.head * 512;
-#pragma unroll 1
-    for (int i = panel; i < panel + 2; ++i) {
-        uint32_t x[32];
+    uint32_t x[64]; // both panels' loads in flight at once
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint4 y = valid ? __ldg(reinterpret_cast<const uint4 *>(src + i * 128) + j)
-                                  : make_uint4(0, 0, 0, 0);
-            x[4 * j] = y.x;
-            x[4 * j + 1] = y.y;
-            x[4 * j + 2] = y.z;
-            x[4 * j + 3] = y.w;
-        }
-        tmem_st32(tmem + G::Q_COL + i * 32 + ((uint32_t)(warp * 32) << 16), x);
+    for (int j = 0; j < 16; ++j) {
+        const uint4 y = valid ? __ldg(reinterpret_cast<const uint4 *>(src + panel * 128) + j)
+                              : make_uint4(0, 0, 0, 0);
+        x[4 * j] = y.x;
+        x[4 * j + 1] = y.y;
+        x[4 * j + 2] = y.z;
+        x[4 * j + 3] = y.w;
     }
+    const uint32_t at = tmem + G::Q_COL + panel * 32 + ((uint32_t)(warp * 32) << 16);
+    tmem_st32(at, x);
+    tmem_st32(at + 32, x + 32);
     tmem_st_wait();
 }
 
@@ -1486,7 +1486,7 @@ __device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, 
     const int pair = t * 4 + warp;
     const int r = warp * 32 + lane;
     const int row = w.row0 + t * kRows + r;
-    const int tok = row / p.group, g = row - tok * p.group;
+    const int tok = p.by_group.quotient(row), g = row - tok * p.group;
     const bool valid = r < m.rows;
     const int pos = w.len - w.n + tok;
     // keys this row sees: [lo, hi) and [0, sk)
@@ -1726,15 +1726,14 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
     if (warp == 0) {
         // block -> (row tile, key head or half, split); heads of one row tile and
         // its halves are neighbours, so their rows meet in L2
-        const int heads = G::MLA ? 2 : p.heads / p.group;
-        uint32_t x = blockIdx.x;
+        const int heads = G::MLA ? 2 : p.kv_heads, x = (int)blockIdx.x;
+        const int y = p.by_heads.quotient(x), tile = p.by_splits.quotient(y);
         Work w{};
-        w.head = (int)(x % heads);
-        x /= heads;
-        w.split = (int)(x % p.max_splits);
+        w.head = x - y * heads;
+        w.split = y - tile * p.max_splits;
         int at = 0;
         bool bad = false;
-        bool go = find_tile<kRows * G::NT>(p, (int)(x / p.max_splits), lane, w, at, bad);
+        bool go = find_tile<kRows * G::NT>(p, tile, lane, w, at, bad);
         if (go) {
             w.row0 = at * kRows * G::NT;
             const int nv = key_tiles<G::KT, G::NT>(p, w);
@@ -2257,11 +2256,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
     const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
     const uint32_t bars = smem + G::BAR_AT;
 
-    const int heads = p.heads / p.group;
+    const int x = (int)blockIdx.x, y = p.by_heads.quotient(x);
     Work w;
-    w.head = (int)(blockIdx.x % heads);
-    w.split = (int)(blockIdx.x / heads % p.max_splits);
-    w.seq = (int)(blockIdx.x / heads / p.max_splits);
+    w.seq = p.by_splits.quotient(y);
+    w.head = x - y * p.kv_heads;
+    w.split = y - w.seq * p.max_splits;
     w.row0 = 0;
     bool bad = !seq_queries(p, w.seq, w.q0, w.n);
     bool go = w.n > 0;
@@ -2378,7 +2377,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
             tok < w.q0 + w.n) {
             const int row = (int)(tok - w.q0) * p.group + h % p.group;
             w.row0 = row / (kRows * G::NT) * (kRows * G::NT);
-            splits = (key_tiles<G::KT, G::NT>(p, w) + p.split_tiles - 1) / p.split_tiles;
+            splits = p.by_run.quotient(key_tiles<G::KT, G::NT>(p, w) + p.split_tiles - 1);
         }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -2450,7 +2449,7 @@ void set_boxes(AttnParams &p)
     p.box_rows = 0;
     const int b = p.block;
     const int64_t rows = p.num_blocks * b;
-    const int heads = p.heads / p.group;
+    const int heads = p.kv_heads;
     if (b % 8 != 0 || (G::KT % b != 0 && b % G::KT != 0) || rows >= 0x7FFFFFFFll)
         return;
     const int box = std::min(b, G::KT);
@@ -2576,6 +2575,11 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
 cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cudaStream_t stream)
 {
     const bool quant = p.cs != nullptr;
+    p.by_group = Divisor((uint32_t)p.group);
+    p.by_block = Divisor((uint32_t)p.block);
+    p.by_heads = Divisor(kind == RowKind::Mla ? 2u : (uint32_t)p.kv_heads);
+    p.by_splits = Divisor((uint32_t)p.max_splits);
+    p.by_run = Divisor((uint32_t)p.split_tiles);
     if (kind == RowKind::Mla)
         return quant ? launch<MlaGeo<true>>(p, pl.blocks, stream)
                      : launch<MlaGeo<false>>(p, pl.blocks, stream);

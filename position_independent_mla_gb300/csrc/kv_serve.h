@@ -73,6 +73,27 @@ struct ExpandParams {
 int expand_blocks(int64_t rows); // blocks of a launch over so many rows
 cudaError_t launch_expand(const ExpandParams &p, RowKind kind, cudaStream_t stream);
 
+// Quotients by a number that only the host knows, for 0 <= n < 2^31 (Granlund and
+// Montgomery, Division by invariant integers using multiplication, 1994): with
+// l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d = (mulhi(m, n) + n) >> l.
+struct Divisor {
+    uint32_t mul = 1, shift = 0;
+
+    Divisor() = default;
+    explicit Divisor(uint32_t d)
+    {
+        while ((uint64_t(1) << shift) < d)
+            ++shift;
+        mul = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - d)) / d + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int quotient(int n) const
+    {
+        return (int)((__umulhi(mul, (uint32_t)n) + (uint32_t)n) >> shift);
+    }
+#endif
+};
+
 struct AttnParams {
     // one layer of the pool: bf16 rows, or e4m3 rows with scales (cs != nullptr)
     const char *copy, *rot;
@@ -88,7 +109,7 @@ struct AttnParams {
     int64_t o_ts, o_hs;
     float *lse;
     int64_t total_q;
-    int32_t heads, group; // query heads; query heads per key head
+    int32_t heads, group, kv_heads; // query heads; of them to a key head; key heads
     int32_t num_seqs, max_q_len, max_kv_len, max_blocks;
     int64_t max_keys; // that a block-table row of the caller holds
     const int32_t *q_off, *kv_len, *block_tables;
@@ -100,7 +121,10 @@ struct AttnParams {
     int64_t wait_limit_ns;
     uint32_t *header;
     uint32_t status_words; // of the call: this kernel's blocks, and those of an expansion
-    // bf16 pools, filled in by launch_attention: rows of a box (0: no boxes)
+    // filled in by launch_attention: quotients by group, block, key heads (MLA: halves),
+    // max_splits and split_tiles
+    Divisor by_group, by_block, by_heads, by_splits, by_run;
+    // bf16 pools, likewise: rows of a box (0: no boxes)
     int32_t box_rows;
     CUtensorMap copy_map, rot_map;
 };
