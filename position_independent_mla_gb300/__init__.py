@@ -155,6 +155,7 @@ def load(build_if_missing: bool = False) -> C.CDLL:
         "kv_set_wait_limit_ns": (None, [i64]),
         "kv_set_debug_checks": (None, [i32]),
         "kv_set_splice_skip_publish": (None, [i64]),
+        "kv_set_attention_skip_block": (None, [i64]),
         "kv_check_wait_timeout": (i32, [vp, sz, i64, vp]),
         "kv_last_launch_count": (i32, []),
         "kv_set_kernel_events": (None, [vp, vp]),
@@ -562,6 +563,12 @@ def kv_set_splice_skip_publish(ticket: int) -> None:
     """Test hook: the splice tile drawing ``ticket`` does not publish its reads
     (its dependants time out); -1 turns it off."""
     load().kv_set_splice_skip_publish(int(ticket))
+
+
+def kv_set_attention_skip_block(block: int) -> None:
+    """Test hook: block ``block`` of every later kv_attention issues no MMA (its
+    waits run out, KV_ERR_TIMEOUT); -1 turns it off."""
+    load().kv_set_attention_skip_block(int(block))
 
 
 def kv_check_wait_timeout(ws: torch.Tensor, limit_ns: int, stream=None) -> int:

@@ -33,6 +33,7 @@ constexpr int64_t kInlineTableTiles = 1024;
 std::atomic<int64_t> g_wait_limit_ns{kDefaultWaitLimitNs};
 std::atomic<int32_t> g_debug_checks{0};   // kv_set_debug_checks
 std::atomic<int64_t> g_skip_publish{-1};  // kv_set_splice_skip_publish (test hook)
+std::atomic<int64_t> g_skip_block{-1};    // kv_set_attention_skip_block (test hook)
 thread_local int32_t t_launches = 0;
 thread_local cudaEvent_t t_ev_start = nullptr, t_ev_stop = nullptr;
 
@@ -1130,6 +1131,8 @@ void kv_set_wait_limit_ns(int64_t limit_ns)
 
 void kv_set_debug_checks(int32_t on) { g_debug_checks.store(on != 0 ? 1 : 0); }
 
+void kv_set_attention_skip_block(int64_t block) { g_skip_block.store(block >= 0 ? block : -1); }
+
 void kv_set_splice_skip_publish(int64_t ticket) { g_skip_publish.store(ticket >= 0 ? ticket : -1); }
 
 kv_status kv_check_wait_timeout(void *d_workspace, size_t workspace_bytes, int64_t limit_ns,
@@ -1182,7 +1185,7 @@ const char *kv_status_string(kv_status s)
     return "unknown status";
 }
 
-int32_t kv_version(void) { return 200; }
+int32_t kv_version(void) { return 300; }
 
 } // extern "C"
 
@@ -1332,7 +1335,8 @@ AttnLayout attn_layout(RowKind kind, const AttnPlan &pl, const kv_attn_desc *a, 
                        int32_t heads, int32_t kv_heads)
 {
     const bool mla = kind == RowKind::Mla;
-    const size_t rows = pl.max_splits > 1 ? (size_t)pl.max_splits * total_q * heads : 0;
+    const bool parts = pl.max_splits > 1 && !pl.cluster;
+    const size_t rows = parts ? (size_t)pl.max_splits * total_q * heads : 0;
     AttnLayout l;
     l.pad = (a->max_kv_len + kExpandBlock - 1) / kExpandBlock * kExpandBlock;
     const int64_t wide = pl.expand ? l.pad * a->num_seqs : 0;
@@ -1422,6 +1426,7 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
     p.part_lse = reinterpret_cast<float *>(static_cast<char *>(ws) + lay.lse);
     p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + lay.part);
     p.wait_limit_ns = g_wait_limit_ns.load();
+    p.skip_block = g_skip_block.load();
     p.header = static_cast<uint32_t *>(ws);
     p.status_words = (uint32_t)(pl.blocks + lay.expand_blocks);
     KV_CUDA(mark(t_ev_start, stream));
@@ -1462,7 +1467,7 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
         p.max_blocks = (int32_t)(lay.pad / kExpandBlock);
     }
     KV_CUDA(launch_attention(p, kind, pl, stream));
-    t_launches += pl.max_splits > 1 ? 2 : 1;
+    t_launches += pl.max_splits > 1 && !pl.cluster ? 2 : 1;
     KV_CUDA(mark(t_ev_stop, stream));
     return KV_OK;
 }

@@ -33,417 +33,16 @@
 //
 // Every wait is bounded; a block whose wait runs out reports KV_ERR_TIMEOUT.
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
-#include <cudaTypedefs.h>
-#include <cuda_fp16.h>
-
-#include "kv_device.cuh"
-#include "kv_serve.h"
+#include "kv_attn_tile.cuh"
 
 namespace kvr {
 
 namespace {
 
-constexpr int kRows = 128;         // rows per tile: the M of an MMA
 constexpr int64_t kExpandBytes = int64_t(2) << 30; // largest workspace for widened rows
 constexpr float kLazy = 8.0f;      // log2 of the growth of a maximum that O tolerates
-
-// ---------------------------------------------------------------------------
-// PTX pieces
-// ---------------------------------------------------------------------------
-
-__device__ __forceinline__ uint32_t smem_u32(const void *p)
-{
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void bar_init_fence()
-{
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-}
-
-__device__ __forceinline__ void bar_signal(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// `count` arrivals at once; the phase then also waits for `bytes` of bulk copies.
-__device__ __forceinline__ void bar_signal_bulk(uint32_t bar, uint32_t count, uint32_t bytes)
-{
-    if (bytes)
-        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar),
-                     "r"(bytes)
-                     : "memory");
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-// Box of a tensor map at column x, row y; what lies outside the tensor is zero.
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                         uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-                 "l"(map), "r"(bar), "r"(x), "r"(y)
-                 : "memory");
-}
-
-// A box of a tensor map on its way to L2.
-__device__ __forceinline__ void prefetch_box(const CUtensorMap *map, int x, int y)
-{
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x),
-                 "r"(y)
-                 : "memory");
-}
-
-// Signals `bar` when this thread's earlier cp.async copies have landed.
-__device__ __forceinline__ void bar_signal_copies(uint32_t bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// Signals `bar` when every MMA the lead lane issued before has finished.
-__device__ __forceinline__ void bar_signal_mma(uint32_t bar, uint32_t lead)
-{
-    asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
-                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
-                 "r"(lead)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint32_t elect_lane()
-{
-    uint32_t r;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.b32 %0, 1, 0, p;\n}" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-                 "selp.b32 %0, 1, 0, p;\n}"
-                 : "=r"(ok)
-                 : "r"(bar), "r"(parity)
-                 : "memory");
-    return ok != 0;
-}
-
-// Bounded wait of a whole warp for a phase; false, for every lane, when it ran
-// out here or elsewhere in the block (*abort).
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *abort,
-                                         int64_t limit_ns)
-{
-    if (__all_sync(0xFFFFFFFFu, bar_try(bar, parity)))
-        return true;
-    const uint64_t t0 = global_ns();
-    for (uint32_t it = 1; it < (1u << 26); ++it) {
-        if (__all_sync(0xFFFFFFFFu, bar_try(bar, parity)))
-            return true;
-        if ((it & 15u) == 0u &&
-            __any_sync(0xFFFFFFFFu, *abort != 0 || (int64_t)(global_ns() - t0) > limit_ns))
-            break;
-    }
-    *abort = 1;
-    return false;
-}
-
-__device__ __forceinline__ void mma_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void mma_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-template <int R>
-__device__ __forceinline__ void reg_inc()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-
-template <int R>
-__device__ __forceinline__ void reg_dec()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
-
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-// All but this thread's newest N groups of copies have landed.
-template <int N>
-__device__ __forceinline__ void copy_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ float lds4(uint32_t src)
-{
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(src) : "memory");
-    return v;
-}
-
-// 16-byte copy to shared memory; bytes = 0 writes zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ void sts16(uint32_t dst, uint4 v)
-{
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y),
-                 "r"(v.z), "r"(v.w)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint4 lds16(uint32_t src)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(src)
-                 : "memory");
-    return v;
-}
-
-// Columns of tensor memory for the block, by one warp; the address is left at `to`.
-__device__ __forceinline__ void tmem_alloc(uint32_t to, uint32_t columns)
-{
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to),
-                 "r"(columns)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t columns)
-{
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
-}
-
-#define KV_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), \
-                    "=r"(a[i + 5]), "=r"(a[i + 6]), "=r"(a[i + 7])
-#define KV_P8(a, i) "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3]), "+r"(a[i + 4]), \
-                    "+r"(a[i + 5]), "+r"(a[i + 6]), "+r"(a[i + 7])
-#define KV_W8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), \
-                    "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
-
-// 32 columns of this thread's tensor-memory lane (no wait).
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-                 : KV_R8(r, 0), KV_R8(r, 8), KV_R8(r, 16), KV_R8(r, 24)
-                 : "r"(addr));
-}
-
-// Uses of r stay behind the wait that comes before this.
-__device__ __forceinline__ void tmem_pin32(uint32_t *r)
-{
-    asm volatile("" : KV_P8(r, 0), KV_P8(r, 8), KV_P8(r, 16), KV_P8(r, 24));
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::KV_W8(r, 0),
-                 KV_W8(r, 8), KV_W8(r, 16), KV_W8(r, 24), "r"(addr)
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : KV_R8(r, 0), KV_R8(r, 8)
-                 : "r"(addr));
-}
-
-__device__ __forceinline__ void tmem_pin16(uint32_t *r)
-{
-    asm volatile("" : KV_P8(r, 0), KV_P8(r, 8));
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::KV_W8(r, 0),
-                 KV_W8(r, 8), "r"(addr)
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Shared-memory operand in panels of 64 bf16 columns: rows of 128 bytes, the
-// 16-byte piece c of row r at c ^ (r & 7) (128-byte swizzle), 1024 bytes per
-// eight rows.  Along a K-major operand the next 16 columns are 32 bytes on;
-// of an MN-major one (V: the MMA's N runs along the row) the next 16 keys are
-// 2048 bytes on and the next 64 columns `lead` bytes.  The low word holds the
-// address, in units of 16 bytes, and the lead; the high word is the same for all.
-__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t lead)
-{
-    return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
-}
-
-constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
-
-// kind::f16: D fp32, A and B bf16; each along K (0) or along M / N (1).
-template <int N, int BMAJOR, int AMAJOR = 0>
-__device__ __forceinline__ constexpr uint32_t mma_desc()
-{
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)AMAJOR << 15) | ((uint32_t)BMAJOR << 16) |
-           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
-}
-
-// The MMA warp runs as one: every lane holds the same operands (they stay in
-// uniform registers) and the lane with `lead` set issues.
-template <int N, int MAJOR = 0>
-__device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t acc,
-                                         uint32_t lead, uint32_t b_high = kOperandHigh)
-{
-    asm volatile("{\n.reg .pred p, q;\n.reg .b64 x, y;\nsetp.ne.b32 p, %4, 0;\n"
-                 "setp.ne.b32 q, %6, 0;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %7};\n"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d),
-                 "r"(a), "r"(b), "r"(mma_desc<N, MAJOR, MAJOR>()), "r"(acc), "r"(kOperandHigh),
-                 "r"(lead), "r"(b_high)
-                 : "memory");
-}
-
-// kind::f8f6f4: D fp32, A and B e4m3.
-template <int N, int MAJOR>
-__device__ __forceinline__ void mma_smem_e4m3(uint32_t d, uint32_t a, uint32_t b, uint32_t acc,
-                                              uint32_t lead, uint32_t b_high)
-{
-    constexpr uint32_t desc = (1u << 4) | ((uint32_t)MAJOR << 15) | ((uint32_t)MAJOR << 16) |
-                              ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
-    asm volatile("{\n.reg .pred p, q;\n.reg .b64 x, y;\nsetp.ne.b32 p, %4, 0;\n"
-                 "setp.ne.b32 q, %6, 0;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %7};\n"
-                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n}" ::"r"(d),
-                 "r"(a), "r"(b), "r"(desc), "r"(acc), "r"(kOperandHigh), "r"(lead), "r"(b_high)
-                 : "memory");
-}
-
-template <int N, int BMAJOR>
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t acc,
-                                         uint32_t lead)
-{
-    asm volatile("{\n.reg .pred p, q;\n.reg .b64 y;\nsetp.ne.b32 p, %4, 0;\n"
-                 "setp.ne.b32 q, %6, 0;\nmov.b64 y, {%2, %5};\n"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}" ::"r"(d),
-                 "r"(a), "r"(b), "r"(mma_desc<N, BMAJOR>()), "r"(acc), "r"(kOperandHigh), "r"(lead)
-                 : "memory");
-}
-
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float y;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-    return y;
-}
-
-// 32 bytes, aligned so: a whole sector of a row.
-__device__ __forceinline__ void st32(void *to, const uint32_t *r)
-{
-    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::KV_W8(r, 0), "l"(to)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// Two e4m3 values (bytes 1 and 3 of y) to a bf16 pair, times `mul`.  Moved into
-// a bf16's exponent and top mantissa bits a value reads 2^-120 of itself,
-// subnormal ones included, so one exact product with 2^120 * scale puts it right.
-__device__ __forceinline__ uint32_t e4m3_bf16(uint32_t y, uint32_t mul)
-{
-    uint32_t b = (y & 0x80008000u) | ((y >> 4) & 0x07F007F0u);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(mul));
-    return b;
-}
-
-// A value of 0x7F or 0xFF (NaN) among four e4m3 values sets a bit.
-__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w)
-{
-    return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-}
-
-// Scale 2^e of a row as the multiplier pairs of convert16: 2^(120 + min(e, 7)),
-// the largest that bf16 holds, and what is left of e (1 but for huge rows).
-__device__ __forceinline__ uint32_t scale_mul(float scale)
-{
-    const int e = (int)(__float_as_uint(scale) >> 23) - 127;
-    return (uint32_t)(247 + min(e, 7)) << 7 | (uint32_t)(127 + max(e - 7, 0)) << 23;
-}
-
-// A 16-byte piece needs convert_rare: it holds a NaN, or its scale is above 2^7.
-__device__ __forceinline__ uint32_t rare16(uint4 v, uint32_t mul)
-{
-    return e4m3_nan(v.x) | e4m3_nan(v.y) | e4m3_nan(v.z) | e4m3_nan(v.w) |
-           ((mul >> 16) ^ 0x3F80u);
-}
-
-// Sixteen e4m3 values (one 16-byte piece) to two pieces of bf16.  RARE: with the
-// second factor of the scale, and NaN.  The callers test a whole batch of pieces
-// first, so that the usual form is free of branches and its chains interleave.
-template <bool RARE>
-__device__ __forceinline__ void convert16(uint4 v, uint32_t mul, uint4 &lo, uint4 &hi)
-{
-    const uint32_t m = __byte_perm(mul, 0, 0x1010);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t r[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r[2 * i] = e4m3_bf16(__byte_perm(w[i], 0, 0x1404), m);
-        r[2 * i + 1] = e4m3_bf16(__byte_perm(w[i], 0, 0x3424), m);
-    }
-    if constexpr (RARE) {
-        const uint32_t m2 = __byte_perm(mul, 0, 0x3232);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(r[i]), "r"(m2));
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (((w[i >> 2] >> ((i & 3) * 8)) & 0x7Fu) == 0x7Fu)
-                r[i >> 1] |= (i & 1) ? 0x7FC00000u : 0x7FC0u;
-    }
-    lo = make_uint4(r[0], r[1], r[2], r[3]);
-    hi = make_uint4(r[4], r[5], r[6], r[7]);
-}
-
-// Sets bit 15 or 31 when the low or the high bf16 of a pair is not finite.
-__device__ __forceinline__ uint32_t nonfinite2(uint32_t w)
-{
-    return (w & 0x7F807F80u) + 0x00800080u;
-}
-
-// The pair with values that are not finite zeroed.
-__device__ __forceinline__ uint32_t finite2(uint32_t w)
-{
-    const uint32_t n = nonfinite2(w);
-    return w & ((n & 0x8000u) ? 0xFFFF0000u : ~0u) & ((n & 0x80000000u) ? 0xFFFFu : ~0u);
-}
 
 // ---------------------------------------------------------------------------
 // Geometry
@@ -523,192 +122,6 @@ struct Smem {
     static constexpr int BYTES = BAR + NBARS * 8 + 1024;         // + alignment of the base
 };
 
-enum { kBarQ = 0, kBarDone = 1, kBarS = 2, kBarP = 4, kBarO = 6, kBarRing = 8 };
-
-// What a block works on, the same for every thread.
-struct Work {
-    int seq, head;       // sequence, key head (MLA: half of the value columns)
-    int n, len;          // new tokens, cached tokens
-    int64_t q0;          // first query token of the sequence
-    int row0;            // first row of the block within (sequence, key head)
-    int beg, end;        // virtual key tiles of this block
-    int sink_tiles;      // virtual tile v < sink_tiles is tile v, else first + v - sink_tiles
-    int first;
-    int lo, hi, sk;      // keys that some row sees: [lo, hi) and [0, sk)
-    int split, splits;
-};
-
-// Mask of the rows of one 128-row tile.
-struct TileMask {
-    int pos0, pos1;      // positions of the first and last token
-    int hi0, hi1;        // first key not seen by the first / last token
-    int lo0, lo1;        // first key in the window of the first / last token
-    int sk;              // sinks outside the last token's window
-    int rows;            // rows that exist
-};
-
-__device__ __forceinline__ TileMask tile_mask(const AttnParams &p, int n, int len, int row0)
-{
-    TileMask m;
-    const int total = n * p.group;
-    m.rows = max(0, min(kRows, total - row0));
-    const int i0 = p.by_group.quotient(row0);
-    const int i1 = p.by_group.quotient(row0 + max(m.rows, 1) - 1);
-    m.pos0 = len - n + i0;
-    m.pos1 = len - n + i1;
-    m.hi0 = p.causal ? max(0, min(len, m.pos0 + 1)) : len;
-    m.hi1 = p.causal ? max(0, min(len, m.pos1 + 1)) : len;
-    m.lo0 = p.window ? max(0, m.pos0 - p.window + 1) : 0;
-    m.lo1 = p.window ? max(0, m.pos1 - p.window + 1) : 0;
-    m.sk = p.window ? min(p.sinks, m.lo1) : 0;
-    return m;
-}
-
-// Key tile kt has a key that some row of the tile sees.
-template <int KT>
-__device__ __forceinline__ bool tile_active(const TileMask &m, int kt)
-{
-    const int k0 = kt * KT;
-    return m.rows > 0 && k0 < m.hi1 && (k0 + KT > m.lo0 || k0 < m.sk);
-}
-
-// Every row of the tile sees every key of tile kt.
-template <int KT>
-__device__ __forceinline__ bool tile_full(const AttnParams &p, const TileMask &m, int kt)
-{
-    const int k0 = kt * KT;
-    return k0 + KT <= m.hi0 && (k0 >= m.lo1 || k0 + KT <= p.sinks);
-}
-
-// The key range of the rows of a block and its virtual tiles: returns their
-// number.
-template <int KT, int NT>
-__device__ __forceinline__ int key_tiles(const AttnParams &p, Work &w)
-{
-    const TileMask a = tile_mask(p, w.n, w.len, w.row0);
-    TileMask b = a;
-    if (NT == 2) {
-        const TileMask c = tile_mask(p, w.n, w.len, w.row0 + kRows);
-        if (c.rows > 0)
-            b = c;
-    }
-    w.lo = a.lo0;
-    w.hi = b.hi1;
-    w.sk = p.window ? min(p.sinks, w.lo) : 0;
-    w.first = w.lo / KT;
-    w.sink_tiles = min((w.sk + KT - 1) / KT, w.first);
-    return w.hi <= 0 ? 0 : w.sink_tiles + max(0, (w.hi + KT - 1) / KT - w.first);
-}
-
-__device__ __forceinline__ int real_tile(const Work &w, int v)
-{
-    return v < w.sink_tiles ? v : w.first + v - w.sink_tiles;
-}
-
-// The block's share of nv key tiles: as many equal runs as runs of split_tiles would be.
-// False where there is none.
-__device__ __forceinline__ bool take_split(const AttnParams &p, int nv, Work &w)
-{
-    w.splits = max(1, p.by_run.quotient(nv + p.split_tiles - 1));
-    const int run = w.splits == 1 ? nv : (nv + w.splits - 1) / w.splits;
-    w.beg = min(nv, w.split * run);
-    w.end = min(nv, w.beg + run);
-    return w.split < w.splits;
-}
-
-// Lengths of sequence s; false when they do not fit what the call stated.
-__device__ __forceinline__ bool seq_queries(const AttnParams &p, int s, int64_t &q0, int &n)
-{
-    const int a = p.q_off[s], b = p.q_off[s + 1];
-    q0 = a;
-    n = b - a;
-    if (a < 0 || b < a || b > p.total_q || n > p.max_q_len) {
-        n = 0;
-        return false;
-    }
-    return true;
-}
-
-__device__ __forceinline__ bool seq_keys(const AttnParams &p, int s, int &len)
-{
-    len = p.kv_len[s];
-    return len >= 0 && len <= p.max_kv_len && (int64_t)len <= p.max_keys;
-}
-
-// Row tile `tile` of the call -> sequence, its queries and keys, and the row tile
-// within it: one warp counts the sequences' tiles 32 at a time.  Returns false past
-// the last tile or for a sequence whose keys do not fit; `bad`: some sequence's
-// offsets, or this one's keys, do not fit what the call stated.
-template <int ROWS>
-__device__ __forceinline__ bool find_tile(const AttnParams &p, int tile, int lane, Work &w, int &at,
-                                          bool &bad)
-{
-    int before = 0;
-    bool found = false, wrong = false, keys = false;
-    for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-        int n = 0, tiles = 0, len = 0;
-        int64_t q0 = 0;
-        bool fits = false;
-        if (s0 + lane < p.num_seqs) {
-            fits = seq_keys(p, s0 + lane, len);
-            if (!seq_queries(p, s0 + lane, q0, n))
-                wrong = true;
-            tiles = (n * p.group + ROWS - 1) / ROWS;
-        }
-        int sum = tiles;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-            if (lane >= d)
-                sum += o;
-        }
-        const bool mine = !found && tile >= before + sum - tiles && tile < before + sum;
-        const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine);
-        if (who) {
-            const int l = __ffs((int)who) - 1;
-            w.seq = s0 + l;
-            w.n = __shfl_sync(0xFFFFFFFFu, n, l);
-            w.len = __shfl_sync(0xFFFFFFFFu, len, l);
-            w.q0 = __shfl_sync(0xFFFFFFFFu, q0, l);
-            keys = __shfl_sync(0xFFFFFFFFu, (int)fits, l) != 0;
-            // the last tiles of a causal chunk see the most keys: first
-            const int t = __shfl_sync(0xFFFFFFFFu, tiles, l), e = __shfl_sync(0xFFFFFFFFu, sum, l);
-            at = t - 1 - (tile - (before + e - t));
-            found = true;
-        }
-        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
-    }
-    bad = __any_sync(0xFFFFFFFFu, wrong) || (found && !keys);
-    return found && keys;
-}
-
-__device__ __forceinline__ bool key_seen(const Work &w, int k)
-{
-    return k < w.hi && (k >= w.lo || k < w.sk);
-}
-
-// Block id of key k of the block's sequence (anything for keys that no row sees).
-// The load roles ask for it well before they use it: the first use waits.
-__device__ __forceinline__ int32_t key_block(const AttnParams &p, const Work &w, int k)
-{
-    const int b = p.by_block.quotient(k);
-    return key_seen(w, k) ? __ldg(p.block_tables + (int64_t)w.seq * p.max_blocks + b) : 0;
-}
-
-// Slot of key k in block `blk`, or -1: not seen by any row, or (bad) the block
-// lies outside the pool.
-__device__ __forceinline__ int64_t key_slot(const AttnParams &p, const Work &w, int k, int32_t blk,
-                                            bool &bad)
-{
-    if (!key_seen(w, k))
-        return -1;
-    if (blk < 0 || blk >= p.num_blocks) {
-        bad = true;
-        return -1;
-    }
-    return (int64_t)blk * p.block + (k - p.by_block.quotient(k) * p.block);
-}
-
 // ---------------------------------------------------------------------------
 // Load roles
 // ---------------------------------------------------------------------------
@@ -746,182 +159,6 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, const Work &w,
             ++tok;
         }
     }
-}
-
-// Every key of tile kt is seen by some row: its rows can be copied as they are.
-template <int KT>
-__device__ __forceinline__ bool tile_whole(const Work &w, int kt)
-{
-    const int k0 = kt * KT;
-    return (k0 >= w.lo && k0 + KT <= w.hi) || k0 + KT <= w.sk;
-}
-
-// Waits for the boxes that may be in flight when `filled` tiles went into a ring, also
-// when the block gives up early: its shared memory goes after that.
-template <int STAGES>
-__device__ __forceinline__ void copies_land(uint32_t full, int filled)
-{
-    int none = 0;
-    for (int i = 0; i < STAGES; ++i)
-        if (filled > i)
-            bar_wait(full + i * 8, ((filled - 1 - i) / STAGES) & 1, &none, 10000000ll);
-}
-
-// Stages filled by cp.async: their threads wait for the copies, make them visible to
-// the MMAs and signal, one stage behind the one that they are filling.
-struct Copies {
-    uint32_t full = 0; // barrier of the stage that is not signalled yet
-
-    __device__ void flush()
-    {
-        if (full) {
-            copy_wait<0>();
-            async_fence();
-            bar_signal(full);
-            full = 0;
-        }
-    }
-
-    __device__ void filled(uint32_t bar)
-    {
-        copy_commit();
-        if (full) {
-            copy_wait<1>();
-            async_fence();
-            bar_signal(full);
-        }
-        full = bar;
-    }
-
-    // before a wait for a stage: nobody waits for this one meanwhile
-    __device__ void before_wait(uint32_t empty, uint32_t parity)
-    {
-        if (full && !__all_sync(0xFFFFFFFFu, bar_try(empty, parity)))
-            flush();
-    }
-};
-
-// A vote over the load warps, also their meeting point.
-template <class G>
-__device__ __forceinline__ bool load_any(bool x)
-{
-    uint32_t r;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 q, %1, 0;\n"
-                 "barrier.cta.red.or.pred p, 15, %2, q;\nselp.b32 %0, 1, 0, p;\n}"
-                 : "=r"(r)
-                 : "r"((uint32_t)x), "n"(G::LOAD_WARPS * 32)
-                 : "memory");
-    return r != 0;
-}
-
-// Head rows into the ring as they are stored.  Whole tiles are boxes of the
-// tensor maps that one warp asks for (a box is at most a block of the pool), a run
-// of tiles in a loop of few instructions: a tile's boxes have to go out within the
-// time of its MMAs.  Tiles that hold keys nobody sees, and pools whose blocks do
-// not divide a tile, are copied row by row by all warps with zeros in the place of
-// those keys: a lane owns one key row of its warp, 16 lanes copy 256 bytes (8 lanes
-// 128).  The warps meet after every run, so none waits for a stage that is more than
-// one phase away, which a parity would not show; a warp whose wait ran out goes on to
-// the next meeting, where they all give up.
-template <class G>
-__device__ __forceinline__ void load_heads(const AttnParams &p, const Work &w, uint32_t ring,
-                                           uint32_t bars, int warp, int lane,
-                                           volatile int *abort, bool &bad)
-{
-    constexpr int WARPS = G::LOAD_WARPS, ROWS = G::KT / WARPS; // rows of a warp: 32 or 16
-    constexpr int PIECES = G::STAGE / G::KT / 16, PER = 32 / PIECES; // of a row; rows at a time
-    const int base = warp * ROWS;
-    const int c = lane & (PIECES - 1), sub = lane / PIECES;
-    const int32_t *const table = p.block_tables + (int64_t)w.seq * p.max_blocks;
-    auto whole = [&](int v) { return p.box_rows > 0 && tile_whole<G::KT>(w, real_tile(w, v)); };
-    Copies copies;
-    int stage = 0, phase = 1, filled = 0;
-    bool ok = true;
-    auto next = [&] {
-        ++filled;
-        if (++stage == G::STAGES) {
-            stage = 0;
-            phase ^= 1;
-        }
-    };
-    for (int v = w.beg; v < w.end;) {
-        if (whole(v)) {
-            int last = v + 1;
-            while (last < w.end && whole(last))
-                ++last;
-            copies.flush();
-            if (warp == 0) {
-                // a tile is `per` blocks, or a part of one
-                const int per = G::KT / p.box_rows, in = p.block / p.box_rows;
-                const bool mine = lane < per;
-                auto block_of = [&](int kt) { return in == 1 ? kt * per + lane : kt / in; };
-                int kt = real_tile(w, v);
-                int32_t blk = mine ? __ldg(table + block_of(kt)) : 0;
-                for (int u = v; ok && u < last; ++u) {
-                    const int row = (in == 1 ? 0 : (kt % in) * G::KT) + blk * p.block;
-                    const bool fits = (uint32_t)blk < (uint32_t)p.num_blocks;
-                    bad |= !fits;
-                    const int y = fits ? row : (int)(p.num_blocks * p.block); // else zeros
-                    kt = real_tile(w, u + 1);
-                    if (mine && u + 1 < last)
-                        blk = __ldg(table + block_of(kt));
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) { // K, then V
-                        const uint32_t full = bars + stage * 8;
-                        ok = ok && bar_wait(full + G::STAGES * 8, phase, abort, p.wait_limit_ns);
-                        if (!ok)
-                            break;
-                        if (lane == 0)
-                            bar_signal_bulk(full, WARPS * 32, G::STAGE);
-                        if (mine) {
-                            const CUtensorMap *map = part == 0 ? &p.rot_map : &p.copy_map;
-                            const uint32_t at = ring + stage * G::STAGE + lane * p.box_rows * 128;
-                            copy_box(at, map, w.head * 128, y, full);
-                            if (PIECES == 16) // 64 columns of bf16 to a box
-                                copy_box(at + 16384, map, w.head * 128 + 64, y, full);
-                        }
-                        next();
-                    }
-                }
-            } else { // where warp 0 will be
-                filled += 2 * (last - v);
-                stage += 2 * (last - v);
-                phase ^= (stage / G::STAGES) & 1;
-                stage %= G::STAGES;
-            }
-            v = last;
-            if (load_any<G>(!ok))
-                break;
-            continue;
-        }
-        const int k = real_tile(w, v) * G::KT + base + (lane & (ROWS - 1));
-        const int64_t slot = key_slot(p, w, k, key_block(p, w, k), bad);
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-            const uint32_t full = bars + stage * 8, dst = ring + stage * G::STAGE;
-            copies.before_wait(full + G::STAGES * 8, phase);
-            ok = ok && bar_wait(full + G::STAGES * 8, phase, abort, p.wait_limit_ns);
-            if (ok) {
-                const char *src = part == 0 ? p.rot : p.copy;
-                const int64_t ss = part == 0 ? p.rot_ss : p.copy_ss;
-                const char *col = src + w.head * PIECES * 16 + c * 16;
-#pragma unroll
-                for (int i = 0; i < ROWS / PER; ++i) {
-                    const int r = i * PER + sub;
-                    const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, r);
-                    const int row = base + r;
-                    copy16(dst + ((c >> 3) << 14) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                           col + (s < 0 ? 0 : s * ss), s < 0 ? 0u : 16u);
-                }
-                copies.filled(full);
-                next();
-            }
-        }
-        ++v;
-    }
-    copies.flush();
-    if (warp == 0)
-        copies_land<G::STAGES>(bars, filled);
 }
 
 // Head rows in e4m3: copied as they are stored, RAW tiles ahead, then converted
@@ -1816,7 +1053,8 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
     if (s_go && warp == kMmaWarp<G>) {
         const Work w = s_work;
         const uint32_t lead = elect_lane();
-        bool ok = bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
+        bool ok = blockIdx.x != p.skip_block &&
+                  bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
         if (ok) {
             mma_fence_after();
             if constexpr (G::NT == 2)
@@ -1839,660 +1077,6 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
         write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, p.status_words);
 }
 
-// ---------------------------------------------------------------------------
-// One new token per sequence, up to 16 query heads to a key head
-// ---------------------------------------------------------------------------
-//
-// With so few rows the products are turned round: keys are the M of the MMA,
-//     Sᵀ (128 keys x 16 rows) = K Qᵀ,   Oᵀ (128 x 16) += Vᵀ Pᵀ,
-// so a thread has one key and all rows: R exponentials a tile instead of 128, and
-// its key's mask is one comparison.  The rows' maxima are references that all
-// threads hold; a vote finds a score that passes its reference by more than
-// 2^8, and only then are the true maxima formed across the block and O rescaled.
-// Sums stay per key until the end.  An MMA with N = 16 takes 40 clocks (the
-// operand A is read at 128 bytes a clock), 640 a tile, where the tile's rows take
-// 2700 from HBM: the kernel is bound by memory.  Two blocks share an SM, so that
-// one's start and end lie under the other's loads.
-//
-// e4m3 rows go into 8-bit MMAs as they are stored; 1400 clocks of HBM a tile
-// leave no time to widen them.  Queries and weights are split instead, x = hi +
-// lo / 16 with both parts e4m3: with 4 bits each that is every bit of a bf16
-// query, and a weight to 2^-8, as good as bf16 (below 2^-10 of the row's
-// reference to 2^-18 of it).  The parts are rows of their own (16 for up to 8
-// heads, 32 for up to 16).  A key's scale multiplies its scores, its value's scale
-// 2^e its weights: they are 2^(s + e - reference), the references being those of
-// s + e, and the sums take 2^-e of them.
-template <bool QUANT_, int R_>
-struct FewGeo {
-    static constexpr bool MLA = false, QUANT = QUANT_;
-    static constexpr int R = R_;                    // rows: 8 or 16
-    static constexpr int N = QUANT ? 2 * R : 16;    // rows of the MMAs
-    static constexpr int NT = 1, KT = 128;
-    static constexpr int DV = 128;
-    static constexpr int LOAD_WARPS = 4;
-    static constexpr int STAGE = (QUANT ? 1 : 2) * 128 * 128, STAGES = QUANT ? 6 : 3;
-    static constexpr int RING = STAGES * STAGE;
-    // a key's weights: N values of 1 or 2 bytes
-    static constexpr int Q_BYTES = N * (QUANT ? 128 : 256), P_BYTES = 128 * N * (QUANT ? 1 : 2);
-    static constexpr int P_AT = RING, Q_AT = P_AT + 2 * P_BYTES, BAR_AT = Q_AT + Q_BYTES;
-    static constexpr int BYTES = BAR_AT + (kBarRing + 2 * STAGES) * 8 + 1024;
-    // tensor memory: two S, O
-    static constexpr int O_COL = 2 * N, COLS = 4 * N;
-};
-
-constexpr int kFewThreads = 288; // 4 softmax warps, 4 load warps, 1 MMA warp
-constexpr int kFewRows = 16;
-constexpr float kLazyFew = 4.0f;   // growth of a reference: e4m3 weights start at 2^4, end at 448
-
-// Byte of (key, first of 8 rows) of Pᵀ: core matrices of 8 keys x 8 rows (16 bytes
-// a key), the second 8 rows 128 bytes on, the next 8 keys 256 bytes on.
-__device__ __forceinline__ uint32_t few_weight(int key) { return (key >> 3) * 256 + (key & 7) * 16; }
-
-// Two values to e4m3 parts x = hi + lo / 16.
-__device__ __forceinline__ void split_e4m3(float a, float b, uint32_t &hi, uint32_t &lo)
-{
-    uint16_t h, l;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
-    uint32_t w;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(w) : "h"(h));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(l)
-        : "f"((b - f.y) * 16.0f), "f"((a - f.x) * 16.0f));
-    hi = h;
-    lo = l;
-}
-
-// Eight values to eight bytes of each part.
-__device__ __forceinline__ void split8(const float *x, uint2 &hi, uint2 &lo)
-{
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        split_e4m3(x[2 * i], x[2 * i + 1], h[i], l[i]);
-    hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-    lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
-}
-
-// A vote over the four softmax warps.  Each of them comes to every vote, also
-// when its own wait ran out: they go on or give up together.
-__device__ __forceinline__ bool softmax_any(bool x)
-{
-    uint32_t r;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 q, %1, 0;\n"
-                 "barrier.cta.red.or.pred p, 1, 128, q;\nselp.b32 %0, 1, 0, p;\n}"
-                 : "=r"(r)
-                 : "r"((uint32_t)x)
-                 : "memory");
-    return r != 0;
-}
-
-template <class G>
-__device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, uint32_t tmem,
-                                            uint32_t smem, uint32_t bars, int tid,
-                                            volatile int *abort, float (*red)[kFewRows],
-                                            const float *q_scale)
-{
-    constexpr int R = G::R;
-    const int warp = tid >> 5, lane = tid & 31;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    const float c = p.scale * 1.4426950408889634f;
-    float ref[R], sum[R]; // references in units of log2
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        ref[r] = -INFINITY;
-        sum[r] = 0.0f;
-    }
-    // e4m3: this thread's key's scales, asked for a tile ahead
-    float ks = 1.0f, vs = 1.0f;
-    int32_t blk = 0;
-    bool none = false;
-    auto key_at = [&](int v) { return real_tile(w, v) * G::KT + tid; };
-    auto ask = [&](int v, int32_t b) {
-        const int64_t slot = v < w.end ? key_slot(p, w, key_at(v), b, none) : -1;
-        ks = slot < 0 ? 1.0f : __ldg(p.rs + slot * p.rs_ss + w.head);
-        vs = slot < 0 ? 1.0f : __ldg(p.cs + slot * p.cs_ss + w.head);
-    };
-    if constexpr (G::QUANT) {
-        if (w.beg < w.end)
-            ask(w.beg, key_block(p, w, key_at(w.beg)));
-        if (w.beg + 1 < w.end)
-            blk = key_block(p, w, key_at(w.beg + 1));
-    }
-    for (int v = w.beg; v < w.end; ++v) {
-        const int ord = v - w.beg, i = ord & 1;
-        const bool see = key_seen(w, key_at(v));
-        const float my_ks = ks, my_vs = vs;
-        if constexpr (G::QUANT) {
-            ask(v + 1, blk);
-            if (v + 2 < w.end)
-                blk = key_block(p, w, key_at(v + 2));
-        }
-        bool ok = bar_wait(bars + (kBarS + i) * 8, (ord >> 1) & 1, abort, p.wait_limit_ns);
-        mma_fence_after();
-        uint32_t raw[G::N];
-#pragma unroll
-        for (int n = 0; n < G::N; n += 16)
-            tmem_ld16(tmem + i * G::N + n + lanes, raw + n);
-        tmem_ld_wait();
-#pragma unroll
-        for (int n = 0; n < G::N; n += 16)
-            tmem_pin16(raw + n);
-        float x[R], inv = 1.0f;
-        if constexpr (G::QUANT) {
-            const float e = (float)((int)(__float_as_uint(my_vs) >> 23) - 127);
-            inv = __uint_as_float((254u << 23) - __float_as_uint(my_vs)); // 1 / 2^e
-            const float cks = c * my_ks;
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                x[r] = fmaf(fmaf(__uint_as_float(raw[R + r]), 0.0625f, __uint_as_float(raw[r])),
-                            cks * q_scale[r], e);
-        } else {
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                x[r] = __uint_as_float(raw[r]) * c;
-        }
-        bool grew = false;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            x[r] = see ? x[r] : -INFINITY;
-            grew |= x[r] - ref[r] > kLazyFew;
-        }
-        if (softmax_any(grew || !ok)) {
-            if (softmax_any(!ok))
-                return false;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                float m = x[r];
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1)
-                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-                if (lane == 0)
-                    red[warp][r] = m;
-            }
-            bar_wait_all(1, 128);
-            float f[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float m = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
-                const bool up = m - ref[r] > kLazyFew;
-                f[r] = up ? exp2_fast(ref[r] - m) : 1.0f;
-                ref[r] = up ? m : ref[r];
-                sum[r] *= f[r];
-            }
-            if (ord > 0) { // a lane of Oᵀ is a value column, its columns are the rows
-                ok = bar_wait(bars + kBarO * 8, (ord - 1) & 1, abort, p.wait_limit_ns);
-                if (softmax_any(!ok))
-                    return false;
-                mma_fence_after();
-                uint32_t o[G::N];
-#pragma unroll
-                for (int n = 0; n < G::N; n += 16)
-                    tmem_ld16(tmem + G::O_COL + n + lanes, o + n);
-                tmem_ld_wait();
-#pragma unroll
-                for (int n = 0; n < G::N; n += 16)
-                    tmem_pin16(o + n);
-#pragma unroll
-                for (int n = 0; n < G::N; ++n)
-                    if (G::QUANT || n < R)
-                        o[n] = __float_as_uint(__uint_as_float(o[n]) * f[n % R]);
-#pragma unroll
-                for (int n = 0; n < G::N; n += 16)
-                    tmem_st16(tmem + G::O_COL + n + lanes, o + n);
-                tmem_st_wait();
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            x[r] = exp2_fast(x[r] - (ref[r] == -INFINITY ? 0.0f : ref[r]));
-            sum[r] = G::QUANT ? fmaf(x[r], inv, sum[r]) : sum[r] + x[r];
-        }
-        const uint32_t buf = smem + G::P_AT + i * G::P_BYTES;
-        if constexpr (G::QUANT) {
-            // 16 bytes a key and 16 rows: the high parts, then the low ones
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                x[r] *= 16.0f;
-            uint2 hi[R / 8], lo[R / 8];
-#pragma unroll
-            for (int r = 0; r < R; r += 8)
-                split8(x + r, hi[r / 8], lo[r / 8]);
-            if constexpr (R == 8) {
-                sts16(buf + tid * 16, make_uint4(hi[0].x, hi[0].y, lo[0].x, lo[0].y));
-            } else {
-                sts16(buf + few_weight(tid), make_uint4(hi[0].x, hi[0].y, hi[1].x, hi[1].y));
-                sts16(buf + few_weight(tid) + 128, make_uint4(lo[0].x, lo[0].y, lo[1].x, lo[1].y));
-            }
-        } else {
-#pragma unroll
-            for (int r = 0; r < R; r += 8)
-                sts16(buf + few_weight(tid) + r * 16,
-                      make_uint4(pack_bf16(x[r], x[r + 1]), pack_bf16(x[r + 2], x[r + 3]),
-                                 pack_bf16(x[r + 4], x[r + 5]), pack_bf16(x[r + 6], x[r + 7])));
-        }
-        async_fence();
-        mma_fence_before();
-        bar_signal(bars + (kBarP + i) * 8);
-    }
-    if (softmax_any(!bar_wait(bars + kBarDone * 8, 0, abort, p.wait_limit_ns)))
-        return false;
-    mma_fence_after();
-    // the sums of the block's keys
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        float m = sum[r];
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            m += __shfl_xor_sync(0xFFFFFFFFu, m, d);
-        if (lane == 0)
-            red[warp][r] = m;
-    }
-    bar_wait_all(1, 128);
-    uint32_t o[G::N];
-#pragma unroll
-    for (int n = 0; n < G::N; n += 16)
-        tmem_ld16(tmem + G::O_COL + n + lanes, o + n);
-    tmem_ld_wait();
-#pragma unroll
-    for (int n = 0; n < G::N; n += 16)
-        tmem_pin16(o + n);
-    const bool parts = w.splits > 1;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (r >= p.group)
-            break;
-        const float l = (red[0][r] + red[1][r]) + (red[2][r] + red[3][r]);
-        float y = __uint_as_float(o[r]);
-        if constexpr (G::QUANT)
-            y = fmaf(__uint_as_float(o[R + r]), 0.0625f, y) * 0.0625f;
-        y = l == 0.0f ? 0.0f : y / l;
-        const int h = w.head * p.group + r;
-        const int64_t at = w.q0 * p.heads + h;
-        if (parts)
-            p.part[(w.split * p.total_q * p.heads + at) * G::DV + tid] = y;
-        else
-            *reinterpret_cast<uint16_t *>(p.out + w.q0 * p.o_ts + h * p.o_hs + tid * 2) =
-                (uint16_t)pack_bf16(y, y);
-        if (tid == 0) {
-            const float lse = l == 0.0f ? -INFINITY : ref[r] * 0.6931471805599453f + logf(l);
-            if (parts)
-                p.part_lse[w.split * p.total_q * p.heads + at] = lse;
-            else if (p.lse)
-                p.lse[at] = lse;
-        }
-    }
-    return true;
-}
-
-template <class G>
-__device__ __forceinline__ bool few_mma(const AttnParams &p, const Work &w, uint32_t tmem,
-                                        uint32_t smem, uint32_t bars, uint32_t lead,
-                                        volatile int *abort)
-{
-    const uint32_t full = bars + kBarRing * 8, empty = full + G::STAGES * 8;
-    const uint32_t q = operand(smem + G::Q_AT, 16);
-    // Pᵀ: no swizzle; core matrices of 8 keys x 16 bytes, 128 bytes to the rows of the
-    // next 16 bytes, P_BYTES / 16 to the next 8 keys
-    constexpr uint32_t kWeightHigh = (128u >> 4) | (1u << 14);
-    constexpr uint32_t kKeys8 = G::P_BYTES / 16;
-    int stage = 0, phase = 0, vstage = 0;
-    auto next = [&] {
-        if (++stage == G::STAGES) {
-            stage = 0;
-            phase ^= 1;
-        }
-    };
-    for (int v = w.beg; v <= w.end; ++v) {
-        const int ord = v - w.beg, i = ord & 1;
-        const bool more = v < w.end;
-        if (more) {
-            if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
-                return false;
-            const uint32_t k = operand(smem + stage * G::STAGE, 16);
-            if constexpr (G::QUANT) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) // 32 columns of 8 bits
-                    mma_smem_e4m3<G::N, 0>(tmem + i * G::N, k + j * 2, q + j * 2, j > 0, lead,
-                                           kOperandHigh);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    mma_smem<G::N>(tmem + i * G::N, k + (j >> 2) * (16384 >> 4) + (j & 3) * 2,
-                                   q + (j >> 2) * (2048 >> 4) + (j & 3) * 2, j > 0, lead);
-            }
-            bar_signal_mma(bars + (kBarS + i) * 8, lead);
-            bar_signal_mma(empty + stage * 8, lead);
-            next();
-        }
-        if (ord > 0) {
-            const int b = 1 - i;
-            if (!bar_wait(bars + (kBarP + b) * 8, ((ord - 1) >> 1) & 1, abort, p.wait_limit_ns))
-                return false;
-            mma_fence_after();
-            const uint32_t a = operand(smem + vstage * G::STAGE, 16384);
-            const uint32_t pt = operand(smem + G::P_AT + b * G::P_BYTES, kKeys8);
-            if constexpr (G::QUANT) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) // 32 keys
-                    mma_smem_e4m3<G::N, 1>(tmem + G::O_COL, a + j * (4096 >> 4),
-                                           pt + j * (4 * kKeys8 >> 4), ord > 1 || j > 0, lead,
-                                           kWeightHigh);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) // 16 keys
-                    mma_smem<G::N, 1>(tmem + G::O_COL, a + j * (2048 >> 4),
-                                      pt + j * (2 * kKeys8 >> 4), ord > 1 || j > 0, lead,
-                                      kWeightHigh);
-            }
-            bar_signal_mma(empty + vstage * 8, lead);
-            bar_signal_mma(bars + kBarO * 8, lead);
-        }
-        if (more) {
-            vstage = stage;
-            if (!bar_wait(full + stage * 8, phase, abort, p.wait_limit_ns))
-                return false;
-            next();
-        }
-    }
-    bar_signal_mma(bars + kBarDone * 8, lead);
-    return true;
-}
-
-// The queries of a block as e4m3 parts, a row's largest value in [128, 256) after a
-// power-of-two scale; rows past the group are 0.  16 threads to a row.
-template <class G>
-__device__ __forceinline__ void few_queries_e4m3(const AttnParams &p, const Work &w, uint32_t q_smem,
-                                                 int lt, float *q_scale)
-{
-    for (int r = lt >> 4; r < G::R; r += 8) {
-        const int c = lt & 15;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < p.group)
-            v = __ldg(reinterpret_cast<const uint4 *>(
-                    p.q + w.q0 * p.q_ts + (int64_t)(w.head * p.group + r) * p.q_hs) + c);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t a = u[i] & 0x7FFFu, b = (u[i] >> 16) & 0x7FFFu;
-            m = max(m, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
-        }
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1)
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        // 2^e of the row's scale: the exponent of its largest value, less 7
-        const int e = min(max((int)(m >> 7) - 134, -120), 120);
-        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(u[i] << 16) * inv;
-            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u) * inv;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) // what was infinite is NaN
-            x[i] = fabsf(x[i]) < 256.0f ? x[i] : __uint_as_float(0x7FC00000u);
-        uint2 hi, lo;
-        split8(x, hi, lo);
-        const uint32_t at = q_smem + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi.x), "r"(hi.y) : "memory");
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + G::R * 128), "r"(lo.x), "r"(lo.y)
-                     : "memory");
-        if (c == 0)
-            q_scale[r] = __uint_as_float((uint32_t)(127 + e) << 23);
-    }
-}
-
-template <class G>
-__global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
-    const __grid_constant__ AttnParams p)
-{
-    extern __shared__ unsigned char raw_smem[];
-    __shared__ uint32_t s_tmem, s_status;
-    __shared__ volatile int s_abort;
-    __shared__ float s_red[4][kFewRows], s_qscale[kFewRows];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
-    const uint32_t bars = smem + G::BAR_AT;
-
-    const int x = (int)blockIdx.x, y = p.by_heads.quotient(x);
-    Work w;
-    w.seq = p.by_splits.quotient(y);
-    w.head = x - y * p.kv_heads;
-    w.split = y - w.seq * p.max_splits;
-    w.row0 = 0;
-    bool bad = !seq_queries(p, w.seq, w.q0, w.n);
-    bool go = w.n > 0;
-    if (go && !seq_keys(p, w.seq, w.len)) {
-        bad = true;
-        go = false;
-    }
-    if (go) {
-        const int nv = key_tiles<G::KT, 1>(p, w);
-        go = take_split(p, nv, w);
-    }
-    if (!go) {
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        if (tid == 0)
-            write_block_status(p.header, bad ? kStatusOutOfRange : kStatusOk, blockIdx.x,
-                               p.status_words);
-        return;
-    }
-    if (tid == 0) {
-        s_status = kStatusOk;
-        s_abort = 0;
-        bar_init(bars + kBarQ * 8, 128);
-        bar_init(bars + kBarDone * 8, 1);
-        for (int i = 0; i < 2; ++i) {
-            bar_init(bars + (kBarS + i) * 8, 1);
-            bar_init(bars + (kBarP + i) * 8, 128);
-            bar_init(bars + (kBarO + i) * 8, 1); // the second: drain
-        }
-        for (int i = 0; i < G::STAGES; ++i) {
-            bar_init(bars + (kBarRing + i) * 8, 128);
-            bar_init(bars + (kBarRing + G::STAGES + i) * 8, 1);
-        }
-        bar_init_fence();
-    }
-    if (warp == 8)
-        tmem_alloc(smem_u32(&s_tmem), G::COLS);
-    mma_fence_before();
-    __syncthreads();
-    mma_fence_after();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const uint32_t tmem = s_tmem;
-
-    if (warp < 4) {
-        if constexpr (G::QUANT) // the scales of the queries
-            bar_wait_all(2, 256);
-        few_softmax<G>(p, w, tmem, smem, bars, tid, &s_abort, s_red, s_qscale);
-    } else if (warp < 8) {
-        const int lt = tid - 128;
-        if constexpr (G::QUANT) {
-            few_queries_e4m3<G>(p, w, smem + G::Q_AT, lt, s_qscale);
-            bar_arrive(2, 256);
-            async_fence();
-            bar_signal(bars + kBarQ * 8);
-        } else {
-            for (int i = lt; i < kFewRows * 16; i += 128) { // rows past the group are 0
-                const int r = i >> 4, c = i & 15;
-                const bool ok = r < p.group;
-                const char *src = p.q + w.q0 * p.q_ts +
-                                  (int64_t)(w.head * p.group + (ok ? r : 0)) * p.q_hs + c * 16;
-                copy16(smem + G::Q_AT + (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                       src, ok ? 16u : 0u);
-            }
-            bar_signal_copies(bars + kBarQ * 8);
-        }
-        bool out = false;
-        load_heads<G>(p, w, smem, bars + kBarRing * 8, warp - 4, lane, &s_abort, out);
-        if (out)
-            s_status = kStatusOutOfRange;
-        asm volatile("cp.async.wait_all;" ::: "memory");
-    } else {
-        const uint32_t lead = elect_lane();
-        bool ok = bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
-        if (ok) {
-            async_fence();
-            ok = few_mma<G>(p, w, tmem, smem, bars, lead, &s_abort);
-        }
-        if (!ok) { // let what was issued finish before tensor memory goes
-            int none = 0;
-            bar_signal_mma(bars + (kBarO + 1) * 8, lead);
-            bar_wait(bars + (kBarO + 1) * 8, 0, &none, 1000000000ll);
-        }
-    }
-    mma_fence_before();
-    __syncthreads();
-    mma_fence_after();
-    if (warp == 8)
-        tmem_free(tmem, G::COLS);
-    if (tid == 0)
-        write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, p.status_words);
-}
-
-// Joins the parts of rows whose keys were split: a warp per (token, head).
-//   lse = log Σ exp(lse_s),  out = Σ exp(lse_s - lse) out_s
-template <class G>
-__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnParams p)
-{
-    const int lane = threadIdx.x & 31;
-    const int64_t rows = p.total_q * p.heads;
-    const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int64_t tok = at / p.heads;
-    const int h = (int)(at - tok * p.heads);
-    int splits = 0;
-    if (at < rows) {
-        int a = 0, b = p.num_seqs; // the last sequence that starts at or before the token
-        while (b - a > 1) {
-            const int mid = (a + b) / 2;
-            if (p.q_off[mid] <= tok)
-                a = mid;
-            else
-                b = mid;
-        }
-        Work w;
-        if (seq_queries(p, a, w.q0, w.n) && seq_keys(p, a, w.len) && tok >= w.q0 &&
-            tok < w.q0 + w.n) {
-            const int row = (int)(tok - w.q0) * p.group + h % p.group;
-            w.row0 = row / (kRows * G::NT) * (kRows * G::NT);
-            splits = p.by_run.quotient(key_tiles<G::KT, G::NT>(p, w) + p.split_tiles - 1);
-        }
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (splits <= 1)
-        return; // the row's block wrote it
-    float top = -INFINITY;
-    for (int s = lane; s < splits; s += 32)
-        top = fmaxf(top, p.part_lse[s * rows + at]);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float acc[G::DV / 32] = {}, sum = 0.0f;
-    for (int s = 0; s < splits; ++s) {
-        const float wgt = expf(p.part_lse[s * rows + at] - ref);
-        sum += wgt;
-        const float4 *o = reinterpret_cast<const float4 *>(p.part + (s * rows + at) * G::DV);
-#pragma unroll
-        for (int i = 0; i < G::DV / 128; ++i) {
-            const float4 x = o[i * 32 + lane];
-            acc[i * 4] = fmaf(wgt, x.x, acc[i * 4]);
-            acc[i * 4 + 1] = fmaf(wgt, x.y, acc[i * 4 + 1]);
-            acc[i * 4 + 2] = fmaf(wgt, x.z, acc[i * 4 + 2]);
-            acc[i * 4 + 3] = fmaf(wgt, x.w, acc[i * 4 + 3]);
-        }
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    char *out = p.out + tok * p.o_ts + h * p.o_hs;
-#pragma unroll
-    for (int i = 0; i < G::DV / 128; ++i)
-        *reinterpret_cast<uint2 *>(out + (i * 128 + lane * 4) * 2) =
-            make_uint2(pack_bf16(acc[i * 4] * inv, acc[i * 4 + 1] * inv),
-                       pack_bf16(acc[i * 4 + 2] * inv, acc[i * 4 + 3] * inv));
-    if (lane == 0 && p.lse)
-        p.lse[at] = sum == 0.0f ? -INFINITY : ref + logf(sum);
-}
-
-// Tensor map of one part of the pool's rows (`width` columns of bf16 or bytes): boxes
-// of 128 bytes and p.box_rows rows, swizzled as the MMAs read them.
-bool encode_map(CUtensorMap *map, const char *base, int64_t row_bytes, int64_t rows, int width,
-                int box_rows, bool bytes)
-{
-    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
-                                             cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    if (!encode)
-        return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-    const cuuint32_t box[2] = {bytes ? 128u : 64u, (cuuint32_t)box_rows}, step[2] = {1, 1};
-    return encode(map,
-                  bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<char *>(base), dims, strides,
-                  box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Rows are copied as boxes where a block of the pool is a multiple of 8 rows (the
-// swizzle's period) and divides a key tile, or the other way round.
-template <class G>
-void set_boxes(AttnParams &p)
-{
-    p.box_rows = 0;
-    const int b = p.block;
-    const int64_t rows = p.num_blocks * b;
-    const int heads = p.kv_heads;
-    if (b % 8 != 0 || (G::KT % b != 0 && b % G::KT != 0) || rows >= 0x7FFFFFFFll)
-        return;
-    const int box = std::min(b, G::KT);
-    const int copy = G::MLA ? 512 : heads * 128, rot = G::MLA ? 64 : heads * 128;
-    if (encode_map(&p.copy_map, p.copy, p.copy_ss, rows, copy, box, G::QUANT) &&
-        encode_map(&p.rot_map, p.rot, p.rot_ss, rows, rot, box, G::QUANT))
-        p.box_rows = box;
-}
-
-// Joins split rows; starts while the last blocks run and waits for them on the
-// device.
-template <class G>
-cudaError_t launch_join(const AttnParams &p, cudaStream_t stream)
-{
-    if (p.max_splits == 1)
-        return cudaSuccess;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((p.total_q * p.heads + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<G>, p);
-}
-
-// The kernel's limit of dynamic shared memory, raised once on each device.
-template <auto KERNEL>
-cudaError_t allow_smem(int bytes)
-{
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && (done.load() >> dev) & 1u))
-        return e;
-    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev < 64)
-        done.fetch_or(uint64_t(1) << dev);
-    return e;
-}
-
 template <class G>
 cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
 {
@@ -2512,20 +1096,6 @@ cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
             return cudaErrorInvalidConfiguration;
     }
     attention_kernel<G><<<(unsigned)blocks, kAttnThreads<G>, bytes, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess)
-        return e;
-    return launch_join<G>(p, stream);
-}
-
-template <class G>
-cudaError_t launch_few(AttnParams &p, int64_t blocks, cudaStream_t stream)
-{
-    static_assert(G::BYTES <= 113 * 1024, "two blocks to an SM");
-    set_boxes<G>(p);
-    cudaError_t e = allow_smem<attention_few_kernel<G>>(G::BYTES);
-    if (e != cudaSuccess)
-        return e;
-    attention_few_kernel<G><<<(unsigned)blocks, kFewThreads, G::BYTES, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     return launch_join<G>(p, stream);
@@ -2567,6 +1137,11 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
                              ? nv
                              : std::max<int64_t>(4, (units * nv + 4 * slots - 1) / (4 * slots));
     pl.split_tiles = (int32_t)std::min(nv, want);
+    // one round of few blocks and short rows: up to 8 runs in a cluster
+    const int64_t run = (nv + 7) / 8;
+    pl.cluster = few && nv > 1 && run <= 4 && units * ((nv + run - 1) / run) <= slots;
+    if (pl.cluster)
+        pl.split_tiles = (int32_t)run;
     pl.max_splits = (int32_t)((nv + pl.split_tiles - 1) / pl.split_tiles);
     pl.blocks = units * pl.max_splits;
     return pl;
@@ -2575,6 +1150,7 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
 cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cudaStream_t stream)
 {
     const bool quant = p.cs != nullptr;
+    p.cluster = pl.cluster ? 1 : 0;
     p.by_group = Divisor((uint32_t)p.group);
     p.by_block = Divisor((uint32_t)p.block);
     p.by_heads = Divisor(kind == RowKind::Mla ? 2u : (uint32_t)p.kv_heads);
@@ -2583,12 +1159,8 @@ cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cu
     if (kind == RowKind::Mla)
         return quant ? launch<MlaGeo<true>>(p, pl.blocks, stream)
                      : launch<MlaGeo<false>>(p, pl.blocks, stream);
-    if (pl.row_tiles == 0 && p.group <= 8)
-        return quant ? launch_few<FewGeo<true, 8>>(p, pl.blocks, stream)
-                     : launch_few<FewGeo<false, 8>>(p, pl.blocks, stream);
     if (pl.row_tiles == 0)
-        return quant ? launch_few<FewGeo<true, 16>>(p, pl.blocks, stream)
-                     : launch_few<FewGeo<false, 16>>(p, pl.blocks, stream);
+        return launch_attention_few(p, pl.blocks, stream);
     if (pl.row_tiles == 2)
         return launch<HeadGeo<false, 2>>(p, pl.blocks, stream);
     return quant ? launch<HeadGeo<true, 1>>(p, pl.blocks, stream)

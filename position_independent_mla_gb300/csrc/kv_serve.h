@@ -116,9 +116,10 @@ struct AttnParams {
     int32_t causal, window, sinks;
     float scale;
     // split of the key axis, and the parts that are joined afterwards
-    int32_t split_tiles, max_splits;
+    int32_t split_tiles, max_splits, cluster;
     float *part, *part_lse; // [max_splits][total_q][heads][value width], [..][heads]
     int64_t wait_limit_ns;
+    int64_t skip_block; // test hook: this block issues no MMA (-1: none)
     uint32_t *header;
     uint32_t status_words; // of the call: this kernel's blocks, and those of an expansion
     // filled in by launch_attention: quotients by group, block, key heads (MLA: halves),
@@ -142,6 +143,7 @@ struct AttnPlan {
     int32_t row_tiles;   // 128-row tiles of a block; 0: the kernel for few rows
     int32_t split_tiles; // key tiles of a block
     int32_t max_splits;
+    bool cluster;        // the splits of a row are a cluster that joins them itself
     int64_t blocks;
 };
 

@@ -181,3 +181,39 @@ def test_offsets_beyond_32_bits():
     kv.kv_attention(desc, 0, attn, b.q, out, lse, kv.attn_workspace(desc, attn, b.q))
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("kind,heads,lens", [("mla", 128, [(1, 700), (1, 300)]),
+                                             ("gqa", 32, [(70, 700)]), ("gqa", 32, [(1, 700)]),
+                                             ("gqa", 32, [(1, 9000)] * 3),
+                                             ("mha", 32, [(40, 300)])])
+@pytest.mark.parametrize("block", [0, 3])
+def test_a_wait_that_runs_out_is_reported_and_ends(kind, heads, lens, block):
+    """A block that gets no MMA gives up after the wait limit; the other blocks and
+    the next call are not affected."""
+    b = Batch(kind, lens, heads, seed=20)
+    want, wl = (t.clone() for t in b.run())
+    kv.kv_set_wait_limit_ns(20_000_000)
+    kv.kv_set_attention_skip_block(block)
+    try:
+        b.run(kv.KV_ERR_TIMEOUT)
+    finally:
+        kv.kv_set_attention_skip_block(-1)
+        kv.kv_set_wait_limit_ns(0)
+    out, lse = b.run()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_widened_rows_and_rows_beyond_that_workspace_agree():
+    """Chunks over a quantised pool: widened first, or (max_kv_len stated so large that
+    the widened rows would pass the limit) converted by every tile on its way."""
+    for kind in ("gqa", "mla"):
+        b = Batch(kind, [(40, 700), (33, 33)], HEADS[kind], quant=True, seed=21)
+        out, lse = (t.clone() for t in b.check())
+        assert kv.kv_last_launch_count() >= 2
+        b.attn.max_kv_len = 1 << 20
+        b.attn.max_blocks = b.table.shape[1]
+        n = kv.kv_attention_workspace_size(b.desc, b.attn, b.n, b.heads)
+        assert n < 1 << 30
+        b.ws = kv.attn_workspace(b.desc, b.attn, b.q)
+        b.check()
