@@ -424,8 +424,9 @@ size_t kv_quantize_workspace_size(const kv_quant_pool_desc *pool);
  * slot i when d_src_slots is NULL) goes to slot d_dst_slots[i] of `dst`, in
  * layers dst_layer .. dst_layer + src->num_layers - 1 (layer l of src in layer
  * dst_layer + l).  `src` describes new rows ([layers][rows], block_size 1) or a
- * paged pool.  Slots of dst that occur twice hold either row.  An index outside
- * its pool is skipped and sets KV_ERR_OUT_OF_RANGE.  One kernel. */
+ * paged pool.  A slot of dst occurs once in a call (of rows that share one, values
+ * and scales mix).  An index outside its pool is skipped and sets
+ * KV_ERR_OUT_OF_RANGE.  One kernel. */
 kv_status kv_quantize(const kv_pool_desc *src, const int32_t *d_src_slots,
                       const kv_quant_pool_desc *dst, int32_t dst_layer, int64_t num_rows,
                       const int32_t *d_dst_slots, void *d_workspace, size_t workspace_bytes,
@@ -487,7 +488,8 @@ size_t kv_attention_quant_workspace_size(const kv_quant_pool_desc *pool, const k
  * d_q + t*q_tok_stride + h*q_head_stride + i, of the result likewise at d_out
  * (strides multiples of 8 elements, bases 16-byte aligned); d_lse (NULL = not
  * wanted) is fp32 [total_q][num_heads].  num_heads is a multiple of rot_heads,
- * at most 128 query heads to a key head (else KV_ERR_UNSUPPORTED).  A sequence
+ * at most 128 query heads to a key head and 2^30 (token, head) rows of a sequence
+ * to a key head (else KV_ERR_UNSUPPORTED).  A sequence
  * whose lengths on the device pass max_q_len, max_kv_len or its block-table row
  * is skipped, and a block id outside the pool reads as rows of zeros; both set
  * KV_ERR_OUT_OF_RANGE.  One to three kernels: rows of a quantised pool that

@@ -1109,16 +1109,21 @@ kv_status kv_get_device_status(const void *d_workspace, kv_stream_t stream)
         return KV_ERR_WORKSPACE;
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return KV_ERR_CUDA;
-    uint32_t head[kHeaderCountWord + 1];
+    uint32_t head[kHeaderCountWord + 2];
     if (cudaMemcpy(head, d_workspace, sizeof head, cudaMemcpyDeviceToHost) != cudaSuccess)
         return KV_ERR_CUDA;
     uint32_t st = head[0];
-    if (head[kHeaderCountWord] > 0) { // one word per block of the call (kv_serve.h)
-        std::vector<uint32_t> words(head[kHeaderCountWord]);
-        if (cudaMemcpy(words.data(), static_cast<const char *>(d_workspace) + kHeaderBytes,
-                       words.size() * sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
+    // one word per block of the call (kv_serve.h); a workspace no call has used may hold
+    // anything
+    const uint32_t count = head[kHeaderCountWord + 1] == ~head[kHeaderCountWord]
+                               ? head[kHeaderCountWord] : 0;
+    uint32_t words[1024];
+    for (uint32_t at = 0, n = 0; at < count && st == kStatusOk; at += n) {
+        n = std::min<uint32_t>(count - at, 1024);
+        if (cudaMemcpy(words, static_cast<const char *>(d_workspace) + kHeaderBytes + (size_t)at * 4,
+                       n * sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
             return KV_ERR_CUDA;
-        for (size_t i = 0; i < words.size() && st == kStatusOk; ++i)
+        for (uint32_t i = 0; i < n && st == kStatusOk; ++i)
             st = words[i];
     }
     return static_cast<kv_status>(st);
@@ -1303,7 +1308,15 @@ kv_status attn_ok(const kv_attn_desc *a, int64_t total_q, int32_t heads, int32_t
         return KV_ERR_INVALID_ARG;
     if (total_q > (int64_t)a->num_seqs * a->max_q_len)
         return KV_ERR_INVALID_ARG;
-    return heads / kv_heads > 128 ? KV_ERR_UNSUPPORTED : KV_OK;
+    const int32_t group = heads / kv_heads; // rows of a sequence are counted in 32 bits
+    return group > 128 || std::min<int64_t>(total_q, a->max_q_len) * group > kMaxRows
+               ? KV_ERR_UNSUPPORTED : KV_OK;
+}
+
+// A window as long as any sequence hides nothing.
+int32_t attn_window(const kv_attn_desc *a)
+{
+    return a->window >= a->max_kv_len ? 0 : a->window;
 }
 
 AttnPlan attn_plan(RowKind kind, bool quant, const kv_attn_desc *a, int64_t total_q,
@@ -1315,7 +1328,7 @@ AttnPlan attn_plan(RowKind kind, bool quant, const kv_attn_desc *a, int64_t tota
     s.num_seqs = a->num_seqs;
     s.max_q_len = a->max_q_len;
     s.max_kv_len = a->max_kv_len;
-    s.window = a->window;
+    s.window = attn_window(a);
     s.sinks = a->sinks;
     s.group = heads / kv_heads;
     s.kv_heads = kv_heads;
@@ -1413,12 +1426,12 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
     p.max_q_len = a->max_q_len;
     p.max_kv_len = a->max_kv_len;
     p.max_blocks = a->max_blocks;
-    p.max_keys = (int64_t)a->max_blocks * block;
+    p.max_keys = std::min<int64_t>((int64_t)a->max_blocks * block, kMaxKeys);
     p.q_off = a->d_q_off;
     p.kv_len = a->d_kv_len;
     p.block_tables = a->d_block_tables;
     p.causal = a->causal;
-    p.window = a->window;
+    p.window = attn_window(a);
     p.sinks = a->sinks;
     p.scale = a->scale;
     p.split_tiles = pl.split_tiles;
@@ -1444,7 +1457,7 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
         e.num_seqs = a->num_seqs;
         e.max_kv_len = a->max_kv_len;
         e.max_blocks = a->max_blocks;
-        e.window = a->window;
+        e.window = p.window;
         e.sinks = a->sinks;
         e.q_off = a->d_q_off;
         e.kv_len = a->d_kv_len;
@@ -1463,7 +1476,7 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
         p.block = kExpandBlock;
         p.block_tables = e.table;
         p.num_blocks = lay.pad / kExpandBlock * a->num_seqs;
-        p.max_keys = std::min<int64_t>((int64_t)p.max_blocks * block, lay.pad);
+        p.max_keys = std::min(p.max_keys, lay.pad);
         p.max_blocks = (int32_t)(lay.pad / kExpandBlock);
     }
     KV_CUDA(launch_attention(p, kind, pl, stream));

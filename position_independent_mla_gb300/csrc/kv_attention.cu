@@ -42,6 +42,7 @@ namespace kvr {
 namespace {
 
 constexpr int64_t kExpandBytes = int64_t(2) << 30; // largest workspace for widened rows
+constexpr int64_t kPrefetchWait = 20000; // ns that a warp waits before it prefetches anyway
 constexpr float kLazy = 8.0f;      // log2 of the growth of a maximum that O tolerates
 
 // ---------------------------------------------------------------------------
@@ -316,10 +317,11 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
                     blk = ask(u + 1 + skip);
                     const int ord = u - w.beg, stage = ord & 1, phase = ((ord >> 1) & 1) ^ 1;
                     const uint32_t full = bars + (part * 2 + stage) * 8;
-                    ok = bar_wait(full + G::BARS / 2 * 8, phase, abort, p.wait_limit_ns);
-                    if (!ok)
-                        break;
-                    if (before) {
+                    if (before) { // keeps step with the others, who do not wait for it
+                        int late = 0;
+                        bar_wait(full + G::BARS / 2 * 8, phase, &late, kPrefetchWait);
+                        if (*abort)
+                            break;
                         if (mine && u + skip < last) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
@@ -329,6 +331,9 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
                         }
                         continue;
                     }
+                    ok = bar_wait(full + G::BARS / 2 * 8, phase, abort, p.wait_limit_ns);
+                    if (!ok)
+                        break;
                     if (lane == 0)
                         bar_signal_bulk(full, G::LOAD_WARPS * 32,
                                         part == 0 ? G::OTHER : 2 * G::PANEL);

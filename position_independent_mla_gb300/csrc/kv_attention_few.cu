@@ -417,7 +417,7 @@ __device__ __forceinline__ void few_queries_e4m3(const AttnParams &p, const Work
 }
 
 // The blocks of a cluster hold the parts of one (sequence, key head): each joins some of
-// its rows.  `idle`: this block has no part.
+// its rows.  `idle`: this block has no part (or gave up).
 template <class G>
 __device__ __forceinline__ void few_join(const AttnParams &p, const Work &w, uint32_t smem, int tid,
                                          bool idle)
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
     if (warp == 8)
         tmem_free(tmem, G::COLS);
     if (p.cluster)
-        few_join<G>(p, w, smem, tid, false);
+        few_join<G>(p, w, smem, tid, s_abort != 0);
     if (tid == 0)
         write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, p.status_words);
 }

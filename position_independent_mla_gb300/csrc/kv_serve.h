@@ -13,7 +13,7 @@ constexpr int kGroup = 128; // values that share one scale of a quantised row
 // Status of a call without a clearing launch: every block of the call's main
 // kernel writes its own word after the workspace header (0 or an error code)
 // and block 0 writes the header, so nothing needs to be zero beforehand;
-// kv_get_device_status scans the words.
+// kv_get_device_status scans the words.  The count is followed by its complement.
 constexpr int kHeaderCountWord = 8; // header word: number of block words (0: word 0 holds all)
 
 __device__ __forceinline__ void write_block_status(uint32_t *header, uint32_t code,
@@ -23,6 +23,7 @@ __device__ __forceinline__ void write_block_status(uint32_t *header, uint32_t co
     if (block == 0) {
         header[0] = kStatusOk;
         header[kHeaderCountWord] = blocks;
+        header[kHeaderCountWord + 1] = ~blocks;
     }
 }
 
@@ -93,6 +94,10 @@ struct Divisor {
     }
 #endif
 };
+
+// Rows and keys of a sequence are 32-bit numbers in the kernels, with room for a tile past
+// the end.
+constexpr int64_t kMaxRows = 0x40000000, kMaxKeys = 0x7FFFFF00;
 
 struct AttnParams {
     // one layer of the pool: bf16 rows, or e4m3 rows with scales (cs != nullptr)

@@ -217,3 +217,32 @@ def test_widened_rows_and_rows_beyond_that_workspace_agree():
         assert n < 1 << 30
         b.ws = kv.attn_workspace(b.desc, b.attn, b.q)
         b.check()
+
+
+@pytest.mark.parametrize("kind,heads,quant", [("mla", 16, False), ("gqa", 32, True), ("gqa4", 28, False)])
+@pytest.mark.parametrize("window", [130, 391, (1 << 31) - 1])
+def test_windows_as_long_as_the_context(kind, heads, quant, window):
+    """Also with more queries than keys, whose first positions are negative."""
+    Batch(kind, [(150, 3), (1, 391), (130, 391)], heads, quant=quant, window=window, sinks=2,
+          seed=22).check()
+
+
+def test_workspaces_may_hold_anything_before_a_call():
+    b = Batch("gqa", [(1, 700), (5, 130)], 32, seed=23)
+    want = b.run()[0].clone()
+    for byte in (0xFF, 0x01, 0x80):
+        b.ws.fill_(byte)
+        assert torch.equal(b.run()[0], want)
+    kv.kv_set_wait_limit_ns(1_000_000)
+    try:  # a call whose status is one word, after one with a word per block
+        kv.kv_check_wait_timeout(b.ws, 1_000_000)
+        assert kv.kv_get_device_status(b.ws) == kv.KV_ERR_TIMEOUT
+    finally:
+        kv.kv_set_wait_limit_ns(0)
+    assert b.run()[0].equal(want)
+
+
+def test_more_rows_than_32_bits_count_are_refused():
+    b = Batch("gqa", [(1, 64)], 32, seed=24)
+    a = kv.attn_desc(*b.attn._tensors, 1 << 29, 64, b.scale)
+    assert kv.kv_attention_workspace_size(b.desc, a, 1 << 29, 32) == 0
