@@ -1349,7 +1349,9 @@ AttnLayout attn_layout(RowKind kind, const AttnPlan &pl, const kv_attn_desc *a, 
 {
     const bool mla = kind == RowKind::Mla;
     const bool parts = pl.max_splits > 1 && !pl.cluster;
-    const size_t rows = parts ? (size_t)pl.max_splits * total_q * heads : 0;
+    const size_t rows = !parts ? 0 : pl.rounds > 0 ? (size_t)pl.blocks * kRows
+                                   : (size_t)pl.max_splits * total_q * heads;
+    const int width = pl.rounds > 0 && mla ? 256 : mla ? 512 : 128;
     AttnLayout l;
     l.pad = (a->max_kv_len + kExpandBlock - 1) / kExpandBlock * kExpandBlock;
     const int64_t wide = pl.expand ? l.pad * a->num_seqs : 0;
@@ -1357,7 +1359,7 @@ AttnLayout attn_layout(RowKind kind, const AttnPlan &pl, const kv_attn_desc *a, 
     l.expand_blocks = wide > 0 ? expand_blocks(wide) : 0;
     l.lse = align256(kHeaderBytes + (size_t)(pl.blocks + l.expand_blocks) * 4);
     l.part = align256(l.lse + rows * 4);
-    l.table = align256(l.part + rows * (mla ? 512 : 128) * 4);
+    l.table = align256(l.part + rows * width * 4);
     l.rows = align256(l.table + (size_t)(wide / kExpandBlock) * 4);
     l.bytes = align256(l.rows + (size_t)wide * l.row_size);
     return l;

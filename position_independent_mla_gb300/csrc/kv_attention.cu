@@ -56,6 +56,7 @@ struct HeadGeo {
     static constexpr int NT = NT_, KT = 128;
     static constexpr int QPANELS = 2, OC = 128;    // query panels in shared memory; columns of O
     static constexpr int DV = 128;
+    static constexpr bool RUNS = NT == 1; // keys divided by find_run
     static_assert(NT == 1 || !QUANT, "e4m3 rows are widened before two row tiles read them");
     static constexpr int SOFT_WARPS = 8 * NT, LOAD_WARPS = NT == 2 ? 4 : 8;
     static constexpr int STAGE = 2 * 128 * 128;    // bytes of a K or V tile
@@ -83,6 +84,7 @@ struct MlaGeo {
     static constexpr bool MLA = true, QUANT = QUANT_;
     static constexpr int NT = 1, KT = 64;
     static constexpr int QPANELS = 5, OC = 256;
+    static constexpr bool RUNS = true;
     static constexpr int DV = 512;
     // e4m3 rows are converted by the load warps: twice as many
     static constexpr int SOFT_WARPS = 8, LOAD_WARPS = QUANT ? 16 : 8;
@@ -889,13 +891,15 @@ __device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, 
     if (valid && half == 0 && (!G::MLA || w.head == 0)) {
         const float lse = sum == 0.0f ? -INFINITY : st.top * p.scale + logf(sum);
         if (parts)
-            p.part_lse[w.split * p.total_q * p.heads + at] = lse;
+            p.part_lse[G::RUNS && p.rounds ? (int64_t)blockIdx.x * kRows + r
+                                : w.split * p.total_q * p.heads + at] = lse;
         else if (p.lse)
             p.lse[at] = lse;
     }
     char *out = p.out + (w.q0 + tok) * p.o_ts + h * p.o_hs + col0 * 2;
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0; // a row's sectors are whole
-    float *part = p.part + (w.split * p.total_q * p.heads + at) * G::DV + col0;
+    float *part = p.part + (G::RUNS && p.rounds ? ((int64_t)blockIdx.x * kRows + r) * G::OC + half * HO
+                                     : (w.split * p.total_q * p.heads + at) * G::DV + col0);
 #pragma unroll 1
     for (int i = 0; i < HO; i += 32) {
         uint32_t o[32];
@@ -969,17 +973,29 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
         // block -> (row tile, key head or half, split); heads of one row tile and
         // its halves are neighbours, so their rows meet in L2
         const int heads = G::MLA ? 2 : p.kv_heads, x = (int)blockIdx.x;
-        const int y = p.by_heads.quotient(x), tile = p.by_splits.quotient(y);
         Work w{};
-        w.head = x - y * heads;
-        w.split = y - tile * p.max_splits;
         int at = 0;
-        bool bad = false;
-        bool go = find_tile<kRows * G::NT>(p, tile, lane, w, at, bad);
-        if (go) {
-            w.row0 = at * kRows * G::NT;
-            const int nv = key_tiles<G::KT, G::NT>(p, w);
-            go = take_split(p, nv, w);
+        bool bad = false, go;
+        if (G::RUNS && p.rounds > 0) {
+            go = find_run<G>(p, lane, x, -1, w, at, bad);
+        } else {
+            const int y = p.by_heads.quotient(x), tile = p.by_splits.quotient(y);
+            w.head = x - y * heads;
+            w.split = y - tile * p.max_splits;
+            if (G::NT == 1 && p.by_seq) {
+                w.seq = tile;
+                bad = !seq_queries(p, tile, w.q0, w.n);
+                const bool keys = seq_keys(p, tile, w.len);
+                go = w.n > 0 && keys;
+                bad |= w.n > 0 && !keys;
+            } else {
+                go = find_tile<kRows * G::NT>(p, tile, lane, w, at, bad);
+            }
+            if (go) {
+                w.row0 = at * kRows * G::NT;
+                const int nv = key_tiles<G::KT, G::NT>(p, w);
+                go = take_split(p, nv, w);
+            }
         }
         if (lane == 0) {
             s_work = w;
@@ -1123,7 +1139,8 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
     pl.row_tiles = few ? 0 : !mla && tiles_share && (!a.quant || pl.expand) ? 2 : 1;
     const int64_t rows = kRows * std::max(1, pl.row_tiles);
     // row tiles over all sequences: at most one partly filled one each
-    const int64_t tiles = few ? a.num_seqs : a.total_q * a.group / rows + a.num_seqs;
+    pl.by_seq = !few && !tiles_share;
+    const int64_t tiles = few || pl.by_seq ? a.num_seqs : a.total_q * a.group / rows + a.num_seqs;
     const int64_t units = tiles * (mla ? 2 : a.kv_heads);
     // most key tiles of one row tile
     int64_t nv = (a.max_kv_len + kt - 1) / kt;
@@ -1137,7 +1154,7 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
     // pieces of the key axis: enough blocks for a few on every SM, none shorter
     // than four tiles (a block's start and end cost about as much as two)
     // (whole rows when there are units for two rounds, and their parts need no joining)
-    const int64_t slots = few ? 2 * 152 : 152;
+    const int64_t slots = few ? 2 * kSms : kSms;
     const int64_t want = units >= 2 * slots && !few
                              ? nv
                              : std::max<int64_t>(4, (units * nv + 4 * slots - 1) / (4 * slots));
@@ -1149,6 +1166,12 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
         pl.split_tiles = (int32_t)run;
     pl.max_splits = (int32_t)((nv + pl.split_tiles - 1) / pl.split_tiles);
     pl.blocks = units * pl.max_splits;
+    // a sequence to a row tile, and they leave SMs idle: the device divides the keys
+    if (pl.by_seq && a.num_seqs <= kBalanceSeqs && units < 2 * slots && nv > kMinRun) {
+        pl.rounds = (int32_t)(units / slots) + 1;
+        pl.blocks = (pl.rounds + 1) * slots;
+        pl.max_splits = (int32_t)nv; // so many and no more
+    }
     return pl;
 }
 
@@ -1156,6 +1179,8 @@ cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cu
 {
     const bool quant = p.cs != nullptr;
     p.cluster = pl.cluster ? 1 : 0;
+    p.by_seq = pl.by_seq ? 1 : 0;
+    p.rounds = pl.rounds;
     p.by_group = Divisor((uint32_t)p.group);
     p.by_block = Divisor((uint32_t)p.block);
     p.by_heads = Divisor(kind == RowKind::Mla ? 2u : (uint32_t)p.kv_heads);

@@ -37,7 +37,8 @@ struct FewGeo {
     static constexpr int R = R_;                    // rows: 8 or 16
     static constexpr int N = QUANT ? 2 * R : 16;    // rows of the MMAs
     static constexpr int NT = 1, KT = 128;
-    static constexpr int DV = 128;
+    static constexpr int DV = 128, OC = 128;
+    static constexpr bool RUNS = false;
     static constexpr int LOAD_WARPS = 4;
     static constexpr int STAGE = (QUANT ? 1 : 2) * 128 * 128, STAGES = QUANT ? 6 : 3;
     static constexpr int RING = STAGES * STAGE;

@@ -10,7 +10,6 @@
 
 namespace kvr {
 
-constexpr int kRows = 128; // rows per tile: the M of an MMA
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p)
 {

@@ -107,23 +107,30 @@ __device__ __forceinline__ bool take_split(const AttnParams &p, int nv, Work &w)
     return w.split < w.splits;
 }
 
-// Lengths of sequence s; false when they do not fit what the call stated.
+// Queries [a, b) of a sequence, n of them; false (and none) when they do not fit what the
+// call stated.  Likewise its keys.
+__device__ __forceinline__ bool queries_fit(const AttnParams &p, int a, int b, int &n)
+{
+    const bool fit = a >= 0 && b >= a && b <= p.total_q && b - a <= p.max_q_len;
+    n = fit ? b - a : 0;
+    return fit;
+}
+
+__device__ __forceinline__ bool keys_fit(const AttnParams &p, int len)
+{
+    return len >= 0 && len <= p.max_kv_len && (int64_t)len <= p.max_keys;
+}
+
 __device__ __forceinline__ bool seq_queries(const AttnParams &p, int s, int64_t &q0, int &n)
 {
-    const int a = p.q_off[s], b = p.q_off[s + 1];
-    q0 = a;
-    n = b - a;
-    if (a < 0 || b < a || b > p.total_q || n > p.max_q_len) {
-        n = 0;
-        return false;
-    }
-    return true;
+    q0 = p.q_off[s];
+    return queries_fit(p, (int)q0, p.q_off[s + 1], n);
 }
 
 __device__ __forceinline__ bool seq_keys(const AttnParams &p, int s, int &len)
 {
     len = p.kv_len[s];
-    return len >= 0 && len <= p.max_kv_len && (int64_t)len <= p.max_keys;
+    return keys_fit(p, len);
 }
 
 // Row tile `tile` of the call -> sequence, its queries and keys, and the row tile
@@ -171,6 +178,103 @@ __device__ __forceinline__ bool find_tile(const AttnParams &p, int tile, int lan
     }
     bad = __any_sync(0xFFFFFFFFu, wrong) || (found && !keys);
     return found && keys;
+}
+
+// Where every sequence is one row tile, the device knows all the work of a call and can
+// divide it evenly: runs of keys as long as it takes for all blocks to fill whole rounds
+// of the SMs, p.rounds or one more, whichever ends earlier when a block costs as much as
+// kBlockCost tiles by itself.  So a long sequence among short ones gets more blocks.
+constexpr int kBalanceSeqs = 160, kMinRun = 4, kBlockCost = 5, kSms = 152;
+
+// The work of block `block`, or (block < 0) the blocks of sequence `seq`: `first` is the
+// first block of the sequence, whose blocks are [split][head].  One warp; false where
+// there is none.  `bad`: some sequence does not fit what the call stated.
+template <class G>
+__device__ __forceinline__ bool find_run(const AttnParams &p, int lane, int block, int seq, Work &w,
+                                         int &first, bool &bad)
+{
+    constexpr int PER = kBalanceSeqs / 32; // sequences of a lane
+    const int heads = G::MLA ? 2 : p.kv_heads;
+    int from[PER], to[PER], len[PER], nv[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) { // all loads in flight at once
+        const int s = i * 32 + lane;
+        const bool is = s < p.num_seqs;
+        from[i] = is ? p.q_off[s] : 0;
+        to[i] = is ? p.q_off[s + 1] : 0;
+        len[i] = is ? p.kv_len[s] : 0;
+    }
+    bool wrong = false;
+    int units = 0;
+    int64_t total = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        Work x{};
+        const bool fits = queries_fit(p, from[i], to[i], x.n);
+        x.len = len[i];
+        const bool keys = keys_fit(p, x.len);
+        wrong |= !fits || (x.n > 0 && !keys);
+        nv[i] = x.n > 0 && keys ? max(1, key_tiles<G::KT, 1>(p, x)) : 0;
+        units += nv[i] > 0;
+        total += nv[i];
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
+    units = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)units) * heads;
+    total *= heads;
+    bad = __any_sync(0xFFFFFFFFu, wrong);
+    const int turn = p.rounds + (lane & 1), room = turn * kSms - units; // at least 1
+    const int mine = (int)min(max((int64_t)kMinRun, (total + room - 1) / room),
+                               (int64_t)kMaxRows);
+    const int other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
+    const int less = lane & 1 ? other : mine, more = lane & 1 ? mine : other;
+    const int run = (int64_t)p.rounds * (less + kBlockCost) <=
+                            (int64_t)(p.rounds + 1) * (more + kBlockCost)
+                        ? less
+                        : more;
+    bool found = false;
+    int before = 0, tiles = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (i * 32 >= p.num_seqs)
+            break;
+        const int blocks = (nv[i] + run - 1) / run * heads;
+        int sum = blocks;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+            if (lane >= d)
+                sum += o;
+        }
+        const int at = before + sum - blocks;
+        const bool here = blocks > 0 && (block < 0 ? i * 32 + lane == seq
+                                                   : block >= at && block < at + blocks);
+        const uint32_t who = __ballot_sync(0xFFFFFFFFu, here);
+        if (who) {
+            const int l = __ffs((int)who) - 1;
+            w.seq = i * 32 + l;
+            w.q0 = __shfl_sync(0xFFFFFFFFu, from[i], l);
+            w.n = __shfl_sync(0xFFFFFFFFu, to[i], l) - (int)w.q0;
+            w.len = __shfl_sync(0xFFFFFFFFu, len[i], l);
+            tiles = __shfl_sync(0xFFFFFFFFu, nv[i], l);
+            first = __shfl_sync(0xFFFFFFFFu, at, l);
+            found = true;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    if (!found)
+        return false;
+    const int rel = max(0, block - first);
+    w.row0 = 0;
+    w.split = p.by_heads.quotient(rel);
+    w.head = rel - w.split * heads;
+    const int real = key_tiles<G::KT, 1>(p, w);
+    w.splits = (tiles + run - 1) / run;
+    const int each = (tiles + w.splits - 1) / w.splits;
+    w.beg = min(real, w.split * each);
+    w.end = min(real, w.beg + each);
+    return true;
 }
 
 __device__ __forceinline__ bool key_seen(const Work &w, int k)
@@ -394,7 +498,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
     const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int64_t tok = at / p.heads;
     const int h = (int)(at - tok * p.heads);
-    int splits = 0;
+    int splits = 0, first = 0, row = 0;
     if (at < rows) {
         int a = 0, b = p.num_seqs; // the last sequence that starts at or before the token
         while (b - a > 1) {
@@ -407,29 +511,45 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
         Work w;
         if (seq_queries(p, a, w.q0, w.n) && seq_keys(p, a, w.len) && tok >= w.q0 &&
             tok < w.q0 + w.n) {
-            const int row = (int)(tok - w.q0) * p.group + h % p.group;
-            w.row0 = row / (kRows * G::NT) * (kRows * G::NT);
-            splits = p.by_run.quotient(key_tiles<G::KT, G::NT>(p, w) + p.split_tiles - 1);
+            row = (int)(tok - w.q0) * p.group + h % p.group;
+            bool bad;
+            if (G::RUNS && p.rounds > 0) {
+                if constexpr (G::RUNS)
+                    splits = find_run<G>(p, lane, -1, a, w, first, bad) ? w.splits : 0;
+            } else {
+                w.row0 = row / (kRows * G::NT) * (kRows * G::NT);
+                splits = p.by_run.quotient(key_tiles<G::KT, G::NT>(p, w) + p.split_tiles - 1);
+            }
         }
     }
+    // part s of this row: of its lse, and of columns i * 128 ...
+    const int heads = G::MLA ? 2 : p.kv_heads, head = G::MLA ? 0 : h / p.group;
+    auto block_row = [&](int s, int half) {
+        return (int64_t)(first + s * heads + head + half) * kRows + row;
+    };
+    auto lse_at = [&](int s) { return G::RUNS && p.rounds ? block_row(s, 0) : s * rows + at; };
+    auto part_at = [&](int s, int i) {
+        constexpr int PER = G::OC / 128;
+        return G::RUNS && p.rounds ? block_row(s, i / PER) * G::OC + i % PER * 128
+                        : (s * rows + at) * G::DV + i * 128;
+    };
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (splits <= 1)
         return; // the row's block wrote it
     float top = -INFINITY;
     for (int s = lane; s < splits; s += 32)
-        top = fmaxf(top, p.part_lse[s * rows + at]);
+        top = fmaxf(top, p.part_lse[lse_at(s)]);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
     const float ref = top == -INFINITY ? 0.0f : top;
     float acc[G::DV / 32] = {}, sum = 0.0f;
     for (int s = 0; s < splits; ++s) {
-        const float wgt = expf(p.part_lse[s * rows + at] - ref);
+        const float wgt = expf(p.part_lse[lse_at(s)] - ref);
         sum += wgt;
-        const float4 *o = reinterpret_cast<const float4 *>(p.part + (s * rows + at) * G::DV);
 #pragma unroll
         for (int i = 0; i < G::DV / 128; ++i) {
-            const float4 x = o[i * 32 + lane];
+            const float4 x = reinterpret_cast<const float4 *>(p.part + part_at(s, i))[lane];
             acc[i * 4] = fmaf(wgt, x.x, acc[i * 4]);
             acc[i * 4 + 1] = fmaf(wgt, x.y, acc[i * 4 + 1]);
             acc[i * 4 + 2] = fmaf(wgt, x.z, acc[i * 4 + 2]);

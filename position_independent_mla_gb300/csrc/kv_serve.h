@@ -97,6 +97,7 @@ struct Divisor {
 
 // Rows and keys of a sequence are 32-bit numbers in the kernels, with room for a tile past
 // the end.
+constexpr int kRows = 128; // rows of a tile: the M of an MMA
 constexpr int64_t kMaxRows = 0x40000000, kMaxKeys = 0x7FFFFF00;
 
 struct AttnParams {
@@ -123,6 +124,9 @@ struct AttnParams {
     // split of the key axis, and the parts that are joined afterwards
     int32_t split_tiles, max_splits, cluster;
     float *part, *part_lse; // [max_splits][total_q][heads][value width], [..][heads]
+    // a row tile to a sequence; > 0: runs of keys so that the blocks fill this many rounds
+    // of the SMs, or one more (their parts: [blocks][kRows][columns of a block])
+    int32_t by_seq, rounds;
     int64_t wait_limit_ns;
     int64_t skip_block; // test hook: this block issues no MMA (-1: none)
     uint32_t *header;
@@ -149,6 +153,8 @@ struct AttnPlan {
     int32_t split_tiles; // key tiles of a block
     int32_t max_splits;
     bool cluster;        // the splits of a row are a cluster that joins them itself
+    bool by_seq;         // every sequence is one row tile
+    int32_t rounds;      // > 0: the split is made on the device (find_run)
     int64_t blocks;
 };
 
