@@ -1348,10 +1348,10 @@ AttnLayout attn_layout(RowKind kind, const AttnPlan &pl, const kv_attn_desc *a, 
                        int32_t heads, int32_t kv_heads)
 {
     const bool mla = kind == RowKind::Mla;
-    const bool parts = pl.max_splits > 1 && !pl.cluster;
-    const size_t rows = !parts ? 0 : pl.rounds > 0 ? (size_t)pl.blocks * kRows
+    // a block's slice begins and ends inside a unit at most
+    const size_t rows = !pl.joins() ? 0 : pl.slices ? (size_t)2 * pl.blocks * pl.row_tiles * kRows
                                    : (size_t)pl.max_splits * total_q * heads;
-    const int width = pl.rounds > 0 && mla ? 256 : mla ? 512 : 128;
+    const int width = pl.slices && mla ? 256 : mla ? 512 : 128;
     AttnLayout l;
     l.pad = (a->max_kv_len + kExpandBlock - 1) / kExpandBlock * kExpandBlock;
     const int64_t wide = pl.expand ? l.pad * a->num_seqs : 0;
@@ -1482,7 +1482,7 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
         p.max_blocks = (int32_t)(lay.pad / kExpandBlock);
     }
     KV_CUDA(launch_attention(p, kind, pl, stream));
-    t_launches += pl.max_splits > 1 && !pl.cluster ? 2 : 1;
+    t_launches += pl.joins() ? 2 : 1;
     KV_CUDA(mark(t_ev_stop, stream));
     return KV_OK;
 }

@@ -56,7 +56,7 @@ struct HeadGeo {
     static constexpr int NT = NT_, KT = 128;
     static constexpr int QPANELS = 2, OC = 128;    // query panels in shared memory; columns of O
     static constexpr int DV = 128;
-    static constexpr bool RUNS = NT == 1; // keys divided by find_run
+    static constexpr int HALVES = 1, JOIN_BLOCKS = 4, UNIT_COST = NT == 2 ? 4 : 6; // see Slices
     static_assert(NT == 1 || !QUANT, "e4m3 rows are widened before two row tiles read them");
     static constexpr int SOFT_WARPS = 8 * NT, LOAD_WARPS = NT == 2 ? 4 : 8;
     static constexpr int STAGE = 2 * 128 * 128;    // bytes of a K or V tile
@@ -84,7 +84,7 @@ struct MlaGeo {
     static constexpr bool MLA = true, QUANT = QUANT_;
     static constexpr int NT = 1, KT = 64;
     static constexpr int QPANELS = 5, OC = 256;
-    static constexpr bool RUNS = true;
+    static constexpr int HALVES = 2, JOIN_BLOCKS = 8, UNIT_COST = 6;
     static constexpr int DV = 512;
     // e4m3 rows are converted by the load warps: twice as many
     static constexpr int SOFT_WARPS = 8, LOAD_WARPS = QUANT ? 16 : 8;
@@ -124,6 +124,212 @@ struct Smem {
     static constexpr int NBARS = 8 + G::BARS;
     static constexpr int BYTES = BAR + NBARS * 8 + 1024;         // + alignment of the base
 };
+
+// ---------------------------------------------------------------------------
+// Slices of the key tiles
+// ---------------------------------------------------------------------------
+
+// Few row tiles, or a ragged batch of them, leave SMs idle or uneven whatever fixed run of
+// keys a block takes.  So the key tiles of all (sequence, row tile, head) units of a call
+// are counted in a row and cut into equal slices, one to each SM (MLA: one to a pair of
+// SMs, the two halves of the value columns, so that they read the same rows at the same
+// time).  A block works off its slice unit by unit; a unit that a cut goes through is
+// joined from parts.  A unit counts UNIT_COST tiles more than it has, as its queries, first
+// loads and results take that long, unless slices are short.  All row tiles of a sequence count as many key tiles as the one that
+// has most.
+// 32 ragged MLA sequences: 112 us, 124 with runs of equal length in two rounds of blocks.
+constexpr int kMinRun = 4; // fewest tiles of a slice
+
+// What one warp knows of the slices.
+template <class G>
+struct Slices {
+    static constexpr int PER = 5; // sequences of a lane: fewer than 2 * kSms units, two to a sequence
+    static constexpr int64_t COUNT = G::MLA ? kSms / 2 : kSms;
+    int64_t size, total; // of a slice, of the call, in tiles
+    int cost;            // of a unit, besides its tiles
+    // of the sequence that was asked for
+    int seq, q0, n, len, tiles, heads; // tiles: key tiles of a unit
+    int64_t first;                     // its first place in the row of all tiles
+    bool bad;                          // some sequence does not fit what the call stated
+
+    // Finds the sequence of slice tile `pos`, or (ask >= 0) sequence `ask`; a negative pos
+    // is the start of slice -1 - pos.  False where there is none.
+    __device__ __forceinline__ bool find(const AttnParams &p, int lane, int64_t &pos, int ask)
+    {
+        constexpr int ROWS = kRows * G::NT;
+        heads = G::MLA ? 1 : p.kv_heads;
+        int from[PER], to[PER], keys[PER], nv[PER];
+        int64_t units = 0, all[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) { // all loads in flight at once
+            const int s = i * 32 + lane;
+            const bool is = s < p.num_seqs;
+            from[i] = is ? __ldg(p.q_off + s) : 0;
+            to[i] = is ? __ldg(p.q_off + s + 1) : 0;
+            keys[i] = is ? __ldg(p.kv_len + s) : 0;
+        }
+        bool wrong = false;
+        total = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            Work x{};
+            const bool fits = queries_fit(p, from[i], to[i], x.n);
+            x.len = keys[i];
+            const bool held = keys_fit(p, x.len);
+            wrong |= !fits || (x.n > 0 && !held);
+            nv[i] = 0;
+            all[i] = 0;
+            if (x.n > 0 && held) {
+                const int row_tiles = (x.n * p.group + ROWS - 1) / ROWS;
+                x.row0 = (row_tiles - 1) * ROWS;
+                int most = key_tiles<G::KT, G::NT>(p, x);
+                if (p.window > 0 && row_tiles > 1) { // another one's window may lie less even
+                    const int span = p.window + min(x.n, (ROWS - 1) / p.group + 2) - 1;
+                    most = min((x.hi + G::KT - 1) / G::KT,
+                               (min(p.sinks, x.len) + G::KT - 1) / G::KT + (span + G::KT - 2) / G::KT + 1);
+                }
+                nv[i] = max(1, most);
+                all[i] = (int64_t)row_tiles * heads;
+            }
+            units += all[i];
+            total += all[i] * nv[i];
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            units += __shfl_xor_sync(0xFFFFFFFFu, units, d);
+            total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
+        }
+        cost = total >= COUNT * 2 * kMinRun ? G::UNIT_COST : 0;
+        total += units * cost;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            all[i] *= nv[i] + cost;
+        bad = __any_sync(0xFFFFFFFFu, wrong);
+        size = max((int64_t)kMinRun, (total + COUNT - 1) / COUNT);
+        if (pos < 0)
+            pos = (-1 - pos) * size;
+        bool found = false;
+        int64_t before = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (i * 32 >= p.num_seqs)
+                break;
+            int64_t sum = all[i];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+                if (lane >= d)
+                    sum += o;
+            }
+            const int64_t at = before + sum - all[i];
+            const bool here = all[i] > 0 && (ask >= 0 ? i * 32 + lane == ask
+                                                      : pos >= at && pos < at + all[i]);
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, here);
+            if (who) {
+                const int l = __ffs((int)who) - 1;
+                seq = i * 32 + l;
+                q0 = __shfl_sync(0xFFFFFFFFu, from[i], l);
+                n = __shfl_sync(0xFFFFFFFFu, to[i], l) - q0;
+                len = __shfl_sync(0xFFFFFFFFu, keys[i], l);
+                tiles = __shfl_sync(0xFFFFFFFFu, nv[i], l);
+                first = __shfl_sync(0xFFFFFFFFu, at, l);
+                found = true;
+            }
+            before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        }
+        return found;
+    }
+};
+
+// The next piece of this block's slice, from `pos` on (-1 - slice: from its start); false
+// past its end.  w.split is the place of its part: a slice begins and ends inside a unit
+// at most once each.
+template <class G>
+__device__ __forceinline__ bool find_slice(const AttnParams &p, int lane, int64_t &pos, Work &w,
+                                           bool &more, bool &bad)
+{
+    constexpr int HALVES = G::MLA ? 2 : 1;
+    const int slice = (int)blockIdx.x / HALVES, half = (int)blockIdx.x % HALVES;
+    Slices<G> s;
+    const bool found = s.find(p, lane, pos, -1);
+    bad = s.bad;
+    more = false;
+    if (!found)
+        return false;
+    const int64_t end = min(s.total, (slice + 1) * s.size);
+    const int unit = (int)((pos - s.first) / (s.tiles + s.cost));
+    const int64_t start = s.first + (int64_t)unit * (s.tiles + s.cost) + s.cost;
+    pos = max(pos, start); // of the first tile
+    if (pos >= end)
+        return false;
+    const int v = (int)(pos - start), run = (int)min((int64_t)s.tiles - v, end - pos);
+    w.seq = s.seq;
+    w.q0 = s.q0;
+    w.n = s.n;
+    w.len = s.len;
+    w.row0 = unit / s.heads * (kRows * G::NT);
+    w.head = G::MLA ? half : unit % s.heads;
+    w.splits = run < s.tiles ? 2 : 1; // more than one
+    w.split = (2 * slice + (v == 0)) * HALVES + half;
+    const int real = key_tiles<G::KT, G::NT>(p, w);
+    w.beg = min(real, v);
+    w.end = min(real, v + run);
+    pos += run;
+    more = pos + s.cost < end; // a tile more, then
+    return true;
+}
+
+// Joins the units that the ends of slices cut, before the wait for the kernel that writes
+// their parts it finds them.  JOIN_BLOCKS blocks to a slice: they join the unit whose first
+// cut is the slice's start, a warp for a row.
+template <class G>
+__global__ void __launch_bounds__(256) slice_join_kernel(const __grid_constant__ AttnParams p)
+{
+    constexpr int ROWS = kRows * G::NT;
+    __shared__ int s_splits, s_rows, s_row0, s_head, s_q0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int slice = (int)blockIdx.x / G::JOIN_BLOCKS + 1; // the first start is no cut
+    if (warp == 0) {
+        Slices<G> s;
+        int64_t pos = -1 - slice;
+        int splits = 0;
+        if (s.find(p, lane, pos, -1)) {
+            const int unit = (int)((pos - s.first) / (s.tiles + s.cost));
+            const int64_t start = s.first + (int64_t)unit * (s.tiles + s.cost) + s.cost;
+            if (start < pos && start / s.size == slice - 1)
+                splits = (int)((start + s.tiles - 1) / s.size) - slice + 2;
+            const int row0 = unit / s.heads * ROWS;
+            s_rows = min(ROWS, s.n * p.group - row0);
+            s_row0 = row0;
+            s_head = unit % s.heads;
+            s_q0 = s.q0;
+        }
+        s_splits = splits;
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (s_splits <= 1)
+        return;
+    const int rows = s_rows;
+    for (int r = (int)blockIdx.x % G::JOIN_BLOCKS * 8 + warp; r < rows; r += G::JOIN_BLOCKS * 8) {
+        const int row = s_row0 + r, i = p.by_group.quotient(row);
+        const int64_t tok = (int64_t)s_q0 + i;
+        const int h = s_head * p.group + row - i * p.group;
+        // the first part lies in the second place of its slice, the others in the first ones
+        auto at = [&](int k) {
+            return (int64_t)(2 * (slice - 1 + k) + (k == 0)) * G::HALVES * ROWS + r;
+        };
+        join_row<G::DV / 128>(
+            s_splits, lane, p.out + tok * p.o_ts + h * p.o_hs,
+            p.lse ? p.lse + tok * p.heads + h : nullptr,
+            [&](int k, int v) {
+                constexpr int PER = G::OC / 128; // the halves of MLA columns are parts of their own
+                return reinterpret_cast<const float4 *>(
+                    p.part + (at(k) + v / PER * ROWS) * G::OC + v % PER * 128);
+            },
+            [&](int k) { return p.part_lse + at(k); });
+    }
+}
 
 // ---------------------------------------------------------------------------
 // Load roles
@@ -891,15 +1097,14 @@ __device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, 
     if (valid && half == 0 && (!G::MLA || w.head == 0)) {
         const float lse = sum == 0.0f ? -INFINITY : st.top * p.scale + logf(sum);
         if (parts)
-            p.part_lse[G::RUNS && p.rounds ? (int64_t)blockIdx.x * kRows + r
-                                : w.split * p.total_q * p.heads + at] = lse;
+            p.part_lse[(int64_t)w.split * (kRows * G::NT) + t * kRows + r] = lse;
         else if (p.lse)
             p.lse[at] = lse;
     }
     char *out = p.out + (w.q0 + tok) * p.o_ts + h * p.o_hs + col0 * 2;
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0; // a row's sectors are whole
-    float *part = p.part + (G::RUNS && p.rounds ? ((int64_t)blockIdx.x * kRows + r) * G::OC + half * HO
-                                     : (w.split * p.total_q * p.heads + at) * G::DV + col0);
+    float *part =
+        p.part + ((int64_t)w.split * (kRows * G::NT) + t * kRows + r) * G::OC + half * HO;
 #pragma unroll 1
     for (int i = 0; i < HO; i += 32) {
         uint32_t o[32];
@@ -954,6 +1159,29 @@ __device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, 
 // The kernel
 // ---------------------------------------------------------------------------
 
+// All commits of a unit of `tiles` key tiles have arrived: its barriers can be made anew.
+template <class G>
+__device__ __forceinline__ void drain(uint32_t bars, int tiles, volatile int *abort, int64_t limit)
+{
+    auto last = [&](uint32_t bar, int count) {
+        if (count > 0)
+            bar_wait(bar, (count - 1) & 1, abort, limit);
+    };
+    const uint32_t empty = bars + (kBarRing + G::BARS / 2) * 8;
+    if (G::NT == 1)
+        last(bars + kBarO * 8, tiles);
+    if constexpr (G::MLA) {
+        for (int i = 0; i < G::BARS / 2; ++i)
+            last(empty + i * 8, (tiles + 1 - (i & 1)) / 2);
+    } else { // two row tiles do not give the last V back
+        const int items = 2 * tiles - (G::NT == 2 ? 1 : 0);
+        for (int i = 0; i < G::STAGES; ++i)
+            last(empty + i * 8, (items - i + G::STAGES - 1) / G::STAGES);
+    }
+}
+
+// A block works off its slice of the call's key tiles, or its one row tile and split, unit by
+// unit; the roles meet before and after each.
 template <class G>
 __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
     const __grid_constant__ AttnParams p)
@@ -962,138 +1190,179 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
     extern __shared__ unsigned char raw_smem[];
     __shared__ Work s_work;
     __shared__ uint32_t s_tmem, s_status;
-    __shared__ int s_go;
+    __shared__ int s_go, s_more;
     __shared__ volatile int s_abort, s_dirty;
     __shared__ RowPairs<G> s_pairs;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
     const uint32_t q_smem = smem + S::Q, ring = smem + S::RING, bars = smem + S::BAR;
+    auto meet = [] {
+        mma_fence_before();
+        __syncthreads();
+        mma_fence_after();
+    };
 
-    if (warp == 0) {
-        // block -> (row tile, key head or half, split); heads of one row tile and
-        // its halves are neighbours, so their rows meet in L2
-        const int heads = G::MLA ? 2 : p.kv_heads, x = (int)blockIdx.x;
-        Work w{};
-        int at = 0;
-        bool bad = false, go;
-        if (G::RUNS && p.rounds > 0) {
-            go = find_run<G>(p, lane, x, -1, w, at, bad);
-        } else {
-            const int y = p.by_heads.quotient(x), tile = p.by_splits.quotient(y);
-            w.head = x - y * heads;
-            w.split = y - tile * p.max_splits;
-            if (G::NT == 1 && p.by_seq) {
-                w.seq = tile;
-                bad = !seq_queries(p, tile, w.q0, w.n);
-                const bool keys = seq_keys(p, tile, w.len);
-                go = w.n > 0 && keys;
-                bad |= w.n > 0 && !keys;
-            } else {
-                go = find_tile<kRows * G::NT>(p, tile, lane, w, at, bad);
-            }
-            if (go) {
-                w.row0 = at * kRows * G::NT;
-                const int nv = key_tiles<G::KT, G::NT>(p, w);
-                go = take_split(p, nv, w);
-            }
-        }
-        if (lane == 0) {
-            s_work = w;
-            s_go = go;
-            s_status = bad ? kStatusOutOfRange : kStatusOk;
-            s_abort = 0;
-            s_dirty = 0;
-            for (int i = 0; i < 2; ++i) { // the warps that have rows signal the weights
-                const int rows = tile_mask(p, w.n, w.len, w.row0 + (G::NT == 2 ? i : 0) * kRows).rows;
-                bar_init(bars + (kBarP + i) * 8, max(1, (rows + 31) / 32) * 64);
-            }
-            bar_init_fence();
-        }
-    } else if (warp == 1 && lane == 0) {
-        bar_init(bars + kBarQ * 8, G::SOFT_WARPS * 32);
-        bar_init(bars + kBarDone * 8, 1);
-        for (int i = 0; i < 2; ++i) {
-            bar_init(bars + (kBarS + i) * 8, 1);
-            bar_init(bars + (kBarO + i) * 8, 1); // the second: drain
-        }
-        for (int i = 0; i < G::BARS / 2; ++i) {
-            bar_init(bars + (kBarRing + i) * 8, G::LOAD_WARPS * 32);
-            bar_init(bars + (kBarRing + G::BARS / 2 + i) * 8, 1);
-        }
-        bar_init_fence();
-    } else if (warp == kMmaWarp<G>) {
-        tmem_alloc(smem_u32(&s_tmem), 512);
-    }
-    mma_fence_before();
-    __syncthreads();
-    mma_fence_after();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const uint32_t tmem = s_tmem;
-
-    if (!s_go) {
-        // nothing for this block
-    } else if (warp < G::SOFT_WARPS) {
+    if (warp < G::SOFT_WARPS) {
         if constexpr (kShares<G>)
             reg_inc<kSoftRegs>();
-        const Work w = s_work;
-        const int t = warp >> 3, half = (warp >> 2) & 1;
-        const TileMask mask = tile_mask(p, w.n, w.len, w.row0 + t * kRows);
-        const int wl = warp & 3, warps = (mask.rows + 31) / 32;
-        load_queries<G>(p, w, q_smem, t, tid & 255);
-        if constexpr (G::MLA)
-            queries_to_tmem<G>(p, w, tmem, wl, lane, mask.rows, half * 2);
-        copy_commit();
-        copy_wait<0>();
-        async_fence();
-        mma_fence_before();
-        bar_signal(bars + kBarQ * 8);
-        if (wl < warps)
-            run_softmax<G>(p, w, mask, t, tmem, ring, bars, wl, half, lane, warps, &s_abort,
-                           &s_dirty, s_pairs);
+        int64_t pos = -1 - (int64_t)(blockIdx.x / G::HALVES);
+        for (bool again = false;; again = true) {
+            if (warp == 0) {
+                Work w{};
+                bool bad = false, rest = false, go;
+                if (p.slices) {
+                    go = find_slice<G>(p, lane, pos, w, rest, bad);
+                } else {
+                    // block -> (row tile, key head or half); heads of one row tile and its
+                    // halves are neighbours, so their rows meet in L2
+                    const int heads = G::MLA ? 2 : p.kv_heads, x = (int)blockIdx.x;
+                    const int tile = p.by_heads.quotient(x);
+                    int at = 0;
+                    w.head = x - tile * heads;
+                    if (p.by_seq) {
+                        w.seq = tile;
+                        bad = !seq_queries(p, tile, w.q0, w.n);
+                        const bool keys = seq_keys(p, tile, w.len);
+                        go = w.n > 0 && keys;
+                        bad |= w.n > 0 && !keys;
+                    } else {
+                        go = find_tile<kRows * G::NT>(p, tile, lane, w, at, bad);
+                    }
+                    if (go) {
+                        w.row0 = at * kRows * G::NT;
+                        w.end = key_tiles<G::KT, G::NT>(p, w);
+                        w.splits = 1;
+                    }
+                }
+                if (lane == 0) {
+                    s_work = w;
+                    s_go = go;
+                    s_more = rest;
+                    s_dirty = 0;
+                    if (!again) {
+                        s_status = kStatusOk;
+                        s_abort = 0;
+                    }
+                    if (bad)
+                        s_status = kStatusOutOfRange;
+                    for (int i = 0; i < 2; ++i) { // the warps that have rows signal the weights
+                        const int rows =
+                            tile_mask(p, w.n, w.len, w.row0 + (G::NT == 2 ? i : 0) * kRows).rows;
+                        if (again)
+                            bar_drop(bars + (kBarP + i) * 8);
+                        bar_init(bars + (kBarP + i) * 8, max(1, (rows + 31) / 32) * 64);
+                    }
+                    bar_init_fence();
+                }
+            } else if (warp == 1 && lane == 0) {
+                auto init = [&](int bar, int count) {
+                    if (again)
+                        bar_drop(bars + bar * 8);
+                    bar_init(bars + bar * 8, count);
+                };
+                init(kBarQ, G::SOFT_WARPS * 32);
+                init(kBarDone, 1);
+                for (int i = 0; i < 2; ++i) {
+                    init(kBarS + i, 1);
+                    init(kBarO + i, 1); // the second: drain
+                }
+                for (int i = 0; i < G::BARS / 2; ++i) {
+                    init(kBarRing + i, G::LOAD_WARPS * 32);
+                    init(kBarRing + G::BARS / 2 + i, 1);
+                }
+                bar_init_fence();
+            }
+            meet();
+            if (!s_go)
+                break;
+            const bool more = s_more;
+            const Work w = s_work;
+            const uint32_t tmem = s_tmem;
+            const int t = warp >> 3, half = (warp >> 2) & 1;
+            const TileMask mask = tile_mask(p, w.n, w.len, w.row0 + t * kRows);
+            const int wl = warp & 3, warps = (mask.rows + 31) / 32;
+            load_queries<G>(p, w, q_smem, t, tid & 255);
+            if constexpr (G::MLA)
+                queries_to_tmem<G>(p, w, tmem, wl, lane, mask.rows, half * 2);
+            copy_commit();
+            copy_wait<0>();
+            async_fence();
+            mma_fence_before();
+            bar_signal(bars + kBarQ * 8);
+            if (wl < warps)
+                run_softmax<G>(p, w, mask, t, tmem, ring, bars, wl, half, lane, warps, &s_abort,
+                               &s_dirty, s_pairs);
+            __syncwarp();
+            meet();
+            if (!more || s_abort)
+                break;
+        }
     } else if (warp < kMmaWarp<G>) {
         if constexpr (kShares<G>)
             reg_dec<kLoadRegs>();
-        const Work w = s_work;
         const int lw = warp - G::SOFT_WARPS;
-        bool bad = false;
-        if constexpr (G::MLA && G::QUANT)
-            load_mla_e4m3<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
-        else if constexpr (G::MLA)
-            load_mla_bf16<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
-        else if constexpr (G::QUANT)
-            load_heads_e4m3<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
-        else
-            load_heads<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
-        if (bad)
-            s_status = kStatusOutOfRange;
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        for (;;) {
+            meet();
+            if (!s_go)
+                break;
+            const bool more = s_more;
+            const Work w = s_work;
+            bool bad = false;
+            if constexpr (G::MLA && G::QUANT)
+                load_mla_e4m3<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
+            else if constexpr (G::MLA)
+                load_mla_bf16<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
+            else if constexpr (G::QUANT)
+                load_heads_e4m3<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
+            else
+                load_heads<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
+            if (bad)
+                s_status = kStatusOutOfRange;
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+            meet();
+            if (!more || s_abort)
+                break;
+        }
     } else {
         if constexpr (kShares<G>)
             reg_dec<kMmaRegs>();
-    }
-    if (s_go && warp == kMmaWarp<G>) {
-        const Work w = s_work;
-        const uint32_t lead = elect_lane();
-        bool ok = blockIdx.x != p.skip_block &&
-                  bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
-        if (ok) {
-            mma_fence_after();
-            if constexpr (G::NT == 2)
-                ok = run_mma_two<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
-            else
-                ok = run_mma_one<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
+        if (warp == kMmaWarp<G>)
+            tmem_alloc(smem_u32(&s_tmem), 512);
+        for (;;) {
+            meet();
+            if (!s_go)
+                break;
+            const bool more = s_more;
+            if (warp == kMmaWarp<G>) {
+                const Work w = s_work;
+                const uint32_t lead = elect_lane(), tmem = s_tmem;
+                bool ok = blockIdx.x != p.skip_block &&
+                          bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
+                if (ok) {
+                    mma_fence_after();
+                    if constexpr (G::NT == 2)
+                        ok = run_mma_two<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
+                    else
+                        ok = run_mma_one<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
+                }
+                if (!ok) { // let what was issued finish before tensor memory goes
+                    int none = 0;
+                    bar_signal_mma(bars + (kBarO + 1) * 8, lead);
+                    bar_wait(bars + (kBarO + 1) * 8, 0, &none, 1000000000ll);
+                } else if (more) {
+                    drain<G>(bars, w.end - w.beg, &s_abort, p.wait_limit_ns);
+                }
+                __syncwarp();
+            }
+            meet();
+            if (!more || s_abort)
+                break;
         }
-        if (!ok) { // let what was issued finish before tensor memory goes
-            int none = 0;
-            bar_signal_mma(bars + (kBarO + 1) * 8, lead);
-            bar_wait(bars + (kBarO + 1) * 8, 0, &none, 1000000000ll);
-        }
+        if (warp == kMmaWarp<G>)
+            tmem_free(s_tmem, 512);
     }
-    mma_fence_before();
-    __syncthreads();
-    mma_fence_after();
-    if (warp == kMmaWarp<G>)
-        tmem_free(tmem, 512);
     if (tid == 0)
         write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, p.status_words);
 }
@@ -1119,7 +1388,10 @@ cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
     attention_kernel<G><<<(unsigned)blocks, kAttnThreads<G>, bytes, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    return launch_join<G>(p, stream);
+    if (!p.slices)
+        return cudaSuccess;
+    constexpr int cuts = (int)Slices<G>::COUNT - 1;
+    return launch_join(slice_join_kernel<G>, p, cuts * G::JOIN_BLOCKS, stream);
 }
 
 } // namespace
@@ -1151,27 +1423,28 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
         nv = std::min(nv, w);
     }
     nv = std::max<int64_t>(nv, 1);
+    pl.max_splits = 1;
+    pl.blocks = units;
+    if (!few) {
+        // too few units to even out by themselves: equal slices; of rows with more units
+        // a block takes one whole (4096 tokens over 16384, 512 units: no parts to join)
+        pl.slices = units < 2 * kSms && nv > kMinRun;
+        if (pl.slices)
+            pl.blocks = kSms;
+        return pl;
+    }
     // pieces of the key axis: enough blocks for a few on every SM, none shorter
     // than four tiles (a block's start and end cost about as much as two)
-    // (whole rows when there are units for two rounds, and their parts need no joining)
-    const int64_t slots = few ? 2 * kSms : kSms;
-    const int64_t want = units >= 2 * slots && !few
-                             ? nv
-                             : std::max<int64_t>(4, (units * nv + 4 * slots - 1) / (4 * slots));
+    const int64_t slots = 2 * kSms;
+    const int64_t want = std::max<int64_t>(4, (units * nv + 4 * slots - 1) / (4 * slots));
     pl.split_tiles = (int32_t)std::min(nv, want);
-    // one round of few blocks and short rows: up to 8 runs in a cluster
+    // one round of blocks and short rows: up to 8 runs in a cluster
     const int64_t run = (nv + 7) / 8;
-    pl.cluster = few && nv > 1 && run <= 4 && units * ((nv + run - 1) / run) <= slots;
+    pl.cluster = nv > 1 && run <= 4 && units * ((nv + run - 1) / run) <= slots;
     if (pl.cluster)
         pl.split_tiles = (int32_t)run;
     pl.max_splits = (int32_t)((nv + pl.split_tiles - 1) / pl.split_tiles);
     pl.blocks = units * pl.max_splits;
-    // a sequence to a row tile, and they leave SMs idle: the device divides the keys
-    if (pl.by_seq && a.num_seqs <= kBalanceSeqs && units < 2 * slots && nv > kMinRun) {
-        pl.rounds = (int32_t)(units / slots) + 1;
-        pl.blocks = (pl.rounds + 1) * slots;
-        pl.max_splits = (int32_t)nv; // so many and no more
-    }
     return pl;
 }
 
@@ -1180,12 +1453,12 @@ cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cu
     const bool quant = p.cs != nullptr;
     p.cluster = pl.cluster ? 1 : 0;
     p.by_seq = pl.by_seq ? 1 : 0;
-    p.rounds = pl.rounds;
+    p.slices = pl.slices ? 1 : 0;
     p.by_group = Divisor((uint32_t)p.group);
     p.by_block = Divisor((uint32_t)p.block);
     p.by_heads = Divisor(kind == RowKind::Mla ? 2u : (uint32_t)p.kv_heads);
     p.by_splits = Divisor((uint32_t)p.max_splits);
-    p.by_run = Divisor((uint32_t)p.split_tiles);
+    p.by_run = Divisor((uint32_t)std::max(1, p.split_tiles));
     if (kind == RowKind::Mla)
         return quant ? launch<MlaGeo<true>>(p, pl.blocks, stream)
                      : launch<MlaGeo<false>>(p, pl.blocks, stream);

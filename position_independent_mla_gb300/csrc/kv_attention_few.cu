@@ -36,9 +36,8 @@ struct FewGeo {
     static constexpr bool MLA = false, QUANT = QUANT_;
     static constexpr int R = R_;                    // rows: 8 or 16
     static constexpr int N = QUANT ? 2 * R : 16;    // rows of the MMAs
-    static constexpr int NT = 1, KT = 128;
-    static constexpr int DV = 128, OC = 128;
-    static constexpr bool RUNS = false;
+    static constexpr int KT = 128;
+    static constexpr int DV = 128;
     static constexpr int LOAD_WARPS = 4;
     static constexpr int STAGE = (QUANT ? 1 : 2) * 128 * 128, STAGES = QUANT ? 6 : 3;
     static constexpr int RING = STAGES * STAGE;
@@ -568,6 +567,39 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
         write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, p.status_words);
 }
 
+// Joins the parts of rows whose keys were split: a warp per (token, head).
+__global__ void __launch_bounds__(256) few_join_kernel(const __grid_constant__ AttnParams p)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = p.total_q * p.heads;
+    const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t tok = at / p.heads;
+    int splits = 0;
+    if (at < rows) {
+        int a = 0, b = p.num_seqs; // the last sequence that starts at or before the token
+        while (b - a > 1) {
+            const int mid = (a + b) / 2;
+            if (p.q_off[mid] <= tok)
+                a = mid;
+            else
+                b = mid;
+        }
+        Work w{};
+        if (seq_queries(p, a, w.q0, w.n) && seq_keys(p, a, w.len) && w.n > 0 && tok == w.q0)
+            splits = p.by_run.quotient(key_tiles<128, 1>(p, w) + p.split_tiles - 1);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (splits <= 1)
+        return; // the row's block wrote it
+    const int h = (int)(at - tok * p.heads);
+    join_row<1>(
+        splits, lane, p.out + tok * p.o_ts + h * p.o_hs, p.lse ? p.lse + at : nullptr,
+        [&](int k, int) {
+            return reinterpret_cast<const float4 *>(p.part + (k * rows + at) * 128);
+        },
+        [&](int k) { return p.part_lse + k * rows + at; });
+}
+
 template <class G>
 cudaError_t launch_few(AttnParams &p, int64_t blocks, cudaStream_t stream)
 {
@@ -593,7 +625,9 @@ cudaError_t launch_few(AttnParams &p, int64_t blocks, cudaStream_t stream)
     attention_few_kernel<G><<<(unsigned)blocks, kFewThreads, G::BYTES, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    return launch_join<G>(p, stream);
+    return p.max_splits == 1
+               ? cudaSuccess
+               : launch_join(few_join_kernel, p, (p.total_q * p.heads + 7) / 8, stream);
 }
 
 } // namespace

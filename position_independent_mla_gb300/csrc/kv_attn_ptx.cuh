@@ -21,6 +21,11 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 
+__device__ __forceinline__ void bar_drop(uint32_t bar)
+{
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void bar_init_fence()
 {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");

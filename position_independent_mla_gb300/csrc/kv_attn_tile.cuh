@@ -180,103 +180,6 @@ __device__ __forceinline__ bool find_tile(const AttnParams &p, int tile, int lan
     return found && keys;
 }
 
-// Where every sequence is one row tile, the device knows all the work of a call and can
-// divide it evenly: runs of keys as long as it takes for all blocks to fill whole rounds
-// of the SMs, p.rounds or one more, whichever ends earlier when a block costs as much as
-// kBlockCost tiles by itself.  So a long sequence among short ones gets more blocks.
-constexpr int kBalanceSeqs = 160, kMinRun = 4, kBlockCost = 5, kSms = 152;
-
-// The work of block `block`, or (block < 0) the blocks of sequence `seq`: `first` is the
-// first block of the sequence, whose blocks are [split][head].  One warp; false where
-// there is none.  `bad`: some sequence does not fit what the call stated.
-template <class G>
-__device__ __forceinline__ bool find_run(const AttnParams &p, int lane, int block, int seq, Work &w,
-                                         int &first, bool &bad)
-{
-    constexpr int PER = kBalanceSeqs / 32; // sequences of a lane
-    const int heads = G::MLA ? 2 : p.kv_heads;
-    int from[PER], to[PER], len[PER], nv[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) { // all loads in flight at once
-        const int s = i * 32 + lane;
-        const bool is = s < p.num_seqs;
-        from[i] = is ? p.q_off[s] : 0;
-        to[i] = is ? p.q_off[s + 1] : 0;
-        len[i] = is ? p.kv_len[s] : 0;
-    }
-    bool wrong = false;
-    int units = 0;
-    int64_t total = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        Work x{};
-        const bool fits = queries_fit(p, from[i], to[i], x.n);
-        x.len = len[i];
-        const bool keys = keys_fit(p, x.len);
-        wrong |= !fits || (x.n > 0 && !keys);
-        nv[i] = x.n > 0 && keys ? max(1, key_tiles<G::KT, 1>(p, x)) : 0;
-        units += nv[i] > 0;
-        total += nv[i];
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
-    units = (int)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)units) * heads;
-    total *= heads;
-    bad = __any_sync(0xFFFFFFFFu, wrong);
-    const int turn = p.rounds + (lane & 1), room = turn * kSms - units; // at least 1
-    const int mine = (int)min(max((int64_t)kMinRun, (total + room - 1) / room),
-                               (int64_t)kMaxRows);
-    const int other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
-    const int less = lane & 1 ? other : mine, more = lane & 1 ? mine : other;
-    const int run = (int64_t)p.rounds * (less + kBlockCost) <=
-                            (int64_t)(p.rounds + 1) * (more + kBlockCost)
-                        ? less
-                        : more;
-    bool found = false;
-    int before = 0, tiles = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        if (i * 32 >= p.num_seqs)
-            break;
-        const int blocks = (nv[i] + run - 1) / run * heads;
-        int sum = blocks;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-            if (lane >= d)
-                sum += o;
-        }
-        const int at = before + sum - blocks;
-        const bool here = blocks > 0 && (block < 0 ? i * 32 + lane == seq
-                                                   : block >= at && block < at + blocks);
-        const uint32_t who = __ballot_sync(0xFFFFFFFFu, here);
-        if (who) {
-            const int l = __ffs((int)who) - 1;
-            w.seq = i * 32 + l;
-            w.q0 = __shfl_sync(0xFFFFFFFFu, from[i], l);
-            w.n = __shfl_sync(0xFFFFFFFFu, to[i], l) - (int)w.q0;
-            w.len = __shfl_sync(0xFFFFFFFFu, len[i], l);
-            tiles = __shfl_sync(0xFFFFFFFFu, nv[i], l);
-            first = __shfl_sync(0xFFFFFFFFu, at, l);
-            found = true;
-        }
-        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
-    }
-    if (!found)
-        return false;
-    const int rel = max(0, block - first);
-    w.row0 = 0;
-    w.split = p.by_heads.quotient(rel);
-    w.head = rel - w.split * heads;
-    const int real = key_tiles<G::KT, 1>(p, w);
-    w.splits = (tiles + run - 1) / run;
-    const int each = (tiles + w.splits - 1) / w.splits;
-    w.beg = min(real, w.split * each);
-    w.end = min(real, w.beg + each);
-    return true;
-}
-
 __device__ __forceinline__ bool key_seen(const Work &w, int k)
 {
     return k < w.hi && (k >= w.lo || k < w.sk);
@@ -488,83 +391,60 @@ __device__ __forceinline__ void load_heads(const AttnParams &p, const Work &w, u
 // Split rows, launches
 // ---------------------------------------------------------------------------
 
-// Joins the parts of rows whose keys were split: a warp per (token, head).
+// One row's parts into its result, by a warp:
 //   lse = log Σ exp(lse_s),  out = Σ exp(lse_s - lse) out_s
-template <class G>
-__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnParams p)
+// V float4 to a lane; part(s, v) and lse(s) say where they lie.  The first parts are asked
+// for before their weights are known.
+template <int V, class PartAt, class LseAt>
+__device__ __forceinline__ void join_row(int splits, int lane, char *out, float *out_lse,
+                                         PartAt part, LseAt lse)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t rows = p.total_q * p.heads;
-    const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int64_t tok = at / p.heads;
-    const int h = (int)(at - tok * p.heads);
-    int splits = 0, first = 0, row = 0;
-    if (at < rows) {
-        int a = 0, b = p.num_seqs; // the last sequence that starts at or before the token
-        while (b - a > 1) {
-            const int mid = (a + b) / 2;
-            if (p.q_off[mid] <= tok)
-                a = mid;
-            else
-                b = mid;
-        }
-        Work w;
-        if (seq_queries(p, a, w.q0, w.n) && seq_keys(p, a, w.len) && tok >= w.q0 &&
-            tok < w.q0 + w.n) {
-            row = (int)(tok - w.q0) * p.group + h % p.group;
-            bool bad;
-            if (G::RUNS && p.rounds > 0) {
-                if constexpr (G::RUNS)
-                    splits = find_run<G>(p, lane, -1, a, w, first, bad) ? w.splits : 0;
-            } else {
-                w.row0 = row / (kRows * G::NT) * (kRows * G::NT);
-                splits = p.by_run.quotient(key_tiles<G::KT, G::NT>(p, w) + p.split_tiles - 1);
-            }
-        }
-    }
-    // part s of this row: of its lse, and of columns i * 128 ...
-    const int heads = G::MLA ? 2 : p.kv_heads, head = G::MLA ? 0 : h / p.group;
-    auto block_row = [&](int s, int half) {
-        return (int64_t)(first + s * heads + head + half) * kRows + row;
-    };
-    auto lse_at = [&](int s) { return G::RUNS && p.rounds ? block_row(s, 0) : s * rows + at; };
-    auto part_at = [&](int s, int i) {
-        constexpr int PER = G::OC / 128;
-        return G::RUNS && p.rounds ? block_row(s, i / PER) * G::OC + i % PER * 128
-                        : (s * rows + at) * G::DV + i * 128;
-    };
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (splits <= 1)
-        return; // the row's block wrote it
-    float top = -INFINITY;
-    for (int s = lane; s < splits; s += 32)
-        top = fmaxf(top, p.part_lse[lse_at(s)]);
+    constexpr int AHEAD = 2;
+    float4 x[AHEAD][V];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+    for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            x[k][v] = part(k, v)[lane];
+    const float my = lane < splits ? *lse(lane) : -INFINITY;
+    float top = my;
+    for (int k = 32 + lane; k < splits; k += 32)
+        top = fmaxf(top, *lse(k));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     const float ref = top == -INFINITY ? 0.0f : top;
-    float acc[G::DV / 32] = {}, sum = 0.0f;
-    for (int s = 0; s < splits; ++s) {
-        const float wgt = expf(p.part_lse[lse_at(s)] - ref);
+    float acc[V][4] = {}, sum = 0.0f;
+    auto add = [&](int k, const float4 (&y)[V]) {
+        const float wgt = expf((k < 32 ? __shfl_sync(0xFFFFFFFFu, my, k) : *lse(k)) - ref);
         sum += wgt;
 #pragma unroll
-        for (int i = 0; i < G::DV / 128; ++i) {
-            const float4 x = reinterpret_cast<const float4 *>(p.part + part_at(s, i))[lane];
-            acc[i * 4] = fmaf(wgt, x.x, acc[i * 4]);
-            acc[i * 4 + 1] = fmaf(wgt, x.y, acc[i * 4 + 1]);
-            acc[i * 4 + 2] = fmaf(wgt, x.z, acc[i * 4 + 2]);
-            acc[i * 4 + 3] = fmaf(wgt, x.w, acc[i * 4 + 3]);
+        for (int v = 0; v < V; ++v) {
+            acc[v][0] = fmaf(wgt, y[v].x, acc[v][0]);
+            acc[v][1] = fmaf(wgt, y[v].y, acc[v][1]);
+            acc[v][2] = fmaf(wgt, y[v].z, acc[v][2]);
+            acc[v][3] = fmaf(wgt, y[v].w, acc[v][3]);
         }
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+        add(k, x[k]);
+#pragma unroll 2
+    for (int k = AHEAD; k < splits; ++k) {
+        float4 y[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            y[v] = part(k, v)[lane];
+        add(k, y);
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    char *out = p.out + tok * p.o_ts + h * p.o_hs;
 #pragma unroll
-    for (int i = 0; i < G::DV / 128; ++i)
-        *reinterpret_cast<uint2 *>(out + (i * 128 + lane * 4) * 2) =
-            make_uint2(pack_bf16(acc[i * 4] * inv, acc[i * 4 + 1] * inv),
-                       pack_bf16(acc[i * 4 + 2] * inv, acc[i * 4 + 3] * inv));
-    if (lane == 0 && p.lse)
-        p.lse[at] = sum == 0.0f ? -INFINITY : ref + logf(sum);
+    for (int v = 0; v < V; ++v)
+        *reinterpret_cast<uint2 *>(out + (v * 128 + lane * 4) * 2) =
+            make_uint2(pack_bf16(acc[v][0] * inv, acc[v][1] * inv),
+                       pack_bf16(acc[v][2] * inv, acc[v][3] * inv));
+    if (lane == 0 && out_lse)
+        *out_lse = sum == 0.0f ? -INFINITY : ref + logf(sum);
 }
 
 // Tensor map of one part of the pool's rows (`width` columns of bf16 or bytes): boxes
@@ -611,23 +491,21 @@ void set_boxes(AttnParams &p)
         p.box_rows = box;
 }
 
-// Joins split rows; starts while the last blocks run and waits for them on the
-// device.
-template <class G>
-cudaError_t launch_join(const AttnParams &p, cudaStream_t stream)
+// A kernel that joins the parts of the one before: it starts while the last blocks of that
+// one run and waits for them on the device.
+inline cudaError_t launch_join(void (*kernel)(AttnParams), const AttnParams &p, int64_t blocks,
+                               cudaStream_t stream)
 {
-    if (p.max_splits == 1)
-        return cudaSuccess;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((p.total_q * p.heads + 7) / 8));
+    cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<G>, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 // The kernel's limit of dynamic shared memory, raised once on each device.

@@ -98,6 +98,7 @@ struct Divisor {
 // Rows and keys of a sequence are 32-bit numbers in the kernels, with room for a tile past
 // the end.
 constexpr int kRows = 128; // rows of a tile: the M of an MMA
+constexpr int kSms = 152;
 constexpr int64_t kMaxRows = 0x40000000, kMaxKeys = 0x7FFFFF00;
 
 struct AttnParams {
@@ -124,9 +125,9 @@ struct AttnParams {
     // split of the key axis, and the parts that are joined afterwards
     int32_t split_tiles, max_splits, cluster;
     float *part, *part_lse; // [max_splits][total_q][heads][value width], [..][heads]
-    // a row tile to a sequence; > 0: runs of keys so that the blocks fill this many rounds
-    // of the SMs, or one more (their parts: [blocks][kRows][columns of a block])
-    int32_t by_seq, rounds;
+    // every sequence is one row tile; blocks take equal slices of all key tiles of the call
+    // (their parts: [2 * kSms][rows of a block][columns of a block])
+    int32_t by_seq, slices;
     int64_t wait_limit_ns;
     int64_t skip_block; // test hook: this block issues no MMA (-1: none)
     uint32_t *header;
@@ -150,12 +151,14 @@ struct AttnShape {
 struct AttnPlan {
     bool expand;         // e4m3 rows are widened first
     int32_t row_tiles;   // 128-row tiles of a block; 0: the kernel for few rows
-    int32_t split_tiles; // key tiles of a block
+    int32_t split_tiles; // few rows: key tiles of a block
     int32_t max_splits;
     bool cluster;        // the splits of a row are a cluster that joins them itself
     bool by_seq;         // every sequence is one row tile
-    int32_t rounds;      // > 0: the split is made on the device (find_run)
+    bool slices;         // the split is made on the device (Slices)
     int64_t blocks;
+
+    bool joins() const { return slices || (max_splits > 1 && !cluster); }
 };
 
 AttnPlan plan_attention(RowKind kind, const AttnShape &a);
