@@ -110,10 +110,10 @@ constexpr int kMmaWarp = G::SOFT_WARPS + G::LOAD_WARPS;
 template <class G>
 constexpr bool kShares = G::NT == 2;
 
-constexpr int kSoftRegs = 96, kLoadRegs = 56, kMmaRegs = 40;
+constexpr int kSoftRegs = 96, kLoadRegs = 48, kMmaRegs = 48;
 
 template <class G>
-constexpr int kAttnThreads = (kMmaWarp<G> + (kShares<G> ? 4 : 1)) * 32;
+constexpr int kAttnThreads = (kMmaWarp<G> + (kShares<G> ? 4 : 2)) * 32;
 
 template <class G>
 struct Smem {
@@ -122,123 +122,155 @@ struct Smem {
     static constexpr int BAR = RING + G::RING;                   // barriers
     // q, out; then per tile or buffer: S ready, P ready; O steps; then the ring's
     static constexpr int NBARS = 8 + G::BARS;
-    static constexpr int BYTES = BAR + NBARS * 8 + 1024;         // + alignment of the base
+    static constexpr int BYTES = BAR + 2 * NBARS * 8 + 1024;     // + alignment of the base
 };
 
 // ---------------------------------------------------------------------------
 // Slices of the key tiles
 // ---------------------------------------------------------------------------
 
-// Few row tiles, or a ragged batch of them, leave SMs idle or uneven whatever fixed run of
-// keys a block takes.  So the key tiles of all (sequence, row tile, head) units of a call
-// are counted in a row and cut into equal slices, one to each SM (MLA: one to a pair of
-// SMs, the two halves of the value columns, so that they read the same rows at the same
-// time).  A block works off its slice unit by unit; a unit that a cut goes through is
-// joined from parts.  A unit counts UNIT_COST tiles more than it has, as its queries, first
-// loads and results take that long, unless slices are short.  All row tiles of a sequence count as many key tiles as the one that
-// has most.
+// Blocks of one (sequence, row tile, head) unit or one run of its keys leave SMs idle at the
+// end.  So the keys of all units of a call are counted in a row and cut into equal slices,
+// one to each SM (MLA: one to a pair of SMs, the two halves of the value columns, so that
+// they read the same rows at the same time).  A block works off its slice unit by unit; a
+// unit that a cut goes through is joined from parts.  Places are counted in keys times the
+// group: a row tile of a causal sequence is kRows * NT places longer than the one before,
+// which holds for every group.  A unit takes UNIT_COST tiles besides (its queries, first
+// loads and results), unless slices are short.
 // 32 ragged MLA sequences: 112 us, 124 with runs of equal length in two rounds of blocks.
-constexpr int kMinRun = 4; // fewest tiles of a slice
+constexpr int kMinRun = 4;      // fewest tiles of a slice
+constexpr int kSliceSeqs = 160; // most sequences: a block walks over them
 
 // What one warp knows of the slices.
 template <class G>
 struct Slices {
-    static constexpr int PER = 5; // sequences of a lane: fewer than 2 * kSms units, two to a sequence
     static constexpr int64_t COUNT = G::MLA ? kSms / 2 : kSms;
-    int64_t size, total; // of a slice, of the call, in tiles
-    int cost;            // of a unit, besides its tiles
-    // of the sequence that was asked for
-    int seq, q0, n, len, tiles, heads; // tiles: key tiles of a unit
-    int64_t first;                     // its first place in the row of all tiles
-    bool bad;                          // some sequence does not fit what the call stated
+    static constexpr int ROWS = kRows * G::NT;
+    int64_t size, total; // places of a slice, of the call
+    int64_t tile, cost;  // of a key tile, of a unit besides its tiles
+    // of the unit that was asked for
+    int seq, q0, n, len, row_tile, head, tiles;
+    int64_t start, next; // places of its first tile and of the next unit
+    bool bad;      // some sequence does not fit what the call stated
 
-    // Finds the sequence of slice tile `pos`, or (ask >= 0) sequence `ask`; a negative pos
-    // is the start of slice -1 - pos.  False where there is none.
-    __device__ __forceinline__ bool find(const AttnParams &p, int lane, int64_t &pos, int ask)
+    // Finds the unit of place `pos`; a negative one is the start of slice -1 - pos.  False
+    // past the last.
+    __device__ __forceinline__ bool find(const AttnParams &p, int lane, int64_t &pos)
     {
-        constexpr int ROWS = kRows * G::NT;
-        heads = G::MLA ? 1 : p.kv_heads;
-        int from[PER], to[PER], keys[PER], nv[PER];
-        int64_t units = 0, all[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) { // all loads in flight at once
-            const int s = i * 32 + lane;
-            const bool is = s < p.num_seqs;
-            from[i] = is ? __ldg(p.q_off + s) : 0;
-            to[i] = is ? __ldg(p.q_off + s + 1) : 0;
-            keys[i] = is ? __ldg(p.kv_len + s) : 0;
-        }
-        bool wrong = false;
-        total = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            Work x{};
-            const bool fits = queries_fit(p, from[i], to[i], x.n);
-            x.len = keys[i];
-            const bool held = keys_fit(p, x.len);
-            wrong |= !fits || (x.n > 0 && !held);
-            nv[i] = 0;
-            all[i] = 0;
-            if (x.n > 0 && held) {
-                const int row_tiles = (x.n * p.group + ROWS - 1) / ROWS;
-                x.row0 = (row_tiles - 1) * ROWS;
-                int most = key_tiles<G::KT, G::NT>(p, x);
-                if (p.window > 0 && row_tiles > 1) { // another one's window may lie less even
-                    const int span = p.window + min(x.n, (ROWS - 1) / p.group + 2) - 1;
-                    most = min((x.hi + G::KT - 1) / G::KT,
-                               (min(p.sinks, x.len) + G::KT - 1) / G::KT + (span + G::KT - 2) / G::KT + 1);
-                }
-                nv[i] = max(1, most);
-                all[i] = (int64_t)row_tiles * heads;
+        const int heads = G::MLA ? 1 : p.kv_heads;
+        tile = (int64_t)G::KT * p.group;
+        const int64_t grow = p.causal && p.window == 0 ? ROWS : 0;
+        // sequence s: queries and keys, row tiles, places of the first one's unit
+        struct Seq {
+            int from, n, len, many;
+            int64_t first;
+            bool fits;
+        };
+        auto look = [&](int s) {
+            Seq x{0, 0, 0, 0, 0, true};
+            if (s >= p.num_seqs)
+                return x;
+            x.from = __ldg(p.q_off + s);
+            const int to = __ldg(p.q_off + s + 1);
+            x.len = __ldg(p.kv_len + s);
+            x.fits = queries_fit(p, x.from, to, x.n) && (x.n == 0 || keys_fit(p, x.len));
+            if (!x.fits || x.n == 0)
+                return x;
+            x.many = p.by_rows.quotient(x.n * p.group + ROWS - 1);
+            if (grow) {
+                x.first = (int64_t)max(0, x.len - x.n) * p.group + ROWS + p.group - 1;
+            } else if (p.window == 0) {
+                x.first = max(1, x.len) * (int64_t)p.group;
+            } else { // at most
+                const int span = p.window + min(x.n, p.by_group.quotient(ROWS - 1) + 2) - 1;
+                const int most = min((x.len + G::KT - 1) / G::KT,
+                                     (min(p.sinks, x.len) + G::KT - 1) / G::KT +
+                                         (span + G::KT - 2) / G::KT + 1);
+                x.first = max(1, most) * tile;
             }
-            units += all[i];
-            total += all[i] * nv[i];
+            return x;
+        };
+        auto places = [&](const Seq &x) {
+            return heads * (x.many * x.first + grow * (((int64_t)x.many * (x.many - 1)) >> 1));
+        };
+        bool wrong = false;
+        int64_t units = 0;
+        total = 0;
+#pragma unroll 1
+        for (int s = lane; s < p.num_seqs; s += 32) {
+            const Seq x = look(s);
+            wrong |= !x.fits;
+            units += (int64_t)x.many * heads;
+            total += places(x);
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
             units += __shfl_xor_sync(0xFFFFFFFFu, units, d);
             total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
         }
-        cost = total >= COUNT * 2 * kMinRun ? G::UNIT_COST : 0;
-        total += units * cost;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            all[i] *= nv[i] + cost;
         bad = __any_sync(0xFFFFFFFFu, wrong);
-        size = max((int64_t)kMinRun, (total + COUNT - 1) / COUNT);
+        cost = total >= COUNT * 2 * kMinRun * tile ? G::UNIT_COST * tile : 0;
+        total += units * cost;
+        size = max(kMinRun * tile, (total + COUNT - 1) / COUNT);
         if (pos < 0)
             pos = (-1 - pos) * size;
         bool found = false;
-        int64_t before = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if (i * 32 >= p.num_seqs)
-                break;
-            int64_t sum = all[i];
+        int64_t before = 0, base = 0, unit = 0;
+        int count = 0;
+#pragma unroll 1
+        for (int s = 0; s < p.num_seqs && !found; s += 32) {
+            Seq x = look(s + lane);
+            x.first += cost;
+            const int64_t all = places(x);
+            int64_t sum = all;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int64_t o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
                 if (lane >= d)
                     sum += o;
             }
-            const int64_t at = before + sum - all[i];
-            const bool here = all[i] > 0 && (ask >= 0 ? i * 32 + lane == ask
-                                                      : pos >= at && pos < at + all[i]);
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, here);
+            const int64_t at = before + sum - all;
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, pos >= at && pos < at + all);
             if (who) {
                 const int l = __ffs((int)who) - 1;
-                seq = i * 32 + l;
-                q0 = __shfl_sync(0xFFFFFFFFu, from[i], l);
-                n = __shfl_sync(0xFFFFFFFFu, to[i], l) - q0;
-                len = __shfl_sync(0xFFFFFFFFu, keys[i], l);
-                tiles = __shfl_sync(0xFFFFFFFFu, nv[i], l);
-                first = __shfl_sync(0xFFFFFFFFu, at, l);
+                seq = s + l;
+                q0 = __shfl_sync(0xFFFFFFFFu, x.from, l);
+                n = __shfl_sync(0xFFFFFFFFu, x.n, l);
+                len = __shfl_sync(0xFFFFFFFFu, x.len, l);
+                count = __shfl_sync(0xFFFFFFFFu, x.many, l);
+                unit = __shfl_sync(0xFFFFFFFFu, x.first, l);
+                base = __shfl_sync(0xFFFFFFFFu, at, l);
                 found = true;
             }
             before += __shfl_sync(0xFFFFFFFFu, sum, 31);
         }
-        return found;
+        if (!found)
+            return false;
+        // the row tile: the last whose units start at or before pos
+        auto start_of = [&](int t) {
+            return base + heads * (t * unit + grow * (((int64_t)t * (t - 1)) >> 1));
+        };
+        int lo = 0, hi = count;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (start_of(mid) <= pos)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        row_tile = lo;
+        const int64_t places_of_unit = unit + lo * grow;
+        head = 0;
+        while (head + 1 < heads && start_of(lo) + (head + 1) * places_of_unit <= pos)
+            ++head;
+        start = start_of(lo) + head * places_of_unit + cost;
+        next = start - cost + places_of_unit;
+        tiles = (int)((places_of_unit - cost + tile - 1) / tile);
+        return true;
     }
+
+    // slice of the unit's tile v
+    __device__ __forceinline__ int slice_of(int v) const { return (int)((start + v * tile) / size); }
 };
 
 // The next piece of this block's slice, from `pos` on (-1 - slice: from its start); false
@@ -246,37 +278,37 @@ struct Slices {
 // at most once each.
 template <class G>
 __device__ __forceinline__ bool find_slice(const AttnParams &p, int lane, int64_t &pos, Work &w,
-                                           bool &more, bool &bad)
+                                           bool &bad)
 {
-    constexpr int HALVES = G::MLA ? 2 : 1;
-    const int slice = (int)blockIdx.x / HALVES, half = (int)blockIdx.x % HALVES;
+    const int slice = (int)blockIdx.x / G::HALVES, half = (int)blockIdx.x % G::HALVES;
     Slices<G> s;
-    const bool found = s.find(p, lane, pos, -1);
+    while (s.find(p, lane, pos)) {
+        bad = s.bad;
+        const int64_t end = min(s.total, (slice + 1) * s.size);
+        if (pos >= end)
+            return false;
+        // its tiles whose places are this slice's
+        const int v0 = pos <= s.start ? 0 : (int)((pos - s.start + s.tile - 1) / s.tile);
+        const int v1 = end <= s.start ? 0
+                                      : (int)min((int64_t)s.tiles, (end - s.start + s.tile - 1) / s.tile);
+        pos = s.next; // a unit that goes on goes on in the next slice
+        if (v0 >= v1)
+            continue;
+        w.seq = s.seq;
+        w.q0 = s.q0;
+        w.n = s.n;
+        w.len = s.len;
+        w.row0 = s.row_tile * Slices<G>::ROWS;
+        w.head = G::MLA ? half : s.head;
+        w.splits = v0 > 0 || v1 < s.tiles ? 2 : 1; // more than one
+        w.split = (2 * slice + (v0 == 0)) * G::HALVES + half;
+        const int real = key_tiles<G::KT, G::NT>(p, w);
+        w.beg = min(real, v0);
+        w.end = min(real, v1);
+        return true;
+    }
     bad = s.bad;
-    more = false;
-    if (!found)
-        return false;
-    const int64_t end = min(s.total, (slice + 1) * s.size);
-    const int unit = (int)((pos - s.first) / (s.tiles + s.cost));
-    const int64_t start = s.first + (int64_t)unit * (s.tiles + s.cost) + s.cost;
-    pos = max(pos, start); // of the first tile
-    if (pos >= end)
-        return false;
-    const int v = (int)(pos - start), run = (int)min((int64_t)s.tiles - v, end - pos);
-    w.seq = s.seq;
-    w.q0 = s.q0;
-    w.n = s.n;
-    w.len = s.len;
-    w.row0 = unit / s.heads * (kRows * G::NT);
-    w.head = G::MLA ? half : unit % s.heads;
-    w.splits = run < s.tiles ? 2 : 1; // more than one
-    w.split = (2 * slice + (v == 0)) * HALVES + half;
-    const int real = key_tiles<G::KT, G::NT>(p, w);
-    w.beg = min(real, v);
-    w.end = min(real, v + run);
-    pos += run;
-    more = pos + s.cost < end; // a tile more, then
-    return true;
+    return false;
 }
 
 // Joins the units that the ends of slices cut, before the wait for the kernel that writes
@@ -293,15 +325,12 @@ __global__ void __launch_bounds__(256) slice_join_kernel(const __grid_constant__
         Slices<G> s;
         int64_t pos = -1 - slice;
         int splits = 0;
-        if (s.find(p, lane, pos, -1)) {
-            const int unit = (int)((pos - s.first) / (s.tiles + s.cost));
-            const int64_t start = s.first + (int64_t)unit * (s.tiles + s.cost) + s.cost;
-            if (start < pos && start / s.size == slice - 1)
-                splits = (int)((start + s.tiles - 1) / s.size) - slice + 2;
-            const int row0 = unit / s.heads * ROWS;
-            s_rows = min(ROWS, s.n * p.group - row0);
-            s_row0 = row0;
-            s_head = unit % s.heads;
+        if (s.find(p, lane, pos)) {
+            if (s.slice_of(0) == slice - 1)
+                splits = s.slice_of(s.tiles - 1) - slice + 2;
+            s_row0 = s.row_tile * ROWS;
+            s_rows = min(ROWS, s.n * p.group - s.row_tile * ROWS);
+            s_head = s.head;
             s_q0 = s.q0;
         }
         s_splits = splits;
@@ -925,18 +954,18 @@ __device__ __forceinline__ void queries_to_tmem(const AttnParams &p, const Work 
 // `warp` (0..3) owns rows 32 * warp ..., `half` says which keys of a tile are this
 // thread's; `warps` of the four have rows.
 template <class G>
-__device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, const TileMask &m,
+__device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, const TileMask &m,
                                             int t, uint32_t tmem, uint32_t ring, uint32_t bars,
                                             int warp, int half, int lane, int warps,
                                             volatile int *abort, volatile int *dirty,
-                                            RowPairs<G> &pairs)
+                                            RowPairs<G> &pairs, RowState &st)
 {
     constexpr int KT = G::KT, HK = KT / 2, HO = G::OC / 2; // keys, columns of O of a thread
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     const int pair = t * 4 + warp;
     const int r = warp * 32 + lane;
     const int row = w.row0 + t * kRows + r;
-    const int tok = p.by_group.quotient(row), g = row - tok * p.group;
+    const int tok = p.by_group.quotient(row);
     const bool valid = r < m.rows;
     const int pos = w.len - w.n + tok;
     // keys this row sees: [lo, hi) and [0, sk)
@@ -946,7 +975,6 @@ __device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, 
     const bool one_token = G::NT == 1 && m.pos0 == m.pos1;
     const float c = p.scale * 1.4426950408889634f;
     const uint32_t o_col = tmem + G::O_COL(t) + half * HO + lanes;
-    RowState st;
     int done = 0; // tiles of this row tile so far
     bool ok = true;
     for (int v = w.beg; v < w.end; ++v) {
@@ -986,7 +1014,7 @@ __device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, 
         bool grew = (top - st.top) * c > kLazy; // also from -inf
         if (pair_any(pair, grew || !ok)) {
             if (pair_any(pair, !ok))
-                return;
+                return false;
             top = fmaxf(top, pair_swap<G>(pairs, pair, half, t * kRows + r, top));
             grew = (top - st.top) * c > kLazy;
             const float f = grew ? exp2_fast((st.top - top) * c) : 1.0f;
@@ -1086,10 +1114,29 @@ __device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, 
     ok = ok && bar_wait(bars + kBarDone * 8, 0, abort, p.wait_limit_ns);
     mma_fence_after();
     if (pair_any(pair, !ok))
-        return;
+        return false;
     const float other = pair_swap<G>(pairs, pair, half, t * kRows + r, st.sum);
-    const float sum = half == 0 ? st.sum + other : other + st.sum; // the same in both
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    st.sum = half == 0 ? st.sum + other : other + st.sum; // the same in both
+    return true;
+}
+
+// The results of run_softmax's rows, or their parts.
+template <class G>
+__device__ __forceinline__ void store_rows(const AttnParams &p, const Work &w, const TileMask &m,
+                                           int t, uint32_t tmem, int warp, int half, int lane,
+                                           bool dirty, const RowState &st)
+{
+    constexpr int KT = G::KT, HO = G::OC / 2;
+    const int r = warp * 32 + lane;
+    const int row = w.row0 + t * kRows + r;
+    const int tok = p.by_group.quotient(row), g = row - tok * p.group;
+    const bool valid = r < m.rows;
+    const int pos = w.len - w.n + tok;
+    const int hi = !valid ? 0 : p.causal ? min(w.len, pos + 1) : w.len;
+    const int lo = p.window ? max(0, pos - p.window + 1) : 0;
+    const int sk = p.window ? min(p.sinks, hi) : 0;
+    const uint32_t o_col = tmem + G::O_COL(t) + half * HO + ((uint32_t)(warp * 32) << 16);
+    const float sum = st.sum, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int h = G::MLA ? g : w.head * p.group + g;
     const int64_t at = (w.q0 + tok) * p.heads + h;
     const int col0 = (G::MLA ? w.head * 256 : 0) + half * HO;
@@ -1114,7 +1161,7 @@ __device__ __forceinline__ void run_softmax(const AttnParams &p, const Work &w, 
 #pragma unroll
         for (int j = 0; j < 32; ++j)
             o[j] = sum == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[j]) * inv);
-        if (*dirty) {
+        if (dirty) {
             for (int v = w.beg; v < w.end; ++v) {
                 const int k0 = real_tile(w, v) * KT;
                 for (int k = k0; k < k0 + KT; ++k) {
@@ -1180,91 +1227,155 @@ __device__ __forceinline__ void drain(uint32_t bars, int tiles, volatile int *ab
     }
 }
 
-// A block works off its slice of the call's key tiles, or its one row tile and split, unit by
-// unit; the roles meet before and after each.
+// A block works off its slice of the call's key tiles, or its one unit.  The roles meet once
+// a unit, when its MMAs are done; the rows' results are stored after that, while the next
+// unit's rows and queries are on their way.  One warp finds the next unit and sets its
+// barriers up meanwhile (two sets take turns), which takes 6500 clocks.
+// 6000 tokens under a window, 12 tiles a unit: 57000 clocks a unit, 18000 of them before
+// and after its tiles, when blocks of one unit did all that in turn.
 template <class G>
 __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
     const __grid_constant__ AttnParams p)
 {
     using S = Smem<G>;
     extern __shared__ unsigned char raw_smem[];
-    __shared__ Work s_work;
+    __shared__ Work s_work[3]; // of units k % 3: one to store, one to do, one to come
     __shared__ uint32_t s_tmem, s_status;
-    __shared__ int s_go, s_more;
-    __shared__ volatile int s_abort, s_dirty;
+    __shared__ int s_go[2];
+    __shared__ volatile int s_abort, s_dirty[2];
     __shared__ RowPairs<G> s_pairs;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
-    const uint32_t q_smem = smem + S::Q, ring = smem + S::RING, bars = smem + S::BAR;
-    auto meet = [] {
+    const uint32_t q_smem = smem + S::Q, ring = smem + S::RING;
+    auto bars_of = [&](int k) { return smem + S::BAR + (k & 1) * S::NBARS * 8; };
+    // All threads; true where a wait of some ran out in the unit before.
+    auto meet = [&](bool gave_up) {
         mma_fence_before();
-        __syncthreads();
+        const bool any = __syncthreads_or(gave_up) != 0;
         mma_fence_after();
+        return any;
     };
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp < G::SOFT_WARPS) {
         if constexpr (kShares<G>)
             reg_inc<kSoftRegs>();
+        meet(false);
+        const int t = warp >> 3, half = (warp >> 2) & 1, wl = warp & 3;
+        const uint32_t tmem = s_tmem;
+        // Queries of a unit on their way; its MMAs may start when every thread has signalled.
+        // A warp without rows there does so when the results that the MMAs write over are out.
+        auto signal = [&](int k) {
+            mma_fence_before();
+            bar_signal_copies(bars_of(k) + kBarQ * 8);
+        };
+        auto ask = [&](int k) {
+            const Work w = s_work[k % 3];
+            const int rows = tile_mask(p, w.n, w.len, w.row0 + t * kRows).rows;
+            load_queries<G>(p, w, q_smem, t, tid & 255);
+            if constexpr (G::MLA)
+                queries_to_tmem<G>(p, w, tmem, wl, lane, rows, half * 2);
+            if (wl * 32 < rows)
+                signal(k);
+            return wl * 32 < rows;
+        };
+        bool mine = false;
+        if (s_go[0]) {
+            mine = ask(0);
+            if (!mine)
+                signal(0);
+        }
+        for (int k = 0; s_go[k & 1]; ++k) {
+            RowState st;
+            bool store = false;
+            if (mine) {
+                const Work w = s_work[k % 3];
+                const TileMask mask = tile_mask(p, w.n, w.len, w.row0 + t * kRows);
+                store = run_softmax<G>(p, w, mask, t, tmem, ring, bars_of(k), wl, half, lane,
+                                       (mask.rows + 31) / 32, &s_abort, &s_dirty[k & 1], s_pairs, st);
+            }
+            __syncwarp();
+            const bool dirty = s_dirty[k & 1] != 0;
+            const bool stop = meet(s_abort != 0);
+            const bool more = !stop && s_go[(k + 1) & 1];
+            if (more)
+                mine = ask(k + 1);
+            if (store) {
+                const Work w = s_work[k % 3];
+                store_rows<G>(p, w, tile_mask(p, w.n, w.len, w.row0 + t * kRows), t, tmem, wl, half,
+                              lane, dirty, st);
+            }
+            if (more && !mine)
+                signal(k + 1);
+            if (stop)
+                break;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp < kMmaWarp<G>) {
+        if constexpr (kShares<G>)
+            reg_dec<kLoadRegs>();
+        meet(false);
+        const int lw = warp - G::SOFT_WARPS;
+        for (int k = 0; s_go[k & 1]; ++k) {
+            const Work w = s_work[k % 3];
+            const uint32_t bars = bars_of(k) + kBarRing * 8;
+            bool bad = false;
+            if constexpr (G::MLA && G::QUANT)
+                load_mla_e4m3<G>(p, w, ring, bars, lw, lane, &s_abort, bad);
+            else if constexpr (G::MLA)
+                load_mla_bf16<G>(p, w, ring, bars, lw, lane, &s_abort, bad);
+            else if constexpr (G::QUANT)
+                load_heads_e4m3<G>(p, w, ring, bars, lw, lane, &s_abort, bad);
+            else
+                load_heads<G>(p, w, ring, bars, lw, lane, &s_abort, bad);
+            if (bad)
+                s_status = kStatusOutOfRange;
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+            if (meet(s_abort != 0))
+                break;
+        }
+    } else {
+        if constexpr (kShares<G>)
+            reg_dec<kMmaRegs>();
+        const bool finder = warp == kMmaWarp<G> + 1;
         int64_t pos = -1 - (int64_t)(blockIdx.x / G::HALVES);
-        for (bool again = false;; again = true) {
-            if (warp == 0) {
-                Work w{};
-                bool bad = false, rest = false, go;
-                if (p.slices) {
-                    go = find_slice<G>(p, lane, pos, w, rest, bad);
-                } else {
-                    // block -> (row tile, key head or half); heads of one row tile and its
-                    // halves are neighbours, so their rows meet in L2
-                    const int heads = G::MLA ? 2 : p.kv_heads, x = (int)blockIdx.x;
-                    const int tile = p.by_heads.quotient(x);
-                    int at = 0;
-                    w.head = x - tile * heads;
-                    if (p.by_seq) {
-                        w.seq = tile;
-                        bad = !seq_queries(p, tile, w.q0, w.n);
-                        const bool keys = seq_keys(p, tile, w.len);
-                        go = w.n > 0 && keys;
-                        bad |= w.n > 0 && !keys;
-                    } else {
-                        go = find_tile<kRows * G::NT>(p, tile, lane, w, at, bad);
-                    }
-                    if (go) {
-                        w.row0 = at * kRows * G::NT;
-                        w.end = key_tiles<G::KT, G::NT>(p, w);
-                        w.splits = 1;
-                    }
-                }
-                if (lane == 0) {
-                    s_work = w;
-                    s_go = go;
-                    s_more = rest;
-                    s_dirty = 0;
-                    if (!again) {
-                        s_status = kStatusOk;
-                        s_abort = 0;
-                    }
-                    if (bad)
-                        s_status = kStatusOutOfRange;
-                    for (int i = 0; i < 2; ++i) { // the warps that have rows signal the weights
-                        const int rows =
-                            tile_mask(p, w.n, w.len, w.row0 + (G::NT == 2 ? i : 0) * kRows).rows;
-                        if (again)
-                            bar_drop(bars + (kBarP + i) * 8);
-                        bar_init(bars + (kBarP + i) * 8, max(1, (rows + 31) / 32) * 64);
-                    }
-                    bar_init_fence();
-                }
-            } else if (warp == 1 && lane == 0) {
+        auto next = [&](int k) { // the finder: work and barriers of unit k
+            Work w{};
+            bool bad = false, go = false;
+            if (p.slices) {
+                go = find_slice<G>(p, lane, pos, w, bad);
+            } else if (k == 0) {
+                // block -> (row tile, key head or half); heads of one row tile and its halves
+                // are neighbours, so their rows meet in L2
+                const int heads = G::MLA ? 2 : p.kv_heads, tile = p.by_heads.quotient(blockIdx.x);
+                int at = 0;
+                go = find_tile<kRows * G::NT>(p, tile, lane, w, at, bad);
+                w.head = (int)blockIdx.x - tile * heads;
+                w.row0 = at * kRows * G::NT;
+                if (go)
+                    w.end = key_tiles<G::KT, G::NT>(p, w);
+                w.splits = 1;
+            }
+            if (lane == 0) {
+                s_work[k % 3] = w;
+                s_go[k & 1] = go;
+                s_dirty[k & 1] = 0;
+                if (bad)
+                    s_status = kStatusOutOfRange;
                 auto init = [&](int bar, int count) {
-                    if (again)
-                        bar_drop(bars + bar * 8);
-                    bar_init(bars + bar * 8, count);
+                    if (k >= 2)
+                        bar_drop(bars_of(k) + bar * 8);
+                    bar_init(bars_of(k) + bar * 8, count);
                 };
                 init(kBarQ, G::SOFT_WARPS * 32);
                 init(kBarDone, 1);
                 for (int i = 0; i < 2; ++i) {
+                    // the warps that have rows signal the weights
+                    const int rows =
+                        tile_mask(p, w.n, w.len, w.row0 + (G::NT == 2 ? i : 0) * kRows).rows;
                     init(kBarS + i, 1);
+                    init(kBarP + i, max(1, (rows + 31) / 32) * 64);
                     init(kBarO + i, 1); // the second: drain
                 }
                 for (int i = 0; i < G::BARS / 2; ++i) {
@@ -1273,96 +1384,51 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
                 }
                 bar_init_fence();
             }
-            meet();
-            if (!s_go)
-                break;
-            const bool more = s_more;
-            const Work w = s_work;
-            const uint32_t tmem = s_tmem;
-            const int t = warp >> 3, half = (warp >> 2) & 1;
-            const TileMask mask = tile_mask(p, w.n, w.len, w.row0 + t * kRows);
-            const int wl = warp & 3, warps = (mask.rows + 31) / 32;
-            load_queries<G>(p, w, q_smem, t, tid & 255);
-            if constexpr (G::MLA)
-                queries_to_tmem<G>(p, w, tmem, wl, lane, mask.rows, half * 2);
-            copy_commit();
-            copy_wait<0>();
-            async_fence();
-            mma_fence_before();
-            bar_signal(bars + kBarQ * 8);
-            if (wl < warps)
-                run_softmax<G>(p, w, mask, t, tmem, ring, bars, wl, half, lane, warps, &s_abort,
-                               &s_dirty, s_pairs);
             __syncwarp();
-            meet();
-            if (!more || s_abort)
-                break;
-        }
-    } else if (warp < kMmaWarp<G>) {
-        if constexpr (kShares<G>)
-            reg_dec<kLoadRegs>();
-        const int lw = warp - G::SOFT_WARPS;
-        for (;;) {
-            meet();
-            if (!s_go)
-                break;
-            const bool more = s_more;
-            const Work w = s_work;
-            bool bad = false;
-            if constexpr (G::MLA && G::QUANT)
-                load_mla_e4m3<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
-            else if constexpr (G::MLA)
-                load_mla_bf16<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
-            else if constexpr (G::QUANT)
-                load_heads_e4m3<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
-            else
-                load_heads<G>(p, w, ring, bars + kBarRing * 8, lw, lane, &s_abort, bad);
-            if (bad)
-                s_status = kStatusOutOfRange;
-            asm volatile("cp.async.wait_all;" ::: "memory");
+        };
+        if (finder) {
+            if (lane == 0) {
+                s_status = kStatusOk;
+                s_abort = 0;
+            }
             __syncwarp();
-            meet();
-            if (!more || s_abort)
-                break;
-        }
-    } else {
-        if constexpr (kShares<G>)
-            reg_dec<kMmaRegs>();
-        if (warp == kMmaWarp<G>)
+            next(0);
+        } else if (warp == kMmaWarp<G>) {
             tmem_alloc(smem_u32(&s_tmem), 512);
-        for (;;) {
-            meet();
-            if (!s_go)
-                break;
-            const bool more = s_more;
-            if (warp == kMmaWarp<G>) {
-                const Work w = s_work;
-                const uint32_t lead = elect_lane(), tmem = s_tmem;
+        }
+        meet(false);
+        for (int k = 0; s_go[k & 1]; ++k) {
+            if (finder) {
+                next(k + 1);
+            } else if (warp == kMmaWarp<G>) {
+                const Work w = s_work[k % 3];
+                const uint32_t lead = elect_lane(), tmem = s_tmem, bars = bars_of(k);
                 bool ok = blockIdx.x != p.skip_block &&
                           bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
                 if (ok) {
+                    async_fence(); // the queries came by copies of other threads
                     mma_fence_after();
                     if constexpr (G::NT == 2)
                         ok = run_mma_two<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
                     else
                         ok = run_mma_one<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
                 }
-                if (!ok) { // let what was issued finish before tensor memory goes
+                if (ok) {
+                    drain<G>(bars, w.end - w.beg, &s_abort, p.wait_limit_ns);
+                } else { // let what was issued finish before tensor memory goes
                     int none = 0;
                     bar_signal_mma(bars + (kBarO + 1) * 8, lead);
                     bar_wait(bars + (kBarO + 1) * 8, 0, &none, 1000000000ll);
-                } else if (more) {
-                    drain<G>(bars, w.end - w.beg, &s_abort, p.wait_limit_ns);
                 }
                 __syncwarp();
             }
-            meet();
-            if (!more || s_abort)
+            if (meet(s_abort != 0))
                 break;
         }
-        if (warp == kMmaWarp<G>)
-            tmem_free(s_tmem, 512);
     }
+    meet(false); // all results are out
+    if (warp == kMmaWarp<G>)
+        tmem_free(s_tmem, 512);
     if (tid == 0)
         write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, p.status_words);
 }
@@ -1371,7 +1437,7 @@ template <class G>
 cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
 {
     constexpr int bytes = Smem<G>::BYTES;
-    static_assert(bytes + sizeof(RowPairs<G>) + 256 <= 227 * 1024, "shared memory");
+    static_assert(bytes + sizeof(RowPairs<G>) + 3 * sizeof(Work) + 64 <= 227 * 1024, "shared memory");
     if (!G::QUANT) // e4m3 rows are converted on their way
         set_boxes<G>(p);
     cudaError_t e = allow_smem<attention_kernel<G>>(bytes);
@@ -1411,8 +1477,7 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
     pl.row_tiles = few ? 0 : !mla && tiles_share && (!a.quant || pl.expand) ? 2 : 1;
     const int64_t rows = kRows * std::max(1, pl.row_tiles);
     // row tiles over all sequences: at most one partly filled one each
-    pl.by_seq = !few && !tiles_share;
-    const int64_t tiles = few || pl.by_seq ? a.num_seqs : a.total_q * a.group / rows + a.num_seqs;
+    const int64_t tiles = few || !tiles_share ? a.num_seqs : a.total_q * a.group / rows + a.num_seqs;
     const int64_t units = tiles * (mla ? 2 : a.kv_heads);
     // most key tiles of one row tile
     int64_t nv = (a.max_kv_len + kt - 1) / kt;
@@ -1426,9 +1491,7 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
     pl.max_splits = 1;
     pl.blocks = units;
     if (!few) {
-        // too few units to even out by themselves: equal slices; of rows with more units
-        // a block takes one whole (4096 tokens over 16384, 512 units: no parts to join)
-        pl.slices = units < 2 * kSms && nv > kMinRun;
+        pl.slices = a.num_seqs <= kSliceSeqs && nv > kMinRun;
         if (pl.slices)
             pl.blocks = kSms;
         return pl;
@@ -1452,9 +1515,9 @@ cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cu
 {
     const bool quant = p.cs != nullptr;
     p.cluster = pl.cluster ? 1 : 0;
-    p.by_seq = pl.by_seq ? 1 : 0;
     p.slices = pl.slices ? 1 : 0;
     p.by_group = Divisor((uint32_t)p.group);
+    p.by_rows = Divisor((uint32_t)(kRows * std::max(1, pl.row_tiles)));
     p.by_block = Divisor((uint32_t)p.block);
     p.by_heads = Divisor(kind == RowKind::Mla ? 2u : (uint32_t)p.kv_heads);
     p.by_splits = Divisor((uint32_t)p.max_splits);

@@ -125,16 +125,16 @@ struct AttnParams {
     // split of the key axis, and the parts that are joined afterwards
     int32_t split_tiles, max_splits, cluster;
     float *part, *part_lse; // [max_splits][total_q][heads][value width], [..][heads]
-    // every sequence is one row tile; blocks take equal slices of all key tiles of the call
-    // (their parts: [2 * kSms][rows of a block][columns of a block])
-    int32_t by_seq, slices;
+    // blocks take equal slices of all keys of the call (their parts: [2 * kSms][rows of a
+    // block][columns of a block])
+    int32_t slices;
     int64_t wait_limit_ns;
     int64_t skip_block; // test hook: this block issues no MMA (-1: none)
     uint32_t *header;
     uint32_t status_words; // of the call: this kernel's blocks, and those of an expansion
-    // filled in by launch_attention: quotients by group, block, key heads (MLA: halves),
+    // filled in by launch_attention: quotients by group, rows of a row tile, block, key heads (MLA: halves),
     // max_splits and split_tiles
-    Divisor by_group, by_block, by_heads, by_splits, by_run;
+    Divisor by_group, by_rows, by_block, by_heads, by_splits, by_run;
     // bf16 pools, likewise: rows of a box (0: no boxes)
     int32_t box_rows;
     CUtensorMap copy_map, rot_map;
@@ -154,7 +154,6 @@ struct AttnPlan {
     int32_t split_tiles; // few rows: key tiles of a block
     int32_t max_splits;
     bool cluster;        // the splits of a row are a cluster that joins them itself
-    bool by_seq;         // every sequence is one row tile
     bool slices;         // the split is made on the device (Slices)
     int64_t blocks;
 
