@@ -121,7 +121,7 @@ struct Smem {
     static constexpr int RING = G::NT * G::QPANELS * 128 * 128;  // K and V
     static constexpr int BAR = RING + G::RING;                   // barriers
     // q, out; then per tile or buffer: S ready, P ready; O steps; then the ring's
-    static constexpr int NBARS = 8 + G::BARS;
+    static constexpr int NBARS = kBarRing + G::BARS;
     static constexpr int BYTES = BAR + 2 * NBARS * 8 + 1024;     // + alignment of the base
 };
 
@@ -139,6 +139,9 @@ struct Smem {
 // loads and results), unless slices are short.
 // 32 ragged MLA sequences: 112 us, 124 with runs of equal length in two rounds of blocks.
 constexpr int kMinRun = 4;      // fewest tiles of a slice
+// With so many units to an SM blocks of one unit each even out by themselves (two prompts of
+// 6000 tokens under a window, 2900 units: 520 us, 532 in slices of whole units, 541 cut)
+constexpr int kManyUnits = 16;
 constexpr int kSliceSeqs = 160; // most sequences: a block walks over them
 
 // What one warp knows of the slices.
@@ -517,13 +520,15 @@ __device__ __forceinline__ void load_heads_e4m3(const AttnParams &p, const Work 
 // copy 128 bytes of a row.  The warps meet after every run (see load_heads).
 template <class G>
 __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w, uint32_t ring,
-                                              uint32_t bars, int warp, int lane,
+                                              uint32_t bars, int warp, int lane, bool careful,
                                               volatile int *abort, bool &bad)
 {
     constexpr int AHEAD = 3;
     const int base = warp * 8, c = lane & 7, sub = lane >> 3;
     const int32_t *const table = p.block_tables + (int64_t)w.seq * p.max_blocks;
-    auto whole = [&](int v) { return p.box_rows > 0 && tile_whole<G::KT>(w, real_tile(w, v)); };
+    auto whole = [&](int v) { // as in load_heads
+        return p.box_rows > 0 && (!careful || tile_whole<G::KT>(w, real_tile(w, v)));
+    };
     Copies copies;
     bool ok = true;
     int v = w.beg;
@@ -540,16 +545,20 @@ __device__ __forceinline__ void load_mla_bf16(const AttnParams &p, const Work &w
                 const int skip = before ? AHEAD : 0, part = before ? G::PARTS - 1 : warp;
                 const int col = part == 0 ? (1 - w.head) * 256 : w.head * 256 + (part - 1) * 128;
                 const bool mine = lane < per;
+                auto seen = [&](int u) { // this lane's box
+                    return mine && u < last &&
+                           keys_seen(w, real_tile(w, u) * G::KT + lane * p.box_rows, p.box_rows);
+                };
                 auto ask = [&](int u) {
                     const int kt = real_tile(w, u);
-                    return mine && u < last ? __ldg(table + (in == 1 ? kt * per + lane : kt / in)) : 0;
+                    return seen(u) ? __ldg(table + (in == 1 ? kt * per + lane : kt / in)) : 0;
                 };
                 int32_t blk = ask(v + skip);
                 for (int u = v; ok && u < last; ++u) {
                     const int kt = real_tile(w, u + skip);
                     const bool fits = (uint32_t)blk < (uint32_t)p.num_blocks;
                     bad |= !fits;
-                    const int y = fits ? (in == 1 ? 0 : (kt % in) * G::KT) + blk * p.block
+                    const int y = fits && seen(u + skip) ? (in == 1 ? 0 : (kt % in) * G::KT) + blk * p.block
                                        : (int)(p.num_blocks * p.block); // past the pool: zeros
                     blk = ask(u + 1 + skip);
                     const int ord = u - w.beg, stage = ord & 1, phase = ((ord >> 1) & 1) ^ 1;
@@ -953,12 +962,17 @@ __device__ __forceinline__ void queries_to_tmem(const AttnParams &p, const Work 
 
 // `warp` (0..3) owns rows 32 * warp ..., `half` says which keys of a tile are this
 // thread's; `warps` of the four have rows.
+//
+// A weight of 0 does not keep an infinite or NaN value of a key that the row does not see
+// out of the products.  `finite`: O shows none of that; if it does, the unit is done again,
+// `careful`: keys that no row sees are zeros, and such values of others are taken out of V
+// before they are used and given back at the end to the rows that do see them.
 template <class G>
 __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, const TileMask &m,
                                             int t, uint32_t tmem, uint32_t ring, uint32_t bars,
                                             int warp, int half, int lane, int warps,
-                                            volatile int *abort, volatile int *dirty,
-                                            RowPairs<G> &pairs, RowState &st)
+                                            bool careful, volatile int *abort, volatile int *dirty,
+                                            RowPairs<G> &pairs, RowState &st, bool &finite)
 {
     constexpr int KT = G::KT, HK = KT / 2, HO = G::OC / 2; // keys, columns of O of a thread
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
@@ -975,6 +989,7 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
     const bool one_token = G::NT == 1 && m.pos0 == m.pos1;
     const float c = p.scale * 1.4426950408889634f;
     const uint32_t o_col = tmem + G::O_COL(t) + half * HO + lanes;
+    bool partial = false;
     int done = 0; // tiles of this row tile so far
     bool ok = true;
     for (int v = w.beg; v < w.end; ++v) {
@@ -1063,10 +1078,8 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
         asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(f2_add(sum2[0], sum2[1])));
         st.sum += s0 + s1;
         tmem_st_wait();
-        if (!full && !one_token) {
-            // A weight of 0 does not keep an infinite or NaN value out of the
-            // product: take such values out of V here; rows that do see them get
-            // them back at the end.
+        partial |= !full && (!one_token || p.box_rows > 0);
+        if (careful && !full && !one_token) {
             const int ord = v - w.beg;
             uint32_t vbase;
             int pieces;
@@ -1117,6 +1130,21 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
         return false;
     const float other = pair_swap<G>(pairs, pair, half, t * kRows + r, st.sum);
     st.sum = half == 0 ? st.sum + other : other + st.sum; // the same in both
+    finite = true;
+    if (partial && !careful) {
+        float x = 0.0f; // NaN once a value is not finite
+#pragma unroll 1
+        for (int i = 0; i < HO; i += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_col + i, o);
+            tmem_ld_wait();
+            tmem_pin32(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                x = fmaf(__uint_as_float(o[j]), 0.0f, x);
+        }
+        finite = !valid || x == 0.0f;
+    }
     return true;
 }
 
@@ -1287,16 +1315,26 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
         }
         for (int k = 0; s_go[k & 1]; ++k) {
             RowState st;
-            bool store = false;
-            if (mine) {
-                const Work w = s_work[k % 3];
-                const TileMask mask = tile_mask(p, w.n, w.len, w.row0 + t * kRows);
-                store = run_softmax<G>(p, w, mask, t, tmem, ring, bars_of(k), wl, half, lane,
-                                       (mask.rows + 31) / 32, &s_abort, &s_dirty[k & 1], s_pairs, st);
+            bool store = false, stop, dirty;
+            for (bool careful = false;; careful = true) {
+                bool finite = true;
+                st = RowState{};
+                if (mine) {
+                    const Work w = s_work[k % 3];
+                    const TileMask mask = tile_mask(p, w.n, w.len, w.row0 + t * kRows);
+                    store = run_softmax<G>(p, w, mask, t, tmem, ring, bars_of(k), wl, half, lane,
+                                           (mask.rows + 31) / 32, careful, &s_abort, &s_dirty[k & 1],
+                                           s_pairs, st, finite);
+                }
+                __syncwarp();
+                dirty = s_dirty[k & 1] != 0;
+                stop = meet(s_abort != 0);
+                if (!meet(!finite) || stop)
+                    break;
+                meet(false);
+                mma_fence_before();
+                bar_signal(bars_of(k) + kBarQ * 8); // the queries are there
             }
-            __syncwarp();
-            const bool dirty = s_dirty[k & 1] != 0;
-            const bool stop = meet(s_abort != 0);
             const bool more = !stop && s_go[(k + 1) & 1];
             if (more)
                 mine = ask(k + 1);
@@ -1319,20 +1357,27 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
         for (int k = 0; s_go[k & 1]; ++k) {
             const Work w = s_work[k % 3];
             const uint32_t bars = bars_of(k) + kBarRing * 8;
-            bool bad = false;
-            if constexpr (G::MLA && G::QUANT)
-                load_mla_e4m3<G>(p, w, ring, bars, lw, lane, &s_abort, bad);
-            else if constexpr (G::MLA)
-                load_mla_bf16<G>(p, w, ring, bars, lw, lane, &s_abort, bad);
-            else if constexpr (G::QUANT)
-                load_heads_e4m3<G>(p, w, ring, bars, lw, lane, &s_abort, bad);
-            else
-                load_heads<G>(p, w, ring, bars, lw, lane, &s_abort, bad);
-            if (bad)
-                s_status = kStatusOutOfRange;
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncwarp();
-            if (meet(s_abort != 0))
+            bool stop;
+            for (bool careful = false;; careful = true) {
+                bool bad = false;
+                if constexpr (G::MLA && G::QUANT)
+                    load_mla_e4m3<G>(p, w, ring, bars, lw, lane, &s_abort, bad);
+                else if constexpr (G::MLA)
+                    load_mla_bf16<G>(p, w, ring, bars, lw, lane, careful, &s_abort, bad);
+                else if constexpr (G::QUANT)
+                    load_heads_e4m3<G>(p, w, ring, bars, lw, lane, &s_abort, bad);
+                else
+                    load_heads<G>(p, w, ring, bars, lw, lane, careful, &s_abort, bad);
+                if (bad)
+                    s_status = kStatusOutOfRange;
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncwarp();
+                stop = meet(s_abort != 0);
+                if (!meet(false) || stop)
+                    break;
+                meet(false);
+            }
+            if (stop)
                 break;
         }
     } else {
@@ -1340,7 +1385,26 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
             reg_dec<kMmaRegs>();
         const bool finder = warp == kMmaWarp<G> + 1;
         int64_t pos = -1 - (int64_t)(blockIdx.x / G::HALVES);
-        auto next = [&](int k) { // the finder: work and barriers of unit k
+        // the finder: barriers of unit k; `old`: they have been used
+        auto set_up = [&](int k, const Work &w, bool old) {
+            for (int i = lane; i < S::NBARS; i += 32) {
+                int count = 1; // commits
+                if (i == kBarQ)
+                    count = G::SOFT_WARPS * 32;
+                else if (i == kBarP || i == kBarP + 1) // the warps that have rows signal the weights
+                    count = max(1, (tile_mask(p, w.n, w.len,
+                                              w.row0 + (G::NT == 2 ? i - kBarP : 0) * kRows).rows +
+                                    31) / 32) * 64;
+                else if (i >= kBarRing && i < kBarRing + G::BARS / 2)
+                    count = G::LOAD_WARPS * 32;
+                if (old)
+                    bar_drop(bars_of(k) + i * 8);
+                bar_init(bars_of(k) + i * 8, count);
+            }
+            bar_init_fence();
+            __syncwarp();
+        };
+        auto next = [&](int k) { // the finder: work of unit k
             Work w{};
             bool bad = false, go = false;
             if (p.slices) {
@@ -1363,28 +1427,8 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
                 s_dirty[k & 1] = 0;
                 if (bad)
                     s_status = kStatusOutOfRange;
-                auto init = [&](int bar, int count) {
-                    if (k >= 2)
-                        bar_drop(bars_of(k) + bar * 8);
-                    bar_init(bars_of(k) + bar * 8, count);
-                };
-                init(kBarQ, G::SOFT_WARPS * 32);
-                init(kBarDone, 1);
-                for (int i = 0; i < 2; ++i) {
-                    // the warps that have rows signal the weights
-                    const int rows =
-                        tile_mask(p, w.n, w.len, w.row0 + (G::NT == 2 ? i : 0) * kRows).rows;
-                    init(kBarS + i, 1);
-                    init(kBarP + i, max(1, (rows + 31) / 32) * 64);
-                    init(kBarO + i, 1); // the second: drain
-                }
-                for (int i = 0; i < G::BARS / 2; ++i) {
-                    init(kBarRing + i, G::LOAD_WARPS * 32);
-                    init(kBarRing + G::BARS / 2 + i, 1);
-                }
-                bar_init_fence();
             }
-            __syncwarp();
+            set_up(k, w, k >= 2);
         };
         if (finder) {
             if (lane == 0) {
@@ -1398,31 +1442,40 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
         }
         meet(false);
         for (int k = 0; s_go[k & 1]; ++k) {
-            if (finder) {
-                next(k + 1);
-            } else if (warp == kMmaWarp<G>) {
-                const Work w = s_work[k % 3];
-                const uint32_t lead = elect_lane(), tmem = s_tmem, bars = bars_of(k);
-                bool ok = blockIdx.x != p.skip_block &&
-                          bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
-                if (ok) {
-                    async_fence(); // the queries came by copies of other threads
-                    mma_fence_after();
-                    if constexpr (G::NT == 2)
-                        ok = run_mma_two<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
-                    else
-                        ok = run_mma_one<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
+            bool stop;
+            for (bool again = false;; again = true) {
+                if (finder && !again) {
+                    next(k + 1);
+                } else if (warp == kMmaWarp<G>) {
+                    const Work w = s_work[k % 3];
+                    const uint32_t lead = elect_lane(), tmem = s_tmem, bars = bars_of(k);
+                    bool ok = blockIdx.x != p.skip_block &&
+                              bar_wait(bars + kBarQ * 8, 0, &s_abort, p.wait_limit_ns);
+                    if (ok) {
+                        async_fence(); // the queries came by copies of other threads
+                        mma_fence_after();
+                        if constexpr (G::NT == 2)
+                            ok = run_mma_two<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
+                        else
+                            ok = run_mma_one<G>(p, w, tmem, q_smem, ring, bars, lead, &s_abort);
+                    }
+                    if (ok) {
+                        drain<G>(bars, w.end - w.beg, &s_abort, p.wait_limit_ns);
+                    } else { // let what was issued finish before tensor memory goes
+                        int none = 0;
+                        bar_signal_mma(bars + (kBarO + 1) * 8, lead);
+                        bar_wait(bars + (kBarO + 1) * 8, 0, &none, 1000000000ll);
+                    }
+                    __syncwarp();
                 }
-                if (ok) {
-                    drain<G>(bars, w.end - w.beg, &s_abort, p.wait_limit_ns);
-                } else { // let what was issued finish before tensor memory goes
-                    int none = 0;
-                    bar_signal_mma(bars + (kBarO + 1) * 8, lead);
-                    bar_wait(bars + (kBarO + 1) * 8, 0, &none, 1000000000ll);
-                }
-                __syncwarp();
+                stop = meet(s_abort != 0);
+                if (!meet(false) || stop)
+                    break;
+                if (finder)
+                    set_up(k, s_work[k % 3], true);
+                meet(false);
             }
-            if (meet(s_abort != 0))
+            if (stop)
                 break;
         }
     }
@@ -1491,7 +1544,7 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
     pl.max_splits = 1;
     pl.blocks = units;
     if (!few) {
-        pl.slices = a.num_seqs <= kSliceSeqs && nv > kMinRun;
+        pl.slices = a.num_seqs <= kSliceSeqs && nv > kMinRun && units < kManyUnits * kSms;
         if (pl.slices)
             pl.blocks = kSms;
         return pl;

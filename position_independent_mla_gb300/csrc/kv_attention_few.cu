@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
             bar_signal_copies(bars + kBarQ * 8);
         }
         bool out = false;
-        load_heads<G>(p, w, smem, bars + kBarRing * 8, warp - 4, lane, &s_abort, out);
+        load_heads<G>(p, w, smem, bars + kBarRing * 8, warp - 4, lane, true, &s_abort, out);
         if (out)
             s_status = kStatusOutOfRange;
         asm volatile("cp.async.wait_all;" ::: "memory");

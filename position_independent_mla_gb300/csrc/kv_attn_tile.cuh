@@ -219,6 +219,12 @@ __device__ __forceinline__ bool tile_whole(const Work &w, int kt)
     return (k0 >= w.lo && k0 + KT <= w.hi) || k0 + KT <= w.sk;
 }
 
+// Some key of [k, k + n) is seen by some row.
+__device__ __forceinline__ bool keys_seen(const Work &w, int k, int n)
+{
+    return (k < w.hi && k + n > w.lo) || k < w.sk;
+}
+
 // Waits for the boxes that may be in flight when `filled` tiles went into a ring, also
 // when the block gives up early: its shared memory goes after that.
 template <int STAGES>
@@ -280,15 +286,16 @@ __device__ __forceinline__ bool load_any(bool x)
 // Head rows into the ring as they are stored.  Whole tiles are boxes of the
 // tensor maps that one warp asks for (a box is at most a block of the pool), a run
 // of tiles in a loop of few instructions: a tile's boxes have to go out within the
-// time of its MMAs.  Tiles that hold keys nobody sees, and pools whose blocks do
-// not divide a tile, are copied row by row by all warps with zeros in the place of
-// those keys: a lane owns one key row of its warp, 16 lanes copy 256 bytes (8 lanes
-// 128).  The warps meet after every run, so none waits for a stage that is more than
+// time of its MMAs.  Tiles that hold keys nobody sees (`careful`: otherwise they are
+// boxes too, with zeros only for boxes of which nobody sees a key), and pools whose
+// blocks do not divide a tile, are copied row by row by all warps with zeros in the
+// place of those keys: a lane owns one key row of its warp, 16 lanes copy 256 bytes (8
+// lanes 128); that takes 4000 clocks a tile, where its MMAs take 2100.  The warps meet after every run, so none waits for a stage that is more than
 // one phase away, which a parity would not show; a warp whose wait ran out goes on to
 // the next meeting, where they all give up.
 template <class G>
 __device__ __forceinline__ void load_heads(const AttnParams &p, const Work &w, uint32_t ring,
-                                           uint32_t bars, int warp, int lane,
+                                           uint32_t bars, int warp, int lane, bool careful,
                                            volatile int *abort, bool &bad)
 {
     constexpr int WARPS = G::LOAD_WARPS, ROWS = G::KT / WARPS; // rows of a warp: 32 or 16
@@ -296,7 +303,9 @@ __device__ __forceinline__ void load_heads(const AttnParams &p, const Work &w, u
     const int base = warp * ROWS;
     const int c = lane & (PIECES - 1), sub = lane / PIECES;
     const int32_t *const table = p.block_tables + (int64_t)w.seq * p.max_blocks;
-    auto whole = [&](int v) { return p.box_rows > 0 && tile_whole<G::KT>(w, real_tile(w, v)); };
+    auto whole = [&](int v) {
+        return p.box_rows > 0 && (!careful || tile_whole<G::KT>(w, real_tile(w, v)));
+    };
     Copies copies;
     int stage = 0, phase = 1, filled = 0;
     bool ok = true;
@@ -318,16 +327,20 @@ __device__ __forceinline__ void load_heads(const AttnParams &p, const Work &w, u
                 const int per = G::KT / p.box_rows, in = p.block / p.box_rows;
                 const bool mine = lane < per;
                 auto block_of = [&](int kt) { return in == 1 ? kt * per + lane : kt / in; };
+                auto seen = [&](int kt) { // this lane's box
+                    return mine && keys_seen(w, kt * G::KT + lane * p.box_rows, p.box_rows);
+                };
                 int kt = real_tile(w, v);
-                int32_t blk = mine ? __ldg(table + block_of(kt)) : 0;
+                bool see = seen(kt);
+                int32_t blk = see ? __ldg(table + block_of(kt)) : 0;
                 for (int u = v; ok && u < last; ++u) {
                     const int row = (in == 1 ? 0 : (kt % in) * G::KT) + blk * p.block;
                     const bool fits = (uint32_t)blk < (uint32_t)p.num_blocks;
                     bad |= !fits;
-                    const int y = fits ? row : (int)(p.num_blocks * p.block); // else zeros
+                    const int y = see && fits ? row : (int)(p.num_blocks * p.block); // else zeros
                     kt = real_tile(w, u + 1);
-                    if (mine && u + 1 < last)
-                        blk = __ldg(table + block_of(kt));
+                    see = u + 1 < last && seen(kt);
+                    blk = see ? __ldg(table + block_of(kt)) : 0;
 #pragma unroll
                     for (int part = 0; part < 2; ++part) { // K, then V
                         const uint32_t full = bars + stage * 8;

@@ -280,8 +280,9 @@ __global__ void __launch_bounds__(kQuantThreads) quant_kernel(const __grid_const
 }
 
 // The cached rows of a batch that its queries see, as bf16 rows: key k of sequence s
-// goes to row s * p.pad + k.  Rows of a bad block become zeros.  Also writes the block
-// table of those rows.
+// goes to row s * p.pad + k.  Rows of a bad block become zeros, and so do the others of a
+// block of kExpandBlock rows with some that are seen.  Also writes the block table of those
+// rows.
 template <class R>
 __global__ void __launch_bounds__(kQuantThreads) expand_kernel(const __grid_constant__ ExpandParams p)
 {
@@ -303,7 +304,9 @@ __global__ void __launch_bounds__(kQuantThreads) expand_kernel(const __grid_cons
                           (int64_t)len <= (int64_t)p.max_blocks * p.block;
         const int lo = p.window ? len - n - p.window + 1 : 0;
         const bool seen = fits && k < len && (k >= lo || k < p.sinks);
-        if (!__any_sync(0xFFFFFFFFu, seen))
+        const int k0 = k / kExpandBlock * kExpandBlock;
+        const bool block_seen = fits && k0 < len && (k0 + kExpandBlock > lo || k0 < p.sinks);
+        if (!__any_sync(0xFFFFFFFFu, block_seen))
             continue;
         int64_t ps = -1;
         if (seen) {
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(kQuantThreads) expand_kernel(const __grid_cons
             else
                 ps = (int64_t)blk * p.block + (k - b * p.block);
         }
-        move_unit<R, Move::Keep>(p.rows, p.pool, 0, seen ? row : -1, ps, lane);
+        move_unit<R, Move::Keep>(p.rows, p.pool, 0, block_seen ? row : -1, ps, lane);
     }
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0)
