@@ -489,13 +489,12 @@ size_t kv_attention_quant_workspace_size(const kv_quant_pool_desc *pool, const k
  * (strides multiples of 8 elements, bases 16-byte aligned); d_lse (NULL = not
  * wanted) is fp32 [total_q][num_heads].  num_heads is a multiple of rot_heads,
  * at most 128 query heads to a key head and 2^30 (token, head) rows of a sequence
- * to a key head (else KV_ERR_UNSUPPORTED).  A sequence
- * whose lengths on the device pass max_q_len, max_kv_len or its block-table row
- * is skipped, and a block id outside the pool reads as rows of zeros; both set
- * KV_ERR_OUT_OF_RANGE.  One to three kernels: rows of a quantised pool that
+ * to a key head (else KV_ERR_UNSUPPORTED).  A sequence whose lengths on the device
+ * pass max_q_len, max_kv_len or its block-table row is skipped, and a block id
+ * outside the pool reads as rows of zeros; both set KV_ERR_OUT_OF_RANGE.  One to three kernels: rows of a quantised pool that
  * several row tiles share are widened into the workspace first (where that takes
  * at most 2 GiB), and the parts of rows whose keys were split are joined last.
- * The split depends on the arguments alone: equal calls give equal bits. */
+ * The split depends on the call's lengths alone: equal calls give equal bits. */
 kv_status kv_attention(const kv_pool_desc *pool, int32_t layer, const kv_attn_desc *attn,
                        int64_t total_q, int32_t num_heads, const void *d_q, int64_t q_tok_stride,
                        int64_t q_head_stride, void *d_out, int64_t out_tok_stride,
@@ -532,7 +531,8 @@ kv_status kv_attention_quant(const kv_quant_pool_desc *pool, int32_t layer,
 void kv_set_debug_checks(int32_t on);
 
 /* Upper bound, in nanoseconds, of every inter-block wait inside kv_splice and of
- * every wait between the roles of a kv_attention block (default 2e9).  Values <= 0 restore the default.  Process-wide. */
+ * every wait between the roles of a kv_attention block (default 2e9).  Values
+ * <= 0 restore the default.  Process-wide. */
 void kv_set_wait_limit_ns(int64_t limit_ns);
 
 /* Test hook for the failure path of the in-place splices (process-wide; -1,

@@ -122,11 +122,12 @@ struct AttnParams {
     const int32_t *q_off, *kv_len, *block_tables;
     int32_t causal, window, sinks;
     float scale;
-    // split of the key axis, and the parts that are joined afterwards
+    // split of the key axis, and the parts that are joined afterwards: of few rows
+    // [max_splits][total_q][heads][value width], lse [..][heads]
     int32_t split_tiles, max_splits, cluster;
-    float *part, *part_lse; // [max_splits][total_q][heads][value width], [..][heads]
-    // blocks take equal slices of all keys of the call (their parts: [2 * kSms][rows of a
-    // block][columns of a block])
+    float *part, *part_lse;
+    // of others, where blocks take equal slices of all keys of the call: [2 * kSms][rows of
+    // a block][columns of a block]
     int32_t slices;
     int64_t wait_limit_ns;
     int64_t skip_block; // test hook: this block issues no MMA (-1: none)
