@@ -24,7 +24,10 @@
 // Short contexts of few sequences leave most of the SMs idle and are a matter of
 // latency: their runs of keys become the blocks of a cluster, which join their parts
 // through shared memory instead of a second kernel (one token over 577 keys, 32
-// heads over 8: 9 us a call, 11 with the second kernel).
+// heads over 8: 10.2 us a call, 11.4 with the second kernel).
+//
+// 64 ragged sequences over e4m3 rows: 186 us, 6.1 TB/s, 0.90 of the copy bandwidth; 8
+// sequences under a window of 4096, 32 heads of their own, bf16: 98 us, 5.5 TB/s, 0.81.
 #include "kv_attn_tile.cuh"
 
 namespace kvr {
