@@ -246,3 +246,29 @@ def test_more_rows_than_32_bits_count_are_refused():
     b = Batch("gqa", [(1, 64)], 32, seed=24)
     a = kv.attn_desc(*b.attn._tensors, 1 << 29, 64, b.scale)
     assert kv.kv_attention_workspace_size(b.desc, a, 1 << 29, 32) == 0
+
+
+@pytest.mark.parametrize("kind,heads,seqs,quant", [("mla", 16, 170, False), ("gqa4", 28, 170, True),
+                                                   ("mha", 32, 90, False), ("gqa", 32, 170, False)])
+def test_many_sequences(kind, heads, seqs, quant):
+    """More sequences than slices are made for, and many units to an SM."""
+    lens = [((7 * i) % 6, (7 * i) % 6 + (131 * i) % 640) for i in range(seqs)]
+    Batch(kind, lens, heads, quant=quant, seed=25).check()
+
+
+def test_a_long_sequence_among_short_ones():
+    lens = [(1, 40 + i) for i in range(20)] + [(3, 20000)] + [(2, 9)] * 5
+    for kind, heads in (("mla", 128), ("gqa", 32)):
+        Batch(kind, lens, heads, seed=26).check()
+
+
+def test_not_a_number_behind_the_last_token_of_single_queries():
+    b = Batch("mla", [(1, 1000), (1, 65), (2, 700)], 128, seed=27)
+    want, wl = (t.clone() for t in b.run())
+    keep = torch.zeros(b.pool.copy.shape[1], dtype=torch.bool)
+    for s in range(len(b.lens)):
+        keep[b.slots(s)] = True
+    for t in (b.pool.copy, b.pool.rot):
+        t[:, (~keep).cuda()] = math.nan
+    out, lse = b.run()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
