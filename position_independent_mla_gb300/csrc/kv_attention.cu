@@ -1552,7 +1552,20 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
     pl.max_splits = 1;
     pl.blocks = units;
     if (!few) {
-        pl.slices = a.num_seqs <= kSliceSeqs && nv > kMinRun && units < kManyUnits * kSms;
+        // Slices, or a block to a unit: what each takes, in key tiles, if every unit were as
+        // long as the longest may be.  A unit starts and ends in the time of `around` tiles,
+        // a join takes `join`.  1024 tokens over themselves, 32 heads over 8: 23 us with a
+        // block to a unit, 80 in slices; 16 tokens over 1024: 14 and 19, over 2048 both 20,
+        // over 8192: 28 in slices, some 65 otherwise.  A ragged batch has more to gain than
+        // that shows.
+        const int64_t around = mla ? 6 : pl.row_tiles == 2 ? 4 : 9;
+        const int64_t join = mla ? 7 : pl.row_tiles == 2 ? 5 : 12;
+        const int64_t u = mla ? units / 2 : units, at_once = mla ? kSms / 2 : kSms;
+        const int64_t whole = (u + at_once - 1) / at_once * (nv + around);
+        const int64_t cut = std::max<int64_t>(kMinRun, u * nv / at_once) + around +
+                            u * around / at_once + join;
+        pl.slices = a.num_seqs <= kSliceSeqs && units < kManyUnits * kSms &&
+                    (a.num_seqs > 1 ? cut * 10 <= whole * 11 : cut <= whole);
         if (pl.slices)
             pl.blocks = kSms;
         return pl;
