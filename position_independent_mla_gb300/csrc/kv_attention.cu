@@ -1538,7 +1538,11 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
     pl.row_tiles = few ? 0 : !mla && tiles_share && (!a.quant || pl.expand) ? 2 : 1;
     const int64_t rows = kRows * std::max(1, pl.row_tiles);
     // row tiles over all sequences: at most one partly filled one each
-    const int64_t tiles = few || !tiles_share ? a.num_seqs : a.total_q * a.group / rows + a.num_seqs;
+    // (and no sequence has more than its longest chunk would)
+    const int64_t most = (std::min<int64_t>(a.total_q, a.max_q_len) * a.group + rows - 1) / rows;
+    const int64_t tiles = few || !tiles_share
+                              ? a.num_seqs
+                              : std::min(a.total_q * a.group / rows + a.num_seqs, a.num_seqs * most);
     const int64_t units = tiles * (mla ? 2 : a.kv_heads);
     // most key tiles of one row tile
     int64_t nv = (a.max_kv_len + kt - 1) / kt;
