@@ -19,7 +19,9 @@
 // reference to 2^-18 of it).  The parts are rows of their own (16 for up to 8
 // heads, 32 for up to 16).  A key's scale multiplies its scores, its value's scale
 // 2^e its weights: they are 2^(s + e - reference), the references being those of
-// s + e, and the sums take 2^-e of them.
+// s + e.  The sums are of 2^(s - reference) with references of the scores alone, so that
+// they (and lse) do not depend on the values: 2^(s + e) of keys whose scales lie 2^120
+// apart has no place in one fp32 sum.
 //
 // Short contexts of few sequences leave most of the SMs idle and are a matter of
 // latency: their runs of keys become the blocks of a cluster, which join their parts
@@ -74,6 +76,12 @@ __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t &hi, uint3
     lo = l;
 }
 
+// What the softmax warps share: maxima of a tile, and the references (in units of log2) with
+// the factors of their last growth; of the scores, and (e4m3) of the weights.
+struct FewRefs {
+    float top[2][4][kFewRows], ref[2][kFewRows], grow[2][kFewRows];
+};
+
 // Eight values to eight bytes of each part.
 __device__ __forceinline__ void split8(const float *x, uint2 &hi, uint2 &lo)
 {
@@ -101,19 +109,21 @@ __device__ __forceinline__ bool softmax_any(bool x)
 template <class G>
 __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, uint32_t tmem,
                                             uint32_t smem, uint32_t bars, int tid,
-                                            volatile int *abort, float (*red)[kFewRows],
+                                            volatile int *abort, FewRefs &refs,
                                             const float *q_scale)
 {
     constexpr int R = G::R;
+    constexpr int KINDS = G::QUANT ? 2 : 1, WEIGHTS = KINDS - 1; // of references; the weights'
     const int warp = tid >> 5, lane = tid & 31;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     const float c = p.scale * 1.4426950408889634f;
-    float ref[R], sum[R]; // references in units of log2
+    float sum[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        ref[r] = -INFINITY;
+    for (int r = 0; r < R; ++r)
         sum[r] = 0.0f;
-    }
+    if (tid < 2 * kFewRows)
+        refs.ref[tid / kFewRows][tid % kFewRows] = -INFINITY;
+    bar_wait_all(1, 128);
     // e4m3: this thread's key's scales, asked for a tile ahead
     float ks = 1.0f, vs = 1.0f;
     int32_t blk = 0;
@@ -149,15 +159,14 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
 #pragma unroll
         for (int n = 0; n < G::N; n += 16)
             tmem_pin16(raw + n);
-        float x[R], inv = 1.0f;
+        float x[R], e = 0.0f; // scores; exponent of the value's scale
         if constexpr (G::QUANT) {
-            const float e = (float)((int)(__float_as_uint(my_vs) >> 23) - 127);
-            inv = __uint_as_float((254u << 23) - __float_as_uint(my_vs)); // 1 / 2^e
+            e = (float)((int)(__float_as_uint(my_vs) >> 23) - 127);
             const float cks = c * my_ks;
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                x[r] = fmaf(fmaf(__uint_as_float(raw[R + r]), 0.0625f, __uint_as_float(raw[r])),
-                            cks * q_scale[r], e);
+                x[r] = fmaf(__uint_as_float(raw[R + r]), 0.0625f, __uint_as_float(raw[r])) *
+                       (cks * q_scale[r]);
         } else {
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -167,30 +176,38 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             x[r] = see ? x[r] : -INFINITY;
-            grew |= x[r] - ref[r] > kLazyFew;
+            grew |= x[r] - refs.ref[0][r] > kLazyFew;
+            if (G::QUANT)
+                grew |= x[r] + e - refs.ref[WEIGHTS][r] > kLazyFew;
         }
         if (softmax_any(grew || !ok)) {
             if (softmax_any(!ok))
                 return false;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                float m = x[r];
+            for (int k = 0; k < KINDS; ++k)
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1)
-                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-                if (lane == 0)
-                    red[warp][r] = m;
+                for (int r = 0; r < R; ++r) {
+                    float m = k == 0 ? x[r] : x[r] + e;
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1)
+                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+                    if (lane == 0)
+                        refs.top[k][warp][r] = m;
+                }
+            bar_wait_all(1, 128);
+            if (tid < KINDS * R) {
+                const int k = tid / R, r = tid % R;
+                const float(&top)[4][kFewRows] = refs.top[k];
+                const float m = fmaxf(fmaxf(top[0][r], top[1][r]), fmaxf(top[2][r], top[3][r]));
+                const float ref = refs.ref[k][r];
+                const bool up = m - ref > kLazyFew;
+                refs.grow[k][r] = up ? exp2_fast(ref - m) : 1.0f;
+                refs.ref[k][r] = up ? m : ref;
             }
             bar_wait_all(1, 128);
-            float f[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float m = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
-                const bool up = m - ref[r] > kLazyFew;
-                f[r] = up ? exp2_fast(ref[r] - m) : 1.0f;
-                ref[r] = up ? m : ref[r];
-                sum[r] *= f[r];
-            }
+            for (int r = 0; r < R; ++r)
+                sum[r] *= refs.grow[0][r];
             if (ord > 0) { // a lane of Oᵀ is a value column, its columns are the rows
                 ok = bar_wait(bars + kBarO * 8, (ord - 1) & 1, abort, p.wait_limit_ns);
                 if (softmax_any(!ok))
@@ -207,17 +224,24 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
 #pragma unroll
                 for (int n = 0; n < G::N; ++n)
                     if (G::QUANT || n < R)
-                        o[n] = __float_as_uint(__uint_as_float(o[n]) * f[n % R]);
+                        o[n] = __float_as_uint(__uint_as_float(o[n]) * refs.grow[WEIGHTS][n % R]);
 #pragma unroll
                 for (int n = 0; n < G::N; n += 16)
                     tmem_st16(tmem + G::O_COL + n + lanes, o + n);
                 tmem_st_wait();
             }
         }
+        auto against = [&](int k, int r) {
+            const float ref = refs.ref[k][r];
+            return ref == -INFINITY ? 0.0f : ref;
+        };
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            x[r] = exp2_fast(x[r] - (ref[r] == -INFINITY ? 0.0f : ref[r]));
-            sum[r] = G::QUANT ? fmaf(x[r], inv, sum[r]) : sum[r] + x[r];
+            const float s = x[r];
+            x[r] = exp2_fast(s - against(0, r));
+            sum[r] += x[r];
+            if (G::QUANT)
+                x[r] = exp2_fast(s + e - against(WEIGHTS, r));
         }
         const uint32_t buf = smem + G::P_AT + i * G::P_BYTES;
         if constexpr (G::QUANT) {
@@ -257,7 +281,7 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
         for (int d = 16; d > 0; d >>= 1)
             m += __shfl_xor_sync(0xFFFFFFFFu, m, d);
         if (lane == 0)
-            red[warp][r] = m;
+            refs.top[0][warp][r] = m;
     }
     bar_wait_all(1, 128);
     uint32_t o[G::N];
@@ -273,10 +297,12 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
     for (int r = 0; r < R; ++r) {
         if (r >= p.group)
             break;
-        const float l = (red[0][r] + red[1][r]) + (red[2][r] + red[3][r]);
+        const float(&part)[4][kFewRows] = refs.top[0];
+        const float l = (part[0][r] + part[1][r]) + (part[2][r] + part[3][r]);
         float y = __uint_as_float(o[r]);
-        if constexpr (G::QUANT)
-            y = fmaf(__uint_as_float(o[R + r]), 0.0625f, y) * 0.0625f;
+        if constexpr (G::QUANT) // from the references of the weights to those of the scores
+            y = fmaf(__uint_as_float(o[R + r]), 0.0625f, y) * 0.0625f *
+                exp2f(refs.ref[WEIGHTS][r] - refs.ref[0][r]);
         y = l == 0.0f ? 0.0f : y / l;
         const int h = w.head * p.group + r;
         const int64_t at = w.q0 * p.heads + h;
@@ -288,7 +314,7 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
             *reinterpret_cast<uint16_t *>(p.out + w.q0 * p.o_ts + h * p.o_hs + tid * 2) =
                 (uint16_t)pack_bf16(y, y);
         if (tid == 0) {
-            const float lse = l == 0.0f ? -INFINITY : ref[r] * 0.6931471805599453f + logf(l);
+            const float lse = l == 0.0f ? -INFINITY : refs.ref[0][r] * 0.6931471805599453f + logf(l);
             if (p.cluster)
                 sts4(smem + G::R * 512 + r * 4, lse);
             else if (parts)
@@ -461,7 +487,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
     extern __shared__ unsigned char raw_smem[];
     __shared__ uint32_t s_tmem, s_status;
     __shared__ volatile int s_abort;
-    __shared__ float s_red[4][kFewRows], s_qscale[kFewRows];
+    __shared__ FewRefs s_refs;
+    __shared__ float s_qscale[kFewRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
     const uint32_t bars = smem + G::BAR_AT;
@@ -521,7 +548,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
     if (warp < 4) {
         if constexpr (G::QUANT) // the scales of the queries
             bar_wait_all(2, 256);
-        few_softmax<G>(p, w, tmem, smem, bars, tid, &s_abort, s_red, s_qscale);
+        few_softmax<G>(p, w, tmem, smem, bars, tid, &s_abort, s_refs, s_qscale);
     } else if (warp < 8) {
         const int lt = tid - 128;
         if constexpr (G::QUANT) {
