@@ -21,7 +21,10 @@
 // 2^e its weights: they are 2^(s + e - reference), the references being those of
 // s + e.  The sums are of 2^(s - reference) with references of the scores alone, so that
 // they (and lse) do not depend on the values: 2^(s + e) of keys whose scales lie 2^120
-// apart has no place in one fp32 sum.
+// apart has no place in one fp32 sum.  A value row without values other than 0 (and NaN)
+// has the scale 1, which says nothing of its size: it raises no reference of the weights.
+// Rows at that scale are looked at for it, in the shared memory that the MMA reads them
+// from, only when a reference is about to grow.
 //
 // Short contexts of few sequences leave most of the SMs idle and are a matter of
 // latency: their runs of keys become the blocks of a cluster, which join their parts
@@ -106,6 +109,21 @@ __device__ __forceinline__ bool softmax_any(bool x)
     return r != 0;
 }
 
+// An e4m3 row of 128 bytes, swizzled, holds a value that is neither 0 nor NaN.
+__device__ __forceinline__ bool few_has_values(uint32_t row, int key)
+{
+    uint32_t any = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint4 v = lds16(row + ((j ^ (key & 7)) << 4));
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) // 0x7F in the bytes that are NaN
+            any |= x[i] & 0x7F7F7F7Fu & ~((e4m3_nan(x[i]) >> 7) * 0x7Fu);
+    }
+    return any != 0;
+}
+
 template <class G>
 __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, uint32_t tmem,
                                             uint32_t smem, uint32_t bars, int tid,
@@ -181,13 +199,24 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
                 grew |= x[r] + e - refs.ref[WEIGHTS][r] > kLazyFew;
         }
         if (softmax_any(grew || !ok)) {
+            bool sized = see; // the value's scale tells its size
+            if constexpr (G::QUANT) {
+                const bool look = see && my_vs == 1.0f;
+                if (ok && __any_sync(0xFFFFFFFFu, look)) { // V of this tile stays until its weights
+                    const int item = 2 * ord + 1, at = item % G::STAGES;
+                    ok = bar_wait(bars + (kBarRing + at) * 8, (item / G::STAGES) & 1, abort,
+                                  p.wait_limit_ns);
+                    if (ok && look)
+                        sized = few_has_values(smem + at * G::STAGE + tid * 128, tid);
+                }
+            }
             if (softmax_any(!ok))
                 return false;
 #pragma unroll
             for (int k = 0; k < KINDS; ++k)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    float m = k == 0 ? x[r] : x[r] + e;
+                    float m = k == 0 ? x[r] : sized ? x[r] + e : -INFINITY;
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1)
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));

@@ -53,3 +53,42 @@ def test_the_sum_counts_tiny_values_beside_ordinary_ones(kind, heads):
     requantise(b, lambda v, k: v.mul_(size[:, None, None]))
     b.check()
     assert float((b.lse - want).abs().max()) < 2.0 ** -15
+
+
+def dominate(b, v, k, s, key, gap, others=None):
+    """Key `key` of sequence s scores about `gap` (nats) with the first query head of every key
+    head; `others`: what all keys of the sequence hold else (None: as they are)."""
+    slots = b.slots(s).cuda()
+    if others is not None:
+        k[b.layer, slots] = others
+    first = sum(n for n, _ in b.lens[:s])
+    q = b.q[first, :: b.heads // b.h].double()
+    k[b.layer, slots[key]] = q * (gap / b.scale / q.square().sum(-1, keepdim=True))
+
+
+@pytest.mark.parametrize("gap", [3.0, 6.0, 11.0, 25.0])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -6, 2.0 ** -20])
+@pytest.mark.parametrize("kind,heads", [("gqa", 32), ("gqa4", 64), ("mha", 32)])
+def test_a_row_without_values_takes_no_precision_from_others(kind, heads, size, gap):
+    """A value row of zeros (a null key, a blanked slot) is stored with scale 1; its weight adds
+    nothing to the result, however large it is."""
+    b = Batch(kind, [(1, 300), (1, 1000), (1, 129)], heads, quant=True, seed=42)
+
+    def change(v, k):
+        v.mul_(size)
+        for s, key in enumerate((0, 700, 128)):
+            dominate(b, v, k, s, key, gap)
+            v[b.layer, b.slots(s)[key]] = 0.0
+            v[b.layer, b.slots(s)[key], ::2, 5] = -0.0
+    requantise(b, change).check()
+
+
+def test_not_a_number_among_zeros_takes_no_precision_from_others():
+    b = Batch("gqa", [(1, 1000)], 32, quant=True, seed=43)
+
+    def change(v, k):
+        v.mul_(2.0 ** -20)
+        dominate(b, v, k, 0, 500, 11.0)
+        v[b.layer, b.slots(0)[500]] = 0.0
+        v[b.layer, b.slots(0)[500], :, 3] = float("nan")
+    requantise(b, change).check()
