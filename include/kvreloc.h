@@ -460,7 +460,12 @@ kv_status kv_dequantize(const kv_quant_pool_desc *src, int32_t src_layer,
  * c_KV (512 wide).
  * Products of bf16 values are summed in fp32; scores, maxima and sums are
  * fp32; the weights exp(S_k - max) are rounded to bf16 for the second product
- * (the sum in lse uses the unrounded ones), and out once to bf16.
+ * (the sum in lse uses the unrounded ones), and out once to bf16.  Calls of one new
+ * token per sequence (max_q_len 1) over quantised head rows multiply in 8 bits
+ * instead, with each query value and weight in three parts: a query value is exact
+ * down to 2^-29 of its head's largest and held to 2^-37 of that below; a weight
+ * times its value row's scale is rounded to 2^-9 of itself down to 2^-25 of the
+ * largest such product of the query, and held to 2^-34 of that below.
  * ------------------------------------------------------------------- */
 typedef struct {
     int32_t num_seqs;

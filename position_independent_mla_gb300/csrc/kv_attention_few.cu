@@ -13,25 +13,30 @@
 // one's start and end lie under the other's loads.
 //
 // e4m3 rows go into 8-bit MMAs as they are stored; 1400 clocks of HBM a tile
-// leave no time to widen them.  Queries and weights are split instead, x = hi +
-// lo / 16 with both parts e4m3: with 4 bits each that is every bit of a bf16
-// query, and a weight to 2^-8, as good as bf16 (below 2^-10 of the row's
-// reference to 2^-18 of it).  The parts are rows of their own (16 for up to 8
-// heads, 32 for up to 16).  A key's scale multiplies its scores, its value's scale
-// 2^e its weights: they are 2^(s + e - reference), the references being those of
-// s + e.  The sums are of 2^(s - reference) with references of the scores alone, so that
-// they (and lse) do not depend on the values: 2^(s + e) of keys whose scales lie 2^120
-// apart has no place in one fp32 sum.  A value row without values other than 0 (and NaN)
-// has the scale 1, which says nothing of its size: it raises no reference of the weights.
-// Rows at that scale are looked at for it, in the shared memory that the MMA reads them
-// from, only when a reference is about to grow.
+// leave no time to widen them.  Queries and weights are split instead into three e5m2
+// parts of 3 bits each, x = a + b / 8 + c / 64: every bit of a bf16 query down to 2^-29 of
+// its head's largest value (to 2^-37 of it below), and a weight to 2^-9, better than bf16, down
+// to 2^-25 of the row's reference (to 2^-34 of it below).  The exponents' range is what
+// counts: two e4m3 parts have the bits too, but end at 2^-18 of a reference, and the sum
+// of ten thousand weights that small may be a few per cent of the result (64 ragged
+// sequences 187 us with those, 190 with three).  The parts are
+// rows of their own (24 of 32 for up to 8 heads, 48 for up to 16).
+//
+// A key's scale multiplies its scores, its value's scale 2^e its weights: they are
+// 2^(s + e - reference), the references being those of s + e.  The sums are of
+// 2^(s - reference) with references of the scores alone, so that they (and lse) do not
+// depend on the values: 2^(s + e) of keys whose scales lie 2^120 apart has no place in
+// one fp32 sum.  A value row without values other than 0 (and NaN) has the scale 1, which
+// says nothing of its size: it raises no reference of the weights.  Rows at that scale are
+// looked at for it, in the shared memory that the MMA reads them from, only when a
+// reference is about to grow.
 //
 // Short contexts of few sequences leave most of the SMs idle and are a matter of
 // latency: their runs of keys become the blocks of a cluster, which join their parts
 // through shared memory instead of a second kernel (one token over 577 keys, 32
 // heads over 8: 10.2 us a call, 11.4 with the second kernel).
 //
-// 64 ragged sequences over e4m3 rows: 186 us, 6.1 TB/s, 0.90 of the copy bandwidth; 8
+// 64 ragged sequences over e4m3 rows: 190 us, 6.0 TB/s, 0.89 of the copy bandwidth; 8
 // sequences under a window of 4096, 32 heads of their own, bf16: 98 us, 5.5 TB/s, 0.81.
 #include "kv_attn_tile.cuh"
 
@@ -43,40 +48,48 @@ template <bool QUANT_, int R_>
 struct FewGeo {
     static constexpr bool MLA = false, QUANT = QUANT_;
     static constexpr int R = R_;                    // rows: 8 or 16
-    static constexpr int N = QUANT ? 2 * R : 16;    // rows of the MMAs
+    // rows of the MMAs; e4m3: R for each of three parts, to whole 16 (others: 16)
+    static constexpr int N = QUANT ? (3 * R + 15) / 16 * 16 : 16;
     static constexpr int KT = 128;
     static constexpr int DV = 128;
     static constexpr int LOAD_WARPS = 4;
-    static constexpr int STAGE = (QUANT ? 1 : 2) * 128 * 128, STAGES = QUANT ? 6 : 3;
+    static constexpr int STAGE = (QUANT ? 1 : 2) * 128 * 128;
+    static constexpr int STAGES = !QUANT ? 3 : R == 8 ? 6 : 5;
     static constexpr int RING = STAGES * STAGE;
     // a key's weights: N values of 1 or 2 bytes
     static constexpr int Q_BYTES = N * (QUANT ? 128 : 256), P_BYTES = 128 * N * (QUANT ? 1 : 2);
     static constexpr int P_AT = RING, Q_AT = P_AT + 2 * P_BYTES, BAR_AT = Q_AT + Q_BYTES;
     static constexpr int BYTES = BAR_AT + (kBarRing + 2 * STAGES) * 8 + 1024;
     // tensor memory: two S, O
-    static constexpr int O_COL = 2 * N, COLS = 4 * N;
+    static constexpr int O_COL = 2 * N, COLS = N == 48 ? 256 : 4 * N;
 };
 
 constexpr int kFewThreads = 288; // 4 softmax warps, 4 load warps, 1 MMA warp
-constexpr float kLazyFew = 4.0f;   // growth of a reference: e4m3 weights start at 2^4, end at 448
+constexpr float kLazyFew = 4.0f;   // growth of a reference
+constexpr float kWeightUnit = 2048.0f; // of e5m2 weights, which grow to 2^15 then; e5m2 ends at 57344
 
-// Byte of (key, first of 8 rows) of Pᵀ: core matrices of 8 keys x 8 rows (16 bytes
-// a key), the second 8 rows 128 bytes on, the next 8 keys 256 bytes on.
-__device__ __forceinline__ uint32_t few_weight(int key) { return (key >> 3) * 256 + (key & 7) * 16; }
-
-// Two values to e4m3 parts x = hi + lo / 16.
-__device__ __forceinline__ void split_e4m3(float a, float b, uint32_t &hi, uint32_t &lo)
+// Byte of a key's first 16 bytes of Pᵀ: core matrices of 8 keys x 16 bytes, the next 16 bytes
+// of a key 128 on, the next 8 keys behind all rows of these.
+template <class G>
+__device__ __forceinline__ uint32_t few_weight(int key)
 {
-    uint16_t h, l;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
-    uint32_t w;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(w) : "h"(h));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(l)
-        : "f"((b - f.y) * 16.0f), "f"((a - f.x) * 16.0f));
-    hi = h;
-    lo = l;
+    return (key >> 3) * (G::P_BYTES / 16) + (key & 7) * 16;
+}
+
+// Two values to e5m2 parts x = a + b / 8 + c / 64.
+__device__ __forceinline__ void split_e5m2(float x, float y, uint32_t (&part)[3])
+{
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        uint16_t h;
+        uint32_t w;
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(h) : "f"(y), "f"(x));
+        part[i] = h;
+        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(w) : "h"(h));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        x = (x - f.x) * 8.0f;
+        y = (y - f.y) * 8.0f;
+    }
 }
 
 // What the softmax warps share: maxima of a tile, and the references (in units of log2) with
@@ -86,14 +99,48 @@ struct FewRefs {
 };
 
 // Eight values to eight bytes of each part.
-__device__ __forceinline__ void split8(const float *x, uint2 &hi, uint2 &lo)
+__device__ __forceinline__ void split8(const float *x, uint2 (&to)[3])
 {
-    uint32_t h[4], l[4];
+    uint32_t h[4][3];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        split_e4m3(x[2 * i], x[2 * i + 1], h[i], l[i]);
-    hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-    lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+        split_e5m2(x[2 * i], x[2 * i + 1], h[i]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        to[k] = make_uint2(h[0][k] | (h[1][k] << 16), h[2][k] | (h[3][k] << 16));
+}
+
+// This thread's values of the R rows in tensor memory.  16 rows in three parts come in two
+// steps, half of the registers at a time.
+template <class G>
+__device__ __forceinline__ void few_rows(uint32_t at, float (&x)[G::R])
+{
+    constexpr int R = G::R, FIRST = G::N == 48 ? 16 : 0;
+    uint32_t raw[G::N];
+#pragma unroll
+    for (int n = FIRST; n < G::N; n += 16)
+        tmem_ld16(at + n, raw + n);
+    tmem_ld_wait();
+#pragma unroll
+    for (int n = FIRST; n < G::N; n += 16)
+        tmem_pin16(raw + n);
+    if constexpr (!G::QUANT) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            x[r] = __uint_as_float(raw[r]);
+    } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            x[r] = fmaf(__uint_as_float(raw[2 * R + r]), 0.125f, __uint_as_float(raw[R + r]));
+        if (FIRST) {
+            tmem_ld16(at, raw);
+            tmem_ld_wait();
+            tmem_pin16(raw);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            x[r] = fmaf(x[r], 0.125f, __uint_as_float(raw[r]));
+    }
 }
 
 // A vote over the four softmax warps.  Each of them comes to every vote, also
@@ -169,27 +216,14 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
         }
         bool ok = bar_wait(bars + (kBarS + i) * 8, (ord >> 1) & 1, abort, p.wait_limit_ns);
         mma_fence_after();
-        uint32_t raw[G::N];
-#pragma unroll
-        for (int n = 0; n < G::N; n += 16)
-            tmem_ld16(tmem + i * G::N + n + lanes, raw + n);
-        tmem_ld_wait();
-#pragma unroll
-        for (int n = 0; n < G::N; n += 16)
-            tmem_pin16(raw + n);
         float x[R], e = 0.0f; // scores; exponent of the value's scale
-        if constexpr (G::QUANT) {
+        few_rows<G>(tmem + i * G::N + lanes, x);
+        if constexpr (G::QUANT)
             e = (float)((int)(__float_as_uint(my_vs) >> 23) - 127);
-            const float cks = c * my_ks;
+        const float cks = G::QUANT ? c * my_ks : c;
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                x[r] = fmaf(__uint_as_float(raw[R + r]), 0.0625f, __uint_as_float(raw[r])) *
-                       (cks * q_scale[r]);
-        } else {
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                x[r] = __uint_as_float(raw[r]) * c;
-        }
+        for (int r = 0; r < R; ++r)
+            x[r] *= G::QUANT ? cks * q_scale[r] : cks;
         bool grew = false;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -242,21 +276,18 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
                 if (softmax_any(!ok))
                     return false;
                 mma_fence_after();
-                uint32_t o[G::N];
 #pragma unroll
-                for (int n = 0; n < G::N; n += 16)
-                    tmem_ld16(tmem + G::O_COL + n + lanes, o + n);
-                tmem_ld_wait();
+                for (int n = 0; n < G::N; n += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(tmem + G::O_COL + n + lanes, o);
+                    tmem_ld_wait();
+                    tmem_pin16(o);
 #pragma unroll
-                for (int n = 0; n < G::N; n += 16)
-                    tmem_pin16(o + n);
-#pragma unroll
-                for (int n = 0; n < G::N; ++n)
-                    if (G::QUANT || n < R)
-                        o[n] = __float_as_uint(__uint_as_float(o[n]) * refs.grow[WEIGHTS][n % R]);
-#pragma unroll
-                for (int n = 0; n < G::N; n += 16)
-                    tmem_st16(tmem + G::O_COL + n + lanes, o + n);
+                    for (int j = 0; j < 16; ++j)
+                        o[j] = __float_as_uint(__uint_as_float(o[j]) *
+                                               refs.grow[WEIGHTS][(n + j) % R]);
+                    tmem_st16(tmem + G::O_COL + n + lanes, o);
+                }
                 tmem_st_wait();
             }
         }
@@ -274,24 +305,27 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
         }
         const uint32_t buf = smem + G::P_AT + i * G::P_BYTES;
         if constexpr (G::QUANT) {
-            // 16 bytes a key and 16 rows: the high parts, then the low ones
+            // 16 bytes a key and 16 rows of the MMA
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                x[r] *= 16.0f;
-            uint2 hi[R / 8], lo[R / 8];
+                x[r] *= kWeightUnit;
+            uint2 y[G::N / 8] = {}; // rows past the parts are 0
 #pragma unroll
-            for (int r = 0; r < R; r += 8)
-                split8(x + r, hi[r / 8], lo[r / 8]);
-            if constexpr (R == 8) {
-                sts16(buf + tid * 16, make_uint4(hi[0].x, hi[0].y, lo[0].x, lo[0].y));
-            } else {
-                sts16(buf + few_weight(tid), make_uint4(hi[0].x, hi[0].y, hi[1].x, hi[1].y));
-                sts16(buf + few_weight(tid) + 128, make_uint4(lo[0].x, lo[0].y, lo[1].x, lo[1].y));
+            for (int r = 0; r < R; r += 8) {
+                uint2 part[3];
+                split8(x + r, part);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    y[(k * R + r) / 8] = part[k];
             }
+#pragma unroll
+            for (int n = 0; n < G::N / 16; ++n)
+                sts16(buf + few_weight<G>(tid) + n * 128,
+                      make_uint4(y[2 * n].x, y[2 * n].y, y[2 * n + 1].x, y[2 * n + 1].y));
         } else {
 #pragma unroll
             for (int r = 0; r < R; r += 8)
-                sts16(buf + few_weight(tid) + r * 16,
+                sts16(buf + few_weight<G>(tid) + r * 16,
                       make_uint4(pack_bf16(x[r], x[r + 1]), pack_bf16(x[r + 2], x[r + 3]),
                                  pack_bf16(x[r + 4], x[r + 5]), pack_bf16(x[r + 6], x[r + 7])));
         }
@@ -313,14 +347,8 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
             refs.top[0][warp][r] = m;
     }
     bar_wait_all(1, 128);
-    uint32_t o[G::N];
-#pragma unroll
-    for (int n = 0; n < G::N; n += 16)
-        tmem_ld16(tmem + G::O_COL + n + lanes, o + n);
-    tmem_ld_wait();
-#pragma unroll
-    for (int n = 0; n < G::N; n += 16)
-        tmem_pin16(o + n);
+    float o[R];
+    few_rows<G>(tmem + G::O_COL + lanes, o);
     const bool parts = w.splits > 1;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -328,10 +356,9 @@ __device__ __forceinline__ bool few_softmax(const AttnParams &p, const Work &w, 
             break;
         const float(&part)[4][kFewRows] = refs.top[0];
         const float l = (part[0][r] + part[1][r]) + (part[2][r] + part[3][r]);
-        float y = __uint_as_float(o[r]);
+        float y = o[r];
         if constexpr (G::QUANT) // from the references of the weights to those of the scores
-            y = fmaf(__uint_as_float(o[R + r]), 0.0625f, y) * 0.0625f *
-                exp2f(refs.ref[WEIGHTS][r] - refs.ref[0][r]);
+            y *= (1.0f / kWeightUnit) * exp2f(refs.ref[WEIGHTS][r] - refs.ref[0][r]);
         y = l == 0.0f ? 0.0f : y / l;
         const int h = w.head * p.group + r;
         const int64_t at = w.q0 * p.heads + h;
@@ -383,7 +410,7 @@ __device__ __forceinline__ bool few_mma(const AttnParams &p, const Work &w, uint
             if constexpr (G::QUANT) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) // 32 columns of 8 bits
-                    mma_smem_e4m3<G::N, 0>(tmem + i * G::N, k + j * 2, q + j * 2, j > 0, lead,
+                    mma_smem_8bit<G::N, 0>(tmem + i * G::N, k + j * 2, q + j * 2, j > 0, lead,
                                            kOperandHigh);
             } else {
 #pragma unroll
@@ -405,7 +432,7 @@ __device__ __forceinline__ bool few_mma(const AttnParams &p, const Work &w, uint
             if constexpr (G::QUANT) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) // 32 keys
-                    mma_smem_e4m3<G::N, 1>(tmem + G::O_COL, a + j * (4096 >> 4),
+                    mma_smem_8bit<G::N, 1>(tmem + G::O_COL, a + j * (4096 >> 4),
                                            pt + j * (4 * kKeys8 >> 4), ord > 1 || j > 0, lead,
                                            kWeightHigh);
             } else {
@@ -429,14 +456,20 @@ __device__ __forceinline__ bool few_mma(const AttnParams &p, const Work &w, uint
     return true;
 }
 
-// The queries of a block as e4m3 parts, a row's largest value in [128, 256) after a
-// power-of-two scale; rows past the group are 0.  16 threads to a row.
+// The queries of a block as e5m2 parts, a row's largest value in [2^14, 2^15) after a
+// power-of-two scale; rows past the group (and past the parts) are 0.  16 threads to a row.
 template <class G>
-__device__ __forceinline__ void few_queries_e4m3(const AttnParams &p, const Work &w, uint32_t q_smem,
+__device__ __forceinline__ void few_queries_e5m2(const AttnParams &p, const Work &w, uint32_t q_smem,
                                                  int lt, float *q_scale)
 {
+    const int c = lt & 15;
+    auto store = [&](int row, uint2 v) {
+        const uint32_t at = q_smem + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8;
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(v.x), "r"(v.y) : "memory");
+    };
+    if (G::N > 3 * G::R)
+        store(3 * G::R + (lt >> 4), make_uint2(0, 0));
     for (int r = lt >> 4; r < G::R; r += 8) {
-        const int c = lt & 15;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (r < p.group)
             v = __ldg(reinterpret_cast<const uint4 *>(
@@ -451,8 +484,8 @@ __device__ __forceinline__ void few_queries_e4m3(const AttnParams &p, const Work
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1)
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        // 2^e of the row's scale: the exponent of its largest value, less 7
-        const int e = min(max((int)(m >> 7) - 134, -120), 120);
+        // 2^e of the row's scale: the exponent of its largest value, less 14
+        const int e = max((int)(m >> 7) - 141, -120);
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
         float x[8];
 #pragma unroll
@@ -462,13 +495,12 @@ __device__ __forceinline__ void few_queries_e4m3(const AttnParams &p, const Work
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) // what was infinite is NaN
-            x[i] = fabsf(x[i]) < 256.0f ? x[i] : __uint_as_float(0x7FC00000u);
-        uint2 hi, lo;
-        split8(x, hi, lo);
-        const uint32_t at = q_smem + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi.x), "r"(hi.y) : "memory");
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + G::R * 128), "r"(lo.x), "r"(lo.y)
-                     : "memory");
+            x[i] = fabsf(x[i]) < 32768.0f ? x[i] : __uint_as_float(0x7FC00000u);
+        uint2 part[3];
+        split8(x, part);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            store(k * G::R + r, part[k]);
         if (c == 0)
             q_scale[r] = __uint_as_float((uint32_t)(127 + e) << 23);
     }
@@ -581,7 +613,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attention_few_kernel(
     } else if (warp < 8) {
         const int lt = tid - 128;
         if constexpr (G::QUANT) {
-            few_queries_e4m3<G>(p, w, smem + G::Q_AT, lt, s_qscale);
+            few_queries_e5m2<G>(p, w, smem + G::Q_AT, lt, s_qscale);
             bar_arrive(2, 256);
             async_fence();
             bar_signal(bars + kBarQ * 8);

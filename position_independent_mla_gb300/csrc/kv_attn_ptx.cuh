@@ -305,12 +305,12 @@ __device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uin
                  : "memory");
 }
 
-// kind::f8f6f4: D fp32, A and B e4m3.
+// kind::f8f6f4: D fp32, A e4m3, B e5m2.
 template <int N, int MAJOR>
-__device__ __forceinline__ void mma_smem_e4m3(uint32_t d, uint32_t a, uint32_t b, uint32_t acc,
+__device__ __forceinline__ void mma_smem_8bit(uint32_t d, uint32_t a, uint32_t b, uint32_t acc,
                                               uint32_t lead, uint32_t b_high)
 {
-    constexpr uint32_t desc = (1u << 4) | ((uint32_t)MAJOR << 15) | ((uint32_t)MAJOR << 16) |
+    constexpr uint32_t desc = (1u << 4) | (1u << 10) | ((uint32_t)MAJOR << 15) | ((uint32_t)MAJOR << 16) |
                               ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
     asm volatile("{\n.reg .pred p, q;\n.reg .b64 x, y;\nsetp.ne.b32 p, %4, 0;\n"
                  "setp.ne.b32 q, %6, 0;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %7};\n"

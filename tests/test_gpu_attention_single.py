@@ -92,3 +92,47 @@ def test_not_a_number_among_zeros_takes_no_precision_from_others():
         v[b.layer, b.slots(0)[500]] = 0.0
         v[b.layer, b.slots(0)[500], :, 3] = float("nan")
     requantise(b, change).check()
+
+
+@pytest.mark.parametrize("gap", [8.0, 13.0, 16.0])
+@pytest.mark.parametrize("kind,heads,n", [("gqa", 32, 16000), ("gqa4", 64, 16000),
+                                          ("mha", 32, 4000)])
+def test_many_small_weights_beside_a_large_one(kind, heads, n, gap):
+    """Thousands of equal keys far below one: each weight is small, not their sum."""
+    b = Batch(kind, [(1, n), (1, 200)], heads, quant=True, seed=44)
+
+    def change(v, k):
+        v.abs_()
+        dominate(b, v, k, 0, n // 3, gap, others=0.0)
+    requantise(b, change).check()
+
+
+@pytest.mark.parametrize("kind,heads", [("gqa", 32), ("gqa4", 64)])
+def test_values_of_far_apart_sizes(kind, heads):
+    """Rows 2^-20 to 2^-12 of another's size, and a large row that is zero in half of its columns:
+    there the small ones are all of the result.  A weight times its value's scale is held to
+    2^-34 of the largest such product, a value is at most 448 scales."""
+    b = Batch(kind, [(1, 700), (1, 3000)], heads, quant=True, seed=45)
+    g = torch.Generator().manual_seed(5)
+    size = torch.exp2(torch.randint(-20, -11, b.pool.copy.shape[1:2], generator=g).double()).cuda()
+
+    def change(v, k):
+        v.mul_(size[:, None, None])
+        for s, key in enumerate((200, 1111)):
+            dominate(b, v, k, s, key, 2.0)
+            v[b.layer, b.slots(s)[key]] = 2.0
+            v[b.layer, b.slots(s)[key], :, ::2] = 0.0
+    requantise(b, change).check()
+
+
+@pytest.mark.parametrize("kind,heads", [("gqa", 32), ("gqa4", 64)])
+def test_queries_with_a_channel_that_stands_out(kind, heads):
+    """A query value 2^18 times the others, where the keys are zero: the others decide."""
+    b = Batch(kind, [(1, 700), (1, 3000)], heads, quant=True, seed=46)
+
+    def change(v, k):
+        k[..., 0] = 0.0
+    requantise(b, change)
+    b.q[..., 0] = 2.0 ** 18
+    b.q[::2, ..., 0] = -2.0 ** 18
+    b.check()
