@@ -867,7 +867,8 @@ __device__ __forceinline__ bool run_mma_one(const AttnParams &p, const Work &w, 
                                        ring + vstage * G::STAGE, ord == 1, lead);
                 bar_signal_mma(full + (G::STAGES + vstage) * 8, lead);
             }
-            bar_signal_mma(bars + kBarO * 8, lead);
+            if (more) // the last one is kBarDone's
+                bar_signal_mma(bars + kBarO * 8, lead);
         }
         if constexpr (!G::MLA) {
             if (more) {
@@ -1243,6 +1244,10 @@ __device__ __forceinline__ void store_rows(const AttnParams &p, const Work &w, c
 // ---------------------------------------------------------------------------
 
 // All commits of a unit of `tiles` key tiles have arrived: its barriers can be made anew.
+// A parity shows the last phase of a barrier when the one before is known to be over.  It is
+// for the stages (their copies waited for it) and for O: what came before the scores of the
+// last tile, whose weights were waited for, leaves one commit of O, that of the tile before
+// the last.
 template <class G>
 __device__ __forceinline__ void drain(uint32_t bars, int tiles, volatile int *abort, int64_t limit)
 {
@@ -1252,7 +1257,7 @@ __device__ __forceinline__ void drain(uint32_t bars, int tiles, volatile int *ab
     };
     const uint32_t empty = bars + (kBarRing + G::BARS / 2) * 8;
     if (G::NT == 1)
-        last(bars + kBarO * 8, tiles);
+        last(bars + kBarO * 8, tiles - 1);
     if constexpr (G::MLA) {
         for (int i = 0; i < G::BARS / 2; ++i)
             last(empty + i * 8, (tiles + 1 - (i & 1)) / 2);
