@@ -482,7 +482,13 @@ typedef struct {
 } kv_attn_desc;
 
 /* Bytes of workspace a kv_attention / kv_attention_quant call needs (256-byte
- * aligned), 0 for invalid arguments. */
+ * aligned), 0 for invalid arguments.  The size follows from how the call is divided,
+ * which depends on num_seqs, max_q_len, max_kv_len, window, sinks, total_q and
+ * num_heads, and it does not only grow with them: a batch that fills the GPU with
+ * whole rows needs little, a smaller one whose keys are split needs room for their
+ * parts, and a batch whose widened rows pass 2 GiB does without them.  A workspace
+ * that serves several calls has to be as large as the largest of their sizes; a
+ * smaller one is refused with KV_ERR_WORKSPACE. */
 size_t kv_attention_workspace_size(const kv_pool_desc *pool, const kv_attn_desc *attn,
                                    int64_t total_q, int32_t num_heads);
 size_t kv_attention_quant_workspace_size(const kv_quant_pool_desc *pool, const kv_attn_desc *attn,

@@ -480,7 +480,8 @@ def kv_attention_workspace_size(pool, attn: kv_attn_desc, total_q: int, num_head
 
 
 def attn_workspace(pool, attn: kv_attn_desc, q: torch.Tensor) -> torch.Tensor:
-    """A device workspace for kv_attention of queries like ``q``."""
+    """A device workspace for kv_attention of queries like ``q`` with ``attn``.  A smaller call may
+    need more than a larger one: for several, take the largest kv_attention_workspace_size."""
     n = kv_attention_workspace_size(pool, attn, q.shape[0], q.shape[1])
     if n == 0:
         raise KVError(KV_ERR_INVALID_ARG, "kv_attention_workspace_size")
