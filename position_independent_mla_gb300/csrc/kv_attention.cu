@@ -6,7 +6,9 @@
 // for one layer of a paged pool, with one pass over the keys: for a tile of
 // keys the running maximum m and sum l of every query row are updated, the
 // weights 2^((s - m) * scale * log2 e) are rounded to bf16 and multiplied with
-// V onto the accumulator O, which is rescaled when m moves.
+// V onto the accumulator O, which is rescaled when m moves.  bf16 because an MMA takes
+// both operands in one type and V is bf16; it is 2^-8 of each weight, as much as the
+// rounding of out, and l sums the unrounded ones.
 //
 // Rows.  The query heads that share a key head are packed with the tokens:
 // row r of a (sequence, key head) is token r / group, head r % group, and a
@@ -144,12 +146,16 @@ struct Smem {
 // group: a row tile of a causal sequence is kRows * NT places longer than the one before,
 // which holds for every group.  A unit takes UNIT_COST tiles besides (its queries, first
 // loads and results), unless slices are short.
-// 32 ragged MLA sequences: 112 us, 124 with runs of equal length in two rounds of blocks.
+// 32 ragged MLA sequences: 126 us a call, 139 with runs of equal length in two rounds of
+// blocks (123 now, with the next unit found and loaded meanwhile).
 constexpr int kMinRun = 4;      // fewest tiles of a slice
 // With so many units to an SM blocks of one unit each even out by themselves (two prompts of
 // 6000 tokens under a window, 2900 units: 520 us, 532 in slices of whole units, 541 cut)
 constexpr int kManyUnits = 16;
-constexpr int kSliceSeqs = 160; // most sequences: a block walks over them
+// Most sequences: a block walks over them.  Beyond that no unit is cut, and a long context
+// among many short ones is one block's work: 160 MLA sequences of 1000 tokens and one of
+// them of 65536 take 117 us, 161 take 1144.
+constexpr int kSliceSeqs = 160;
 
 // What one warp knows of the slices.
 template <class G>

@@ -6,7 +6,7 @@
 // so a thread has one key and all rows: R exponentials a tile instead of 128, and
 // its key's mask is one comparison.  The rows' maxima are references that all
 // threads hold; a vote finds a score that passes its reference by more than
-// 2^8, and only then are the true maxima formed across the block and O rescaled.
+// 2^4, and only then are the true maxima formed across the block and O rescaled.
 // Sums stay per key until the end.  An MMA with N = 16 takes 40 clocks (the
 // operand A is read at 128 bytes a clock), 640 a tile, where the tile's rows take
 // 2700 from HBM: the kernel is bound by memory.  Two blocks share an SM, so that
@@ -19,8 +19,9 @@
 // to 2^-25 of the row's reference (to 2^-34 of it below).  The exponents' range is what
 // counts: two e4m3 parts have the bits too, but end at 2^-18 of a reference, and the sum
 // of ten thousand weights that small may be a few per cent of the result (64 ragged
-// sequences 187 us with those, 190 with three).  The parts are
-// rows of their own (24 of 32 for up to 8 heads, 48 for up to 16).
+// sequences 187 us with those, 190 to 193 with three).  The parts are rows of their own
+// (24 of 32 for up to 8 heads, 48 for up to 16).  Weights over bf16 rows are rounded to
+// bf16, the type of the rows that they are multiplied with: 2^-8 of each, as out itself.
 //
 // A key's scale multiplies its scores, its value's scale 2^e its weights: they are
 // 2^(s + e - reference), the references being those of s + e.  The sums are of
@@ -38,6 +39,8 @@
 //
 // 64 ragged sequences over e4m3 rows: 190 us, 6.0 TB/s, 0.89 of the copy bandwidth; 8
 // sequences under a window of 4096, 32 heads of their own, bf16: 98 us, 5.5 TB/s, 0.81.
+// With 16 heads to a key head instead of 4: 336 us over bf16 rows, 0.94; 334 over e4m3
+// rows, 0.51, where two blocks' softmax warps split twice 16 weights a key and are the bound.
 #include "kv_attn_tile.cuh"
 
 namespace kvr {

@@ -14,7 +14,8 @@
 // 25 us, one by one in 29, four by four in 27): segments of whole groups, 16 lanes to a
 // group, 16-byte accesses on the bf16 side and 8-byte ones on the e4m3 side; a group's
 // maximum is four shuffles.  16411 GQA rows x 32 layers written in 511 us, 6.4 TB/s, 0.94
-// of the copy bandwidth; 9001 MHA rows x 16 layers read back in 541 us, 6.6 TB/s, 0.97.
+// of the copy bandwidth; 9001 MHA rows x 16 layers read back in 542 to 562 us by the card,
+// 6.4 to 6.6 TB/s, 0.94 to 0.97.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
