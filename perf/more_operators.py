@@ -518,8 +518,9 @@ def run(s):
             kv.kv_evict_select(s["weights"], s["kv_len"], s["budget"], case["sinks"],
                                case["recent"], s["keep"], s["count"], s["kept"], s["ws"])
             return s["keep"], s["count"], s["kept"]
+        more = dict(rope_base=KINDS[case["kind"]][3]) if case["quant"] else {}
         kv.kv_compact(s["pd"], s["table"], s["first"], s["keep"], s["count"], case["rotate"],
-                      s["ws"])
+                      s["ws"], **more)
         return s["pool"]
     return {"tree": _tree, "weights": _weights, "select": _select, "compact": _compact}[
         case["op"]](s)
