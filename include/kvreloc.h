@@ -20,6 +20,11 @@
  *                  back.
  *   - kv_attention computes new tokens' attention over the paged cache, bf16
  *                  or 8-bit, optionally through a sliding window with sinks.
+ *   - kv_tree_attention does so for a tree of drafted tokens.
+ *   - kv_attention_weights sums what each cached key receives of the queries'
+ *                  attention, kv_evict_select chooses the tokens that stay by
+ *                  such sums, and kv_compact closes the rows that stay up (also
+ *                  those of an accepted path of a tree).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -518,6 +523,125 @@ kv_status kv_attention_quant(const kv_quant_pool_desc *pool, int32_t layer,
                              float *d_lse, void *d_workspace, size_t workspace_bytes,
                              kv_stream_t stream);
 
+/* ---------------------------------------------------------------------
+ * Drafted tokens and bounded caches
+ * ------------------------------------------------------------------- */
+
+/* Attention of a tree of drafted tokens over the paged cache.  The sequences'
+ * new tokens are in the cache, as in kv_attention; query i of a sequence sees
+ * every key before the new ones (k < d_kv_len - n), and new token j (key
+ * d_kv_len - n + j) when bit j % 32 of word j / 32 of its mask is set:
+ *     d_mask[t * mask_stride + w],  t = d_q_off[s] + i,  w < ceil(max_q_len / 32).
+ * Bits from n on have no part.  A query sees itself only if its mask says so.
+ * attn->causal has no part; attn->window must be 0 (KV_ERR_UNSUPPORTED: a
+ * query's position would follow from its depth).  mask_stride is at least
+ * ceil(max_q_len / 32).  Everything else is as in kv_attention: results, empty
+ * rows, precision (single tokens too: weights in bf16), errors, strides and the
+ * workspace, whose size is kv_tree_attention_workspace_size's. */
+size_t kv_tree_attention_workspace_size(const kv_pool_desc *pool, const kv_attn_desc *attn,
+                                        int64_t total_q, int32_t num_heads);
+size_t kv_tree_attention_quant_workspace_size(const kv_quant_pool_desc *pool,
+                                              const kv_attn_desc *attn, int64_t total_q,
+                                              int32_t num_heads);
+kv_status kv_tree_attention(const kv_pool_desc *pool, int32_t layer, const kv_attn_desc *attn,
+                            const uint32_t *d_mask, int64_t mask_stride, int64_t total_q,
+                            int32_t num_heads, const void *d_q, int64_t q_tok_stride,
+                            int64_t q_head_stride, void *d_out, int64_t out_tok_stride,
+                            int64_t out_head_stride, float *d_lse, void *d_workspace,
+                            size_t workspace_bytes, kv_stream_t stream);
+kv_status kv_tree_attention_quant(const kv_quant_pool_desc *pool, int32_t layer,
+                                  const kv_attn_desc *attn, const uint32_t *d_mask,
+                                  int64_t mask_stride, int64_t total_q, int32_t num_heads,
+                                  const void *d_q, int64_t q_tok_stride, int64_t q_head_stride,
+                                  void *d_out, int64_t out_tok_stride, int64_t out_head_stride,
+                                  float *d_lse, void *d_workspace, size_t workspace_bytes,
+                                  kv_stream_t stream);
+
+/* What each cached key receives of the new tokens' attention, summed over the
+ * queries that see it (causal, window and sinks as in kv_attention) and over all
+ * query heads:
+ *     weights[s][k] = keep * weights[s][k] + Σ_{i, h} exp(scale * q_ih . key_k - lse_ih)
+ * for 0 <= k < d_kv_len[s]; entry (s, k) is d_weights[s*weight_stride + k]
+ * (weight_stride >= max_kv_len), entries from d_kv_len[s] on are left as they are.
+ * d_lse [total_q][num_heads] is kv_attention's of the same keys; a query
+ * whose lse is -infinity counts nothing.  keep (finite, >= 0): 0 writes without
+ * reading, 1 adds, less lets older steps fade; with one array for all layers, the
+ * first layer's call fades and the others add.  What a key row holds has no part in
+ * the sums of other keys, and none in its own where no query sees it.  Scores are fp32 sums of products of bf16 values, the sums fp32 in an
+ * order that follows from the sizes alone: equal calls give equal bits.  Sequences whose
+ * lengths do not fit are skipped and a block id outside the pool adds nothing to its
+ * keys; both set KV_ERR_OUT_OF_RANGE.  Limits, strides and errors otherwise as in
+ * kv_attention. */
+size_t kv_attention_weights_workspace_size(const kv_pool_desc *pool, const kv_attn_desc *attn,
+                                           int64_t total_q, int32_t num_heads);
+size_t kv_attention_weights_quant_workspace_size(const kv_quant_pool_desc *pool,
+                                                 const kv_attn_desc *attn, int64_t total_q,
+                                                 int32_t num_heads);
+kv_status kv_attention_weights(const kv_pool_desc *pool, int32_t layer, const kv_attn_desc *attn,
+                               int64_t total_q, int32_t num_heads, const void *d_q,
+                               int64_t q_tok_stride, int64_t q_head_stride, const float *d_lse,
+                               float *d_weights, int64_t weight_stride, float keep,
+                               void *d_workspace, size_t workspace_bytes, kv_stream_t stream);
+kv_status kv_attention_weights_quant(const kv_quant_pool_desc *pool, int32_t layer,
+                                     const kv_attn_desc *attn, int64_t total_q, int32_t num_heads,
+                                     const void *d_q, int64_t q_tok_stride, int64_t q_head_stride,
+                                     const float *d_lse, float *d_weights, int64_t weight_stride,
+                                     float keep, void *d_workspace, size_t workspace_bytes,
+                                     kv_stream_t stream);
+
+/* Which tokens of a cache stay.  Sequence s has d_kv_len[s] tokens (at most
+ * max_kv_len <= 2^30) with weights d_weights[s*weight_stride + k]; of them
+ * n = min(d_kv_len[s], d_budget[s]) stay, in this order of preference: the first
+ * `sinks` tokens from the first on, the last `recent` ones from the last back, the
+ * others by falling weight, equal ones (0 and -0 among them) by rising position, NaN
+ * last.  Writes their positions in ascending order to d_keep[s*keep_stride + i],
+ * i < n, n to d_count[s], and, when d_kept_weights is not NULL, their weights to
+ * d_kept_weights[s*kept_stride + i] (another array than d_weights).  A sequence whose
+ * numbers do not fit (a length below 0 or above max_kv_len, a negative budget, n >
+ * max_keep) gets d_count = -1 and sets KV_ERR_OUT_OF_RANGE.  Nothing is written behind
+ * the n entries.  One kernel. */
+size_t kv_evict_workspace_size(int32_t num_seqs, int32_t max_kv_len);
+kv_status kv_evict_select(int32_t num_seqs, const float *d_weights, int64_t weight_stride,
+                          const int32_t *d_kv_len, int32_t max_kv_len, const int32_t *d_budget,
+                          int32_t sinks, int32_t recent, int32_t *d_keep, int64_t keep_stride,
+                          int32_t max_keep, int32_t *d_count, float *d_kept_weights,
+                          int64_t kept_stride, void *d_workspace, size_t workspace_bytes,
+                          kv_stream_t stream);
+
+/* Rows that stay close up, in place, in every layer: for i < d_count[s] the row at
+ * position b + d_keep[s*keep_stride + i] of sequence s moves to position b + i, where
+ * b = d_first[s] (d_first NULL: 0).  The list ascends strictly from 0 or above.  Its copy
+ * part is moved as it is; its rotary part is turned by R(i - d_keep[i]), rounded once,
+ * when rotate = 1, so that keys fit the positions that they move to, and moved as it is
+ * when rotate = 0.  Rows that keep their place are not touched, and positions from
+ * b + d_count[s] on keep what they held.  d_keep and d_count are as kv_evict_select
+ * writes them; an accepted path of drafted tokens closes up with b the number of tokens
+ * before them and the path's token numbers as the list (no turn: a draft stands in
+ * the cache at the position of its depth).  Block tables as in kv_splice, and distinct
+ * blocks likewise.
+ * A quantised pool moves values and scales as they are; MLA rows, whose k_pe is bf16,
+ * are turned when rope_base > 0 (its base; pair_convention as in kv_pool_desc), head rows
+ * are not (rope_base > 0: KV_ERR_UNSUPPORTED).
+ * A sequence with d_count < 0 or > max_count, or a negative d_first, is skipped, as is a
+ * row out of order or outside the table or the pool; all set KV_ERR_OUT_OF_RANGE.  With a
+ * list out of order, rows of that sequence may be overwritten before they are read.  One
+ * kernel, and one for the tables of cos and sin when rows turn. */
+size_t kv_compact_workspace_size(const kv_pool_desc *pool, int32_t num_seqs, int32_t max_blocks,
+                                 int32_t max_count);
+size_t kv_compact_quant_workspace_size(const kv_quant_pool_desc *pool, int32_t num_seqs,
+                                       int32_t max_blocks, int32_t max_count);
+kv_status kv_compact(const kv_pool_desc *pool, int32_t num_seqs, const int32_t *d_block_tables,
+                     int32_t max_blocks, const int32_t *d_first, const int32_t *d_keep,
+                     int64_t keep_stride, const int32_t *d_count, int32_t max_count,
+                     int32_t rotate, void *d_workspace, size_t workspace_bytes,
+                     kv_stream_t stream);
+kv_status kv_compact_quant(const kv_quant_pool_desc *pool, int32_t num_seqs,
+                           const int32_t *d_block_tables, int32_t max_blocks,
+                           const int32_t *d_first, const int32_t *d_keep, int64_t keep_stride,
+                           const int32_t *d_count, int32_t max_count, double rope_base,
+                           int32_t pair_convention, void *d_workspace, size_t workspace_bytes,
+                           kv_stream_t stream);
+
 /* Debug checks of the caller contracts that the in-place kernels rely on
  * (process-wide; off by default).  When on:
  *  - kv_relocate (and kv_relocate_noalloc) on a source and destination that
@@ -541,14 +665,15 @@ kv_status kv_attention_quant(const kv_quant_pool_desc *pool, int32_t layer,
  * no kernel reads anything more. */
 void kv_set_debug_checks(int32_t on);
 
-/* Upper bound, in nanoseconds, of every inter-block wait inside kv_splice and of
- * every wait between the roles of a kv_attention block (default 2e9).  Values
+/* Upper bound, in nanoseconds, of every inter-block wait inside kv_splice and
+ * kv_compact and of every wait between the roles of a kv_attention, kv_tree_attention
+ * or kv_attention_weights block (default 2e9).  Values
  * <= 0 restore the default.  Process-wide. */
 void kv_set_wait_limit_ns(int64_t limit_ns);
 
 /* Test hook for the failure path of the in-place splices (process-wide; -1,
- * the default, turns it off).  The tile of each kv_splice / kv_splice_composed
- * launch that draws ticket `ticket` does not publish that it has read its
+ * the default, turns it off).  The tile of each kv_splice / kv_splice_composed /
+ * kv_compact launch that draws ticket `ticket` does not publish that it has read its
  * rows; the tiles whose destination overlaps those rows then wait in vain
  * until the wait limit, record KV_ERR_TIMEOUT, skip their stores and keep
  * publishing, so the launch still finishes.  Lets a test run the kernels' own

@@ -11,6 +11,10 @@ missing, importing the binding's entry points raises.
     kv_patch(pool, ...)          in-place rank-m patch U_m V_mᵀ
     kv_quantize / kv_dequantize  rows into an 8-bit pool and back
     kv_attention(pool, ...)      new tokens' attention over a bf16 or 8-bit pool
+    kv_tree_attention(pool, ...) the same for a tree of drafted tokens
+    kv_attention_weights(pool, ...) what each cached key receives of it, summed
+    kv_evict_select(weights, ...) which tokens of a cache stay
+    kv_compact(pool, ...)        the rows that stay close up, in place
 """
 from __future__ import annotations
 
@@ -142,6 +146,8 @@ def load(build_if_missing: bool = False) -> C.CDLL:
     P, PP = C.POINTER(kv_pool_desc), C.POINTER(kv_patch_desc)
     Q, A = C.POINTER(kv_quant_pool_desc), C.POINTER(kv_attn_desc)
     attn = [i32, A, i64, i32, vp, i64, i64, vp, i64, i64, vp, vp, sz, vp]
+    tree = [i32, A, vp, i64, *attn[2:]]
+    weights = [i32, A, i64, i32, vp, i64, i64, vp, vp, i64, C.c_float, vp, sz, vp]
     sig = {
         "kv_workspace_size": (sz, [P, i64, i32]),
         "kv_relocate": (i32, [P, P, i32, i64, vp, vp, vp, vp, vp, vp, i32, i32, PP, vp, sz, vp]),
@@ -172,6 +178,22 @@ def load(build_if_missing: bool = False) -> C.CDLL:
         "kv_attention_quant_workspace_size": (sz, [Q, A, i64, i32]),
         "kv_attention": (i32, [P, *attn]),
         "kv_attention_quant": (i32, [Q, *attn]),
+        "kv_tree_attention_workspace_size": (sz, [P, A, i64, i32]),
+        "kv_tree_attention_quant_workspace_size": (sz, [Q, A, i64, i32]),
+        "kv_tree_attention": (i32, [P, *tree]),
+        "kv_tree_attention_quant": (i32, [Q, *tree]),
+        "kv_attention_weights_workspace_size": (sz, [P, A, i64, i32]),
+        "kv_attention_weights_quant_workspace_size": (sz, [Q, A, i64, i32]),
+        "kv_attention_weights": (i32, [P, *weights]),
+        "kv_attention_weights_quant": (i32, [Q, *weights]),
+        "kv_evict_workspace_size": (sz, [i32, i32]),
+        "kv_evict_select": (i32, [i32, vp, i64, vp, i32, vp, i32, i32, vp, i64, i32, vp, vp, i64,
+                                  vp, sz, vp]),
+        "kv_compact_workspace_size": (sz, [P, i32, i32, i32]),
+        "kv_compact_quant_workspace_size": (sz, [Q, i32, i32, i32]),
+        "kv_compact": (i32, [P, i32, vp, i32, vp, vp, i64, vp, i32, i32, vp, sz, vp]),
+        "kv_compact_quant": (i32, [Q, i32, vp, i32, vp, vp, i64, vp, i32, C.c_double, i32, vp, sz,
+                                   vp]),
         "kv_status_string": (C.c_char_p, [i32]),
         "kv_version": (i32, []),
     }
@@ -513,6 +535,196 @@ def kv_attention(pool, layer: int, attn: kv_attn_desc, q: torch.Tensor, out: tor
            ws.data_ptr(), ws.nbytes, _stream(stream))
     if check:
         _check(st, "kv_attention")
+    return st
+
+
+def _kind(pool, name: str):
+    """The library's function ``name`` for a pool of either kind (``_quant`` goes before
+    ``_workspace_size``)."""
+    if isinstance(pool, kv_quant_pool_desc):
+        head, _, tail = name.partition("_workspace_size")
+        name = head + "_quant" + ("_workspace_size" if _ else "") + tail
+    return getattr(load(), name)
+
+
+def _sized_workspace(size: int, where: str, device) -> torch.Tensor:
+    if size == 0:
+        raise KVError(KV_ERR_INVALID_ARG, where)
+    return torch.empty(int(size), dtype=torch.uint8, device=device)
+
+
+def _check_queries(pool, q, where: str) -> None:
+    mla = pool.rot_heads == 1
+    if (q.dtype != torch.bfloat16 or q.dim() != 3 or q.stride(2) != 1
+            or q.shape[2] != (pool.copy_dim + pool.rot_head_dim if mla else pool.rot_head_dim)):
+        raise ValueError(f"{where}: q must be bf16 (tokens, heads, key width) with a unit last "
+                         "stride")
+
+
+def _check_int32(where: str, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and (t.dtype != torch.int32 or t.stride(-1) != 1):
+            raise ValueError(f"{where}: {name} must be int32 with a unit last stride")
+
+
+def tree_mask(parents, device="cuda") -> torch.Tensor:
+    """Masks for kv_tree_attention of one tree for every sequence: ``parents[s][j]`` is the
+    token that token j hangs on (before j; -1: none).  A token sees itself and its
+    ancestors.  int32 (tokens, words)."""
+    words = max([1] + [-(-len(p) // 32) for p in parents])
+    rows = []
+    for p in parents:
+        sees = []
+        for j, up in enumerate(p):
+            if not -1 <= up < j:
+                raise ValueError(f"tree_mask: token {j} hangs on {up}")
+            sees.append((sees[up] if up >= 0 else 0) | 1 << j)
+        rows += [[(x >> 32 * w) & 0xFFFFFFFF for w in range(words)] for x in sees]
+    bits = torch.tensor(rows, dtype=torch.int64).reshape(-1, words)
+    return (bits - ((bits >> 31) << 32)).to(torch.int32).to(device)
+
+
+def tree_workspace(pool, attn: kv_attn_desc, q: torch.Tensor) -> torch.Tensor:
+    """A device workspace for kv_tree_attention of queries like ``q`` with ``attn``."""
+    name = "kv_tree_attention_workspace_size"
+    n = _kind(pool, name)(C.byref(pool), C.byref(attn), q.shape[0], q.shape[1])
+    return _sized_workspace(n, name, q.device)
+
+
+def kv_tree_attention(pool, layer: int, attn: kv_attn_desc, mask: torch.Tensor, q: torch.Tensor,
+                      out: torch.Tensor, lse: Optional[torch.Tensor], ws: torch.Tensor,
+                      stream=None, check: bool = True) -> int:
+    """kv_attention of drafted trees: ``mask`` int32 (tokens, words), bit j of a query's words:
+    it sees its sequence's new token j (tree_mask); the keys before the new tokens are seen
+    by all.  ``attn``'s causal has no part, its window must be 0."""
+    n, heads, dk = q.shape
+    _check_queries(pool, q, "kv_tree_attention")
+    if (out.dtype != torch.bfloat16 or out.stride(2) != 1
+            or out.shape != (n, heads, pool.copy_dim if pool.rot_heads == 1 else dk)):
+        raise ValueError("kv_tree_attention: out must be bf16 (tokens, heads, value width) with a "
+                         "unit last stride")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, heads)
+                            or not lse.is_contiguous()):
+        raise ValueError("kv_tree_attention: lse must be contiguous fp32 (tokens, heads)")
+    _check_int32("kv_tree_attention", mask=mask)
+    if mask.dim() != 2 or mask.shape[0] != n or mask.shape[1] * 32 < attn.max_q_len:
+        raise ValueError("kv_tree_attention: mask must be (tokens, words) with a bit for each of "
+                         "max_q_len tokens")
+    stride = mask.stride(0) if n > 1 else mask.shape[1]
+    st = _kind(pool, "kv_tree_attention")(
+        C.byref(pool), layer, C.byref(attn), mask.data_ptr(), stride, n, heads,
+        q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), out.stride(0), out.stride(1),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes, _stream(stream))
+    if check:
+        _check(st, "kv_tree_attention")
+    return st
+
+
+def weights_workspace(pool, attn: kv_attn_desc, q: torch.Tensor) -> torch.Tensor:
+    """A device workspace for kv_attention_weights of queries like ``q`` with ``attn``."""
+    name = "kv_attention_weights_workspace_size"
+    n = _kind(pool, name)(C.byref(pool), C.byref(attn), q.shape[0], q.shape[1])
+    return _sized_workspace(n, name, q.device)
+
+
+def kv_attention_weights(pool, layer: int, attn: kv_attn_desc, q: torch.Tensor,
+                         lse: torch.Tensor, weights: torch.Tensor, keep: float, ws: torch.Tensor,
+                         stream=None, check: bool = True) -> int:
+    """``weights`` fp32 (seqs, >= max_kv_len) = ``keep`` * weights + what each key of layer
+    ``layer`` receives of the queries' attention, over all queries and heads; ``lse`` fp32
+    (tokens, heads) is kv_attention's."""
+    n, heads, _ = q.shape
+    _check_queries(pool, q, "kv_attention_weights")
+    if lse.dtype != torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous():
+        raise ValueError("kv_attention_weights: lse must be contiguous fp32 (tokens, heads)")
+    if (weights.dtype != torch.float32 or weights.dim() != 2 or weights.stride(1) != 1
+            or weights.shape[0] != attn.num_seqs or weights.shape[1] < attn.max_kv_len):
+        raise ValueError("kv_attention_weights: weights must be fp32 (seqs, at least max_kv_len) "
+                         "with a unit last stride")
+    stride = weights.stride(0) if attn.num_seqs > 1 else max(attn.max_kv_len, weights.shape[1])
+    st = _kind(pool, "kv_attention_weights")(
+        C.byref(pool), layer, C.byref(attn), n, heads, q.data_ptr(), q.stride(0), q.stride(1),
+        lse.data_ptr(), weights.data_ptr(), stride, float(keep), ws.data_ptr(), ws.nbytes,
+        _stream(stream))
+    if check:
+        _check(st, "kv_attention_weights")
+    return st
+
+
+def evict_workspace(num_seqs: int, max_kv_len: int, device="cuda") -> torch.Tensor:
+    """A device workspace for kv_evict_select."""
+    name = "kv_evict_workspace_size"
+    return _sized_workspace(load().kv_evict_workspace_size(int(num_seqs), int(max_kv_len)), name,
+                            device)
+
+
+def kv_evict_select(weights: torch.Tensor, kv_len: torch.Tensor, budget: torch.Tensor, sinks: int,
+                    recent: int, keep: torch.Tensor, count: torch.Tensor,
+                    kept_weights: Optional[torch.Tensor], ws: torch.Tensor, stream=None,
+                    check: bool = True) -> int:
+    """Which tokens stay: ``budget`` int32 (seqs,) of the ``kv_len`` int32 (seqs,) of each
+    sequence, first the ``sinks`` first and ``recent`` last ones, then by ``weights`` fp32
+    (seqs, longest).  Writes positions, ascending, to ``keep`` int32 (seqs, most), their number
+    to ``count`` int32 (seqs,) and their weights to ``kept_weights`` fp32 (seqs, most) or
+    None."""
+    where = "kv_evict_select"
+    s = kv_len.numel()
+    _check_int32(where, kv_len=kv_len, budget=budget, keep=keep, count=count)
+    for name, t in (("weights", weights), ("kept_weights", kept_weights)):
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != s
+                              or t.stride(1) != 1):
+            raise ValueError(f"{where}: {name} must be fp32 (seqs, ...) with a unit last stride")
+    if (keep.dim() != 2 or keep.shape[0] != s or budget.shape != (s,) or count.shape != (s,)
+            or kv_len.dim() != 1
+            or (kept_weights is not None and kept_weights.shape[1] < keep.shape[1])):
+        raise ValueError(f"{where}: kv_len, budget and count must be (seqs,), keep (seqs, most), "
+                         "kept_weights as wide")
+    wide = lambda t: 0 if t is None else t.stride(0) if s > 1 else t.shape[1]  # noqa: E731
+    st = load().kv_evict_select(
+        s, weights.data_ptr(), wide(weights), kv_len.data_ptr(), weights.shape[1],
+        budget.data_ptr(), int(sinks), int(recent), keep.data_ptr(), wide(keep), keep.shape[1],
+        count.data_ptr(), _ptr(kept_weights), wide(kept_weights), ws.data_ptr(), ws.nbytes,
+        _stream(stream))
+    if check:
+        _check(st, where)
+    return st
+
+
+def compact_workspace(pool, num_seqs: int, max_blocks: int, max_count: int,
+                      device="cuda") -> torch.Tensor:
+    """A device workspace for kv_compact of lists of up to ``max_count`` rows."""
+    name = "kv_compact_workspace_size"
+    n = _kind(pool, name)(C.byref(pool), int(num_seqs), int(max_blocks), int(max_count))
+    return _sized_workspace(n, name, device)
+
+
+def kv_compact(pool, block_tables: torch.Tensor, first: Optional[torch.Tensor],
+               keep: torch.Tensor, count: torch.Tensor, rotate: bool, ws: torch.Tensor,
+               rope_base: float = 0.0, pair_convention: int = 0, stream=None,
+               check: bool = True) -> int:
+    """Rows ``keep`` int32 (seqs, most; ``count`` int32 (seqs,) of them, ascending) of each
+    sequence move to its positions 0, 1, ..., both counted from ``first`` int32 (seqs,) or 0,
+    in every layer of ``pool``; ``rotate`` turns rotary parts to their new positions.  A
+    quantised pool does not hold its ``rope_base`` and ``pair_convention``: they are given
+    here (MLA rows only)."""
+    where = "kv_compact"
+    s = count.numel()
+    _check_int32(where, block_tables=block_tables, first=first, keep=keep, count=count)
+    if (block_tables.dim() != 2 or not block_tables.is_contiguous() or keep.dim() != 2
+            or block_tables.shape[0] != s or keep.shape[0] != s or count.dim() != 1
+            or (first is not None and first.shape != (s,))):
+        raise ValueError(f"{where}: block_tables must be contiguous (seqs, blocks), keep (seqs, "
+                         "most), count and first (seqs,)")
+    quant = isinstance(pool, kv_quant_pool_desc)
+    if quant and rotate and not rope_base > 0:
+        raise ValueError(f"{where}: rows of a quantised pool turn with a rope_base")
+    how = (float(rope_base) if rotate else 0.0, int(pair_convention)) if quant else (int(rotate),)
+    st = _kind(pool, where)(
+        C.byref(pool), s, block_tables.data_ptr(), block_tables.shape[1], _ptr(first),
+        keep.data_ptr(), keep.stride(0) if s > 1 else keep.shape[1], count.data_ptr(),
+        keep.shape[1], *how, ws.data_ptr(), ws.nbytes, _stream(stream))
+    if check:
+        _check(st, where)
     return st
 
 

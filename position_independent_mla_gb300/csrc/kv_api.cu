@@ -1319,11 +1319,12 @@ int32_t attn_window(const kv_attn_desc *a)
     return a->window >= a->max_kv_len ? 0 : a->window;
 }
 
-AttnPlan attn_plan(RowKind kind, bool quant, const kv_attn_desc *a, int64_t total_q,
+AttnPlan attn_plan(RowKind kind, bool quant, bool tree, const kv_attn_desc *a, int64_t total_q,
                    int32_t heads, int32_t kv_heads)
 {
     AttnShape s{};
     s.quant = quant;
+    s.tree = tree;
     s.total_q = total_q;
     s.num_seqs = a->num_seqs;
     s.max_q_len = a->max_q_len;
@@ -1365,15 +1366,32 @@ AttnLayout attn_layout(RowKind kind, const AttnPlan &pl, const kv_attn_desc *a, 
     return l;
 }
 
+// Masks of drafted trees.
+struct TreeMask {
+    const uint32_t *words;
+    int64_t stride;
+};
+
+// Checks of a tree call beyond attn_ok's: queries of a tree have no place in a window.
+kv_status tree_ok(const kv_attn_desc *a) { return a->window > 0 ? KV_ERR_UNSUPPORTED : KV_OK; }
+
 kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind kind,
                          int64_t num_slots, int32_t block, int32_t kv_heads,
-                         const kv_attn_desc *a, int64_t total_q, int32_t heads, const void *q,
-                         int64_t q_ts, int64_t q_hs, void *out, int64_t o_ts, int64_t o_hs,
-                         float *lse, void *ws, size_t ws_bytes, cudaStream_t stream)
+                         const kv_attn_desc *a, const TreeMask *tree, int64_t total_q,
+                         int32_t heads, const void *q, int64_t q_ts, int64_t q_hs, void *out,
+                         int64_t o_ts, int64_t o_hs, float *lse, void *ws, size_t ws_bytes,
+                         cudaStream_t stream)
 {
     kv_status st = attn_ok(a, total_q, heads, kv_heads);
     if (st != KV_OK)
         return st;
+    if (tree) {
+        if ((st = tree_ok(a)) != KV_OK)
+            return st;
+        if ((total_q > 0 && !tree->words) || !aligned_to(tree->words, 4) ||
+            tree->stride < (a->max_q_len + 31) / 32)
+            return KV_ERR_INVALID_ARG;
+    }
     const int64_t strides[4] = {total_q > 1 ? q_ts : 0, heads > 1 ? q_hs : 0,
                                 total_q > 1 ? o_ts : 0, heads > 1 ? o_hs : 0};
     for (int64_t s : strides)
@@ -1385,7 +1403,7 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
     if (!aligned16(q) || !aligned16(out) || !aligned_to(lse, 4) || !aligned_to(a->d_q_off, 4) ||
         !aligned_to(a->d_kv_len, 4) || !aligned_to(a->d_block_tables, 4))
         return KV_ERR_INVALID_ARG;
-    const AttnPlan pl = attn_plan(kind, quant != nullptr, a, total_q, heads, kv_heads);
+    const AttnPlan pl = attn_plan(kind, quant != nullptr, tree != nullptr, a, total_q, heads, kv_heads);
     const AttnLayout lay = attn_layout(kind, pl, a, total_q, heads, kv_heads);
     if (pl.blocks > 0x7FFFFFFFll || num_slots > 0x7FFFFFFFll)
         return KV_ERR_INVALID_ARG;
@@ -1432,9 +1450,14 @@ kv_status attention_impl(const PoolView *bf16, const QuantView *quant, RowKind k
     p.q_off = a->d_q_off;
     p.kv_len = a->d_kv_len;
     p.block_tables = a->d_block_tables;
-    p.causal = a->causal;
+    p.causal = tree ? 0 : a->causal;
     p.window = attn_window(a);
     p.sinks = a->sinks;
+    if (tree) {
+        p.tree = tree->words;
+        p.tree_stride = tree->stride;
+        p.tree_words = (a->max_q_len + 31) / 32;
+    }
     p.scale = a->scale;
     p.split_tiles = pl.split_tiles;
     p.max_splits = pl.max_splits;
@@ -1521,7 +1544,7 @@ size_t kv_attention_workspace_size(const kv_pool_desc *pool, const kv_attn_desc 
     if (!pool_ok(pool) || !row_kind(pool, &kind) ||
         attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK)
         return 0;
-    return attn_layout(kind, attn_plan(kind, false, attn, total_q, num_heads, pool->rot_heads), attn,
+    return attn_layout(kind, attn_plan(kind, false, false, attn, total_q, num_heads, pool->rot_heads), attn,
                        total_q, num_heads, pool->rot_heads)
         .bytes;
 }
@@ -1533,7 +1556,7 @@ size_t kv_attention_quant_workspace_size(const kv_quant_pool_desc *pool, const k
     if (!quant_pool_ok(pool) || !quant_row_kind(pool, &kind) ||
         attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK)
         return 0;
-    return attn_layout(kind, attn_plan(kind, true, attn, total_q, num_heads, pool->rot_heads), attn,
+    return attn_layout(kind, attn_plan(kind, true, false, attn, total_q, num_heads, pool->rot_heads), attn,
                        total_q, num_heads, pool->rot_heads)
         .bytes;
 }
@@ -1554,7 +1577,7 @@ kv_status kv_attention(const kv_pool_desc *pool, int32_t layer, const kv_attn_de
     v.copy += layer * v.copy_ls;
     v.rot += layer * v.rot_ls;
     return attention_impl(&v, nullptr, kind, pool->num_slots, pool->block_size, pool->rot_heads,
-                          attn, total_q, num_heads, d_q, q_tok_stride, q_head_stride, d_out,
+                          attn, nullptr, total_q, num_heads, d_q, q_tok_stride, q_head_stride, d_out,
                           out_tok_stride, out_head_stride, d_lse, d_workspace, workspace_bytes,
                           reinterpret_cast<cudaStream_t>(stream));
 }
@@ -1574,9 +1597,535 @@ kv_status kv_attention_quant(const kv_quant_pool_desc *pool, int32_t layer,
         return KV_ERR_UNSUPPORTED;
     const QuantView v = quant_view(pool, layer);
     return attention_impl(nullptr, &v, kind, pool->num_slots, pool->block_size, pool->rot_heads,
-                          attn, total_q, num_heads, d_q, q_tok_stride, q_head_stride, d_out,
+                          attn, nullptr, total_q, num_heads, d_q, q_tok_stride, q_head_stride, d_out,
                           out_tok_stride, out_head_stride, d_lse, d_workspace, workspace_bytes,
                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+} // extern "C"
+
+// ---------------------------------------------------------------------------
+// Attention of drafted trees
+// ---------------------------------------------------------------------------
+
+extern "C" {
+
+size_t kv_tree_attention_workspace_size(const kv_pool_desc *pool, const kv_attn_desc *attn,
+                                        int64_t total_q, int32_t num_heads)
+{
+    RowKind kind;
+    if (!pool_ok(pool) || !row_kind(pool, &kind) ||
+        attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK || tree_ok(attn) != KV_OK)
+        return 0;
+    return attn_layout(kind,
+                       attn_plan(kind, false, true, attn, total_q, num_heads, pool->rot_heads),
+                       attn, total_q, num_heads, pool->rot_heads)
+        .bytes;
+}
+
+size_t kv_tree_attention_quant_workspace_size(const kv_quant_pool_desc *pool,
+                                              const kv_attn_desc *attn, int64_t total_q,
+                                              int32_t num_heads)
+{
+    RowKind kind;
+    if (!quant_pool_ok(pool) || !quant_row_kind(pool, &kind) ||
+        attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK || tree_ok(attn) != KV_OK)
+        return 0;
+    return attn_layout(kind,
+                       attn_plan(kind, true, true, attn, total_q, num_heads, pool->rot_heads),
+                       attn, total_q, num_heads, pool->rot_heads)
+        .bytes;
+}
+
+kv_status kv_tree_attention(const kv_pool_desc *pool, int32_t layer, const kv_attn_desc *attn,
+                            const uint32_t *d_mask, int64_t mask_stride, int64_t total_q,
+                            int32_t num_heads, const void *d_q, int64_t q_tok_stride,
+                            int64_t q_head_stride, void *d_out, int64_t out_tok_stride,
+                            int64_t out_head_stride, float *d_lse, void *d_workspace,
+                            size_t workspace_bytes, kv_stream_t stream)
+{
+    t_launches = 0;
+    if (!pool_ok(pool) || layer < 0 || layer >= pool->num_layers)
+        return KV_ERR_INVALID_ARG;
+    RowKind kind;
+    if (!row_kind(pool, &kind))
+        return KV_ERR_UNSUPPORTED;
+    PoolView v = view_of(pool);
+    v.copy += layer * v.copy_ls;
+    v.rot += layer * v.rot_ls;
+    const TreeMask tree{d_mask, mask_stride};
+    return attention_impl(&v, nullptr, kind, pool->num_slots, pool->block_size, pool->rot_heads,
+                          attn, &tree, total_q, num_heads, d_q, q_tok_stride, q_head_stride, d_out,
+                          out_tok_stride, out_head_stride, d_lse, d_workspace, workspace_bytes,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+kv_status kv_tree_attention_quant(const kv_quant_pool_desc *pool, int32_t layer,
+                                  const kv_attn_desc *attn, const uint32_t *d_mask,
+                                  int64_t mask_stride, int64_t total_q, int32_t num_heads,
+                                  const void *d_q, int64_t q_tok_stride, int64_t q_head_stride,
+                                  void *d_out, int64_t out_tok_stride, int64_t out_head_stride,
+                                  float *d_lse, void *d_workspace, size_t workspace_bytes,
+                                  kv_stream_t stream)
+{
+    t_launches = 0;
+    if (!quant_pool_ok(pool) || layer < 0 || layer >= pool->num_layers)
+        return KV_ERR_INVALID_ARG;
+    RowKind kind;
+    if (!quant_row_kind(pool, &kind))
+        return KV_ERR_UNSUPPORTED;
+    const QuantView v = quant_view(pool, layer);
+    const TreeMask tree{d_mask, mask_stride};
+    return attention_impl(nullptr, &v, kind, pool->num_slots, pool->block_size, pool->rot_heads,
+                          attn, &tree, total_q, num_heads, d_q, q_tok_stride, q_head_stride, d_out,
+                          out_tok_stride, out_head_stride, d_lse, d_workspace, workspace_bytes,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+} // extern "C"
+
+// ---------------------------------------------------------------------------
+// What each key receives of the queries' attention
+// ---------------------------------------------------------------------------
+
+namespace {
+
+WeightsPlan weights_plan(RowKind kind, const kv_attn_desc *a, int64_t total_q, int32_t heads,
+                         int32_t kv_heads)
+{
+    AttnShape s{};
+    s.total_q = total_q;
+    s.num_seqs = a->num_seqs;
+    s.max_q_len = a->max_q_len;
+    s.max_kv_len = a->max_kv_len;
+    s.group = heads / kv_heads;
+    s.kv_heads = kv_heads;
+    return plan_weights(kind, s);
+}
+
+size_t weights_bytes(const WeightsPlan &pl)
+{
+    return pl.blocks > 0x7FFFFFFFll ? 0 : align256(kHeaderBytes + (size_t)pl.blocks * 4);
+}
+
+kv_status weights_impl(AttnParams p, RowKind kind, int64_t num_slots, int32_t block,
+                       int32_t kv_heads, const kv_attn_desc *a, int64_t total_q, int32_t heads,
+                       const void *q, int64_t q_ts, int64_t q_hs, const float *lse,
+                       float *weights, int64_t weight_stride, float keep, void *ws,
+                       size_t ws_bytes, cudaStream_t stream)
+{
+    kv_status st = attn_ok(a, total_q, heads, kv_heads);
+    if (st != KV_OK)
+        return st;
+    for (int64_t s : {total_q > 1 ? q_ts : 0, heads > 1 ? q_hs : 0})
+        if (s < 0 || s % 8 != 0)
+            return KV_ERR_INVALID_ARG;
+    const bool any = a->num_seqs > 0 && a->max_kv_len > 0;
+    if (any && (!a->d_q_off || !a->d_kv_len || !a->d_block_tables || a->max_blocks == 0 ||
+                !weights || (total_q > 0 && (!q || !lse))))
+        return KV_ERR_INVALID_ARG;
+    if (weight_stride < a->max_kv_len || !(keep >= 0.0f) || !(keep < INFINITY))
+        return KV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned_to(lse, 4) || !aligned_to(weights, 4) ||
+        !aligned_to(a->d_q_off, 4) || !aligned_to(a->d_kv_len, 4) ||
+        !aligned_to(a->d_block_tables, 4) || num_slots > 0x7FFFFFFFll)
+        return KV_ERR_INVALID_ARG;
+    const WeightsPlan pl = weights_plan(kind, a, total_q, heads, kv_heads);
+    const size_t need = weights_bytes(pl);
+    if (need == 0)
+        return KV_ERR_INVALID_ARG;
+    if ((st = ws_ok(ws, ws_bytes, need)) != KV_OK)
+        return st;
+    if (!any) {
+        KV_CUDA(cudaMemsetAsync(ws, 0, kHeaderBytes, stream));
+        return KV_OK;
+    }
+    p.num_blocks = num_slots / block;
+    p.block = block;
+    p.q = static_cast<const char *>(q);
+    p.q_ts = q_ts * 2;
+    p.q_hs = q_hs * 2;
+    p.total_q = total_q;
+    p.heads = heads;
+    p.group = heads / kv_heads;
+    p.kv_heads = kv_heads;
+    p.num_seqs = a->num_seqs;
+    p.max_q_len = a->max_q_len;
+    p.max_kv_len = a->max_kv_len;
+    p.max_blocks = a->max_blocks;
+    p.max_keys = std::min<int64_t>((int64_t)a->max_blocks * block, kMaxKeys);
+    p.q_off = a->d_q_off;
+    p.kv_len = a->d_kv_len;
+    p.block_tables = a->d_block_tables;
+    p.causal = a->causal;
+    p.window = attn_window(a);
+    p.sinks = a->sinks;
+    p.scale = a->scale;
+    p.wait_limit_ns = g_wait_limit_ns.load();
+    p.skip_block = g_skip_block.load();
+    p.header = static_cast<uint32_t *>(ws);
+    WeightsParams wp{};
+    wp.a = p;
+    wp.lse = lse;
+    wp.weights = weights;
+    wp.weight_stride = weight_stride;
+    wp.keep = keep;
+    KV_CUDA(mark(t_ev_start, stream));
+    KV_CUDA(launch_weights(wp, kind, pl, stream));
+    ++t_launches;
+    KV_CUDA(mark(t_ev_stop, stream));
+    return KV_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+size_t kv_attention_weights_workspace_size(const kv_pool_desc *pool, const kv_attn_desc *attn,
+                                           int64_t total_q, int32_t num_heads)
+{
+    RowKind kind;
+    if (!pool_ok(pool) || !row_kind(pool, &kind) ||
+        attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK)
+        return 0;
+    return weights_bytes(weights_plan(kind, attn, total_q, num_heads, pool->rot_heads));
+}
+
+size_t kv_attention_weights_quant_workspace_size(const kv_quant_pool_desc *pool,
+                                                 const kv_attn_desc *attn, int64_t total_q,
+                                                 int32_t num_heads)
+{
+    RowKind kind;
+    if (!quant_pool_ok(pool) || !quant_row_kind(pool, &kind) ||
+        attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK)
+        return 0;
+    return weights_bytes(weights_plan(kind, attn, total_q, num_heads, pool->rot_heads));
+}
+
+kv_status kv_attention_weights(const kv_pool_desc *pool, int32_t layer, const kv_attn_desc *attn,
+                               int64_t total_q, int32_t num_heads, const void *d_q,
+                               int64_t q_tok_stride, int64_t q_head_stride, const float *d_lse,
+                               float *d_weights, int64_t weight_stride, float keep,
+                               void *d_workspace, size_t workspace_bytes, kv_stream_t stream)
+{
+    t_launches = 0;
+    if (!pool_ok(pool) || layer < 0 || layer >= pool->num_layers)
+        return KV_ERR_INVALID_ARG;
+    RowKind kind;
+    if (!row_kind(pool, &kind))
+        return KV_ERR_UNSUPPORTED;
+    const PoolView v = view_of(pool);
+    AttnParams p{};
+    p.copy = v.copy + layer * v.copy_ls;
+    p.rot = v.rot + layer * v.rot_ls;
+    p.copy_ss = v.copy_ss;
+    p.rot_ss = v.rot_ss;
+    return weights_impl(p, kind, pool->num_slots, pool->block_size, pool->rot_heads, attn, total_q,
+                        num_heads, d_q, q_tok_stride, q_head_stride, d_lse, d_weights,
+                        weight_stride, keep, d_workspace, workspace_bytes,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+kv_status kv_attention_weights_quant(const kv_quant_pool_desc *pool, int32_t layer,
+                                     const kv_attn_desc *attn, int64_t total_q, int32_t num_heads,
+                                     const void *d_q, int64_t q_tok_stride, int64_t q_head_stride,
+                                     const float *d_lse, float *d_weights, int64_t weight_stride,
+                                     float keep, void *d_workspace, size_t workspace_bytes,
+                                     kv_stream_t stream)
+{
+    t_launches = 0;
+    if (!quant_pool_ok(pool) || layer < 0 || layer >= pool->num_layers)
+        return KV_ERR_INVALID_ARG;
+    RowKind kind;
+    if (!quant_row_kind(pool, &kind))
+        return KV_ERR_UNSUPPORTED;
+    const QuantView v = quant_view(pool, layer);
+    AttnParams p{};
+    p.copy = v.copy;
+    p.rot = v.rot;
+    p.copy_ss = v.copy_ss;
+    p.rot_ss = v.rot_ss;
+    p.cs = v.cs;
+    p.cs_ss = v.cs_ss;
+    p.rs = v.rs;
+    p.rs_ss = v.rs_ss;
+    return weights_impl(p, kind, pool->num_slots, pool->block_size, pool->rot_heads, attn, total_q,
+                        num_heads, d_q, q_tok_stride, q_head_stride, d_lse, d_weights,
+                        weight_stride, keep, d_workspace, workspace_bytes,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+} // extern "C"
+
+// ---------------------------------------------------------------------------
+// Which tokens stay
+// ---------------------------------------------------------------------------
+
+namespace {
+
+constexpr int32_t kMaxSelect = 1 << 30; // tokens of a sequence, counted in 32 bits
+
+} // namespace
+
+extern "C" {
+
+size_t kv_evict_workspace_size(int32_t num_seqs, int32_t max_kv_len)
+{
+    if (num_seqs < 0 || max_kv_len < 0 || max_kv_len > kMaxSelect)
+        return 0;
+    const size_t blocks = (size_t)num_seqs * select_cluster(num_seqs, max_kv_len);
+    return blocks > 0x7FFFFFFFu ? 0 : align256(kHeaderBytes + blocks * 4u);
+}
+
+kv_status kv_evict_select(int32_t num_seqs, const float *d_weights, int64_t weight_stride,
+                          const int32_t *d_kv_len, int32_t max_kv_len, const int32_t *d_budget,
+                          int32_t sinks, int32_t recent, int32_t *d_keep, int64_t keep_stride,
+                          int32_t max_keep, int32_t *d_count, float *d_kept_weights,
+                          int64_t kept_stride, void *d_workspace, size_t workspace_bytes,
+                          kv_stream_t stream_)
+{
+    t_launches = 0;
+    const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const size_t need = kv_evict_workspace_size(num_seqs, max_kv_len);
+    if (need == 0 || sinks < 0 || recent < 0 || max_keep < 0 || weight_stride < max_kv_len ||
+        keep_stride < max_keep || (d_kept_weights && kept_stride < max_keep))
+        return KV_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!d_kv_len || !d_budget || !d_count || (max_kv_len > 0 && !d_weights) ||
+                         (max_keep > 0 && !d_keep)))
+        return KV_ERR_INVALID_ARG;
+    for (const void *a : {static_cast<const void *>(d_weights), static_cast<const void *>(d_kv_len),
+                          static_cast<const void *>(d_budget), static_cast<const void *>(d_keep),
+                          static_cast<const void *>(d_count),
+                          static_cast<const void *>(d_kept_weights)})
+        if (!aligned_to(a, 4))
+            return KV_ERR_INVALID_ARG;
+    kv_status st = ws_ok(d_workspace, workspace_bytes, need);
+    if (st != KV_OK)
+        return st;
+    if (num_seqs == 0) {
+        KV_CUDA(cudaMemsetAsync(d_workspace, 0, kHeaderBytes, stream));
+        return KV_OK;
+    }
+    SelectParams p{};
+    p.weights = d_weights;
+    p.weight_stride = weight_stride;
+    p.kv_len = d_kv_len;
+    p.budget = d_budget;
+    p.num_seqs = num_seqs;
+    p.max_kv_len = max_kv_len;
+    p.sinks = sinks;
+    p.recent = recent;
+    p.keep = d_keep;
+    p.keep_stride = keep_stride;
+    p.max_keep = max_keep;
+    p.count = d_count;
+    p.kept = d_kept_weights;
+    p.kept_stride = kept_stride;
+    p.cluster = select_cluster(num_seqs, max_kv_len);
+    p.header = static_cast<uint32_t *>(d_workspace);
+    KV_CUDA(mark(t_ev_start, stream));
+    KV_CUDA(launch_select(p, stream));
+    ++t_launches;
+    KV_CUDA(mark(t_ev_stop, stream));
+    return KV_OK;
+}
+
+} // extern "C"
+
+// ---------------------------------------------------------------------------
+// Rows that close up in place
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// Workspace: header, the units' read counters, the cos / sin tables.
+struct CompactLayout {
+    int64_t tiles, units; // of a sequence; of the call
+    int32_t groups, per;  // layer groups, layers of one
+    int32_t bits, lo_rows, hi_rows;
+    size_t table, bytes;
+};
+
+// False: sizes beyond what the kernel counts.
+bool compact_layout(RowKind kind, bool quant, int32_t layers, int32_t block, int32_t half,
+                    int32_t num_seqs, int32_t max_blocks, int32_t max_count, CompactLayout *l)
+{
+    const int32_t rows = compact_tile_rows(kind, quant);
+    l->tiles = ((int64_t)max_count + rows - 1) / rows;
+    const int64_t units = std::max<int64_t>(1, l->tiles * num_seqs);
+    // layer groups as in kv_splice: enough units for about kUnitsTarget blocks
+    const int64_t want = std::min<int64_t>(layers, (kUnitsTarget + units - 1) / units);
+    l->per = (int32_t)((layers + want - 1) / want);
+    l->groups = (layers + l->per - 1) / l->per;
+    l->units = l->tiles * num_seqs * l->groups;
+    if (l->units > 0x7FFFFFFFll)
+        return false;
+    // shifts are below the last position of a block-table row
+    const int64_t most = std::min<int64_t>((int64_t)max_blocks * block, 0x7FFFFFFFll);
+    l->bits = 0;
+    while (((int64_t)1 << (2 * l->bits)) < most)
+        ++l->bits;
+    l->lo_rows = 1 << l->bits;
+    l->hi_rows = (int32_t)(most >> l->bits) + 1;
+    l->table = align256(kHeaderBytes + (size_t)l->units * 4u);
+    l->bytes = align256(l->table + (size_t)(l->lo_rows + l->hi_rows) * half * sizeof(float4));
+    return true;
+}
+
+bool compact_sizes_ok(int32_t num_seqs, int32_t max_blocks, int32_t max_count)
+{
+    return num_seqs >= 0 && max_blocks >= 0 && max_count >= 0;
+}
+
+kv_status compact_impl(const CompactParams &rows, RowKind kind, double base, int32_t head_dim,
+                       int32_t num_seqs, const int32_t *block_tables, int32_t max_blocks,
+                       const int32_t *first, const int32_t *keep, int64_t keep_stride,
+                       const int32_t *count, int32_t max_count, bool rotate, void *ws,
+                       size_t ws_bytes, cudaStream_t stream)
+{
+    if (!compact_sizes_ok(num_seqs, max_blocks, max_count) || keep_stride < max_count)
+        return KV_ERR_INVALID_ARG;
+    const bool any = num_seqs > 0 && max_count > 0;
+    if (any && (!block_tables || max_blocks == 0 || !keep || !count))
+        return KV_ERR_INVALID_ARG;
+    for (const void *a : {static_cast<const void *>(block_tables), static_cast<const void *>(first),
+                          static_cast<const void *>(keep), static_cast<const void *>(count)})
+        if (!aligned_to(a, 4))
+            return KV_ERR_INVALID_ARG;
+    CompactLayout l;
+    if (!compact_layout(kind, rows.cs != nullptr, rows.pool.num_layers, rows.pool.block,
+                        head_dim / 2, num_seqs, max_blocks, max_count, &l))
+        return KV_ERR_INVALID_ARG;
+    kv_status st = ws_ok(ws, ws_bytes, l.bytes);
+    if (st != KV_OK)
+        return st;
+    char *const w = static_cast<char *>(ws);
+    KV_CUDA(cudaMemsetAsync(w, 0, kHeaderBytes + (any ? (size_t)l.units * 4u : 0u), stream));
+    if (!any)
+        return KV_OK;
+    CompactParams p = rows;
+    p.block_tables = block_tables;
+    p.max_blocks = max_blocks;
+    p.num_seqs = num_seqs;
+    p.first = first;
+    p.keep = keep;
+    p.keep_stride = keep_stride;
+    p.count = count;
+    p.max_count = max_count;
+    p.layer_groups = l.groups;
+    p.group_layers = l.per;
+    p.status = reinterpret_cast<uint32_t *>(w);
+    p.ticket = p.status + 1;
+    p.flags = reinterpret_cast<uint32_t *>(w + kHeaderBytes);
+    p.wait_limit_ns = g_wait_limit_ns.load();
+    p.skip_publish = g_skip_publish.load();
+    if (rotate) {
+        TurnParams tp{};
+        tp.base = base;
+        tp.half = head_dim / 2;
+        tp.bits = l.bits;
+        tp.lo_rows = l.lo_rows;
+        tp.hi_rows = l.hi_rows;
+        tp.table = reinterpret_cast<float4 *>(w + l.table);
+        KV_CUDA(launch_turn_table(tp, stream));
+        ++t_launches;
+        p.turn_lo = tp.table;
+        p.turn_hi = tp.table + (int64_t)l.lo_rows * tp.half;
+        p.turn_bits = l.bits;
+        p.turn_half = tp.half;
+    }
+    KV_CUDA(mark(t_ev_start, stream));
+    KV_CUDA(launch_compact(p, kind, l.units, stream));
+    ++t_launches;
+    KV_CUDA(mark(t_ev_stop, stream));
+    return KV_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+size_t kv_compact_workspace_size(const kv_pool_desc *pool, int32_t num_seqs, int32_t max_blocks,
+                                 int32_t max_count)
+{
+    RowKind kind;
+    CompactLayout l;
+    if (!pool_ok(pool) || !row_kind(pool, &kind) ||
+        !compact_sizes_ok(num_seqs, max_blocks, max_count) ||
+        !compact_layout(kind, false, pool->num_layers, pool->block_size, pool->rot_head_dim / 2,
+                        num_seqs, max_blocks, max_count, &l))
+        return 0;
+    return l.bytes;
+}
+
+size_t kv_compact_quant_workspace_size(const kv_quant_pool_desc *pool, int32_t num_seqs,
+                                       int32_t max_blocks, int32_t max_count)
+{
+    RowKind kind;
+    CompactLayout l;
+    if (!quant_pool_ok(pool) || !quant_row_kind(pool, &kind) ||
+        !compact_sizes_ok(num_seqs, max_blocks, max_count) ||
+        !compact_layout(kind, true, pool->num_layers, pool->block_size, pool->rot_head_dim / 2,
+                        num_seqs, max_blocks, max_count, &l))
+        return 0;
+    return l.bytes;
+}
+
+kv_status kv_compact(const kv_pool_desc *pool, int32_t num_seqs, const int32_t *d_block_tables,
+                     int32_t max_blocks, const int32_t *d_first, const int32_t *d_keep,
+                     int64_t keep_stride, const int32_t *d_count, int32_t max_count,
+                     int32_t rotate, void *d_workspace, size_t workspace_bytes, kv_stream_t stream)
+{
+    t_launches = 0;
+    if (!pool_ok(pool) || (rotate != 0 && rotate != 1))
+        return KV_ERR_INVALID_ARG;
+    RowKind kind;
+    if (!row_kind(pool, &kind))
+        return KV_ERR_UNSUPPORTED;
+    CompactParams p{};
+    p.pool = view_of(pool);
+    return compact_impl(p, kind, pool->rope_base, pool->rot_head_dim, num_seqs, d_block_tables,
+                        max_blocks, d_first, d_keep, keep_stride, d_count, max_count, rotate != 0,
+                        d_workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+kv_status kv_compact_quant(const kv_quant_pool_desc *pool, int32_t num_seqs,
+                           const int32_t *d_block_tables, int32_t max_blocks,
+                           const int32_t *d_first, const int32_t *d_keep, int64_t keep_stride,
+                           const int32_t *d_count, int32_t max_count, double rope_base,
+                           int32_t pair_convention, void *d_workspace, size_t workspace_bytes,
+                           kv_stream_t stream)
+{
+    t_launches = 0;
+    if (!quant_pool_ok(pool) || !(rope_base >= 0.0) || !(rope_base < INFINITY) ||
+        (pair_convention != 0 && pair_convention != 1))
+        return KV_ERR_INVALID_ARG;
+    RowKind kind;
+    if (!quant_row_kind(pool, &kind) || (rope_base > 0.0 && kind != RowKind::Mla))
+        return KV_ERR_UNSUPPORTED;
+    const QuantView v = quant_view(pool, 0);
+    CompactParams p{};
+    p.pool.copy = v.copy;
+    p.pool.copy_ls = v.copy_ls;
+    p.pool.copy_ss = v.copy_ss;
+    p.pool.rot = v.rot;
+    p.pool.rot_ls = v.rot_ls;
+    p.pool.rot_ss = v.rot_ss;
+    p.pool.num_slots = pool->num_slots;
+    p.pool.num_blocks = pool->num_slots / pool->block_size;
+    p.pool.block = pool->block_size;
+    p.pool.num_layers = pool->num_layers;
+    p.pool.il = pair_convention;
+    p.cs = v.cs;
+    p.cs_ls = v.cs_ls;
+    p.cs_ss = v.cs_ss;
+    p.rs = v.rs;
+    p.rs_ls = v.rs_ls;
+    p.rs_ss = v.rs_ss;
+    return compact_impl(p, kind, rope_base, pool->rot_head_dim, num_seqs, d_block_tables,
+                        max_blocks, d_first, d_keep, keep_stride, d_count, max_count,
+                        rope_base > 0.0, d_workspace, workspace_bytes,
+                        reinterpret_cast<cudaStream_t>(stream));
 }
 
 } // extern "C"

@@ -1001,7 +1001,8 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
     const int hi = !valid ? 0 : p.causal ? min(w.len, pos + 1) : w.len;
     const int lo = p.window ? max(0, pos - p.window + 1) : 0;
     const int sk = p.window ? min(p.sinks, hi) : 0;
-    const bool one_token = G::NT == 1 && m.pos0 == m.pos1;
+    // no key is seen by some rows only
+    const bool one_token = G::NT == 1 && m.pos0 == m.pos1 && !p.tree;
     const float c = p.scale * 1.4426950408889634f;
     const uint32_t o_col = tmem + G::O_COL(t) + half * HO + lanes;
     bool partial = false;
@@ -1030,7 +1031,9 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
 #pragma unroll
             for (int i = 0; i < HK; i += 32) { // a bit per key that is seen
                 const int k0 = kt * KT + half * HK + i;
-                const uint32_t see = below(hi - k0) & (~below(lo - k0) | below(sk - k0));
+                uint32_t see = below(hi - k0) & (~below(lo - k0) | below(sk - k0));
+                if (p.tree && valid)
+                    see &= tree_bits(p, w.q0 + tok, w.len - w.n, k0);
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     s[i + j] = (see >> j) & 1u ? s[i + j] : 0xFF800000u;
@@ -1209,6 +1212,8 @@ __device__ __forceinline__ void store_rows(const AttnParams &p, const Work &w, c
                 const int k0 = real_tile(w, v) * KT;
                 for (int k = k0; k < k0 + KT; ++k) {
                     if (!valid || !(k < hi && (k >= lo || k < sk)))
+                        continue;
+                    if (p.tree && !(tree_bits(p, w.q0 + tok, w.len - w.n, k) & 1u))
                         continue;
                     bool bad = false;
                     const int64_t s = key_slot(p, w, k, key_block(p, w, k), bad);
@@ -1539,7 +1544,7 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
     const bool mla = kind == RowKind::Mla;
     const int64_t kt = mla ? 64 : 128;
     AttnPlan pl{};
-    const bool few = !mla && a.max_q_len <= 1 && a.group <= kFewRows;
+    const bool few = !mla && a.max_q_len <= 1 && a.group <= kFewRows && !a.tree;
     // More than one row tile to a sequence: e4m3 rows are widened once, in a pass of
     // their own, where the workspace for that stays moderate.  8 chunks of up to 513
     // tokens x 28 heads: 265 us when every tile widened them; an MLA batch 372 us.

@@ -47,12 +47,27 @@ __device__ __forceinline__ TileMask tile_mask(const AttnParams &p, int n, int le
     const int i1 = p.by_group.quotient(row0 + max(m.rows, 1) - 1);
     m.pos0 = len - n + i0;
     m.pos1 = len - n + i1;
-    m.hi0 = p.causal ? max(0, min(len, m.pos0 + 1)) : len;
+    // every token of a tree sees the keys before the new ones
+    m.hi0 = p.tree ? max(0, len - n) : p.causal ? max(0, min(len, m.pos0 + 1)) : len;
     m.hi1 = p.causal ? max(0, min(len, m.pos1 + 1)) : len;
     m.lo0 = p.window ? max(0, m.pos0 - p.window + 1) : 0;
     m.lo1 = p.window ? max(0, m.pos1 - p.window + 1) : 0;
     m.sk = p.window ? min(p.sinks, m.lo1) : 0;
     return m;
+}
+
+// Keys [k, k + 32) that new token `tok` of a sequence's tree sees, a bit each: those before
+// the new tokens (from `base` on) and what its mask says.
+__device__ __forceinline__ uint32_t tree_bits(const AttnParams &p, int64_t tok, int base, int k)
+{
+    const int64_t b = (int64_t)k - base; // the mask's bit of key k
+    if (b <= -32)
+        return ~0u;
+    const uint32_t *const words = p.tree + tok * p.tree_stride;
+    auto word = [&](int64_t i) { return i < p.tree_words ? __ldg(words + i) : 0u; };
+    if (b < 0)
+        return word(0) << (uint32_t)-b | ((1u << (uint32_t)-b) - 1u);
+    return __funnelshift_r(word(b >> 5), word((b >> 5) + 1), (uint32_t)b & 31u);
 }
 
 // Key tile kt has a key that some row of the tile sees.
@@ -460,10 +475,8 @@ __device__ __forceinline__ void join_row(int splits, int lane, char *out, float 
         *out_lse = sum == 0.0f ? -INFINITY : ref + logf(sum);
 }
 
-// Tensor map of one part of the pool's rows (`width` columns of bf16 or bytes): boxes
-// of 128 bytes and p.box_rows rows, swizzled as the MMAs read them.
-inline bool encode_map(CUtensorMap *map, const char *base, int64_t row_bytes, int64_t rows, int width,
-                int box_rows, bool bytes)
+// The driver's function that makes tensor maps (nullptr: there is none).
+inline PFN_cuTensorMapEncodeTiled_v12000 map_encoder()
 {
     static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         void *f = nullptr;
@@ -474,6 +487,15 @@ inline bool encode_map(CUtensorMap *map, const char *base, int64_t row_bytes, in
             f = nullptr;
         return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     }();
+    return encode;
+}
+
+// Tensor map of one part of the pool's rows (`width` columns of bf16 or bytes): boxes
+// of 128 bytes and p.box_rows rows, swizzled as the MMAs read them.
+inline bool encode_map(CUtensorMap *map, const char *base, int64_t row_bytes, int64_t rows, int width,
+                int box_rows, bool bytes)
+{
+    const auto encode = map_encoder();
     if (!encode)
         return false;
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};

@@ -1,0 +1,351 @@
+// kv_compact.cu -- rows that stay in a cache close up, in place.
+//
+// Row i of a sequence's list moves from position first + keep[i] to first + i: its
+// verbatim part (and scales) as it is, its rotary part turned by R(i - keep[i]) where the
+// call asks for it.  The list ascends, so keep[i] >= i: rows only move down.
+//
+// Order.  Tile k writes positions [k T, k T + T) (from first on), which earlier tiles may
+// still have to read: those whose rows lie there, at most T of them, so at most two tiles
+// besides itself.  Tickets are drawn in the order of tiles, every tile reads its rows
+// without waiting, publishes that for each layer, and waits (bounded) for those tiles before
+// it writes the layer: the protocol of the splices (kv_splice.cu), with the shift of every
+// row taken from the list.  A ninth warp, which moves no rows, looks the tiles up in
+// the list, publishes and waits.
+//
+// Rotation.  Every row has a shift of its own, so cos and sin of m θ_j, m = keep[i] - i, come
+// from two small tables, m = a 2^b + c: (cos, sin)(a 2^b θ) and (cos, sin)(c θ), formed in
+// fp64 and held as pairs of fp32 (48 bits), multiplied as complex numbers in pairs of fp32.
+// That costs a tile some 30 fp32 operations an entry, once for all layers; fp64 sincos of
+// every row took longer than moving it.
+//
+// Bound: HBM, one read and one write of every row that moves.
+#include <algorithm>
+
+#include "kv_serve.h"
+#include "kv_tiles.cuh"
+
+namespace kvr {
+
+namespace {
+
+constexpr uint32_t kMoveWarps = kThreads / 32;
+constexpr int kMoveThreads = kThreads + 32; // the row-moving warps, and one that publishes
+constexpr int kMoveMinBlocks = 3;
+constexpr uint32_t kReadBar = 1; // named barrier: the warps' loads of a layer have landed
+
+// 8-bit rows in tiles: half the bytes, so about twice the rows of a bf16 tile; the 128 bytes
+// of a head count as its two "halves" and are moved as they are.
+using GeoMla8 = Geo<64, 32, 1, 4, 3>;
+using GeoGqa8 = Geo<16, 64, 8, 4, 3>;
+using GeoGqa48 = Geo<32, 32, 4, 4, 3>;
+using GeoMha8 = Geo<4, 256, 32, 4, 3>;
+
+template <class F>
+cudaError_t with_move_geo(RowKind kind, bool quant, F &&f)
+{
+    if (!quant)
+        return with_inplace_geo(kind, f);
+    switch (kind) {
+    case RowKind::Mla:
+        return f(GeoTag<GeoMla8>{});
+    case RowKind::Gqa:
+        return f(GeoTag<GeoGqa8>{});
+    case RowKind::Gqa4:
+        return f(GeoTag<GeoGqa48>{});
+    case RowKind::Mha:
+        return f(GeoTag<GeoMha8>{});
+    }
+    return cudaErrorInvalidValue;
+}
+
+// A number as the sum of two fp32, and products and sums of such (Dekker, A floating-point
+// technique for extending the available precision, 1971; with a fused product).
+struct Pair {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Pair pair_of(float hi, float lo)
+{
+    const float s = hi + lo;
+    return {s, lo - (s - hi)};
+}
+
+__device__ __forceinline__ Pair operator*(Pair a, Pair b)
+{
+    const float p = __fmul_rn(a.hi, b.hi);
+    float e = fmaf(a.hi, b.hi, -p);
+    e = fmaf(a.hi, b.lo, e);
+    e = fmaf(a.lo, b.hi, e);
+    return pair_of(p, e);
+}
+
+__device__ __forceinline__ Pair operator+(Pair a, Pair b)
+{
+    float s, e;
+    two_sum(a.hi, b.hi, s, e);
+    return pair_of(s, e + (a.lo + b.lo));
+}
+
+__device__ __forceinline__ Pair operator-(Pair a) { return {-a.hi, -a.lo}; }
+
+// The two parts that the rotation wants: 16 leading bits, and the rest.
+__device__ __forceinline__ void lead_parts(Pair a, float &x, float &y)
+{
+    x = __uint_as_float(__float_as_uint(a.hi) & 0xFFFFFF00u);
+    y = (a.hi - x) + a.lo;
+}
+
+// Table entry of R(-m) at frequency j.
+__device__ __forceinline__ float4 turn_entry(const CompactParams &p, int32_t m, int j)
+{
+    const float4 a = __ldg(p.turn_hi + (int64_t)(m >> p.turn_bits) * p.turn_half + j);
+    const float4 b = __ldg(p.turn_lo + (int64_t)(m & ((1 << p.turn_bits) - 1)) * p.turn_half + j);
+    const Pair ca{a.x, a.y}, sa{a.z, a.w}, cb{b.x, b.y}, sb{b.z, b.w};
+    const Pair c = ca * cb + -(sa * sb), s = -(sa * cb + ca * sb);
+    float4 r;
+    lead_parts(c, r.x, r.y);
+    lead_parts(s, r.z, r.w);
+    return r;
+}
+
+// First of the list's entries [0, n) that is not below x, by one warp.
+__device__ __forceinline__ int first_not_below(const int32_t *list, int n, int64_t x, int lane)
+{
+    int lo = 0; // entries before lo are below x, those from n on are not
+    while (n > lo) {
+        const int step = (n - lo + 31) / 32, at = lo + lane * step;
+        const uint32_t below = __ballot_sync(0xFFFFFFFFu, at < n && __ldg(list + at) < x);
+        const int c = __popc(below); // probes are in order: the first c are below
+        if (c == 0)
+            break; // list[lo] is not
+        if (step == 1)
+            return lo + c;
+        const int from = lo + (c - 1) * step + 1;
+        n = min(n, lo + c * step);
+        lo = from;
+    }
+    return lo;
+}
+
+template <class G, bool IL, bool QUANT>
+__global__ void __launch_bounds__(kMoveThreads, kMoveMinBlocks) compact_kernel(
+    const __grid_constant__ CompactParams p)
+{
+    constexpr bool TURNS = !QUANT || G::NH == 1; // e4m3 heads are not turned
+    constexpr bool PACKED = CsOrder<G, false, IL>::kPacked;
+    // scales of a row, and how many a thread moves
+    constexpr int CS = G::CV / 8, RS = G::NH == 1 ? 0 : G::NH, NS = CS + RS;
+    constexpr int SPER = (G::T * NS + kThreads - 1) / kThreads;
+    __shared__ uint32_t s_ticket;
+    __shared__ volatile int32_t s_abort; // 0 -> 1 once a wait ran out; never reset
+    __shared__ int64_t s_src[G::T], s_dst[G::T];
+    __shared__ int32_t s_ident[G::T], s_shift[G::T];
+    __shared__ float4 s_cs[TURNS ? G::T * G::kCsRow : 1];
+    __shared__ uint32_t s_sink;
+
+    const int tid = threadIdx.x;
+    if (tid == 0) {
+        s_ticket = atomicAdd(p.ticket, 1u);
+        s_abort = 0;
+    }
+    __syncthreads();
+    // layer group g of tile k of sequence q
+    const int64_t t = s_ticket, u = t / p.layer_groups;
+    const int g = (int)(t - u * p.layer_groups);
+    const int64_t k = u / p.num_seqs;
+    const int q = (int)(u - k * p.num_seqs);
+    const int l0 = g * p.group_layers, l1 = min(p.pool.num_layers, l0 + p.group_layers);
+    const int32_t count = __ldg(p.count + q), first = p.first ? __ldg(p.first + q) : 0;
+    if (count < 0 || count > p.max_count || first < 0) {
+        if (k == 0 && tid == 0)
+            set_status(p.status, kStatusOutOfRange);
+        return;
+    }
+    const int64_t lo = k * G::T, hi = min(lo + (int64_t)G::T, (int64_t)count);
+    if (lo >= hi)
+        return;
+    const int32_t *const keep = p.keep + q * p.keep_stride;
+    uint32_t *const flags = p.flags + (int64_t)q * p.layer_groups + g; // tile j: + j * flag_step
+    const int64_t flag_step = (int64_t)p.num_seqs * p.layer_groups;
+    if (__ldg(keep + hi - 1) == hi - 1) { // ascending: nothing up to here moves
+        if (tid == 0)
+            red_release_add(flags + k * flag_step, kMoveWarps * (uint32_t)(l1 - l0));
+        return;
+    }
+    if (tid < G::T) {
+        int64_t src = -1, dst = -1;
+        int32_t shift = 0;
+        const int64_t i = lo + tid;
+        if (i < hi) {
+            const int32_t *bt = p.block_tables + (int64_t)q * p.max_blocks;
+            const int32_t from = __ldg(keep + i), before = i > 0 ? __ldg(keep + i - 1) : -1;
+            if (from <= before || from < i) {
+                set_status(p.status, kStatusOutOfRange);
+            } else if (from > i) {
+                src = slot_of(bt, p.max_blocks, p.pool.block, p.pool.num_blocks,
+                              (int64_t)first + from);
+                dst = slot_of(bt, p.max_blocks, p.pool.block, p.pool.num_blocks, first + i);
+                shift = from - (int32_t)i;
+                if (src < 0 || dst < 0) {
+                    set_status(p.status, kStatusOutOfRange);
+                    src = dst = -1;
+                }
+            }
+        }
+        s_src[tid] = src;
+        s_dst[tid] = dst;
+        s_shift[tid] = shift;
+        s_ident[tid] = !TURNS || p.turn_lo == nullptr;
+    }
+    __syncthreads();
+
+    if (tid >= kThreads) {
+        const int lane = tid & 31;
+        // earlier tiles with rows in [lo, hi)
+        const int a = first_not_below(keep, (int)hi, lo, lane);
+        const int b = first_not_below(keep, (int)hi, hi, lane);
+        int64_t dep[2] = {-1, -1};
+        if (a < b) {
+            const int64_t j0 = a / G::T, j1 = (b - 1) / G::T;
+            if (j0 < k)
+                dep[0] = j0;
+            if (j1 > j0 && j1 < k)
+                dep[1] = j1;
+        }
+        uint32_t seen[2] = {0, 0};
+        for (int l = l0; l < l1; ++l) {
+            bar_wait_all(kReadBar, kMoveThreads);
+            if (lane == 0) {
+                if (t != p.skip_publish)
+                    red_release_add(flags + k * flag_step, kMoveWarps);
+                const uint32_t want = ((uint32_t)(l - l0) + 1u) * kMoveWarps;
+                for (int d = 0; d < 2 && !s_abort; ++d) {
+                    if (dep[d] < 0 || seen[d] >= want)
+                        continue;
+                    seen[d] = wait_count(flags + dep[d] * flag_step, want, p.wait_limit_ns);
+                    if (seen[d] < want) {
+                        set_status(p.status, kStatusTimeout);
+                        s_abort = 1;
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        return;
+    }
+    const PatchAt none{nullptr, 0, nullptr, nullptr};
+    for (int l = l0; l < l1; ++l) {
+        const RowsAt at{p.pool.copy + l * p.pool.copy_ls, p.pool.copy_ss,
+                        p.pool.rot + l * p.pool.rot_ls, p.pool.rot_ss};
+        TileRegs<G> regs;
+        float scale[SPER];
+        uint32_t f = 0;
+        if (!s_abort)
+            load_tile<G>(at, s_src, regs);
+        else
+            regs = TileRegs<G>{};
+        auto scale_of = [&](int i, const int64_t *slots) -> float * {
+            const int64_t s = i < G::T * NS ? slots[i / NS] : -1;
+            const int v = i % NS;
+            return s < 0 ? nullptr
+                   : v < CS ? p.cs + l * p.cs_ls + s * p.cs_ss + v
+                            : p.rs + l * p.rs_ls + s * p.rs_ss + (v - CS);
+        };
+        if constexpr (QUANT) {
+#pragma unroll
+            for (int i = 0; i < SPER; ++i) {
+                const float *from = scale_of(threadIdx.x + i * kThreads, s_src);
+                scale[i] = from && !s_abort ? *from : 0.0f;
+                f ^= __float_as_uint(scale[i]);
+            }
+        }
+        if constexpr (TURNS) {
+            if (l == l0 && p.turn_lo)
+                for (int i = tid; i < G::T * G::kHalf; i += kThreads) {
+                    const int r = i / G::kHalf, j = i % G::kHalf;
+                    if (s_src[r] >= 0)
+                        stage_cs<G, PACKED>(s_cs + r * G::kCsRow, j, turn_entry(p, s_shift[r], j));
+                }
+        }
+        // every load completes before the barrier (see fold_tile)
+        f ^= fold_tile<G>(regs);
+        if (p.num_seqs < 0)
+            s_sink = f;
+        bar_arrive(kReadBar, kMoveThreads);
+        __syncthreads();
+        if (!s_abort) {
+            store_tile<G, false, true, IL>(at, s_dst, regs, s_cs, TURNS ? G::kCsRow : 0, s_ident,
+                                           none);
+            if constexpr (QUANT) {
+#pragma unroll
+                for (int i = 0; i < SPER; ++i)
+                    if (float *to = scale_of(threadIdx.x + i * kThreads, s_dst))
+                        *to = scale[i];
+            }
+        }
+    }
+}
+
+// Rows n of turn_lo (n θ_j) and of turn_hi (n 2^bits θ_j).
+__global__ void __launch_bounds__(256) turn_kernel(const __grid_constant__ TurnParams p)
+{
+    __shared__ double s_theta[64];
+    if (threadIdx.x < p.half)
+        s_theta[threadIdx.x] = pow(p.base, -2.0 * (double)threadIdx.x / (double)(2 * p.half));
+    __syncthreads();
+    const int per = 256 / p.half, j = threadIdx.x % p.half;
+    const int row = blockIdx.x * per + threadIdx.x / p.half;
+    if (threadIdx.x / p.half >= per || row >= p.lo_rows + p.hi_rows)
+        return;
+    const bool high = row >= p.lo_rows;
+    const int64_t n = high ? (int64_t)(row - p.lo_rows) << p.bits : row;
+    double s, c;
+    sincos((double)n * s_theta[j], &s, &c);
+    const float ch = (float)c, sh = (float)s;
+    p.table[(int64_t)row * p.half + j] =
+        make_float4(ch, (float)(c - ch), sh, (float)(s - sh));
+}
+
+} // namespace
+
+int compact_tile_rows(RowKind kind, bool quant)
+{
+    int rows = 0;
+    with_move_geo(kind, quant, [&](auto g) {
+        rows = decltype(g)::type::T;
+        return cudaSuccess;
+    });
+    return rows;
+}
+
+cudaError_t launch_turn_table(const TurnParams &p, cudaStream_t stream)
+{
+    const int per = 256 / p.half, rows = p.lo_rows + p.hi_rows;
+    turn_kernel<<<(unsigned)((rows + per - 1) / per), 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_compact(const CompactParams &p, RowKind kind, int64_t tickets,
+                           cudaStream_t stream)
+{
+    const bool quant = p.cs != nullptr;
+    return with_move_geo(kind, quant, [&](auto g) {
+        using G = typename decltype(g)::type;
+        const unsigned n = (unsigned)tickets;
+        if (quant) {
+            if constexpr (G::NH == 1) {
+                if (p.pool.il) {
+                    compact_kernel<G, true, true><<<n, kMoveThreads, 0, stream>>>(p);
+                    return cudaGetLastError();
+                }
+            }
+            compact_kernel<G, false, true><<<n, kMoveThreads, 0, stream>>>(p);
+        } else if (p.pool.il)
+            compact_kernel<G, true, false><<<n, kMoveThreads, 0, stream>>>(p);
+        else
+            compact_kernel<G, false, false><<<n, kMoveThreads, 0, stream>>>(p);
+        return cudaGetLastError();
+    });
+}
+
+} // namespace kvr

@@ -121,6 +121,10 @@ struct AttnParams {
     int64_t max_keys; // that a block-table row of the caller holds
     const int32_t *q_off, *kv_len, *block_tables;
     int32_t causal, window, sinks;
+    // drafted trees (causal and window are 0): bit j of a query's words: it sees new token j
+    const uint32_t *tree; // nullptr: none
+    int64_t tree_stride;  // words
+    int32_t tree_words;
     float scale;
     // split of the key axis, and the parts that are joined afterwards: of few rows
     // [max_splits][total_q][heads][value width], lse [..][heads]
@@ -143,7 +147,7 @@ struct AttnParams {
 
 // Sizes of a call that the host knows, and the launch they lead to.
 struct AttnShape {
-    bool quant;
+    bool quant, tree;
     int64_t total_q;
     int32_t num_seqs, max_q_len, max_kv_len, window, sinks;
     int32_t group, kv_heads;
@@ -160,6 +164,82 @@ struct AttnPlan {
 
     bool joins() const { return slices || (max_splits > 1 && !cluster); }
 };
+
+// Rows that close up in place (kv_compact.cu).
+struct CompactParams {
+    PoolView pool; // bytes of either kind of pool
+    float *cs, *rs; // scales of a quantised pool (cs == nullptr: bf16)
+    int64_t cs_ls, cs_ss, rs_ls, rs_ss;
+    const int32_t *block_tables;
+    int32_t max_blocks, num_seqs;
+    const int32_t *first; // nullptr: 0
+    const int32_t *keep;  // [num_seqs][max_count], keep_stride apart
+    int64_t keep_stride;
+    const int32_t *count;
+    int32_t max_count;
+    int32_t layer_groups, group_layers; // a tile's layers are cut into this many units
+    const float4 *turn_lo, *turn_hi;    // cos / sin tables (nullptr: rows are not turned)
+    int32_t turn_bits, turn_half;
+    uint32_t *status, *ticket, *flags; // flags: [tiles][num_seqs][layer_groups]
+    int64_t wait_limit_ns;
+    int64_t skip_publish; // test hook: this ticket does not publish its reads (-1: none)
+};
+
+struct TurnParams {
+    double base;
+    int32_t half, bits, lo_rows, hi_rows;
+    float4 *table; // lo_rows of turn_lo, then hi_rows of turn_hi
+};
+
+int compact_tile_rows(RowKind kind, bool quant);
+cudaError_t launch_turn_table(const TurnParams &p, cudaStream_t stream);
+cudaError_t launch_compact(const CompactParams &p, RowKind kind, int64_t tickets,
+                           cudaStream_t stream);
+
+// Which tokens stay (kv_select.cu).
+struct SelectParams {
+    const float *weights; // [num_seqs][max_kv_len], weight_stride apart
+    int64_t weight_stride;
+    const int32_t *kv_len, *budget;
+    int32_t num_seqs, max_kv_len, sinks, recent;
+    int32_t *keep;        // [num_seqs][max_keep], keep_stride apart
+    int64_t keep_stride;
+    int32_t max_keep;
+    int32_t *count;
+    float *kept;          // nullptr: not wanted
+    int64_t kept_stride;
+    int32_t cluster;      // blocks of a sequence
+    uint32_t *header;
+};
+
+int select_cluster(int32_t num_seqs, int32_t max_kv_len);
+cudaError_t launch_select(const SelectParams &p, cudaStream_t stream);
+
+// What each key receives of the queries' attention (kv_weights.cu).
+struct WeightsParams {
+    AttnParams a; // the batch, its pool and its queries; out and the split have no part
+    const float *lse;
+    float *weights;
+    int64_t weight_stride;
+    float keep;
+    int32_t toks, rows, n; // of a row tile: tokens; rows; rows with those that pad it
+    int32_t parts;         // blocks of a cluster: they divide a key tile's row tiles and heads
+    int32_t stages;
+    int32_t q_boxes;       // query rows come as boxes of q_map
+    Divisor by_toks;
+    CUtensorMap q_map;
+};
+
+struct WeightsPlan {
+    bool hold;         // two key tiles to a block, held while the queries pass
+    int32_t toks, rows, n, parts, stages;
+    int64_t blocks;
+    int32_t smem;
+};
+
+WeightsPlan plan_weights(RowKind kind, const AttnShape &a);
+cudaError_t launch_weights(WeightsParams &p, RowKind kind, const WeightsPlan &pl,
+                           cudaStream_t stream);
 
 AttnPlan plan_attention(RowKind kind, const AttnShape &a);
 cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cudaStream_t stream);

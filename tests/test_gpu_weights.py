@@ -1,0 +1,168 @@
+"""What each cached key receives of the queries' attention, against the 64-bit form."""
+import math
+
+import pytest
+import torch
+
+import position_independent_mla_gb300 as kv
+from _keep import Sums
+
+pytestmark = pytest.mark.gpu
+
+HEADS = {"mla": 16, "gqa": 32, "gqa4": 28, "mha": 32}
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("kind", sorted(HEADS))
+def test_ragged_chunks(kind, quant):
+    Sums(kind, [(1, 1), (3, 130), (1, 577), (67, 67), (130, 391), (2, 64)], HEADS[kind],
+         quant=quant).check()
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("kind,heads", [("mla", 128), ("mla", 7), ("gqa", 8), ("gqa", 64),
+                                        ("gqa4", 4), ("gqa4", 28), ("mha", 32)])
+def test_single_tokens(kind, heads, quant):
+    Sums(kind, [(1, 1), (1, 63), (1, 64), (1, 65), (1, 1000), (1, 128), (1, 129)], heads,
+         quant=quant, seed=3).check()
+
+
+@pytest.mark.parametrize("keep", [0.0, 0.95, 1.0, 2.5])
+def test_keep(keep):
+    s = Sums("gqa", [(1, 300), (9, 140)], 32, keep=keep, seed=2)
+    if keep == 0.0:
+        s.weights[:, ::7] = float("nan")  # is not read
+        old = s.weights.clone()
+        got = s.run()
+        assert not bool(torch.isnan(got[0, :300]).any() or torch.isnan(got[1, :140]).any())
+        s.weights = torch.nan_to_num(old, nan=0.5)
+    s.check()
+
+
+@pytest.mark.parametrize("block", [1, 5, 16, 48, 128, 256])
+@pytest.mark.parametrize("kind,quant", [("mla", False), ("gqa", True), ("gqa4", False), ("mla", True)])
+def test_block_sizes(kind, quant, block):
+    Sums(kind, [(1, 300), (40, 259), (5, 5)], HEADS[kind], block=block, quant=quant, seed=4).check()
+
+
+@pytest.mark.parametrize("kind", ["mla", "gqa", "gqa4"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (64, 0), (100, 4), (130, 67), (5000, 4),
+                                          (17, 1000)])
+def test_window_and_sinks(kind, window, sinks):
+    Sums(kind, [(1, 900), (70, 640), (33, 33), (1, 1), (300, 300), (1, 105)], HEADS[kind],
+         window=window, sinks=sinks, seed=6).check()
+
+
+@pytest.mark.parametrize("kind", ["mla", "gqa"])
+def test_every_key_without_causal_mask(kind):
+    Sums(kind, [(1, 200), (50, 333), (129, 64)], HEADS[kind], causal=False, seed=8).check()
+
+
+@pytest.mark.parametrize("kind,quant", [("mla", False), ("gqa", False), ("gqa", True), ("mha", False)])
+def test_strided_and_heads_outside_tokens(kind, quant):
+    Sums(kind, [(20, 300), (3, 90)], HEADS[kind], strided=True, quant=quant, seed=5).check()
+
+
+def test_empty_sequences():
+    # no queries: older steps fade all the same; no keys: nothing to write; more queries than keys
+    s = Sums("gqa", [(0, 200), (3, 0), (9, 5), (2, 130)], 32, keep=0.5, seed=9)
+    old = s.weights.clone()
+    s.check()
+    assert torch.equal(s.weights[0, :200], old[0, :200] * 0.5)
+    assert torch.equal(s.weights[1], old[1])
+
+
+@pytest.mark.parametrize("kind,quant", [("mla", False), ("gqa", False), ("gqa", True)])
+def test_a_key_that_is_nan_has_no_part_in_others(kind, quant):
+    s = Sums(kind, [(5, 200), (70, 150)], HEADS[kind], quant=quant, seed=10)
+    rows = torch.stack([s.slots(0)[7], s.slots(1)[149]]).cuda()
+    x = s.pool.rot[s.layer].view(torch.uint8 if s.pool.rot.element_size() == 1 else torch.int16)
+    x[rows, 3] = 0x7F if s.pool.rot.element_size() == 1 else 0x7FC0
+    # rows behind the last key of a block
+    for q in range(2):
+        m = s.lens[q][1]
+        last = int(s.table[q][m // s.block]) * s.block + m % s.block
+        x[last:last + 3] = 0x7F if s.pool.rot.element_size() == 1 else 0x7FC0
+    old, got = s.weights.clone(), s.run()
+    # (its last key: seen by the last query alone)
+    for q, k in ((0, 7), (1, 149)):
+        assert math.isnan(float(got[q, k]))
+        got[q, k] = old[q, k]
+        assert bool(torch.isfinite(got[q]).all())
+
+
+def test_queries_that_count_nothing():
+    s = Sums("gqa", [(4, 200)], 32, seed=11)
+    s.lse[1] = -math.inf
+    s.lse[2, 5:9] = -math.inf
+    s.check()
+
+
+def test_queries_of_another_sequence_have_no_part():
+    s = Sums("gqa", [(5, 300), (3, 290)], 32, seed=12)
+    s.q[5:] = float("nan")
+    s.lse[5:] = float("nan")
+    old = s.weights.clone()
+    got = s.run()
+    assert bool(torch.isfinite(got[0]).all())
+    assert bool(torch.isnan(got[1, :287]).all()) and torch.equal(got[1, 290:], old[1, 290:])
+
+
+def test_many_queries_over_a_long_context_and_equal_bits():
+    s = Sums("gqa", [(700, 3000), (64, 513)], 32, keep=0.0, seed=13)
+    first = s.check().clone()
+    assert torch.equal(first[0, :3000], s.run().double()[0, :3000])
+
+
+def test_scores_far_apart():
+    Sums("gqa", [(9, 400)], 32, q_scale=12.0, seed=14).check()
+
+
+def test_sums_to_the_number_of_rows():
+    s = Sums("gqa4", [(33, 700)], 28, keep=0.0, seed=15)
+    assert abs(float(s.run()[0, :700].double().sum()) - 33 * 28) < 1e-3 * 33 * 28
+
+
+def test_errors_of_the_device():
+    s = Sums("gqa", [(3, 200), (3, 100)], 32, seed=16)
+    s.table_dev = s.attn._tensors[2]
+    s.table_dev[0, 1] = 10 ** 6
+    old, got = s.weights.clone(), s.run(kv.KV_ERR_OUT_OF_RANGE)
+    assert torch.equal(got[0, 64:128], old[0, 64:128])  # nothing is added to the keys of that block
+    assert bool((got[0, :64] > old[0, :64]).all())
+    s.attn.max_kv_len = 150
+    s.wws = kv.weights_workspace(s.desc, s.attn, s.q)
+    old, got = s.weights.clone(), s.run(kv.KV_ERR_OUT_OF_RANGE)
+    assert torch.equal(got[0], old[0]) and bool((got[1, :90] > old[1, :90]).all())
+
+
+def test_a_wait_that_runs_out():
+    s = Sums("gqa", [(3, 200)], 32, seed=17)
+    old = s.weights.clone()
+    kv.kv_set_wait_limit_ns(2_000_000)
+    kv.kv_set_attention_skip_block(1)
+    try:
+        s.run(kv.KV_ERR_TIMEOUT)
+        # the other key tile, of the blocks that went on
+        n = 128 if bool(torch.equal(s.weights[0, :128], old[0, :128])) else 0
+        assert torch.equal(s.weights[0, 200:], old[0, 200:])
+        assert n == 128
+    finally:
+        kv.kv_set_attention_skip_block(-1)
+        kv.kv_set_wait_limit_ns(0)
+    s.weights.copy_(old)
+    s.check()
+
+
+def test_captured_and_replayed():
+    s = Sums("mla", [(20, 300), (3, 90)], 16, keep=0.0, seed=18)
+    want = s.check().clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kv.kv_attention_weights(s.desc, s.layer, s.attn, s.q, s.lse, s.weights, 0.0, s.wws)
+    for _ in range(2):
+        s.weights.fill_(9.0)
+        g.replay()
+        torch.cuda.synchronize()
+        for q, (_, m) in enumerate(s.lens):
+            assert torch.equal(s.weights[q, :m].double(), want[q, :m])
