@@ -1703,9 +1703,15 @@ WeightsPlan weights_plan(RowKind kind, const kv_attn_desc *a, int64_t total_q, i
     return plan_weights(kind, s);
 }
 
+// Workspace: header, a status word per block, sums of parts.
+size_t weights_parts_at(const WeightsPlan &pl)
+{
+    return align256(kHeaderBytes + (size_t)pl.blocks * 4);
+}
+
 size_t weights_bytes(const WeightsPlan &pl)
 {
-    return pl.blocks > 0x7FFFFFFFll ? 0 : align256(kHeaderBytes + (size_t)pl.blocks * 4);
+    return pl.blocks > 0x7FFFFFFFll ? 0 : weights_parts_at(pl) + align256(pl.part_bytes);
 }
 
 kv_status weights_impl(AttnParams p, RowKind kind, int64_t num_slots, int32_t block,
@@ -1770,9 +1776,10 @@ kv_status weights_impl(AttnParams p, RowKind kind, int64_t num_slots, int32_t bl
     wp.weights = weights;
     wp.weight_stride = weight_stride;
     wp.keep = keep;
+    wp.a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + weights_parts_at(pl));
     KV_CUDA(mark(t_ev_start, stream));
     KV_CUDA(launch_weights(wp, kind, pl, stream));
-    ++t_launches;
+    t_launches += pl.launches();
     KV_CUDA(mark(t_ev_stop, stream));
     return KV_OK;
 }

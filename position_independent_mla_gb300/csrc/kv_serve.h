@@ -215,7 +215,7 @@ struct SelectParams {
 int select_cluster(int32_t num_seqs, int32_t max_kv_len);
 cudaError_t launch_select(const SelectParams &p, cudaStream_t stream);
 
-// What each key receives of the queries' attention (kv_weights.cu).
+// What each key receives of the queries' attention (kv_weights.cu, kv_weights_many.cu).
 struct WeightsParams {
     AttnParams a; // the batch, its pool and its queries; out and the split have no part
     const float *lse;
@@ -223,7 +223,8 @@ struct WeightsParams {
     int64_t weight_stride;
     float keep;
     int32_t toks, rows, n; // of a row tile: tokens; rows; rows with those that pad it
-    int32_t parts;         // blocks of a cluster: they divide a key tile's row tiles and heads
+    int32_t parts;         // that the row tiles and heads over some keys are divided into
+    int64_t total_parts;   // many row tiles: of the call; a.part holds 256 sums of each
     int32_t stages;
     int32_t q_boxes;       // query rows come as boxes of q_map
     Divisor by_toks;
@@ -231,10 +232,13 @@ struct WeightsParams {
 };
 
 struct WeightsPlan {
-    bool hold;         // two key tiles to a block, held while the queries pass
+    bool many;         // head rows under more than one row tile
     int32_t toks, rows, n, parts, stages;
-    int64_t blocks;
+    int64_t blocks, units;
     int32_t smem;
+    size_t part_bytes; // of the workspace, for sums of parts
+
+    int launches() const { return many && parts > 1 ? 2 : 1; }
 };
 
 WeightsPlan plan_weights(RowKind kind, const AttnShape &a);

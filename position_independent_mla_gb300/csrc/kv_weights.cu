@@ -19,55 +19,30 @@
 //          queries that boxes do not fit, by all of them);
 //   lse    one warp brings the queries' lse, a step ahead;
 //   mma    one warp issues every MMA.
-#include <algorithm>
-
-#include "kv_attn_tile.cuh"
+#include "kv_weights.cuh"
 
 namespace kvr {
 
 namespace {
 
-template <bool MLA_, bool QUANT_, bool HOLD_>
+template <bool MLA_, bool QUANT_>
 struct SumGeo {
     static constexpr bool MLA = MLA_, QUANT = QUANT_;
-    static constexpr bool HOLD = HOLD_; // K of the block's head stays, Q passes
     static constexpr int KT = 128;
-    static constexpr int NT = HOLD ? 2 : 1;       // key tiles of a block
     static constexpr int CHUNKS = MLA ? 9 : 1;    // of a step, and
     static constexpr int PANELS = MLA ? 1 : 2;    // panels of 64 columns of each
-    static constexpr int K_CHUNK = NT * PANELS * 128 * 128; // bytes
-    static constexpr int SUM_WARPS = 8 * NT, LOAD_WARPS = 4;
+    static constexpr int K_CHUNK = PANELS * 128 * 128; // bytes
+    static constexpr int SUM_WARPS = 8, LOAD_WARPS = 4;
     static constexpr int LSE_WARP = SUM_WARPS + LOAD_WARPS, MMA_WARP = LSE_WARP + 1;
     static constexpr int THREADS = (MMA_WARP + 1) * 32;
-    static constexpr int BLOCKS = HOLD ? 1 : 2;   // to an SM
-    static constexpr int HELD = HOLD ? K_CHUNK : 0;
-    static int stage_bytes(int n) { return (HOLD ? 0 : K_CHUNK) + PANELS * n * 128; }
 };
 
 constexpr int kSumMaxStages = 6;
 constexpr int kSumSmem = 104 * 1024, kSumSmemAlone = 200 * 1024; // two blocks to an SM, one
 
-// Barriers: K held, and free again; S of two buffers, and free again; lse likewise; then the
-// ring's, full and empty.
-enum { kBarK = 0, kBarKFree = 1, kBarSum = 2, kBarSumFree = 4, kBarLse = 6, kBarEnd = 8, kBarStage = 9 };
-
-struct SumWork {
-    int seq, n, len, base; // new tokens, cached ones, those before the new ones
-    int q0;                // first query token
-    int k0;                // first key
-    int ra;                // first row tile, and
-    int tiles;             // row tiles that see a key of the block
-    int step0, step1;      // this block's steps: step s is row tile ra + s % tiles of head s / tiles
-};
-
-__device__ __forceinline__ void copy_box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
-                                          uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-                 "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
-                 : "memory");
-}
+// Barriers: S of two buffers, and free again; lse likewise; every MMA done; then the ring's,
+// full and empty.
+enum { kBarSum = 0, kBarSumFree = 2, kBarLse = 4, kBarEnd = 6, kBarStage = 7 };
 
 // D (128 x n) of A (128 rows) and B (n rows), both along K.
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t desc,
@@ -78,29 +53,6 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uin
                  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d),
                  "r"(a), "r"(b), "r"(desc), "r"(acc), "r"(kOperandHigh), "r"(lead)
                  : "memory");
-}
-
-__device__ __forceinline__ uint32_t low_bits(int n)
-{
-    return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
-}
-
-// Keys of the block that some query sees exist; their tokens [i0, i1) of the block.
-template <class G>
-__device__ __forceinline__ void find_steps(const WeightsParams &p, SumWork &w, int rank)
-{
-    const AttnParams &a = p.a;
-    const int k1 = min(w.len, w.k0 + G::NT * 128) - 1; // last key
-    int i0 = 0, i1 = w.n;
-    if (a.causal)
-        i0 = max(0, w.k0 - w.base);
-    if (a.window && w.k0 >= a.sinks)
-        i1 = (int)min((int64_t)w.n, max((int64_t)0, (int64_t)k1 + a.window - w.base));
-    w.ra = p.by_toks.quotient(i0);
-    w.tiles = i1 <= i0 ? 0 : p.by_toks.quotient(i1 + p.toks - 1) - w.ra;
-    const int64_t steps = (int64_t)w.tiles * a.kv_heads;
-    w.step0 = (int)(steps * rank / p.parts);
-    w.step1 = (int)(steps * (rank + 1) / p.parts);
 }
 
 // A step after another, without divisions.
@@ -174,7 +126,7 @@ struct HandKeys {
 };
 
 template <class G>
-__global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
+__global__ void __launch_bounds__(G::THREADS, 2) weights_kernel(
     const __grid_constant__ WeightsParams p)
 {
     const AttnParams &a = p.a;
@@ -183,10 +135,10 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ int s_bad;
-    __shared__ int64_t s_slot[G::NT * 128]; // of the block's keys; -1: none
+    __shared__ int64_t s_slot[128]; // of the block's keys; -1: none
     __shared__ __align__(16) float s_off[2][128];
-    __shared__ float s_sum[2][G::NT * 128];
-    __shared__ float s_part[G::NT * 128 + 1]; // and whether the block gave up
+    __shared__ float s_sum[2][128];
+    __shared__ float s_part[128 + 1]; // and whether the block gave up
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)blockIdx.x % p.parts, unit = (int)blockIdx.x / p.parts;
     const int tile = unit / a.num_seqs, seq = unit - tile * a.num_seqs;
@@ -200,31 +152,26 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
     const bool fits = seq_queries(a, seq, q0, w.n) && seq_keys(a, seq, w.len);
     w.q0 = (int)q0;
     w.base = w.len - w.n;
-    w.k0 = tile * G::NT * 128;
+    w.k0 = tile * 128;
     if (!fits || w.k0 >= w.len) { // the same for the whole cluster
         leave(fits || tile > 0 ? kStatusOk : kStatusOutOfRange);
         return;
     }
-    find_steps<G>(p, w, rank);
+    find_steps(p, w, 128, rank);
 
-    const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
-    const uint32_t ring = smem + G::HELD;
-    const uint32_t stage_bytes = (G::HOLD ? 0 : G::K_CHUNK) + G::PANELS * p.n * 128;
-    const uint32_t q_in_stage = G::HOLD ? 0 : G::K_CHUNK;
+    const uint32_t ring = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const uint32_t stage_bytes = G::K_CHUNK + G::PANELS * p.n * 128;
     const uint32_t bars = smem_u32(s_bars);
     const uint32_t full = bars + kBarStage * 8, empty = full + kSumMaxStages * 8;
     const bool k_boxes = !G::QUANT && a.box_rows > 0;
     const bool hand = !k_boxes || !p.q_boxes;
-    const uint32_t columns = G::NT * p.n * 2 <= 32 ? 32 : G::NT * p.n * 2 <= 64 ? 64
-                           : G::NT * p.n * 2 <= 128 ? 128 : G::NT * p.n * 2 <= 256 ? 256 : 512;
+    const uint32_t columns = p.n <= 32 ? 64 : p.n <= 64 ? 128 : 256; // two S
     if (warp == G::MMA_WARP) {
         tmem_alloc(smem_u32(&s_tmem), columns);
     } else if (tid == 0) {
         s_abort = 0;
         s_bad = 0;
         const uint32_t fill = hand ? 1 + G::LOAD_WARPS * 32 : 1;
-        bar_init(bars + kBarK * 8, fill);
-        bar_init(bars + kBarKFree * 8, 1);
         bar_init(bars + kBarEnd * 8, 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(bars + (kBarSum + i) * 8, 1);
@@ -241,20 +188,11 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
     for (int i = tid; i < p.stages * G::PANELS * (p.n - p.rows) * 8; i += G::THREADS) {
         const int c = i & 7, r = i >> 3, pad = p.n - p.rows;
         const int panel = r / pad % G::PANELS, st = r / pad / G::PANELS;
-        sts16(ring + st * stage_bytes + q_in_stage + (panel * p.n + p.rows + r % pad) * 128 + c * 16,
+        sts16(ring + st * stage_bytes + G::K_CHUNK + (panel * p.n + p.rows + r % pad) * 128 + c * 16,
               make_uint4(0, 0, 0, 0));
     }
-    for (int i = tid; i < G::NT * 128; i += G::THREADS) {
-        const int k = w.k0 + i;
-        int64_t s = -1;
-        if (k < w.len) {
-            const int b = a.by_block.quotient(k);
-            const int32_t blk = __ldg(a.block_tables + (int64_t)seq * a.max_blocks + b);
-            if (blk >= 0 && blk < a.num_blocks)
-                s = (int64_t)blk * a.block + (k - b * a.block);
-        }
-        s_slot[i] = s;
-    }
+    if (tid < 128)
+        s_slot[tid] = sum_slot(a, w, w.k0 + tid);
     async_fence();
     mma_fence_before();
     __syncthreads();
@@ -262,26 +200,14 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
     const int64_t limit = a.wait_limit_ns;
 
     if (warp < G::SUM_WARPS) {
-        const int t = warp >> 3, half = (warp >> 2) & 1;
-        const int key = t * 128 + (warp & 3) * 32 + lane, k = w.k0 + key;
+        const int half = warp >> 2, key = (warp & 3) * 32 + lane, k = w.k0 + key;
         const bool mine = s_slot[key] >= 0;
         if (k < w.len && !mine && half == 0)
             s_bad = 1;
         const float c = a.scale * 1.4426950408889634f;
         const f2 c2 = f2_of_bits(__float_as_uint(c), __float_as_uint(c));
-        // tokens that see this key: [lo, hi)
-        const int lo = a.causal ? max(0, k - w.base) : 0;
-        const int hi = !mine ? 0
-                     : a.window && k >= a.sinks
-                         ? (int)max((int64_t)0, min((int64_t)w.n, (int64_t)k + a.window - w.base))
-                         : w.n;
-        // and those that see every key of this tile
-        const int k1 = w.k0 + t * 128 + 127;
-        const int all_lo = a.causal ? max(0, k1 - w.base) : 0;
-        const int all_hi = a.window && k1 >= a.sinks
-                               ? (int)max((int64_t)0, min((int64_t)w.n, (int64_t)w.k0 + t * 128 +
-                                                                            a.window - w.base))
-                               : w.n;
+        const TokenRange see = tokens_of(a, w, k, 1), all = tokens_of(a, w, w.k0, 128);
+        const bool warp_mine = __all_sync(0xFFFFFFFFu, mine);
         f2 sum = 0ull;
         Step st(w, w.step0);
         for (int s = w.step0; s < w.step1; ++s, st.next(w)) {
@@ -291,43 +217,21 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
                 break;
             mma_fence_after();
             const int tok0 = st.tile * p.toks;
-            const bool whole = mine && tok0 >= all_lo && tok0 + p.toks <= all_hi;
+            const bool whole = warp_mine && tok0 >= all.lo && tok0 + p.toks <= all.hi;
             // columns of the tokens that see this key
-            const int c_lo = (max(lo, tok0) - tok0) * a.group;
-            const int c_hi = (min(hi, tok0 + p.toks) - tok0) * a.group;
+            const int c_lo = (max(see.lo, tok0) - tok0) * a.group;
+            const int c_hi = mine ? (min(see.hi, tok0 + p.toks) - tok0) * a.group : 0;
             f2 part[2] = {0ull, 0ull};
             for (int at = half * 32; at < p.n; at += 64) {
                 uint32_t x[32];
-                tmem_ld32(s_tmem + (buf * G::NT + t) * p.n + at + ((uint32_t)((warp & 3) * 32) << 16), x);
+                tmem_ld32(s_tmem + buf * p.n + at + ((uint32_t)((warp & 3) * 32) << 16), x);
                 tmem_ld_wait();
                 tmem_pin32(x);
-                const float *off = s_off[buf] + at;
-                if (__all_sync(0xFFFFFFFFu, whole)) {
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float4 o = *reinterpret_cast<const float4 *>(off + 2 * j);
-                        const f2 y0 = f2_fma(f2_of_bits(x[2 * j], x[2 * j + 1]), c2,
-                                             f2_of_bits(__float_as_uint(o.x), __float_as_uint(o.y)));
-                        const f2 y1 = f2_fma(f2_of_bits(x[2 * j + 2], x[2 * j + 3]), c2,
-                                             f2_of_bits(__float_as_uint(o.z), __float_as_uint(o.w)));
-                        float e0, e1, e2, e3;
-                        asm("mov.b64 {%0, %1}, %2;" : "=f"(e0), "=f"(e1) : "l"(y0));
-                        asm("mov.b64 {%0, %1}, %2;" : "=f"(e2), "=f"(e3) : "l"(y1));
-                        part[0] = f2_add(part[0], f2_of_bits(__float_as_uint(exp2_fast(e0)),
-                                                             __float_as_uint(exp2_fast(e1))));
-                        part[1] = f2_add(part[1], f2_of_bits(__float_as_uint(exp2_fast(e2)),
-                                                             __float_as_uint(exp2_fast(e3))));
-                    }
-                } else {
-                    const uint32_t see = low_bits(c_hi - at) & ~low_bits(c_lo - at);
-                    float add[2] = {0.0f, 0.0f};
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float e = exp2_fast(fmaf(__uint_as_float(x[j]), c, off[j]));
-                        add[j & 1] += (see >> j) & 1u ? e : 0.0f;
-                    }
-                    part[0] = f2_add(part[0], f2_of_bits(__float_as_uint(add[0]), __float_as_uint(add[1])));
-                }
+                if (whole)
+                    add_columns(x, s_off[buf] + at, c2, part);
+                else
+                    add_seen_columns(x, s_off[buf] + at, c, low_bits(c_hi - at) & ~low_bits(c_lo - at),
+                                     part);
             }
             sum = f2_add(sum, f2_add(part[0], part[1]));
             mma_fence_before();
@@ -343,19 +247,13 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
             int stage = 0, phase = 1, filled = 0;
             bool ok = true;
             Step st(w, w.step0);
-            int held = -1, heads = 0; // HOLD: the head whose K is held; how many there were
             // K by boxes: a lane's box of a key tile
             const int per = k_boxes ? 128 / a.box_rows : 0;
             auto boxes = [&](uint32_t dst, uint32_t bar, int head, int chunk, bool ask) {
-                uint32_t bytes = 0;
-#pragma unroll
-                for (int t = 0; t < G::NT; ++t) {
-                    const int64_t slot = lane < per ? s_slot[t * 128 + lane * a.box_rows] : -1;
-                    const uint32_t who = __ballot_sync(0xFFFFFFFFu, slot >= 0);
-                    bytes += __popc(who) * a.box_rows * 128 * G::PANELS;
-                    if (!ask || slot < 0)
-                        continue;
-                    const uint32_t to = dst + t * (G::PANELS << 14) + lane * a.box_rows * 128;
+                const int64_t slot = lane < per ? s_slot[lane * a.box_rows] : -1;
+                const uint32_t who = __ballot_sync(0xFFFFFFFFu, slot >= 0);
+                const uint32_t to = dst + lane * a.box_rows * 128;
+                if (ask && slot >= 0) {
                     if (G::MLA) {
                         if (chunk < 8)
                             copy_box(to, &a.copy_map, chunk * 64, (int)slot, bar);
@@ -366,42 +264,38 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
                         copy_box(to + 16384, &a.rot_map, head * 128 + 64, (int)slot, bar);
                     }
                 }
-                return bytes;
+                return (uint32_t)(__popc(who) * a.box_rows * 128 * G::PANELS);
             };
-            auto by_hand = [&](uint32_t dst, int head, int chunk) {
-#pragma unroll 1
-                for (int t = 0; t < G::NT; ++t) {
-                    const uint32_t to = dst + t * (G::PANELS << 14);
-                    if (G::MLA && chunk == 8) {
+            auto by_hand = [&](uint32_t to, int head, int chunk) {
+                if (G::MLA && chunk == 8) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int i = lt + j * H::TH, row = i >> 3, c = i & 7;
-                            const int64_t s = s_slot[t * 128 + row];
-                            const uint4 v = s < 0 ? make_uint4(0, 0, 0, 0)
-                                                  : ld_stream(a.rot + s * a.rot_ss + c * 16);
-                            sts16(to + row * 128 + ((c ^ (row & 7)) << 4), v);
-                        }
-                        continue;
+                    for (int j = 0; j < 8; ++j) {
+                        const int i = lt + j * H::TH, row = i >> 3, c = i & 7;
+                        const int64_t s = s_slot[row];
+                        const uint4 v = s < 0 ? make_uint4(0, 0, 0, 0)
+                                              : ld_stream(a.rot + s * a.rot_ss + c * 16);
+                        sts16(to + row * 128 + ((c ^ (row & 7)) << 4), v);
                     }
-                    constexpr int B = H::PER < 8 ? H::PER : 8;
+                    return;
+                }
+                constexpr int B = H::PER < 8 ? H::PER : 8;
 #pragma unroll 1
-                    for (int j0 = 0; j0 < H::PER; j0 += B) {
-                        uint4 v[B];
-                        float sc[B];
+                for (int j0 = 0; j0 < H::PER; j0 += B) {
+                    uint4 v[B];
+                    float sc[B];
 #pragma unroll
-                        for (int j = 0; j < B; ++j) {
-                            int row, c;
-                            H::at(lt, j0 + j, row, c);
-                            const int64_t s = s_slot[t * 128 + row];
-                            v[j] = H::load(a, s, head, chunk, c);
-                            sc[j] = H::scale(a, s, head, chunk);
-                        }
+                    for (int j = 0; j < B; ++j) {
+                        int row, c;
+                        H::at(lt, j0 + j, row, c);
+                        const int64_t s = s_slot[row];
+                        v[j] = H::load(a, s, head, chunk, c);
+                        sc[j] = H::scale(a, s, head, chunk);
+                    }
 #pragma unroll
-                        for (int j = 0; j < B; ++j) {
-                            int row, c;
-                            H::at(lt, j0 + j, row, c);
-                            H::store(to, row, c, v[j], sc[j]);
-                        }
+                    for (int j = 0; j < B; ++j) {
+                        int row, c;
+                        H::at(lt, j0 + j, row, c);
+                        H::store(to, row, c, v[j], sc[j]);
                     }
                 }
             };
@@ -419,29 +313,6 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
                 }
             };
             for (int s = w.step0; ok && s < w.step1; ++s, st.next(w)) {
-                if (G::HOLD && st.head != held) {
-                    // the MMAs of the head before are done with K
-                    ok = heads == 0 || bar_wait(bars + kBarKFree * 8, (heads - 1) & 1, &s_abort, limit);
-                    if (!ok)
-                        break;
-                    held = st.head;
-                    ++heads;
-                    const uint32_t bar = bars + kBarK * 8;
-                    if (lt < 32) {
-                        const uint32_t bytes = k_boxes ? boxes(smem, bar, held, 0, false) : 0;
-                        if (lane == 0)
-                            bar_signal_bulk(bar, 1, bytes);
-                        __syncwarp();
-                        if (k_boxes)
-                            boxes(smem, bar, held, 0, true);
-                    }
-                    if (hand) {
-                        if (!k_boxes)
-                            by_hand(smem, held, 0);
-                        async_fence();
-                        bar_signal(bar);
-                    }
-                }
                 for (int chunk = 0; chunk < G::CHUNKS; ++chunk) {
                     ok = bar_wait(empty + stage * 8, phase, &s_abort, limit);
                     if (!ok)
@@ -449,26 +320,26 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
                     const uint32_t at = ring + stage * stage_bytes, bar = full + stage * 8;
                     if (lt < 32) {
                         uint32_t bytes = p.q_boxes ? p.rows * G::PANELS * 128 : 0;
-                        if (!G::HOLD && k_boxes)
+                        if (k_boxes)
                             bytes += boxes(at, bar, st.head, chunk, false);
                         if (lane == 0) {
                             bar_signal_bulk(bar, 1, bytes);
                             if (p.q_boxes)
 #pragma unroll
                                 for (int i = 0; i < G::PANELS; ++i)
-                                    copy_box3(at + q_in_stage + i * p.n * 128, &p.q_map,
+                                    copy_box3(at + G::K_CHUNK + i * p.n * 128, &p.q_map,
                                               (chunk * G::PANELS + i) * 64, st.head * a.group,
                                               w.q0 + st.tile * p.toks, bar);
                         }
                         __syncwarp();
-                        if (!G::HOLD && k_boxes)
+                        if (k_boxes)
                             boxes(at, bar, st.head, chunk, true);
                     }
                     if (hand) {
-                        if (!G::HOLD && !k_boxes)
+                        if (!k_boxes)
                             by_hand(at, st.head, chunk);
                         if (!p.q_boxes)
-                            queries(at + q_in_stage, chunk);
+                            queries(at + G::K_CHUNK, chunk);
                         async_fence();
                         bar_signal(bar);
                     }
@@ -482,39 +353,21 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
             // boxes in flight land before the block's memory goes, also after an early end
             if (lt < 32) {
                 int none = 0;
-                if (G::HOLD && heads > 0)
-                    bar_wait(bars + kBarK * 8, (heads - 1) & 1, &none, 10000000ll);
                 for (int i = 0; i < p.stages; ++i)
                     if (filled > i)
                         bar_wait(full + i * 8, ((filled - 1 - i) / p.stages) & 1, &none, 10000000ll);
             }
         }
     } else if (warp == G::LSE_WARP) {
-        // -lse * log2 e of a step's rows, four to a lane; -inf: the row counts nothing
-        auto fetch = [&](const Step &st) {
-            float4 r;
-            float *v = &r.x;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int col = lane * 4 + j;
-                const int tok = a.by_group.quotient(col), at = st.tile * p.toks + tok;
-                float x = -INFINITY;
-                if (col < p.rows && at < w.n)
-                    x = __ldg(p.lse + (int64_t)(w.q0 + at) * a.heads + st.head * a.group +
-                              (col - tok * a.group));
-                v[j] = x == -INFINITY ? -INFINITY : -x * 1.4426950408889634f;
-            }
-            return r;
-        };
         if (w.step0 < w.step1) {
             Step st(w, w.step0);
-            float4 next = fetch(st);
+            float4 next = row_offsets(p, w, st.head, st.tile, lane * 4);
             for (int s = w.step0; s < w.step1; ++s) {
                 const int i = s - w.step0, buf = i & 1;
                 const float4 now = next;
                 if (s + 1 < w.step1) {
                     st.next(w);
-                    next = fetch(st);
+                    next = row_offsets(p, w, st.head, st.tile, lane * 4);
                 }
                 if (i >= 2 && !bar_wait(bars + (kBarSumFree + buf) * 8, ((i >> 1) - 1) & 1, &s_abort, limit))
                     break;
@@ -526,18 +379,12 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
         const uint32_t lead = elect_lane(), tmem = s_tmem;
         const uint32_t desc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.n >> 3) << 17) |
                               ((uint32_t)(kRows >> 4) << 24);
-        int stage = 0, phase = 0, held = -1, heads = 0;
+        int stage = 0, phase = 0;
         bool ok = blockIdx.x != a.skip_block;
-        Step st(w, w.step0);
-        for (int s = w.step0; ok && s < w.step1; ++s) {
-            const int i = s - w.step0, buf = i & 1;
+        for (int i = 0; ok && i < w.step1 - w.step0; ++i) {
+            const int buf = i & 1;
             if (i >= 2)
                 ok = bar_wait(bars + (kBarSumFree + buf) * 8, ((i >> 1) - 1) & 1, &s_abort, limit);
-            if (G::HOLD && ok && st.head != held) {
-                held = st.head;
-                ok = bar_wait(bars + kBarK * 8, heads & 1, &s_abort, limit);
-                ++heads;
-            }
             mma_fence_after();
             for (int chunk = 0; ok && chunk < G::CHUNKS; ++chunk) {
                 ok = bar_wait(full + stage * 8, phase, &s_abort, limit);
@@ -545,18 +392,14 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
                     break;
                 async_fence();
                 const uint32_t at = ring + stage * stage_bytes;
-                const uint32_t q = operand(at + q_in_stage, 16);
+                const uint32_t k = operand(at, 16), q = operand(at + G::K_CHUNK, 16);
 #pragma unroll
-                for (int t = 0; t < G::NT; ++t) {
-                    const uint32_t d = tmem + (buf * G::NT + t) * p.n;
-                    const uint32_t k = operand((G::HOLD ? smem : at) + t * (G::PANELS << 14), 16);
+                for (int pn = 0; pn < G::PANELS; ++pn)
 #pragma unroll
-                    for (int pn = 0; pn < G::PANELS; ++pn)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_rows(d, k + pn * (16384 >> 4) + kk * 2, q + pn * (p.n * 128 >> 4) + kk * 2,
-                                     desc, chunk > 0 || pn > 0 || kk > 0, lead);
-                }
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_rows(tmem + buf * p.n, k + pn * (16384 >> 4) + kk * 2,
+                                 q + pn * (p.n * 128 >> 4) + kk * 2, desc,
+                                 chunk > 0 || pn > 0 || kk > 0, lead);
                 bar_signal_mma(empty + stage * 8, lead);
                 if (++stage == p.stages) {
                     stage = 0;
@@ -566,9 +409,6 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
             if (!ok)
                 break;
             bar_signal_mma(bars + (kBarSum + buf) * 8, lead);
-            st.next(w);
-            if (G::HOLD && (s + 1 == w.step1 || st.head != held))
-                bar_signal_mma(bars + kBarKFree * 8, lead);
         }
         // every MMA is done before tensor memory goes
         int none = 0;
@@ -583,16 +423,16 @@ __global__ void __launch_bounds__(G::THREADS, G::BLOCKS) weights_kernel(
     mma_fence_after();
     if (warp == G::MMA_WARP)
         tmem_free(s_tmem, columns);
-    if (tid < G::NT * 128)
+    if (tid < 128)
         s_part[tid] = s_sum[0][tid] + s_sum[1][tid];
     if (tid == 0)
-        s_part[G::NT * 128] = s_abort ? 1.0f : 0.0f;
+        s_part[128] = s_abort ? 1.0f : 0.0f;
     cluster_sync();
-    if (rank == 0 && tid < G::NT * 128 && w.k0 + tid < w.len) {
+    if (rank == 0 && tid < 128 && w.k0 + tid < w.len) {
         float sum = 0.0f, gave_up = 0.0f;
         for (int r = 0; r < p.parts; ++r) {
             sum += lds4_of(smem_u32(&s_part[tid]), r);
-            gave_up += lds4_of(smem_u32(&s_part[G::NT * 128]), r);
+            gave_up += lds4_of(smem_u32(&s_part[128]), r);
         }
         float *const to = p.weights + seq * p.weight_stride + w.k0 + tid;
         if (gave_up == 0.0f)
@@ -625,26 +465,6 @@ cudaError_t launch(WeightsParams &p, const WeightsPlan &pl, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, weights_kernel<G>, p);
 }
 
-// Query rows as boxes: `toks` tokens of the heads of one key head, 64 columns.
-bool encode_queries(WeightsParams &p, int width)
-{
-    const auto encode = map_encoder();
-    const AttnParams &a = p.a;
-    if (!encode)
-        return false;
-    const int64_t row = width * 2, hs = a.heads > 1 ? a.q_hs : row;
-    const int64_t ts = a.total_q > 1 ? a.q_ts : std::max(hs * a.heads, row);
-    if (hs <= 0 || ts <= 0)
-        return false; // queries that share their memory
-    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)a.heads, (cuuint64_t)a.total_q};
-    const cuuint64_t strides[2] = {(cuuint64_t)hs, (cuuint64_t)ts};
-    const cuuint32_t box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)p.toks}, step[3] = {1, 1, 1};
-    return encode(&p.q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<char *>(a.q), dims,
-                  strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 } // namespace
 
 WeightsPlan plan_weights(RowKind kind, const AttnShape &a)
@@ -656,19 +476,27 @@ WeightsPlan plan_weights(RowKind kind, const AttnShape &a)
     pl.rows = pl.toks * group;
     pl.n = (pl.rows + 31) / 32 * 32;
     const int64_t row_tiles = std::max<int64_t>(1, (a.max_q_len + pl.toks - 1) / pl.toks);
-    pl.hold = !mla && row_tiles > 1;
-    const int64_t keys = pl.hold ? 256 : 128;
-    const int64_t units = a.num_seqs * std::max<int64_t>(1, (a.max_kv_len + keys - 1) / keys);
     const int64_t steps = row_tiles * a.kv_heads;
-    pl.parts = 1; // enough blocks for a few rounds
-    while (pl.parts < 8 && units * pl.parts < 4 * kSms && steps >= 2 * pl.parts)
+    pl.many = !mla && row_tiles > 1;
+    const int64_t keys = pl.many ? 256 : 128;
+    pl.units = a.num_seqs * std::max<int64_t>(1, (a.max_kv_len + keys - 1) / keys);
+    pl.parts = 1;
+    if (pl.many) {
+        // some 8 parts to an SM, so that they even out
+        pl.parts = (int32_t)std::min<int64_t>(
+            steps, std::max<int64_t>(1, (8 * kSms + pl.units - 1) / pl.units));
+        pl.blocks = std::min<int64_t>(kSms, pl.units * pl.parts);
+        pl.part_bytes = pl.parts > 1 ? (size_t)pl.units * pl.parts * 256 * sizeof(float) : 0;
+        return pl;
+    }
+    // enough blocks for a few rounds
+    while (pl.parts < 8 && pl.units * pl.parts < 4 * kSms && steps >= 2 * pl.parts)
         pl.parts *= 2;
-    pl.blocks = units * pl.parts;
-    const int held = pl.hold ? 2 * 2 * 128 * 128 : 0;
-    const int stage = (pl.hold ? 0 : (mla ? 1 : 2) * 128 * 128) + (mla ? 1 : 2) * pl.n * 128;
-    const int room = pl.hold || 2 * stage > kSumSmem ? kSumSmemAlone : kSumSmem;
-    pl.stages = std::min(kSumMaxStages, (room - held) / stage);
-    pl.smem = held + pl.stages * stage + 1024;
+    pl.blocks = pl.units * pl.parts;
+    const int stage = (mla ? 1 : 2) * (128 + pl.n) * 128;
+    const int room = 2 * stage > kSumSmem ? kSumSmemAlone : kSumSmem;
+    pl.stages = std::min(kSumMaxStages, room / stage);
+    pl.smem = pl.stages * stage + 1024;
     return pl;
 }
 
@@ -680,19 +508,19 @@ cudaError_t launch_weights(WeightsParams &p, RowKind kind, const WeightsPlan &pl
     p.rows = pl.rows;
     p.n = pl.n;
     p.parts = pl.parts;
+    p.total_parts = pl.units * pl.parts;
     p.stages = pl.stages;
     p.by_toks = Divisor((uint32_t)pl.toks);
     p.a.by_group = Divisor((uint32_t)p.a.group);
     p.a.by_block = Divisor((uint32_t)p.a.block);
     p.q_boxes = encode_queries(p, kind == RowKind::Mla ? 576 : 128);
+    if (pl.many)
+        return launch_weights_many(p, pl, stream);
     if (kind == RowKind::Mla)
-        return quant ? launch<SumGeo<true, true, false>>(p, pl, stream)
-                     : launch<SumGeo<true, false, false>>(p, pl, stream);
-    if (pl.hold)
-        return quant ? launch<SumGeo<false, true, true>>(p, pl, stream)
-                     : launch<SumGeo<false, false, true>>(p, pl, stream);
-    return quant ? launch<SumGeo<false, true, false>>(p, pl, stream)
-                 : launch<SumGeo<false, false, false>>(p, pl, stream);
+        return quant ? launch<SumGeo<true, true>>(p, pl, stream)
+                     : launch<SumGeo<true, false>>(p, pl, stream);
+    return quant ? launch<SumGeo<false, true>>(p, pl, stream)
+                 : launch<SumGeo<false, false>>(p, pl, stream);
 }
 
 } // namespace kvr

@@ -1,0 +1,154 @@
+// kv_weights.cuh -- what the kernels of kv_attention_weights share (kv_weights.cu,
+// kv_weights_many.cu).
+#pragma once
+
+#include <algorithm>
+
+#include "kv_attn_tile.cuh"
+
+namespace kvr {
+
+// Keys of a block and the steps that it takes over them: a step is a row tile (the tokens that
+// fill 128 rows with the query heads of one key head) of one key head.
+struct SumWork {
+    int seq, n, len, base; // new tokens, cached ones, those before the new ones
+    int q0;                // first query token
+    int k0;                // first key
+    int ra;                // first row tile that sees one of the keys, and
+    int tiles;             // how many do
+    int step0, step1;      // this block's steps: step s is row tile ra + s % tiles of head s / tiles
+};
+
+// The steps of part `part` of w.parts equal parts of those over `keys` keys from w.k0 on.
+__device__ __forceinline__ void find_steps(const WeightsParams &p, SumWork &w, int keys, int part)
+{
+    const AttnParams &a = p.a;
+    const int k1 = min(w.len, w.k0 + keys) - 1; // last key
+    int i0 = 0, i1 = w.n;
+    if (a.causal)
+        i0 = max(0, w.k0 - w.base);
+    if (a.window && w.k0 >= a.sinks)
+        i1 = (int)min((int64_t)w.n, max((int64_t)0, (int64_t)k1 + a.window - w.base));
+    w.ra = p.by_toks.quotient(i0);
+    w.tiles = i1 <= i0 ? 0 : p.by_toks.quotient(i1 + p.toks - 1) - w.ra;
+    const int64_t steps = (int64_t)w.tiles * a.kv_heads;
+    w.step0 = (int)(steps * part / p.parts);
+    w.step1 = (int)(steps * (part + 1) / p.parts);
+}
+
+// The slot of key k, or -1: there is none, or its block lies outside the pool.
+__device__ __forceinline__ int64_t sum_slot(const AttnParams &a, const SumWork &w, int k)
+{
+    if (k >= w.len)
+        return -1;
+    const int b = a.by_block.quotient(k);
+    const int32_t blk = __ldg(a.block_tables + (int64_t)w.seq * a.max_blocks + b);
+    return blk >= 0 && blk < a.num_blocks ? (int64_t)blk * a.block + (k - b * a.block) : -1;
+}
+
+// Tokens that see a key: [lo, hi); and those that see every one of `keys` keys from k0 on.
+struct TokenRange {
+    int lo, hi;
+};
+
+__device__ __forceinline__ TokenRange tokens_of(const AttnParams &a, const SumWork &w, int k0,
+                                                int keys)
+{
+    const int64_t k1 = (int64_t)k0 + keys - 1;
+    TokenRange r;
+    r.lo = a.causal ? (int)max((int64_t)0, min((int64_t)w.n, k1 - w.base)) : 0;
+    r.hi = a.window && k1 >= a.sinks
+               ? (int)max((int64_t)0, min((int64_t)w.n, (int64_t)k0 + a.window - w.base))
+               : w.n;
+    return r;
+}
+
+__device__ __forceinline__ uint32_t low_bits(int n)
+{
+    return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
+__device__ __forceinline__ void copy_box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                          uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+                 "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+// -lse * log2 e of four rows of a row tile (-inf: the row counts nothing, or there is none).
+__device__ __forceinline__ float4 row_offsets(const WeightsParams &p, const SumWork &w, int head,
+                                              int tile, int row)
+{
+    const AttnParams &a = p.a;
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int tok = a.by_group.quotient(row + j), at = tile * p.toks + tok;
+        float x = -INFINITY;
+        if (row + j < p.rows && at < w.n)
+            x = __ldg(p.lse + (int64_t)(w.q0 + at) * a.heads + head * a.group +
+                      (row + j - tok * a.group));
+        v[j] = x == -INFINITY ? -INFINITY : -x * 1.4426950408889634f;
+    }
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// Adds 2^(x * c + off) of 32 columns, four offsets at a time (aligned so).
+__device__ __forceinline__ void add_columns(const uint32_t *x, const float *off, f2 c2, f2 (&sum)[2])
+{
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        const float4 o = *reinterpret_cast<const float4 *>(off + j);
+        const f2 y0 = f2_fma(f2_of_bits(x[j], x[j + 1]), c2,
+                             f2_of_bits(__float_as_uint(o.x), __float_as_uint(o.y)));
+        const f2 y1 = f2_fma(f2_of_bits(x[j + 2], x[j + 3]), c2,
+                             f2_of_bits(__float_as_uint(o.z), __float_as_uint(o.w)));
+        float e0, e1, e2, e3;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(e0), "=f"(e1) : "l"(y0));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(e2), "=f"(e3) : "l"(y1));
+        sum[0] = f2_add(sum[0], f2_of_bits(__float_as_uint(exp2_fast(e0)),
+                                           __float_as_uint(exp2_fast(e1))));
+        sum[1] = f2_add(sum[1], f2_of_bits(__float_as_uint(exp2_fast(e2)),
+                                           __float_as_uint(exp2_fast(e3))));
+    }
+}
+
+// The same where only columns with a bit in `see` count, whatever the others hold.
+__device__ __forceinline__ void add_seen_columns(const uint32_t *x, const float *off, float c,
+                                                 uint32_t see, f2 (&sum)[2])
+{
+    float add[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const float e = exp2_fast(fmaf(__uint_as_float(x[j]), c, off[j]));
+        add[j & 1] += (see >> j) & 1u ? e : 0.0f;
+    }
+    sum[0] = f2_add(sum[0], f2_of_bits(__float_as_uint(add[0]), __float_as_uint(add[1])));
+}
+
+// Query rows as boxes: p.toks tokens of the heads of one key head, 64 columns.
+inline bool encode_queries(WeightsParams &p, int width)
+{
+    const auto encode = map_encoder();
+    const AttnParams &a = p.a;
+    if (!encode)
+        return false;
+    const int64_t row = width * 2, hs = a.heads > 1 ? a.q_hs : row;
+    const int64_t ts = a.total_q > 1 ? a.q_ts : std::max(hs * a.heads, row);
+    if (hs <= 0 || ts <= 0 || a.total_q <= 0)
+        return false; // queries that share their memory, or none
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)a.heads, (cuuint64_t)a.total_q};
+    const cuuint64_t strides[2] = {(cuuint64_t)hs, (cuuint64_t)ts};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)p.toks}, step[3] = {1, 1, 1};
+    return encode(&p.q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<char *>(a.q), dims,
+                  strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Head rows under more than one row tile (kv_weights_many.cu).
+cudaError_t launch_weights_many(WeightsParams &p, const WeightsPlan &pl, cudaStream_t stream);
+
+} // namespace kvr

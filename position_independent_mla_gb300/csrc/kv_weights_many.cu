@@ -1,0 +1,549 @@
+// kv_weights_many.cu -- kv_attention_weights over head rows where the queries fill more than
+// one row tile: the scores of a chunk or a prompt, bound by the tensor cores and by the
+// exponentials, 32 a clock and SM, which take about as long.
+//
+// The 256 keys of a unit stay: two tiles of 128 keys x 128 bf16 in tensor memory, as the A
+// operands, so that an MMA reads only its queries from shared memory (64 of its 128 bytes
+// a clock; with both operands there the MMAs alone took all of it).  Row tiles of queries
+// pass, each for both key tiles.  A thread has a key and half of the columns: it takes 64
+// scores into registers, gives S back to the next MMA and then forms their exponentials.
+//
+// The units' steps are cut into p.parts parts each; 152 blocks take the parts of the call in
+// turn.  A part's sums go to the workspace, and a second kernel adds up each key's in the
+// order of the parts (p.parts = 1: the block writes the result).
+//
+// Roles of a block's warps: 16 sum (8 to a key tile), 4 bring a run's keys into tensor
+// memory, one brings the queries, one their lse, one issues every MMA, and one finds the
+// next parts and their keys' slots: when each role looked for its work itself, a part cost
+// some 17 us beside its steps.
+#include "kv_weights.cuh"
+
+namespace kvr {
+
+namespace {
+
+constexpr int kManyStages = 6, kManyOffs = 4, kManyParts = 3;
+constexpr int kManySum = 16; // warps, then
+constexpr int kManyKey = kManySum, kManyLoad = kManyKey + 4, kManyLse = kManyLoad + 1,
+              kManyMma = kManyLse + 1, kManyFind = kManyMma + 1;
+constexpr int kManyThreads = (kManyFind + 1) * 32;
+constexpr int kManySumRegs = 88, kManyRegs = 64; // of the sum warps' threads, of the others
+constexpr int kManyStage = 2 * 128 * 128; // bytes of 128 query rows
+constexpr int kManySmem = kManyStages * kManyStage + 1024;
+
+enum {
+    kManyK = 0,      // keys of a run are in tensor memory (two buffers), and free again
+    kManyKFree = 2,
+    kManyS = 4,      // S of a key tile, and read again
+    kManyRead = 6,
+    kManyOff = 8,    // offsets of a step, and free again
+    kManyOffFree = kManyOff + kManyOffs,
+    kManyFull = kManyOffFree + kManyOffs, // queries of a step
+    kManyEmpty = kManyFull + kManyStages,
+    kManyPart = kManyEmpty + kManyStages, // parts of the call, and done by every warp
+    kManyPartFree = kManyPart + kManyParts,
+    kManyEnd = kManyPartFree + kManyParts,
+    kManyBars
+};
+
+__device__ __forceinline__ uint32_t key_columns(int buf, int tile) { return 256 + buf * 128 + tile * 64; }
+
+// A part of the call, and the slots of its keys (-1: none).
+struct Part {
+    SumWork w;
+    int64_t at;
+    int there; // 0: past the last
+    int32_t slot[256];
+};
+
+// A part's steps run by run: a run is the steps of one head.
+struct Runs {
+    int step, step1, tiles, ra;
+    int head, tile, end; // row tiles [tile, end) of the run
+
+    __device__ explicit Runs(const SumWork &w) : step(w.step0), step1(w.step1), tiles(w.tiles), ra(w.ra) {}
+
+    __device__ __forceinline__ bool next()
+    {
+        if (step >= step1)
+            return false;
+        head = step / tiles;
+        const int first = step - head * tiles, many = min(tiles - first, step1 - step);
+        tile = ra + first;
+        end = tile + many;
+        step += many;
+        return true;
+    }
+};
+
+// A vote over the eight warps of a key tile, also their meeting point.
+__device__ __forceinline__ bool tile_any(int tile, bool x)
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 q, %1, 0;\n"
+                 "barrier.cta.red.or.pred p, %2, 256, q;\nselp.b32 %0, 1, 0, p;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)x), "r"(1 + tile)
+                 : "memory");
+    return r != 0;
+}
+
+// This thread's half (64 columns) of its key's row into tensor memory.
+template <bool QUANT>
+__device__ __forceinline__ void key_to_tmem(const AttnParams &a, int64_t slot, int head, int half,
+                                            uint32_t to)
+{
+    uint32_t x[32];
+    if (slot < 0) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            x[j] = 0;
+    } else if constexpr (QUANT) {
+        const char *src = a.rot + slot * a.rot_ss + head * 128 + half * 64;
+        const uint32_t mul = scale_mul(__ldg(a.rs + slot * a.rs_ss + head));
+        uint4 v[4];
+        uint32_t rare = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = ld_stream(src + j * 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            rare |= rare16(v[j], mul);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint4 lo, hi;
+            if (rare)
+                convert16<true>(v[j], mul, lo, hi);
+            else
+                convert16<false>(v[j], mul, lo, hi);
+            x[8 * j] = lo.x, x[8 * j + 1] = lo.y, x[8 * j + 2] = lo.z, x[8 * j + 3] = lo.w;
+            x[8 * j + 4] = hi.x, x[8 * j + 5] = hi.y, x[8 * j + 6] = hi.z, x[8 * j + 7] = hi.w;
+        }
+    } else {
+        const char *src = a.rot + slot * a.rot_ss + head * 256 + half * 128;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint4 v = ld_stream(src + j * 16);
+            x[4 * j] = v.x, x[4 * j + 1] = v.y, x[4 * j + 2] = v.z, x[4 * j + 3] = v.w;
+        }
+    }
+    tmem_st32(to, x);
+    tmem_st_wait();
+}
+
+template <bool QUANT>
+__global__ void __launch_bounds__(kManyThreads, 1) weights_many_kernel(
+    const __grid_constant__ WeightsParams p)
+{
+    const AttnParams &a = p.a;
+    extern __shared__ unsigned char raw_smem[];
+    __shared__ __align__(8) uint64_t s_bars[kManyBars];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    __shared__ int s_bad;
+    __shared__ __align__(16) float s_off[kManyOffs][128];
+    __shared__ float s_sum[256]; // of a half's threads
+    __shared__ Part s_part[kManyParts];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t ring = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const uint32_t bars = smem_u32(s_bars);
+    const int64_t limit = a.wait_limit_ns;
+    auto bar = [&](int i) { return bars + i * 8; };
+    auto wait = [&](int i, int parity) { return bar_wait(bar(i), parity, &s_abort, limit); };
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == kManyMma) {
+        tmem_alloc(smem_u32(&s_tmem), 512);
+    } else if (tid == 0) {
+        s_abort = 0;
+        s_bad = 0;
+        for (int i = 0; i < kManyBars; ++i) {
+            int count = 1;
+            if (i < kManyKFree)
+                count = 128;
+            else if (i >= kManyRead && i < kManyOff)
+                count = kManySum / 2;
+            else if (i >= kManyOffFree && i < kManyFull)
+                count = kManySum;
+            else if (i >= kManyFull && i < kManyEmpty)
+                count = p.q_boxes ? 1 : 32;
+            else if (i >= kManyPartFree && i < kManyEnd)
+                count = kManyFind; // every warp but the finder
+            bar_init(bar(i), count);
+        }
+        bar_init_fence();
+    }
+    // rows that pad Q
+    const int pad = 128 - p.rows;
+    for (int i = tid; i < kManyStages * 2 * pad * 8; i += kManyThreads) {
+        const int r = i >> 3;
+        sts16(ring + (r / pad >> 1) * kManyStage + (r / pad & 1) * 16384 +
+                  (p.rows + r % pad) * 128 + (i & 7) * 16,
+              make_uint4(0, 0, 0, 0));
+    }
+    async_fence();
+    mma_fence_before();
+    __syncthreads();
+    mma_fence_after();
+    const uint32_t tmem = s_tmem;
+    // The parts one after another, for every role but the finder: the next one is there, or
+    // (false) there is none or a wait ran out; and it is not needed any more.
+    int at = 0, round = 0;
+    auto part_there = [&] { return wait(kManyPart + at, round & 1) && s_part[at].there; };
+    auto part_done = [&] {
+        __syncwarp();
+        if (lane == 0)
+            bar_signal(bar(kManyPartFree + at));
+        if (++at == kManyParts) {
+            at = 0;
+            ++round;
+        }
+    };
+
+    if (warp < kManySum) {
+        reg_inc<kManySumRegs>();
+        const int t = warp >> 3, half = (warp >> 2) & 1, key = t * 128 + (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const float c = a.scale * 1.4426950408889634f;
+        const f2 c2 = f2_of_bits(__float_as_uint(c), __float_as_uint(c));
+        uint32_t i = 0; // steps so far
+        bool ok = true;
+        for (;;) {
+            // the warps of a key tile meet at the end of each part: they go on together
+            ok = !tile_any(t, !(ok && wait(kManyPart + at, round & 1)));
+            if (!ok || !s_part[at].there)
+                break;
+            const SumWork w = s_part[at].w;
+            const int k = w.k0 + key;
+            const bool mine = s_part[at].slot[key] >= 0;
+            if (k < w.len && !mine)
+                s_bad = 1;
+            const TokenRange see = tokens_of(a, w, k, 1);
+            const TokenRange all = tokens_of(a, w, w.k0 + t * 128, 128);
+            const bool warp_mine = __all_sync(0xFFFFFFFFu, mine);
+            f2 sum = 0ull;
+            Runs run(w);
+            while (ok && run.next()) {
+                for (int tile = run.tile; tile < run.end; ++tile, ++i) {
+                    const int off_at = (int)(i & (kManyOffs - 1));
+                    ok = wait(kManyS + t, i & 1);
+                    if (!ok)
+                        break;
+                    mma_fence_after();
+                    uint32_t x[64];
+                    tmem_ld32(tmem + t * 128 + half * 64 + lanes, x);
+                    tmem_ld32(tmem + t * 128 + half * 64 + 32 + lanes, x + 32);
+                    tmem_ld_wait();
+                    tmem_pin32(x);
+                    tmem_pin32(x + 32);
+                    mma_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_signal(bar(kManyRead + t));
+                    ok = wait(kManyOff + off_at, (i / kManyOffs) & 1);
+                    if (!ok)
+                        break;
+                    const float *off = s_off[off_at] + half * 64;
+                    const int tok0 = tile * p.toks;
+                    f2 part[2] = {0ull, 0ull};
+                    if (warp_mine && tok0 >= all.lo && tok0 + p.toks <= all.hi) {
+                        add_columns(x, off, c2, part);
+                        add_columns(x + 32, off + 32, c2, part);
+                    } else if (mine) {
+                        const int lo = (max(see.lo, tok0) - tok0) * a.group;
+                        const int hi = (min(see.hi, tok0 + p.toks) - tok0) * a.group;
+#pragma unroll
+                        for (int j = 0; j < 64; j += 32)
+                            add_seen_columns(x + j, off + j, c,
+                                             low_bits(hi - half * 64 - j) & ~low_bits(lo - half * 64 - j),
+                                             part);
+                    }
+                    sum = f2_add(sum, f2_add(part[0], part[1]));
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_signal(bar(kManyOffFree + off_at));
+                }
+            }
+            float s0, s1;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(sum));
+            if (half == 1)
+                s_sum[key] = s0 + s1;
+            ok = !tile_any(t, !ok);
+            if (ok && half == 0 && k < w.len) {
+                const float total = s0 + s1 + s_sum[key];
+                if (p.parts > 1) {
+                    p.a.part[s_part[at].at * 256 + key] = total;
+                } else {
+                    float *const to = p.weights + w.seq * p.weight_stride + k;
+                    *to = p.keep == 0.0f ? total : fmaf(p.keep, *to, total);
+                }
+            }
+            part_done();
+        }
+    } else {
+        reg_dec<kManyRegs>();
+        if (warp < kManyLoad) { // keys: a lane of tensor memory to a thread
+            const int row = (warp & 3) * 32 + lane;
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            uint32_t runs = 0;
+            bool ok = true;
+            while (ok && part_there()) {
+                const int64_t slot[2] = {s_part[at].slot[row], s_part[at].slot[128 + row]};
+                Runs run(s_part[at].w);
+                while (ok && run.next()) {
+                    const int buf = (int)runs & 1;
+                    ok = runs < 2 || wait(kManyKFree + buf, ((runs >> 1) - 1) & 1);
+                    if (!ok)
+                        break;
+                    mma_fence_after();
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j)
+                        key_to_tmem<QUANT>(a, slot[j >> 1], run.head, j & 1,
+                                           tmem + key_columns(buf, j >> 1) + (j & 1) * 32 + lanes);
+                    mma_fence_before();
+                    bar_signal(bar(kManyK + buf));
+                    ++runs;
+                }
+                part_done();
+            }
+        } else if (warp == kManyLoad) {
+            int stage = 0, phase = 1, filled = 0;
+            bool ok = true;
+            while (ok && part_there()) {
+                const SumWork w = s_part[at].w;
+                Runs run(w);
+                while (ok && run.next()) {
+                    for (int tile = run.tile; tile < run.end; ++tile) {
+                        ok = wait(kManyEmpty + stage, phase);
+                        if (!ok)
+                            break;
+                        const uint32_t to = ring + stage * kManyStage, full = bar(kManyFull + stage);
+                        if (p.q_boxes) {
+                            if (lane == 0) {
+                                bar_signal_bulk(full, 1, p.rows * 256);
+                                for (int pn = 0; pn < 2; ++pn)
+                                    copy_box3(to + pn * 16384, &p.q_map, pn * 64, run.head * a.group,
+                                              w.q0 + tile * p.toks, full);
+                            }
+                            __syncwarp();
+                        } else { // a row at a time, 16 lanes to one
+                            for (int r = lane >> 4; r < p.rows; r += 2) {
+                                const int tok = a.by_group.quotient(r), g = r - tok * a.group;
+                                const int q = tile * p.toks + tok, c = lane & 15;
+                                const char *src = a.q + (int64_t)(w.q0 + q) * a.q_ts +
+                                                  (int64_t)(run.head * a.group + g) * a.q_hs + c * 16;
+                                const uint4 v = q < w.n ? __ldg(reinterpret_cast<const uint4 *>(src))
+                                                        : make_uint4(0, 0, 0, 0);
+                                sts16(to + ((c >> 3) << 14) + r * 128 + (((c & 7) ^ (r & 7)) << 4), v);
+                            }
+                            async_fence();
+                            bar_signal(full);
+                        }
+                        filled = min(filled + 1, kManyStages);
+                        if (++stage == kManyStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+                part_done();
+            }
+            // boxes in flight land before the block's memory goes, also after an early end: the
+            // stages from the one filled last backwards
+            int none = 0;
+            for (int i = 0; i < filled; ++i) {
+                const bool wrapped = stage - 1 - i < 0; // filled in the round before
+                const int st = wrapped ? stage - 1 - i + kManyStages : stage - 1 - i;
+                bar_wait(bar(kManyFull + st), phase ^ 1 ^ (wrapped ? 1 : 0), &none, 10000000ll);
+            }
+        } else if (warp == kManyLse) {
+            uint32_t i = 0;
+            bool ok = true;
+            while (ok && part_there()) {
+                const SumWork w = s_part[at].w;
+                Runs run(w);
+                while (ok && run.next()) {
+                    float4 next = row_offsets(p, w, run.head, run.tile, lane * 4);
+                    for (int tile = run.tile; tile < run.end; ++tile, ++i) {
+                        const float4 now = next;
+                        if (tile + 1 < run.end)
+                            next = row_offsets(p, w, run.head, tile + 1, lane * 4);
+                        const int to = (int)(i & (kManyOffs - 1));
+                        ok = i < kManyOffs || wait(kManyOffFree + to, (i / kManyOffs - 1) & 1);
+                        if (!ok)
+                            break;
+                        *reinterpret_cast<float4 *>(&s_off[to][lane * 4]) = now;
+                        __syncwarp();
+                        if (lane == 0)
+                            bar_signal(bar(kManyOff + to));
+                    }
+                }
+                part_done();
+            }
+        } else if (warp == kManyMma) {
+            const uint32_t lead = elect_lane();
+            int stage = 0, phase = 0;
+            uint32_t i = 0, runs = 0;
+            bool ok = blockIdx.x != a.skip_block;
+            while (ok && part_there()) {
+                Runs run(s_part[at].w);
+                while (ok && run.next()) {
+                    const int buf = (int)runs & 1;
+                    ok = wait(kManyK + buf, (runs >> 1) & 1);
+                    ++runs;
+                    for (int tile = run.tile; ok && tile < run.end; ++tile, ++i) {
+                        ok = wait(kManyFull + stage, phase);
+                        if (!ok)
+                            break;
+                        async_fence();
+                        const uint32_t q = operand(ring + stage * kManyStage, 16);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            ok = ok && (i == 0 || wait(kManyRead + t, (i - 1) & 1));
+                            if (!ok)
+                                break;
+                            mma_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_tmem<128, 0>(tmem + t * 128, tmem + key_columns(buf, t) + kk * 8,
+                                                 q + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, kk > 0,
+                                                 lead);
+                            bar_signal_mma(bar(kManyS + t), lead);
+                        }
+                        if (!ok)
+                            break;
+                        bar_signal_mma(bar(kManyEmpty + stage), lead);
+                        if (++stage == kManyStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    if (ok)
+                        bar_signal_mma(bar(kManyKFree + buf), lead);
+                }
+                part_done();
+            }
+            if (blockIdx.x == a.skip_block)
+                s_abort = 1;
+            int none = 0; // every MMA is done before tensor memory goes
+            bar_signal_mma(bar(kManyEnd), lead);
+            bar_wait(bar(kManyEnd), 0, &none, 1000000000ll);
+            __syncwarp();
+        } else { // find
+            bool bad = false, ok = true;
+            for (int64_t n = blockIdx.x; ok; n += gridDim.x) {
+                SumWork w{};
+                bool there = false;
+                for (; n < p.total_parts; n += gridDim.x) {
+                    const int64_t unit = n / p.parts, tile = unit / a.num_seqs;
+                    w.seq = (int)(unit - tile * a.num_seqs);
+                    int64_t q0;
+                    const bool fits = seq_queries(a, w.seq, q0, w.n) && seq_keys(a, w.seq, w.len);
+                    bad |= !fits;
+                    if (!fits || tile * 256 >= w.len)
+                        continue;
+                    w.q0 = (int)q0;
+                    w.base = w.len - w.n;
+                    w.k0 = (int)tile * 256;
+                    find_steps(p, w, 256, (int)(n - unit * p.parts));
+                    there = true;
+                    break;
+                }
+                int32_t slot[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    slot[j] = there ? (int32_t)sum_slot(a, w, w.k0 + j * 32 + lane) : -1;
+                ok = round == 0 || wait(kManyPartFree + at, (round - 1) & 1);
+                if (!ok)
+                    break;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    s_part[at].slot[j * 32 + lane] = slot[j];
+                if (lane == 0) {
+                    s_part[at].w = w;
+                    s_part[at].at = n;
+                    s_part[at].there = there;
+                }
+                __syncwarp();
+                if (lane == 0)
+                    bar_signal(bar(kManyPart + at));
+                if (++at == kManyParts) {
+                    at = 0;
+                    ++round;
+                }
+                if (!there)
+                    break;
+            }
+            if (bad)
+                s_bad = 1;
+        }
+    }
+    mma_fence_before();
+    __syncthreads();
+    mma_fence_after();
+    if (warp == kManyMma)
+        tmem_free(tmem, 512);
+    if (tid == 0)
+        write_block_status(a.header, s_abort ? kStatusTimeout : s_bad ? kStatusOutOfRange : kStatusOk,
+                           blockIdx.x, gridDim.x);
+}
+
+// Adds up the parts of each key.  Where a block gave up nothing is stored.
+__global__ void __launch_bounds__(256) weights_join_kernel(const __grid_constant__ WeightsParams p,
+                                                           int blocks)
+{
+    const AttnParams &a = p.a;
+    const int64_t unit = blockIdx.x, tile = unit / a.num_seqs;
+    const int seq = (int)(unit - tile * a.num_seqs);
+    int64_t q0;
+    int n, len = 0;
+    const bool fits = seq_queries(a, seq, q0, n) && seq_keys(a, seq, len);
+    const int64_t k = tile * 256 + threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    bool gave_up = false;
+    for (int i = threadIdx.x; i < blocks; i += 256)
+        gave_up |= a.header[kHeaderBytes / 4 + i] == kStatusTimeout;
+    if (__syncthreads_or(gave_up) || !fits || k >= len)
+        return;
+    const float *part = a.part + unit * p.parts * 256 + threadIdx.x;
+    float sum = 0.0f;
+    for (int c = 0; c < p.parts; ++c)
+        sum += part[c * 256];
+    float *const to = p.weights + seq * p.weight_stride + k;
+    *to = p.keep == 0.0f ? sum : fmaf(p.keep, *to, sum);
+}
+
+template <bool QUANT>
+cudaError_t launch(const WeightsParams &p, const WeightsPlan &pl, cudaStream_t stream)
+{
+    cudaError_t e = allow_smem<weights_many_kernel<QUANT>>(kManySmem);
+    if (e != cudaSuccess)
+        return e;
+    cudaFuncAttributes fa; // the shares come out of what a block starts with, or it would wait
+    if ((e = cudaFuncGetAttributes(&fa, weights_many_kernel<QUANT>)) != cudaSuccess)
+        return e;
+    if (kManySum * kManySumRegs + (kManyThreads / 32 - kManySum) * kManyRegs >
+        kManyThreads / 32 * fa.numRegs)
+        return cudaErrorInvalidConfiguration;
+    weights_many_kernel<QUANT><<<(unsigned)pl.blocks, kManyThreads, kManySmem, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess || p.parts == 1)
+        return e;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.total_parts / p.parts));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, weights_join_kernel, p, (int)pl.blocks);
+}
+
+} // namespace
+
+cudaError_t launch_weights_many(WeightsParams &p, const WeightsPlan &pl, cudaStream_t stream)
+{
+    return p.a.cs ? launch<true>(p, pl, stream) : launch<false>(p, pl, stream);
+}
+
+} // namespace kvr

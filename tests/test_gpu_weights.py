@@ -166,3 +166,35 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for q, (_, m) in enumerate(s.lens):
             assert torch.equal(s.weights[q, :m].double(), want[q, :m])
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_many_queries_a_wait_that_runs_out(quant):
+    s = Sums("gqa", [(300, 1000), (40, 513)], 32, seed=19, quant=quant)
+    old = s.weights.clone()
+    kv.kv_set_wait_limit_ns(2_000_000)
+    kv.kv_set_attention_skip_block(3)
+    try:
+        s.run(kv.KV_ERR_TIMEOUT)
+    finally:
+        kv.kv_set_attention_skip_block(-1)
+        kv.kv_set_wait_limit_ns(0)
+    assert torch.equal(s.weights, old)  # what parts of a key's sum there are is not stored
+    s.check()
+
+
+@pytest.mark.parametrize("kind,heads,quant", [("gqa", 8, False), ("gqa", 40, False), ("gqa4", 28, True),
+                                              ("mha", 32, False), ("gqa4", 12, False), ("gqa", 64, True)])
+def test_many_queries_of_several_sequences(kind, heads, quant):
+    lens = [(260, 1000), (1, 300), (0, 40), (129, 129), (400, 2000), (17, 700)]
+    Sums(kind, lens, heads, quant=quant, seed=20, keep=0.5).check()
+
+
+def test_many_queries_with_more_units_than_parts():
+    lens = [(70 + i, 200 + 90 * i) for i in range(40)]
+    Sums("gqa4", lens, 28, seed=21).check()
+
+
+@pytest.mark.parametrize("window,sinks", [(300, 4), (40, 300), (1, 0)])
+def test_many_queries_under_a_window(window, sinks):
+    Sums("gqa", [(500, 1500), (200, 200)], 32, window=window, sinks=sinks, seed=22).check()
