@@ -77,19 +77,25 @@ __device__ __forceinline__ void copy_box3(uint32_t dst, const CUtensorMap *map, 
                  : "memory");
 }
 
-// -lse * log2 e of four rows of a row tile (-inf: the row counts nothing, or there is none).
+// lse of a row of a row tile (-inf: there is none).
+__device__ __forceinline__ float row_lse(const WeightsParams &p, const SumWork &w, int head, int tile,
+                                         int row)
+{
+    const AttnParams &a = p.a;
+    const int tok = a.by_group.quotient(row), at = tile * p.toks + tok;
+    return row < p.rows && at < w.n ? __ldg(p.lse + (int64_t)(w.q0 + at) * a.heads +
+                                            head * a.group + (row - tok * a.group))
+                                    : -INFINITY;
+}
+
+// -lse * log2 e of four rows (-inf: the row counts nothing).
 __device__ __forceinline__ float4 row_offsets(const WeightsParams &p, const SumWork &w, int head,
                                               int tile, int row)
 {
-    const AttnParams &a = p.a;
     float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int tok = a.by_group.quotient(row + j), at = tile * p.toks + tok;
-        float x = -INFINITY;
-        if (row + j < p.rows && at < w.n)
-            x = __ldg(p.lse + (int64_t)(w.q0 + at) * a.heads + head * a.group +
-                      (row + j - tok * a.group));
+        const float x = row_lse(p, w, head, tile, row + j);
         v[j] = x == -INFINITY ? -INFINITY : -x * 1.4426950408889634f;
     }
     return make_float4(v[0], v[1], v[2], v[3]);

@@ -2,6 +2,11 @@
 // one row tile: the scores of a chunk or a prompt, bound by the tensor cores and by the
 // exponentials, 32 a clock and SM, which take about as long.
 //
+// The scores come less lse: an MMA of 16 columns more adds -lse / scale, which is three bf16
+// numbers against ones, so that a thread needs nothing but its row of S.  (Offsets read from
+// shared memory, one of 16 loads for each four scores, held the threads up: 4096 tokens over
+// 16384, 32 heads: 457 us.)
+//
 // The 256 keys of a unit stay: two tiles of 128 keys x 128 bf16 in tensor memory, as the A
 // operands, so that an MMA reads only its queries from shared memory (64 of its 128 bytes
 // a clock; with both operands there the MMAs alone took all of it).  Row tiles of queries
@@ -22,23 +27,23 @@ namespace kvr {
 
 namespace {
 
-constexpr int kManyStages = 6, kManyOffs = 4, kManyParts = 3;
+constexpr int kManyStages = 4, kManyParts = 3;
 constexpr int kManySum = 16; // warps, then
 constexpr int kManyKey = kManySum, kManyLoad = kManyKey + 4, kManyLse = kManyLoad + 1,
               kManyMma = kManyLse + 1, kManyFind = kManyMma + 1;
 constexpr int kManyThreads = (kManyFind + 1) * 32;
 constexpr int kManySumRegs = 88, kManyRegs = 64; // of the sum warps' threads, of the others
-constexpr int kManyStage = 2 * 128 * 128; // bytes of 128 query rows
-constexpr int kManySmem = kManyStages * kManyStage + 1024;
+// A stage: 128 query rows in two panels, and a panel with their -lse / scale.  Before the
+// stages a panel of ones, by which the MMA adds that to the scores.
+constexpr int kManyPanel = 128 * 128, kManyStage = 3 * kManyPanel;
+constexpr int kManySmem = kManyPanel + kManyStages * kManyStage + 1024;
 
 enum {
     kManyK = 0,      // keys of a run are in tensor memory (two buffers), and free again
     kManyKFree = 2,
     kManyS = 4,      // S of a key tile, and read again
     kManyRead = 6,
-    kManyOff = 8,    // offsets of a step, and free again
-    kManyOffFree = kManyOff + kManyOffs,
-    kManyFull = kManyOffFree + kManyOffs, // queries of a step
+    kManyFull = 8, // queries of a step and their lse, and free again
     kManyEmpty = kManyFull + kManyStages,
     kManyPart = kManyEmpty + kManyStages, // parts of the call, and done by every warp
     kManyPartFree = kManyPart + kManyParts,
@@ -141,11 +146,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) weights_many_kernel(
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ int s_bad;
-    __shared__ __align__(16) float s_off[kManyOffs][128];
     __shared__ float s_sum[256]; // of a half's threads
     __shared__ Part s_part[kManyParts];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t ring = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const uint32_t ones = (smem_u32(raw_smem) + 1023u) & ~1023u, ring = ones + kManyPanel;
     const uint32_t bars = smem_u32(s_bars);
     const int64_t limit = a.wait_limit_ns;
     auto bar = [&](int i) { return bars + i * 8; };
@@ -160,25 +164,30 @@ __global__ void __launch_bounds__(kManyThreads, 1) weights_many_kernel(
             int count = 1;
             if (i < kManyKFree)
                 count = 128;
-            else if (i >= kManyRead && i < kManyOff)
+            else if (i >= kManyRead && i < kManyFull)
                 count = kManySum / 2;
-            else if (i >= kManyOffFree && i < kManyFull)
-                count = kManySum;
             else if (i >= kManyFull && i < kManyEmpty)
-                count = p.q_boxes ? 1 : 32;
+                count = p.q_boxes ? 2 : 33;
             else if (i >= kManyPartFree && i < kManyEnd)
                 count = kManyFind; // every warp but the finder
             bar_init(bar(i), count);
         }
         bar_init_fence();
     }
-    // rows that pad Q
+    // rows that pad Q; of the other panels 16 columns are used: ones against the three parts of
+    // an offset, and zeros
     const int pad = 128 - p.rows;
     for (int i = tid; i < kManyStages * 2 * pad * 8; i += kManyThreads) {
         const int r = i >> 3;
-        sts16(ring + (r / pad >> 1) * kManyStage + (r / pad & 1) * 16384 +
+        sts16(ring + (r / pad >> 1) * kManyStage + (r / pad & 1) * kManyPanel +
                   (p.rows + r % pad) * 128 + (i & 7) * 16,
               make_uint4(0, 0, 0, 0));
+    }
+    for (int i = tid; i < (kManyStages + 1) * 128; i += kManyThreads) {
+        const int r = i & 127, panel = i >> 7;
+        const uint32_t to = (panel == 0 ? ones : ring + (panel - 1) * kManyStage + 2 * kManyPanel) + r * 128;
+        sts16(to + ((0 ^ (r & 7)) << 4), make_uint4(panel == 0 ? 0x3F803F80u : 0u, panel == 0 ? 0x3F80u : 0u, 0, 0));
+        sts16(to + ((1 ^ (r & 7)) << 4), make_uint4(0, 0, 0, 0));
     }
     async_fence();
     mma_fence_before();
@@ -224,7 +233,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) weights_many_kernel(
             Runs run(w);
             while (ok && run.next()) {
                 for (int tile = run.tile; tile < run.end; ++tile, ++i) {
-                    const int off_at = (int)(i & (kManyOffs - 1));
                     ok = wait(kManyS + t, i & 1);
                     if (!ok)
                         break;
@@ -239,28 +247,28 @@ __global__ void __launch_bounds__(kManyThreads, 1) weights_many_kernel(
                     __syncwarp();
                     if (lane == 0)
                         bar_signal(bar(kManyRead + t));
-                    ok = wait(kManyOff + off_at, (i / kManyOffs) & 1);
-                    if (!ok)
-                        break;
-                    const float *off = s_off[off_at] + half * 64;
                     const int tok0 = tile * p.toks;
                     f2 part[2] = {0ull, 0ull};
                     if (warp_mine && tok0 >= all.lo && tok0 + p.toks <= all.hi) {
-                        add_columns(x, off, c2, part);
-                        add_columns(x + 32, off + 32, c2, part);
+#pragma unroll
+                        for (int j = 0; j < 64; j += 2) {
+                            float y0, y1;
+                            asm("mov.b64 {%0, %1}, %2;" : "=f"(y0), "=f"(y1) : "l"(f2_mul(f2_of_bits(x[j], x[j + 1]), c2)));
+                            part[(j >> 1) & 1] =
+                                f2_add(part[(j >> 1) & 1], f2_of_bits(__float_as_uint(exp2_fast(y0)),
+                                                                      __float_as_uint(exp2_fast(y1))));
+                        }
                     } else if (mine) {
                         const int lo = (max(see.lo, tok0) - tok0) * a.group;
                         const int hi = (min(see.hi, tok0 + p.toks) - tok0) * a.group;
 #pragma unroll
-                        for (int j = 0; j < 64; j += 32)
-                            add_seen_columns(x + j, off + j, c,
-                                             low_bits(hi - half * 64 - j) & ~low_bits(lo - half * 64 - j),
-                                             part);
+                        for (int j = 0; j < 64; ++j) { // whatever the others hold
+                            const int col = half * 64 + j;
+                            const float e = exp2_fast(__uint_as_float(x[j]) * c);
+                            part[j & 1] = f2_add(part[j & 1], f2_of_bits(col >= lo && col < hi ? __float_as_uint(e) : 0u, 0u));
+                        }
                     }
                     sum = f2_add(sum, f2_add(part[0], part[1]));
-                    __syncwarp();
-                    if (lane == 0)
-                        bar_signal(bar(kManyOffFree + off_at));
                 }
             }
             float s0, s1;
@@ -321,7 +329,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) weights_many_kernel(
                             if (lane == 0) {
                                 bar_signal_bulk(full, 1, p.rows * 256);
                                 for (int pn = 0; pn < 2; ++pn)
-                                    copy_box3(to + pn * 16384, &p.q_map, pn * 64, run.head * a.group,
+                                    copy_box3(to + pn * kManyPanel, &p.q_map, pn * 64, run.head * a.group,
                                               w.q0 + tile * p.toks, full);
                             }
                             __syncwarp();
@@ -333,7 +341,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) weights_many_kernel(
                                                   (int64_t)(run.head * a.group + g) * a.q_hs + c * 16;
                                 const uint4 v = q < w.n ? __ldg(reinterpret_cast<const uint4 *>(src))
                                                         : make_uint4(0, 0, 0, 0);
-                                sts16(to + ((c >> 3) << 14) + r * 128 + (((c & 7) ^ (r & 7)) << 4), v);
+                                sts16(to + (c >> 3) * kManyPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4), v);
                             }
                             async_fence();
                             bar_signal(full);
@@ -356,25 +364,50 @@ __global__ void __launch_bounds__(kManyThreads, 1) weights_many_kernel(
                 bar_wait(bar(kManyFull + st), phase ^ 1 ^ (wrapped ? 1 : 0), &none, 10000000ll);
             }
         } else if (warp == kManyLse) {
-            uint32_t i = 0;
+            // -lse / scale as the sum of three bf16 (24 bits, as many as it has)
+            const float by = -1.0f / a.scale;
+            int stage = 0, phase = 1;
             bool ok = true;
             while (ok && part_there()) {
                 const SumWork w = s_part[at].w;
                 Runs run(w);
                 while (ok && run.next()) {
-                    float4 next = row_offsets(p, w, run.head, run.tile, lane * 4);
-                    for (int tile = run.tile; tile < run.end; ++tile, ++i) {
-                        const float4 now = next;
+                    float next[4], now[4];
+                    auto ask = [&](int tile) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            next[j] = row_lse(p, w, run.head, tile, j * 32 + lane);
+                    };
+                    ask(run.tile);
+                    for (int tile = run.tile; tile < run.end; ++tile) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            now[j] = next[j];
                         if (tile + 1 < run.end)
-                            next = row_offsets(p, w, run.head, tile + 1, lane * 4);
-                        const int to = (int)(i & (kManyOffs - 1));
-                        ok = i < kManyOffs || wait(kManyOffFree + to, (i / kManyOffs - 1) & 1);
+                            ask(tile + 1);
+                        ok = wait(kManyEmpty + stage, phase);
                         if (!ok)
                             break;
-                        *reinterpret_cast<float4 *>(&s_off[to][lane * 4]) = now;
+                        const uint32_t to = ring + stage * kManyStage + 2 * kManyPanel;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int r = j * 32 + lane;
+                            // -infinity: the row counts nothing, or there is none
+                            const float v = now[j] == -INFINITY ? -INFINITY : now[j] * by;
+                            const uint32_t hi = pack_bf16(v, 0.0f);
+                            const float v1 = isinf(v) ? 0.0f : v - __uint_as_float(hi << 16);
+                            const uint32_t mid = pack_bf16(v1, 0.0f);
+                            const uint32_t lo = pack_bf16(v1 - __uint_as_float(mid << 16), 0.0f);
+                            sts16(to + r * 128 + ((r & 7) << 4), make_uint4(hi | mid << 16, lo, 0, 0));
+                        }
+                        async_fence();
                         __syncwarp();
                         if (lane == 0)
-                            bar_signal(bar(kManyOff + to));
+                            bar_signal(bar(kManyFull + stage));
+                        if (++stage == kManyStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
                     }
                 }
                 part_done();
@@ -405,8 +438,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) weights_many_kernel(
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
                                 mma_tmem<128, 0>(tmem + t * 128, tmem + key_columns(buf, t) + kk * 8,
-                                                 q + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, kk > 0,
-                                                 lead);
+                                                 q + (kk >> 2) * (kManyPanel >> 4) + (kk & 3) * 2,
+                                                 kk > 0, lead);
+                            mma_smem<128>(tmem + t * 128, operand(ones, 16), q + 2 * (kManyPanel >> 4),
+                                          1u, lead);
                             bar_signal_mma(bar(kManyS + t), lead);
                         }
                         if (!ok)
