@@ -982,7 +982,8 @@ __device__ __forceinline__ void queries_to_tmem(const AttnParams &p, const Work 
 // out of the products.  `finite`: O shows none of that; if it does, the unit is done again,
 // `careful`: keys that no row sees are zeros, and such values of others are taken out of V
 // before they are used and given back at the end to the rows that do see them.
-template <class G>
+// TREE: a row sees the keys before the new tokens, and new tokens by its mask.
+template <class G, bool TREE>
 __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, const TileMask &m,
                                             int t, uint32_t tmem, uint32_t ring, uint32_t bars,
                                             int warp, int half, int lane, int warps,
@@ -1002,7 +1003,7 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
     const int lo = p.window ? max(0, pos - p.window + 1) : 0;
     const int sk = p.window ? min(p.sinks, hi) : 0;
     // no key is seen by some rows only
-    const bool one_token = G::NT == 1 && m.pos0 == m.pos1 && !p.tree;
+    const bool one_token = G::NT == 1 && m.pos0 == m.pos1 && !TREE;
     const float c = p.scale * 1.4426950408889634f;
     const uint32_t o_col = tmem + G::O_COL(t) + half * HO + lanes;
     bool partial = false;
@@ -1017,7 +1018,7 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
         const uint32_t parity = G::NT == 2 ? (done & 1) : ((done >> 1) & 1);
         ok = ok && bar_wait(bars + (kBarS + buf) * 8, parity, abort, p.wait_limit_ns);
         mma_fence_after();
-        const bool full = tile_full<KT>(p, m, kt);
+        const bool full = TREE ? (kt + 1) * KT <= w.len - w.n : tile_full<KT>(p, m, kt);
         // the half row in registers: tensor memory takes some 300 clocks to answer, once
         uint32_t s[HK];
 #pragma unroll
@@ -1032,7 +1033,7 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
             for (int i = 0; i < HK; i += 32) { // a bit per key that is seen
                 const int k0 = kt * KT + half * HK + i;
                 uint32_t see = below(hi - k0) & (~below(lo - k0) | below(sk - k0));
-                if (p.tree && valid)
+                if (TREE && valid)
                     see &= tree_bits(p, w.q0 + tok, w.len - w.n, k0);
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
@@ -1167,7 +1168,7 @@ __device__ __forceinline__ bool run_softmax(const AttnParams &p, const Work &w, 
 }
 
 // The results of run_softmax's rows, or their parts.
-template <class G>
+template <class G, bool TREE>
 __device__ __forceinline__ void store_rows(const AttnParams &p, const Work &w, const TileMask &m,
                                            int t, uint32_t tmem, int warp, int half, int lane,
                                            bool dirty, const RowState &st)
@@ -1213,7 +1214,7 @@ __device__ __forceinline__ void store_rows(const AttnParams &p, const Work &w, c
                 for (int k = k0; k < k0 + KT; ++k) {
                     if (!valid || !(k < hi && (k >= lo || k < sk)))
                         continue;
-                    if (p.tree && !(tree_bits(p, w.q0 + tok, w.len - w.n, k) & 1u))
+                    if (TREE && !(tree_bits(p, w.q0 + tok, w.len - w.n, k) & 1u))
                         continue;
                     bool bad = false;
                     const int64_t s = key_slot(p, w, k, key_block(p, w, k), bad);
@@ -1285,7 +1286,7 @@ __device__ __forceinline__ void drain(uint32_t bars, int tiles, volatile int *ab
 // barriers up meanwhile (two sets take turns), which takes 6500 clocks.  Chunks of several
 // units to a block: 181 us when all that was done in turn, 177 so (8 ragged, 28 heads over
 // 4), MLA 222 and 214, 4096 tokens over 16384 729 and 690.
-template <class G>
+template <class G, bool TREE>
 __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
     const __grid_constant__ AttnParams p)
 {
@@ -1346,7 +1347,7 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
                 if (mine) {
                     const Work w = s_work[k % 3];
                     const TileMask mask = tile_mask(p, w.n, w.len, w.row0 + t * kRows);
-                    store = run_softmax<G>(p, w, mask, t, tmem, ring, bars_of(k), wl, half, lane,
+                    store = run_softmax<G, TREE>(p, w, mask, t, tmem, ring, bars_of(k), wl, half, lane,
                                            (mask.rows + 31) / 32, careful, &s_abort, &s_dirty[k & 1],
                                            s_pairs, st, finite);
                 }
@@ -1364,7 +1365,7 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
                 mine = ask(k + 1);
             if (store) {
                 const Work w = s_work[k % 3];
-                store_rows<G>(p, w, tile_mask(p, w.n, w.len, w.row0 + t * kRows), t, tmem, wl, half,
+                store_rows<G, TREE>(p, w, tile_mask(p, w.n, w.len, w.row0 + t * kRows), t, tmem, wl, half,
                               lane, dirty, st);
             }
             if (more && !mine)
@@ -1510,25 +1511,25 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
         write_block_status(p.header, s_abort ? kStatusTimeout : s_status, blockIdx.x, p.status_words);
 }
 
-template <class G>
+template <class G, bool TREE>
 cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
 {
     constexpr int bytes = Smem<G>::BYTES;
     static_assert(bytes + sizeof(RowPairs<G>) + 3 * sizeof(Work) + 64 <= 227 * 1024, "shared memory");
     if (!G::QUANT) // e4m3 rows are converted on their way
         set_boxes<G>(p);
-    cudaError_t e = allow_smem<attention_kernel<G>>(bytes);
+    cudaError_t e = allow_smem<attention_kernel<G, TREE>>(bytes);
     if (e != cudaSuccess)
         return e;
     if (kShares<G>) { // the shares come out of what a block starts with, or it would wait
         cudaFuncAttributes fa;
-        if ((e = cudaFuncGetAttributes(&fa, attention_kernel<G>)) != cudaSuccess)
+        if ((e = cudaFuncGetAttributes(&fa, attention_kernel<G, TREE>)) != cudaSuccess)
             return e;
         if (G::SOFT_WARPS * kSoftRegs + G::LOAD_WARPS * kLoadRegs + 4 * kMmaRegs >
             kAttnThreads<G> / 32 * fa.numRegs)
             return cudaErrorInvalidConfiguration;
     }
-    attention_kernel<G><<<(unsigned)blocks, kAttnThreads<G>, bytes, stream>>>(p);
+    attention_kernel<G, TREE><<<(unsigned)blocks, kAttnThreads<G>, bytes, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     if (!p.slices)
@@ -1616,15 +1617,19 @@ cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cu
     p.by_heads = Divisor(kind == RowKind::Mla ? 2u : (uint32_t)p.kv_heads);
     p.by_splits = Divisor((uint32_t)p.max_splits);
     p.by_run = Divisor((uint32_t)std::max(1, p.split_tiles));
-    if (kind == RowKind::Mla)
-        return quant ? launch<MlaGeo<true>>(p, pl.blocks, stream)
-                     : launch<MlaGeo<false>>(p, pl.blocks, stream);
     if (pl.row_tiles == 0)
         return launch_attention_few(p, pl.blocks, stream);
-    if (pl.row_tiles == 2)
-        return launch<HeadGeo<false, 2>>(p, pl.blocks, stream);
-    return quant ? launch<HeadGeo<true, 1>>(p, pl.blocks, stream)
-                 : launch<HeadGeo<false, 1>>(p, pl.blocks, stream);
+    const auto run = [&](auto tree) {
+        constexpr bool TREE = decltype(tree)::value;
+        if (kind == RowKind::Mla)
+            return quant ? launch<MlaGeo<true>, TREE>(p, pl.blocks, stream)
+                         : launch<MlaGeo<false>, TREE>(p, pl.blocks, stream);
+        if (pl.row_tiles == 2)
+            return launch<HeadGeo<false, 2>, TREE>(p, pl.blocks, stream);
+        return quant ? launch<HeadGeo<true, 1>, TREE>(p, pl.blocks, stream)
+                     : launch<HeadGeo<false, 1>, TREE>(p, pl.blocks, stream);
+    };
+    return p.tree ? run(std::true_type{}) : run(std::false_type{});
 }
 
 } // namespace kvr

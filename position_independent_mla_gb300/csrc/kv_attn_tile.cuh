@@ -47,8 +47,7 @@ __device__ __forceinline__ TileMask tile_mask(const AttnParams &p, int n, int le
     const int i1 = p.by_group.quotient(row0 + max(m.rows, 1) - 1);
     m.pos0 = len - n + i0;
     m.pos1 = len - n + i1;
-    // every token of a tree sees the keys before the new ones
-    m.hi0 = p.tree ? max(0, len - n) : p.causal ? max(0, min(len, m.pos0 + 1)) : len;
+    m.hi0 = p.causal ? max(0, min(len, m.pos0 + 1)) : len;
     m.hi1 = p.causal ? max(0, min(len, m.pos1 + 1)) : len;
     m.lo0 = p.window ? max(0, m.pos0 - p.window + 1) : 0;
     m.lo1 = p.window ? max(0, m.pos1 - p.window + 1) : 0;
