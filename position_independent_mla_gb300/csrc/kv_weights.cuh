@@ -77,15 +77,15 @@ __device__ __forceinline__ void copy_box3(uint32_t dst, const CUtensorMap *map, 
                  : "memory");
 }
 
-// lse of a row of a row tile (-inf: there is none).
-__device__ __forceinline__ float row_lse(const WeightsParams &p, const SumWork &w, int head, int tile,
-                                         int row)
+// Where lse of a row of a row tile lies (nullptr: there is no such row).
+__device__ __forceinline__ const float *row_lse(const WeightsParams &p, const SumWork &w, int head,
+                                                int tile, int row)
 {
     const AttnParams &a = p.a;
     const int tok = a.by_group.quotient(row), at = tile * p.toks + tok;
-    return row < p.rows && at < w.n ? __ldg(p.lse + (int64_t)(w.q0 + at) * a.heads +
-                                            head * a.group + (row - tok * a.group))
-                                    : -INFINITY;
+    return row < p.rows && at < w.n ? p.lse + (int64_t)(w.q0 + at) * a.heads + head * a.group +
+                                          (row - tok * a.group)
+                                    : nullptr;
 }
 
 // -lse * log2 e of four rows (-inf: the row counts nothing).
@@ -95,7 +95,8 @@ __device__ __forceinline__ float4 row_offsets(const WeightsParams &p, const SumW
     float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float x = row_lse(p, w, head, tile, row + j);
+        const float *at = row_lse(p, w, head, tile, row + j);
+        const float x = at ? __ldg(at) : -INFINITY;
         v[j] = x == -INFINITY ? -INFINITY : -x * 1.4426950408889634f;
     }
     return make_float4(v[0], v[1], v[2], v[3]);

@@ -27,7 +27,7 @@ namespace kvr {
 
 namespace {
 
-constexpr int kManyStages = 4, kManyParts = 3;
+constexpr int kManyStages = 4, kManyParts = 3, kManyAhead = 8;
 constexpr int kManySum = 16; // warps, then
 constexpr int kManyKey = kManySum, kManyLoad = kManyKey + 4, kManyLse = kManyLoad + 1,
               kManyMma = kManyLse + 1, kManyFind = kManyMma + 1;
@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) weights_many_kernel(
     __shared__ volatile int s_abort;
     __shared__ int s_bad;
     __shared__ float s_sum[256]; // of a half's threads
+    __shared__ float s_lse[kManyAhead * 128];
     __shared__ Part s_part[kManyParts];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ones = (smem_u32(raw_smem) + 1023u) & ~1023u, ring = ones + kManyPanel;
@@ -364,52 +365,79 @@ __global__ void __launch_bounds__(kManyThreads, 1) weights_many_kernel(
                 bar_wait(bar(kManyFull + st), phase ^ 1 ^ (wrapped ? 1 : 0), &none, 10000000ll);
             }
         } else if (warp == kManyLse) {
-            // -lse / scale as the sum of three bf16 (24 bits, as many as it has)
+            // -lse / scale as the sum of three bf16 (24 bits, as many as it has).  lse comes
+            // kManyAhead steps ahead, into places that the same thread reads: asked for one
+            // step ahead it held every step up for the time of a load, 1200 clocks.
             const float by = -1.0f / a.scale;
+            const uint32_t raw = smem_u32(s_lse);
+            int my_tok[4], my_at[4]; // of this lane's rows in a row tile: token; place from its first row's on
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = j * 32 + lane, t = a.by_group.quotient(r);
+                my_tok[j] = r < p.rows ? t : 0x40000000;
+                my_at[j] = t * a.heads + r - t * a.group;
+            }
             int stage = 0, phase = 1;
             bool ok = true;
             while (ok && part_there()) {
                 const SumWork w = s_part[at].w;
-                Runs run(w);
-                while (ok && run.next()) {
-                    float next[4], now[4];
-                    auto ask = [&](int tile) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            next[j] = row_lse(p, w, run.head, tile, j * 32 + lane);
-                    };
-                    ask(run.tile);
-                    for (int tile = run.tile; tile < run.end; ++tile) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            now[j] = next[j];
-                        if (tile + 1 < run.end)
-                            ask(tile + 1);
-                        ok = wait(kManyEmpty + stage, phase);
-                        if (!ok)
-                            break;
-                        const uint32_t to = ring + stage * kManyStage + 2 * kManyPanel;
+                const int head0 = w.tiles ? w.step0 / w.tiles : 0, first = w.step0 - head0 * w.tiles;
+                int tile = first, tok = (w.ra + first) * p.toks; // of the sequence's tokens
+                const float *from = p.lse + (int64_t)(w.q0 + tok) * a.heads + head0 * a.group;
+                auto ask = [&](int s) { // the steps in turn
+                    if (s < w.step1) {
+                        const uint32_t to = raw + ((s & (kManyAhead - 1)) * 128 + lane) * 4;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int r = j * 32 + lane;
-                            // -infinity: the row counts nothing, or there is none
-                            const float v = now[j] == -INFINITY ? -INFINITY : now[j] * by;
-                            const uint32_t hi = pack_bf16(v, 0.0f);
-                            const float v1 = isinf(v) ? 0.0f : v - __uint_as_float(hi << 16);
-                            const uint32_t mid = pack_bf16(v1, 0.0f);
-                            const uint32_t lo = pack_bf16(v1 - __uint_as_float(mid << 16), 0.0f);
-                            sts16(to + r * 128 + ((r & 7) << 4), make_uint4(hi | mid << 16, lo, 0, 0));
+                            if (tok + my_tok[j] < w.n)
+                                copy4(to + j * 128, from + my_at[j]);
+                            else
+                                sts4(to + j * 128, -INFINITY);
                         }
-                        async_fence();
-                        __syncwarp();
-                        if (lane == 0)
-                            bar_signal(bar(kManyFull + stage));
-                        if (++stage == kManyStages) {
-                            stage = 0;
-                            phase ^= 1;
+                        tok += p.toks;
+                        from += p.toks * a.heads;
+                        if (++tile == w.tiles) { // the next head
+                            tile = 0;
+                            tok -= w.tiles * p.toks;
+                            from += a.group - (int64_t)w.tiles * p.toks * a.heads;
                         }
                     }
+                    copy_commit();
+                };
+                for (int s = w.step0; s < w.step0 + kManyAhead - 1; ++s)
+                    ask(s);
+                for (int s = w.step0; s < w.step1; ++s) {
+                    ask(s + kManyAhead - 1);
+                    copy_wait<kManyAhead - 1>();
+                    uint4 parts[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float lse = lds4(raw + ((s & (kManyAhead - 1)) * 128 + j * 32 + lane) * 4);
+                        // -infinity: the row counts nothing, or there is none
+                        const float v = lse == -INFINITY ? -INFINITY : lse * by;
+                        const uint32_t hi = pack_bf16(v, 0.0f);
+                        const float v1 = isinf(v) ? 0.0f : v - __uint_as_float(hi << 16);
+                        const uint32_t mid = pack_bf16(v1, 0.0f);
+                        const uint32_t lo = pack_bf16(v1 - __uint_as_float(mid << 16), 0.0f);
+                        parts[j] = make_uint4(hi | mid << 16, lo, 0, 0);
+                    }
+                    ok = wait(kManyEmpty + stage, phase);
+                    if (!ok)
+                        break;
+                    const uint32_t to = ring + stage * kManyStage + 2 * kManyPanel;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        sts16(to + (j * 32 + lane) * 128 + ((lane & 7) << 4), parts[j]);
+                    async_fence();
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_signal(bar(kManyFull + stage));
+                    if (++stage == kManyStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
                 }
+                copy_wait<0>();
                 part_done();
             }
         } else if (warp == kManyMma) {
@@ -427,7 +455,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) weights_many_kernel(
                         ok = wait(kManyFull + stage, phase);
                         if (!ok)
                             break;
-                        async_fence();
                         const uint32_t q = operand(ring + stage * kManyStage, 16);
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
@@ -464,11 +491,18 @@ __global__ void __launch_bounds__(kManyThreads, 1) weights_many_kernel(
             bar_wait(bar(kManyEnd), 0, &none, 1000000000ll);
             __syncwarp();
         } else { // find
+            // one part of each 152, from the front and from the back in turn: the last keys of a
+            // causal sequence have the fewest steps
             bool bad = false, ok = true;
-            for (int64_t n = blockIdx.x; ok; n += gridDim.x) {
+            const int64_t rounds = (p.total_parts + gridDim.x - 1) / gridDim.x;
+            for (int64_t r = 0; ok; ++r) {
                 SumWork w{};
+                int64_t n = 0;
                 bool there = false;
-                for (; n < p.total_parts; n += gridDim.x) {
+                for (; r < rounds; ++r) {
+                    n = r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                    if (n >= p.total_parts)
+                        continue;
                     const int64_t unit = n / p.parts, tile = unit / a.num_seqs;
                     w.seq = (int)(unit - tile * a.num_seqs);
                     int64_t q0;
