@@ -1690,10 +1690,11 @@ kv_status kv_tree_attention_quant(const kv_quant_pool_desc *pool, int32_t layer,
 
 namespace {
 
-WeightsPlan weights_plan(RowKind kind, const kv_attn_desc *a, int64_t total_q, int32_t heads,
-                         int32_t kv_heads)
+WeightsPlan weights_plan(RowKind kind, bool quant, const kv_attn_desc *a, int64_t total_q,
+                         int32_t heads, int32_t kv_heads)
 {
     AttnShape s{};
+    s.quant = quant;
     s.total_q = total_q;
     s.num_seqs = a->num_seqs;
     s.max_q_len = a->max_q_len;
@@ -1706,12 +1707,12 @@ WeightsPlan weights_plan(RowKind kind, const kv_attn_desc *a, int64_t total_q, i
 // Workspace: header, a status word per block, sums of parts.
 size_t weights_parts_at(const WeightsPlan &pl)
 {
-    return align256(kHeaderBytes + (size_t)pl.blocks * 4);
+    return align256(kHeaderBytes + (size_t)pl.most_blocks() * 4);
 }
 
 size_t weights_bytes(const WeightsPlan &pl)
 {
-    return pl.blocks > 0x7FFFFFFFll ? 0 : weights_parts_at(pl) + align256(pl.part_bytes);
+    return pl.most_blocks() > 0x7FFFFFFFll ? 0 : weights_parts_at(pl) + align256(pl.part_bytes);
 }
 
 kv_status weights_impl(AttnParams p, RowKind kind, int64_t num_slots, int32_t block,
@@ -1736,7 +1737,7 @@ kv_status weights_impl(AttnParams p, RowKind kind, int64_t num_slots, int32_t bl
         !aligned_to(a->d_q_off, 4) || !aligned_to(a->d_kv_len, 4) ||
         !aligned_to(a->d_block_tables, 4) || num_slots > 0x7FFFFFFFll)
         return KV_ERR_INVALID_ARG;
-    const WeightsPlan pl = weights_plan(kind, a, total_q, heads, kv_heads);
+    const WeightsPlan pl = weights_plan(kind, p.cs != nullptr, a, total_q, heads, kv_heads);
     const size_t need = weights_bytes(pl);
     if (need == 0)
         return KV_ERR_INVALID_ARG;
@@ -1795,7 +1796,7 @@ size_t kv_attention_weights_workspace_size(const kv_pool_desc *pool, const kv_at
     if (!pool_ok(pool) || !row_kind(pool, &kind) ||
         attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK)
         return 0;
-    return weights_bytes(weights_plan(kind, attn, total_q, num_heads, pool->rot_heads));
+    return weights_bytes(weights_plan(kind, false, attn, total_q, num_heads, pool->rot_heads));
 }
 
 size_t kv_attention_weights_quant_workspace_size(const kv_quant_pool_desc *pool,
@@ -1806,7 +1807,7 @@ size_t kv_attention_weights_quant_workspace_size(const kv_quant_pool_desc *pool,
     if (!quant_pool_ok(pool) || !quant_row_kind(pool, &kind) ||
         attn_ok(attn, total_q, num_heads, pool->rot_heads) != KV_OK)
         return 0;
-    return weights_bytes(weights_plan(kind, attn, total_q, num_heads, pool->rot_heads));
+    return weights_bytes(weights_plan(kind, true, attn, total_q, num_heads, pool->rot_heads));
 }
 
 kv_status kv_attention_weights(const kv_pool_desc *pool, int32_t layer, const kv_attn_desc *attn,

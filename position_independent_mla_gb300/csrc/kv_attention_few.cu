@@ -79,39 +79,11 @@ __device__ __forceinline__ uint32_t few_weight(int key)
     return (key >> 3) * (G::P_BYTES / 16) + (key & 7) * 16;
 }
 
-// Two values to e5m2 parts x = a + b / 8 + c / 64.
-__device__ __forceinline__ void split_e5m2(float x, float y, uint32_t (&part)[3])
-{
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        uint16_t h;
-        uint32_t w;
-        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(h) : "f"(y), "f"(x));
-        part[i] = h;
-        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(w) : "h"(h));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-        x = (x - f.x) * 8.0f;
-        y = (y - f.y) * 8.0f;
-    }
-}
-
 // What the softmax warps share: maxima of a tile, and the references (in units of log2) with
 // the factors of their last growth; of the scores, and (e4m3) of the weights.
 struct FewRefs {
     float top[2][4][kFewRows], ref[2][kFewRows], grow[2][kFewRows];
 };
-
-// Eight values to eight bytes of each part.
-__device__ __forceinline__ void split8(const float *x, uint2 (&to)[3])
-{
-    uint32_t h[4][3];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        split_e5m2(x[2 * i], x[2 * i + 1], h[i]);
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-        to[k] = make_uint2(h[0][k] | (h[1][k] << 16), h[2][k] | (h[3][k] << 16));
-}
 
 // This thread's values of the R rows in tensor memory.  16 rows in three parts come in two
 // steps, half of the registers at a time.
@@ -477,35 +449,13 @@ __device__ __forceinline__ void few_queries_e5m2(const AttnParams &p, const Work
         if (r < p.group)
             v = __ldg(reinterpret_cast<const uint4 *>(
                     p.q + w.q0 * p.q_ts + (int64_t)(w.head * p.group + r) * p.q_hs) + c);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t a = u[i] & 0x7FFFu, b = (u[i] >> 16) & 0x7FFFu;
-            m = max(m, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
-        }
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1)
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        // 2^e of the row's scale: the exponent of its largest value, less 14
-        const int e = max((int)(m >> 7) - 141, -120);
-        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(u[i] << 16) * inv;
-            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u) * inv;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) // what was infinite is NaN
-            x[i] = fabsf(x[i]) < 32768.0f ? x[i] : __uint_as_float(0x7FC00000u);
         uint2 part[3];
-        split8(x, part);
+        const float scale = query_e5m2(v, part);
 #pragma unroll
         for (int k = 0; k < 3; ++k)
             store(k * G::R + r, part[k]);
         if (c == 0)
-            q_scale[r] = __uint_as_float((uint32_t)(127 + e) << 23);
+            q_scale[r] = scale;
     }
 }
 

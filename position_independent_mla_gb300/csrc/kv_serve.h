@@ -215,7 +215,8 @@ struct SelectParams {
 int select_cluster(int32_t num_seqs, int32_t max_kv_len);
 cudaError_t launch_select(const SelectParams &p, cudaStream_t stream);
 
-// What each key receives of the queries' attention (kv_weights.cu, kv_weights_many.cu).
+// What each key receives of the queries' attention (kv_weights.cu, kv_weights_few.cu,
+// kv_weights_many.cu).
 struct WeightsParams {
     AttnParams a; // the batch, its pool and its queries; out and the split have no part
     const float *lse;
@@ -227,6 +228,7 @@ struct WeightsParams {
     int64_t total_parts;   // many row tiles: of the call; a.part holds 256 sums of each
     int32_t stages;
     int32_t q_boxes;       // query rows come as boxes of q_map
+    int32_t run, row_pad;  // few rows: key tiles of a block; rows of a head, to a power of two
     Divisor by_toks;
     CUtensorMap q_map;
 };
@@ -237,6 +239,12 @@ struct WeightsPlan {
     int64_t blocks, units;
     int32_t smem;
     size_t part_bytes; // of the workspace, for sums of parts
+    // few rows, where the pool's rows come as boxes
+    bool few;
+    int32_t few_parts, few_stages, run, row_pad, few_smem;
+    int64_t few_blocks;
+
+    int64_t most_blocks() const { return few && few_blocks > blocks ? few_blocks : blocks; }
 
     int launches() const { return many && parts > 1 ? 2 : 1; }
 };

@@ -497,6 +497,7 @@ WeightsPlan plan_weights(RowKind kind, const AttnShape &a)
     const int room = 2 * stage > kSumSmem ? kSumSmemAlone : kSumSmem;
     pl.stages = std::min(kSumMaxStages, room / stage);
     pl.smem = pl.stages * stage + 1024;
+    plan_weights_few(kind, a, pl);
     return pl;
 }
 
@@ -513,6 +514,13 @@ cudaError_t launch_weights(WeightsParams &p, RowKind kind, const WeightsPlan &pl
     p.by_toks = Divisor((uint32_t)pl.toks);
     p.a.by_group = Divisor((uint32_t)p.a.group);
     p.a.by_block = Divisor((uint32_t)p.a.block);
+    if (pl.few) {
+        WeightsParams few = p;
+        bool done = false;
+        const cudaError_t e = launch_weights_few(few, kind, pl, stream, done);
+        if (e != cudaSuccess || done)
+            return e;
+    }
     p.q_boxes = encode_queries(p, kind == RowKind::Mla ? 576 : 128);
     if (pl.many)
         return launch_weights_many(p, pl, stream);

@@ -155,6 +155,13 @@ inline bool encode_queries(WeightsParams &p, int width)
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A sequence's queries in one row tile, few rows to a key head or latent rows
+// (kv_weights_few.cu): whether such a call is planned that way, and the launch.  `done`: the
+// pool's rows come as boxes; otherwise nothing was launched.
+void plan_weights_few(RowKind kind, const AttnShape &a, WeightsPlan &pl);
+cudaError_t launch_weights_few(WeightsParams &p, RowKind kind, const WeightsPlan &pl,
+                               cudaStream_t stream, bool &done);
+
 // Head rows under more than one row tile (kv_weights_many.cu).
 cudaError_t launch_weights_many(WeightsParams &p, const WeightsPlan &pl, cudaStream_t stream);
 

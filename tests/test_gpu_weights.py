@@ -198,3 +198,34 @@ def test_many_queries_with_more_units_than_parts():
 @pytest.mark.parametrize("window,sinks", [(300, 4), (40, 300), (1, 0)])
 def test_many_queries_under_a_window(window, sinks):
     Sums("gqa", [(500, 1500), (200, 200)], 32, window=window, sinks=sinks, seed=22).check()
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("kind,heads,n", [("gqa", 8, 1), ("gqa", 16, 1), ("gqa", 24, 1), ("gqa", 32, 4),
+                                          ("gqa", 64, 2), ("gqa", 128, 1), ("gqa4", 4, 3), ("gqa4", 28, 2),
+                                          ("mha", 32, 1), ("mha", 32, 3), ("mha", 32, 5), ("mha", 32, 16),
+                                          ("mla", 5, 2), ("mla", 16, 3), ("mla", 48, 1), ("mla", 128, 1)])
+def test_few_rows(kind, heads, n, quant):
+    Sums(kind, [(n, 130), (1, 300), (n, 2000), (0, 65), (n, n)], heads, quant=quant, seed=23,
+         keep=0.7).check()
+
+
+@pytest.mark.parametrize("kind,heads,quant", [("gqa", 32, False), ("gqa", 32, True), ("mla", 64, False)])
+def test_few_rows_in_runs(kind, heads, quant):
+    # so many sequences that a block takes several key tiles
+    lens = [(1, 1100 + 37 * i) for i in range(64)] + [(1, 20000)]
+    Sums(kind, lens, heads, quant=quant, seed=24, block=16).check()
+
+
+@pytest.mark.parametrize("kind,heads,quant", [("gqa", 32, False), ("gqa", 32, True), ("mla", 64, False)])
+def test_few_rows_under_a_window(kind, heads, quant):
+    lens = [(1, 1100 + 37 * i) for i in range(40)]
+    Sums(kind, lens, heads, quant=quant, seed=25, window=200, sinks=4).check()
+
+
+def test_few_rows_queries_far_apart_over_quantised_rows():
+    s = Sums("gqa", [(2, 700)], 32, quant=True, seed=26)
+    s.q[0, :, ::3] *= 2.0 ** -12
+    s.q[1, 5] = 0.0
+    s.lse = s.scores_lse().float().contiguous()
+    s.check()
