@@ -228,7 +228,8 @@ struct WeightsParams {
     int64_t total_parts;   // many row tiles: of the call; a.part holds 256 sums of each
     int32_t stages;
     int32_t q_boxes;       // query rows come as boxes of q_map
-    int32_t run, row_pad;  // few rows: key tiles of a block; rows of a head, to a power of two
+    int32_t run, slices;   // few rows: key tiles of a block, or equal slices of all of them;
+    int32_t row_pad;       // rows of a head, to a power of two
     Divisor by_toks;
     CUtensorMap q_map;
 };
@@ -240,7 +241,7 @@ struct WeightsPlan {
     int32_t smem;
     size_t part_bytes; // of the workspace, for sums of parts
     // few rows, where the pool's rows come as boxes
-    bool few;
+    bool few, few_slices;
     int32_t few_parts, few_stages, run, row_pad, few_smem;
     int64_t few_blocks;
 

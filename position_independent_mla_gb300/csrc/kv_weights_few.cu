@@ -35,8 +35,10 @@ struct FewSum {
     static constexpr int BLOCKS = MLA ? 1 : 2; // to an SM
 };
 
-constexpr int kFewSumThreads = 192; // 4 sum warps, load, mma
+constexpr int kFewSumThreads = 192; // 4 sum warps, mma, load
+constexpr int kFewWorkers = 160;    // all but the load warp, which runs ahead of them
 constexpr int kFewSumStages = 6, kFewSumBufs = 4, kFewSumRows = 512;
+constexpr int kFewSeqs = 1024; // most sequences whose tiles a block counts
 constexpr int kFewSumRoom = 104 * 1024, kFewSumRoomMla = 212 * 1024;
 
 enum {
@@ -44,7 +46,8 @@ enum {
     kFewEmpty = kFewSumStages,
     kFewS = 2 * kFewSumStages,
     kFewRead = kFewS + kFewSumBufs,
-    kFewEnd = kFewRead + kFewSumBufs,
+    kFewQ = kFewRead + kFewSumBufs, // latent rows: queries as boxes
+    kFewEnd,
     kFewBars
 };
 
@@ -85,81 +88,41 @@ __device__ __forceinline__ void mma_window(uint32_t d, uint32_t a, uint32_t b, u
                      : "memory");
 }
 
+// A vote over the block's workers, also their meeting point.
+__device__ __forceinline__ bool workers_any(bool x)
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 q, %1, 0;\n"
+                 "barrier.cta.red.or.pred p, 1, %2, q;\nselp.b32 %0, 1, 0, p;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)x), "n"(kFewWorkers)
+                 : "memory");
+    return r != 0;
+}
+
+// The queries of a sequence, heads [h0, h1) of them, with the factors and offsets of their
+// rows, by the block's workers.  Latent rows come as boxes (p.q_boxes) elsewhere.
 template <class G>
-__global__ void __launch_bounds__(kFewSumThreads, G::BLOCKS) weights_few_kernel(
-    const __grid_constant__ WeightsParams p)
+__device__ __forceinline__ void bring_queries(const WeightsParams &p, const SumWork &w, uint32_t q_smem,
+                                              int h0, int h1, int n, int tid, float2 *s_row)
 {
     const AttnParams &a = p.a;
-    extern __shared__ unsigned char raw_smem[];
-    __shared__ __align__(8) uint64_t s_bars[kFewBars];
-    __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_abort;
-    __shared__ int s_bad;
-    __shared__ float2 s_row[kFewSumRows]; // of a query row: factor of its scores, offset
-    __shared__ float s_part[128 + 1];     // and whether the block gave up
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = (int)blockIdx.x % p.parts, unit = (int)blockIdx.x / p.parts;
-    const int run = unit / a.num_seqs, seq = unit - run * a.num_seqs;
-    auto leave = [&](uint32_t code) {
-        if (tid == 0)
-            write_block_status(a.header, code, blockIdx.x, gridDim.x);
-    };
-    SumWork w{};
-    w.seq = seq;
-    int64_t q0;
-    const bool fits = seq_queries(a, seq, q0, w.n) && seq_keys(a, seq, w.len);
-    const int64_t first = (int64_t)run * p.run * 128;
-    if (!fits || first >= w.len) { // the same for the whole cluster
-        leave(fits || run > 0 ? kStatusOk : kStatusOutOfRange);
-        return;
-    }
-    w.q0 = (int)q0;
-    w.base = w.len - w.n;
-    const int tile0 = run * p.run, tile1 = min(tile0 + p.run, (w.len + 127) / 128);
-    const int h0 = G::MLA ? 0 : a.kv_heads * rank / p.parts;
-    const int h1 = G::MLA ? 1 : a.kv_heads * (rank + 1) / p.parts;
-    const int rows = w.n * a.group; // of a head
-    // some query sees some key of a tile
-    auto seen = [&](int tile) {
-        const int64_t k1 = min(w.len, tile * 128 + 128) - 1;
-        return w.n > 0 && (!a.window || tile * 128 < a.sinks || k1 + a.window - w.base > 0);
-    };
-
-    const uint32_t ring = (smem_u32(raw_smem) + 1023u) & ~1023u;
-    const uint32_t q_smem = ring + p.stages * G::STAGE;
-    const uint32_t bars = smem_u32(s_bars);
-    const int64_t limit = a.wait_limit_ns;
-    auto bar = [&](int i) { return bars + i * 8; };
-    auto wait = [&](int i, int parity) { return bar_wait(bar(i), parity, &s_abort, limit); };
-    const int rp = p.row_pad;                   // head rows: rows of a head, to a power of two
-    const int rq = G::QUANT ? 4 * rp : rp;      // and of its parts
-    const int n = G::MLA ? p.n : max(16, rq);   // columns of S
-    const int bufs = n > 32 ? 2 : kFewSumBufs;  // buffers of S, and columns that are read behind them
-    const uint32_t columns = n <= 16 ? 128 : 256;
-    if (warp == 5) {
-        tmem_alloc(smem_u32(&s_tmem), columns);
-    } else if (tid == 0) {
-        s_abort = 0;
-        s_bad = 0;
-        for (int i = 0; i < kFewBars; ++i)
-            bar_init(bar(i), i >= kFewRead && i < kFewEnd ? 4 : 1);
-        bar_init_fence();
-    }
-    // queries
     const float c = a.scale * 1.4426950408889634f;
+    const int rp = p.row_pad, rq = G::QUANT ? 4 * rp : rp, rows = w.n * a.group;
     auto query = [&](int head, int r) {
         const int tok = a.by_group.quotient(r);
         return a.q + (int64_t)(w.q0 + tok) * a.q_ts + (int64_t)(head * a.group + r - tok * a.group) * a.q_hs;
     };
     if constexpr (G::MLA) {
-        for (int i = tid; i < n * 72; i += kFewSumThreads) {
-            const int r = i / 72, piece = i - r * 72;
-            const uint4 v = r < rows ? __ldg(reinterpret_cast<const uint4 *>(query(0, r)) + piece)
-                                     : make_uint4(0, 0, 0, 0);
-            sts16(q_smem + (piece >> 3) * n * 128 + r * 128 + (((piece & 7) ^ (r & 7)) << 4), v);
-        }
+        if (!p.q_boxes)
+            for (int i = tid; i < p.rows * 72; i += kFewWorkers) {
+                const int r = i / 72, piece = i - r * 72;
+                const uint4 v = r < rows ? __ldg(reinterpret_cast<const uint4 *>(query(0, r)) + piece)
+                                         : make_uint4(0, 0, 0, 0);
+                sts16(q_smem + (piece >> 3) * n * 128 + r * 128 + (((piece & 7) ^ (r & 7)) << 4), v);
+            }
     } else {
-        const int pieces = 16, per = kFewSumThreads / pieces, cc = tid & 15;
+        const int pieces = 16, per = kFewWorkers / pieces, cc = tid & 15;
         const uint32_t panel = query_rows(a.kv_heads, rq) * 128;
         for (int i = h0 * rp + tid / pieces; i - tid / pieces < h1 * rp; i += per) {
             const int head = i / rp, r = i - head * rp;
@@ -188,7 +151,7 @@ __global__ void __launch_bounds__(kFewSumThreads, G::BLOCKS) weights_few_kernel(
             }
         }
     }
-    for (int i = tid; i < (G::MLA ? n : a.kv_heads * rp); i += kFewSumThreads) {
+    for (int i = tid; i < (G::MLA ? n : a.kv_heads * rp); i += kFewWorkers) {
         const int head = G::MLA ? 0 : i / rp, r = i - head * rp;
         float x = -INFINITY;
         if (r < rows) {
@@ -200,137 +163,179 @@ __global__ void __launch_bounds__(kFewSumThreads, G::BLOCKS) weights_few_kernel(
         if (G::MLA)
             s_row[i].x = c;
     }
+}
+
+template <class G>
+__global__ void __launch_bounds__(kFewSumThreads, G::BLOCKS) weights_few_kernel(
+    const __grid_constant__ WeightsParams p)
+{
+    const AttnParams &a = p.a;
+    extern __shared__ unsigned char raw_smem[];
+    __shared__ __align__(8) uint64_t s_bars[kFewBars];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    __shared__ int s_bad;
+    __shared__ float2 s_row[kFewSumRows]; // of a query row: factor of its scores, offset
+    __shared__ float s_part[128 + 1];     // and whether the block gave up
+    __shared__ int s_end[kFewSeqs];       // key tiles up to the end of a sequence
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    SumWork w{};
+    int tile0 = 0, tile1 = 0; // key tiles of w.seq
+    auto look = [&](int seq) {
+        w.seq = seq;
+        int64_t q0;
+        const bool fits = seq_queries(a, seq, q0, w.n) && seq_keys(a, seq, w.len);
+        w.q0 = (int)q0;
+        w.base = w.len - w.n;
+        return fits;
+    };
+    const int rank = (int)blockIdx.x % p.parts;
+    const int h0 = G::MLA ? 0 : a.kv_heads * rank / p.parts;
+    const int h1 = G::MLA ? 1 : a.kv_heads * (rank + 1) / p.parts;
+    // some query sees some key of a tile
+    auto seen = [&](int tile) {
+        const int64_t k1 = min(w.len, tile * 128 + 128) - 1;
+        return w.n > 0 && (!a.window || tile * 128 < a.sinks || k1 + a.window - w.base > 0);
+    };
+    // The block's key tiles: a run of one sequence, or an equal slice of all tiles of the call,
+    // sequence by sequence.
+    int64_t pos = 0, end = 0;
+    bool bad = false;
+    if (!p.slices) {
+        const int unit = (int)blockIdx.x / p.parts, run = unit / a.num_seqs;
+        const bool fits = look(unit - run * a.num_seqs);
+        bad = !fits;
+        tile0 = run * p.run;
+        tile1 = fits ? (int)min((int64_t)tile0 + p.run, ((int64_t)w.len + 127) / 128) : 0;
+        if (tile0 >= tile1) { // the same for the whole cluster
+            if (tid == 0)
+                write_block_status(a.header, bad && run == 0 ? kStatusOutOfRange : kStatusOk,
+                                   blockIdx.x, gridDim.x);
+            return;
+        }
+    } else {
+        for (int s = tid; s < a.num_seqs; s += kFewSumThreads) {
+            const bool fits = look(s);
+            bad |= !fits;
+            s_end[s] = fits ? (w.len + 127) >> 7 : 0;
+        }
+        bad = __syncthreads_or(bad) != 0;
+        if (warp == 0) {
+            int sum = 0;
+            for (int s = lane; s - lane < a.num_seqs; s += 32) {
+                int x = s < a.num_seqs ? s_end[s] : 0;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xFFFFFFFFu, x, d);
+                    if (lane >= d)
+                        x += o;
+                }
+                x += sum;
+                if (s < a.num_seqs)
+                    s_end[s] = x;
+                sum = __shfl_sync(0xFFFFFFFFu, x, 31);
+            }
+        }
+        __syncthreads();
+        const int64_t total = s_end[a.num_seqs - 1];
+        pos = total * blockIdx.x / gridDim.x;
+        end = total * (blockIdx.x + 1) / gridDim.x;
+    }
+    auto next_segment = [&] {
+        if (pos >= end)
+            return false;
+        int lo = 0, hi = a.num_seqs - 1; // the first sequence that ends behind pos
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (s_end[mid] > pos)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        const int before = lo > 0 ? s_end[lo - 1] : 0;
+        look(lo);
+        tile0 = (int)(pos - before);
+        tile1 = (int)(min(end, (int64_t)s_end[lo]) - before);
+        pos += tile1 - tile0;
+        return true;
+    };
+
+    const uint32_t ring = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const uint32_t q_smem = ring + p.stages * G::STAGE;
+    const uint32_t bars = smem_u32(s_bars);
+    const int64_t limit = a.wait_limit_ns;
+    auto bar = [&](int i) { return bars + i * 8; };
+    auto wait = [&](int i, int parity) { return bar_wait(bar(i), parity, &s_abort, limit); };
+    const int rp = p.row_pad;                   // head rows: rows of a head, to a power of two
+    const int rq = G::QUANT ? 4 * rp : rp;      // and of its parts
+    const int n = G::MLA ? p.n : max(16, rq);   // columns of S
+    const int bufs = n > 32 ? 2 : kFewSumBufs;  // buffers of S, and columns that are read behind them
+    const uint32_t columns = n <= 16 ? 128 : 256;
+    if (warp == 4) {
+        tmem_alloc(smem_u32(&s_tmem), columns);
+    } else if (tid == 0) {
+        s_abort = 0;
+        s_bad = 0;
+        for (int i = 0; i < kFewBars; ++i)
+            bar_init(bar(i), i >= kFewRead && i < kFewQ ? 4 : 1);
+        bar_init_fence();
+    }
+    if (G::MLA) // rows that pad the queries
+        for (int i = tid; i < (n - p.rows) * 72; i += kFewSumThreads) {
+            const int r = p.rows + i / 72, piece = i % 72;
+            sts16(q_smem + (piece >> 3) * n * 128 + r * 128 + ((piece & 7) << 4), make_uint4(0, 0, 0, 0));
+        }
     async_fence();
     mma_fence_before();
     __syncthreads();
     mma_fence_after();
     const uint32_t tmem = s_tmem;
-
-    if (warp < 4) { // sum
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        float *const weight = p.weights + seq * p.weight_stride;
-        int64_t slot = sum_slot(a, w, tile0 * 128 + tid);
-        uint32_t i = 0; // steps so far
-        bool ok = true;
-        for (int tile = tile0; ok && tile < tile1; ++tile) {
-            const int k = tile * 128 + tid;
-            const bool mine = slot >= 0;
-            const float *const scale = a.rs + (mine ? slot * a.rs_ss : 0);
-            if (k < w.len && !mine)
-                s_bad = 1;
-            slot = tile + 1 < tile1 ? sum_slot(a, w, k + 128) : -1; // of the next tile
-            const float old = p.parts == 1 && k < w.len && p.keep != 0.0f ? weight[k] : 0.0f;
-            const TokenRange see = tokens_of(a, w, k, 1);
-            const int lo = see.lo * a.group, hi = mine ? see.hi * a.group : 0; // rows that see this key
-            float sum = 0.0f;
-            if (seen(tile)) {
-                float next = G::QUANT && mine ? __ldg(scale + h0) : 1.0f;
-                for (int head = h0; head < h1; ++head, ++i) {
-                    const int buf = (int)i % bufs, at = G::MLA ? 0 : head * rq & 7;
-                    const uint32_t from = tmem + buf * n + at + lanes;
-                    const float ks = next;
-                    if (G::QUANT && mine && head + 1 < h1)
-                        next = __ldg(scale + head + 1);
-                    ok = wait(kFewS + buf, (i / bufs) & 1);
-                    if (!ok)
-                        break;
-                    mma_fence_after();
-                    const float2 *const row = s_row + (G::MLA ? 0 : head * rp);
-                    if constexpr (G::MLA) {
-                        f2 part[2] = {0ull, 0ull};
-                        for (int col = 0; col < rows; col += 32) {
-                            uint32_t x[32];
-                            tmem_ld32(from + col, x);
-                            tmem_ld_wait();
-                            tmem_pin32(x);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const float2 o = row[col + j];
-                                const float e = exp2_fast(fmaf(__uint_as_float(x[j]), o.x, o.y));
-                                part[j & 1] = f2_add(
-                                    part[j & 1],
-                                    f2_of_bits(col + j >= lo && col + j < hi ? __float_as_uint(e) : 0u, 0u));
+    // places in the rings, which each role keeps from one segment to the next
+    int stage = 0, phase = 0;
+    bool ok = true, more = !p.slices || next_segment();
+    if (warp == 5) { // load
+        int filled = 0;
+        phase = 1;
+        for (; ok && more; more = p.slices && next_segment()) {
+            // a tile is `per` blocks of the pool, or a part of one: a lane's first key of a box
+            const int per = 128 / a.box_rows;
+            auto box_slot = [&](int tile) {
+                return lane < per && tile < tile1 ? sum_slot(a, w, tile * 128 + lane * a.box_rows) : -1;
+            };
+            int64_t next = box_slot(tile0);
+            for (int tile = tile0; ok && tile < tile1; ++tile) {
+                const int64_t slot = next;
+                next = box_slot(tile + 1);
+                const uint32_t many = __popc(__ballot_sync(0xFFFFFFFFu, slot >= 0)) * a.box_rows;
+                if (!seen(tile))
+                    continue;
+                for (int head = h0; ok && head < h1; ++head) {
+                    for (int chunk = 0; chunk < G::CHUNKS; ++chunk) {
+                        ok = wait(kFewEmpty + stage, phase);
+                        if (!ok)
+                            break;
+                        const uint32_t full = bar(kFewFull + stage);
+                        if (lane == 0)
+                            bar_signal_bulk(full, 1, many * (G::STAGE / 128));
+                        __syncwarp();
+                        if (slot >= 0) {
+                            const uint32_t to = ring + stage * G::STAGE + lane * a.box_rows * 128;
+                            if (G::MLA) {
+                                if (chunk < 8)
+                                    copy_box(to, &a.copy_map, chunk * 64, (int)slot, full);
+                                else
+                                    copy_box(to, &a.rot_map, 0, (int)slot, full);
+                            } else {
+                                copy_box(to, &a.rot_map, head * 128, (int)slot, full);
+                                if (!G::QUANT)
+                                    copy_box(to + 16384, &a.rot_map, head * 128 + 64, (int)slot, full);
                             }
                         }
-                        float s0, s1;
-                        asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(f2_add(part[0], part[1])));
-                        sum += s0 + s1;
-                    } else {
-                        for (int r0 = 0; r0 < rows; r0 += 4) {
-                            uint32_t x[3][4];
-#pragma unroll
-                            for (int k3 = 0; k3 < (G::QUANT ? 3 : 1); ++k3)
-                                tmem_ld4(from + k3 * rp + r0, x[k3]);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int k3 = 0; k3 < (G::QUANT ? 3 : 1); ++k3)
-                                tmem_pin4(x[k3]);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                if (r0 + j >= rp)
-                                    break;
-                                const float2 o = row[r0 + j];
-                                float s = __uint_as_float(x[0][j]);
-                                if (G::QUANT)
-                                    s = ks * fmaf(fmaf(__uint_as_float(x[2][j]), 0.125f,
-                                                       __uint_as_float(x[1][j])), 0.125f, s);
-                                const float e = exp2_fast(fmaf(s, o.x, o.y));
-                                sum += r0 + j >= lo && r0 + j < hi ? e : 0.0f;
-                            }
+                        filled = min(filled + 1, p.stages);
+                        if (++stage == p.stages) {
+                            stage = 0;
+                            phase ^= 1;
                         }
-                    }
-                    mma_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        bar_signal(bar(kFewRead + buf));
-                }
-            }
-            if (p.parts > 1)
-                s_part[tid] = sum;
-            else if (ok && k < w.len)
-                weight[k] = p.keep == 0.0f ? sum : fmaf(p.keep, old, sum);
-        }
-    } else if (warp == 4) { // load
-        int stage = 0, phase = 1, filled = 0;
-        bool ok = true;
-        // a tile is `per` blocks of the pool, or a part of one: a lane's first key of a box
-        const int per = 128 / a.box_rows;
-        auto box_slot = [&](int tile) {
-            return lane < per && tile < tile1 ? sum_slot(a, w, tile * 128 + lane * a.box_rows) : -1;
-        };
-        int64_t next = box_slot(tile0);
-        for (int tile = tile0; ok && tile < tile1; ++tile) {
-            const int64_t slot = next;
-            next = box_slot(tile + 1);
-            const uint32_t many = __popc(__ballot_sync(0xFFFFFFFFu, slot >= 0)) * a.box_rows;
-            if (!seen(tile))
-                continue;
-            for (int head = h0; ok && head < h1; ++head) {
-                for (int chunk = 0; chunk < G::CHUNKS; ++chunk) {
-                    ok = wait(kFewEmpty + stage, phase);
-                    if (!ok)
-                        break;
-                    const uint32_t full = bar(kFewFull + stage);
-                    if (lane == 0)
-                        bar_signal_bulk(full, 1, many * (G::STAGE / 128));
-                    __syncwarp();
-                    if (slot >= 0) {
-                        const uint32_t to = ring + stage * G::STAGE + lane * a.box_rows * 128;
-                        if (G::MLA) {
-                            if (chunk < 8)
-                                copy_box(to, &a.copy_map, chunk * 64, (int)slot, full);
-                            else
-                                copy_box(to, &a.rot_map, 0, (int)slot, full);
-                        } else {
-                            copy_box(to, &a.rot_map, head * 128, (int)slot, full);
-                            if (!G::QUANT)
-                                copy_box(to + 16384, &a.rot_map, head * 128 + 64, (int)slot, full);
-                        }
-                    }
-                    filled = min(filled + 1, p.stages);
-                    if (++stage == p.stages) {
-                        stage = 0;
-                        phase ^= 1;
                     }
                 }
             }
@@ -343,81 +348,193 @@ __global__ void __launch_bounds__(kFewSumThreads, G::BLOCKS) weights_few_kernel(
             const int st = wrapped ? stage - 1 - i + p.stages : stage - 1 - i;
             bar_wait(bar(kFewFull + st), phase ^ 1 ^ (wrapped ? 1 : 0), &none, 10000000ll);
         }
-    } else { // mma
-        const uint32_t lead = elect_lane();
-        int stage = 0, phase = 0;
-        uint32_t i = 0;
-        bool ok = blockIdx.x != a.skip_block;
-        for (int tile = tile0; ok && tile < tile1; ++tile) {
-            if (!seen(tile))
-                continue;
-            for (int head = h0; ok && head < h1; ++head, ++i) {
-                const int buf = (int)i % bufs;
-                ok = i < (uint32_t)bufs || wait(kFewRead + buf, (i / bufs - 1) & 1);
-                mma_fence_after();
-                for (int chunk = 0; ok && chunk < G::CHUNKS; ++chunk) {
-                    ok = wait(kFewFull + stage, phase);
-                    if (!ok)
-                        break;
-                    const uint32_t k = operand(ring + stage * G::STAGE, 16), d = tmem + buf * n;
-                    if constexpr (G::MLA) {
-                        const uint32_t q = operand(q_smem + chunk * n * 128, 16);
+    } else {
+        uint32_t i = 0; // steps so far
+        int boxed = 0;
+        if (blockIdx.x == a.skip_block) {
+            ok = false;
+            s_abort = 1;
+        }
+        // the workers meet before a segment, when all steps of the one before are summed, and go
+        // on or give up together
+        for (; !workers_any(!ok) && more; more = p.slices && next_segment()) {
+            const int rows = w.n * a.group; // of a head
+            bring_queries<G>(p, w, q_smem, h0, h1, n, tid, s_row);
+            async_fence();
+            workers_any(false);
+            if (warp < 4) { // sum
+                const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+                float *const weight = p.weights + w.seq * p.weight_stride;
+                int64_t slot = sum_slot(a, w, tile0 * 128 + tid);
+                for (int tile = tile0; ok && tile < tile1; ++tile) {
+                    const int k = tile * 128 + tid;
+                    const bool mine = slot >= 0;
+                    const float *const scale = a.rs + (mine ? slot * a.rs_ss : 0);
+                    if (k < w.len && !mine)
+                        s_bad = 1;
+                    slot = tile + 1 < tile1 ? sum_slot(a, w, k + 128) : -1; // of the next tile
+                    const float old = p.parts == 1 && k < w.len && p.keep != 0.0f ? weight[k] : 0.0f;
+                    const TokenRange see = tokens_of(a, w, k, 1);
+                    const int lo = see.lo * a.group, hi = mine ? see.hi * a.group : 0; // rows that see this key
+                    float sum = 0.0f;
+                    if (seen(tile)) {
+                        float next = G::QUANT && mine ? __ldg(scale + h0) : 1.0f;
+                        for (int head = h0; head < h1; ++head, ++i) {
+                            const int buf = (int)i % bufs, at = G::MLA ? 0 : head * rq & 7;
+                            const uint32_t from = tmem + buf * n + at + lanes;
+                            const float ks = next;
+                            if (G::QUANT && mine && head + 1 < h1)
+                                next = __ldg(scale + head + 1);
+                            ok = wait(kFewS + buf, (i / bufs) & 1);
+                            if (!ok)
+                                break;
+                            mma_fence_after();
+                            const float2 *const row = s_row + (G::MLA ? 0 : head * rp);
+                            if constexpr (G::MLA) {
+                                f2 part[2] = {0ull, 0ull};
+                                for (int col = 0; col < rows; col += 32) {
+                                    uint32_t x[32];
+                                    tmem_ld32(from + col, x);
+                                    tmem_ld_wait();
+                                    tmem_pin32(x);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_window<false>(d, k + kk * 2, q + kk * 2, n, chunk > 0 || kk > 0, lead);
-                    } else if constexpr (G::QUANT) {
-                        const uint32_t q = operand(q_smem + (head * rq & ~7) * 128, 16);
+                                    for (int j = 0; j < 32; ++j) {
+                                        const float2 o = row[col + j];
+                                        const float e = exp2_fast(fmaf(__uint_as_float(x[j]), o.x, o.y));
+                                        part[j & 1] = f2_add(
+                                            part[j & 1],
+                                            f2_of_bits(col + j >= lo && col + j < hi ? __float_as_uint(e) : 0u, 0u));
+                                    }
+                                }
+                                float s0, s1;
+                                asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(f2_add(part[0], part[1])));
+                                sum += s0 + s1;
+                            } else {
+                                for (int r0 = 0; r0 < rows; r0 += 4) {
+                                    uint32_t x[3][4];
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_window<true>(d, k + kk * 2, q + kk * 2, n, kk > 0, lead);
-                    } else {
-                        const uint32_t panel = query_rows(a.kv_heads, rq) * 128 >> 4;
-                        const uint32_t q = operand(q_smem + (head * rq & ~7) * 128, 16);
+                                    for (int k3 = 0; k3 < (G::QUANT ? 3 : 1); ++k3)
+                                        tmem_ld4(from + k3 * rp + r0, x[k3]);
+                                    tmem_ld_wait();
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_window<false>(d, k + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2,
-                                              q + (kk >> 2) * panel + (kk & 3) * 2, n, kk > 0, lead);
+                                    for (int k3 = 0; k3 < (G::QUANT ? 3 : 1); ++k3)
+                                        tmem_pin4(x[k3]);
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) {
+                                        if (r0 + j >= rp)
+                                            break;
+                                        const float2 o = row[r0 + j];
+                                        float s = __uint_as_float(x[0][j]);
+                                        if (G::QUANT)
+                                            s = ks * fmaf(fmaf(__uint_as_float(x[2][j]), 0.125f,
+                                                               __uint_as_float(x[1][j])), 0.125f, s);
+                                        const float e = exp2_fast(fmaf(s, o.x, o.y));
+                                        sum += r0 + j >= lo && r0 + j < hi ? e : 0.0f;
+                                    }
+                                }
+                            }
+                            mma_fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                bar_signal(bar(kFewRead + buf));
+                        }
                     }
-                    bar_signal_mma(bar(kFewEmpty + stage), lead);
-                    if (++stage == p.stages) {
-                        stage = 0;
-                        phase ^= 1;
+                    if (p.parts > 1)
+                        s_part[tid] = sum;
+                    else if (ok && k < w.len)
+                        weight[k] = p.keep == 0.0f ? sum : fmaf(p.keep, old, sum);
+                }
+            } else { // mma
+                const uint32_t lead = elect_lane();
+                if (G::MLA && p.q_boxes && w.n > 0) { // those of the segment before have been used
+                    if (lane == 0) {
+                        bar_signal_bulk(bar(kFewQ), 1, p.rows * 9 * 128);
+                        for (int j = 0; j < 9; ++j)
+                            copy_box3(q_smem + j * n * 128, &p.q_map, j * 64, 0, w.q0, bar(kFewQ));
+                    }
+                    __syncwarp();
+                    int late = 0; // they land before the block's memory goes, also when it gives up
+                    if (!bar_wait(bar(kFewQ), boxed & 1, &late, limit)) {
+                        s_abort = 1;
+                        ok = false;
+                    }
+                    ++boxed;
+                }
+                for (int tile = tile0; ok && tile < tile1; ++tile) {
+                    if (!seen(tile))
+                        continue;
+                    for (int head = h0; ok && head < h1; ++head, ++i) {
+                        const int buf = (int)i % bufs;
+                        ok = i < (uint32_t)bufs || wait(kFewRead + buf, (i / bufs - 1) & 1);
+                        mma_fence_after();
+                        for (int chunk = 0; ok && chunk < G::CHUNKS; ++chunk) {
+                            ok = wait(kFewFull + stage, phase);
+                            if (!ok)
+                                break;
+                            const uint32_t k = operand(ring + stage * G::STAGE, 16), d = tmem + buf * n;
+                            if constexpr (G::MLA) {
+                                const uint32_t q = operand(q_smem + chunk * n * 128, 16);
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    mma_window<false>(d, k + kk * 2, q + kk * 2, n, chunk > 0 || kk > 0, lead);
+                            } else if constexpr (G::QUANT) {
+                                const uint32_t q = operand(q_smem + (head * rq & ~7) * 128, 16);
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    mma_window<true>(d, k + kk * 2, q + kk * 2, n, kk > 0, lead);
+                            } else {
+                                const uint32_t panel = query_rows(a.kv_heads, rq) * 128 >> 4;
+                                const uint32_t q = operand(q_smem + (head * rq & ~7) * 128, 16);
+#pragma unroll
+                                for (int kk = 0; kk < 8; ++kk)
+                                    mma_window<false>(d, k + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2,
+                                                      q + (kk >> 2) * panel + (kk & 3) * 2, n, kk > 0, lead);
+                            }
+                            bar_signal_mma(bar(kFewEmpty + stage), lead);
+                            if (++stage == p.stages) {
+                                stage = 0;
+                                phase ^= 1;
+                            }
+                        }
+                        if (ok)
+                            bar_signal_mma(bar(kFewS + buf), lead);
                     }
                 }
-                if (ok)
-                    bar_signal_mma(bar(kFewS + buf), lead);
             }
         }
-        if (blockIdx.x == a.skip_block)
-            s_abort = 1;
-        int none = 0; // every MMA is done before tensor memory goes
-        bar_signal_mma(bar(kFewEnd), lead);
-        bar_wait(bar(kFewEnd), 0, &none, 1000000000ll);
-        __syncwarp();
+        if (warp == 4) { // every MMA is done before tensor memory goes
+            int none = 0;
+            const uint32_t lead = elect_lane();
+            bar_signal_mma(bar(kFewEnd), lead);
+            bar_wait(bar(kFewEnd), 0, &none, 1000000000ll);
+            __syncwarp();
+        }
     }
     mma_fence_before();
     __syncthreads();
     mma_fence_after();
-    if (warp == 5)
+    if (warp == 4)
         tmem_free(tmem, columns);
     if (p.parts > 1) { // the heads' parts of one key tile, in their order
         if (tid == 0)
             s_part[128] = s_abort ? 1.0f : 0.0f;
         cluster_sync();
-        const int64_t k = first + tid;
+        const int64_t k = (int64_t)tile0 * 128 + tid;
         if (rank == 0 && tid < 128 && k < w.len) {
             float sum = 0.0f, gave_up = 0.0f;
             for (int r = 0; r < p.parts; ++r) {
                 sum += lds4_of(smem_u32(&s_part[tid]), r);
                 gave_up += lds4_of(smem_u32(&s_part[128]), r);
             }
-            float *const to = p.weights + seq * p.weight_stride + k;
+            float *const to = p.weights + w.seq * p.weight_stride + k;
             if (gave_up == 0.0f)
                 *to = p.keep == 0.0f ? sum : fmaf(p.keep, *to, sum);
         }
         cluster_sync(); // the others' sums have been read
     }
-    leave(s_abort ? kStatusTimeout : s_bad ? kStatusOutOfRange : kStatusOk);
+    if (tid == 0)
+        write_block_status(a.header, s_abort ? kStatusTimeout : s_bad || bad ? kStatusOutOfRange : kStatusOk,
+                           blockIdx.x, gridDim.x);
 }
 
 template <class G>
@@ -431,9 +548,12 @@ cudaError_t launch(WeightsParams &p, const WeightsPlan &pl, cudaStream_t stream,
     p.parts = pl.few_parts;
     p.stages = pl.few_stages;
     p.run = pl.run;
+    p.slices = pl.few_slices;
     p.row_pad = pl.row_pad;
-    if (G::MLA)
+    if (G::MLA) {
         p.n = (p.rows + 15) / 16 * 16;
+        p.q_boxes = encode_queries(p, 576);
+    }
     constexpr int most = (G::MLA ? kFewSumRoomMla : kFewSumRoom) + 1024;
     cudaError_t e = allow_smem<weights_few_kernel<G>>(most);
     if (e != cudaSuccess)
@@ -478,16 +598,17 @@ void plan_weights_few(RowKind kind, const AttnShape &a, WeightsPlan &pl)
     pl.few = true;
     pl.few_stages = (int32_t)std::min<int64_t>(kFewSumStages, stages);
     pl.few_smem = (int32_t)(pl.few_stages * stage + queries + 1024);
-    // runs of key tiles: some four rounds of blocks; a small call divides the heads as well
-    const int64_t tiles = std::max<int64_t>(1, (a.max_kv_len + 127) / 128) * a.num_seqs;
-    const int64_t slots = (mla ? 1 : 2) * kSms;
-    pl.run = (int32_t)std::min<int64_t>(16, std::max<int64_t>(1, tiles / (4 * slots)));
+    // Key tiles in slices, one to a block; a small call, a block to a tile and to some heads.
+    // Of very many sequences runs of some tiles, four rounds of blocks.
+    const int64_t per_seq = std::max<int64_t>(1, (a.max_kv_len + 127) / 128);
+    const int64_t tiles = per_seq * a.num_seqs, slots = (mla ? 1 : 2) * kSms;
+    pl.few_slices = tiles > slots && tiles < (1 << 30) && a.num_seqs <= kFewSeqs;
+    pl.run = pl.few_slices ? 0 : (int32_t)std::max<int64_t>(1, tiles / (4 * slots));
     pl.few_parts = 1;
     while (!mla && pl.run == 1 && pl.few_parts < 8 && tiles * pl.few_parts < slots &&
            a.kv_heads >= 2 * pl.few_parts)
         pl.few_parts *= 2;
-    const int64_t runs = (std::max<int64_t>(1, (a.max_kv_len + 127) / 128) + pl.run - 1) / pl.run;
-    pl.few_blocks = runs * a.num_seqs * pl.few_parts;
+    pl.few_blocks = pl.few_slices ? slots : (per_seq + pl.run - 1) / pl.run * a.num_seqs * pl.few_parts;
 }
 
 cudaError_t launch_weights_few(WeightsParams &p, RowKind kind, const WeightsPlan &pl,

@@ -213,7 +213,7 @@ def test_few_rows(kind, heads, n, quant):
 @pytest.mark.parametrize("kind,heads,quant", [("gqa", 32, False), ("gqa", 32, True), ("mla", 64, False)])
 def test_few_rows_in_runs(kind, heads, quant):
     # so many sequences that a block takes several key tiles
-    lens = [(1, 1100 + 37 * i) for i in range(64)] + [(1, 20000)]
+    lens = [(1, 900 + 17 * i) for i in range(48)]
     Sums(kind, lens, heads, quant=quant, seed=24, block=16).check()
 
 
