@@ -37,7 +37,7 @@ struct FewSum {
 
 constexpr int kFewSumThreads = 192; // 4 sum warps, mma, load
 constexpr int kFewWorkers = 160;    // all but the load warp, which runs ahead of them
-constexpr int kFewSumStages = 6, kFewSumBufs = 4, kFewSumRows = 512;
+constexpr int kFewSumStages = 4, kFewSumBufs = 4, kFewSumRows = 512;
 constexpr int kFewSeqs = 1024; // most sequences whose tiles a block counts
 constexpr int kFewSumRoom = 104 * 1024, kFewSumRoomMla = 212 * 1024;
 
