@@ -1946,8 +1946,11 @@ kv_status kv_evict_select(int32_t num_seqs, const float *d_weights, int64_t weig
 
 namespace {
 
-// Workspace: header, the units' read counters, the cos / sin tables.
+constexpr int64_t kOneRound = 152 * 4; // blocks
+
+// Workspace: header, the units' read counters (or status words), the cos / sin tables.
 struct CompactLayout {
+    bool one;             // every list fits one tile
     int64_t tiles, units; // of a sequence; of the call
     int32_t groups, per;  // layer groups, layers of one
     int32_t bits, lo_rows, hi_rows;
@@ -1958,11 +1961,14 @@ struct CompactLayout {
 bool compact_layout(RowKind kind, bool quant, int32_t layers, int32_t block, int32_t half,
                     int32_t num_seqs, int32_t max_blocks, int32_t max_count, CompactLayout *l)
 {
-    const int32_t rows = compact_tile_rows(kind, quant);
+    l->one = max_count <= compact_tile_rows(kind, quant, true);
+    const int32_t rows = compact_tile_rows(kind, quant, l->one);
     l->tiles = ((int64_t)max_count + rows - 1) / rows;
     const int64_t units = std::max<int64_t>(1, l->tiles * num_seqs);
-    // layer groups as in kv_splice: enough units for about kUnitsTarget blocks
-    const int64_t want = std::min<int64_t>(layers, (kUnitsTarget + units - 1) / units);
+    // layer groups as in kv_splice: enough units for about kUnitsTarget blocks; of short lists
+    // for one round
+    const int64_t target = l->one ? kOneRound : kUnitsTarget;
+    const int64_t want = std::min<int64_t>(layers, (target + units - 1) / units);
     l->per = (int32_t)((layers + want - 1) / want);
     l->groups = (layers + l->per - 1) / l->per;
     l->units = l->tiles * num_seqs * l->groups;
@@ -2008,7 +2014,8 @@ kv_status compact_impl(const CompactParams &rows, RowKind kind, double base, int
     if (st != KV_OK)
         return st;
     char *const w = static_cast<char *>(ws);
-    KV_CUDA(cudaMemsetAsync(w, 0, kHeaderBytes + (any ? (size_t)l.units * 4u : 0u), stream));
+    if (!any || !l.one)
+        KV_CUDA(cudaMemsetAsync(w, 0, kHeaderBytes + (any ? (size_t)l.units * 4u : 0u), stream));
     if (!any)
         return KV_OK;
     CompactParams p = rows;
@@ -2043,7 +2050,7 @@ kv_status compact_impl(const CompactParams &rows, RowKind kind, double base, int
         p.turn_half = tp.half;
     }
     KV_CUDA(mark(t_ev_start, stream));
-    KV_CUDA(launch_compact(p, kind, l.units, stream));
+    KV_CUDA(launch_compact(p, kind, l.one, l.units, stream));
     ++t_launches;
     KV_CUDA(mark(t_ev_stop, stream));
     return KV_OK;

@@ -30,7 +30,6 @@ namespace {
 
 constexpr uint32_t kMoveWarps = kThreads / 32;
 constexpr int kMoveThreads = kThreads + 32; // the row-moving warps, and one that publishes
-constexpr int kMoveMinBlocks = 3;
 constexpr uint32_t kReadBar = 1; // named barrier: the warps' loads of a layer have landed
 
 // 8-bit rows in tiles: half the bytes, so about twice the rows of a bf16 tile; the 128 bytes
@@ -39,6 +38,27 @@ using GeoMla8 = Geo<64, 32, 1, 4, 3>;
 using GeoGqa8 = Geo<16, 64, 8, 4, 3>;
 using GeoGqa48 = Geo<32, 32, 4, 4, 3>;
 using GeoMha8 = Geo<4, 256, 32, 4, 3>;
+
+// Blocks to an SM: the turn of whole heads gains by the fourth (8192 GQA rows down to 3276, 4
+// sequences: 560 us with three, 529 with four), latent rows lose by it (384 and 419 us).
+template <class G>
+constexpr int kMoveBlocks = G::NH > 1 ? 4 : 3;
+
+// Lists of a few rows, those of one tile (an accepted path): nothing to wait for, small
+// latent tiles.
+using GeoMlaFew = Geo<8, 64, 1, 4, 3>;
+using GeoMla8Few = Geo<16, 32, 1, 4, 3>;
+
+template <class F>
+cudaError_t with_move_geo(RowKind kind, bool quant, F &&f);
+
+template <class F>
+cudaError_t with_few_geo(RowKind kind, bool quant, F &&f)
+{
+    if (kind == RowKind::Mla)
+        return quant ? f(GeoTag<GeoMla8Few>{}) : f(GeoTag<GeoMlaFew>{});
+    return with_move_geo(kind, quant, f);
+}
 
 template <class F>
 cudaError_t with_move_geo(RowKind kind, bool quant, F &&f)
@@ -127,8 +147,10 @@ __device__ __forceinline__ int first_not_below(const int32_t *list, int n, int64
     return lo;
 }
 
-template <class G, bool IL, bool QUANT>
-__global__ void __launch_bounds__(kMoveThreads, kMoveMinBlocks) compact_kernel(
+// ONE: every list fits one tile.  Then no tile waits for another: blocks take their units by
+// number, and each leaves a status word of its own, so that nothing has to be cleared first.
+template <class G, bool IL, bool QUANT, bool ONE>
+__global__ void __launch_bounds__(ONE ? kThreads : kMoveThreads, kMoveBlocks<G>) compact_kernel(
     const __grid_constant__ CompactParams p)
 {
     constexpr bool TURNS = !QUANT || G::NH == 1; // e4m3 heads are not turned
@@ -136,7 +158,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveMinBlocks) compact_kernel(
     // scales of a row, and how many a thread moves
     constexpr int CS = G::CV / 8, RS = G::NH == 1 ? 0 : G::NH, NS = CS + RS;
     constexpr int SPER = (G::T * NS + kThreads - 1) / kThreads;
-    __shared__ uint32_t s_ticket;
+    __shared__ uint32_t s_ticket, s_status;
     __shared__ volatile int32_t s_abort; // 0 -> 1 once a wait ran out; never reset
     __shared__ int64_t s_src[G::T], s_dst[G::T];
     __shared__ int32_t s_ident[G::T], s_shift[G::T];
@@ -144,9 +166,15 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveMinBlocks) compact_kernel(
     __shared__ uint32_t s_sink;
 
     const int tid = threadIdx.x;
+    uint32_t *const status = ONE ? &s_status : p.status;
+    auto leave = [&] { // a thread; ONE: behind a barrier
+        if (ONE && tid == 0)
+            write_block_status(p.status, s_status, blockIdx.x, gridDim.x);
+    };
     if (tid == 0) {
-        s_ticket = atomicAdd(p.ticket, 1u);
+        s_ticket = ONE ? blockIdx.x : atomicAdd(p.ticket, 1u);
         s_abort = 0;
+        s_status = kStatusOk;
     }
     __syncthreads();
     // layer group g of tile k of sequence q
@@ -157,19 +185,24 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveMinBlocks) compact_kernel(
     const int l0 = g * p.group_layers, l1 = min(p.pool.num_layers, l0 + p.group_layers);
     const int32_t count = __ldg(p.count + q), first = p.first ? __ldg(p.first + q) : 0;
     if (count < 0 || count > p.max_count || first < 0) {
-        if (k == 0 && tid == 0)
-            set_status(p.status, kStatusOutOfRange);
+        if (k == 0 && tid == 0) {
+            set_status(status, kStatusOutOfRange);
+            leave();
+        }
         return;
     }
     const int64_t lo = k * G::T, hi = min(lo + (int64_t)G::T, (int64_t)count);
-    if (lo >= hi)
+    if (lo >= hi) {
+        leave();
         return;
+    }
     const int32_t *const keep = p.keep + q * p.keep_stride;
     uint32_t *const flags = p.flags + (int64_t)q * p.layer_groups + g; // tile j: + j * flag_step
     const int64_t flag_step = (int64_t)p.num_seqs * p.layer_groups;
     if (__ldg(keep + hi - 1) == hi - 1) { // ascending: nothing up to here moves
-        if (tid == 0)
+        if (!ONE && tid == 0)
             red_release_add(flags + k * flag_step, kMoveWarps * (uint32_t)(l1 - l0));
+        leave();
         return;
     }
     if (tid < G::T) {
@@ -180,14 +213,14 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveMinBlocks) compact_kernel(
             const int32_t *bt = p.block_tables + (int64_t)q * p.max_blocks;
             const int32_t from = __ldg(keep + i), before = i > 0 ? __ldg(keep + i - 1) : -1;
             if (from <= before || from < i) {
-                set_status(p.status, kStatusOutOfRange);
+                set_status(status, kStatusOutOfRange);
             } else if (from > i) {
                 src = slot_of(bt, p.max_blocks, p.pool.block, p.pool.num_blocks,
                               (int64_t)first + from);
                 dst = slot_of(bt, p.max_blocks, p.pool.block, p.pool.num_blocks, first + i);
                 shift = from - (int32_t)i;
                 if (src < 0 || dst < 0) {
-                    set_status(p.status, kStatusOutOfRange);
+                    set_status(status, kStatusOutOfRange);
                     src = dst = -1;
                 }
             }
@@ -199,7 +232,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveMinBlocks) compact_kernel(
     }
     __syncthreads();
 
-    if (tid >= kThreads) {
+    if (!ONE && tid >= kThreads) {
         const int lane = tid & 31;
         // earlier tiles with rows in [lo, hi)
         const int a = first_not_below(keep, (int)hi, lo, lane);
@@ -271,7 +304,8 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveMinBlocks) compact_kernel(
         f ^= fold_tile<G>(regs);
         if (p.num_seqs < 0)
             s_sink = f;
-        bar_arrive(kReadBar, kMoveThreads);
+        if (!ONE)
+            bar_arrive(kReadBar, kMoveThreads);
         __syncthreads();
         if (!s_abort) {
             store_tile<G, false, true, IL>(at, s_dst, regs, s_cs, TURNS ? G::kCsRow : 0, s_ident,
@@ -284,6 +318,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveMinBlocks) compact_kernel(
             }
         }
     }
+    leave();
 }
 
 // Rows n of turn_lo (n θ_j) and of turn_hi (n 2^bits θ_j).
@@ -308,13 +343,14 @@ __global__ void __launch_bounds__(256) turn_kernel(const __grid_constant__ TurnP
 
 } // namespace
 
-int compact_tile_rows(RowKind kind, bool quant)
+int compact_tile_rows(RowKind kind, bool quant, bool one)
 {
     int rows = 0;
-    with_move_geo(kind, quant, [&](auto g) {
+    const auto get = [&](auto g) {
         rows = decltype(g)::type::T;
         return cudaSuccess;
-    });
+    };
+    one ? with_few_geo(kind, quant, get) : with_move_geo(kind, quant, get);
     return rows;
 }
 
@@ -325,27 +361,32 @@ cudaError_t launch_turn_table(const TurnParams &p, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-cudaError_t launch_compact(const CompactParams &p, RowKind kind, int64_t tickets,
+cudaError_t launch_compact(const CompactParams &p, RowKind kind, bool one, int64_t units,
                            cudaStream_t stream)
 {
     const bool quant = p.cs != nullptr;
-    return with_move_geo(kind, quant, [&](auto g) {
+    const auto run = [&](auto g, auto is_one) {
         using G = typename decltype(g)::type;
-        const unsigned n = (unsigned)tickets;
+        constexpr bool ONE = decltype(is_one)::value;
+        constexpr int threads = ONE ? kThreads : kMoveThreads;
+        const unsigned n = (unsigned)units;
         if (quant) {
             if constexpr (G::NH == 1) {
                 if (p.pool.il) {
-                    compact_kernel<G, true, true><<<n, kMoveThreads, 0, stream>>>(p);
+                    compact_kernel<G, true, true, ONE><<<n, threads, 0, stream>>>(p);
                     return cudaGetLastError();
                 }
             }
-            compact_kernel<G, false, true><<<n, kMoveThreads, 0, stream>>>(p);
-        } else if (p.pool.il)
-            compact_kernel<G, true, false><<<n, kMoveThreads, 0, stream>>>(p);
-        else
-            compact_kernel<G, false, false><<<n, kMoveThreads, 0, stream>>>(p);
+            compact_kernel<G, false, true, ONE><<<n, threads, 0, stream>>>(p);
+        } else if (p.pool.il) {
+            compact_kernel<G, true, false, ONE><<<n, threads, 0, stream>>>(p);
+        } else {
+            compact_kernel<G, false, false, ONE><<<n, threads, 0, stream>>>(p);
+        }
         return cudaGetLastError();
-    });
+    };
+    return one ? with_few_geo(kind, quant, [&](auto g) { return run(g, BoolTag<true>{}); })
+               : with_move_geo(kind, quant, [&](auto g) { return run(g, BoolTag<false>{}); });
 }
 
 } // namespace kvr

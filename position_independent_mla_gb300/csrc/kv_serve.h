@@ -191,9 +191,10 @@ struct TurnParams {
     float4 *table; // lo_rows of turn_lo, then hi_rows of turn_hi
 };
 
-int compact_tile_rows(RowKind kind, bool quant);
+// Rows of a tile; `one`: where every list fits one.
+int compact_tile_rows(RowKind kind, bool quant, bool one);
 cudaError_t launch_turn_table(const TurnParams &p, cudaStream_t stream);
-cudaError_t launch_compact(const CompactParams &p, RowKind kind, int64_t tickets,
+cudaError_t launch_compact(const CompactParams &p, RowKind kind, bool one, int64_t units,
                            cudaStream_t stream);
 
 // Which tokens stay (kv_select.cu).
