@@ -1946,7 +1946,7 @@ kv_status kv_evict_select(int32_t num_seqs, const float *d_weights, int64_t weig
 
 namespace {
 
-constexpr int64_t kOneRound = 152 * 4; // blocks
+constexpr int64_t kOneRound = 152 * 2; // blocks
 
 // Workspace: header, the units' read counters (or status words), the cos / sin tables.
 struct CompactLayout {

@@ -4,13 +4,17 @@
 // A sequence's weights are read once, as 32-bit keys in the order of the numbers (tokens
 // that stay in any case above all, NaN below all), into the shared memory of a cluster of
 // blocks, a run of tokens to a block.  The key of the budget-th token is found digit by
-// digit (11, 11 and 10 bits): each pass counts the keys that share the digits found so far,
-// the cluster adds its counts up in its first block (whole numbers: the order of the
-// additions does not show), which finds the digit and tells the others.  Then every warp
-// counts what it keeps, and after a sum over warps and blocks writes its tokens in
-// ascending order; ties are taken from the lowest index on.
+// digit (11, 11 and 10 bits): each pass counts the keys that share the digits found so far;
+// a cluster adds its counts (those that are not 0: a few hundred) up in its first block (whole
+// numbers: the order of the additions does not show), which finds the digit and tells the
+// others.  The keys that share the first digit, few as a rule, are listed, and the later
+// passes go over the list.  Then every warp knows what it keeps, and after a sum over warps and
+// blocks writes its tokens in ascending order; ties are taken from the lowest index on.
 //
-// Bound: latency (a call reads little: 64 sequences of up to 16384 tokens are 2 MB).
+// Bound: latency (a call reads little: 64 sequences of up to 16384 tokens are 2 MB): loads,
+// which are asked for eight at a time, sweeps over the keys, and the cluster's barriers, two
+// to a pass.  With every pass over all keys and single loads, 64 ragged sequences took 17.4
+// us, 8192 of 131072 tokens 24.6.
 #include <algorithm>
 
 #include "kv_attn_tile.cuh"
@@ -23,13 +27,18 @@ constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
 constexpr int kSelCluster = 8;   // most blocks of a sequence
 constexpr int kSelSlice = 2048;  // fewest tokens that are worth a block
-constexpr int kSelHeld = 49152;  // keys that a block holds; it reads others again
+constexpr int kSelHeld = 40960;  // keys that a block holds; it reads others again
+
+constexpr int kSelList = 4096;   // keys that share the first digit; more of them: all are gone over
 
 struct SelShared {
     uint32_t bins[kSelBins];
+    uint32_t all[3][kSelBins];  // of each pass, the cluster's (in its first block)
+    uint16_t list[kSelList];
+    uint32_t listed;
     uint32_t warp[2][kSelWarps];
     uint32_t above[kSelWarps];  // keys in the bins of later warps
-    uint32_t digit, left;       // found by the cluster's first block
+    uint32_t digit, left;
     uint32_t more[kSelCluster], same[kSelCluster]; // of every block, in each
 };
 
@@ -94,50 +103,93 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const __grid_con
     const int slice = (len + many - 1) / many, from = min(len, rank * slice);
     const int size = min(len, from + slice) - from;
     const int run = (size + kSelThreads - 1) / kSelThreads * 32;
-    auto key_at = [&](int i) { // of the slice
+    auto key_at = [&](int i, float w) { // of the slice
         const int at = from + i;
-        return at < sinks || at >= tail ? 0xFFFFFFFFu : weight_key(__ldg(weight + at));
+        return at < sinks || at >= tail ? 0xFFFFFFFFu : weight_key(w);
     };
-    auto key = [&](int i) { return i < kSelHeld ? s_key[i] : key_at(i); };
-    for (int i = tid; i < min(size, kSelHeld); i += kSelThreads)
-        s_key[i] = key_at(i);
+    for (int i = tid; i < 3 * kSelBins; i += kSelThreads)
+        (&sh.all[0][0])[i] = 0;
+    for (int i = tid; i < kSelBins; i += kSelThreads)
+        sh.bins[i] = 0;
+    if (tid < kSelWarps)
+        sh.warp[0][tid] = sh.warp[1][tid] = 0;
+    if (tid == 0)
+        sh.listed = 0;
+    const int held = min(size, kSelHeld);
+    for (int i0 = 0; i0 < held; i0 += 8 * kSelThreads) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kSelThreads + tid;
+            x[j] = i < held ? __ldg(weight + from + i) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kSelThreads + tid;
+            if (i < held)
+                s_key[i] = key_at(i, x[j]);
+        }
+    }
+    auto key = [&](int i) { return i < kSelHeld ? s_key[i] : key_at(i, __ldg(weight + from + i)); };
+    if (many > 1)
+        cluster_sync(); // the first block's counts are 0
+    else
+        __syncthreads();
 
     uint32_t prefix = 0, left = (uint32_t)n; // digits found; keys still wanted among those
-    const uint32_t bins = smem_u32(sh.bins);
+    uint32_t digit0 = 0;
+    bool listed = true;
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-        for (int i = tid; i < kSelBins; i += kSelThreads)
-            sh.bins[i] = 0;
-        __syncthreads();
-        for (int i = warp * 32 + lane; i - lane < size; i += kSelThreads) {
-            const uint32_t k = i < size ? key(i) : 0u;
-            const bool in = i < size && (pass == 0 || (k >> (shift + bits)) == prefix);
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
-            if (!who)
-                continue;
-            // tokens that were never seen share a key: one addition for a warp of them
-            const uint32_t bin = (k >> shift) & ((1u << bits) - 1u);
-            const uint32_t lead = __shfl_sync(0xFFFFFFFFu, bin, __ffs((int)who) - 1);
-            if (__all_sync(0xFFFFFFFFu, !in || bin == lead)) {
+        if (pass == 0) {
+#pragma unroll 4
+            for (int i = tid; i < size; i += kSelThreads)
+                atomicAdd(&sh.bins[key(i) >> 21], 1u);
+        } else {
+            if (pass == 1) { // list them, and count what lies above, a warp its own run
+                const int a = warp * run, b = min(size, a + run);
+                uint32_t more = 0;
+#pragma unroll 4
+                for (int i = a + lane; i < b; i += 32) {
+                    const uint32_t d = key(i) >> 21;
+                    more += d > prefix;
+                    if (d == prefix) {
+                        const uint32_t at = atomicAdd(&sh.listed, 1u);
+                        if (at < kSelList && i < 0x10000)
+                            sh.list[at] = (uint16_t)i;
+                        else
+                            sh.listed = kSelList + 1; // (a sum of more than that stays above it)
+                    }
+                }
+                more = __reduce_add_sync(0xFFFFFFFFu, more);
                 if (lane == 0)
-                    atomicAdd(&sh.bins[lead], (uint32_t)__popc(who));
-            } else if (in) {
-                atomicAdd(&sh.bins[bin], 1u);
+                    sh.warp[0][warp] = more;
+                digit0 = prefix;
+                for (int i = tid; i < kSelBins; i += kSelThreads)
+                    sh.bins[i] = 0;
+                __syncthreads();
+                listed = sh.listed <= kSelList;
+            }
+            const int all = listed ? (int)sh.listed : size;
+            for (int j = tid; j < all; j += kSelThreads) {
+                const uint32_t k = key(listed ? sh.list[j] : j);
+                if ((k >> (shift + bits)) == prefix)
+                    atomicAdd(&sh.bins[(k >> shift) & ((1u << bits) - 1u)], 1u);
             }
         }
+        __syncthreads();
+        uint32_t *const sums = many > 1 ? sh.all[pass] : sh.bins;
         if (many > 1) {
-            cluster_sync(); // the first block's own counts are in
-            if (rank > 0)
-                for (int i = tid; i < kSelBins; i += kSelThreads)
-                    if (const uint32_t c = sh.bins[i])
-                        remote_add(remote_of(bins + i * 4, 0), c);
+            const uint32_t at = remote_of(smem_u32(sh.all[pass]), 0);
+            for (int i = tid; i < kSelBins; i += kSelThreads)
+                if (const uint32_t c = sh.bins[i])
+                    remote_add(at + i * 4, c);
             cluster_sync();
-        } else {
-            __syncthreads();
         }
         if (rank == 0) {
             // the bin in which the left-th largest key lies: a thread holds two bins
-            const uint32_t c0 = sh.bins[2 * tid], c1 = sh.bins[2 * tid + 1];
+            const uint32_t c0 = sums[2 * tid], c1 = sums[2 * tid + 1];
             uint32_t sum = c0 + c1; // of this and the later lanes
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -146,22 +198,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const __grid_con
                     sum += o;
             }
             if (lane == 0)
-                sh.warp[0][warp] = sum;
+                sh.above[warp] = sum;
             __syncthreads();
-            if (warp == 0) {
-                uint32_t s = sh.warp[0][lane];
-                const uint32_t mine = s;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const uint32_t o = __shfl_down_sync(0xFFFFFFFFu, s, d);
-                    if (lane + d < 32)
-                        s += o;
-                }
-                sh.above[lane] = s - mine;
-            }
-            __syncthreads();
-            const uint32_t upto = sh.above[warp] + sum;  // keys from bin 2 tid on
-            const uint32_t past = upto - c0 - c1;        // beyond this thread's bins
+            uint32_t past = __reduce_add_sync(0xFFFFFFFFu, lane > warp ? sh.above[lane] : 0u);
+            const uint32_t upto = past + sum; // keys from bin 2 tid on
+            past = upto - c0 - c1;            // beyond this thread's bins
             if (past < left && left <= upto) {
                 const bool high = left <= past + c1;
                 const uint32_t digit = 2 * tid + (high ? 1 : 0);
@@ -172,26 +213,29 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const __grid_con
                 }
             }
         }
+        if (pass == 1) // (all have read them)
+            for (int i = tid; i < kSelBins && many > 1; i += kSelThreads)
+                sh.bins[i] = 0;
         if (many > 1)
             cluster_sync();
         else
             __syncthreads();
         prefix = pass == 0 ? sh.digit : prefix << bits | sh.digit;
         left = sh.left;
+        if (pass == 1 && many == 1) {
+            for (int i = tid; i < kSelBins; i += kSelThreads)
+                sh.bins[i] = 0;
+            __syncthreads();
+        }
     }
     // keys above prefix stay, and the first `left` of those equal to it
     const int a = warp * run, b = min(size, a + run);
-    uint32_t more = 0, same = 0;
-    for (int i = a + lane; i < b; i += 32) {
+    const int all = listed ? (int)sh.listed : size;
+    for (int j = tid; j < all; j += kSelThreads) {
+        const int i = listed ? sh.list[j] : j;
         const uint32_t k = key(i);
-        more += k > prefix;
-        same += k == prefix;
-    }
-    more = __reduce_add_sync(0xFFFFFFFFu, more);
-    same = __reduce_add_sync(0xFFFFFFFFu, same);
-    if (lane == 0) {
-        sh.warp[0][warp] = more;
-        sh.warp[1][warp] = same;
+        if ((k >> 21) == digit0 && k >= prefix)
+            atomicAdd(&sh.warp[k == prefix][i / run], 1u);
     }
     __syncthreads();
     uint32_t before_more = 0, before_same = 0;
@@ -225,7 +269,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const __grid_con
             const uint32_t at = before_more + __popc(gt & lower) + min(e, left);
             keep[at] = from + i;
             if (kept)
-                kept[at] = __ldg(weight + from + i);
+                kept[at] = k == 0u || k == 0x80000000u || k == 0xFFFFFFFFu
+                               ? __ldg(weight + from + i) // NaN, 0 of either sign, or not its own key
+                               : __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
         }
         before_more += __popc(gt);
         before_same += __popc(eq);

@@ -348,3 +348,13 @@ def test_captured_together():
             for k in before:
                 assert np.array_equal(after[k][:, dst], before[k][:, src])
         assert kv.kv_get_device_status(cws) == kv.KV_OK
+
+
+def test_select_long_and_alike():
+    # more keys of one first digit than are listed; runs of more than 2^16 tokens in a block
+    w = 1.0 + heavy(11, 2, 200000) * 1e-3
+    w[1, ::2] = 1.25
+    check_select(w, [200000, 199999], [70000, 33333], 4, 100)
+    w = heavy(12, 80, 70000)
+    check_select(w, [70000 - 7 * i for i in range(80)], [500 + i for i in range(80)], 0, 3)
+    check_select(torch.zeros(2, 66000), [66000, 40000], [100, 39999], 1, 1)
