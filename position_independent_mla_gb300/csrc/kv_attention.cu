@@ -157,10 +157,19 @@ constexpr int kManyUnits = 16;
 // them of 65536 take 117 us, 161 take 1144.
 constexpr int kSliceSeqs = 160;
 
+// Blocks that take the same slice of the keys, side by side: the halves of MLA columns, and
+// the heads of a tree (p.side of them).  Every key of a long context is read once there, and the heads'
+// 256 bytes of a row, which lie next to each other, should be asked for at about the same
+// time.  16 ragged trees, 32 heads over 8: 151 us when each head had slices of its own.
+template <class G, bool TREE>
+__device__ __forceinline__ int slice_sides(const AttnParams &p)
+{
+    return G::MLA ? G::HALVES : TREE ? p.side : 1;
+}
+
 // What one warp knows of the slices.
-template <class G>
+template <class G, bool TREE>
 struct Slices {
-    static constexpr int64_t COUNT = G::MLA ? kSms / 2 : kSms;
     static constexpr int ROWS = kRows * G::NT;
     int64_t size, total; // places of a slice, of the call
     int64_t tile, cost;  // of a key tile, of a unit besides its tiles
@@ -173,7 +182,9 @@ struct Slices {
     // past the last.
     __device__ __forceinline__ bool find(const AttnParams &p, int lane, int64_t &pos)
     {
-        const int heads = G::MLA ? 1 : p.kv_heads;
+        const int side = slice_sides<G, TREE>(p);
+        const int heads = G::MLA ? 1 : TREE ? p.kv_heads / side : p.kv_heads;
+        const int64_t slices = TREE || G::MLA ? kSms / side : kSms;
         tile = (int64_t)G::KT * p.group;
         const int64_t grow = p.causal && p.window == 0 ? ROWS : 0;
         // sequence s: queries and keys, row tiles, places of the first one's unit
@@ -225,9 +236,9 @@ struct Slices {
             total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
         }
         bad = __any_sync(0xFFFFFFFFu, wrong);
-        cost = total >= COUNT * 2 * kMinRun * tile ? G::UNIT_COST * tile : 0;
+        cost = total >= slices * 2 * kMinRun * tile ? G::UNIT_COST * tile : 0;
         total += units * cost;
-        size = max(kMinRun * tile, (total + COUNT - 1) / COUNT);
+        size = max(kMinRun * tile, (total + slices - 1) / slices);
         if (pos < 0)
             pos = (-1 - pos) * size;
         bool found = false;
@@ -292,12 +303,13 @@ struct Slices {
 // The next piece of this block's slice, from `pos` on (-1 - slice: from its start); false
 // past its end.  w.split is the place of its part: a slice begins and ends inside a unit
 // at most once each.
-template <class G>
+template <class G, bool TREE>
 __device__ __forceinline__ bool find_slice(const AttnParams &p, int lane, int64_t &pos, Work &w,
                                            bool &bad)
 {
-    const int slice = (int)blockIdx.x / G::HALVES, half = (int)blockIdx.x % G::HALVES;
-    Slices<G> s;
+    const int side = slice_sides<G, TREE>(p);
+    const int slice = (int)blockIdx.x / side, half = (int)blockIdx.x % side;
+    Slices<G, TREE> s;
     while (s.find(p, lane, pos)) {
         bad = s.bad;
         const int64_t end = min(s.total, (slice + 1) * s.size);
@@ -314,10 +326,10 @@ __device__ __forceinline__ bool find_slice(const AttnParams &p, int lane, int64_
         w.q0 = s.q0;
         w.n = s.n;
         w.len = s.len;
-        w.row0 = s.row_tile * Slices<G>::ROWS;
-        w.head = G::MLA ? half : s.head;
+        w.row0 = s.row_tile * Slices<G, TREE>::ROWS;
+        w.head = G::MLA ? half : TREE ? s.head * side + half : s.head;
         w.splits = v0 > 0 || v1 < s.tiles ? 2 : 1; // more than one
-        w.split = (2 * slice + (v0 == 0)) * G::HALVES + half;
+        w.split = (2 * slice + (v0 == 0)) * side + half;
         const int real = key_tiles<G::KT, G::NT>(p, w);
         w.beg = min(real, v0);
         w.end = min(real, v1);
@@ -331,15 +343,18 @@ __device__ __forceinline__ bool find_slice(const AttnParams &p, int lane, int64_
 // the kernel that writes their parts.  Bound by latency: 11 to 13 us by itself for 40 MB of
 // parts, 29 to 50 when every row of the call looked for its parts.  JOIN_BLOCKS blocks to a slice: they join the unit whose first
 // cut is the slice's start, a warp for a row.
-template <class G>
+template <class G, bool TREE>
 __global__ void __launch_bounds__(256) slice_join_kernel(const __grid_constant__ AttnParams p)
 {
     constexpr int ROWS = kRows * G::NT;
     __shared__ int s_splits, s_rows, s_row0, s_head, s_q0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int slice = (int)blockIdx.x / G::JOIN_BLOCKS + 1; // the first start is no cut
+    // heads side by side have parts of their own
+    const int side = slice_sides<G, TREE>(p), lanes = G::MLA ? 1 : side;
+    const int mine = TREE ? (int)blockIdx.x / G::JOIN_BLOCKS % lanes : 0;
+    const int slice = (int)blockIdx.x / (G::JOIN_BLOCKS * lanes) + 1; // the first start is no cut
     if (warp == 0) {
-        Slices<G> s;
+        Slices<G, TREE> s;
         int64_t pos = -1 - slice;
         int splits = 0;
         if (s.find(p, lane, pos)) {
@@ -347,7 +362,7 @@ __global__ void __launch_bounds__(256) slice_join_kernel(const __grid_constant__
                 splits = s.slice_of(s.tiles - 1) - slice + 2;
             s_row0 = s.row_tile * ROWS;
             s_rows = min(ROWS, s.n * p.group - s.row_tile * ROWS);
-            s_head = s.head;
+            s_head = s.head * lanes + mine;
             s_q0 = s.q0;
         }
         s_splits = splits;
@@ -363,7 +378,7 @@ __global__ void __launch_bounds__(256) slice_join_kernel(const __grid_constant__
         const int h = s_head * p.group + row - i * p.group;
         // the first part lies in the second place of its slice, the others in the first ones
         auto at = [&](int k) {
-            return (int64_t)(2 * (slice - 1 + k) + (k == 0)) * G::HALVES * ROWS + r;
+            return ((int64_t)(2 * (slice - 1 + k) + (k == 0)) * side + mine) * ROWS + r;
         };
         join_row<G::DV / 128>(
             s_splits, lane, p.out + tok * p.o_ts + h * p.o_hs,
@@ -1409,7 +1424,7 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
         if constexpr (kShares<G>)
             reg_dec<kMmaRegs>();
         const bool finder = warp == kMmaWarp<G> + 1;
-        int64_t pos = -1 - (int64_t)(blockIdx.x / G::HALVES);
+        int64_t pos = -1 - (int64_t)blockIdx.x / slice_sides<G, TREE>(p);
         // the finder: barriers of unit k; `old`: they have been used
         auto set_up = [&](int k, const Work &w, bool old) {
             for (int i = lane; i < S::NBARS; i += 32) {
@@ -1433,7 +1448,7 @@ __global__ void __launch_bounds__(kAttnThreads<G>, 1) attention_kernel(
             Work w{};
             bool bad = false, go = false;
             if (p.slices) {
-                go = find_slice<G>(p, lane, pos, w, bad);
+                go = find_slice<G, TREE>(p, lane, pos, w, bad);
             } else if (k == 0) {
                 // block -> (row tile, key head or half); heads of one row tile and its halves
                 // are neighbours, so their rows meet in L2
@@ -1534,8 +1549,9 @@ cudaError_t launch(AttnParams &p, int64_t blocks, cudaStream_t stream)
         return e;
     if (!p.slices)
         return cudaSuccess;
-    constexpr int cuts = (int)Slices<G>::COUNT - 1;
-    return launch_join(slice_join_kernel<G>, p, cuts * G::JOIN_BLOCKS, stream);
+    const int side = G::MLA ? G::HALVES : TREE ? p.side : 1, cuts = kSms / side - 1;
+    return launch_join(slice_join_kernel<G, TREE>, p, cuts * G::JOIN_BLOCKS * (G::MLA ? 1 : side),
+                       stream);
 }
 
 } // namespace
@@ -1587,6 +1603,12 @@ AttnPlan plan_attention(RowKind kind, const AttnShape &a)
                             u * around / at_once + join;
         pl.slices = a.num_seqs <= kSliceSeqs && units < kManyUnits * kSms &&
                     (a.num_seqs > 1 ? cut * 10 <= whole * 11 : cut <= whole);
+        // the most heads side by side that divide both the heads and the SMs
+        pl.side = mla ? 2 : 1;
+        if (a.tree && !mla)
+            for (int d = 2; d <= 8; d *= 2)
+                if (a.kv_heads % d == 0 && kSms % d == 0)
+                    pl.side = d;
         if (pl.slices)
             pl.blocks = kSms;
         return pl;
@@ -1611,6 +1633,7 @@ cudaError_t launch_attention(AttnParams &p, RowKind kind, const AttnPlan &pl, cu
     const bool quant = p.cs != nullptr;
     p.cluster = pl.cluster ? 1 : 0;
     p.slices = pl.slices ? 1 : 0;
+    p.side = pl.side;
     p.by_group = Divisor((uint32_t)p.group);
     p.by_rows = Divisor((uint32_t)(kRows * std::max(1, pl.row_tiles)));
     p.by_block = Divisor((uint32_t)p.block);

@@ -133,6 +133,7 @@ struct AttnParams {
     // of others, where blocks take equal slices of all keys of the call: [2 * kSms][rows of
     // a block][columns of a block]
     int32_t slices;
+    int32_t side; // trees: key heads whose blocks read the same keys side by side
     int64_t wait_limit_ns;
     int64_t skip_block; // test hook: this block issues no MMA (-1: none)
     uint32_t *header;
@@ -160,6 +161,7 @@ struct AttnPlan {
     int32_t max_splits;
     bool cluster;        // the splits of a row are a cluster that joins them itself
     bool slices;         // the split is made on the device (Slices)
+    int32_t side;        // its blocks that take the same keys, for heads of their own
     int64_t blocks;
 
     bool joins() const { return slices || (max_splits > 1 && !cluster); }
