@@ -92,6 +92,10 @@ class Sums(Batch):
         assert kv.kv_get_device_status(self.wws) == status
         return self.weights
 
+    def run_attention(self):
+        """(out, lse) of kv_attention over the same keys."""
+        return Batch.run(self)
+
     def check(self):
         """Bounds, derived: a score is an fp32 sum of at most 576 exact products, off by less
         than 2^-20 of B = scale * sum|q||k|; the exponent is formed with a rounding each of

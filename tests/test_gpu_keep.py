@@ -358,3 +358,77 @@ def test_select_long_and_alike():
     w = heavy(12, 80, 70000)
     check_select(w, [70000 - 7 * i for i in range(80)], [500 + i for i in range(80)], 0, 3)
     check_select(torch.zeros(2, 66000), [66000, 40000], [100, 39999], 1, 1)
+
+
+def step_by_step(kind, quant):
+    """One request under a bounded cache: attention, what its keys received, the choice, the
+    move, and attention over what is left, against the same in 64 bits."""
+    from _keep import Sums
+    s = Sums(kind, [(3, 400), (1, 250)], 16 if kind == "mla" else 32, keep=0.0, quant=quant, seed=5)
+    out, lse = s.run_attention()
+    kv.kv_attention_weights(s.desc, s.layer, s.attn, s.q, lse, s.weights, 0.0, s.wws)
+    lens = torch.tensor([400, 250], dtype=torch.int32, device="cuda")
+    budget = torch.tensor([120, 250], dtype=torch.int32, device="cuda")
+    keep, count = torch.zeros(2, 250, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    kept = torch.zeros(2, 250, device="cuda")
+    ws = kv.evict_workspace(2, s.weights.shape[1])
+    kv.kv_evict_select(s.weights, lens, budget, 4, 32, keep, count, kept, ws)
+    table = s.table.cuda()
+    cws = kv.compact_workspace(s.desc, 2, table.shape[1], 250)
+    before = [getattr(s.pool, n)[s.layer].clone() for n in ("copy", "rot")]
+    kv.kv_compact(s.desc, table, None, keep, count, False, cws)
+    assert [kv.kv_get_device_status(w) for w in (s.wws, ws, cws)] == [kv.KV_OK] * 3
+    want = ref_select(s.weights.cpu(), [400, 250], [120, 250], 4, 32)
+    assert count.tolist() == [120, 250]
+    for q in range(2):
+        assert keep[q, : len(want[q])].tolist() == want[q]
+        src, dst = s.slots(q)[want[q]].cuda(), s.slots(q)[: len(want[q])].cuda()
+        for part, old in zip(("copy", "rot"), before):
+            new = getattr(s.pool, part)[s.layer]
+            v = torch.uint8 if new.element_size() == 1 else torch.int16
+            assert torch.equal(new.view(v)[dst], old.view(v)[src])
+    # the kept keys' attention: their shares of the whole context's, which sum to what is kept
+    attn = kv.attn_desc(s.attn._tensors[0], count, table, 3, 250, s.scale)
+    lse2 = torch.empty_like(lse)
+    kv.kv_attention(s.desc, s.layer, attn, s.q, out, lse2, kv.attn_workspace(s.desc, attn, s.q))
+    share = torch.exp(lse2 - lse)  # of each row's weight that the kept keys hold
+    rows = [share[:3].sum(), share[3:].sum()]
+    for q in range(2):
+        assert abs(float(kept[q, : count[q]].sum()) - float(rows[q])) < 1e-3 * float(rows[q])
+
+
+@pytest.mark.parametrize("kind,quant", [("mla", False), ("gqa", False), ("gqa", True), ("mla", True)])
+def test_a_bounded_cache_step_by_step(kind, quant):
+    step_by_step(kind, quant)
+
+
+@pytest.mark.parametrize("kind,quant", [("mla", False), ("gqa", True)])
+def test_drafted_tokens_are_verified_and_close_up(kind, quant):
+    """A tree's path that is accepted has the results of the same tokens as a causal chunk, and
+    closes up into the cache that they would have left."""
+    from _keep import Tree
+    parents = [-1, 0, 0, 1, 3, 2, 3, 6]
+    path = [0, 1, 3, 6, 7]
+    sees = []
+    for j, up in enumerate(parents):
+        sees.append((sees[up] if up >= 0 else 0) | 1 << j)
+    assert torch.equal(kv.tree_mask([parents], "cpu")[:, 0], torch.tensor(sees, dtype=torch.int32))
+    t = Tree(kind, [(8, 208)], 16 if kind == "mla" else 32, masks=[sees], quant=quant, seed=6)
+    out, lse = t.check()
+    out, lse = out[path].clone(), lse[path].clone()
+    table = t.table.cuda()
+    first = torch.tensor([200], dtype=torch.int32, device="cuda")
+    keep = torch.tensor([path], dtype=torch.int32, device="cuda")
+    count = torch.tensor([5], dtype=torch.int32, device="cuda")
+    ws = kv.compact_workspace(t.desc, 1, table.shape[1], 5)
+    kv.kv_compact(t.desc, table, first, keep, count, False, ws)
+    assert kv.kv_get_device_status(ws) == kv.KV_OK
+    off = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    attn = kv.attn_desc(off, torch.tensor([205], dtype=torch.int32, device="cuda"), table, 5, 205, t.scale)
+    q = t.q[path].contiguous()
+    got, glse = torch.empty_like(out), torch.empty_like(lse)
+    kv.kv_attention(t.desc, t.layer, attn, q, got, glse, kv.attn_workspace(t.desc, attn, q))
+    # both are within the bounds of Batch.reference of the same numbers
+    _, _, to, tl = t.reference()
+    assert not ((got.double() - out.double()).abs() > 2 * to[path]).any()
+    assert not ((glse.double() - lse.double()).abs() > 2 * tl[path]).any()

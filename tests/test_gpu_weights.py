@@ -154,8 +154,11 @@ def test_a_wait_that_runs_out():
     s.check()
 
 
-def test_captured_and_replayed():
-    s = Sums("mla", [(20, 300), (3, 90)], 16, keep=0.0, seed=18)
+@pytest.mark.parametrize("kind,heads,lens,quant", [
+    ("mla", 16, [(20, 300), (3, 90)], False), ("mla", 16, [(2, 300), (3, 90)], True),
+    ("gqa", 32, [(1, 300), (1, 90)], False), ("gqa", 32, [(90, 300), (40, 500)], False)])
+def test_captured_and_replayed(kind, heads, lens, quant):
+    s = Sums(kind, lens, heads, keep=0.0, seed=18, quant=quant)
     want = s.check().clone()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
@@ -166,6 +169,29 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for q, (_, m) in enumerate(s.lens):
             assert torch.equal(s.weights[q, :m].double(), want[q, :m])
+
+
+@pytest.mark.parametrize("kind,quant", [("mla", False), ("mla", True), ("gqa", False), ("gqa", True)])
+def test_no_queries_at_all(kind, quant):
+    s = Sums(kind, [(0, 200), (0, 3), (0, 0)], HEADS[kind], keep=0.25, quant=quant, seed=27)
+    old = s.weights.clone()
+    s.run()
+    for q, m in enumerate((200, 3, 0)):
+        assert torch.equal(s.weights[q, :m], old[q, :m] * 0.25)
+        assert torch.equal(s.weights[q, m:], old[q, m:])
+
+
+def test_on_another_stream():
+    s = Sums("gqa", [(3, 500)], 32, seed=28)
+    old = s.weights.clone()
+    want = s.run().clone()
+    s.weights.copy_(old)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        kv.kv_attention_weights(s.desc, s.layer, s.attn, s.q, s.lse, s.weights, s.keep, s.wws)
+    torch.cuda.current_stream().wait_stream(st)
+    assert torch.equal(s.weights, want)
 
 
 @pytest.mark.parametrize("quant", [False, True])
