@@ -133,9 +133,8 @@ def ref_select(weights, kv_len, budget, sinks, recent):
     got = []
     for w, n, b in zip(weights.tolist(), kv_len, budget):
         w = w[:n]
-        front = list(range(min(sinks, n)))
-        back = list(range(n - 1, max(len(front), n - recent) - 1, -1))
-        rest = [i for i in range(len(front), n - len(back))]
+        fixed = [i for i in range(n) if i < sinks or i >= n - recent]
+        rest = [i for i in range(n) if sinks <= i < n - recent]
         rest.sort(key=lambda i: (0, -w[i], i) if w[i] == w[i] else (1, 0.0, i))
-        got.append(sorted((front + back + rest)[:b]))
+        got.append(sorted((fixed + rest)[:b]))
     return got
