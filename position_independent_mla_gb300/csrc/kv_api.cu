@@ -1699,6 +1699,8 @@ WeightsPlan weights_plan(RowKind kind, bool quant, const kv_attn_desc *a, int64_
     s.num_seqs = a->num_seqs;
     s.max_q_len = a->max_q_len;
     s.max_kv_len = a->max_kv_len;
+    s.window = attn_window(a);
+    s.sinks = a->sinks;
     s.group = heads / kv_heads;
     s.kv_heads = kv_heads;
     return plan_weights(kind, s);

@@ -482,9 +482,9 @@ WeightsPlan plan_weights(RowKind kind, const AttnShape &a)
     pl.units = a.num_seqs * std::max<int64_t>(1, (a.max_kv_len + keys - 1) / keys);
     pl.parts = 1;
     if (pl.many) {
-        // some 8 parts to an SM, so that they even out
+        // some 8 parts to an SM, so that they even out, none of few steps
         pl.parts = (int32_t)std::min<int64_t>(
-            steps, std::max<int64_t>(1, (8 * kSms + pl.units - 1) / pl.units));
+            (steps + 3) / 4, std::max<int64_t>(1, (8 * kSms + pl.units - 1) / pl.units));
         pl.blocks = std::min<int64_t>(kSms, pl.units * pl.parts);
         pl.part_bytes = pl.parts > 1 ? (size_t)pl.units * pl.parts * 256 * sizeof(float) : 0;
         return pl;

@@ -213,6 +213,21 @@ __global__ void __launch_bounds__(kFewSumThreads, G::BLOCKS) weights_few_kernel(
                                    blockIdx.x, gridDim.x);
             return;
         }
+        bool any = false;
+        for (int tile = tile0; tile < tile1; ++tile)
+            any |= seen(tile);
+        if (!any) { // older steps fade, no more
+            for (int64_t k = (int64_t)tile0 * 128 + tid; rank == 0 && k < min((int64_t)w.len, (int64_t)tile1 * 128);
+                 k += kFewSumThreads) {
+                float *const to = p.weights + w.seq * p.weight_stride + k;
+                *to = p.keep == 0.0f ? 0.0f : p.keep * *to;
+                bad |= sum_slot(a, w, (int)k) < 0;
+            }
+            bad = __syncthreads_or(bad) != 0;
+            if (tid == 0)
+                write_block_status(a.header, bad ? kStatusOutOfRange : kStatusOk, blockIdx.x, gridDim.x);
+            return;
+        }
     } else {
         for (int s = tid; s < a.num_seqs; s += kFewSumThreads) {
             const bool fits = look(s);
@@ -598,12 +613,18 @@ void plan_weights_few(RowKind kind, const AttnShape &a, WeightsPlan &pl)
     pl.few = true;
     pl.few_stages = (int32_t)std::min<int64_t>(kFewSumStages, stages);
     pl.few_smem = (int32_t)(pl.few_stages * stage + queries + 1024);
-    // Key tiles in slices, one to a block; a small call, a block to a tile and to some heads.
-    // Of very many sequences runs of some tiles, four rounds of blocks.
+    // Key tiles in slices, one to a block; a small call, a block to a tile and to some heads;
+    // under a window, where few of the tiles are seen, a block to a tile (8 sequences of
+    // 32768, a window of 4096, 32 heads of their own: 153 us in slices).  Of very many
+    // sequences runs of some tiles, four rounds of blocks.
     const int64_t per_seq = std::max<int64_t>(1, (a.max_kv_len + 127) / 128);
-    const int64_t tiles = per_seq * a.num_seqs, slots = (mla ? 1 : 2) * kSms;
-    pl.few_slices = tiles > slots && tiles < (1 << 30) && a.num_seqs <= kFewSeqs;
-    pl.run = pl.few_slices ? 0 : (int32_t)std::max<int64_t>(1, tiles / (4 * slots));
+    const int64_t slots = (mla ? 1 : 2) * kSms, all = per_seq * a.num_seqs;
+    const int64_t tiles =
+        a.window == 0 ? all
+                      : std::min<int64_t>(per_seq, ((int64_t)a.window + std::min(a.sinks, a.max_kv_len) +
+                                                    a.max_q_len) / 128 + 3) * a.num_seqs;
+    pl.few_slices = a.window == 0 && tiles > slots && tiles < (1 << 30) && a.num_seqs <= kFewSeqs;
+    pl.run = pl.few_slices || a.window > 0 ? 1 : (int32_t)std::max<int64_t>(1, tiles / (4 * slots));
     pl.few_parts = 1;
     while (!mla && pl.run == 1 && pl.few_parts < 8 && tiles * pl.few_parts < slots &&
            a.kv_heads >= 2 * pl.few_parts)
