@@ -570,8 +570,9 @@ kv_status kv_tree_attention_quant(const kv_quant_pool_desc *pool, int32_t layer,
  * the sums of other keys, and none in its own where no query sees it.  Scores are fp32 sums of products of bf16 values, the sums fp32 in an
  * order that follows from the sizes alone: equal calls give equal bits.  Sequences whose
  * lengths do not fit are skipped and a block id outside the pool adds nothing to its
- * keys; both set KV_ERR_OUT_OF_RANGE.  Limits, strides and errors otherwise as in
- * kv_attention. */
+ * keys; both set KV_ERR_OUT_OF_RANGE.  After KV_ERR_TIMEOUT some keys have their new
+ * sums and others their old ones.  Limits, strides and errors otherwise as in
+ * kv_attention.  One or two kernels. */
 size_t kv_attention_weights_workspace_size(const kv_pool_desc *pool, const kv_attn_desc *attn,
                                            int64_t total_q, int32_t num_heads);
 size_t kv_attention_weights_quant_workspace_size(const kv_quant_pool_desc *pool,

@@ -7,14 +7,23 @@
 // has one key and sums its own row of tensor memory; nothing is exchanged until the end,
 // and what a key row holds has no part in another key's sum.
 //
-// A block owns 128 keys of a sequence (two such tiles where there are many queries) and
-// takes steps: a row tile (the tokens that fill 128 rows with the query heads of one key
-// head) of one key head.  The steps of a key tile are divided among the blocks of a
-// cluster, which add their sums up in the order of the blocks: equal calls give equal bits.
+// Three kernels.  Few query rows to a key head, and latent rows under one row tile:
+// kv_weights_few.cu, bound by memory.  Head rows under several row tiles: kv_weights_many.cu,
+// bound by the tensor cores and the exponentials.  This one takes what is left: 17 to 128 query
+// rows to a key head, latent rows in e4m3 or under several row tiles, and pools whose rows do
+// not come as boxes.
+//
+// A block owns 128 keys of a sequence and takes steps: a row tile (the tokens that fill 128
+// rows with the query heads of one key head) of one key head, keys and queries streamed
+// through the same stages.  The steps of a key tile are divided among the blocks of a cluster,
+// which add their sums up in the order of the blocks: equal calls give equal bits.  Bound by
+// what passes through shared memory: 16 sequences of 16 tokens over 8192 (32 heads over 8) 64
+// us, 0.63 of the copy bandwidth, 101 over e4m3 rows; 1024 tokens over 8192 latent rows, 16
+// heads, 179 us, where both operands of every product are brought in anew.
 //
 // Roles of a block's warps:
-//   sum    8 a key tile, two threads to a key, one for each half of the columns: read S
-//          from tensor memory, 2^(s * scale * log2 e - lse * log2 e), add up;
+//   sum    8, two threads to a key, one for each half of the columns: read S from tensor
+//          memory, 2^(s * scale * log2 e - lse * log2 e), add up;
 //   load   bring K and Q (boxes of tensor maps by one thread; e4m3 rows, and pools and
 //          queries that boxes do not fit, by all of them);
 //   lse    one warp brings the queries' lse, a step ahead;
@@ -69,8 +78,7 @@ struct Step {
     }
 };
 
-// 16-byte pieces of a chunk of K by the load warps' threads: PER rows' worth to a thread at
-// a time.  Asked for a chunk ahead, converted and stored when its stage is free.
+// 16-byte pieces of a chunk of K by the load warps' threads: PER to a thread.
 template <class G>
 struct HandKeys {
     static constexpr int TH = G::LOAD_WARPS * 32;

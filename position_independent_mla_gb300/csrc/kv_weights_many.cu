@@ -17,6 +17,10 @@
 // turn.  A part's sums go to the workspace, and a second kernel adds up each key's in the
 // order of the parts (p.parts = 1: the block writes the result).
 //
+// 4096 tokens over 16384, 32 heads over 8: 363 us, 1325 TFLOP/s, 0.69 of the rate of a large
+// matrix product.  A step (a row tile over 256 keys) takes 1650 clocks: 1150 of MMAs, 1024 of
+// exponentials, and the time from a finished product over the read of S to the next one.
+//
 // Roles of a block's warps: 16 sum (8 to a key tile), 4 bring a run's keys into tensor
 // memory, one brings the queries, one their lse, one issues every MMA, and one finds the
 // next parts and their keys' slots: when each role looked for its work itself, a part cost
