@@ -255,3 +255,20 @@ def test_few_rows_queries_far_apart_over_quantised_rows():
     s.q[1, 5] = 0.0
     s.lse = s.scores_lse().float().contiguous()
     s.check()
+
+
+@pytest.mark.parametrize("kind,heads,lens", [
+    ("gqa", 32, [(1, 300), (2, 100)]), ("gqa", 32, [(20, 300), (3, 100)]),
+    ("gqa", 32, [(90, 300), (300, 700)]), ("mla", 16, [(2, 300), (1, 100)]), ("mla", 16, [(40, 300)])])
+def test_heads_that_share_their_queries(kind, heads, lens):
+    s = Sums(kind, lens, heads, seed=29)
+    s.q = s.q[:, :1].expand(-1, heads, -1)  # no stride between heads: rows that boxes do not fit
+    assert s.q.stride(1) == 0
+    s.lse = s.scores_lse().float().contiguous()
+    s.check()
+
+
+@pytest.mark.parametrize("heads,quant", [(8 * 80, False), (8 * 100, True), (8 * 128, False)])
+def test_many_heads_to_a_key_head(heads, quant):
+    Sums("gqa", [(3, 300), (1, 140)], heads, seed=30, quant=quant).check()
+    Sums("gqa", [(1, 300), (1, 140)], heads, seed=31, quant=quant).check()
