@@ -567,8 +567,11 @@ kv_status kv_tree_attention_quant(const kv_quant_pool_desc *pool, int32_t layer,
  * whose lse is -infinity counts nothing.  keep (finite, >= 0): 0 writes without
  * reading, 1 adds, less lets older steps fade; with one array for all layers, the
  * first layer's call fades and the others add.  What a key row holds has no part in
- * the sums of other keys, and none in its own where no query sees it.  Scores are fp32 sums of products of bf16 values, the sums fp32 in an
- * order that follows from the sizes alone: equal calls give equal bits.  Sequences whose
+ * the sums of other keys, and none in its own where no query sees it.  Scores are fp32
+ * sums of products of bf16 values (of up to 16 query rows to a key head over quantised
+ * head rows: of e4m3 values and queries in three parts, exact down to 2^-29 of a head's
+ * largest and held to 2^-37 of that below), the sums fp32 in an order that follows from
+ * the sizes alone: equal calls give equal bits.  Sequences whose
  * lengths do not fit are skipped and a block id outside the pool adds nothing to its
  * keys; both set KV_ERR_OUT_OF_RANGE.  After KV_ERR_TIMEOUT some keys have their new
  * sums and others their old ones.  Limits, strides and errors otherwise as in

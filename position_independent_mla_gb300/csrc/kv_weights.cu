@@ -94,7 +94,7 @@ struct HandKeys {
         c = i % PIECES;
     }
 
-    // `pe`: the chunk of k_pe, bf16 in both pools (two rounds of pieces in a quantised one)
+    // piece c of a row; not of k_pe, which is bf16 in both pools
     __device__ static uint4 load(const AttnParams &a, int64_t slot, int head, int chunk, int c)
     {
         if (slot < 0)
